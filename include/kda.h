@@ -313,6 +313,168 @@ kda_status kda_commit_replay(kda_dims dims, const float *ring, int B, int T,
                              const int32_t *accepted, float *state_pool, int pool_slots,
                              const int32_t *state_idx, int32_t *err_flag, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated delta rule with one decay per value head.
+ *
+ *   S_t = (I - beta_t k_t k_t^T) exp(g_t) S_{t-1} + beta_t k_t v_t^T
+ *   o_t = scale * S_t^T q_t
+ *
+ * with a scalar log-decay g_t per token and value head, of any size: either
+ * given in FP32, or g = -exp(A_log[h]) * softplus(a + dt_bias[h]), which has
+ * no lower bound.  Token tensors, state pool, snapshots, heads, slots, error
+ * bits and the rules of capture are those of the KDA calls above; kda_commit
+ * takes the snapshots of these verifies.
+ */
+typedef struct {
+  const float *A_log;   /* device [HV] FP32, or NULL: the gate input is the log-decay, FP32 */
+  const float *dt_bias; /* device [HV] FP32, or NULL (zero bias); read with A_log only */
+  int beta_is_raw;      /* 1: beta <- sigmoid(beta) */
+  int use_qk_l2norm;    /* 1: q, k <- x / sqrt(sum x^2 + 1e-6) */
+  float scale;          /* output scale, usually K^-0.5 */
+} kda_scalar_gate;
+
+/*
+ * Varlen prefill from an indexed initial-state pool, as kda_prefill with
+ *   a             [gb_rows, HV]: with A_log the 16-bit gate input
+ *                 (kda_dims.dtype), without it the FP32 log-decay.  A value
+ *                 below -128 counts as -128 (its factor is zero in FP32).
+ *   beta          [gb_rows, HV] 16-bit: raw beta (beta_is_raw) or beta.
+ * No workspace is needed.  intermediate and intermediate_chunks as
+ * kda_prefill's: the state at the start of every 64-token chunk.
+ */
+kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *q,
+                           const kda_bf16 *k, const kda_bf16 *v, const void *a,
+                           const kda_bf16 *beta, int64_t gb_rows, float *state_pool,
+                           int pool_slots, const int32_t *state_idx, const int32_t *cu_seqlens,
+                           int num_seqs, int64_t total_tokens, kda_bf16 *o, float *intermediate,
+                           int64_t intermediate_chunks, int32_t *err_flag, void *stream);
+
+/*
+ * Packed single-token decode, chain verify and tree verify: as
+ * kda_decode_packed, kda_verify_chain and kda_verify_tree, with a [rows, HV]
+ * as in kda_gdn_prefill.
+ */
+kda_status kda_gdn_decode_packed(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *mixed_qkv,
+                                 int64_t row_stride, const void *a, const kda_bf16 *b, int B,
+                                 float *state_pool, int pool_slots, const int32_t *state_idx,
+                                 kda_bf16 *o, int32_t *err_flag, void *stream);
+kda_status kda_gdn_verify_chain(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *mixed_qkv,
+                                int64_t row_stride, const void *a, const kda_bf16 *b, int B, int T,
+                                const float *state_pool, int pool_slots, const int32_t *state_idx,
+                                kda_bf16 *o, float *snapshots, int32_t *err_flag, void *stream);
+kda_status kda_gdn_verify_tree(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *mixed_qkv,
+                               int64_t row_stride, const void *a, const kda_bf16 *b, int B, int T,
+                               const int32_t *parent_idx, const float *state_pool, int pool_slots,
+                               const int32_t *state_idx, kda_bf16 *o, float *snapshots,
+                               int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Verification of drafted tokens against the target's probabilities, between a
+ * verify call and its commit.  Random numbers are inputs; results are exact
+ * whole numbers (accept tests in exact arithmetic, sums in 48 bits or more).
+ *
+ * Rows of a request are those of the verify call: row 0 is the token already
+ * sampled, rows 1..T-1 the drafted ones.
+ *   target        probabilities behind every row: row r*T + i is the
+ *                 distribution of the token that follows token i of request
+ *                 r; `vocab` elements, rows target_stride elements apart
+ *   probs_dtype   element type of target and draft: KDA_DTYPE_F32,
+ *                 KDA_DTYPE_BF16 or KDA_DTYPE_F16.  NaN, negative and
+ *                 infinite entries count as zero.
+ *   tokens        [B, T] int32; a drafted token outside [0, vocab) sets
+ *                 KDA_DEVERR_TOKEN and falls
+ *   uniforms      [B, T] FP32 in [0, 1): u[r][i] tests drafted token i,
+ *                 u[r][0] draws the next token
+ *   lengths       [B] int32 rows of each request, in [0, T], or NULL (all T).
+ *                 0 marks a padding request: accepted = next = -1.  Others set
+ *                 KDA_DEVERR_SEQLENS and count as 0.
+ *   accepted      [B] int32 out: the last row that stands (0: no draft does),
+ *                 which is what kda_commit takes
+ *   next_token    [B] int32 out: the token drawn behind it: the lowest j whose
+ *                 running sum of weights w_0 + .. + w_j exceeds u[r][0] times
+ *                 their whole; -1 where the row has no weight at all
+ */
+#define KDA_DTYPE_F32 2 /* for probs_dtype only */
+#define KDA_DEVERR_TOKEN 64 /* drafted token outside [0, vocab) */
+#define KDA_ACCEPT_MAX_T 1024
+
+/*
+ * Chain: token i stands while all before it do and u[r][i] * q < p, p its
+ * probability in target row i - 1 and q the one it was drawn with.  The next
+ * token is drawn from max(p - q, 0) of the row whose draft fell (from p where
+ * that leaves nothing), or from p behind the last row.
+ *   draft         probabilities the drafts were drawn with: row r*(T-1) + i - 1
+ *                 for token i, draft_stride apart; NULL: proposed with
+ *                 certainty (q = 1 at the token, 0 elsewhere)
+ */
+kda_status kda_accept_chain(int probs_dtype, const void *target, int64_t target_stride,
+                            const void *draft, int64_t draft_stride, const int32_t *tokens,
+                            const float *uniforms, const int32_t *lengths, int B, int T, int vocab,
+                            int32_t *accepted, int32_t *next_token, int32_t *err_flag,
+                            void *stream);
+
+/*
+ * Tree of tokens proposed with certainty: node 0 is the root (parent -1), the
+ * parent of node i > 0 is a node in [0, i) (else KDA_DEVERR_PARENT and the
+ * request counts as padding).  From the root, the children of the node
+ * reached are tried in order of their index: child c stands where
+ * u[r][c] * Z < p, with p its probability in the node's row and Z = 1 minus
+ * the probabilities of the siblings that fell; a token tried before has p = 0.
+ * Where none stands the next token is drawn from the node's row without the
+ * tokens that fell (from the whole row where that leaves nothing).
+ *   path          [B, T] int32 out: nodes from the root to accepted[r], then -1
+ */
+kda_status kda_accept_tree(int probs_dtype, const void *target, int64_t target_stride,
+                           const int32_t *tokens, const int32_t *parent_idx, const float *uniforms,
+                           const int32_t *lengths, int B, int T, int vocab, int32_t *accepted,
+                           int32_t *path, int32_t *next_token, int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a state pool.  A page is one slot's record in every layer:
+ * `layers` pieces of page_bytes, layer_stride bytes apart.  `used` holds one
+ * byte per slot, 0 for a free page (4-byte aligned, slots rounded up to 4
+ * bytes).  `table` maps the caller's rows (requests) to slots, -1 for none; it
+ * is the state_idx of the other calls.  All of it is on the device: no call
+ * reads it from the host.  No two rows share a slot.
+ */
+typedef struct {
+  void *base;           /* 16-byte aligned */
+  int64_t page_bytes;   /* bytes of a page in one layer, a multiple of 16 */
+  int64_t layer_stride; /* bytes from a slot in one layer to the next layer's, a multiple of 16 */
+  int layers;
+  int slots;
+} kda_pages;
+#define KDA_DEVERR_PAGE 128      /* a slot or table row out of range, a page that is not in use,
+                                    or a copy into a page that the call also reads or writes twice */
+#define KDA_DEVERR_POOL_FULL 256 /* no free page was left; the row got -1 */
+
+/* page dst[i] <- page src[i], i < n; a -1 in either skips the pair.  A pair
+ * whose dst is the dst or the src of another pair sets KDA_DEVERR_PAGE and is
+ * not copied. */
+kda_status kda_pool_copy(kda_pages pages, const int32_t *src, const int32_t *dst, int n,
+                         int32_t *err_flag, void *stream);
+
+/* For i < n: the page of table row rows[i] becomes free and the row -1 (a row
+ * that is -1 already stays so).  rows[i] = -1 is skipped. */
+kda_status kda_pool_free(uint8_t *used, int slots, int32_t *table, int table_rows,
+                         const int32_t *rows, int n, int32_t *err_flag, void *stream);
+
+/* Moves pages so that the used ones are slots 0 .. count-1: the k-th lowest
+ * free slot below count takes the k-th lowest used page at or above it.
+ * table and used follow; *count (device) receives the number of used pages. */
+kda_status kda_pool_compact(kda_pages pages, uint8_t *used, int32_t *table, int table_rows,
+                            int32_t *count, int32_t *err_flag, void *stream);
+
+/* For i < n, in order: table row rows[i] gets the lowest free page, filled
+ * from the page that table row parents[i] held before the call, or with zeros
+ * where parents[i] is -1.  rows[i] = -1 is skipped.  A row that holds a page
+ * or was listed before, and a parent row without a page, set KDA_DEVERR_PAGE
+ * and change nothing.
+ *   children      [n] int32 out: the slot each entry got, -1 for none */
+kda_status kda_pool_fork(kda_pages pages, uint8_t *used, int32_t *table, int table_rows,
+                         const int32_t *parents, const int32_t *rows, int n, int32_t *children,
+                         int32_t *err_flag, void *stream);
+
 /*
  * Profiling aid (not part of the pages' contract): per-kernel timing of every
  * entry point.  After kda_set_stage_events(ev) with three cudaEvent_t

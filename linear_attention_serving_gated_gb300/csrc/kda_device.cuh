@@ -29,6 +29,15 @@ struct GateArgs {
   float scale;
 };
 
+// Gate of the rule with one decay per value head (kda_scalar_gate).
+struct ScalarGateArgs {
+  const float* A_log;    // [HV] or nullptr: the gate input is the FP32 log-decay
+  const float* dt_bias;  // [HV] or nullptr
+  int beta_is_raw;
+  int use_qk_l2norm;
+  float scale;
+};
+
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t x) {
   return __uint_as_float(static_cast<uint32_t>(x) << 16);
 }
@@ -91,6 +100,23 @@ __device__ __forceinline__ float gate_log_decay(const GateArgs& ga, float a_in, 
 
 __device__ __forceinline__ float fold_beta(const GateArgs& ga, float b_in) {
   return ga.beta_is_raw ? sigmoidf_(b_in) : b_in;
+}
+
+// Log-decay of one token and value head: -exp(A_log) softplus(a + dt_bias), or
+// given.  neg_rate = -exp(A_log[h]), bias = dt_bias[h].  Below -128 the decay
+// is zero in FP32 and stays zero in any sum with other log-decays <= 0; the
+// cut keeps such sums finite (-inf - -inf) and lets a NaN through.
+template <bool F16>
+__device__ __forceinline__ float scalar_log_decay(const ScalarGateArgs& ga, const void* a, int64_t at, float neg_rate,
+                                                  float bias) {
+  float g;
+  if (ga.A_log) {
+    const float x = in16_to_float<F16>(static_cast<const uint16_t*>(a)[at]) + bias;
+    g = neg_rate * (x > 20.f ? x : log1pf(expf(x)));  // softplus; past 20 it is x to 2^-28
+  } else {
+    g = static_cast<const float*>(a)[at];
+  }
+  return g < -128.f ? -128.f : g;
 }
 
 // Packed FP32 pair arithmetic (sm_100+ f32x2 instructions).

@@ -42,6 +42,21 @@ inline kda_status check_gate(const kda_gate& g, GateArgs* out) {
   return KDA_OK;
 }
 
+inline kda_status check_scalar_gate(const kda_scalar_gate& g, const void* a, const void* beta, ScalarGateArgs* out) {
+  // the gate input is read one element at a time, so it needs only its own alignment
+  const uintptr_t a_mask = g.A_log ? 1u : 3u;
+  if ((reinterpret_cast<uintptr_t>(a) & a_mask) || (reinterpret_cast<uintptr_t>(beta) & 1u)) return KDA_ERR_ALIGNMENT;
+  out->A_log = g.A_log;
+  out->dt_bias = g.A_log ? g.dt_bias : nullptr;
+  out->beta_is_raw = g.beta_is_raw;
+  out->use_qk_l2norm = g.use_qk_l2norm;
+  out->scale = g.scale;
+  return KDA_OK;
+}
+
+// SMs of the current device (looked up once per device); 0 on an error.
+int sm_count();
+
 inline kda_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

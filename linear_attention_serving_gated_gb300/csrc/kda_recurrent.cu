@@ -562,6 +562,8 @@ __global__ void __launch_bounds__(256) commit_kernel(const float* __restrict__ s
   }
 }
 
+}  // namespace
+
 // SMs of the current device (looked up once per device).
 int sm_count() {
   static std::atomic<int> counts[64];
@@ -574,6 +576,8 @@ int sm_count() {
   }
   return n;
 }
+
+namespace {
 
 template <int MODE>
 kda_status launch_recurrent(const StepArgs& a, cudaStream_t stream, bool stages = true) {

@@ -31,6 +31,9 @@ KDA_DEVERR_SEQLENS = 4
 KDA_DEVERR_ACCEPTED = 8
 KDA_DEVERR_TIMEOUT = 16
 KDA_DEVERR_INTERMEDIATE = 32
+KDA_DEVERR_TOKEN = 64
+KDA_DEVERR_PAGE = 128
+KDA_DEVERR_POOL_FULL = 256
 
 CHUNK = 64
 
@@ -42,6 +45,7 @@ class KdaError(RuntimeError):
 
 
 KDA_DTYPE_BF16, KDA_DTYPE_F16 = 0, 1
+KDA_DTYPE_F32 = 2  # probabilities of kda_accept_chain / kda_accept_tree only
 
 
 class kda_dims(ctypes.Structure):
@@ -55,10 +59,22 @@ class kda_gate(ctypes.Structure):
                 ("use_qk_l2norm", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+class kda_scalar_gate(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("beta_is_raw", ctypes.c_int),
+                ("use_qk_l2norm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class kda_pages(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("layers", ctypes.c_int), ("slots", ctypes.c_int)]
+
+
 EXPORTS = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill", "kda_decode_packed",
            "kda_verify_chain", "kda_verify_tree", "kda_commit", "kda_set_stage_events",
            "kda_prefill_noalloc", "kda_replay_ring_bytes", "kda_verify_chain_replay",
-           "kda_commit_replay")
+           "kda_commit_replay", "kda_gdn_prefill", "kda_gdn_decode_packed", "kda_gdn_verify_chain",
+           "kda_gdn_verify_tree", "kda_accept_chain", "kda_accept_tree", "kda_pool_copy", "kda_pool_free",
+           "kda_pool_compact", "kda_pool_fork")
 
 PREFILL_STATIC_SCRATCH_BYTES = 128 << 20  # KDA_PREFILL_STATIC_SCRATCH_BYTES in include/kda.h
 
@@ -101,6 +117,30 @@ def load(path: str = LIB_PATH):
                                                 vp, vp, vp, vp, vp]
         lib.kda_commit_replay.restype = i32
         lib.kda_commit_replay.argtypes = [kda_dims, vp, i32, i32, vp, vp, i32, vp, vp, vp]
+        lib.kda_gdn_prefill.restype = i32
+        lib.kda_gdn_prefill.argtypes = [kda_dims, kda_scalar_gate, vp, vp, vp, vp, vp, i64, vp, i32, vp, vp,
+                                        i32, i64, vp, vp, i64, vp, vp]
+        lib.kda_gdn_decode_packed.restype = i32
+        lib.kda_gdn_decode_packed.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, vp, i32, vp, i32, vp,
+                                              vp, vp, vp]
+        lib.kda_gdn_verify_chain.restype = i32
+        lib.kda_gdn_verify_chain.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, vp, i32, i32, vp, i32,
+                                             vp, vp, vp, vp, vp]
+        lib.kda_gdn_verify_tree.restype = i32
+        lib.kda_gdn_verify_tree.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, vp, i32, i32, vp, vp,
+                                            i32, vp, vp, vp, vp, vp]
+        lib.kda_accept_chain.restype = i32
+        lib.kda_accept_chain.argtypes = [i32, vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+        lib.kda_accept_tree.restype = i32
+        lib.kda_accept_tree.argtypes = [i32, vp, i64, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+        lib.kda_pool_copy.restype = i32
+        lib.kda_pool_copy.argtypes = [kda_pages, vp, vp, i32, vp, vp]
+        lib.kda_pool_free.restype = i32
+        lib.kda_pool_free.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp]
+        lib.kda_pool_compact.restype = i32
+        lib.kda_pool_compact.argtypes = [kda_pages, vp, vp, i32, vp, vp, vp]
+        lib.kda_pool_fork.restype = i32
+        lib.kda_pool_fork.argtypes = [kda_pages, vp, vp, i32, vp, vp, i32, vp, vp, vp]
         lib.kda_set_stage_events.restype = None
         lib.kda_set_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
         _lib = lib
@@ -364,3 +404,267 @@ def kda_set_stage_events(events=None):
     arr = (ctypes.c_void_p * 3)(*[ctypes.c_void_p(e.cuda_event if e is not None else None)
                                   for e in events])
     load().kda_set_stage_events(arr)
+
+
+# -- the gated delta rule with one decay per value head ----------------------
+
+
+class ScalarGate:
+    """Fold options of the kda_gdn_* calls (kda_scalar_gate): A_log and dt_bias
+    [HV] FP32 device tensors.  Without A_log the gate input is the log-decay
+    itself, FP32."""
+
+    def __init__(self, A_log=None, dt_bias=None, beta_is_raw=True, use_qk_l2norm=True, scale=128 ** -0.5):
+        self.A_log, self.dt_bias = A_log, dt_bias
+        self.beta_is_raw, self.use_qk_l2norm, self.scale = beta_is_raw, use_qk_l2norm, scale
+
+    def c(self, d):
+        for t, name in ((self.A_log, "A_log"), (self.dt_bias, "dt_bias")):
+            if t is not None:
+                if t.dtype != torch.float32:
+                    raise TypeError("A_log and dt_bias must be float32")
+                _at_least(t, d.HV, name, "[HV]")
+        return kda_scalar_gate(_p(self.A_log), _p(self.dt_bias), int(bool(self.beta_is_raw)),
+                               int(bool(self.use_qk_l2norm)), float(self.scale))
+
+
+def _typed(t, dtype, name):
+    """A device tensor of one element type (None allowed)."""
+    if t is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    return _p(t)
+
+
+def _scalar_gate_input(d, gate, a):
+    """The gate input: 16-bit with A_log, FP32 log-decays without."""
+    return _in16(d, a, "a") if gate.A_log is not None else _typed(a, torch.float32, "a (log-decays)")
+
+
+def _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, rows, reqs):
+    if state_pool.dim() < 3 or tuple(state_pool.shape[-3:]) != (d.HV, d.V, d.K):
+        raise ValueError(f"state_pool must end in [HV, V, K] = [{d.HV}, {d.V}, {d.K}] "
+                         f"(got {tuple(state_pool.shape)})")
+    _at_least(state_pool, 0, "state_pool", "[slots, HV, V, K]")
+    width = 2 * d.H * d.K + d.HV * d.V
+    if mixed_qkv.dim() != 2 or mixed_qkv.shape[0] < rows or mixed_qkv.shape[1] < width \
+            or mixed_qkv.stride(1) != 1:
+        raise ValueError(f"mixed_qkv must be [>= {rows}, >= {width}] with unit column stride "
+                         f"(got {tuple(mixed_qkv.shape)})")
+    if a.shape[-1] != d.HV:
+        raise ValueError(f"`a` must have shape [B, HV] = [{rows}, {d.HV}] (got {tuple(a.shape)})")
+    _at_least(a, rows * d.HV, "a", f"[{rows}, HV]")
+    _at_least(b, rows * d.HV, "b", f"[{rows}, HV]")
+    _at_least(state_idx, reqs, "state_idx", f"[{reqs}]")
+
+
+def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, cu_seqlens, num_seqs, o,
+                    intermediate=None, err_flag=None, stream=None):
+    """Varlen prefill (see kda.h).  q,k [T,H,K], v [T,HV,V], a and b
+    [gb_rows,HV]; state_pool [slots,HV,V,K] fp32 (in place); o [T,HV,V]
+    (written)."""
+    T, gb_rows = q.shape[0], a.shape[0]
+    if a.shape[-1] != d.HV:
+        raise ValueError(f"`a` must have shape [gb_rows, HV] = [*, {d.HV}] (got {tuple(a.shape)})")
+    if state_pool.dim() < 3 or tuple(state_pool.shape[-3:]) != (d.HV, d.V, d.K):
+        raise ValueError(f"state_pool must end in [HV, V, K] = [{d.HV}, {d.V}, {d.K}] "
+                         f"(got {tuple(state_pool.shape)})")
+    _at_least(state_pool, 0, "state_pool", "[slots, HV, V, K]")
+    _at_least(q, T * d.H * d.K, "q", f"[{T}, H, K]")
+    _at_least(k, T * d.H * d.K, "k", f"[{T}, H, K]")
+    _at_least(v, T * d.HV * d.V, "v", f"[{T}, HV, V]")
+    _at_least(a, gb_rows * d.HV, "a", f"[{gb_rows}, HV]")
+    _at_least(b, gb_rows * d.HV, "b", f"[{gb_rows}, HV]")
+    _at_least(o, T * d.HV * d.V, "o", f"[{T}, HV, V]")
+    _at_least(state_idx, num_seqs, "state_idx", f"[{num_seqs}]")
+    _at_least(cu_seqlens, num_seqs + 1, "cu_seqlens", f"[{num_seqs + 1}]")
+    inter_chunks = _intermediate_chunks(d, intermediate)
+    st = load().kda_gdn_prefill(
+        d, gate.c(d), _in16(d, q, "q"), _in16(d, k, "k"), _in16(d, v, "v"), _scalar_gate_input(d, gate, a),
+        _in16(d, b, "b"), int(gb_rows), _typed(state_pool, torch.float32, "state_pool"), int(state_pool.shape[0]),
+        _typed(state_idx, torch.int32, "state_idx"), _typed(cu_seqlens, torch.int32, "cu_seqlens"), int(num_seqs),
+        int(T), _in16(d, o, "o"), _p(intermediate), inter_chunks, _p(err_flag), _stream(stream))
+    _check(st, "kda_gdn_prefill")
+
+
+def kda_gdn_decode_packed(d, gate: ScalarGate, mixed_qkv, a, b, state_pool, state_idx, o, err_flag=None,
+                          stream=None):
+    """One token per request, state in place; a, b [B, HV]."""
+    B = mixed_qkv.shape[0]
+    _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, B, B)
+    _at_least(o, B * d.HV * d.V, "o", f"[{B}, HV, V]")
+    st = load().kda_gdn_decode_packed(
+        d, gate.c(d), _in16(d, mixed_qkv, "mixed_qkv"), int(mixed_qkv.stride(0)), _scalar_gate_input(d, gate, a),
+        _in16(d, b, "b"), int(B), _typed(state_pool, torch.float32, "state_pool"), int(state_pool.shape[0]),
+        _typed(state_idx, torch.int32, "state_idx"), _in16(d, o, "o"), _p(err_flag), _stream(stream))
+    _check(st, "kda_gdn_decode_packed")
+
+
+def _gdn_verify(name, d, gate, mixed_qkv, a, b, B, T, parents, state_pool, state_idx, o, snapshots, err_flag,
+                stream):
+    _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, B * T, B)
+    _at_least(o, B * T * d.HV * d.V, "o", f"[{B}, {T}, HV, V]")
+    _at_least(snapshots, B * T * d.HV * d.V * d.K, "snapshots", f"[{B}, {T}, HV, V, K]")
+    st = getattr(load(), name)(
+        d, gate.c(d), _in16(d, mixed_qkv, "mixed_qkv"), int(mixed_qkv.stride(0)), _scalar_gate_input(d, gate, a),
+        _in16(d, b, "b"), int(B), int(T), *parents, _typed(state_pool, torch.float32, "state_pool"),
+        int(state_pool.shape[0]), _typed(state_idx, torch.int32, "state_idx"), _in16(d, o, "o"),
+        _typed(snapshots, torch.float32, "snapshots"), _p(err_flag), _stream(stream))
+    _check(st, name)
+
+
+def kda_gdn_verify_chain(d, gate: ScalarGate, mixed_qkv, a, b, B, T, state_pool, state_idx, o, snapshots,
+                         err_flag=None, stream=None):
+    """Chain verify; snapshots as kda_verify_chain's, for kda_commit."""
+    _gdn_verify("kda_gdn_verify_chain", d, gate, mixed_qkv, a, b, B, T, (), state_pool, state_idx, o, snapshots,
+                err_flag, stream)
+
+
+def kda_gdn_verify_tree(d, gate: ScalarGate, mixed_qkv, a, b, B, T, parent_idx, state_pool, state_idx, o,
+                        snapshots, err_flag=None, stream=None):
+    """Tree verify; parent_idx [B, T] int32."""
+    _at_least(parent_idx, B * T, "parent_idx", f"[{B}, {T}]")
+    _gdn_verify("kda_gdn_verify_tree", d, gate, mixed_qkv, a, b, B, T, (_typed(parent_idx, torch.int32, "parent_idx"),),
+                state_pool, state_idx, o, snapshots, err_flag, stream)
+
+
+# -- verification of drafted tokens ------------------------------------------
+
+_PROBS = {torch.float32: KDA_DTYPE_F32, torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_F16}
+
+
+def _rows_stride(t, name, B, T):
+    """Elements between the rows of probabilities [B, T, vocab]: the rows may be
+    padded, but have one stride throughout."""
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != T or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [B, T, vocab] = [{B}, {T}, *] with dense rows (got {tuple(t.shape)})")
+    stride = t.stride(1) if T > 1 else t.stride(0) if B > 1 else t.shape[2]
+    if (B > 1 and t.stride(0) != T * stride) or stride < t.shape[2]:
+        raise ValueError(f"the rows of {name} must lie one stride apart (got strides {tuple(t.stride())})")
+    return int(stride)
+
+
+def _accept_args(target, tokens, uniforms, lengths, accepted, next_token):
+    if tokens.dim() != 2:
+        raise ValueError(f"tokens must be [B, T] (got {tuple(tokens.shape)})")
+    B, T = tokens.shape
+    if target.dtype not in _PROBS:
+        raise TypeError(f"target must be float32, bfloat16 or float16 (got {target.dtype})")
+    stride = _rows_stride(target, "target", B, T)
+    _at_least(tokens, B * T, "tokens", f"[{B}, {T}]")
+    _at_least(uniforms, B * T, "uniforms", f"[{B}, {T}]")
+    _at_least(lengths, B, "lengths", f"[{B}]")
+    _at_least(accepted, B, "accepted", f"[{B}]")
+    _at_least(next_token, B, "next_token", f"[{B}]")
+    return B, T, stride
+
+
+def kda_accept_chain(target, draft, tokens, uniforms, accepted, next_token, lengths=None, err_flag=None,
+                     stream=None):
+    """Which drafted tokens stand, and the token behind them (see kda.h).
+    target [B,T,vocab] and draft [B,T-1,vocab] (or None) probabilities of one
+    element type, rows possibly padded; tokens [B,T] int32, uniforms [B,T] fp32,
+    lengths [B] int32 or None; accepted [B] int32 (for kda_commit) and
+    next_token [B] int32 (written)."""
+    B, T, stride = _accept_args(target, tokens, uniforms, lengths, accepted, next_token)
+    draft_stride = 0
+    if T == 1:
+        draft = None  # nothing was drafted
+    if draft is not None:
+        if draft.dtype != target.dtype or draft.shape[-1] != target.shape[-1]:
+            raise ValueError("draft must have target's element type and vocabulary")
+        draft_stride = _rows_stride(draft, "draft", B, T - 1)
+    st = load().kda_accept_chain(
+        _PROBS[target.dtype], _p(target), stride, _p(draft), draft_stride, _typed(tokens, torch.int32, "tokens"),
+        _typed(uniforms, torch.float32, "uniforms"), _typed(lengths, torch.int32, "lengths"), int(B), int(T),
+        int(target.shape[2]), _typed(accepted, torch.int32, "accepted"), _typed(next_token, torch.int32, "next_token"),
+        _p(err_flag), _stream(stream))
+    _check(st, "kda_accept_chain")
+
+
+def kda_accept_tree(target, tokens, parent_idx, uniforms, accepted, path, next_token, lengths=None, err_flag=None,
+                    stream=None):
+    """As kda_accept_chain for a tree proposed without probabilities:
+    parent_idx [B,T] int32; path [B,T] int32 (written)."""
+    B, T, stride = _accept_args(target, tokens, uniforms, lengths, accepted, next_token)
+    _at_least(parent_idx, B * T, "parent_idx", f"[{B}, {T}]")
+    _at_least(path, B * T, "path", f"[{B}, {T}]")
+    st = load().kda_accept_tree(
+        _PROBS[target.dtype], _p(target), stride, _typed(tokens, torch.int32, "tokens"),
+        _typed(parent_idx, torch.int32, "parent_idx"), _typed(uniforms, torch.float32, "uniforms"),
+        _typed(lengths, torch.int32, "lengths"), int(B), int(T), int(target.shape[2]),
+        _typed(accepted, torch.int32, "accepted"), _typed(path, torch.int32, "path"),
+        _typed(next_token, torch.int32, "next_token"), _p(err_flag), _stream(stream))
+    _check(st, "kda_accept_tree")
+
+
+# -- pages of a state pool ---------------------------------------------------
+
+
+def _pages(pool):
+    """Pages of a pool tensor [layers, slots, ...] whose slots are dense; the
+    layers may lie further apart."""
+    if pool.dim() < 3:
+        raise ValueError(f"pool must be [layers, slots, ...] (got {tuple(pool.shape)})")
+    layers, slots = pool.shape[0], pool.shape[1]
+    if layers > 0 and not pool[0].is_contiguous():
+        raise ValueError("the slots of a layer must be dense")
+    page = pool.element_size() * math.prod(pool.shape[2:])
+    stride = pool.element_size() * (pool.stride(0) if layers > 1 else slots * math.prod(pool.shape[2:]))
+    return kda_pages(_p(pool), page, stride, int(layers), int(slots))
+
+
+def _int32_list(t, name):
+    if t is None or t.dim() != 1:
+        raise ValueError(f"{name} must be a list [n]")
+    _at_least(t, 0, name, "[n]")
+    return _typed(t, torch.int32, name)
+
+
+def _used(used, slots):
+    if used.dtype not in (torch.uint8, torch.bool):
+        raise TypeError(f"used must be uint8 or bool (got {used.dtype})")
+    _at_least(used, slots, "used", f"[{slots}]")
+    return _p(used)
+
+
+def kda_pool_copy(pool, src, dst, err_flag=None, stream=None):
+    """pool[:, dst[i]] <- pool[:, src[i]]; pool [layers, slots, ...]."""
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have one length")
+    st = load().kda_pool_copy(_pages(pool), _int32_list(src, "src"), _int32_list(dst, "dst"), int(src.shape[0]),
+                              _p(err_flag), _stream(stream))
+    _check(st, "kda_pool_copy")
+
+
+def kda_pool_free(used, table, rows, err_flag=None, stream=None):
+    """Frees the pages of table rows `rows` and sets the rows to -1."""
+    slots = int(used.shape[0])
+    st = load().kda_pool_free(_used(used, slots), slots, _int32_list(table, "table"), int(table.shape[0]),
+                              _int32_list(rows, "rows"), int(rows.shape[0]), _p(err_flag), _stream(stream))
+    _check(st, "kda_pool_free")
+
+
+def kda_pool_compact(pool, used, table, count, err_flag=None, stream=None):
+    """Moves the used pages to slots 0 .. count-1; table, used and count [1]
+    int32 follow."""
+    _at_least(count, 1, "count", "[1]")
+    st = load().kda_pool_compact(_pages(pool), _used(used, pool.shape[1]), _int32_list(table, "table"),
+                                 int(table.shape[0]), _typed(count, torch.int32, "count"), _p(err_flag), _stream(stream))
+    _check(st, "kda_pool_compact")
+
+
+def kda_pool_fork(pool, used, table, parents, rows, children=None, err_flag=None, stream=None):
+    """Table row rows[i] gets the lowest free page, a copy of the page of row
+    parents[i] (zeros where that is -1); returns children [n] int32, the slots
+    given."""
+    if parents.shape != rows.shape:
+        raise ValueError("parents and rows must have one length")
+    n = int(rows.shape[0])
+    if children is None:
+        children = torch.empty(n, dtype=torch.int32, device=rows.device)
+    _at_least(children, n, "children", "[n]")
+    st = load().kda_pool_fork(_pages(pool), _used(used, pool.shape[1]), _int32_list(table, "table"),
+                              int(table.shape[0]), _int32_list(parents, "parents"), _int32_list(rows, "rows"), n,
+                              _int32_list(children, "children"), _p(err_flag), _stream(stream))
+    _check(st, "kda_pool_fork")
+    return children
