@@ -21,7 +21,7 @@
 namespace kda {
 namespace {
 
-enum GdnMode { kGdnDecode = 0, kGdnChain = 1, kGdnTree = 2, kGdnSeq = 3 };
+enum GdnMode { kGdnDecode = 0, kGdnChain = 1, kGdnTree = 2 };
 
 struct GdnStepArgs {
   ScalarGateArgs gate;
@@ -38,12 +38,6 @@ struct GdnStepArgs {
   kda_bf16* o;
   float* snapshots;
   int32_t* err_flag;
-  // kGdnSeq
-  const int32_t* cu_seqlens;
-  int num_seqs;
-  int64_t total_tokens;
-  float* intermediate;
-  int64_t inter_chunks;
 };
 
 __device__ __forceinline__ float dot16(const float4 (&x)[4], const float4 (&y)[4]) {
@@ -54,10 +48,6 @@ __device__ __forceinline__ float dot16(const float4 (&x)[4], const float4 (&y)[4
     a = fma2(make_float2(x[i].z, x[i].w), make_float2(y[i].z, y[i].w), a);
   }
   return a.x + a.y;
-}
-
-__device__ __forceinline__ int64_t seq_begin(const GdnStepArgs& a, int n) {
-  return a.cu_seqlens ? (int64_t)a.cu_seqlens[n] : a.total_tokens / a.num_seqs * n;
 }
 
 // What one lane needs of a token: its 16 channels of q and k, the v of its
@@ -81,29 +71,8 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
   const int HV = args.HV;
   const bool reporter = tid == 0 && rb == 0 && h == 0;
 
-  int64_t t0 = (int64_t)r * args.T;
-  int T = MODE == kGdnDecode ? 1 : args.T;
-  int64_t cbase = 0;
-  if constexpr (MODE == kGdnSeq) {
-    t0 = seq_begin(args, r);
-    const int64_t t1 = seq_begin(args, r + 1);
-    const bool bad = t0 < 0 || t1 < t0 || t1 > args.total_tokens || (r == 0 && t0 != 0) ||
-                     (r == args.num_seqs - 1 && t1 != args.total_tokens);
-    if (bad) {
-      if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
-      return;
-    }
-    T = (int)(t1 - t0);
-    if (T == 0) return;
-    if (args.intermediate) {
-      for (int n = lane; n < r; n += 32) {
-        const int64_t L = seq_begin(args, n + 1) - seq_begin(args, n);
-        cbase += L > 0 ? (L + 63) / 64 : 0;
-      }
-#pragma unroll
-      for (int m = 16; m; m >>= 1) cbase += __shfl_xor_sync(0xffffffffu, cbase, m);
-    }
-  }
+  const int64_t t0 = (int64_t)r * args.T;
+  const int T = MODE == kGdnDecode ? 1 : args.T;
 
   auto load = [&](int t, Token<GROUPS>& x) {
     const int64_t row = t0 + t;
@@ -175,15 +144,6 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
       if (p != t - 1)
         load_state(p < 0 ? root : args.snapshots + (((size_t)t0 + p) * HV + h) * head_elems + (size_t)row0 * K + sub * 4);
     }
-    if constexpr (MODE == kGdnSeq) {
-      if (args.intermediate && t % 64 == 0) {
-        const int64_t cid = cbase + t / 64;
-        if (cid < args.inter_chunks)
-          store_state(args.intermediate + ((size_t)cid * HV + h) * head_elems + (size_t)row0 * K + sub * 4);
-        else if (reporter)
-          set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
-      }
-    }
     float4 q[4], k[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -224,7 +184,7 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
     if (MODE == kGdnChain || MODE == kGdnTree)
       store_state(args.snapshots + ((size_t)row * HV + h) * head_elems + (size_t)row0 * K + sub * 4);
   }
-  if (MODE == kGdnDecode || MODE == kGdnSeq) store_state(root);
+  if (MODE == kGdnDecode) store_state(root);
 }
 
 template <int MODE>
@@ -300,51 +260,6 @@ kda_status gdn_verify(kda_dims dims, kda_scalar_gate gate, const kda_bf16* mixed
 }  // namespace kda
 
 using namespace kda;
-
-extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
-                                      const kda_bf16* v, const void* a, const kda_bf16* beta, int64_t gb_rows,
-                                      float* state_pool, int pool_slots, const int32_t* state_idx,
-                                      const int32_t* cu_seqlens, int num_seqs, int64_t total_tokens, kda_bf16* o,
-                                      float* intermediate, int64_t intermediate_chunks, int32_t* err_flag,
-                                      void* stream) {
-  kda_status s = check_dims(dims);
-  if (s != KDA_OK) return s;
-  if (!state_pool || !state_idx) return KDA_ERR_NULL_ARG;
-  if (num_seqs < 0 || pool_slots < 0 || total_tokens < 0 || total_tokens > INT32_MAX || gb_rows < total_tokens)
-    return KDA_ERR_SHAPE;
-  if (intermediate && intermediate_chunks < 0) return KDA_ERR_SHAPE;
-  if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_SHAPE;
-  if (!cu_seqlens && total_tokens % num_seqs != 0) return KDA_ERR_SHAPE;
-  if (total_tokens == 0) return KDA_OK;
-  if (!q || !k || !v || !a || !beta || !o) return KDA_ERR_NULL_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state_pool) ||
-      !aligned16(intermediate))
-    return KDA_ERR_ALIGNMENT;
-  GdnStepArgs args{};
-  s = check_scalar_gate(gate, a, beta, &args.gate);
-  if (s != KDA_OK) return s;
-  args.H = dims.H;
-  args.HV = dims.HV;
-  args.G = dims.HV / dims.H;
-  args.q = q;
-  args.k = k;
-  args.v = v;
-  args.q_stride = args.k_stride = (int64_t)dims.H * dims.K;
-  args.v_stride = (int64_t)dims.HV * dims.V;
-  args.a = a;
-  args.b = beta;
-  args.pool = state_pool;
-  args.pool_slots = pool_slots;
-  args.state_idx = state_idx;
-  args.o = o;
-  args.err_flag = err_flag;
-  args.cu_seqlens = cu_seqlens;
-  args.num_seqs = num_seqs;
-  args.total_tokens = total_tokens;
-  args.intermediate = intermediate;
-  args.inter_chunks = intermediate_chunks;
-  return launch_gdn<kGdnSeq>(args, num_seqs, dims.dtype, static_cast<cudaStream_t>(stream));
-}
 
 extern "C" kda_status kda_gdn_decode_packed(kda_dims dims, kda_scalar_gate gate, const kda_bf16* mixed_qkv,
                                             int64_t row_stride, const void* a, const kda_bf16* b, int B,

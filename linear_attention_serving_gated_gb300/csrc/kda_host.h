@@ -8,6 +8,8 @@
 // bug", key source snippets of kda_prefill.py and kda_decode.py.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -53,6 +55,9 @@ inline kda_status check_scalar_gate(const kda_scalar_gate& g, const void* a, con
   out->scale = g.scale;
   return KDA_OK;
 }
+
+// The driver's tensor map encoder, fetched through the runtime; NULL on an error.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // SMs of the current device (looked up once per device); 0 on an error.
 int sm_count();

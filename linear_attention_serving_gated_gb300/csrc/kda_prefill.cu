@@ -1781,6 +1781,8 @@ unsigned transform_grid(int64_t units, int dev) {
 
 cudaEvent_t g_stage_events[3] = {nullptr, nullptr, nullptr};
 
+}  // namespace
+
 // The driver's tensor-map encoder, fetched once through the runtime.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::atomic<void*> fn{nullptr};
@@ -1794,6 +1796,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   }
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
+
+namespace {
 
 // Tensor map of a [T][heads][128] 16-bit tensor, box (box0 elements, 1 head,
 // 64 tokens); elements outside the tensor land as zeros.

@@ -52,6 +52,23 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr) {
   return d;
 }
 
+// As sw128_desc for an operand stored MN-major: 128-byte lines of 64
+// consecutive rows (M or N) of one k, lines of consecutive k 128 bytes apart.
+// Eight k form a 1024-byte swizzle atom (stride byte offset); the next 64
+// rows follow `rows64_bytes` further on (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem_addr, uint32_t rows64_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((rows64_bytes >> 4) & 0x3FFFu) << 16;  // LBO
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;                     // SBO
+  d |= static_cast<uint64_t>(1u) << 46;                             // version
+  d |= static_cast<uint64_t>(2u) << 61;                             // SWIZZLE_128B
+  return d;
+}
+
+// Operand majors of an instruction descriptor: set for an MN-major A or B.
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
+
 // Instruction descriptor of kind::f16 with BF16 A/B, FP32 accumulator,
 // both operands K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
