@@ -339,15 +339,21 @@ typedef struct {
  *                 (kda_dims.dtype), without it the FP32 log-decay.  A value
  *                 below -128 counts as -128 (its factor is zero in FP32).
  *   beta          [gb_rows, HV] 16-bit: raw beta (beta_is_raw) or beta.
- * No workspace is needed.  intermediate and intermediate_chunks as
- * kda_prefill's: the state at the start of every 64-token chunk.
+ * intermediate and intermediate_chunks as kda_prefill's: the state at the
+ * start of every 64-token chunk.  workspace: none for BF16 token tensors
+ * (NULL, 0); for FP16 kda_gdn_prefill_workspace_size bytes, 16-byte aligned:
+ *   3 * total_tokens * H * 128 * 2 (q and k as BF16 operands).
+ * The first call on each device sets the kernels' shared-memory limits; make
+ * it before capturing calls into a CUDA graph.
  */
+size_t kda_gdn_prefill_workspace_size(kda_dims dims, int64_t total_tokens);
 kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *q,
                            const kda_bf16 *k, const kda_bf16 *v, const void *a,
                            const kda_bf16 *beta, int64_t gb_rows, float *state_pool,
                            int pool_slots, const int32_t *state_idx, const int32_t *cu_seqlens,
                            int num_seqs, int64_t total_tokens, kda_bf16 *o, float *intermediate,
-                           int64_t intermediate_chunks, int32_t *err_flag, void *stream);
+                           int64_t intermediate_chunks, void *workspace, size_t workspace_bytes,
+                           int32_t *err_flag, void *stream);
 
 /*
  * Packed single-token decode, chain verify and tree verify: as

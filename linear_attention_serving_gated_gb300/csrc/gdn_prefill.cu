@@ -24,16 +24,21 @@
 //       D  = T Y          rows 0..63 of [T; P] x Y
 //       dS = K^T D'       128 x DVS x 64, D'_j = e^(c_last - c_j) r_j D_j
 //     then P D for the output while the state is being updated;
-//   * prep groups of 4 warps, on alternating chunks, build T and P ahead of
-//     the chain from [K; Q] K^T (tensor cores), with the 64 x 64 inverse by
-//     blocks of 16 in FP32;
-//   * one warp each issues the chain's products, [K; Q] K^T, and the TMA loads.
+//   * the CTAs that own a head's columns form a cluster.  Its T and P are the
+//     same for all of them, so each CTA's prep group of 4 warps builds them for
+//     every (128 / DVS)-th chunk, ahead of the chain, from [K; Q] K^T (tensor
+//     cores) with the 64 x 64 inverse by blocks of 16 in FP32, and copies them
+//     with the chunk's row factors into the other CTAs' shared memory;
+//   * one warp issues the chain's products, one the TMA loads, and a courier
+//     tells the CTA that fills a slot next that it has been used up here.
 // Y, D' and S enter as MN-major operands: a thread writes one token's (or key
 // channel's) columns with 16-byte stores, never a transpose.
 //
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
-// wherever the state depends on them: S, T, Y and D'.  K and Q are BF16 already;
-// FP16 ones are split exactly.  P alone is rounded to BF16 once (2^-9): it
+// wherever the state depends on them: S, T, Y and D'.  K and Q are BF16 already.
+// FP16 keys are split exactly (11 bits into 8 + 8) and FP16 queries rounded to
+// BF16 by a pass over them before the kernel; FP16 operands would need S and D
+// in FP16 halves, whose range is not the state's.  P alone is rounded to BF16 once (2^-9): it
 // only enters the output, itself rounded to 16 bits.
 #include <atomic>
 
@@ -66,52 +71,69 @@ struct GdnPrefillArgs {
 };
 
 struct GdnMaps {
-  CUtensorMap q, k;
+  CUtensorMap q, k, k_lo;
 };
 
-// Per prep group: what the chain warps read of a chunk (a, s, o, last) and what
-// the group keeps for itself.
+// What the chain warps read of a chunk beside T and P.
 struct ChunkScalars {
-  float a[kC];     // r_i e^(c_i)
-  float s[kC];     // r_j e^(c_last - c_j), 0 past the sequence's end
-  float o[kC];     // scale rq_i e^(c_i)
+  float a[kC];  // r_i e^(c_i)
+  float s[kC];  // r_j e^(c_last - c_j), 0 past the sequence's end
+  float o[kC];  // scale rq_i e^(c_i)
+  float last;   // e^(c_last)
+  float pad[3];
+};
+// The prep group's own.
+struct PrepScalars {
   float hi[kC], lo[kC];  // c_i = hi + lo
   float beta[kC], rk[kC];
-  float last;      // e^(c_last)
-  float pad[3];
+};
+
+struct Bars {
+  uint64_t full[2], free_[2];  // the chain's K/Q stages: landed, consumed
+  uint64_t tail;               // rows past the end of the last chunk zeroed
+  uint64_t p_full, a_full;     // prep: K/Q landed, [K; Q] K^T done
+  uint64_t tp_ready[4], tp_used[4];  // a slot's T, P and scalars: written, consumed by this CTA
+  uint64_t slot_free;          // prep: its next slot has been consumed by every CTA
+  uint64_t s_ready, x_full, y_ready, d_full, u_ready, v_ready, u_full;
+  uint64_t o_full[2];
+  uint32_t tmem;
+  int timed_out;
 };
 
 template <int DVS, bool F16>
 struct Cfg {
-  static constexpr int kStages = DVS == 64 || F16 ? 2 : 3;  // chunks of K and Q in shared memory
-  static constexpr int kGroups = F16 ? 1 : 2;               // prep groups
+  static constexpr int kCl = kHeadDim / DVS;   // CTAs of a cluster
+  // Slots of T and P.  No more than kCl: a chunk's slot is then used up before
+  // the chunk that its own CTA prepares next asks for one, so that one barrier
+  // counts both.
+  static constexpr int kSlots = DVS == 64 || F16 ? 2 : 3;
   static constexpr int kTiles = DVS * 2 / 64;  // 64-wide operand tiles: [hi], [lo], or one [hi | lo]
-  static constexpr int kStageBytes = 32768 * (F16 ? 2 : 1);
-  static constexpr int kS = kStages * kStageBytes;
-  static constexpr int kTP = kS + kTiles * 16384;
+  static constexpr int kStageBytes = 32768 + (F16 ? 16384 : 0);  // [K; Q], K lo
+  static constexpr int kPrep = 2 * kStageBytes;                  // the prep group's K and Q
+  static constexpr int kS = kPrep + kStageBytes;
+  static constexpr int kSlot = kS + kTiles * 16384;
   static constexpr int kTPBytes = 16384 + 8192;  // [T; P] hi, T lo
-  static constexpr int kY = kTP + kGroups * kTPBytes;
+  static constexpr int kCopyBytes = kTPBytes + (int)sizeof(ChunkScalars);
+  static constexpr int kSlotBytes = 25600;
+  static constexpr int kY = kSlot + kSlots * kSlotBytes;
   static constexpr int kD = kY + kTiles * 8192;
-  static constexpr int kScratch = kD + kTiles * 8192;
+  // A, its inverse and the scratch of the inversion: in the prep group's K and
+  // Q where shared memory is short, which are loaded again only after that
+  static constexpr bool kAlias = DVS == 64 || F16;
   static constexpr int kScratchBytes = (kC * kLdA + 32 * kLdZ) * 4;
-  static constexpr int kScalars = kScratch + kGroups * kScratchBytes;
-  static constexpr int kEnd = kScalars + kGroups * (int)sizeof(ChunkScalars);
-  static constexpr int kSmem = kEnd + 1024;  // alignment slack
+  static constexpr int kScratch = kAlias ? kPrep : kD + kTiles * 8192;
+  static constexpr int kScalars = kAlias ? kD + kTiles * 8192 : kScratch + kScratchBytes;
+  static constexpr int kBars = kSlot + kCopyBytes;  // behind the first slot's 25360 bytes
+  static_assert(kCopyBytes + sizeof(Bars) <= kSlotBytes, "barriers");
+  static constexpr int kSmem = kScalars + (int)sizeof(PrepScalars);
   static constexpr int kPrepWarp = kChainWarps;
-  static constexpr int kMmaWarp = kPrepWarp + 4 * kGroups;
-  static constexpr int kThreads = (kMmaWarp + 3) * 32;
+  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kCourierWarp = kMmaWarp + 2;
+  static constexpr int kThreads = (kMmaWarp + 4) * 32;
 };
 
-// TMEM columns
-constexpr int kTmX = 0, kTmD = 64, kTmU = 128, kTmO = 192, kTmA = 320, kTmCols = 512;
-
-struct Bars {
-  uint64_t full[3], ready[3], free_[3];  // K/Q stage: landed, tail zeroed (or split), consumed
-  uint64_t a_full[2];                    // [K; Q] K^T done
-  uint64_t tp_ready[2], tp_free[2];      // T, P and the chunk's scalars
-  uint64_t s_ready, x_full, y_ready, d_full, u_ready, v_ready, u_full;
-  uint64_t o_full[2];
-};
+// TMEM columns; X2 and A2 take the products of FP16 keys' low halves, whose
+// rows 64..127 mean nothing
+constexpr int kTmX = 0, kTmD = 64, kTmU = 128, kTmO = 192, kTmA = 320, kTmX2 = 384, kTmA2 = 448, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -127,6 +149,58 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_peer(const void* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, rank)) : "memory");
+}
+// Shared memory of this CTA -> the same place in a peer, counted on its barrier.
+__device__ __forceinline__ void copy_to_peer(const void* p, uint32_t bytes, const void* bar, uint32_t rank) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          peer_addr(p, rank)),
+      "r"(tc::smem_u32(p)), "r"(bytes), "r"(peer_addr(bar, rank))
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// As warp_wait for a barrier that peers arrive on.
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
+  bool done = false;
+  for (uint32_t i = 0; i < (1u << 22) && !done; ++i) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    done = r != 0;
+  }
+  return __all_sync(0xffffffffu, done);
 }
 
 // A warp's writes to shared memory are for the tensor core, and its TMEM reads
@@ -324,15 +398,15 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     gdn_prefill_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
   using C = Cfg<DVS, F16>;
   constexpr int N = DVS / 2;  // value columns per chain thread
-  constexpr int kSlices = kHeadDim / DVS;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bars;
-  __shared__ uint32_t tmem_slot;
-  __shared__ int timed_out;
-  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slice = blockIdx.x % kSlices;
-  const int unit = blockIdx.x / kSlices;
+  if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
+    if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+    return;
+  }
+  const int slice = (int)cluster_rank();  // the cluster's CTAs are the slices of a head
+  const int unit = blockIdx.x / C::kCl;
   const int h = unit % args.HV, n = unit / args.HV;
   const bool reporter = tid == 0 && slice == 0 && h == 0;
 
@@ -340,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
   if (t0 < 0 || t1 < t0 || t1 > args.total_tokens || (n == 0 && t0 != 0) ||
       (n == args.num_seqs - 1 && t1 != args.total_tokens)) {
     if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
-    return;
+    return;  // here and below the whole cluster returns
   }
   const int L = (int)(t1 - t0);
   if (L == 0) return;
@@ -355,20 +429,22 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
   }
   const int nch = (L + kC - 1) / kC;
 
-  if (warp == C::kMmaWarp) tc::tmem_alloc(&tmem_slot, kTmCols);
+  if (warp == C::kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
-    timed_out = 0;
-    for (int i = 0; i < 3; ++i) {
-      tc::mbar_init(&bars.full[i], 1);
-      tc::mbar_init(&bars.ready[i], 4);
-      tc::mbar_init(&bars.free_[i], 1);
-    }
+    bars.timed_out = 0;
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bars.a_full[i], 1);
-      tc::mbar_init(&bars.tp_ready[i], 4);
-      tc::mbar_init(&bars.tp_free[i], 1 + kChainWarps);
+      tc::mbar_init(&bars.full[i], 1);
+      tc::mbar_init(&bars.free_[i], 1);
       tc::mbar_init(&bars.o_full[i], 1);
     }
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(&bars.tp_ready[i], 1);
+      tc::mbar_init(&bars.tp_used[i], 1 + kChainWarps);
+    }
+    tc::mbar_init(&bars.tail, 1);
+    tc::mbar_init(&bars.p_full, 1);
+    tc::mbar_init(&bars.a_full, 1);
+    tc::mbar_init(&bars.slot_free, C::kCl);
     tc::mbar_init(&bars.s_ready, kChainWarps);
     tc::mbar_init(&bars.x_full, 1);
     tc::mbar_init(&bars.y_ready, kChainWarps / 2);
@@ -380,9 +456,31 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
   }
   tc::tc_fence_before();
   __syncthreads();
+  cluster_sync();  // every CTA's barriers are up
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = bars.tmem;
   bool ok = true;
+  // FP16: K and Q were split by the launch before
+  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  auto load_rows = [&](uint8_t* kq, int c, uint64_t* bar) {
+    tc::mbar_expect_tx(bar, C::kStageBytes);
+    const int tok = (int)t0 + c * kC, hk = h / args.G;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, bar);
+      tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, bar);
+      if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, bar);
+    }
+  };
+  // K rows [len, 64) zeroed by `threads` threads: they belong to the next
+  // sequence or lie past the last token, and NaN times a zero factor is NaN
+  auto zero_tail = [&](uint8_t* kq, int len, int t, int threads) {
+    for (int x = t; x < (kC - len) * 16; x += threads) {
+      *line16(kq + (x & 1) * 16384, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
+      if (F16) *line16(kq + 32768 + (x & 1) * 8192, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
+    }
+  };
 
   if (warp < kChainWarps) {
     // ---------------------------------------------------------------- chain
@@ -419,9 +517,9 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     };
     uint4 vraw[N / 8];
     load_v(0, vraw);
-    for (int c = 0; c < nch && ok; ++c) {
-      const int g = c % C::kGroups;
-      const uint32_t gp = (uint32_t)(c / C::kGroups) & 1u, cp = (uint32_t)c & 1u;
+    for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kSlots;
+      const uint32_t cp = (uint32_t)c & 1u;
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
@@ -431,15 +529,22 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
         }
       }
-      const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kScalars + g * sizeof(ChunkScalars));
-      if (!(ok = warp_wait(&bars.tp_ready[g], gp))) break;
+      const ChunkScalars& sc =
+          *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
+      if (!(ok = warp_wait(&bars.tp_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
       const float last = sc.last, fa = krow ? sc.a[row] : sc.o[row], fs = sc.s[row];
       __syncwarp();
-      if (lane == 0) arrive(&bars.tp_free[g]);
+      if (lane == 0) arrive(&bars.tp_used[sl]);
       if (!(ok = warp_wait(&bars.x_full, cp))) break;
       tc::tc_fence_after();
       float x[N];
       get_acc<N>(lanes + kTmX, half, x);
+      if (F16 && krow) {
+        float x2[N];
+        get_acc<N>(lanes + kTmX2, half, x2);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] += x2[j];
+      }
       if (krow) {
         // Y = v - r e^c (K S)
         const uint32_t* vw = reinterpret_cast<const uint32_t*>(vraw);
@@ -499,17 +604,15 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       for (int j = 0; j < N; ++j) root[j * kHeadDim] = S[j];
   } else if (warp < C::kMmaWarp) {
     // ----------------------------------------------------------------- prep
-    const int g = (warp - C::kPrepWarp) >> 2;
-    const int t = tid - (C::kPrepWarp + 4 * g) * 32, quad = warp & 3;
-    const int bar_id = 1 + g;
+    const int t = tid - C::kPrepWarp * 32, quad = warp & 3;
+    const int bar_id = 1;
     const bool krow = quad < 2;
     const int i = 32 * (quad & 1) + lane;  // token of the chunk
-    const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + kTmA + 64 * g;
-    uint8_t* tp_hi = smem + C::kTP + g * C::kTPBytes;
-    uint8_t* tp_lo = tp_hi + 16384;
-    float* am = reinterpret_cast<float*>(smem + C::kScratch + g * C::kScratchBytes);
+    const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16);
+    uint8_t* kq = smem + C::kPrep;
+    float* am = reinterpret_cast<float*>(smem + C::kScratch);
     float* zm = am + kC * kLdA;
-    ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(smem + C::kScalars + g * sizeof(ChunkScalars));
+    PrepScalars& ps = *reinterpret_cast<PrepScalars*>(smem + C::kScalars);
     const ScalarGateArgs& ga = args.gate;
     const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
     const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
@@ -528,58 +631,65 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         }
       }
     };
-    if (quad == 3) load_gate(g);
-    for (int c = g; c < nch; c += C::kGroups) {
-      const int k = c / C::kGroups, st = c % C::kStages;
+    if (quad == 3) load_gate(slice);
+    if (t == 0 && slice < nch) load_rows(kq, slice, &bars.p_full);
+    for (int c = slice, k = 0; c < nch; c += C::kCl, ++k) {
+      const int sl = c % C::kSlots;
       const int len = L - c * kC < kC ? L - c * kC : kC;
-      uint8_t* kq = smem + st * C::kStageBytes;
-      bool bad = !warp_wait(&bars.full[st], (uint32_t)(c / C::kStages) & 1u);
+      uint8_t* tp_hi = smem + C::kSlot + sl * C::kSlotBytes;
+      uint8_t* tp_lo = tp_hi + 16384;
+      ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(tp_hi + C::kTPBytes);
+      bool bad = !warp_wait(&bars.p_full, (uint32_t)k & 1u);
+      if (len < kC) {
+        zero_tail(kq, len, t, 128);
+        tc::fence_async_smem();
+        group_sync(bar_id);
+      }
+      if (quad == 0 && !bad && elect_one()) {  // [K; Q] K^T
+        constexpr uint32_t kIdA = tc::idesc_bf16_f32(128, 64);
+        const uint64_t hi = tc::sw128_desc(tc::smem_u32(kq)), lo = tc::sw128_desc(tc::smem_u32(kq + 32768));
+        tc::tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t off = ((j >> 2) * 16384 + (j & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + kTmA, hi + off, hi + off, kIdA, j > 0);
+        }
+        if constexpr (F16) {  // K = hi + lo: K hi K lo^T, Q K lo^T beside, and K lo K hi^T apart
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            tc::mma_bf16(tmem + kTmA, hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
+                         lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kIdA, true);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            tc::mma_bf16(tmem + kTmA2, lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4),
+                         hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4), kIdA, j > 0);
+        }
+        tc::mma_commit(&bars.a_full);
+      }
+      __syncwarp();
       const int row = krow ? i : 64 + i;  // row of [K; Q]
       float ss = 0.f;
-      if constexpr (F16) {
-        // FP16 rows as two BF16 halves (exact: 11 bits into 8 + 8), K rows past the end zero
-        const bool drop = krow && i >= len;
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            uint4* src = line16(kq + a * 16384, row, p);
-            const uint4 w = *src;
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            float f[8];
+        for (int p = 0; p < 8; ++p) {
+          const uint4 w = *line16(kq + a * 16384, row, p);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint4 w2 = make_uint4(0, 0, 0, 0);
+          if (F16 && krow) w2 = *line16(kq + 32768 + a * 8192, row, p);
+          const uint32_t ww2[4] = {w2.x, w2.y, w2.z, w2.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              f[e] = drop ? 0.f : in16_to_float<true>((uint16_t)(e & 1 ? ww[e / 2] >> 16 : ww[e / 2] & 0xffffu));
-              ss = fmaf(f[e], f[e], ss);
+          for (int e = 0; e < 4; ++e) {
+            float f0 = __uint_as_float(ww[e] << 16), f1 = __uint_as_float(ww[e] & 0xffff0000u);
+            if (F16) {
+              f0 += __uint_as_float(ww2[e] << 16);
+              f1 += __uint_as_float(ww2[e] & 0xffff0000u);
             }
-            uint4 hi, lo;
-            split8(f, hi, lo);
-            *src = hi;
-            *line16(kq + 32768 + a * 16384, row, p) = lo;
+            ss = fmaf(f0, f0, fmaf(f1, f1, ss));
           }
         }
-      } else if (len < kC) {  // rows of the next sequence, or past the last: K rows zero
-        for (int x = t; x < (kC - len) * 16; x += 128)
-          *line16(kq + (x & 1) * 16384, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
-      }
-      warp_arrive(&bars.ready[st], lane);
-      if constexpr (!F16) {
-        if (len < kC) group_sync(bar_id);  // other threads' zeros are read below
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint4 w = *line16(kq + a * 16384, row, p);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f0 = __uint_as_float(ww[e] << 16), f1 = __uint_as_float(ww[e] & 0xffff0000u);
-              ss = fmaf(f0, f0, fmaf(f1, f1, ss));
-            }
-          }
-      }
       const float r = (krow ? 1.f : ga.scale) * (ga.use_qk_l2norm ? rsqrtf(ss + kNormEps) : 1.f);
-      if (krow) sc.rk[i] = r;
+      if (krow) ps.rk[i] = r;
       if (quad == 3) {  // running sums of the log-decays, in FP64, kept as two floats
         const double g0 = gl[0], g1 = g0 + (double)gl[1];
         double run = g1;
@@ -589,43 +699,45 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           if (lane >= d) run += up;
         }
         const double c1 = run, c0 = run - (double)gl[1];
-        sc.hi[2 * lane] = (float)c0;
-        sc.lo[2 * lane] = (float)(c0 - (double)(float)c0);
-        sc.hi[2 * lane + 1] = (float)c1;
-        sc.lo[2 * lane + 1] = (float)(c1 - (double)(float)c1);
-        sc.beta[2 * lane] = be[0];
-        sc.beta[2 * lane + 1] = be[1];
-        load_gate(c + C::kGroups);
+        ps.hi[2 * lane] = (float)c0;
+        ps.lo[2 * lane] = (float)(c0 - (double)(float)c0);
+        ps.hi[2 * lane + 1] = (float)c1;
+        ps.lo[2 * lane + 1] = (float)(c1 - (double)(float)c1);
+        ps.beta[2 * lane] = be[0];
+        ps.beta[2 * lane + 1] = be[1];
+        load_gate(c + C::kCl);
       }
-      // the previous chunk's T, P and scalars of this group have been used
-      if (k > 0) bad |= !warp_wait(&bars.tp_free[g], (uint32_t)(k - 1) & 1u);
-      bad |= !warp_wait(&bars.a_full[g], (uint32_t)k & 1u);
+      bad |= !warp_wait(&bars.a_full, (uint32_t)k & 1u);
       if (group_any(bar_id, bad)) {
         ok = false;
         break;
       }
-      tc::tc_fence_after();
-      const float ci_hi = sc.hi[i], ci_lo = sc.lo[i];
-      const float ei = __expf(ci_hi + ci_lo);
-      if (krow) {
-        sc.a[i] = r * ei;
-        sc.s[i] = i < len ? r * __expf((sc.hi[63] - ci_hi) + (sc.lo[63] - ci_lo)) : 0.f;
-        if (i == 63) sc.last = ei;
-      } else {
-        sc.o[i] = r * ei;
+      if (!C::kAlias && t == 0 && c + C::kCl < nch) {
+        tc::fence_async_smem();  // the reads above come before the copies
+        load_rows(kq, c + C::kCl, &bars.p_full);
       }
-      const float ri = krow ? r * sc.beta[i] : r;
+      tc::tc_fence_after();
+      const float ci_hi = ps.hi[i], ci_lo = ps.lo[i];
+      const float ei = __expf(ci_hi + ci_lo);
+      const float si = krow && i < len ? r * __expf((ps.hi[63] - ci_hi) + (ps.lo[63] - ci_lo)) : 0.f;
+      const float ri = krow ? r * ps.beta[i] : r;
       const int top = 32 * (quad & 1) + 31;  // last row of this warp
+      uint4 prow[8];  // P's row, kept until the slot is free
 #pragma unroll
       for (int jb = 0; jb < 4; ++jb) {
         float d[16];
-        const bool any = 16 * jb <= top;
-        if (any) {
-          tc::tmem_ld16(acc + 16 * jb, d);
+        if (16 * jb <= top) {
+          tc::tmem_ld16(acc + kTmA + 16 * jb, d);
+          if (F16 && krow) {
+            float d2[16];
+            tc::tmem_ld16(acc + kTmA2 + 16 * jb, d2);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) d[e] += d2[e];
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int j = 16 * jb + e;
-            const float f = ri * sc.rk[j] * __expf((ci_hi - sc.hi[j]) + (ci_lo - sc.lo[j]));
+            const float f = ri * ps.rk[j] * __expf((ci_hi - ps.hi[j]) + (ci_lo - ps.lo[j]));
             d[e] = (krow ? j < i : j <= i) ? f * d[e] : 0.f;
           }
         } else {
@@ -638,13 +750,30 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
             *reinterpret_cast<float4*>(am + i * kLdA + 16 * jb + 4 * e) =
                 make_float4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
         } else {
-          *line16(tp_hi, 64 + i, 2 * jb) = round8(d);
-          *line16(tp_hi, 64 + i, 2 * jb + 1) = round8(d + 8);
+          prow[2 * jb] = round8(d);
+          prow[2 * jb + 1] = round8(d + 8);
         }
       }
       tc::tc_fence_before();
       group_sync(bar_id);
       invert64(am, zm, t, bar_id);
+      // the slot's last chunk has been used by every CTA of the cluster
+      if (c >= C::kSlots) {
+        bad = !warp_wait_cluster(&bars.slot_free, (uint32_t)(k - (C::kSlots > slice ? 1 : 0)) & 1u);
+        if (group_any(bar_id, bad)) {
+          ok = false;
+          break;
+        }
+      }
+      if (krow) {
+        sc.a[i] = r * ei;
+        sc.s[i] = si;
+        if (i == 63) sc.last = ei;
+      } else {
+        sc.o[i] = r * ei;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) *line16(tp_hi, 64 + i, p) = prow[p];
+      }
       {  // T Diag(beta), half a row a thread
         const int ti = t >> 1, j0 = (t & 1) * 32;
 #pragma unroll
@@ -653,7 +782,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int j = j0 + 8 * p + e;
-            f[e] = j <= ti ? am[ti * kLdA + j] * sc.beta[j] : 0.f;
+            f[e] = j <= ti ? am[ti * kLdA + j] * ps.beta[j] : 0.f;
           }
           uint4 hi, lo;
           split8(f, hi, lo);
@@ -661,133 +790,140 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           *line16(tp_lo, ti, (j0 >> 3) + p) = lo;
         }
       }
-      warp_arrive(&bars.tp_ready[g], lane);
-      group_sync(bar_id);  // the scratch and scalars are rewritten by the next chunk
+      tc::fence_async_smem();
+      group_sync(bar_id);  // all of the slot is written, and the scratch is free
+      if (t == 0) {
+        arrive(&bars.tp_ready[sl]);
+#pragma unroll
+        for (int p = 1; p < C::kCl; ++p)
+          copy_to_peer(tp_hi, C::kCopyBytes, &bars.tp_ready[sl], (uint32_t)(slice + p) % C::kCl);
+        if (C::kAlias && c + C::kCl < nch) load_rows(kq, c + C::kCl, &bars.p_full);
+      }
     }
   } else if (warp == C::kMmaWarp) {
     // ----------------------------------------------------- the chain's products
-    if (lane == 0) {
-      constexpr uint32_t kIdX = tc::idesc_bf16_f32(128, 64) | tc::kIdescMnB;
-      constexpr uint32_t kIdU = kIdX | tc::kIdescMnA;
-      const uint32_t s_op = tc::smem_u32(smem + C::kS), y_op = tc::smem_u32(smem + C::kY),
-                     d_op = tc::smem_u32(smem + C::kD);
-      for (int c = 0; c < nch; ++c) {
-        const int g = c % C::kGroups, st = c % C::kStages;
-        const uint32_t gp = (uint32_t)(c / C::kGroups) & 1u, cp = (uint32_t)c & 1u;
-        const uint32_t kq = tc::smem_u32(smem + st * C::kStageBytes);
-        const uint32_t tp = tc::smem_u32(smem + C::kTP + g * C::kTPBytes);
-        if (!(ok = tc::mbar_wait(&bars.ready[st], (uint32_t)(c / C::kStages) & 1u))) break;
-        if (!(ok = tc::mbar_wait(&bars.s_ready, cp))) break;
-        tc::tc_fence_after();
-        // X = [K; Q] S
+    constexpr uint32_t kIdX = tc::idesc_bf16_f32(128, 64) | tc::kIdescMnB;
+    constexpr uint32_t kIdU = kIdX | tc::kIdescMnA;
+    const bool leader = elect_one();
+    const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
+    const uint64_t y_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kY), 0);
+    const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
+    for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kSlots, st = c & 1;
+      const uint32_t cp = (uint32_t)c & 1u;
+      const uint32_t kq = tc::smem_u32(smem + st * C::kStageBytes);
+      const uint64_t tp = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes));
+      const uint64_t kq_op = tc::sw128_desc(kq), kt_op = tc::sw128_desc_mn(kq, 16384);
+      const uint64_t kl_op = tc::sw128_desc(kq + 32768), klt_op = tc::sw128_desc_mn(kq + 32768, 8192);
+      if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
+      if (c == nch - 1 && L % kC != 0 && !(ok = warp_wait(&bars.tail, 0))) break;
+      if (!(ok = warp_wait(&bars.s_ready, cp))) break;
+      tc::tc_fence_after();
+      if (leader) {  // X = [K; Q] S
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX, tc::sw128_desc(kq + (j >> 2) * 16384 + (j & 3) * 32),
-                         tc::sw128_desc_mn(s_op + b * 16384 + j * 2048, 0), kIdX, b + j > 0);
+            tc::mma_bf16(tmem + kTmX, kq_op + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
+                         s_op + ((b * 16384 + j * 2048) >> 4), kIdX, b + j > 0);
         if constexpr (F16) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX, tc::sw128_desc(kq + 32768 + (j >> 2) * 16384 + (j & 3) * 32),
-                         tc::sw128_desc_mn(s_op + j * 2048, 0), kIdX, true);
+            tc::mma_bf16(tmem + kTmX2, kl_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kIdX,
+                         j > 0);
         }
         tc::mma_commit(&bars.x_full);
-        if (!(ok = tc::mbar_wait(&bars.tp_ready[g], gp))) break;
-        if (!(ok = tc::mbar_wait(&bars.y_ready, cp))) break;
-        tc::tc_fence_after();
-        // D = T Y (rows 0..63)
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(&bars.tp_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+      if (!(ok = warp_wait(&bars.y_ready, cp))) break;
+      tc::tc_fence_after();
+      if (leader) {  // D = T Y (rows 0..63)
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmD, tc::sw128_desc(tp + j * 32), tc::sw128_desc_mn(y_op + b * 8192 + j * 2048, 0), kIdX,
-                         b + j > 0);
+            tc::mma_bf16(tmem + kTmD, tp + ((j * 32) >> 4), y_op + ((b * 8192 + j * 2048) >> 4), kIdX, b + j > 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          tc::mma_bf16(tmem + kTmD, tc::sw128_desc(tp + 16384 + j * 32), tc::sw128_desc_mn(y_op + j * 2048, 0), kIdX, true);
+          tc::mma_bf16(tmem + kTmD, tp + ((16384 + j * 32) >> 4), y_op + ((j * 2048) >> 4), kIdX, true);
         tc::mma_commit(&bars.d_full);
-        if (!(ok = tc::mbar_wait(&bars.u_ready, cp))) break;
-        tc::tc_fence_after();
-        // dS = K^T D'
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(&bars.u_ready, cp))) break;
+      tc::tc_fence_after();
+      if (leader) {  // dS = K^T D'
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmU, tc::sw128_desc_mn(kq + j * 2048, 16384),
-                         tc::sw128_desc_mn(y_op + b * 8192 + j * 2048, 0), kIdU, b + j > 0);
+            tc::mma_bf16(tmem + kTmU, kt_op + ((j * 2048) >> 4), y_op + ((b * 8192 + j * 2048) >> 4), kIdU, b + j > 0);
         if constexpr (F16) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmU, tc::sw128_desc_mn(kq + 32768 + j * 2048, 16384),
-                         tc::sw128_desc_mn(y_op + j * 2048, 0), kIdU, true);
+            tc::mma_bf16(tmem + kTmU, klt_op + ((j * 2048) >> 4), y_op + ((j * 2048) >> 4), kIdU, true);
         }
         tc::mma_commit(&bars.u_full);
         tc::mma_commit(&bars.free_[st]);
-        if (!(ok = tc::mbar_wait(&bars.v_ready, cp))) break;
-        tc::tc_fence_after();
-        // P D (rows 64..127)
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(&bars.v_ready, cp))) break;
+      tc::tc_fence_after();
+      if (leader) {  // P D (rows 64..127)
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO + 64 * (c & 1), tc::sw128_desc(tp + j * 32),
-                         tc::sw128_desc_mn(d_op + b * 8192 + j * 2048, 0), kIdX, b + j > 0);
+            tc::mma_bf16(tmem + kTmO + 64 * (c & 1), tp + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
+                         b + j > 0);
         tc::mma_commit(&bars.o_full[c & 1]);
-        tc::mma_commit(&bars.tp_free[g]);
+        tc::mma_commit(&bars.tp_used[sl]);
       }
+      __syncwarp();
     }
-  } else if (warp == C::kMmaWarp + 1) {
-    // ------------------------------------------------------------ [K; Q] K^T
-    if (lane == 0) {
-      constexpr uint32_t kIdA = tc::idesc_bf16_f32(128, 64);
-      for (int c = 0; c < nch; ++c) {
-        const int st = c % C::kStages;
-        const uint32_t kq = tc::smem_u32(smem + st * C::kStageBytes);
-        if (!(ok = tc::mbar_wait(&bars.ready[st], (uint32_t)(c / C::kStages) & 1u))) break;
-        tc::tc_fence_after();
-        const uint32_t d = tmem + kTmA + 64 * (c % C::kGroups);
-        const uint32_t lo = kq + 32768;  // FP16: hi hi + hi lo + lo hi
-#pragma unroll
-        for (int p = 0; p < (F16 ? 3 : 1); ++p)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t off = (j >> 2) * 16384 + (j & 3) * 32;
-            tc::mma_bf16(d, tc::sw128_desc((p == 2 ? lo : kq) + off), tc::sw128_desc((p == 1 ? lo : kq) + off), kIdA,
-                         p + j > 0);
-          }
-        tc::mma_commit(&bars.a_full[c % C::kGroups]);
-      }
-    }
-  } else {
+  } else if (warp == C::kLoadWarp) {
     // -------------------------------------------------------------- TMA loads
-    if (lane == 0) {
-      int issued = 0;
-      for (int c = 0; c < nch; ++c) {
-        const int st = c % C::kStages;
-        if (c >= C::kStages &&
-            !(ok = tc::mbar_wait(&bars.free_[st], (uint32_t)(c / C::kStages - 1) & 1u)))
-          break;
-        uint8_t* kq = smem + st * C::kStageBytes;
-        tc::mbar_expect_tx(&bars.full[st], 32768);
-        const int tok = (int)t0 + c * kC, hk = h / args.G;
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, &bars.full[st]);
-          tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, &bars.full[st]);
-        }
-        issued = c + 1;
+    const bool leader = elect_one();
+    for (int c = 0; c < nch; ++c) {
+      const int st = c & 1;
+      if (c >= 2 && !(ok = warp_wait(&bars.free_[st], (uint32_t)(c / 2 - 1) & 1u))) break;
+      uint8_t* kq = smem + st * C::kStageBytes;
+      if (leader) load_rows(kq, c, &bars.full[st]);
+      __syncwarp();
+      if (c == nch - 1 && L % kC != 0) {
+        if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
+        zero_tail(kq, L % kC, lane, 32);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (leader) arrive(&bars.tail);
       }
-      // nothing may land after the CTA is gone
-      for (int c = issued > C::kStages ? issued - C::kStages : 0; c < issued; ++c)
-        tc::mbar_wait(&bars.full[c % C::kStages], (uint32_t)(c / C::kStages) & 1u);
+    }
+  } else if (warp == C::kCourierWarp) {
+    // ---------------------------------------------------------------- courier
+    const bool leader = elect_one();
+    auto expect = [&](int c) {  // a peer's copy will land in this slot
+      if (leader && c < nch && c % C::kCl != slice) tc::mbar_expect_tx(&bars.tp_ready[c % C::kSlots], C::kCopyBytes);
+    };
+    for (int c = 0; c < C::kSlots; ++c) expect(c);
+    for (int c = 0; c + C::kSlots < nch; ++c) {
+      if (!(ok = warp_wait(&bars.tp_used[c % C::kSlots], (uint32_t)(c / C::kSlots) & 1u))) break;
+      expect(c + C::kSlots);
+      if (leader) arrive_peer(&bars.slot_free, (uint32_t)(c + C::kSlots) % C::kCl);
+      __syncwarp();
     }
   }
-  if (!ok) timed_out = 1;
+  if (!ok) bars.timed_out = 1;
   tc::tc_fence_before();
   __syncthreads();
+  // peers copy into this CTA's shared memory and signal its barriers
+  cluster_sync();
   tc::tc_fence_after();
-  if (tid == 0 && timed_out) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+  if (bars.timed_out) {
+    if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+    // every role has stopped, but not all copies were waited for: none takes
+    // this long, and none may land after the CTA is gone
+    for (int i = 0; i < 4; ++i) __nanosleep(500000);
+  }
   if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
 }
 
@@ -805,10 +941,33 @@ bool encode_half_rows(CUtensorMap* m, const void* base, int64_t heads, int64_t T
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// FP16 q and k as the BF16 operands of the kernel: keys as two halves, whose sum
+// is the key, queries rounded.  One 16-byte piece of each a thread.
+__global__ void __launch_bounds__(256) split_rows_kernel(const uint4* __restrict__ q, const uint4* __restrict__ k,
+                                                         int64_t n, uint4* q_hi, uint4* k_hi, uint4* k_lo) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const uint4 wq = __ldg(q + i), wk = __ldg(k + i);
+  const uint32_t a[4] = {wq.x, wq.y, wq.z, wq.w}, b[4] = {wk.x, wk.y, wk.z, wk.w};
+  float fq[8], fk[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    fq[e] = in16_to_float<true>((uint16_t)(e & 1 ? a[e / 2] >> 16 : a[e / 2] & 0xffffu));
+    fk[e] = in16_to_float<true>((uint16_t)(e & 1 ? b[e / 2] >> 16 : b[e / 2] & 0xffffu));
+  }
+  uint4 hi, lo;
+  split8(fk, hi, lo);
+  q_hi[i] = round8(fq);
+  k_hi[i] = hi;
+  k_lo[i] = lo;
+}
+
 template <int DVS, bool F16>
 kda_status launch_prefill(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
   using C = Cfg<DVS, F16>;
-  static_assert(C::kSmem + 1024 <= 232448, "shared memory of one CTA");
+  static_assert(C::kSmem <= 232448, "shared memory of one CTA");
+  static_assert(C::kSlots <= C::kCl && sizeof(ChunkScalars) % 16 == 0, "slots");
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
@@ -818,14 +977,23 @@ kda_status launch_prefill(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_
       return KDA_ERR_CUDA;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  const int64_t grid = (int64_t)a.num_seqs * a.HV * (kHeadDim / DVS);
+  const int64_t grid = (int64_t)a.num_seqs * a.HV * C::kCl;
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  record_stage(0, st);
-  gdn_prefill_kernel<DVS, F16><<<(unsigned)grid, C::kThreads, C::kSmem, st>>>(a, m);
-  const kda_status s = launch_status();
-  record_stage(1, st);
-  record_stage(2, st);
-  return s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C::kCl;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // behind split_rows_kernel
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = F16 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, gdn_prefill_kernel<DVS, F16>, a, m);
+  return launch_status();
 }
 
 }  // namespace
@@ -833,12 +1001,18 @@ kda_status launch_prefill(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_
 
 using namespace kda;
 
+extern "C" size_t kda_gdn_prefill_workspace_size(kda_dims dims, int64_t total_tokens) {
+  if (dims.dtype != KDA_DTYPE_F16 || dims.H <= 0 || total_tokens < 0) return 0;
+  if (total_tokens > INT32_MAX) return SIZE_MAX;  // refused; no capacity check may pass
+  return 3 * (size_t)total_tokens * dims.H * kHeadDim * 2;
+}
+
 extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
                                       const kda_bf16* v, const void* a, const kda_bf16* beta, int64_t gb_rows,
                                       float* state_pool, int pool_slots, const int32_t* state_idx,
                                       const int32_t* cu_seqlens, int num_seqs, int64_t total_tokens, kda_bf16* o,
-                                      float* intermediate, int64_t intermediate_chunks, int32_t* err_flag,
-                                      void* stream) {
+                                      float* intermediate, int64_t intermediate_chunks, void* workspace,
+                                      size_t workspace_bytes, int32_t* err_flag, void* stream) {
   kda_status s = check_dims(dims);
   if (s != KDA_OK) return s;
   if (!state_pool || !state_idx) return KDA_ERR_NULL_ARG;
@@ -852,6 +1026,9 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state_pool) ||
       !aligned16(intermediate))
     return KDA_ERR_ALIGNMENT;
+  const size_t need = kda_gdn_prefill_workspace_size(dims, total_tokens);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
   GdnPrefillArgs args{};
   s = check_scalar_gate(gate, a, beta, &args.gate);
   if (s != KDA_OK) return s;
@@ -871,13 +1048,32 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.intermediate = intermediate;
   args.inter_chunks = intermediate_chunks;
   args.err_flag = err_flag;
-  GdnMaps m;
-  if (!encode_half_rows(&m.q, q, dims.H, total_tokens) || !encode_half_rows(&m.k, k, dims.H, total_tokens))
-    return KDA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dims.dtype == KDA_DTYPE_F16) return launch_prefill<32, true>(args, m, st);
+  const bool f16 = dims.dtype == KDA_DTYPE_F16;
+  const size_t part = need / 3;
+  char* ws = static_cast<char*>(workspace);
+  GdnMaps m{};
+  if (!encode_half_rows(&m.q, f16 ? static_cast<const void*>(ws) : q, dims.H, total_tokens) ||
+      !encode_half_rows(&m.k, f16 ? static_cast<const void*>(ws + part) : k, dims.H, total_tokens) ||
+      (f16 && !encode_half_rows(&m.k_lo, ws + 2 * part, dims.H, total_tokens)))
+    return KDA_ERR_CUDA;
+  record_stage(0, st);
+  if (f16) {
+    const int64_t n = total_tokens * dims.H * (kHeadDim / 8);
+    split_rows_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
+        reinterpret_cast<const uint4*>(q), reinterpret_cast<const uint4*>(k), n, reinterpret_cast<uint4*>(ws),
+        reinterpret_cast<uint4*>(ws + part), reinterpret_cast<uint4*>(ws + 2 * part));
+    s = launch_status();
+    if (s != KDA_OK) return s;
+  }
+  record_stage(1, st);
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
-  return (int64_t)num_seqs * dims.HV * 4 <= sms ? launch_prefill<32, false>(args, m, st)
-                                                : launch_prefill<64, false>(args, m, st);
+  if (f16)
+    s = launch_prefill<32, true>(args, m, st);
+  else
+    s = (int64_t)num_seqs * dims.HV * 4 <= sms ? launch_prefill<32, false>(args, m, st)
+                                               : launch_prefill<64, false>(args, m, st);
+  record_stage(2, st);
+  return s;
 }

@@ -72,7 +72,7 @@ class kda_pages(ctypes.Structure):
 EXPORTS = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill", "kda_decode_packed",
            "kda_verify_chain", "kda_verify_tree", "kda_commit", "kda_set_stage_events",
            "kda_prefill_noalloc", "kda_replay_ring_bytes", "kda_verify_chain_replay",
-           "kda_commit_replay", "kda_gdn_prefill", "kda_gdn_decode_packed", "kda_gdn_verify_chain",
+           "kda_commit_replay", "kda_gdn_prefill_workspace_size", "kda_gdn_prefill", "kda_gdn_decode_packed", "kda_gdn_verify_chain",
            "kda_gdn_verify_tree", "kda_accept_chain", "kda_accept_tree", "kda_pool_copy", "kda_pool_free",
            "kda_pool_compact", "kda_pool_fork")
 
@@ -118,8 +118,10 @@ def load(path: str = LIB_PATH):
         lib.kda_commit_replay.restype = i32
         lib.kda_commit_replay.argtypes = [kda_dims, vp, i32, i32, vp, vp, i32, vp, vp, vp]
         lib.kda_gdn_prefill.restype = i32
+        lib.kda_gdn_prefill_workspace_size.restype = sz
+        lib.kda_gdn_prefill_workspace_size.argtypes = [kda_dims, i64]
         lib.kda_gdn_prefill.argtypes = [kda_dims, kda_scalar_gate, vp, vp, vp, vp, vp, i64, vp, i32, vp, vp,
-                                        i32, i64, vp, vp, i64, vp, vp]
+                                        i32, i64, vp, vp, i64, vp, sz, vp, vp]
         lib.kda_gdn_decode_packed.restype = i32
         lib.kda_gdn_decode_packed.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, vp, i32, vp, i32, vp,
                                               vp, vp, vp]
@@ -457,8 +459,12 @@ def _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, rows, reqs):
     _at_least(state_idx, reqs, "state_idx", f"[{reqs}]")
 
 
+def kda_gdn_prefill_workspace_size(d: kda_dims, total_tokens: int) -> int:
+    return int(load().kda_gdn_prefill_workspace_size(d, int(total_tokens)))
+
+
 def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, cu_seqlens, num_seqs, o,
-                    intermediate=None, err_flag=None, stream=None):
+                    intermediate=None, workspace=None, err_flag=None, stream=None):
     """Varlen prefill (see kda.h).  q,k [T,H,K], v [T,HV,V], a and b
     [gb_rows,HV]; state_pool [slots,HV,V,K] fp32 (in place); o [T,HV,V]
     (written)."""
@@ -478,11 +484,15 @@ def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, c
     _at_least(state_idx, num_seqs, "state_idx", f"[{num_seqs}]")
     _at_least(cu_seqlens, num_seqs + 1, "cu_seqlens", f"[{num_seqs + 1}]")
     inter_chunks = _intermediate_chunks(d, intermediate)
+    if workspace is None and d.dtype == KDA_DTYPE_F16:
+        workspace = torch.empty(max(kda_gdn_prefill_workspace_size(d, T), 1), dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = load().kda_gdn_prefill(
         d, gate.c(d), _in16(d, q, "q"), _in16(d, k, "k"), _in16(d, v, "v"), _scalar_gate_input(d, gate, a),
         _in16(d, b, "b"), int(gb_rows), _typed(state_pool, torch.float32, "state_pool"), int(state_pool.shape[0]),
         _typed(state_idx, torch.int32, "state_idx"), _typed(cu_seqlens, torch.int32, "cu_seqlens"), int(num_seqs),
-        int(T), _in16(d, o, "o"), _p(intermediate), inter_chunks, _p(err_flag), _stream(stream))
+        int(T), _in16(d, o, "o"), _p(intermediate), inter_chunks, _p(workspace), ws_bytes, _p(err_flag),
+        _stream(stream))
     _check(st, "kda_gdn_prefill")
 
 

@@ -27,8 +27,10 @@ def sgate(A_log=D):
 def test_gdn_host_errors(lib):
     row = 3 * 16 * 128
 
-    def pre(d=kda.dims(16), g=sgate(), q=D, a=D, pool=D, idx=D, gb=64, T=64, n=1, inter=None, chunks=0):
-        return lib.kda_gdn_prefill(d, g, q, D, D, a, D, gb, pool, 4, idx, None, n, T, D, inter, chunks, None, None)
+    def pre(d=kda.dims(16), g=sgate(), q=D, a=D, pool=D, idx=D, gb=64, T=64, n=1, inter=None, chunks=0,
+            ws=None, ws_bytes=0):
+        return lib.kda_gdn_prefill(d, g, q, D, D, a, D, gb, pool, 4, idx, None, n, T, D, inter, chunks, ws, ws_bytes,
+                                   None, None)
 
     assert pre(pool=None) == pre(idx=None) == pre(q=None) == kda.KDA_ERR_NULL_ARG
     assert pre(gb=63) == pre(T=65, gb=65, n=2) == pre(T=2 ** 31, gb=2 ** 31) == kda.KDA_ERR_SHAPE
@@ -37,6 +39,11 @@ def test_gdn_host_errors(lib):
     assert pre(q=ODD) == pre(pool=ODD) == kda.KDA_ERR_ALIGNMENT
     assert pre(g=sgate(None), a=ODD) == pre(a=ctypes.c_void_p(0x10001)) == kda.KDA_ERR_ALIGNMENT
     assert pre(T=0, gb=0) == kda.KDA_OK  # nothing to do
+    f16 = kda.dims(16, dtype=kda.KDA_DTYPE_F16)
+    assert kda.kda_gdn_prefill_workspace_size(f16, 64) == 3 * 64 * 16 * 256
+    assert kda.kda_gdn_prefill_workspace_size(kda.dims(16), 64) == 0
+    assert pre(d=f16) == pre(d=f16, ws=D, ws_bytes=3 * 64 * 16 * 256 - 1) == kda.KDA_ERR_WORKSPACE
+    assert pre(d=f16, ws=ODD, ws_bytes=1 << 30) == kda.KDA_ERR_ALIGNMENT
 
     def dec(d=kda.dims(16), stride=row, pool=D, qkv=D, B=2):
         return lib.kda_gdn_decode_packed(d, sgate(), qkv, stride, D, D, B, pool, 240, D, D, None, None)
