@@ -4,8 +4,8 @@
 // Per (sequence, value head), 64 tokens at a time.  c_i is the log-decay summed
 // up to token i of the chunk, r_i the inverse norm of its key, S (K x V) the
 // state before the chunk:
-//   A_ij = beta_i r_i r_j e^(c_i - c_j) k_i.k_j  (j < i),   T = (I + A)^-1
-//   X = K S,  Y_i = v_i - r_i e^(c_i) X_i,                  D = T Diag(beta) Y
+//   A_ij = r_i r_j e^(c_i - c_j) k_i.k_j  (j < i),   T = (Diag(1 / beta) + A)^-1
+//   X = K S,  Y_i = v_i - r_i e^(c_i) X_i,           D = T Y
 //   O_i = scale rq_i e^(c_i) (Q S)_i + sum_(j <= i) P_ij D_j,
 //         P_ij = scale rq_i r_j e^(c_i - c_j) q_i.k_j
 //   S <- e^(c_last) S + sum_j e^(c_last - c_j) r_j k_j D_j^T
@@ -27,8 +27,8 @@
 //   * the CTAs that own a head's columns form a cluster.  Its T and P are the
 //     same for all of them, so each CTA's prep group of 4 warps builds them for
 //     every (128 / DVS)-th chunk, ahead of the chain, from [K; Q] K^T (tensor
-//     cores) with the 64 x 64 inverse by blocks of 16 in FP32, and copies them
-//     with the chunk's row factors into the other CTAs' shared memory;
+//     cores), inverts by blocks, and copies them with the chunk's row factors into
+//     the other CTAs' shared memory; a warp beside it sums up the decays;
 //   * one warp issues the chain's products, one the TMA loads, and a courier
 //     tells the CTA that fills a slot next that it has been used up here.
 // Y, D' and S enter as MN-major operands: a thread writes one token's (or key
@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kC = 64;  // tokens per chunk
 constexpr int kChainWarps = 8;
-constexpr int kLdA = 68, kLdZ = 36;  // FP32 row strides: 16-byte aligned, rows on different banks
+constexpr int kLdG = 20;  // row stride of the FP32 diagonal blocks of A
 
 struct GdnPrefillArgs {
   ScalarGateArgs gate;
@@ -82,20 +82,23 @@ struct ChunkScalars {
   float last;   // e^(c_last)
   float pad[3];
 };
-// The prep group's own.
-struct PrepScalars {
+// Decays and betas of a chunk that this CTA prepares.
+struct GateScalars {
   float hi[kC], lo[kC];  // c_i = hi + lo
-  float beta[kC], rk[kC];
+  float beta[kC];
 };
 
 struct Bars {
   uint64_t full[2], free_[2];  // the chain's K/Q stages: landed, consumed
   uint64_t tail;               // rows past the end of the last chunk zeroed
   uint64_t p_full, a_full;     // prep: K/Q landed, [K; Q] K^T done
-  uint64_t tp_ready[4], tp_used[4];  // a slot's T, P and scalars: written, consumed by this CTA
+  uint64_t g_ready[2], g_free[2];    // its decays and betas
+  uint64_t t_ready[3], p_ready[3], used[3];  // a slot's T and scalars, its P: written; all consumed by this CTA
   uint64_t slot_free;          // prep: its next slot has been consumed by every CTA
   uint64_t s_ready, x_full, y_ready, d_full, u_ready, v_ready, u_full;
   uint64_t o_full[2];
+};
+struct Misc {
   uint32_t tmem;
   int timed_out;
 };
@@ -112,23 +115,28 @@ struct Cfg {
   static constexpr int kPrep = 2 * kStageBytes;                  // the prep group's K and Q
   static constexpr int kS = kPrep + kStageBytes;
   static constexpr int kSlot = kS + kTiles * 16384;
-  static constexpr int kTPBytes = 16384 + 8192;  // [T; P] hi, T lo
+  static constexpr int kTPBytes = 16384 + 8192;  // T hi, P, T lo, then the scalars
   static constexpr int kCopyBytes = kTPBytes + (int)sizeof(ChunkScalars);
   static constexpr int kSlotBytes = 25600;
   static constexpr int kY = kSlot + kSlots * kSlotBytes;
   static constexpr int kD = kY + kTiles * 8192;
-  // A, its inverse and the scratch of the inversion: in the prep group's K and
-  // Q where shared memory is short, which are loaded again only after that
-  static constexpr bool kAlias = DVS == 64 || F16;
-  static constexpr int kScratchBytes = (kC * kLdA + 32 * kLdZ) * 4;
-  static constexpr int kScratch = kAlias ? kPrep : kD + kTiles * 8192;
-  static constexpr int kScalars = kAlias ? kD + kTiles * 8192 : kScratch + kScratchBytes;
-  static constexpr int kBars = kSlot + kCopyBytes;  // behind the first slot's 25360 bytes
+  // The prep group's A (hi, lo, diagonal blocks in FP32) lies in its K and Q,
+  // which are loaded again only when T is there; T waits for its slot in memory
+  // of its own, or, with FP16's larger stages, beside A.
+  static constexpr int kA = kPrep;
+  static constexpr int kABytes = 2 * 8192 + 4 * 16 * kLdG * 4;
+  static constexpr int kT = F16 ? kPrep + 22528 : kD + kTiles * 8192;  // T hi, T lo
+  static_assert(kABytes <= 22528 && (!F16 || 22528 + 16384 <= kStageBytes), "A and T beside each other");
+  static constexpr int kScalars = F16 ? kD + kTiles * 8192 : kT + 16384;
+  static constexpr int kBars = kSlot + kCopyBytes, kMisc = kBars + kSlotBytes;  // behind the slots' 25360 bytes
   static_assert(kCopyBytes + sizeof(Bars) <= kSlotBytes, "barriers");
-  static constexpr int kSmem = kScalars + (int)sizeof(PrepScalars);
+  static constexpr int kGates = DVS == 64 || F16 ? 1 : 2;  // buffers of decays and betas
+  static constexpr int kRk = kScalars + kGates * (int)sizeof(GateScalars);  // inverse key norms
+  static constexpr int kSmem = kRk + kC * 4;
   static constexpr int kPrepWarp = kChainWarps;
-  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kCourierWarp = kMmaWarp + 2;
-  static constexpr int kThreads = (kMmaWarp + 4) * 32;
+  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kCourierWarp = kMmaWarp + 2,
+                       kGateWarp = kMmaWarp + 3;
+  static constexpr int kThreads = (kGateWarp + 1) * 32;
 };
 
 // TMEM columns; X2 and A2 take the products of FP16 keys' low halves, whose
@@ -297,100 +305,160 @@ __device__ __forceinline__ int64_t seq_start(const GdnPrefillArgs& a, int n) {
   return a.cu_seqlens ? (int64_t)a.cu_seqlens[n] : a.total_tokens / a.num_seqs * n;
 }
 
-// (I + A)^-1 in place in `m` ([64][kLdA], A strictly lower, rest ignored above
-// the diagonal blocks), 128 threads; z: [32][kLdZ] scratch.  Diagonal blocks of
-// 16 by forward substitution, one warp each, a column per lane; then
-// T21 = -T22 (A21 T11) for blocks of 16 and of 32.
-__device__ __forceinline__ void invert64(float* m, float* z, int t, int bar_id) {
-  const int warp = t >> 5, lane = t & 31;
+// Fragments of 16 x 16 (or 8 x 16) pieces of 128-byte-swizzled BF16 tiles for
+// the register-to-register products of the inversion, which are too small and
+// too close together for a trip through TMEM.
+__device__ __forceinline__ uint32_t elem_addr(const uint8_t* tile, int row, int col) {
+  return tc::smem_u32(tile) + row * 128 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Left operand: rows [r0, r0 + 16), columns [k0, k0 + 16) of the tile.
+__device__ __forceinline__ void frag_left(const uint8_t* tile, int r0, int k0, int lane, uint32_t (&f)[4]) {
+  ldm4(elem_addr(tile, r0 + (lane & 15), k0 + 8 * (lane >> 4)), f);
+}
+// Left operand, the transpose of rows [k0, k0 + 16), columns [m0, m0 + 16).
+__device__ __forceinline__ void frag_left_t(const uint8_t* tile, int k0, int m0, int lane, uint32_t (&f)[4]) {
+  ldm4t(elem_addr(tile, k0 + (lane & 7) + 8 * (lane >> 4), m0 + (lane & 8)), f);
+}
+// Right operand, the transpose of rows [n0, n0 + 16), columns [k0, k0 + 16):
+// {f0, f1} for n0.., {f2, f3} for n0 + 8...
+__device__ __forceinline__ void frag_right_t(const uint8_t* tile, int n0, int k0, int lane, uint32_t (&f)[4]) {
+  ldm4(elem_addr(tile, n0 + (lane & 7) + 8 * (lane >> 4), k0 + (lane & 8)), f);
+}
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+  const __nv_bfloat162 c =
+      __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+  lo = *reinterpret_cast<const uint32_t*>(&c);
+}
+
+// One warp: 16 rows [r0, ..) and 16 columns [c0, ..) of -T22 (A21 T11), KB blocks
+// of 16 in the middle (rows and columns of T11 from k0, rows of A21 and of T22
+// from l0).  T11 is lower triangular, so the blocks above column block c0 are
+// skipped, and those of T22 right of row block r0.  (A21 T11)^T comes out of the
+// first products in the layout in which the second ones take it.  Every factor
+// is a BF16 pair; lo lo is left out (2^-16).
+template <int KB>
+__device__ __forceinline__ void inverse_block(uint8_t* t_hi, uint8_t* t_lo, const uint8_t* a_hi, const uint8_t* a_lo,
+                                              int k0, int l0, int r0, int c0, int lane) {
+  float z[2 * KB][4];
+#pragma unroll
+  for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[i][e] = 0.f;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int k = k0 + 16 * kb;
+    if (k < c0) continue;
+    uint32_t th[4], tl[4];
+    frag_left_t(t_hi, k, c0, lane, th);
+    frag_left_t(t_lo, k, c0, lane, tl);
+#pragma unroll
+    for (int ib = 0; ib < KB; ++ib) {
+      if (l0 + 16 * ib > r0) continue;  // rows that T22's row block does not use
+      uint32_t ah[4], al[4];
+      frag_right_t(a_hi, l0 + 16 * ib, k, lane, ah);
+      frag_right_t(a_lo, l0 + 16 * ib, k, lane, al);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        mma16(z[2 * ib + p], th, al[2 * p], al[2 * p + 1]);
+        mma16(z[2 * ib + p], tl, ah[2 * p], ah[2 * p + 1]);
+        mma16(z[2 * ib + p], th, ah[2 * p], ah[2 * p + 1]);
+      }
+    }
+  }
+  float w[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[i][e] = 0.f;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int k = l0 + 16 * kb;
+    if (k > r0) continue;
+    uint32_t th[4], tl[4];
+    frag_left(t_hi, r0, k, lane, th);
+    frag_left(t_lo, r0, k, lane, tl);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {  // columns c0 + 8 p ..
+      uint32_t h0, l0_, h1, l1;
+      split2(z[2 * kb][2 * p], z[2 * kb][2 * p + 1], h0, l0_);
+      split2(z[2 * kb + 1][2 * p], z[2 * kb + 1][2 * p + 1], h1, l1);
+      mma16(w[p], th, l0_, l1);
+      mma16(w[p], tl, h0, h1);
+      mma16(w[p], th, h0, h1);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi, lo;
+      split2(-w[p][2 * e], -w[p][2 * e + 1], hi, lo);
+      const int row = r0 + (lane >> 2) + 8 * e, col = c0 + 8 * p + 2 * (lane & 3);
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(elem_addr(t_hi, row, col)), "r"(hi) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(elem_addr(t_lo, row, col)), "r"(lo) : "memory");
+    }
+}
+
+// T = (Diag(1 / beta) + A)^-1 by blocks, 128 threads, into the tiles t_hi, t_lo
+// (whose blocks above the diagonal are zero already): diagonal blocks of 16 by
+// forward substitution in FP32, x_i = beta_i (e_i - sum_(j < i) A_ij x_j), one
+// warp each and a column per lane; then T21 = -T22 A21 T11 for blocks of 16 and
+// of 32.  diag: FP32 diagonal blocks of A.
+__device__ __forceinline__ void invert64(uint8_t* t_hi, uint8_t* t_lo, const uint8_t* a_hi, const uint8_t* a_lo,
+                                         const float* diag, const float* beta, int warp, int lane, int bar_id) {
   {
-    float* d = m + warp * 16 * (kLdA + 1);
+    const float* d = diag + warp * 16 * kLdG;
     const int col = lane & 15;
     float x[16];
-    float4 row[4];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
+      float4 row[4];
 #pragma unroll
-      for (int j = 0; j < (i + 3) / 4; ++j) row[j] = *reinterpret_cast<const float4*>(d + i * kLdA + 4 * j);
+      for (int j = 0; j < (i + 3) / 4; ++j) row[j] = *reinterpret_cast<const float4*>(d + i * kLdG + 4 * j);
       const float* r = reinterpret_cast<const float*>(row);
       float s0 = col == i ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
       for (int j = 0; j < i; ++j) {
         if (j & 1) s1 = fmaf(-r[j], x[j], s1); else s0 = fmaf(-r[j], x[j], s0);
       }
-      x[i] = s0 + s1;
+      x[i] = beta[16 * warp + i] * (s0 + s1);
     }
-    __syncwarp();
-    if (lane < 16)
+    uint8_t* tile = lane < 16 ? t_hi : t_lo;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) d[i * kLdA + col] = x[i];
+    for (int i = 0; i < 16; ++i) {
+      uint16_t hi, lo;
+      tc::split_bf16(x[i], hi, lo);
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(elem_addr(tile, 16 * warp + i, 16 * warp + col)),
+                   "h"(lane < 16 ? hi : lo)
+                   : "memory");
+    }
   }
   group_sync(bar_id);
-  {  // blocks (1,0) and (3,2): 64 threads each, a row and 4 columns a thread
-    const int p = t >> 6, r = (t & 63) >> 2, c = (t & 3) * 4;
-    float* a21 = m + (32 * p + 16) * kLdA + 32 * p;
-    const float* t11 = m + 32 * p * (kLdA + 1);
-    const float* t22 = m + (32 * p + 16) * (kLdA + 1);
-    float* zz = z + p * 16 * kLdZ;
-    auto mul = [&](const float* left, const float* right, int ld) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4) {
-        const float4 l = *reinterpret_cast<const float4*>(left + 4 * k4);
-        const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 b = *reinterpret_cast<const float4*>(right + (4 * k4 + e) * ld + c);
-          acc.x = fmaf(lv[e], b.x, acc.x);
-          acc.y = fmaf(lv[e], b.y, acc.y);
-          acc.z = fmaf(lv[e], b.z, acc.z);
-          acc.w = fmaf(lv[e], b.w, acc.w);
-        }
-      }
-      return acc;
-    };
-    const float4 y = mul(a21 + r * kLdA, t11, kLdA);
-    *reinterpret_cast<float4*>(zz + r * kLdZ + c) = y;
-    group_sync(bar_id);
-    const float4 w = mul(t22 + r * kLdA, zz, kLdZ);
-    *reinterpret_cast<float4*>(a21 + r * kLdA + c) = make_float4(-w.x, -w.y, -w.z, -w.w);
-  }
+  if (warp < 2)
+    inverse_block<1>(t_hi, t_lo, a_hi, a_lo, 32 * warp, 32 * warp + 16, 32 * warp + 16, 32 * warp, lane);
   group_sync(bar_id);
-  {  // block (2..3, 0..1): 2 rows and 4 columns a thread
-    const int r = (t >> 3) * 2, c = (t & 7) * 4;
-    float* a21 = m + 32 * kLdA;
-    auto mul = [&](const float* left, const float* right, int ld, float4 (&acc)[2]) {
-      acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k4 = 0; k4 < 8; ++k4) {
-        const float4 l0 = *reinterpret_cast<const float4*>(left + 4 * k4);
-        const float4 l1 = *reinterpret_cast<const float4*>(left + kLdA + 4 * k4);
-        const float v0[4] = {l0.x, l0.y, l0.z, l0.w}, v1[4] = {l1.x, l1.y, l1.z, l1.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 b = *reinterpret_cast<const float4*>(right + (4 * k4 + e) * ld + c);
-          acc[0].x = fmaf(v0[e], b.x, acc[0].x);
-          acc[0].y = fmaf(v0[e], b.y, acc[0].y);
-          acc[0].z = fmaf(v0[e], b.z, acc[0].z);
-          acc[0].w = fmaf(v0[e], b.w, acc[0].w);
-          acc[1].x = fmaf(v1[e], b.x, acc[1].x);
-          acc[1].y = fmaf(v1[e], b.y, acc[1].y);
-          acc[1].z = fmaf(v1[e], b.z, acc[1].z);
-          acc[1].w = fmaf(v1[e], b.w, acc[1].w);
-        }
-      }
-    };
-    float4 acc[2];
-    mul(a21 + r * kLdA, m, kLdA, acc);
-    *reinterpret_cast<float4*>(z + r * kLdZ + c) = acc[0];
-    *reinterpret_cast<float4*>(z + (r + 1) * kLdZ + c) = acc[1];
-    group_sync(bar_id);
-    mul(m + (32 + r) * kLdA + 32, z, kLdZ, acc);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      *reinterpret_cast<float4*>(a21 + (r + e) * kLdA + c) = make_float4(-acc[e].x, -acc[e].y, -acc[e].z, -acc[e].w);
-  }
-  group_sync(bar_id);
+  inverse_block<2>(t_hi, t_lo, a_hi, a_lo, 0, 32, 32 + 16 * (warp >> 1), 16 * (warp & 1), lane);
 }
 
 template <int DVS, bool F16>
@@ -400,6 +468,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
   constexpr int N = DVS / 2;  // value columns per chain thread
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
+  Misc& misc = *reinterpret_cast<Misc*>(smem + C::kMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
     if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
@@ -429,17 +498,22 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
   }
   const int nch = (L + kC - 1) / kC;
 
-  if (warp == C::kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
+  if (warp == C::kMmaWarp) tc::tmem_alloc(&misc.tmem, kTmCols);
   if (tid == 0) {
-    bars.timed_out = 0;
+    misc.timed_out = 0;
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.full[i], 1);
       tc::mbar_init(&bars.free_[i], 1);
       tc::mbar_init(&bars.o_full[i], 1);
     }
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&bars.tp_ready[i], 1);
-      tc::mbar_init(&bars.tp_used[i], 1 + kChainWarps);
+      tc::mbar_init(&bars.t_ready[i], 1);
+      tc::mbar_init(&bars.p_ready[i], 1);
+      tc::mbar_init(&bars.used[i], 1 + kChainWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bars.g_ready[i], 1);
+      tc::mbar_init(&bars.g_free[i], 1);
     }
     tc::mbar_init(&bars.tail, 1);
     tc::mbar_init(&bars.p_full, 1);
@@ -454,11 +528,14 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     tc::mbar_init(&bars.u_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (!F16)  // blocks of T above the diagonal are never written
+    for (int i = tid; i < 16384 / 16; i += C::kThreads) reinterpret_cast<uint4*>(smem + C::kT)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   cluster_sync();  // every CTA's barriers are up
   tc::tc_fence_after();
-  const uint32_t tmem = bars.tmem;
+  const uint32_t tmem = misc.tmem;
   bool ok = true;
   // FP16: K and Q were split by the launch before
   if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -531,10 +608,10 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       }
       const ChunkScalars& sc =
           *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
-      if (!(ok = warp_wait(&bars.tp_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+      if (!(ok = warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
       const float last = sc.last, fa = krow ? sc.a[row] : sc.o[row], fs = sc.s[row];
       __syncwarp();
-      if (lane == 0) arrive(&bars.tp_used[sl]);
+      if (lane == 0) arrive(&bars.used[sl]);
       if (!(ok = warp_wait(&bars.x_full, cp))) break;
       tc::tc_fence_after();
       float x[N];
@@ -610,35 +687,20 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     const int i = 32 * (quad & 1) + lane;  // token of the chunk
     const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16);
     uint8_t* kq = smem + C::kPrep;
-    float* am = reinterpret_cast<float*>(smem + C::kScratch);
-    float* zm = am + kC * kLdA;
-    PrepScalars& ps = *reinterpret_cast<PrepScalars*>(smem + C::kScalars);
+    uint8_t* a_hi = smem + C::kA;
+    uint8_t* a_lo = a_hi + 8192;
+    uint8_t* t_hi = smem + C::kT;
+    uint8_t* t_lo = t_hi + 8192;
+    float* diag = reinterpret_cast<float*>(a_lo + 8192);
+    float* rks = reinterpret_cast<float*>(smem + C::kRk);
     const ScalarGateArgs& ga = args.gate;
-    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
-    // the gate warp's lane takes tokens 2 lane and 2 lane + 1
-    float gl[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};
-    auto load_gate = [&](int c) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tok = c * kC + 2 * lane + e;
-        gl[e] = be[e] = 0.f;
-        if (c < nch && tok < L) {
-          const int64_t at = (t0 + tok) * args.HV + h;
-          gl[e] = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
-          const float b = in16_to_float<F16>(args.beta[at]);
-          be[e] = ga.beta_is_raw ? sigmoidf_(b) : b;
-        }
-      }
-    };
-    if (quad == 3) load_gate(slice);
     if (t == 0 && slice < nch) load_rows(kq, slice, &bars.p_full);
     for (int c = slice, k = 0; c < nch; c += C::kCl, ++k) {
-      const int sl = c % C::kSlots;
+      const int sl = c % C::kSlots, gb = k % C::kGates;
       const int len = L - c * kC < kC ? L - c * kC : kC;
-      uint8_t* tp_hi = smem + C::kSlot + sl * C::kSlotBytes;
-      uint8_t* tp_lo = tp_hi + 16384;
-      ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(tp_hi + C::kTPBytes);
+      const GateScalars& gs = *reinterpret_cast<const GateScalars*>(smem + C::kScalars + gb * sizeof(GateScalars));
+      uint8_t* slot_s = smem + C::kSlot + sl * C::kSlotBytes;
+      ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(slot_s + C::kTPBytes);
       bool bad = !warp_wait(&bars.p_full, (uint32_t)k & 1u);
       if (len < kC) {
         zero_tail(kq, len, t, 128);
@@ -668,7 +730,9 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       }
       __syncwarp();
       const int row = krow ? i : 64 + i;  // row of [K; Q]
-      float ss = 0.f;
+      float2 ss[4];  // four running sums, for latency
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss[e] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -685,42 +749,36 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
               f0 += __uint_as_float(ww2[e] << 16);
               f1 += __uint_as_float(ww2[e] & 0xffff0000u);
             }
-            ss = fmaf(f0, f0, fmaf(f1, f1, ss));
+            ss[e] = fma2(make_float2(f0, f1), make_float2(f0, f1), ss[e]);
           }
         }
-      const float r = (krow ? 1.f : ga.scale) * (ga.use_qk_l2norm ? rsqrtf(ss + kNormEps) : 1.f);
-      if (krow) ps.rk[i] = r;
-      if (quad == 3) {  // running sums of the log-decays, in FP64, kept as two floats
-        const double g0 = gl[0], g1 = g0 + (double)gl[1];
-        double run = g1;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const double up = __shfl_up_sync(0xffffffffu, run, d);
-          if (lane >= d) run += up;
-        }
-        const double c1 = run, c0 = run - (double)gl[1];
-        ps.hi[2 * lane] = (float)c0;
-        ps.lo[2 * lane] = (float)(c0 - (double)(float)c0);
-        ps.hi[2 * lane + 1] = (float)c1;
-        ps.lo[2 * lane + 1] = (float)(c1 - (double)(float)c1);
-        ps.beta[2 * lane] = be[0];
-        ps.beta[2 * lane + 1] = be[1];
-        load_gate(c + C::kCl);
-      }
+      const float sq = ((ss[0].x + ss[0].y) + (ss[1].x + ss[1].y)) + ((ss[2].x + ss[2].y) + (ss[3].x + ss[3].y));
+      const float r = (krow ? 1.f : ga.scale) * (ga.use_qk_l2norm ? rsqrtf(sq + kNormEps) : 1.f);
+      bad |= !warp_wait(&bars.g_ready[gb], (uint32_t)(k / C::kGates) & 1u);
+      // r_i r_j e^(c_i - c_j) as a product of row and column factors about the
+      // middle of the chunk, where those stay in FP32's range; term by term otherwise
+      const float ci_hi = gs.hi[i], ci_lo = gs.lo[i];
+      const float mid = (ci_hi - gs.hi[kC / 2]) + (ci_lo - gs.lo[kC / 2]);
+      const bool far = !(fabsf(mid) <= 60.f);
+      if (krow) rks[i] = r * expf(-mid);
       bad |= !warp_wait(&bars.a_full, (uint32_t)k & 1u);
-      if (group_any(bar_id, bad)) {
-        ok = false;
-        break;
+      bool wide = false;
+      if (group_any(bar_id, bad || far)) {
+        if (group_any(bar_id, bad)) {
+          ok = false;
+          break;
+        }
+        wide = true;
+        if (krow) rks[i] = r;
+        group_sync(bar_id);
       }
-      if (!C::kAlias && t == 0 && c + C::kCl < nch) {
-        tc::fence_async_smem();  // the reads above come before the copies
-        load_rows(kq, c + C::kCl, &bars.p_full);
+      if (F16) {  // T's place was under K and Q: zeros above the diagonal again
+        for (int x = t; x < 16384 / 16; x += 128) reinterpret_cast<uint4*>(t_hi)[x] = make_uint4(0, 0, 0, 0);
       }
       tc::tc_fence_after();
-      const float ci_hi = ps.hi[i], ci_lo = ps.lo[i];
       const float ei = __expf(ci_hi + ci_lo);
-      const float si = krow && i < len ? r * __expf((ps.hi[63] - ci_hi) + (ps.lo[63] - ci_lo)) : 0.f;
-      const float ri = krow ? r * ps.beta[i] : r;
+      const float ui = wide ? r : r * expf(mid);
+      const float si = krow && i < len ? r * __expf((gs.hi[63] - ci_hi) + (gs.lo[63] - ci_lo)) : 0.f;
       const int top = 32 * (quad & 1) + 31;  // last row of this warp
       uint4 prow[8];  // P's row, kept until the slot is free
 #pragma unroll
@@ -734,21 +792,38 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) d[e] += d2[e];
           }
+          float f[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(f + 4 * e) = *reinterpret_cast<const float4*>(rks + 16 * jb + 4 * e);
+          if (wide) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              f[e] *= __expf((ci_hi - gs.hi[16 * jb + e]) + (ci_lo - gs.lo[16 * jb + e]));
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int j = 16 * jb + e;
-            const float f = ri * ps.rk[j] * __expf((ci_hi - ps.hi[j]) + (ci_lo - ps.lo[j]));
-            d[e] = (krow ? j < i : j <= i) ? f * d[e] : 0.f;
+            d[e] = (krow ? j < i : j <= i) ? (ui * f[e]) * d[e] : 0.f;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) d[e] = 0.f;
         }
         if (krow) {
+          if (jb < (i >> 4)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<float4*>(am + i * kLdA + 16 * jb + 4 * e) =
-                make_float4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
+            for (int p = 0; p < 2; ++p) {
+              uint4 hi, lo;
+              split8(d + 8 * p, hi, lo);
+              *line16(a_hi, i, 2 * jb + p) = hi;
+              *line16(a_lo, i, 2 * jb + p) = lo;
+            }
+          } else if (jb == (i >> 4)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<float4*>(diag + i * kLdG + 4 * e) =
+                  make_float4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
+          }
         } else {
           prow[2 * jb] = round8(d);
           prow[2 * jb + 1] = round8(d + 8);
@@ -756,14 +831,24 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       }
       tc::tc_fence_before();
       group_sync(bar_id);
-      invert64(am, zm, t, bar_id);
+      invert64(t_hi, t_lo, a_hi, a_lo, diag, gs.beta, quad, lane, bar_id);
+      if (!F16) {
+        tc::fence_async_smem();
+        group_sync(bar_id);  // A has been used: the next K and Q may land over it
+        if (t == 0 && c + C::kCl < nch) load_rows(kq, c + C::kCl, &bars.p_full);
+      }
       // the slot's last chunk has been used by every CTA of the cluster
-      if (c >= C::kSlots) {
+      if (c >= C::kSlots)
         bad = !warp_wait_cluster(&bars.slot_free, (uint32_t)(k - (C::kSlots > slice ? 1 : 0)) & 1u);
-        if (group_any(bar_id, bad)) {
-          ok = false;
-          break;
-        }
+      if (group_any(bar_id, bad)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // T hi and lo
+        const int at = (x * 128 + t) * 16;
+        *reinterpret_cast<uint4*>(slot_s + at) = *reinterpret_cast<const uint4*>(t_hi + at);
+        *reinterpret_cast<uint4*>(slot_s + 16384 + at) = *reinterpret_cast<const uint4*>(t_lo + at);
       }
       if (krow) {
         sc.a[i] = r * ei;
@@ -772,32 +857,26 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       } else {
         sc.o[i] = r * ei;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) *line16(tp_hi, 64 + i, p) = prow[p];
-      }
-      {  // T Diag(beta), half a row a thread
-        const int ti = t >> 1, j0 = (t & 1) * 32;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int j = j0 + 8 * p + e;
-            f[e] = j <= ti ? am[ti * kLdA + j] * ps.beta[j] : 0.f;
-          }
-          uint4 hi, lo;
-          split8(f, hi, lo);
-          *line16(tp_hi, ti, (j0 >> 3) + p) = hi;
-          *line16(tp_lo, ti, (j0 >> 3) + p) = lo;
-        }
+        for (int p = 0; p < 8; ++p) *line16(slot_s, 64 + i, p) = prow[p];
       }
       tc::fence_async_smem();
-      group_sync(bar_id);  // all of the slot is written, and the scratch is free
+      group_sync(bar_id);  // all of the slot is written
       if (t == 0) {
-        arrive(&bars.tp_ready[sl]);
+        arrive(&bars.g_free[gb]);
+        arrive(&bars.t_ready[sl]);
+        arrive(&bars.p_ready[sl]);
+        // a peer's shared memory takes about 18 bytes a clock, so what its chain
+        // needs first goes first to all of them
+#pragma unroll
+        for (int p = 1; p < C::kCl; ++p) {
+          const uint32_t to = (uint32_t)(slice + p) % C::kCl;
+          copy_to_peer(slot_s, 8192, &bars.t_ready[sl], to);
+          copy_to_peer(slot_s + 16384, C::kCopyBytes - 16384, &bars.t_ready[sl], to);
+        }
 #pragma unroll
         for (int p = 1; p < C::kCl; ++p)
-          copy_to_peer(tp_hi, C::kCopyBytes, &bars.tp_ready[sl], (uint32_t)(slice + p) % C::kCl);
-        if (C::kAlias && c + C::kCl < nch) load_rows(kq, c + C::kCl, &bars.p_full);
+          copy_to_peer(slot_s + 8192, 8192, &bars.p_ready[sl], (uint32_t)(slice + p) % C::kCl);
+        if (F16 && c + C::kCl < nch) load_rows(kq, c + C::kCl, &bars.p_full);
       }
     }
   } else if (warp == C::kMmaWarp) {
@@ -835,7 +914,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      if (!(ok = warp_wait(&bars.tp_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+      if (!(ok = warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
       if (!(ok = warp_wait(&bars.y_ready, cp))) break;
       tc::tc_fence_after();
       if (leader) {  // D = T Y (rows 0..63)
@@ -867,6 +946,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         tc::mma_commit(&bars.free_[st]);
       }
       __syncwarp();
+      if (!(ok = warp_wait(&bars.p_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
       if (!(ok = warp_wait(&bars.v_ready, cp))) break;
       tc::tc_fence_after();
       if (leader) {  // P D (rows 64..127)
@@ -877,7 +957,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
             tc::mma_bf16(tmem + kTmO + 64 * (c & 1), tp + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
                          b + j > 0);
         tc::mma_commit(&bars.o_full[c & 1]);
-        tc::mma_commit(&bars.tp_used[sl]);
+        tc::mma_commit(&bars.used[sl]);
       }
       __syncwarp();
     }
@@ -902,23 +982,66 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     // ---------------------------------------------------------------- courier
     const bool leader = elect_one();
     auto expect = [&](int c) {  // a peer's copy will land in this slot
-      if (leader && c < nch && c % C::kCl != slice) tc::mbar_expect_tx(&bars.tp_ready[c % C::kSlots], C::kCopyBytes);
+      if (leader && c < nch && c % C::kCl != slice) {
+        tc::mbar_expect_tx(&bars.t_ready[c % C::kSlots], C::kCopyBytes - 8192);
+        tc::mbar_expect_tx(&bars.p_ready[c % C::kSlots], 8192);
+      }
     };
     for (int c = 0; c < C::kSlots; ++c) expect(c);
     for (int c = 0; c + C::kSlots < nch; ++c) {
-      if (!(ok = warp_wait(&bars.tp_used[c % C::kSlots], (uint32_t)(c / C::kSlots) & 1u))) break;
+      if (!(ok = warp_wait(&bars.used[c % C::kSlots], (uint32_t)(c / C::kSlots) & 1u))) break;
       expect(c + C::kSlots);
       if (leader) arrive_peer(&bars.slot_free, (uint32_t)(c + C::kSlots) % C::kCl);
       __syncwarp();
     }
   }
-  if (!ok) bars.timed_out = 1;
+  else {
+    // ------------------------------------------------------------------ gate
+    const ScalarGateArgs& ga = args.gate;
+    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
+    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
+    for (int c = slice, k = 0; c < nch; c += C::kCl, ++k) {
+      const int gb = k % C::kGates;
+      GateScalars& gs = *reinterpret_cast<GateScalars*>(smem + C::kScalars + gb * sizeof(GateScalars));
+      float gl[2], be[2];  // tokens 2 lane, 2 lane + 1; past the end nothing decays and nothing is written
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = c * kC + 2 * lane + e;
+        gl[e] = be[e] = 0.f;
+        if (tok < L) {
+          const int64_t at = (t0 + tok) * args.HV + h;
+          const float b = in16_to_float<F16>(args.beta[at]);
+          gl[e] = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
+          be[e] = ga.beta_is_raw ? sigmoidf_(b) : b;
+        }
+      }
+      // running sums in FP64, kept as two floats: differences of them count
+      const double pair = (double)gl[0] + (double)gl[1];
+      double run = pair;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, run, d);
+        if (lane >= d) run += up;
+      }
+      const double c0 = run - (double)gl[1];
+      if (k >= C::kGates && !(ok = warp_wait(&bars.g_free[gb], (uint32_t)(k / C::kGates - 1) & 1u))) break;
+      gs.hi[2 * lane] = (float)c0;
+      gs.lo[2 * lane] = (float)(c0 - (double)(float)c0);
+      gs.hi[2 * lane + 1] = (float)run;
+      gs.lo[2 * lane + 1] = (float)(run - (double)(float)run);
+      gs.beta[2 * lane] = be[0];
+      gs.beta[2 * lane + 1] = be[1];
+      __syncwarp();
+      if (lane == 0) arrive(&bars.g_ready[gb]);
+    }
+  }
+  if (!ok) misc.timed_out = 1;
   tc::tc_fence_before();
   __syncthreads();
   // peers copy into this CTA's shared memory and signal its barriers
   cluster_sync();
   tc::tc_fence_after();
-  if (bars.timed_out) {
+  if (misc.timed_out) {
     if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
     // every role has stopped, but not all copies were waited for: none takes
     // this long, and none may land after the CTA is gone
