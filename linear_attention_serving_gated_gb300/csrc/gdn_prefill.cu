@@ -18,7 +18,7 @@
 // through memory.  A CTA owns DVS value columns of one head's state; three
 // dependent products a chunk are its chain, and their latency, not bytes or
 // flops, bounds a long sequence, so everything else is kept off it:
-//   * 8 chain warps hold S in FP32 registers and turn each product's TMEM
+//   * 16 chain warps hold S in FP32 registers and turn each product's TMEM
 //     accumulator into the next one's operand; products are
 //       X  = [K; Q] S     128 x DVS x 128  (Q rows ride along for O)
 //       D  = T Y          rows 0..63 of [T; P] x Y
@@ -29,8 +29,9 @@
 //     every (128 / DVS)-th chunk, ahead of the chain, from [K; Q] K^T (tensor
 //     cores), inverts by blocks, and copies them with the chunk's row factors into
 //     the other CTAs' shared memory; a warp beside it sums up the decays;
-//   * one warp issues the chain's products, one the TMA loads, and a courier
-//     tells the CTA that fills a slot next that it has been used up here.
+//   * one warp issues the chain's products, one the TMA loads, and one the
+//     products that only the output needs; it also tells the CTA that fills a
+//     slot next that it has been used up here.
 // Y, D' and S enter as MN-major operands: a thread writes one token's (or key
 // channel's) columns with 16-byte stores, never a transpose.
 //
@@ -49,7 +50,7 @@ namespace kda {
 namespace {
 
 constexpr int kC = 64;  // tokens per chunk
-constexpr int kChainWarps = 8;
+constexpr int kChainWarps = 16;
 constexpr int kLdG = 20;  // row stride of the FP32 diagonal blocks of A
 
 struct GdnPrefillArgs {
@@ -95,7 +96,7 @@ struct Bars {
   uint64_t g_ready[2], g_free[2];    // its decays and betas
   uint64_t t_ready[3], p_ready[3], used[3];  // a slot's T and scalars, its P: written; all consumed by this CTA
   uint64_t slot_free;          // prep: its next slot has been consumed by every CTA
-  uint64_t s_ready, x_full, y_ready, d_full, u_ready, v_ready, u_full;
+  uint64_t s_ready, x_full, xq_full, d_full, v_ready, u_full;
   uint64_t o_full[2];
 };
 struct Misc {
@@ -134,14 +135,15 @@ struct Cfg {
   static constexpr int kRk = kScalars + kGates * (int)sizeof(GateScalars);  // inverse key norms
   static constexpr int kSmem = kRk + kC * 4;
   static constexpr int kPrepWarp = kChainWarps;
-  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kCourierWarp = kMmaWarp + 2,
+  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kOutWarp = kMmaWarp + 2,
                        kGateWarp = kMmaWarp + 3;
   static constexpr int kThreads = (kGateWarp + 1) * 32;
+  static_assert(kThreads == 768, "register split, named barriers");
 };
 
-// TMEM columns; X2 and A2 take the products of FP16 keys' low halves, whose
-// rows 64..127 mean nothing
-constexpr int kTmX = 0, kTmD = 64, kTmU = 128, kTmO = 192, kTmA = 320, kTmX2 = 384, kTmA2 = 448, kTmCols = 512;
+// TMEM columns.  A2 takes the product of FP16 keys' low halves with the high
+// ones, whose rows 64..127 mean nothing.
+constexpr int kTmX = 0, kTmQ = 64, kTmD = 128, kTmU = 192, kTmO = 256, kTmA = 384, kTmA2 = 448, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -233,6 +235,18 @@ __device__ __forceinline__ bool group_any(int id, bool bad) {
       : "memory");
   return r != 0;
 }
+// The chain warps have written the next product's operand: the issuing warp
+// waits for them at the same hardware barrier, which wakes it sooner than an
+// mbarrier would.
+__device__ __forceinline__ void chain_arrive(int id) {
+  tc::fence_async_smem();
+  tc::tc_fence_before();
+  asm volatile("barrier.cta.arrive %0, 544;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void chain_await(int id) {
+  asm volatile("barrier.cta.sync %0, 544;" ::"r"(id) : "memory");
+  tc::tc_fence_after();
+}
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Eight FP32 values as BF16 hi and lo halves.
@@ -265,39 +279,107 @@ __device__ __forceinline__ uint4* line16(uint8_t* tile, int row, int piece) {
   return reinterpret_cast<uint4*>(tile + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-// A row's values as operand halves: columns [half * N, half * N + N) of the CTA's
-// DVS = 2 N, N = 32 in tiles [hi], [lo], N = 16 in one tile [hi | lo].
-template <int N>
-__device__ __forceinline__ void put_split(uint8_t* tiles, int tile_bytes, int row, int half, const float (&x)[N]) {
+// A row's values as operand halves: columns [part * N, part * N + N) of the CTA's
+// DVS = 4 N, in tiles [hi], [lo] 64 wide (DVS = 64) or one tile [hi | lo].
+template <int DVS>
+__device__ __forceinline__ void put_split(uint8_t* tiles, int tile_bytes, int row, int part, const float (&x)[DVS / 4]) {
 #pragma unroll
-  for (int j = 0; j < N / 8; ++j) {
+  for (int j = 0; j < DVS / 32; ++j) {
     uint4 hi, lo;
     split8(x + 8 * j, hi, lo);
-    const int piece = half * (N / 8) + j;
+    const int piece = part * (DVS / 32) + j;
     *line16(tiles, row, piece) = hi;
-    if (N == 32)
+    if (DVS == 64)
       *line16(tiles + tile_bytes, row, piece) = lo;
     else
       *line16(tiles, row, 4 + piece) = lo;
   }
 }
 
-// A warp's accumulator columns of its half: 32 columns, or 16 of the hi product
-// plus the same 16 of the lo product.
-template <int N>
-__device__ __forceinline__ void get_acc(uint32_t taddr, int half, float (&x)[N]) {
-  uint32_t a[16], b[16];
-  tc::tmem_ld16_async(taddr + half * N, a);
-  tc::tmem_ld16_async(taddr + half * N + (N == 32 ? 16 : 32), b);
+__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Waits for this thread's TMEM loads; r is not used before.
+template <int M>
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[M]) {
   tc::tmem_wait_ld();
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (N == 32) {
-      x[j] = __uint_as_float(a[j]);
-      x[(16 + j) % N] = __uint_as_float(b[j]);
-    } else {
-      x[j] = __uint_as_float(a[j]) + __uint_as_float(b[j]);
+  for (int i = 0; i < M; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// A warp's accumulator columns of its part: 16, or 8 of the hi product plus the
+// same 8 of the lo product.
+template <int DVS>
+__device__ __forceinline__ void get_acc(uint32_t taddr, int part, float (&x)[DVS / 4]) {
+  if constexpr (DVS == 64) {
+    uint32_t a[16];
+    tc::tmem_ld16_async(taddr + part * 16, a);
+    wait_ld(a);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(a[j]);
+  } else {
+    uint32_t a[8], b[8];
+    tmem_ld8_async(taddr + part * 8, a);
+    tmem_ld8_async(taddr + 32 + part * 8, b);
+    wait_ld(a);
+    wait_ld(b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(a[j]) + __uint_as_float(b[j]);
+  }
+}
+
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+  const __nv_bfloat162 c =
+      __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+  lo = *reinterpret_cast<const uint32_t*>(&c);
+}
+
+// The same columns as operand halves (see put_split).
+template <int J>
+__device__ __forceinline__ void put_rows(uint8_t* tiles, int row, int part, int lane, const float (&x)[J][4]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi, lo;
+      split2(x[j][2 * e], x[j][2 * e + 1], hi, lo);
+      const int rr = row + 8 * e, piece = part * J + j;
+      uint8_t* line = tiles + rr * 128 + 4 * (lane & 3);
+      *reinterpret_cast<uint32_t*>(line + ((piece ^ (rr & 7)) << 4)) = hi;
+      if (J == 2)
+        *reinterpret_cast<uint32_t*>(line + 8192 + ((piece ^ (rr & 7)) << 4)) = lo;
+      else
+        *reinterpret_cast<uint32_t*>(line + (((4 + piece) ^ (rr & 7)) << 4)) = lo;
     }
+}
+
+// A warp's columns of a token-row accumulator (its part of the slice), 16 rows in
+// the fragment layout: rows lane / 4 and + 8, columns 8 j + 2 (lane % 4) and + 1;
+// 16 columns (J = 2), or 8 of the hi product plus the same 8 of the lo product.
+__device__ __forceinline__ void ld_frag8(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+template <int J>
+__device__ __forceinline__ void get_rows(uint32_t taddr, int part, float (&x)[J][4]) {
+  uint32_t a[4], b[4];
+  ld_frag8(taddr + part * 8 * J, a);
+  ld_frag8(taddr + part * 8 * J + (J == 2 ? 8 : 32), b);
+  wait_ld(a);
+  wait_ld(b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[0][e] = __uint_as_float(a[e]);
+    if (J == 2)
+      x[J - 1][e] = __uint_as_float(b[e]);
+    else
+      x[0][e] += __uint_as_float(b[e]);
   }
 }
 
@@ -342,13 +424,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
-  const __nv_bfloat162 c =
-      __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-  lo = *reinterpret_cast<const uint32_t*>(&c);
 }
 
 // One warp: 16 rows [r0, ..) and 16 columns [c0, ..) of -T22 (A21 T11), KB blocks
@@ -465,7 +540,7 @@ template <int DVS, bool F16>
 __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     gdn_prefill_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
   using C = Cfg<DVS, F16>;
-  constexpr int N = DVS / 2;  // value columns per chain thread
+  constexpr int N = DVS / 4;  // value columns per chain thread
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
   Misc& misc = *reinterpret_cast<Misc*>(smem + C::kMisc);
@@ -503,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     misc.timed_out = 0;
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.full[i], 1);
-      tc::mbar_init(&bars.free_[i], 1);
+      tc::mbar_init(&bars.free_[i], 2);
       tc::mbar_init(&bars.o_full[i], 1);
     }
     for (int i = 0; i < C::kSlots; ++i) {
@@ -521,10 +596,9 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     tc::mbar_init(&bars.slot_free, C::kCl);
     tc::mbar_init(&bars.s_ready, kChainWarps);
     tc::mbar_init(&bars.x_full, 1);
-    tc::mbar_init(&bars.y_ready, kChainWarps / 2);
+    tc::mbar_init(&bars.xq_full, 1);
     tc::mbar_init(&bars.d_full, 1);
-    tc::mbar_init(&bars.u_ready, kChainWarps / 2);
-    tc::mbar_init(&bars.v_ready, kChainWarps / 2);
+    tc::mbar_init(&bars.v_ready, kChainWarps);
     tc::mbar_init(&bars.u_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -559,20 +633,23 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     }
   };
 
+  // 768 threads start with 80 registers each; 72, 144 and 40 use 60416 of those 61440
   if (warp < kChainWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------------------------------------------------------- chain
-    const int quad = warp & 3, half = warp >> 2;
-    const bool krow = quad < 2;
-    const int row = 32 * (quad & 1) + lane;    // token of the chunk (K rows, or Q rows)
+    // A warp that runs out of time goes on without waiting, so that the others
+    // still meet it.
+    constexpr int J = N / 8;
+    const int quad = warp & 3, part = warp >> 2;
+    const int row = 16 * quad + (lane >> 2);   // token rows row and row + 8 of the chunk
+    const int colx = slice * DVS + part * N + 2 * (lane & 3);  // value columns colx + 8 j, + 1 of those
     const int dk = 32 * quad + lane;           // key channel of the state
-    const int col0 = slice * DVS + half * N;
+    const int col0 = slice * DVS + part * N;   // value columns col0 + j of the state
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     float* root = args.pool + (((size_t)slot * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
     float S[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) S[j] = root[j * kHeadDim];
-    put_split<N>(smem + C::kS, 16384, dk, half, S);
-    warp_arrive(&bars.s_ready, lane);
     int64_t cid = 0;  // record of this sequence's first chunk
     if (args.intermediate) {
       for (int m = lane; m < n; m += 32) {
@@ -582,21 +659,43 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
 #pragma unroll
       for (int m = 16; m; m >>= 1) cid += __shfl_xor_sync(0xffffffffu, cid, m);
     }
-    auto load_v = [&](int c, uint4 (&v)[N / 8]) {
-      const int t = c * kC + row;
+    uint32_t vraw[J][2];
+    auto load_v = [&](int c) {
 #pragma unroll
-      for (int j = 0; j < N / 8; ++j) v[j] = make_uint4(0, 0, 0, 0);
-      if (krow && t < L) {
-        const uint4* src = reinterpret_cast<const uint4*>(args.v + ((t0 + t) * args.HV + h) * kHeadDim + col0);
+      for (int e = 0; e < 2; ++e) {
+        const int t = c * kC + row + 8 * e;
+        const kda_bf16* src = args.v + ((t0 + t) * args.HV + h) * kHeadDim + colx;
 #pragma unroll
-        for (int j = 0; j < N / 8; ++j) v[j] = __ldg(src + j);
+        for (int j = 0; j < J; ++j) vraw[j][e] = t < L ? __ldg(reinterpret_cast<const uint32_t*>(src + 8 * j)) : 0u;
       }
     };
-    uint4 vraw[N / 8];
-    load_v(0, vraw);
+    load_v(0);
+    float xq[J][4];  // this chunk's scaled Q S
+    // O = scale rq e^c Q S + P D of chunk c
+    auto finish = [&](int c) {
+      ok = ok && warp_wait(&bars.o_full[c & 1], (uint32_t)(c >> 1) & 1u);
+      tc::tc_fence_after();
+      float u[J][4];
+      get_rows<J>(lanes + kTmO + 64 * (c & 1), part, u);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = c * kC + row + 8 * e;
+        if (t < L) {
+          kda_bf16* dst = args.o + ((t0 + t) * args.HV + h) * kHeadDim + colx;
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            *reinterpret_cast<uint32_t*>(dst + 8 * j) =
+                pack_out16x2<F16>(xq[j][2 * e] + u[j][2 * e], xq[j][2 * e + 1] + u[j][2 * e + 1]);
+        }
+      }
+    };
     for (int c = 0; c < nch; ++c) {
       const int sl = c % C::kSlots;
       const uint32_t cp = (uint32_t)c & 1u;
+      put_split<DVS>(smem + C::kS, 16384, dk, part, S);
+      chain_arrive(2);
+      __syncwarp();
+      if (lane == 0) arrive(&bars.s_ready);  // after chain_arrive's fences
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
@@ -606,80 +705,66 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
         }
       }
+      if (c > 0) finish(c - 1);
       const ChunkScalars& sc =
           *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
-      if (!(ok = warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
-      const float last = sc.last, fa = krow ? sc.a[row] : sc.o[row], fs = sc.s[row];
-      __syncwarp();
-      if (lane == 0) arrive(&bars.used[sl]);
-      if (!(ok = warp_wait(&bars.x_full, cp))) break;
+      ok = ok && warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u);
+      const float last = sc.last;
+      float fa[2] = {sc.a[row], sc.a[row + 8]}, fs[2] = {sc.s[row], sc.s[row + 8]};
+      const float fo[2] = {sc.o[row], sc.o[row + 8]};
+      ok = ok && warp_wait(&bars.x_full, cp);
       tc::tc_fence_after();
-      float x[N];
-      get_acc<N>(lanes + kTmX, half, x);
-      if (F16 && krow) {
-        float x2[N];
-        get_acc<N>(lanes + kTmX2, half, x2);
+      float x[J][4];
+      get_rows<J>(lanes + kTmX, part, x);
+      // Y = v - r e^c (K S)
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] += x2[j];
-      }
-      if (krow) {
-        // Y = v - r e^c (K S)
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vraw);
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const uint32_t w = vw[j / 2];
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = vraw[j][e >> 1];
           float v;
           if constexpr (F16)
-            v = in16_to_float<true>((uint16_t)(j & 1 ? w >> 16 : w & 0xffffu));
+            v = in16_to_float<true>((uint16_t)(e & 1 ? w >> 16 : w & 0xffffu));
           else
-            v = __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
-          x[j] = fmaf(-fa, x[j], v);
+            v = __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+          x[j][e] = fmaf(-fa[e >> 1], x[j][e], v);
         }
-        put_split<N>(smem + C::kY, 8192, row, half, x);
-        warp_arrive(&bars.y_ready, lane);
-        if (c + 1 < nch) load_v(c + 1, vraw);
-        if (!(ok = warp_wait(&bars.d_full, cp))) break;
-        tc::tc_fence_after();
-        get_acc<N>(lanes + kTmD, half, x);
-        float y[N];
+      put_rows<J>(smem + C::kY, row, part, lane, x);
+      chain_arrive(3);
+      if (c + 1 < nch) load_v(c + 1);
+      ok = ok && warp_wait(&bars.d_full, cp);
+      tc::tc_fence_after();
+      get_rows<J>(lanes + kTmD, part, x);
+      float y[J][4];
 #pragma unroll
-        for (int j = 0; j < N; ++j) y[j] = fs * x[j];
-        put_split<N>(smem + C::kY, 8192, row, half, y);
-        warp_arrive(&bars.u_ready, lane);
-        put_split<N>(smem + C::kD, 8192, row, half, x);
-        warp_arrive(&bars.v_ready, lane);
-      }
-      if (!(ok = warp_wait(&bars.u_full, cp))) break;
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[j][e] = fs[e >> 1] * x[j][e];
+      put_rows<J>(smem + C::kY, row, part, lane, y);
+      chain_arrive(4);
+      put_rows<J>(smem + C::kD, row, part, lane, x);
+      warp_arrive(&bars.v_ready, lane);
+      if (lane == 0) arrive(&bars.used[sl]);
+      ok = ok && warp_wait(&bars.xq_full, cp);
+      tc::tc_fence_after();
+      get_rows<J>(lanes + kTmQ, part, xq);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xq[j][e] *= fo[e >> 1];
+      ok = ok && warp_wait(&bars.u_full, cp);
       tc::tc_fence_after();
       float u[N];
-      get_acc<N>(lanes + kTmU, half, u);
+      get_acc<DVS>(lanes + kTmU, part, u);
 #pragma unroll
       for (int j = 0; j < N; ++j) S[j] = fmaf(last, S[j], u[j]);
-      if (c + 1 < nch) put_split<N>(smem + C::kS, 16384, dk, half, S);
-      warp_arrive(&bars.s_ready, lane);
-      if (!krow) {
-        if (!(ok = warp_wait(&bars.o_full[c & 1], (uint32_t)(c >> 1) & 1u))) break;
-        tc::tc_fence_after();
-        get_acc<N>(lanes + kTmO + 64 * (c & 1), half, u);
-        const int t = c * kC + row;
-        if (t < L) {
-          uint4* dst = reinterpret_cast<uint4*>(args.o + ((t0 + t) * args.HV + h) * kHeadDim + col0);
-#pragma unroll
-          for (int j = 0; j < N / 8; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_out16x2<F16>(fmaf(fa, x[8 * j + 2 * e], u[8 * j + 2 * e]),
-                                       fmaf(fa, x[8 * j + 2 * e + 1], u[8 * j + 2 * e + 1]));
-            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
     }
+    finish(nch - 1);
     if (ok)
 #pragma unroll
       for (int j = 0; j < N; ++j) root[j * kHeadDim] = S[j];
   } else if (warp < C::kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // ----------------------------------------------------------------- prep
     const int t = tid - C::kPrepWarp * 32, quad = warp & 3;
     const int bar_id = 1;
@@ -880,58 +965,55 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       }
     }
   } else if (warp == C::kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ----------------------------------------------------- the chain's products
-    constexpr uint32_t kIdX = tc::idesc_bf16_f32(128, 64) | tc::kIdescMnB;
-    constexpr uint32_t kIdU = kIdX | tc::kIdescMnA;
+    // As the chain warps, it goes on without waiting once out of time.
+    constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
+    constexpr uint32_t kIdU = tc::idesc_bf16_f32(128, 64) | tc::kIdescMnA | tc::kIdescMnB;
     const bool leader = elect_one();
     const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
     const uint64_t y_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kY), 0);
-    const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
     for (int c = 0; c < nch; ++c) {
       const int sl = c % C::kSlots, st = c & 1;
-      const uint32_t cp = (uint32_t)c & 1u;
       const uint32_t kq = tc::smem_u32(smem + st * C::kStageBytes);
-      const uint64_t tp = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes));
-      const uint64_t kq_op = tc::sw128_desc(kq), kt_op = tc::sw128_desc_mn(kq, 16384);
-      const uint64_t kl_op = tc::sw128_desc(kq + 32768), klt_op = tc::sw128_desc_mn(kq + 32768, 8192);
-      if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
-      if (c == nch - 1 && L % kC != 0 && !(ok = warp_wait(&bars.tail, 0))) break;
-      if (!(ok = warp_wait(&bars.s_ready, cp))) break;
-      tc::tc_fence_after();
-      if (leader) {  // X = [K; Q] S
+      const uint64_t k_op = tc::sw128_desc(kq), kl_op = tc::sw128_desc(kq + 32768);
+      const uint64_t kt_op = tc::sw128_desc_mn(kq, 16384), klt_op = tc::sw128_desc_mn(kq + 32768, 8192);
+      const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes));
+      ok = ok && warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u);
+      if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
+      chain_await(2);
+      if (leader && ok) {  // X = K S
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX, kq_op + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
+            tc::mma_bf16(tmem + kTmX, k_op + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
                          s_op + ((b * 16384 + j * 2048) >> 4), kIdX, b + j > 0);
         if constexpr (F16) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX2, kl_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kIdX,
-                         j > 0);
+            tc::mma_bf16(tmem + kTmX, kl_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kIdX,
+                         true);
         }
         tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      if (!(ok = warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
-      if (!(ok = warp_wait(&bars.y_ready, cp))) break;
-      tc::tc_fence_after();
-      if (leader) {  // D = T Y (rows 0..63)
+      ok = ok && warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u);
+      chain_await(3);
+      if (leader && ok) {  // D = T Y
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmD, tp + ((j * 32) >> 4), y_op + ((b * 8192 + j * 2048) >> 4), kIdX, b + j > 0);
+            tc::mma_bf16(tmem + kTmD, t_op + ((j * 32) >> 4), y_op + ((b * 8192 + j * 2048) >> 4), kIdX, b + j > 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          tc::mma_bf16(tmem + kTmD, tp + ((16384 + j * 32) >> 4), y_op + ((j * 2048) >> 4), kIdX, true);
+          tc::mma_bf16(tmem + kTmD, t_op + ((16384 + j * 32) >> 4), y_op + ((j * 2048) >> 4), kIdX, true);
         tc::mma_commit(&bars.d_full);
       }
       __syncwarp();
-      if (!(ok = warp_wait(&bars.u_ready, cp))) break;
-      tc::tc_fence_after();
-      if (leader) {  // dS = K^T D'
+      chain_await(4);
+      if (leader && ok) {  // dS = K^T D'
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
@@ -946,22 +1028,9 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         tc::mma_commit(&bars.free_[st]);
       }
       __syncwarp();
-      if (!(ok = warp_wait(&bars.p_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
-      if (!(ok = warp_wait(&bars.v_ready, cp))) break;
-      tc::tc_fence_after();
-      if (leader) {  // P D (rows 64..127)
-#pragma unroll
-        for (int b = 0; b < C::kTiles; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO + 64 * (c & 1), tp + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
-                         b + j > 0);
-        tc::mma_commit(&bars.o_full[c & 1]);
-        tc::mma_commit(&bars.used[sl]);
-      }
-      __syncwarp();
     }
   } else if (warp == C::kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // -------------------------------------------------------------- TMA loads
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
@@ -978,24 +1047,63 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         if (leader) arrive(&bars.tail);
       }
     }
-  } else if (warp == C::kCourierWarp) {
-    // ---------------------------------------------------------------- courier
+  } else if (warp == C::kOutWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    // ------------------------- products for the output alone; the slots' traffic
+    constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
     const bool leader = elect_one();
-    auto expect = [&](int c) {  // a peer's copy will land in this slot
+    auto expect = [&](int c) {  // a peer's copies will land in this slot
       if (leader && c < nch && c % C::kCl != slice) {
         tc::mbar_expect_tx(&bars.t_ready[c % C::kSlots], C::kCopyBytes - 8192);
         tc::mbar_expect_tx(&bars.p_ready[c % C::kSlots], 8192);
       }
     };
     for (int c = 0; c < C::kSlots; ++c) expect(c);
-    for (int c = 0; c + C::kSlots < nch; ++c) {
-      if (!(ok = warp_wait(&bars.used[c % C::kSlots], (uint32_t)(c / C::kSlots) & 1u))) break;
-      expect(c + C::kSlots);
-      if (leader) arrive_peer(&bars.slot_free, (uint32_t)(c + C::kSlots) % C::kCl);
+    const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
+    const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
+    for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kSlots, st = c & 1;
+      const uint32_t cp = (uint32_t)c & 1u;
+      const uint64_t q_op = tc::sw128_desc(tc::smem_u32(smem + st * C::kStageBytes + 8192));
+      const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes + 8192));
+      if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
+      if (!(ok = warp_wait(&bars.s_ready, cp))) break;
+      tc::tc_fence_after();
+      if (leader) {  // Q S
+#pragma unroll
+        for (int b = 0; b < C::kTiles; ++b)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            tc::mma_bf16(tmem + kTmQ, q_op + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
+                         s_op + ((b * 16384 + j * 2048) >> 4), kIdX, b + j > 0);
+        tc::mma_commit(&bars.xq_full);
+        tc::mma_commit(&bars.free_[st]);
+      }
       __syncwarp();
+      if (!(ok = warp_wait(&bars.p_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+      if (!(ok = warp_wait(&bars.v_ready, cp))) break;
+      tc::tc_fence_after();
+      if (leader) {  // P D
+#pragma unroll
+        for (int b = 0; b < C::kTiles; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc::mma_bf16(tmem + kTmO + 64 * (c & 1), p_op + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
+                         b + j > 0);
+        tc::mma_commit(&bars.o_full[c & 1]);
+        tc::mma_commit(&bars.used[sl]);
+      }
+      __syncwarp();
+      // used up here: the CTA that fills the slot next is told
+      if (c + C::kSlots < nch) {
+        if (!(ok = warp_wait(&bars.used[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+        expect(c + C::kSlots);
+        if (leader) arrive_peer(&bars.slot_free, (uint32_t)(c + C::kSlots) % C::kCl);
+        __syncwarp();
+      }
     }
-  }
-  else {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ------------------------------------------------------------------ gate
     const ScalarGateArgs& ga = args.gate;
     const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
