@@ -23,12 +23,13 @@
 //       X  = [K; Q] S     128 x DVS x 128  (Q rows ride along for O)
 //       D  = T Y          rows 0..63 of [T; P] x Y
 //       dS = K^T D'       128 x DVS x 64, D'_j = e^(c_last - c_j) r_j D_j
-//     then P D for the output while the state is being updated;
+//     then P D for the output while the state is being updated, and Q S beside K S;
 //   * the CTAs that own a head's columns form a cluster.  Its T and P are the
 //     same for all of them, so each CTA's prep group of 4 warps builds them for
 //     every (128 / DVS)-th chunk, ahead of the chain, from [K; Q] K^T (tensor
 //     cores), inverts by blocks, and copies them with the chunk's row factors into
 //     the other CTAs' shared memory; a warp beside it sums up the decays;
+//   * 4 output warps join Q S and P D;
 //   * one warp issues the chain's products, one the TMA loads, and one the
 //     products that only the output needs; it also tells the CTA that fills a
 //     slot next that it has been used up here.
@@ -50,7 +51,7 @@ namespace kda {
 namespace {
 
 constexpr int kC = 64;  // tokens per chunk
-constexpr int kChainWarps = 16;
+constexpr int kChainWarps = 16, kOutWarps = 4;
 constexpr int kLdG = 20;  // row stride of the FP32 diagonal blocks of A
 
 struct GdnPrefillArgs {
@@ -97,7 +98,7 @@ struct Bars {
   uint64_t t_ready[3], p_ready[3], used[3];  // a slot's T and scalars, its P: written; all consumed by this CTA
   uint64_t slot_free;          // prep: its next slot has been consumed by every CTA
   uint64_t s_ready, x_full, xq_full, d_full, v_ready, u_full;
-  uint64_t o_full[2];
+  uint64_t o_full, o_read;
 };
 struct Misc {
   uint32_t tmem;
@@ -134,11 +135,11 @@ struct Cfg {
   static constexpr int kGates = DVS == 64 || F16 ? 1 : 2;  // buffers of decays and betas
   static constexpr int kRk = kScalars + kGates * (int)sizeof(GateScalars);  // inverse key norms
   static constexpr int kSmem = kRk + kC * 4;
-  static constexpr int kPrepWarp = kChainWarps;
-  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kOutWarp = kMmaWarp + 2,
+  static constexpr int kPrepWarp = kChainWarps + kOutWarps;
+  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kSideWarp = kMmaWarp + 2,
                        kGateWarp = kMmaWarp + 3;
   static constexpr int kThreads = (kGateWarp + 1) * 32;
-  static_assert(kThreads == 768, "register split, named barriers");
+  static_assert(kThreads == 896, "register split, named barriers");
 };
 
 // TMEM columns.  A2 takes the product of FP16 keys' low halves with the high
@@ -579,12 +580,11 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.full[i], 1);
       tc::mbar_init(&bars.free_[i], 2);
-      tc::mbar_init(&bars.o_full[i], 1);
     }
     for (int i = 0; i < C::kSlots; ++i) {
       tc::mbar_init(&bars.t_ready[i], 1);
       tc::mbar_init(&bars.p_ready[i], 1);
-      tc::mbar_init(&bars.used[i], 1 + kChainWarps);
+      tc::mbar_init(&bars.used[i], 1 + kChainWarps + kOutWarps);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.g_ready[i], 1);
@@ -597,6 +597,8 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     tc::mbar_init(&bars.s_ready, kChainWarps);
     tc::mbar_init(&bars.x_full, 1);
     tc::mbar_init(&bars.xq_full, 1);
+    tc::mbar_init(&bars.o_full, 1);
+    tc::mbar_init(&bars.o_read, kOutWarps);
     tc::mbar_init(&bars.d_full, 1);
     tc::mbar_init(&bars.v_ready, kChainWarps);
     tc::mbar_init(&bars.u_full, 1);
@@ -633,9 +635,9 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     }
   };
 
-  // 768 threads start with 80 registers each; 72, 144 and 40 use 60416 of those 61440
+  // 896 threads start with 72 registers each; 64, 64, 128 and 40 use 62464 of those 64512
   if (warp < kChainWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ---------------------------------------------------------------- chain
     // A warp that runs out of time goes on without waiting, so that the others
     // still meet it.
@@ -660,35 +662,17 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       for (int m = 16; m; m >>= 1) cid += __shfl_xor_sync(0xffffffffu, cid, m);
     }
     uint32_t vraw[J][2];
+    const int64_t vstep = (int64_t)args.HV * kHeadDim;
+    const kda_bf16* vsrc = args.v + ((t0 + row) * args.HV + h) * kHeadDim + colx;
     auto load_v = [&](int c) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = c * kC + row + 8 * e;
-        const kda_bf16* src = args.v + ((t0 + t) * args.HV + h) * kHeadDim + colx;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int j = 0; j < J; ++j) vraw[j][e] = t < L ? __ldg(reinterpret_cast<const uint32_t*>(src + 8 * j)) : 0u;
-      }
+        for (int j = 0; j < J; ++j)
+          vraw[j][e] = c * kC + row + 8 * e < L ? __ldg(reinterpret_cast<const uint32_t*>(vsrc + 8 * e * vstep + 8 * j)) : 0u;
+      vsrc += kC * vstep;
     };
     load_v(0);
-    float xq[J][4];  // this chunk's scaled Q S
-    // O = scale rq e^c Q S + P D of chunk c
-    auto finish = [&](int c) {
-      ok = ok && warp_wait(&bars.o_full[c & 1], (uint32_t)(c >> 1) & 1u);
-      tc::tc_fence_after();
-      float u[J][4];
-      get_rows<J>(lanes + kTmO + 64 * (c & 1), part, u);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = c * kC + row + 8 * e;
-        if (t < L) {
-          kda_bf16* dst = args.o + ((t0 + t) * args.HV + h) * kHeadDim + colx;
-#pragma unroll
-          for (int j = 0; j < J; ++j)
-            *reinterpret_cast<uint32_t*>(dst + 8 * j) =
-                pack_out16x2<F16>(xq[j][2 * e] + u[j][2 * e], xq[j][2 * e + 1] + u[j][2 * e + 1]);
-        }
-      }
-    };
     for (int c = 0; c < nch; ++c) {
       const int sl = c % C::kSlots;
       const uint32_t cp = (uint32_t)c & 1u;
@@ -705,13 +689,11 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
         }
       }
-      if (c > 0) finish(c - 1);
       const ChunkScalars& sc =
           *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
       ok = ok && warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u);
       const float last = sc.last;
       float fa[2] = {sc.a[row], sc.a[row + 8]}, fs[2] = {sc.s[row], sc.s[row + 8]};
-      const float fo[2] = {sc.o[row], sc.o[row + 8]};
       ok = ok && warp_wait(&bars.x_full, cp);
       tc::tc_fence_after();
       float x[J][4];
@@ -742,16 +724,11 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         for (int e = 0; e < 4; ++e) y[j][e] = fs[e >> 1] * x[j][e];
       put_rows<J>(smem + C::kY, row, part, lane, y);
       chain_arrive(4);
+      if (c > 0) ok = ok && warp_wait(&bars.o_full, cp ^ 1u);  // P D of the last chunk has read its D
       put_rows<J>(smem + C::kD, row, part, lane, x);
       warp_arrive(&bars.v_ready, lane);
       if (lane == 0) arrive(&bars.used[sl]);
-      ok = ok && warp_wait(&bars.xq_full, cp);
-      tc::tc_fence_after();
-      get_rows<J>(lanes + kTmQ, part, xq);
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xq[j][e] *= fo[e >> 1];
+      ok = ok && warp_wait(&bars.xq_full, cp);  // Q S has read S
       ok = ok && warp_wait(&bars.u_full, cp);
       tc::tc_fence_after();
       float u[N];
@@ -759,12 +736,59 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < N; ++j) S[j] = fmaf(last, S[j], u[j]);
     }
-    finish(nch - 1);
     if (ok)
 #pragma unroll
       for (int j = 0; j < N; ++j) root[j * kHeadDim] = S[j];
+  } else if (warp < C::kPrepWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // --------------------------------------------------------------- outputs
+    // O = scale rq e^c Q S + P D, 16 token rows a warp.
+    constexpr int J = DVS / 32;
+    const int quad = warp & 3;
+    const int row = 16 * quad + (lane >> 2);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + slice * DVS + 2 * (lane & 3);
+    const int64_t step = (int64_t)args.HV * kHeadDim;
+    for (int c = 0; c < nch; ++c, dst += kC * step) {
+      const int sl = c % C::kSlots;
+      const uint32_t cp = (uint32_t)c & 1u;
+      const ChunkScalars& sc =
+          *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
+      if (!(ok = warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+      const float fo[2] = {sc.o[row], sc.o[row + 8]};
+      __syncwarp();
+      if (lane == 0) arrive(&bars.used[sl]);
+      if (!(ok = warp_wait(&bars.xq_full, cp))) break;
+      if (!(ok = warp_wait(&bars.o_full, cp))) break;
+      tc::tc_fence_after();
+      uint32_t w[4][J][2];
+#pragma unroll
+      for (int part = 0; part < 4; ++part) {
+        float x[J][4], u[J][4];
+        get_rows<J>(lanes + kTmQ, part, x);
+        get_rows<J>(lanes + kTmO, part, u);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            w[part][j][e] = pack_out16x2<F16>(fmaf(fo[e], x[j][2 * e], u[j][2 * e]),
+                                              fmaf(fo[e], x[j][2 * e + 1], u[j][2 * e + 1]));
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&bars.o_read);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (c * kC + row + 8 * e < L) {
+#pragma unroll
+          for (int part = 0; part < 4; ++part)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+              *reinterpret_cast<uint32_t*>(dst + 8 * e * step + 8 * (part * J + j)) = w[part][j][e];
+        }
+    }
   } else if (warp < C::kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // ----------------------------------------------------------------- prep
     const int t = tid - C::kPrepWarp * 32, quad = warp & 3;
     const int bar_id = 1;
@@ -1047,7 +1071,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         if (leader) arrive(&bars.tail);
       }
     }
-  } else if (warp == C::kOutWarp) {
+  } else if (warp == C::kSideWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ------------------------- products for the output alone; the slots' traffic
     constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
@@ -1068,6 +1092,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes + 8192));
       if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
       if (!(ok = warp_wait(&bars.s_ready, cp))) break;
+      if (c > 0 && !(ok = warp_wait(&bars.o_read, cp ^ 1u))) break;  // both accumulators have been read
       tc::tc_fence_after();
       if (leader) {  // Q S
 #pragma unroll
@@ -1088,9 +1113,9 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO + 64 * (c & 1), p_op + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
+            tc::mma_bf16(tmem + kTmO, p_op + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
                          b + j > 0);
-        tc::mma_commit(&bars.o_full[c & 1]);
+        tc::mma_commit(&bars.o_full);
         tc::mma_commit(&bars.used[sl]);
       }
       __syncwarp();
