@@ -340,13 +340,15 @@ typedef struct {
  *                 below -128 counts as -128 (its factor is zero in FP32).
  *   beta          [gb_rows, HV] 16-bit: raw beta (beta_is_raw) or beta.
  * intermediate and intermediate_chunks as kda_prefill's: the state at the
- * start of every 64-token chunk.  workspace: none for BF16 token tensors
- * (NULL, 0); for FP16 kda_gdn_prefill_workspace_size bytes, 16-byte aligned:
- *   3 * total_tokens * H * 128 * 2 (q and k as BF16 operands).
- * The first call on each device sets the kernels' shared-memory limits; make
- * it before capturing calls into a CUDA graph.
+ * start of every 64-token chunk.  workspace: kda_gdn_prefill_workspace_size
+ * bytes, 16-byte aligned:
+ *   (total_tokens / 64 + num_seqs) * HV * 25600      a record per (chunk, head)
+ *   + 3 * align256(total_tokens * H * 256)           FP16 only: q, k as BF16
+ * (SIZE_MAX for more than INT32_MAX tokens).  The first call on each device
+ * sets the kernels' shared-memory limits; make it before capturing calls into
+ * a CUDA graph.
  */
-size_t kda_gdn_prefill_workspace_size(kda_dims dims, int64_t total_tokens);
+size_t kda_gdn_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens);
 kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *q,
                            const kda_bf16 *k, const kda_bf16 *v, const void *a,
                            const kda_bf16 *beta, int64_t gb_rows, float *state_pool,

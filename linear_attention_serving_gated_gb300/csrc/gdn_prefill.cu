@@ -14,28 +14,28 @@
 // they are: K K^T and Q K^T are exact up to FP32 sums, every exponent is of a
 // difference c_i - c_j <= 0, and no decay is too strong for the chunk form.
 //
-// The state stays on the SM for the whole sequence and no workspace goes
-// through memory.  A CTA owns DVS value columns of one head's state; three
-// dependent products a chunk are its chain, and their latency, not bytes or
-// flops, bounds a long sequence, so everything else is kept off it:
+// Two kernels.  Everything of a chunk that does not depend on the state is the
+// same for all value columns and for all chunks at once:
+//   gdn_chunk_kernel, a CTA of 128 threads per (chunk, value head), 3 per SM:
+//     norms, decays, [K; Q] K^T on the tensor cores, A and P, T by blocks, and
+//     one record of 25 KB (T, P, the chunk's row factors) for the second kernel.
+// What is left is a chain of three dependent products a chunk:
+//   gdn_state_kernel, a CTA per (sequence, value head, DVS value columns).  Its
+//     state stays on the SM for the whole sequence.  The chain's latency, not
+//     bytes or flops, bounds a long sequence, so nothing else is on it:
 //   * 16 chain warps hold S in FP32 registers and turn each product's TMEM
 //     accumulator into the next one's operand; products are
-//       X  = [K; Q] S     128 x DVS x 128  (Q rows ride along for O)
-//       D  = T Y          rows 0..63 of [T; P] x Y
+//       X  = K S           64 x DVS x 128
+//       D  = T Y           64 x DVS x 64
 //       dS = K^T D'       128 x DVS x 64, D'_j = e^(c_last - c_j) r_j D_j
-//     then P D for the output while the state is being updated, and Q S beside K S;
-//   * the CTAs that own a head's columns form a cluster.  Its T and P are the
-//     same for all of them, so each CTA's prep group of 4 warps builds them for
-//     every (128 / DVS)-th chunk, ahead of the chain, from [K; Q] K^T (tensor
-//     cores), inverts by blocks, and copies them with the chunk's row factors into
-//     the other CTAs' shared memory; a warp beside it sums up the decays;
-//   * 4 output warps join Q S and P D;
-//   * one warp issues the chain's products, one the TMA loads, and one the
-//     products that only the output needs; it also tells the CTA that fills a
-//     slot next that it has been used up here.
-// Y, D' and S enter as MN-major operands: a thread writes one token's (or key
-// channel's) columns with 16-byte stores, never a transpose.
-//
+//     M = 64 spreads the token rows over all four warp quadrants of TMEM, 16
+//     lanes each, read in the fragment layout so that all 32 threads work;
+//   * one warp issues these products from behind hardware barriers, one Q S and
+//     P D, which only the output needs and 4 warps of their own join; one loads
+//     the chunks' records, K and Q by TMA.
+// Preparing chunks inside the chain's CTAs, shared over clusters of a head's
+// slices, was measured first: it needed no memory in between but slowed the chain
+// on its SM (1 x 4096 at 16 heads 125 us).
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
 // wherever the state depends on them: S, T, Y and D'.  K and Q are BF16 already.
 // FP16 keys are split exactly (11 bits into 8 + 8) and FP16 queries rounded to
@@ -51,7 +51,6 @@ namespace kda {
 namespace {
 
 constexpr int kC = 64;  // tokens per chunk
-constexpr int kChainWarps = 16, kOutWarps = 4;
 constexpr int kLdG = 20;  // row stride of the FP32 diagonal blocks of A
 
 struct GdnPrefillArgs {
@@ -69,6 +68,9 @@ struct GdnPrefillArgs {
   kda_bf16* o;
   float* intermediate;
   int64_t inter_chunks;
+  uint8_t* records;    // one per (chunk, value head)
+  int64_t max_chunks;  // ids the workspace holds
+  int longest_first;   // the state kernel takes the sequences by length
   int32_t* err_flag;
 };
 
@@ -76,75 +78,66 @@ struct GdnMaps {
   CUtensorMap q, k, k_lo;
 };
 
-// What the chain warps read of a chunk beside T and P.
+// What the state kernel reads of a chunk beside T and P.
 struct ChunkScalars {
   float a[kC];  // r_i e^(c_i)
   float s[kC];  // r_j e^(c_last - c_j), 0 past the sequence's end
   float o[kC];  // scale rq_i e^(c_i)
   float last;   // e^(c_last)
-  float pad[3];
+  float done;   // 1: the record is complete
+  float pad[2];
 };
-// Decays and betas of a chunk that this CTA prepares.
-struct GateScalars {
-  float hi[kC], lo[kC];  // c_i = hi + lo
-  float beta[kC];
+// A chunk's record: T hi, P, T lo (tiles of 64 128-byte swizzled lines), scalars.
+constexpr int kRecT = 0, kRecP = 8192, kRecTlo = 16384, kRecScalars = 24576;
+constexpr int kRecBytes = kRecScalars + (int)sizeof(ChunkScalars);
+constexpr int kRecStride = 25600;
+static_assert(kRecBytes % 16 == 0 && kRecBytes <= kRecStride, "record");
+
+template <bool F16>
+constexpr int kRowBytes = 32768 + (F16 ? 16384 : 0);  // a chunk's [K; Q] and, from FP16, the keys' low halves
+
+// Shared memory of the chunk kernel.  A (hi, lo, diagonal blocks in FP32) lies in
+// K and Q once their products are done.
+template <bool F16>
+struct ChunkCfg {
+  static constexpr int kRec = kRowBytes<F16>;
+  static constexpr int kGate = kRec + kRecStride;  // float hi[64], lo[64], beta[64], rk[64]
+  static constexpr int kBar = kGate + 4 * kC * 4;
+  static constexpr int kSmem = kBar + 64;
+  static constexpr int kTmCols = F16 ? 128 : 64;
 };
 
 struct Bars {
-  uint64_t full[2], free_[2];  // the chain's K/Q stages: landed, consumed
-  uint64_t tail;               // rows past the end of the last chunk zeroed
-  uint64_t p_full, a_full;     // prep: K/Q landed, [K; Q] K^T done
-  uint64_t g_ready[2], g_free[2];    // its decays and betas
-  uint64_t t_ready[3], p_ready[3], used[3];  // a slot's T and scalars, its P: written; all consumed by this CTA
-  uint64_t slot_free;          // prep: its next slot has been consumed by every CTA
-  uint64_t s_ready, x_full, xq_full, d_full, v_ready, u_full;
-  uint64_t o_full, o_read;
-};
-struct Misc {
+  uint64_t full[2], free_[2];   // K and Q stages: landed, consumed
+  uint64_t tail;                // rows past the end of the last chunk zeroed
+  uint64_t rec[3], rec_free[3]; // records
+  uint64_t x_full, xq_full, d_full, u_full;
+  uint64_t o_full, q_read, o_read;
+  int64_t chunk0;  // id of the sequence's first chunk
   uint32_t tmem;
   int timed_out;
 };
 
+constexpr int kChainWarps = 16, kOutWarps = 4;
+
 template <int DVS, bool F16>
 struct Cfg {
-  static constexpr int kCl = kHeadDim / DVS;   // CTAs of a cluster
-  // Slots of T and P.  No more than kCl: a chunk's slot is then used up before
-  // the chunk that its own CTA prepares next asks for one, so that one barrier
-  // counts both.
-  static constexpr int kSlots = DVS == 64 || F16 ? 2 : 3;
   static constexpr int kTiles = DVS * 2 / 64;  // 64-wide operand tiles: [hi], [lo], or one [hi | lo]
-  static constexpr int kStageBytes = 32768 + (F16 ? 16384 : 0);  // [K; Q], K lo
-  static constexpr int kPrep = 2 * kStageBytes;                  // the prep group's K and Q
-  static constexpr int kS = kPrep + kStageBytes;
-  static constexpr int kSlot = kS + kTiles * 16384;
-  static constexpr int kTPBytes = 16384 + 8192;  // T hi, P, T lo, then the scalars
-  static constexpr int kCopyBytes = kTPBytes + (int)sizeof(ChunkScalars);
-  static constexpr int kSlotBytes = 25600;
-  static constexpr int kY = kSlot + kSlots * kSlotBytes;
+  static constexpr int kStageBytes = kRowBytes<F16>;
+  static constexpr int kRecs = 3;
+  static constexpr int kRec = 2 * kStageBytes;
+  static constexpr int kS = kRec + kRecs * kRecStride;
+  static constexpr int kY = kS + kTiles * 16384;
   static constexpr int kD = kY + kTiles * 8192;
-  // The prep group's A (hi, lo, diagonal blocks in FP32) lies in its K and Q,
-  // which are loaded again only when T is there; T waits for its slot in memory
-  // of its own, or, with FP16's larger stages, beside A.
-  static constexpr int kA = kPrep;
-  static constexpr int kABytes = 2 * 8192 + 4 * 16 * kLdG * 4;
-  static constexpr int kT = F16 ? kPrep + 22528 : kD + kTiles * 8192;  // T hi, T lo
-  static_assert(kABytes <= 22528 && (!F16 || 22528 + 16384 <= kStageBytes), "A and T beside each other");
-  static constexpr int kScalars = F16 ? kD + kTiles * 8192 : kT + 16384;
-  static constexpr int kBars = kSlot + kCopyBytes, kMisc = kBars + kSlotBytes;  // behind the slots' 25360 bytes
-  static_assert(kCopyBytes + sizeof(Bars) <= kSlotBytes, "barriers");
-  static constexpr int kGates = DVS == 64 || F16 ? 1 : 2;  // buffers of decays and betas
-  static constexpr int kRk = kScalars + kGates * (int)sizeof(GateScalars);  // inverse key norms
-  static constexpr int kSmem = kRk + kC * 4;
-  static constexpr int kPrepWarp = kChainWarps + kOutWarps;
-  static constexpr int kMmaWarp = kPrepWarp + 4, kLoadWarp = kMmaWarp + 1, kSideWarp = kMmaWarp + 2,
-                       kGateWarp = kMmaWarp + 3;
-  static constexpr int kThreads = (kGateWarp + 1) * 32;
-  static_assert(kThreads == 896, "register split, named barriers");
+  static constexpr int kBars = kD + kTiles * 8192;
+  static constexpr int kSmem = kBars + (int)sizeof(Bars);
+  static constexpr int kMmaWarp = kChainWarps + kOutWarps, kSideWarp = kMmaWarp + 1, kRowWarp = kMmaWarp + 2,
+                       kRecWarp = kMmaWarp + 3;
+  static constexpr int kThreads = (kRecWarp + 1) * 32;
 };
 
-// TMEM columns.  A2 takes the product of FP16 keys' low halves with the high
-// ones, whose rows 64..127 mean nothing.
-constexpr int kTmX = 0, kTmQ = 64, kTmD = 128, kTmU = 192, kTmO = 256, kTmA = 384, kTmA2 = 448, kTmCols = 512;
+// TMEM columns of the state kernel
+constexpr int kTmX = 0, kTmQ = 64, kTmD = 128, kTmU = 192, kTmO = 256, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -161,6 +154,10 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
 }
+// The chain warps' wait: skipped once one has run out of time.
+__device__ __forceinline__ void chain_wait(uint64_t* bar, uint32_t parity, bool& ok) {
+  if (ok && !__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) ok = warp_wait(bar, parity);
+}
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -172,73 +169,10 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void arrive_peer(const void* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, rank)) : "memory");
-}
-// Shared memory of this CTA -> the same place in a peer, counted on its barrier.
-__device__ __forceinline__ void copy_to_peer(const void* p, uint32_t bytes, const void* bar, uint32_t rank) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          peer_addr(p, rank)),
-      "r"(tc::smem_u32(p)), "r"(bytes), "r"(peer_addr(bar, rank))
-      : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// As warp_wait for a barrier that peers arrive on.
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
-  bool done = false;
-  for (uint32_t i = 0; i < (1u << 22) && !done; ++i) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    done = r != 0;
-  }
-  return __all_sync(0xffffffffu, done);
-}
-
-// A warp's writes to shared memory are for the tensor core, and its TMEM reads
-// are done: one arrival per warp.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  tc::fence_async_smem();
-  tc::tc_fence_before();
-  __syncwarp();
-  if (lane == 0) arrive(bar);
-}
-
-// Barrier of a prep group's 128 threads that also tells whether any of them failed.
-__device__ __forceinline__ bool group_any(int id, bool bad) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)bad), "r"(id)
-      : "memory");
-  return r != 0;
-}
-// The chain warps have written the next product's operand: the issuing warp
-// waits for them at the same hardware barrier, which wakes it sooner than an
-// mbarrier would.
+// The chain warps have written an operand: the warps that issue its products
+// wait for them at a hardware barrier, which wakes them sooner than an mbarrier
+// would and costs the chain one instruction.
+enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6 };  // kBarSq: S, for Q S
 __device__ __forceinline__ void chain_arrive(int id) {
   tc::fence_async_smem();
   tc::tc_fence_before();
@@ -248,21 +182,21 @@ __device__ __forceinline__ void chain_await(int id) {
   asm volatile("barrier.cta.sync %0, 544;" ::"r"(id) : "memory");
   tc::tc_fence_after();
 }
-__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+// Two FP32 values as BF16 hi and lo halves.
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+  const float2 d = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), make_float2(-1.f, -1.f), x);
+  const __nv_bfloat162 c = __floats2bfloat162_rn(d.x, d.y);
+  lo = *reinterpret_cast<const uint32_t*>(&c);
+}
 
-// Eight FP32 values as BF16 hi and lo halves.
+// Eight of them.
 __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * p], x[2 * p + 1]);
-    h[p] = *reinterpret_cast<const uint32_t*>(&b);
-    const __nv_bfloat162 c = __floats2bfloat162_rn(x[2 * p] - __uint_as_float(h[p] << 16),
-                                                   x[2 * p + 1] - __uint_as_float(h[p] & 0xffff0000u));
-    l[p] = *reinterpret_cast<const uint32_t*>(&c);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  split2(make_float2(x[0], x[1]), hi.x, lo.x);
+  split2(make_float2(x[2], x[3]), hi.y, lo.y);
+  split2(make_float2(x[4], x[5]), hi.z, lo.z);
+  split2(make_float2(x[6], x[7]), hi.w, lo.w);
 }
 
 __device__ __forceinline__ uint4 round8(const float* x) {
@@ -328,17 +262,15 @@ __device__ __forceinline__ void get_acc(uint32_t taddr, int part, float (&x)[DVS
     wait_ld(a);
     wait_ld(b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(a[j]) + __uint_as_float(b[j]);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 s = add2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
+                            make_float2(__uint_as_float(b[j]), __uint_as_float(b[j + 1])));
+      x[j] = s.x;
+      x[j + 1] = s.y;
+    }
   }
 }
 
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
-  const __nv_bfloat162 c =
-      __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-  lo = *reinterpret_cast<const uint32_t*>(&c);
-}
 
 // The same columns as operand halves (see put_split).
 template <int J>
@@ -348,7 +280,7 @@ __device__ __forceinline__ void put_rows(uint8_t* tiles, int row, int part, int 
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       uint32_t hi, lo;
-      split2(x[j][2 * e], x[j][2 * e + 1], hi, lo);
+      split2(make_float2(x[j][2 * e], x[j][2 * e + 1]), hi, lo);
       const int rr = row + 8 * e, piece = part * J + j;
       uint8_t* line = tiles + rr * 128 + 4 * (lane & 3);
       *reinterpret_cast<uint32_t*>(line + ((piece ^ (rr & 7)) << 4)) = hi;
@@ -375,17 +307,32 @@ __device__ __forceinline__ void get_rows(uint32_t taddr, int part, float (&x)[J]
   wait_ld(a);
   wait_ld(b);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[0][e] = __uint_as_float(a[e]);
-    if (J == 2)
-      x[J - 1][e] = __uint_as_float(b[e]);
-    else
-      x[0][e] += __uint_as_float(b[e]);
+  for (int e = 0; e < 4; e += 2) {
+    const float2 u = make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+    const float2 v = make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1]));
+    const float2 s = J == 2 ? u : add2(u, v);
+    x[0][e] = s.x;
+    x[0][e + 1] = s.y;
+    if (J == 2) {
+      x[J - 1][e] = v.x;
+      x[J - 1][e + 1] = v.y;
+    }
   }
 }
 
 __device__ __forceinline__ int64_t seq_start(const GdnPrefillArgs& a, int n) {
   return a.cu_seqlens ? (int64_t)a.cu_seqlens[n] : a.total_tokens / a.num_seqs * n;
+}
+// Tokens of sequence n, -1 where its bounds are not those of a sequence.
+__device__ __forceinline__ int seq_len(const GdnPrefillArgs& a, int n) {
+  const int64_t t0 = seq_start(a, n), t1 = seq_start(a, n + 1);
+  const bool bad = t0 < 0 || t1 < t0 || t1 > a.total_tokens || (n == 0 && t0 != 0) ||
+                   (n == a.num_seqs - 1 && t1 != a.total_tokens);
+  return bad ? -1 : (int)(t1 - t0);
+}
+__device__ __forceinline__ int seq_chunks(const GdnPrefillArgs& a, int n) {
+  const int len = seq_len(a, n);
+  return len > 0 ? (len + kC - 1) / kC : 0;
 }
 
 // Fragments of 16 x 16 (or 8 x 16) pieces of 128-byte-swizzled BF16 tiles for
@@ -477,8 +424,8 @@ __device__ __forceinline__ void inverse_block(uint8_t* t_hi, uint8_t* t_lo, cons
 #pragma unroll
     for (int p = 0; p < 2; ++p) {  // columns c0 + 8 p ..
       uint32_t h0, l0_, h1, l1;
-      split2(z[2 * kb][2 * p], z[2 * kb][2 * p + 1], h0, l0_);
-      split2(z[2 * kb + 1][2 * p], z[2 * kb + 1][2 * p + 1], h1, l1);
+      split2(make_float2(z[2 * kb][2 * p], z[2 * kb][2 * p + 1]), h0, l0_);
+      split2(make_float2(z[2 * kb + 1][2 * p], z[2 * kb + 1][2 * p + 1]), h1, l1);
       mma16(w[p], th, l0_, l1);
       mma16(w[p], tl, h0, h1);
       mma16(w[p], th, h0, h1);
@@ -489,7 +436,7 @@ __device__ __forceinline__ void inverse_block(uint8_t* t_hi, uint8_t* t_lo, cons
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       uint32_t hi, lo;
-      split2(-w[p][2 * e], -w[p][2 * e + 1], hi, lo);
+      split2(make_float2(-w[p][2 * e], -w[p][2 * e + 1]), hi, lo);
       const int row = r0 + (lane >> 2) + 8 * e, col = c0 + 8 * p + 2 * (lane & 3);
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(elem_addr(t_hi, row, col)), "r"(hi) : "memory");
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(elem_addr(t_lo, row, col)), "r"(lo) : "memory");
@@ -502,7 +449,7 @@ __device__ __forceinline__ void inverse_block(uint8_t* t_hi, uint8_t* t_lo, cons
 // warp each and a column per lane; then T21 = -T22 A21 T11 for blocks of 16 and
 // of 32.  diag: FP32 diagonal blocks of A.
 __device__ __forceinline__ void invert64(uint8_t* t_hi, uint8_t* t_lo, const uint8_t* a_hi, const uint8_t* a_lo,
-                                         const float* diag, const float* beta, int warp, int lane, int bar_id) {
+                                         const float* diag, const float* beta, int warp, int lane) {
   {
     const float* d = diag + warp * 16 * kLdG;
     const int col = lane & 15;
@@ -530,114 +477,379 @@ __device__ __forceinline__ void invert64(uint8_t* t_hi, uint8_t* t_lo, const uin
                    : "memory");
     }
   }
-  group_sync(bar_id);
+  __syncthreads();
   if (warp < 2)
     inverse_block<1>(t_hi, t_lo, a_hi, a_lo, 32 * warp, 32 * warp + 16, 32 * warp + 16, 32 * warp, lane);
-  group_sync(bar_id);
+  __syncthreads();
   inverse_block<2>(t_hi, t_lo, a_hi, a_lo, 0, 32, 32 + 16 * (warp >> 1), 16 * (warp & 1), lane);
+}
+
+// The rows of a chunk from token `tok` on: [K; Q] as two halves of 64 channels,
+// 128 lines each, and behind them the low halves of FP16 keys.
+template <bool F16>
+__device__ __forceinline__ void load_rows(const GdnMaps& maps, uint8_t* kq, int tok, int hk, uint64_t* bar) {
+  tc::mbar_expect_tx(bar, kRowBytes<F16>);
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, bar);
+    tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, bar);
+    if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, bar);
+  }
+}
+// K rows [len, 64) zeroed by `threads` threads: they belong to the next sequence
+// or lie past the last token, and NaN times a zero factor is NaN.
+template <bool F16>
+__device__ __forceinline__ void zero_tail(uint8_t* kq, int len, int t, int threads) {
+  for (int x = t; x < (kC - len) * 16; x += threads) {
+    *line16(kq + (x & 1) * 16384, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
+    if (F16) *line16(kq + 32768 + (x & 1) * 8192, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(128, 3)
+    gdn_chunk_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+  using C = ChunkCfg<F16>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);  // rows landed, [K; Q] K^T done, TMEM address
+  const int t = threadIdx.x, quad = t >> 5, lane = t & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");  // K and Q were split by the launch before
+  if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
+    if (t == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+    return;
+  }
+  // the chunk's sequence: every warp walks over the sequences, 128 at a time
+  const int h = blockIdx.x % args.HV, id = blockIdx.x / args.HV;
+  int n = -1, c = 0;
+  for (int n0 = 0, base = 0; n0 < args.num_seqs && n < 0; n0 += 128) {
+    int cnt[4], sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int m = n0 + 4 * lane + e;
+      cnt[e] = m < args.num_seqs ? seq_chunks(args, m) : 0;
+      sum += cnt[e];
+    }
+    int run = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, d);
+      if (lane >= d) run += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, base + run > id);
+    if (past) {
+      int at = base + run - sum, mine = -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (mine < 0 && id < at + cnt[e]) mine = e;
+        if (mine < 0) at += cnt[e];
+      }
+      const int src = __ffs(past) - 1;
+      n = n0 + 4 * src + __shfl_sync(0xffffffffu, mine, src);
+      c = id - __shfl_sync(0xffffffffu, at, src);
+    }
+    base += __shfl_sync(0xffffffffu, run, 31);
+  }
+  if (n < 0) return;  // the grid is an upper bound
+  const int slot = args.state_idx[n];
+  if (slot < 0 || slot >= args.pool_slots) return;
+  const int64_t t0 = seq_start(args, n) + (int64_t)c * kC;
+  const int left = seq_len(args, n) - c * kC, len = left < kC ? left : kC;
+
+  uint8_t* kq = smem;
+  uint8_t* rec = smem + C::kRec;
+  uint8_t* a_hi = smem;
+  uint8_t* a_lo = a_hi + 8192;
+  float* diag = reinterpret_cast<float*>(a_lo + 8192);
+  float* c_hi = reinterpret_cast<float*>(smem + C::kGate);  // c_i = c_hi + c_lo
+  float* c_lo = c_hi + kC;
+  float* beta_s = c_lo + kC;
+  float* rks = beta_s + kC;
+  ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(rec + kRecScalars);
+  const ScalarGateArgs& ga = args.gate;
+  if (t == 0) {
+    tc::mbar_init(&bars[0], 1);
+    tc::mbar_init(&bars[1], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    load_rows<F16>(maps, kq, (int)t0, h / args.G, &bars[0]);
+  }
+  if (quad == 0) tc::tmem_alloc(reinterpret_cast<uint32_t*>(&bars[2]), C::kTmCols);
+  if (quad == 3) {  // decays and betas: tokens 2 lane and 2 lane + 1
+    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
+    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
+    float gl[2], be[2];  // past the end nothing decays and nothing is written
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      gl[e] = be[e] = 0.f;
+      if (2 * lane + e < len) {
+        const int64_t at = (t0 + 2 * lane + e) * args.HV + h;
+        const float b = in16_to_float<F16>(args.beta[at]);
+        gl[e] = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
+        be[e] = ga.beta_is_raw ? sigmoidf_(b) : b;
+      }
+    }
+    // running sums in FP64, kept as two floats: differences of them count
+    double run = (double)gl[0] + (double)gl[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const double up = __shfl_up_sync(0xffffffffu, run, d);
+      if (lane >= d) run += up;
+    }
+    const double c0 = run - (double)gl[1];
+    c_hi[2 * lane] = (float)c0;
+    c_lo[2 * lane] = (float)(c0 - (double)(float)c0);
+    c_hi[2 * lane + 1] = (float)run;
+    c_lo[2 * lane + 1] = (float)(run - (double)(float)run);
+    beta_s[2 * lane] = be[0];
+    beta_s[2 * lane + 1] = be[1];
+  }
+  for (int x = t; x < 8192 / 16; x += 128) {  // blocks of T above the diagonal are not written below
+    reinterpret_cast<uint4*>(rec + kRecT)[x] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(rec + kRecTlo)[x] = make_uint4(0, 0, 0, 0);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(&bars[2]);
+  const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16);
+  bool bad = !warp_wait(&bars[0], 0);
+  if (len < kC) {
+    zero_tail<F16>(kq, len, t, 128);
+    tc::fence_async_smem();
+    __syncthreads();
+  }
+  if (quad == 0 && !bad && elect_one()) {  // [K; Q] K^T
+    constexpr uint32_t kIdA = tc::idesc_bf16_f32(128, 64);
+    const uint64_t hi = tc::sw128_desc(tc::smem_u32(kq)), lo = tc::sw128_desc(tc::smem_u32(kq + 32768));
+    tc::tc_fence_after();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint64_t off = ((j >> 2) * 16384 + (j & 3) * 32) >> 4;
+      tc::mma_bf16(tmem, hi + off, hi + off, kIdA, j > 0);
+    }
+    if constexpr (F16) {  // K = hi + lo: K hi K lo^T, Q K lo^T beside, and K lo K hi^T (rows 0..63) apart
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        tc::mma_bf16(tmem, hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4), lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4),
+                     kIdA, true);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        tc::mma_bf16(tmem + 64, lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4),
+                     hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4), kIdA, j > 0);
+    }
+    tc::mma_commit(&bars[1]);
+  }
+  __syncwarp();
+  const bool krow = quad < 2;
+  const int i = 32 * (quad & 1) + lane;  // token of the chunk
+  const int row = krow ? i : 64 + i;  // row of [K; Q]
+  float2 ss[4];  // four running sums, for latency
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ss[e] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const uint4 w = *line16(kq + a * 16384, row, p);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      uint4 w2 = make_uint4(0, 0, 0, 0);
+      if (F16 && krow) w2 = *line16(kq + 32768 + a * 8192, row, p);
+      const uint32_t ww2[4] = {w2.x, w2.y, w2.z, w2.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float f0 = __uint_as_float(ww[e] << 16), f1 = __uint_as_float(ww[e] & 0xffff0000u);
+        if (F16) {
+          f0 += __uint_as_float(ww2[e] << 16);
+          f1 += __uint_as_float(ww2[e] & 0xffff0000u);
+        }
+        ss[e] = fma2(make_float2(f0, f1), make_float2(f0, f1), ss[e]);
+      }
+    }
+  const float sq = ((ss[0].x + ss[0].y) + (ss[1].x + ss[1].y)) + ((ss[2].x + ss[2].y) + (ss[3].x + ss[3].y));
+  const float r = (krow ? 1.f : ga.scale) * (ga.use_qk_l2norm ? rsqrtf(sq + kNormEps) : 1.f);
+  // r_i r_j e^(c_i - c_j) as a product of row and column factors about the
+  // middle of the chunk, where those stay in FP32's range; term by term otherwise
+  const float ci_hi = c_hi[i], ci_lo = c_lo[i];
+  const float mid = (ci_hi - c_hi[kC / 2]) + (ci_lo - c_lo[kC / 2]);
+  const bool far = !(fabsf(mid) <= 60.f);
+  if (krow) rks[i] = r * expf(-mid);
+  bad |= !warp_wait(&bars[1], 0);
+  const bool wide = __syncthreads_or(far);
+  if (wide) {
+    if (krow) rks[i] = r;
+    __syncthreads();
+  }
+  tc::tc_fence_after();
+  const float ei = __expf(ci_hi + ci_lo);
+  const float ui = wide ? r : r * expf(mid);
+  const float si = krow && i < len ? r * __expf((c_hi[63] - ci_hi) + (c_lo[63] - ci_lo)) : 0.f;
+  const int top = 32 * (quad & 1) + 31;  // last row of this warp
+#pragma unroll
+  for (int jb = 0; jb < 4; ++jb) {
+    float d[16];
+    if (16 * jb <= top) {
+      tc::tmem_ld16(acc + 16 * jb, d);
+      if (F16 && krow) {
+        float d2[16];
+        tc::tmem_ld16(acc + 64 + 16 * jb, d2);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) d[e] += d2[e];
+      }
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(f + 4 * e) = *reinterpret_cast<const float4*>(rks + 16 * jb + 4 * e);
+      if (wide) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          f[e] *= __expf((ci_hi - c_hi[16 * jb + e]) + (ci_lo - c_lo[16 * jb + e]));
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = 16 * jb + e;
+        d[e] = (krow ? j < i : j <= i) ? (ui * f[e]) * d[e] : 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) d[e] = 0.f;
+    }
+    if (krow) {
+      if (jb < (i >> 4)) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint4 hi, lo;
+          split8(d + 8 * p, hi, lo);
+          *line16(a_hi, i, 2 * jb + p) = hi;
+          *line16(a_lo, i, 2 * jb + p) = lo;
+        }
+      } else if (jb == (i >> 4)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<float4*>(diag + i * kLdG + 4 * e) =
+              make_float4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
+      }
+    } else {
+      *line16(rec + kRecP, i, 2 * jb) = round8(d);
+      *line16(rec + kRecP, i, 2 * jb + 1) = round8(d + 8);
+    }
+  }
+  tc::tc_fence_before();
+  bad = __syncthreads_or(bad);
+  if (quad == 0) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, C::kTmCols);
+  }
+  invert64(rec + kRecT, rec + kRecTlo, a_hi, a_lo, diag, beta_s, quad, lane);
+  if (krow) {
+    sc.a[i] = r * ei;
+    sc.s[i] = si;
+    if (i == 63) sc.last = ei;
+  } else {
+    sc.o[i] = r * ei;
+    if (i == 0) sc.done = bad ? 0.f : 1.f;
+  }
+  tc::fence_async_smem();
+  __syncthreads();
+  if (t == 0) {
+    if (bad) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+    tc::bulk_s2g(args.records + ((int64_t)id * args.HV + h) * kRecStride, rec, kRecBytes);
+    tc::bulk_commit();
+    tc::bulk_wait_read();
+  }
 }
 
 template <int DVS, bool F16>
 __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
-    gdn_prefill_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+    gdn_state_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
   using C = Cfg<DVS, F16>;
   constexpr int N = DVS / 4;  // value columns per chain thread
+  constexpr int kSlices = kHeadDim / DVS;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
-  Misc& misc = *reinterpret_cast<Misc*>(smem + C::kMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
-    if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-    return;
-  }
-  const int slice = (int)cluster_rank();  // the cluster's CTAs are the slices of a head
-  const int unit = blockIdx.x / C::kCl;
-  const int h = unit % args.HV, n = unit / args.HV;
+  const int slice = blockIdx.x % kSlices;
+  const int unit = blockIdx.x / kSlices;
+  const int h = unit % args.HV;
+  int n = unit / args.HV;
   const bool reporter = tid == 0 && slice == 0 && h == 0;
-
-  const int64_t t0 = seq_start(args, n), t1 = seq_start(args, n + 1);
-  if (t0 < 0 || t1 < t0 || t1 > args.total_tokens || (n == 0 && t0 != 0) ||
-      (n == args.num_seqs - 1 && t1 != args.total_tokens)) {
-    if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
-    return;  // here and below the whole cluster returns
+  if (args.longest_first) {  // CTAs start in order: sequence n is the n-th longest
+    int* len_s = reinterpret_cast<int*>(smem);
+    for (int m = tid; m < args.num_seqs; m += C::kThreads) len_s[m] = seq_len(args, m);
+    __syncthreads();
+    if (tid < args.num_seqs) {
+      const int mine = len_s[tid];
+      int before = 0;
+      for (int m = 0; m < args.num_seqs; ++m) before += len_s[m] > mine || (len_s[m] == mine && m < tid);
+      if (before == n) len_s[args.num_seqs] = tid;
+    }
+    __syncthreads();
+    n = len_s[args.num_seqs];
+    __syncthreads();
   }
-  const int L = (int)(t1 - t0);
-  if (L == 0) return;
+  const int L = seq_len(args, n);
   const int slot = args.state_idx[n];
-  if (slot < 0 || slot >= args.pool_slots) {  // padding or out of range: zero outputs, no state touched
+  bool stop = L <= 0;
+  if (L < 0 && reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
+  if (L > 0 && (slot < 0 || slot >= args.pool_slots)) {  // padding or out of range: zero outputs, no state touched
+    stop = true;
     if (slot != -1 && reporter) set_error(args.err_flag, KDA_DEVERR_SLOT);
     constexpr int kPieces = DVS / 8;
+    const int64_t t0 = seq_start(args, n);
     for (int64_t i = tid; i < (int64_t)L * kPieces; i += C::kThreads)
       *reinterpret_cast<uint4*>(args.o + ((t0 + i / kPieces) * args.HV + h) * kHeadDim + slice * DVS +
                                 (i % kPieces) * 8) = make_uint4(0, 0, 0, 0);
+  }
+  if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
+    stop = true;
+    if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+  }
+  if (warp == 1) {  // record of this sequence's first chunk
+    int64_t id = 0;
+    for (int m = lane; m < n; m += 32) id += seq_chunks(args, m);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) id += __shfl_xor_sync(0xffffffffu, id, m);
+    if (lane == 0) bars.chunk0 = id;
+  }
+  __syncthreads();
+  const int64_t t0 = seq_start(args, n);
+  const int nch = (L + kC - 1) / kC;
+  if (!stop && bars.chunk0 + nch > args.max_chunks) {  // overlapping sequences have more chunks than tokens allow
+    stop = true;
+    if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
+  }
+  if (stop) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for the one before too
     return;
   }
-  const int nch = (L + kC - 1) / kC;
 
-  if (warp == C::kMmaWarp) tc::tmem_alloc(&misc.tmem, kTmCols);
+  tc::fence_async_smem();  // the lengths lay where rows land
+  if (warp == C::kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
-    misc.timed_out = 0;
+    bars.timed_out = 0;
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.full[i], 1);
       tc::mbar_init(&bars.free_[i], 2);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&bars.t_ready[i], 1);
-      tc::mbar_init(&bars.p_ready[i], 1);
-      tc::mbar_init(&bars.used[i], 1 + kChainWarps + kOutWarps);
-    }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bars.g_ready[i], 1);
-      tc::mbar_init(&bars.g_free[i], 1);
+    for (int i = 0; i < C::kRecs; ++i) {
+      tc::mbar_init(&bars.rec[i], 1);
+      tc::mbar_init(&bars.rec_free[i], 1 + kOutWarps);
     }
     tc::mbar_init(&bars.tail, 1);
-    tc::mbar_init(&bars.p_full, 1);
-    tc::mbar_init(&bars.a_full, 1);
-    tc::mbar_init(&bars.slot_free, C::kCl);
-    tc::mbar_init(&bars.s_ready, kChainWarps);
     tc::mbar_init(&bars.x_full, 1);
     tc::mbar_init(&bars.xq_full, 1);
-    tc::mbar_init(&bars.o_full, 1);
-    tc::mbar_init(&bars.o_read, kOutWarps);
     tc::mbar_init(&bars.d_full, 1);
-    tc::mbar_init(&bars.v_ready, kChainWarps);
     tc::mbar_init(&bars.u_full, 1);
+    tc::mbar_init(&bars.o_full, 1);
+    tc::mbar_init(&bars.q_read, kOutWarps);
+    tc::mbar_init(&bars.o_read, kOutWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (!F16)  // blocks of T above the diagonal are never written
-    for (int i = tid; i < 16384 / 16; i += C::kThreads) reinterpret_cast<uint4*>(smem + C::kT)[i] = make_uint4(0, 0, 0, 0);
-  tc::fence_async_smem();
   tc::tc_fence_before();
   __syncthreads();
-  cluster_sync();  // every CTA's barriers are up
   tc::tc_fence_after();
-  const uint32_t tmem = misc.tmem;
+  const uint32_t tmem = bars.tmem;
   bool ok = true;
-  // FP16: K and Q were split by the launch before
-  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  auto load_rows = [&](uint8_t* kq, int c, uint64_t* bar) {
-    tc::mbar_expect_tx(bar, C::kStageBytes);
-    const int tok = (int)t0 + c * kC, hk = h / args.G;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, bar);
-      tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, bar);
-      if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, bar);
-    }
-  };
-  // K rows [len, 64) zeroed by `threads` threads: they belong to the next
-  // sequence or lie past the last token, and NaN times a zero factor is NaN
-  auto zero_tail = [&](uint8_t* kq, int len, int t, int threads) {
-    for (int x = t; x < (kC - len) * 16; x += threads) {
-      *line16(kq + (x & 1) * 16384, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
-      if (F16) *line16(kq + 32768 + (x & 1) * 8192, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
-    }
-  };
-
-  // 896 threads start with 72 registers each; 64, 64, 128 and 40 use 62464 of those 64512
   if (warp < kChainWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ---------------------------------------------------------------- chain
     // A warp that runs out of time goes on without waiting, so that the others
     // still meet it.
@@ -652,15 +864,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     float S[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) S[j] = root[j * kHeadDim];
-    int64_t cid = 0;  // record of this sequence's first chunk
-    if (args.intermediate) {
-      for (int m = lane; m < n; m += 32) {
-        const int64_t len = seq_start(args, m + 1) - seq_start(args, m);
-        cid += len > 0 ? (len + kC - 1) / kC : 0;
-      }
-#pragma unroll
-      for (int m = 16; m; m >>= 1) cid += __shfl_xor_sync(0xffffffffu, cid, m);
-    }
+    const int64_t cid = bars.chunk0;
     uint32_t vraw[J][2];
     const int64_t vstep = (int64_t)args.HV * kHeadDim;
     const kda_bf16* vsrc = args.v + ((t0 + row) * args.HV + h) * kHeadDim + colx;
@@ -673,13 +877,24 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       vsrc += kC * vstep;
     };
     load_v(0);
+    float last, fa[2], fs[2];  // e^(c_last); -r e^(c_i) and r e^(c_last - c_i) of the two rows
+    auto load_factors = [&](int c) {
+      const int sl = c % C::kRecs;
+      const ChunkScalars& sc =
+          *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecStride + kRecScalars);
+      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u, ok);
+      last = sc.last;
+      fa[0] = -sc.a[row];
+      fa[1] = -sc.a[row + 8];
+      fs[0] = sc.s[row];
+      fs[1] = sc.s[row + 8];
+      ok = ok && sc.done == 1.f;
+    };
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kSlots;
       const uint32_t cp = (uint32_t)c & 1u;
       put_split<DVS>(smem + C::kS, 16384, dk, part, S);
-      chain_arrive(2);
-      __syncwarp();
-      if (lane == 0) arrive(&bars.s_ready);  // after chain_arrive's fences
+      chain_arrive(kBarS);
+      asm volatile("barrier.cta.arrive %0, 544;" ::"r"((int)kBarSq) : "memory");
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
@@ -689,12 +904,8 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
         }
       }
-      const ChunkScalars& sc =
-          *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
-      ok = ok && warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u);
-      const float last = sc.last;
-      float fa[2] = {sc.a[row], sc.a[row + 8]}, fs[2] = {sc.s[row], sc.s[row + 8]};
-      ok = ok && warp_wait(&bars.x_full, cp);
+      load_factors(c);
+      chain_wait(&bars.x_full, cp, ok);
       tc::tc_fence_after();
       float x[J][4];
       get_rows<J>(lanes + kTmX, part, x);
@@ -702,45 +913,51 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; e += 2) {
           const uint32_t w = vraw[j][e >> 1];
-          float v;
+          float2 v;
           if constexpr (F16)
-            v = in16_to_float<true>((uint16_t)(e & 1 ? w >> 16 : w & 0xffffu));
+            v = __half22float2(*reinterpret_cast<const __half2*>(&w));
           else
-            v = __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
-          x[j][e] = fmaf(-fa[e >> 1], x[j][e], v);
+            v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+          v = fma2(make_float2(fa[e >> 1], fa[e >> 1]), make_float2(x[j][e], x[j][e + 1]), v);
+          x[j][e] = v.x;
+          x[j][e + 1] = v.y;
         }
       put_rows<J>(smem + C::kY, row, part, lane, x);
-      chain_arrive(3);
+      chain_arrive(kBarY);
       if (c + 1 < nch) load_v(c + 1);
-      ok = ok && warp_wait(&bars.d_full, cp);
+      chain_wait(&bars.d_full, cp, ok);
       tc::tc_fence_after();
       get_rows<J>(lanes + kTmD, part, x);
       float y[J][4];
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[j][e] = fs[e >> 1] * x[j][e];
+        for (int e = 0; e < 4; e += 2) {
+          const float2 s = mul2(make_float2(fs[e >> 1], fs[e >> 1]), make_float2(x[j][e], x[j][e + 1]));
+          y[j][e] = s.x;
+          y[j][e + 1] = s.y;
+        }
       put_rows<J>(smem + C::kY, row, part, lane, y);
-      chain_arrive(4);
-      if (c > 0) ok = ok && warp_wait(&bars.o_full, cp ^ 1u);  // P D of the last chunk has read its D
+      chain_arrive(kBarDs);
       put_rows<J>(smem + C::kD, row, part, lane, x);
-      warp_arrive(&bars.v_ready, lane);
-      if (lane == 0) arrive(&bars.used[sl]);
-      ok = ok && warp_wait(&bars.xq_full, cp);  // Q S has read S
-      ok = ok && warp_wait(&bars.u_full, cp);
+      chain_arrive(kBarD);
+      chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
       float u[N];
       get_acc<DVS>(lanes + kTmU, part, u);
 #pragma unroll
-      for (int j = 0; j < N; ++j) S[j] = fmaf(last, S[j], u[j]);
+      for (int j = 0; j < N; j += 2) {
+        const float2 s = fma2(make_float2(last, last), make_float2(S[j], S[j + 1]), make_float2(u[j], u[j + 1]));
+        S[j] = s.x;
+        S[j + 1] = s.y;
+      }
     }
     if (ok)
 #pragma unroll
       for (int j = 0; j < N; ++j) root[j * kHeadDim] = S[j];
-  } else if (warp < C::kPrepWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  } else if (warp < C::kMmaWarp) {
     // --------------------------------------------------------------- outputs
     // O = scale rq e^c Q S + P D, 16 token rows a warp.
     constexpr int J = DVS / 32;
@@ -750,29 +967,35 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + slice * DVS + 2 * (lane & 3);
     const int64_t step = (int64_t)args.HV * kHeadDim;
     for (int c = 0; c < nch; ++c, dst += kC * step) {
-      const int sl = c % C::kSlots;
+      const int sl = c % C::kRecs;
       const uint32_t cp = (uint32_t)c & 1u;
       const ChunkScalars& sc =
-          *reinterpret_cast<const ChunkScalars*>(smem + C::kSlot + sl * C::kSlotBytes + C::kTPBytes);
-      if (!(ok = warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
+          *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecStride + kRecScalars);
+      if (!(ok = warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u))) break;
       const float fo[2] = {sc.o[row], sc.o[row + 8]};
       __syncwarp();
-      if (lane == 0) arrive(&bars.used[sl]);
+      if (lane == 0) arrive(&bars.rec_free[sl]);
       if (!(ok = warp_wait(&bars.xq_full, cp))) break;
+      tc::tc_fence_after();
+      float x[4][J][4];
+#pragma unroll
+      for (int part = 0; part < 4; ++part) get_rows<J>(lanes + kTmQ, part, x[part]);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&bars.q_read);
       if (!(ok = warp_wait(&bars.o_full, cp))) break;
       tc::tc_fence_after();
       uint32_t w[4][J][2];
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float x[J][4], u[J][4];
-        get_rows<J>(lanes + kTmQ, part, x);
+        float u[J][4];
         get_rows<J>(lanes + kTmO, part, u);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            w[part][j][e] = pack_out16x2<F16>(fmaf(fo[e], x[j][2 * e], u[j][2 * e]),
-                                              fmaf(fo[e], x[j][2 * e + 1], u[j][2 * e + 1]));
+            w[part][j][e] = pack_out16x2<F16>(fmaf(fo[e], x[part][j][2 * e], u[j][2 * e]),
+                                              fmaf(fo[e], x[part][j][2 * e + 1], u[j][2 * e + 1]));
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -787,209 +1010,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
               *reinterpret_cast<uint32_t*>(dst + 8 * e * step + 8 * (part * J + j)) = w[part][j][e];
         }
     }
-  } else if (warp < C::kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    // ----------------------------------------------------------------- prep
-    const int t = tid - C::kPrepWarp * 32, quad = warp & 3;
-    const int bar_id = 1;
-    const bool krow = quad < 2;
-    const int i = 32 * (quad & 1) + lane;  // token of the chunk
-    const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16);
-    uint8_t* kq = smem + C::kPrep;
-    uint8_t* a_hi = smem + C::kA;
-    uint8_t* a_lo = a_hi + 8192;
-    uint8_t* t_hi = smem + C::kT;
-    uint8_t* t_lo = t_hi + 8192;
-    float* diag = reinterpret_cast<float*>(a_lo + 8192);
-    float* rks = reinterpret_cast<float*>(smem + C::kRk);
-    const ScalarGateArgs& ga = args.gate;
-    if (t == 0 && slice < nch) load_rows(kq, slice, &bars.p_full);
-    for (int c = slice, k = 0; c < nch; c += C::kCl, ++k) {
-      const int sl = c % C::kSlots, gb = k % C::kGates;
-      const int len = L - c * kC < kC ? L - c * kC : kC;
-      const GateScalars& gs = *reinterpret_cast<const GateScalars*>(smem + C::kScalars + gb * sizeof(GateScalars));
-      uint8_t* slot_s = smem + C::kSlot + sl * C::kSlotBytes;
-      ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(slot_s + C::kTPBytes);
-      bool bad = !warp_wait(&bars.p_full, (uint32_t)k & 1u);
-      if (len < kC) {
-        zero_tail(kq, len, t, 128);
-        tc::fence_async_smem();
-        group_sync(bar_id);
-      }
-      if (quad == 0 && !bad && elect_one()) {  // [K; Q] K^T
-        constexpr uint32_t kIdA = tc::idesc_bf16_f32(128, 64);
-        const uint64_t hi = tc::sw128_desc(tc::smem_u32(kq)), lo = tc::sw128_desc(tc::smem_u32(kq + 32768));
-        tc::tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint64_t off = ((j >> 2) * 16384 + (j & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + kTmA, hi + off, hi + off, kIdA, j > 0);
-        }
-        if constexpr (F16) {  // K = hi + lo: K hi K lo^T, Q K lo^T beside, and K lo K hi^T apart
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmA, hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
-                         lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kIdA, true);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmA2, lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4),
-                         hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4), kIdA, j > 0);
-        }
-        tc::mma_commit(&bars.a_full);
-      }
-      __syncwarp();
-      const int row = krow ? i : 64 + i;  // row of [K; Q]
-      float2 ss[4];  // four running sums, for latency
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss[e] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const uint4 w = *line16(kq + a * 16384, row, p);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          uint4 w2 = make_uint4(0, 0, 0, 0);
-          if (F16 && krow) w2 = *line16(kq + 32768 + a * 8192, row, p);
-          const uint32_t ww2[4] = {w2.x, w2.y, w2.z, w2.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float f0 = __uint_as_float(ww[e] << 16), f1 = __uint_as_float(ww[e] & 0xffff0000u);
-            if (F16) {
-              f0 += __uint_as_float(ww2[e] << 16);
-              f1 += __uint_as_float(ww2[e] & 0xffff0000u);
-            }
-            ss[e] = fma2(make_float2(f0, f1), make_float2(f0, f1), ss[e]);
-          }
-        }
-      const float sq = ((ss[0].x + ss[0].y) + (ss[1].x + ss[1].y)) + ((ss[2].x + ss[2].y) + (ss[3].x + ss[3].y));
-      const float r = (krow ? 1.f : ga.scale) * (ga.use_qk_l2norm ? rsqrtf(sq + kNormEps) : 1.f);
-      bad |= !warp_wait(&bars.g_ready[gb], (uint32_t)(k / C::kGates) & 1u);
-      // r_i r_j e^(c_i - c_j) as a product of row and column factors about the
-      // middle of the chunk, where those stay in FP32's range; term by term otherwise
-      const float ci_hi = gs.hi[i], ci_lo = gs.lo[i];
-      const float mid = (ci_hi - gs.hi[kC / 2]) + (ci_lo - gs.lo[kC / 2]);
-      const bool far = !(fabsf(mid) <= 60.f);
-      if (krow) rks[i] = r * expf(-mid);
-      bad |= !warp_wait(&bars.a_full, (uint32_t)k & 1u);
-      bool wide = false;
-      if (group_any(bar_id, bad || far)) {
-        if (group_any(bar_id, bad)) {
-          ok = false;
-          break;
-        }
-        wide = true;
-        if (krow) rks[i] = r;
-        group_sync(bar_id);
-      }
-      if (F16) {  // T's place was under K and Q: zeros above the diagonal again
-        for (int x = t; x < 16384 / 16; x += 128) reinterpret_cast<uint4*>(t_hi)[x] = make_uint4(0, 0, 0, 0);
-      }
-      tc::tc_fence_after();
-      const float ei = __expf(ci_hi + ci_lo);
-      const float ui = wide ? r : r * expf(mid);
-      const float si = krow && i < len ? r * __expf((gs.hi[63] - ci_hi) + (gs.lo[63] - ci_lo)) : 0.f;
-      const int top = 32 * (quad & 1) + 31;  // last row of this warp
-      uint4 prow[8];  // P's row, kept until the slot is free
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        float d[16];
-        if (16 * jb <= top) {
-          tc::tmem_ld16(acc + kTmA + 16 * jb, d);
-          if (F16 && krow) {
-            float d2[16];
-            tc::tmem_ld16(acc + kTmA2 + 16 * jb, d2);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) d[e] += d2[e];
-          }
-          float f[16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(f + 4 * e) = *reinterpret_cast<const float4*>(rks + 16 * jb + 4 * e);
-          if (wide) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              f[e] *= __expf((ci_hi - gs.hi[16 * jb + e]) + (ci_lo - gs.lo[16 * jb + e]));
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = 16 * jb + e;
-            d[e] = (krow ? j < i : j <= i) ? (ui * f[e]) * d[e] : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) d[e] = 0.f;
-        }
-        if (krow) {
-          if (jb < (i >> 4)) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              uint4 hi, lo;
-              split8(d + 8 * p, hi, lo);
-              *line16(a_hi, i, 2 * jb + p) = hi;
-              *line16(a_lo, i, 2 * jb + p) = lo;
-            }
-          } else if (jb == (i >> 4)) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(diag + i * kLdG + 4 * e) =
-                  make_float4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
-          }
-        } else {
-          prow[2 * jb] = round8(d);
-          prow[2 * jb + 1] = round8(d + 8);
-        }
-      }
-      tc::tc_fence_before();
-      group_sync(bar_id);
-      invert64(t_hi, t_lo, a_hi, a_lo, diag, gs.beta, quad, lane, bar_id);
-      if (!F16) {
-        tc::fence_async_smem();
-        group_sync(bar_id);  // A has been used: the next K and Q may land over it
-        if (t == 0 && c + C::kCl < nch) load_rows(kq, c + C::kCl, &bars.p_full);
-      }
-      // the slot's last chunk has been used by every CTA of the cluster
-      if (c >= C::kSlots)
-        bad = !warp_wait_cluster(&bars.slot_free, (uint32_t)(k - (C::kSlots > slice ? 1 : 0)) & 1u);
-      if (group_any(bar_id, bad)) {
-        ok = false;
-        break;
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {  // T hi and lo
-        const int at = (x * 128 + t) * 16;
-        *reinterpret_cast<uint4*>(slot_s + at) = *reinterpret_cast<const uint4*>(t_hi + at);
-        *reinterpret_cast<uint4*>(slot_s + 16384 + at) = *reinterpret_cast<const uint4*>(t_lo + at);
-      }
-      if (krow) {
-        sc.a[i] = r * ei;
-        sc.s[i] = si;
-        if (i == 63) sc.last = ei;
-      } else {
-        sc.o[i] = r * ei;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) *line16(slot_s, 64 + i, p) = prow[p];
-      }
-      tc::fence_async_smem();
-      group_sync(bar_id);  // all of the slot is written
-      if (t == 0) {
-        arrive(&bars.g_free[gb]);
-        arrive(&bars.t_ready[sl]);
-        arrive(&bars.p_ready[sl]);
-        // a peer's shared memory takes about 18 bytes a clock, so what its chain
-        // needs first goes first to all of them
-#pragma unroll
-        for (int p = 1; p < C::kCl; ++p) {
-          const uint32_t to = (uint32_t)(slice + p) % C::kCl;
-          copy_to_peer(slot_s, 8192, &bars.t_ready[sl], to);
-          copy_to_peer(slot_s + 16384, C::kCopyBytes - 16384, &bars.t_ready[sl], to);
-        }
-#pragma unroll
-        for (int p = 1; p < C::kCl; ++p)
-          copy_to_peer(slot_s + 8192, 8192, &bars.p_ready[sl], (uint32_t)(slice + p) % C::kCl);
-        if (F16 && c + C::kCl < nch) load_rows(kq, c + C::kCl, &bars.p_full);
-      }
-    }
   } else if (warp == C::kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ----------------------------------------------------- the chain's products
     // As the chain warps, it goes on without waiting once out of time.
     constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
@@ -998,14 +1019,14 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
     const uint64_t y_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kY), 0);
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kSlots, st = c & 1;
+      const int sl = c % C::kRecs, st = c & 1;
       const uint32_t kq = tc::smem_u32(smem + st * C::kStageBytes);
       const uint64_t k_op = tc::sw128_desc(kq), kl_op = tc::sw128_desc(kq + 32768);
       const uint64_t kt_op = tc::sw128_desc_mn(kq, 16384), klt_op = tc::sw128_desc_mn(kq + 32768, 8192);
-      const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes));
+      const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecStride));
       ok = ok && warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
-      chain_await(2);
+      chain_await(kBarS);
       if (leader && ok) {  // X = K S
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
@@ -1022,8 +1043,10 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      ok = ok && warp_wait(&bars.t_ready[sl], (uint32_t)(c / C::kSlots) & 1u);
-      chain_await(3);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
+      // behind D, the chain overwrites what P D of the last chunk reads
+      if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);
+      chain_await(kBarY);
       if (leader && ok) {  // D = T Y
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
@@ -1036,7 +1059,7 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         tc::mma_commit(&bars.d_full);
       }
       __syncwarp();
-      chain_await(4);
+      chain_await(kBarDs);
       if (leader && ok) {  // dS = K^T D'
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
@@ -1048,53 +1071,30 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
           for (int j = 0; j < 4; ++j)
             tc::mma_bf16(tmem + kTmU, klt_op + ((j * 2048) >> 4), y_op + ((j * 2048) >> 4), kIdU, true);
         }
-        tc::mma_commit(&bars.u_full);
         tc::mma_commit(&bars.free_[st]);
       }
       __syncwarp();
-    }
-  } else if (warp == C::kLoadWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // -------------------------------------------------------------- TMA loads
-    const bool leader = elect_one();
-    for (int c = 0; c < nch; ++c) {
-      const int st = c & 1;
-      if (c >= 2 && !(ok = warp_wait(&bars.free_[st], (uint32_t)(c / 2 - 1) & 1u))) break;
-      uint8_t* kq = smem + st * C::kStageBytes;
-      if (leader) load_rows(kq, c, &bars.full[st]);
+      // behind dS, the chain overwrites what Q S reads
+      ok = ok && warp_wait(&bars.xq_full, (uint32_t)c & 1u);
+      if (leader && ok) tc::mma_commit(&bars.u_full);
       __syncwarp();
-      if (c == nch - 1 && L % kC != 0) {
-        if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
-        zero_tail(kq, L % kC, lane, 32);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (leader) arrive(&bars.tail);
-      }
     }
   } else if (warp == C::kSideWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // ------------------------- products for the output alone; the slots' traffic
+    // ------------------------- products for the output alone
+    // As the chain warps, it goes on without waiting once out of time.
     constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
     const bool leader = elect_one();
-    auto expect = [&](int c) {  // a peer's copies will land in this slot
-      if (leader && c < nch && c % C::kCl != slice) {
-        tc::mbar_expect_tx(&bars.t_ready[c % C::kSlots], C::kCopyBytes - 8192);
-        tc::mbar_expect_tx(&bars.p_ready[c % C::kSlots], 8192);
-      }
-    };
-    for (int c = 0; c < C::kSlots; ++c) expect(c);
     const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
     const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kSlots, st = c & 1;
+      const int sl = c % C::kRecs, st = c & 1;
       const uint32_t cp = (uint32_t)c & 1u;
       const uint64_t q_op = tc::sw128_desc(tc::smem_u32(smem + st * C::kStageBytes + 8192));
-      const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + C::kSlot + sl * C::kSlotBytes + 8192));
-      if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
-      if (!(ok = warp_wait(&bars.s_ready, cp))) break;
-      if (c > 0 && !(ok = warp_wait(&bars.o_read, cp ^ 1u))) break;  // both accumulators have been read
-      tc::tc_fence_after();
-      if (leader) {  // Q S
+      const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecStride + kRecP));
+      ok = ok && warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u);
+      if (c > 0) ok = ok && warp_wait(&bars.q_read, cp ^ 1u);  // the last Q S has been read
+      chain_await(kBarSq);
+      if (leader && ok) {  // Q S
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
@@ -1105,81 +1105,66 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         tc::mma_commit(&bars.free_[st]);
       }
       __syncwarp();
-      if (!(ok = warp_wait(&bars.p_ready[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
-      if (!(ok = warp_wait(&bars.v_ready, cp))) break;
-      tc::tc_fence_after();
-      if (leader) {  // P D
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
+      if (c > 0) ok = ok && warp_wait(&bars.o_read, cp ^ 1u);
+      chain_await(kBarD);  // the chain is also past T and this chunk's scalars
+      if (leader && ok) {  // P D
 #pragma unroll
         for (int b = 0; b < C::kTiles; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO, p_op + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX,
-                         b + j > 0);
+            tc::mma_bf16(tmem + kTmO, p_op + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX, b + j > 0);
         tc::mma_commit(&bars.o_full);
-        tc::mma_commit(&bars.used[sl]);
+        tc::mma_commit(&bars.rec_free[sl]);
       }
       __syncwarp();
-      // used up here: the CTA that fills the slot next is told
-      if (c + C::kSlots < nch) {
-        if (!(ok = warp_wait(&bars.used[sl], (uint32_t)(c / C::kSlots) & 1u))) break;
-        expect(c + C::kSlots);
-        if (leader) arrive_peer(&bars.slot_free, (uint32_t)(c + C::kSlots) % C::kCl);
+    }
+  } else if (warp == C::kRowWarp) {
+    // ------------------------------------------------------------ rows of K, Q
+    const bool leader = elect_one();
+    if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
+    int issued = 0;
+    for (int c = 0; c < nch; ++c) {
+      const int st = c & 1;
+      if (c >= 2 && !(ok = warp_wait(&bars.free_[st], (uint32_t)(c / 2 - 1) & 1u))) break;
+      uint8_t* kq = smem + st * C::kStageBytes;
+      if (leader) load_rows<F16>(maps, kq, (int)t0 + c * kC, h / args.G, &bars.full[st]);
+      __syncwarp();
+      issued = c + 1;
+      if (c == nch - 1 && L % kC != 0) {
+        if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
+        zero_tail<F16>(kq, L % kC, lane, 32);
+        tc::fence_async_smem();
         __syncwarp();
+        if (leader) arrive(&bars.tail);
       }
     }
+    // nothing may land after the CTA is gone
+    for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) warp_wait(&bars.full[c & 1], (uint32_t)(c >> 1) & 1u);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // ------------------------------------------------------------------ gate
-    const ScalarGateArgs& ga = args.gate;
-    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
-    for (int c = slice, k = 0; c < nch; c += C::kCl, ++k) {
-      const int gb = k % C::kGates;
-      GateScalars& gs = *reinterpret_cast<GateScalars*>(smem + C::kScalars + gb * sizeof(GateScalars));
-      float gl[2], be[2];  // tokens 2 lane, 2 lane + 1; past the end nothing decays and nothing is written
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tok = c * kC + 2 * lane + e;
-        gl[e] = be[e] = 0.f;
-        if (tok < L) {
-          const int64_t at = (t0 + tok) * args.HV + h;
-          const float b = in16_to_float<F16>(args.beta[at]);
-          gl[e] = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
-          be[e] = ga.beta_is_raw ? sigmoidf_(b) : b;
-        }
+    // --------------------------------------------------------- chunks' records
+    const bool leader = elect_one();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint8_t* src = args.records + (bars.chunk0 * args.HV + h) * kRecStride;
+    int issued = 0;
+    for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kRecs;
+      if (c >= C::kRecs && !(ok = warp_wait(&bars.rec_free[sl], (uint32_t)(c / C::kRecs - 1) & 1u))) break;
+      if (leader) {
+        tc::mbar_expect_tx(&bars.rec[sl], kRecBytes);
+        tc::bulk_g2s(smem + C::kRec + sl * kRecStride, src + (int64_t)c * args.HV * kRecStride, kRecBytes, &bars.rec[sl]);
       }
-      // running sums in FP64, kept as two floats: differences of them count
-      const double pair = (double)gl[0] + (double)gl[1];
-      double run = pair;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, run, d);
-        if (lane >= d) run += up;
-      }
-      const double c0 = run - (double)gl[1];
-      if (k >= C::kGates && !(ok = warp_wait(&bars.g_free[gb], (uint32_t)(k / C::kGates - 1) & 1u))) break;
-      gs.hi[2 * lane] = (float)c0;
-      gs.lo[2 * lane] = (float)(c0 - (double)(float)c0);
-      gs.hi[2 * lane + 1] = (float)run;
-      gs.lo[2 * lane + 1] = (float)(run - (double)(float)run);
-      gs.beta[2 * lane] = be[0];
-      gs.beta[2 * lane + 1] = be[1];
       __syncwarp();
-      if (lane == 0) arrive(&bars.g_ready[gb]);
+      issued = c + 1;
     }
+    for (int c = issued > C::kRecs ? issued - C::kRecs : 0; c < issued; ++c)
+      warp_wait(&bars.rec[c % C::kRecs], (uint32_t)(c / C::kRecs) & 1u);
   }
-  if (!ok) misc.timed_out = 1;
+  if (!ok) bars.timed_out = 1;
   tc::tc_fence_before();
   __syncthreads();
-  // peers copy into this CTA's shared memory and signal its barriers
-  cluster_sync();
   tc::tc_fence_after();
-  if (misc.timed_out) {
-    if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-    // every role has stopped, but not all copies were waited for: none takes
-    // this long, and none may land after the CTA is gone
-    for (int i = 0; i < 4; ++i) __nanosleep(500000);
-  }
+  if (tid == 0 && bars.timed_out) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
   if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
 }
 
@@ -1219,37 +1204,66 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const uint4* __restrict
   k_lo[i] = lo;
 }
 
-template <int DVS, bool F16>
-kda_status launch_prefill(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
-  using C = Cfg<DVS, F16>;
-  static_assert(C::kSmem <= 232448, "shared memory of one CTA");
-  static_assert(C::kSlots <= C::kCl && sizeof(ChunkScalars) % 16 == 0, "slots");
-  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+// Sets a kernel's shared-memory limit once per device.
+template <typename Kernel>
+kda_status allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>* ready) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
-  if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    if (cudaFuncSetAttribute(gdn_prefill_kernel<DVS, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
-        cudaSuccess)
+  if (!(ready->load(std::memory_order_relaxed) >> dev & 1u)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
       return KDA_ERR_CUDA;
-    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    ready->fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  const int64_t grid = (int64_t)a.num_seqs * a.HV * C::kCl;
-  if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::kCl;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // behind split_rows_kernel
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  return KDA_OK;
+}
+
+// A launch that may start while the one before it runs (its kernel waits).
+template <typename Kernel>
+kda_status launch_after(Kernel kernel, unsigned grid, unsigned threads, int smem, bool dependent, cudaStream_t st,
+                        const GdnPrefillArgs& a, const GdnMaps& m) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = F16 ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, gdn_prefill_kernel<DVS, F16>, a, m);
+  cfg.numAttrs = dependent ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kernel, a, m);
   return launch_status();
+}
+
+template <bool F16>
+kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  static_assert(3 * (ChunkCfg<F16>::kSmem + 1024) <= 233472, "three CTAs per SM");
+  kda_status s = allow_smem(gdn_chunk_kernel<F16>, ChunkCfg<F16>::kSmem, &ready);
+  if (s != KDA_OK) return s;
+  const int64_t grid = a.max_chunks * a.HV;
+  if (grid > INT32_MAX) return KDA_ERR_SHAPE;
+  return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg<F16>::kSmem, F16, st, a, m);
+}
+
+template <int DVS, bool F16>
+kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
+  using C = Cfg<DVS, F16>;
+  static std::atomic<uint64_t> ready{0};
+  static_assert(C::kSmem <= 232448 && C::kThreads == 768, "shared memory and registers of one CTA");
+  kda_status s = allow_smem(gdn_state_kernel<DVS, F16>, C::kSmem, &ready);
+  if (s != KDA_OK) return s;
+  const int64_t grid = (int64_t)a.num_seqs * a.HV * (kHeadDim / DVS);
+  if (grid > INT32_MAX) return KDA_ERR_SHAPE;
+  return launch_after(gdn_state_kernel<DVS, F16>, (unsigned)grid, C::kThreads, C::kSmem, true, st, a, m);
+}
+
+constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred cycles for 8, two thousand for 128
+
+int64_t most_chunks(int num_seqs, int64_t total_tokens) { return total_tokens / kC + num_seqs; }
+
+size_t split_bytes(const kda_dims& d, int64_t total_tokens) {  // one of q, k hi, k lo as BF16
+  return d.dtype == KDA_DTYPE_F16 ? ((size_t)total_tokens * d.H * kHeadDim * 2 + 255) / 256 * 256 : 0;
 }
 
 }  // namespace
@@ -1257,10 +1271,10 @@ kda_status launch_prefill(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_
 
 using namespace kda;
 
-extern "C" size_t kda_gdn_prefill_workspace_size(kda_dims dims, int64_t total_tokens) {
-  if (dims.dtype != KDA_DTYPE_F16 || dims.H <= 0 || total_tokens < 0) return 0;
+extern "C" size_t kda_gdn_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens) {
+  if (num_seqs < 0 || total_tokens < 0 || dims.H <= 0 || dims.HV <= 0) return 0;
   if (total_tokens > INT32_MAX) return SIZE_MAX;  // refused; no capacity check may pass
-  return 3 * (size_t)total_tokens * dims.H * kHeadDim * 2;
+  return 3 * split_bytes(dims, total_tokens) + (size_t)most_chunks(num_seqs, total_tokens) * dims.HV * kRecStride;
 }
 
 extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
@@ -1282,9 +1296,9 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state_pool) ||
       !aligned16(intermediate))
     return KDA_ERR_ALIGNMENT;
-  const size_t need = kda_gdn_prefill_workspace_size(dims, total_tokens);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
-  if (need > 0 && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
+  const size_t need = kda_gdn_prefill_workspace_size(dims, num_seqs, total_tokens);
+  if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KDA_ERR_ALIGNMENT;
   GdnPrefillArgs args{};
   s = check_scalar_gate(gate, a, beta, &args.gate);
   if (s != KDA_OK) return s;
@@ -1306,8 +1320,10 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.err_flag = err_flag;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = dims.dtype == KDA_DTYPE_F16;
-  const size_t part = need / 3;
+  const size_t part = split_bytes(dims, total_tokens);
   char* ws = static_cast<char*>(workspace);
+  args.records = reinterpret_cast<uint8_t*>(ws + 3 * part);
+  args.max_chunks = most_chunks(num_seqs, total_tokens);
   GdnMaps m{};
   if (!encode_half_rows(&m.q, f16 ? static_cast<const void*>(ws) : q, dims.H, total_tokens) ||
       !encode_half_rows(&m.k, f16 ? static_cast<const void*>(ws + part) : k, dims.H, total_tokens) ||
@@ -1322,14 +1338,14 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
     s = launch_status();
     if (s != KDA_OK) return s;
   }
+  s = f16 ? launch_chunks<true>(args, m, st) : launch_chunks<false>(args, m, st);
+  if (s != KDA_OK) return s;
   record_stage(1, st);
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
-  if (f16)
-    s = launch_prefill<32, true>(args, m, st);
-  else
-    s = (int64_t)num_seqs * dims.HV * 4 <= sms ? launch_prefill<32, false>(args, m, st)
-                                               : launch_prefill<64, false>(args, m, st);
+  // CTAs that do not all start at once: the longest sequences first
+  args.longest_first = num_seqs > 1 && num_seqs <= kMaxSorted && (int64_t)num_seqs * dims.HV * 4 > sms;
+  s = f16 ? launch_state<32, true>(args, m, st) : launch_state<32, false>(args, m, st);
   record_stage(2, st);
   return s;
 }

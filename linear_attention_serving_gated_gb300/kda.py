@@ -119,7 +119,7 @@ def load(path: str = LIB_PATH):
         lib.kda_commit_replay.argtypes = [kda_dims, vp, i32, i32, vp, vp, i32, vp, vp, vp]
         lib.kda_gdn_prefill.restype = i32
         lib.kda_gdn_prefill_workspace_size.restype = sz
-        lib.kda_gdn_prefill_workspace_size.argtypes = [kda_dims, i64]
+        lib.kda_gdn_prefill_workspace_size.argtypes = [kda_dims, i32, i64]
         lib.kda_gdn_prefill.argtypes = [kda_dims, kda_scalar_gate, vp, vp, vp, vp, vp, i64, vp, i32, vp, vp,
                                         i32, i64, vp, vp, i64, vp, sz, vp, vp]
         lib.kda_gdn_decode_packed.restype = i32
@@ -459,8 +459,8 @@ def _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, rows, reqs):
     _at_least(state_idx, reqs, "state_idx", f"[{reqs}]")
 
 
-def kda_gdn_prefill_workspace_size(d: kda_dims, total_tokens: int) -> int:
-    return int(load().kda_gdn_prefill_workspace_size(d, int(total_tokens)))
+def kda_gdn_prefill_workspace_size(d: kda_dims, num_seqs: int, total_tokens: int) -> int:
+    return int(load().kda_gdn_prefill_workspace_size(d, int(num_seqs), int(total_tokens)))
 
 
 def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, cu_seqlens, num_seqs, o,
@@ -484,9 +484,10 @@ def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, c
     _at_least(state_idx, num_seqs, "state_idx", f"[{num_seqs}]")
     _at_least(cu_seqlens, num_seqs + 1, "cu_seqlens", f"[{num_seqs + 1}]")
     inter_chunks = _intermediate_chunks(d, intermediate)
-    if workspace is None and d.dtype == KDA_DTYPE_F16:
-        workspace = torch.empty(max(kda_gdn_prefill_workspace_size(d, T), 1), dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is None:
+        workspace = torch.empty(max(kda_gdn_prefill_workspace_size(d, num_seqs, T), 1), dtype=torch.uint8,
+                                device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size()
     st = load().kda_gdn_prefill(
         d, gate.c(d), _in16(d, q, "q"), _in16(d, k, "k"), _in16(d, v, "v"), _scalar_gate_input(d, gate, a),
         _in16(d, b, "b"), int(gb_rows), _typed(state_pool, torch.float32, "state_pool"), int(state_pool.shape[0]),

@@ -28,7 +28,7 @@ def test_gdn_host_errors(lib):
     row = 3 * 16 * 128
 
     def pre(d=kda.dims(16), g=sgate(), q=D, a=D, pool=D, idx=D, gb=64, T=64, n=1, inter=None, chunks=0,
-            ws=None, ws_bytes=0):
+            ws=D, ws_bytes=1 << 40):
         return lib.kda_gdn_prefill(d, g, q, D, D, a, D, gb, pool, 4, idx, None, n, T, D, inter, chunks, ws, ws_bytes,
                                    None, None)
 
@@ -40,10 +40,12 @@ def test_gdn_host_errors(lib):
     assert pre(g=sgate(None), a=ODD) == pre(a=ctypes.c_void_p(0x10001)) == kda.KDA_ERR_ALIGNMENT
     assert pre(T=0, gb=0) == kda.KDA_OK  # nothing to do
     f16 = kda.dims(16, dtype=kda.KDA_DTYPE_F16)
-    assert kda.kda_gdn_prefill_workspace_size(f16, 64) == 3 * 64 * 16 * 256
-    assert kda.kda_gdn_prefill_workspace_size(kda.dims(16), 64) == 0
-    assert pre(d=f16) == pre(d=f16, ws=D, ws_bytes=3 * 64 * 16 * 256 - 1) == kda.KDA_ERR_WORKSPACE
-    assert pre(d=f16, ws=ODD, ws_bytes=1 << 30) == kda.KDA_ERR_ALIGNMENT
+    assert kda.kda_gdn_prefill_workspace_size(kda.dims(16), 3, 100) == 4 * 16 * 25600
+    assert kda.kda_gdn_prefill_workspace_size(f16, 3, 100) == 4 * 16 * 25600 + 3 * 100 * 16 * 256
+    assert kda.kda_gdn_prefill_workspace_size(kda.dims(16), 1, 2 ** 31) == 2 ** 64 - 1
+    assert pre(ws=None) == pre(ws_bytes=2 * 16 * 25600 - 1) == kda.KDA_ERR_WORKSPACE
+    assert pre(d=f16, ws_bytes=2 * 16 * 25600) == kda.KDA_ERR_WORKSPACE
+    assert pre(ws=ODD) == kda.KDA_ERR_ALIGNMENT
 
     def dec(d=kda.dims(16), stride=row, pool=D, qkv=D, B=2):
         return lib.kda_gdn_decode_packed(d, sgate(), qkv, stride, D, D, B, pool, 240, D, D, None, None)
