@@ -14,34 +14,43 @@
 // they are: K K^T and Q K^T are exact up to FP32 sums, every exponent is of a
 // difference c_i - c_j <= 0, and no decay is too strong for the chunk form.
 //
-// Two kernels.  Everything of a chunk that does not depend on the state is the
-// same for all value columns and for all chunks at once:
+// Two kernels.  Everything of a chunk that does not depend on the state is ready
+// for all chunks at once:
 //   gdn_chunk_kernel, a CTA of 128 threads per (chunk, value head), 3 per SM:
 //     norms, decays, [K; Q] K^T on the tensor cores, A and P, T by blocks, and
-//     one record of 25 KB (T, P, the chunk's row factors) for the second kernel.
-// What is left is a chain of three dependent products a chunk:
-//   gdn_state_kernel, a CTA per (sequence, value head, DVS value columns).  Its
-//     state stays on the SM for the whole sequence.  The chain's latency, not
-//     bytes or flops, bounds a long sequence, so nothing else is on it:
-//   * 16 chain warps hold S in FP32 registers and turn each product's TMEM
-//     accumulator into the next one's operand; products are
-//       X  = K S           64 x DVS x 128
-//       D  = T Y           64 x DVS x 64
-//       dS = K^T D'       128 x DVS x 64, D'_j = e^(c_last - c_j) r_j D_j
+//     one record of 41 KB (T, P, Q scaled by scale rq e^c, the chunk's row
+//     factors) for the second kernel.
+// What is left is a chain of three dependent products a chunk.  Its latency, not
+// bytes or flops, bounds a long sequence, so nothing else is on it.  16 chain
+// warps hold the state in FP32 registers for the whole sequence and turn each
+// product's TMEM accumulator into the next one's operand; one warp issues the
+// products from behind hardware barriers, one Q S and P D, which only the output
+// needs and 4 warps of their own store; two load the chunks' keys and records.
+// Two forms of that kernel:
+//   gdn_state_kernel, a CTA per (sequence, value head, 32 value columns):
+//       X  = K S           64 x 32 x 128
+//       D  = T Y           64 x 32 x 64
+//       dS = K^T D'       128 x 32 x 64, D'_j = e^(c_last - c_j) r_j D_j
+//     S, Y and D' are right operands in shared memory, MN-major, the hi and lo
+//     halves beside each other in one 64-wide tile: one product each for both.
 //     M = 64 spreads the token rows over all four warp quadrants of TMEM, 16
-//     lanes each, read in the fragment layout so that all 32 threads work;
-//   * one warp issues these products from behind hardware barriers, one Q S and
-//     P D, which only the output needs and 4 warps of their own join; one loads
-//     the chunks' records, K and Q by TMA.
-// Preparing chunks inside the chain's CTAs, shared over clusters of a head's
-// slices, was measured first: it needed no memory in between but slowed the chain
-// on its SM (1 x 4096 at 16 heads 125 us).
+//     lanes each, read in the fragment layout so that all 32 threads work.
+//   gdn_state_wide_kernel, a CTA per (sequence, value head), transposed:
+//       X^T  = S^T K^T     128 x 64 x 128
+//       D^T  = Y^T T^T     128 x 64 x 64
+//       dS^T = D'^T K      128 x 128 x 64
+//     Every product has the value columns as its rows, and what one's epilogue
+//     makes is the next one's left operand, taken from TMEM: a thread's lane of
+//     the accumulator becomes its lane of the operand, and nothing of the chain
+//     passes through shared memory.
+// The first takes a chunk in less time, the second does four times as much in it:
+// it is taken once its CTAs fill the SMs (kda_gdn_prefill has both sides).
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
 // wherever the state depends on them: S, T, Y and D'.  K and Q are BF16 already.
 // FP16 keys are split exactly (11 bits into 8 + 8) and FP16 queries rounded to
-// BF16 by a pass over them before the kernel; FP16 operands would need S and D
-// in FP16 halves, whose range is not the state's.  P alone is rounded to BF16 once (2^-9): it
-// only enters the output, itself rounded to 16 bits.
+// BF16 by a pass over them before the kernels; FP16 operands would need S and D
+// in FP16 halves, whose range is not the state's.  P, the scaled Q and the S that meets it are
+// rounded to BF16 once (2^-9): they only enter the output, itself of 16 bits.
 #include <atomic>
 
 #include "kda_host.h"
@@ -78,66 +87,69 @@ struct GdnMaps {
   CUtensorMap q, k, k_lo;
 };
 
-// What the state kernel reads of a chunk beside T and P.
+// What the state kernel reads of a chunk beside T, P and Q.
 struct ChunkScalars {
-  float a[kC];  // r_i e^(c_i)
+  float a[kC];  // -r_i e^(c_i)
   float s[kC];  // r_j e^(c_last - c_j), 0 past the sequence's end
-  float o[kC];  // scale rq_i e^(c_i)
   float last;   // e^(c_last)
   float done;   // 1: the record is complete
   float pad[2];
 };
-// A chunk's record: T hi, P, T lo (tiles of 64 128-byte swizzled lines), scalars.
-constexpr int kRecT = 0, kRecP = 8192, kRecTlo = 16384, kRecScalars = 24576;
-constexpr int kRecBytes = kRecScalars + (int)sizeof(ChunkScalars);
-constexpr int kRecStride = 25600;
-static_assert(kRecBytes % 16 == 0 && kRecBytes <= kRecStride, "record");
+// A chunk's record: T hi, P, T lo (tiles of 64 128-byte swizzled lines), scalars,
+// scaled Q (two halves of 64 channels, 64 lines each).
+constexpr int kRecT = 0, kRecP = 8192, kRecTlo = 16384, kRecScalars = 24576, kRecQ = 25600, kRecBytes = 41984;
+static_assert(kRecScalars + sizeof(ChunkScalars) <= kRecQ, "record");
 
-template <bool F16>
-constexpr int kRowBytes = 32768 + (F16 ? 16384 : 0);  // a chunk's [K; Q] and, from FP16, the keys' low halves
-
-// Shared memory of the chunk kernel.  A (hi, lo, diagonal blocks in FP32) lies in
-// K and Q once their products are done.
+// Shared memory of the chunk kernel: [K; Q] as two halves of 64 channels and
+// 128 lines each, the low halves of FP16 keys, and the record but for Q, which is
+// scaled where it lies.  A's hi and lo halves take the place of K once its
+// products are done.
 template <bool F16>
 struct ChunkCfg {
-  static constexpr int kRec = kRowBytes<F16>;
-  static constexpr int kGate = kRec + kRecStride;  // float hi[64], lo[64], beta[64], rk[64]
+  static constexpr int kRowBytes = 32768 + (F16 ? 16384 : 0);
+  static constexpr int kRec = kRowBytes;
+  // A's diagonal blocks in FP32: over the keys' low halves where there are any
+  static constexpr int kDiag = F16 ? 32768 : kRec + kRecQ;
+  static constexpr int kGate = kRec + kRecQ + (F16 ? 0 : 4 * 16 * kLdG * 4);  // float hi[64], lo[64], beta[64], rk[64]
   static constexpr int kBar = kGate + 4 * kC * 4;
   static constexpr int kSmem = kBar + 64;
   static constexpr int kTmCols = F16 ? 128 : 64;
 };
 
 struct Bars {
-  uint64_t full[2], free_[2];   // K and Q stages: landed, consumed
-  uint64_t tail;                // rows past the end of the last chunk zeroed
-  uint64_t rec[3], rec_free[3]; // records
+  uint64_t key[3], key_free[3];  // key stages: landed (rows past the end zeroed: tail), consumed
+  uint64_t tail;
+  uint64_t rec[3], rec_free[3];  // records
   uint64_t x_full, xq_full, d_full, u_full;
-  uint64_t o_full, q_read, o_read;
+  uint64_t o_full, o_read;
   int64_t chunk0;  // id of the sequence's first chunk
   uint32_t tmem;
   int timed_out;
 };
 
+// Roles of a state CTA's warps.
 constexpr int kChainWarps = 16, kOutWarps = 4;
+constexpr int kMmaWarp = kChainWarps + kOutWarps, kSideWarp = kMmaWarp + 1, kKeyWarp = kMmaWarp + 2,
+              kRecWarp = kMmaWarp + 3, kStateThreads = (kRecWarp + 1) * 32;
 
-template <int DVS, bool F16>
+template <bool F16>
 struct Cfg {
-  static constexpr int kTiles = DVS * 2 / 64;  // 64-wide operand tiles: [hi], [lo], or one [hi | lo]
-  static constexpr int kStageBytes = kRowBytes<F16>;
-  static constexpr int kRecs = 3;
-  static constexpr int kRec = 2 * kStageBytes;
-  static constexpr int kS = kRec + kRecs * kRecStride;
-  static constexpr int kY = kS + kTiles * 16384;
-  static constexpr int kD = kY + kTiles * 8192;
-  static constexpr int kBars = kD + kTiles * 8192;
-  static constexpr int kSmem = kBars + (int)sizeof(Bars);
-  static constexpr int kMmaWarp = kChainWarps + kOutWarps, kSideWarp = kMmaWarp + 1, kRowWarp = kMmaWarp + 2,
-                       kRecWarp = kMmaWarp + 3;
-  static constexpr int kThreads = (kRecWarp + 1) * 32;
+  static constexpr int kKeyBytes = 16384 * (F16 ? 2 : 1);  // K, low halves of FP16 keys
+  static constexpr int kDepth = F16 ? 2 : 3;               // chunks in shared memory
+  static constexpr int kRec = kDepth * kKeyBytes;
+  static constexpr int kBars = kRec + kDepth * kRecBytes;
+  // gdn_state_kernel's operands
+  static constexpr int kS = (kBars + (int)sizeof(Bars) + 1023) / 1024 * 1024;
+  static constexpr int kY = kS + 16384;
+  static constexpr int kD = kY + 8192;
+  static constexpr int kSmem = kD + 8192, kWideSmem = kBars + (int)sizeof(Bars);
 };
 
-// TMEM columns of the state kernel
-constexpr int kTmX = 0, kTmQ = 64, kTmD = 128, kTmU = 192, kTmO = 256, kTmCols = 512;
+// TMEM columns of the wide kernel.  Left operands (two BF16 a column): S, Y and
+// after it D', D; accumulators: X and after it D, dS, O.  The other kernel has
+// accumulators alone, in the same columns.
+constexpr int kTmS = 0, kTmSlo = 64, kTmY = 128, kTmYlo = 160, kTmD = 192, kTmDlo = 224;
+constexpr int kTmX = 256, kTmU = 320, kTmO = 448, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -169,22 +181,6 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// The chain warps have written an operand: the warps that issue its products
-// wait for them at a hardware barrier, which wakes them sooner than an mbarrier
-// would and costs the chain one instruction.  The fence between the chain's
-// writes and the tensor core's reads stands behind the barrier, in the issuing
-// warp alone: in front of it, in every chain warp, it took about 280 cycles of
-// each of the chain's stages (1 x 4096 at 16 heads, 28 us of the whole).
-enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6 };  // kBarSq: S, for Q S
-__device__ __forceinline__ void chain_arrive(int id) {
-  tc::tc_fence_before();
-  asm volatile("barrier.cta.arrive %0, 544;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ void chain_await(int id) {
-  asm volatile("barrier.cta.sync %0, 544;" ::"r"(id) : "memory");
-  tc::fence_async_smem();
-  tc::tc_fence_after();
-}
 // Two FP32 values as BF16 hi and lo halves.
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
@@ -217,29 +213,6 @@ __device__ __forceinline__ uint4* line16(uint8_t* tile, int row, int piece) {
   return reinterpret_cast<uint4*>(tile + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-// A row's values as operand halves: columns [part * N, part * N + N) of the CTA's
-// DVS = 4 N, in tiles [hi], [lo] 64 wide (DVS = 64) or one tile [hi | lo].
-template <int DVS>
-__device__ __forceinline__ void put_split(uint8_t* tiles, int tile_bytes, int row, int part, const float (&x)[DVS / 4]) {
-#pragma unroll
-  for (int j = 0; j < DVS / 32; ++j) {
-    uint4 hi, lo;
-    split8(x + 8 * j, hi, lo);
-    const int piece = part * (DVS / 32) + j;
-    *line16(tiles, row, piece) = hi;
-    if (DVS == 64)
-      *line16(tiles + tile_bytes, row, piece) = lo;
-    else
-      *line16(tiles, row, 4 + piece) = lo;
-  }
-}
-
-__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-
 // Waits for this thread's TMEM loads; r is not used before.
 template <int M>
 __device__ __forceinline__ void wait_ld(uint32_t (&r)[M]) {
@@ -247,80 +220,115 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[M]) {
 #pragma unroll
   for (int i = 0; i < M; ++i) asm volatile("" : "+r"(r[i]));
 }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A warp's accumulator columns of its part: 16, or 8 of the hi product plus the
-// same 8 of the lo product.
-template <int DVS>
-__device__ __forceinline__ void get_acc(uint32_t taddr, int part, float (&x)[DVS / 4]) {
-  if constexpr (DVS == 64) {
-    uint32_t a[16];
-    tc::tmem_ld16_async(taddr + part * 16, a);
-    wait_ld(a);
+__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 16 values of a lane as 8 + 8 columns of the operands hi and lo.
+__device__ __forceinline__ void put_split16(uint32_t hi_addr, uint32_t lo_addr, const float* x) {
+  uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(a[j]);
-  } else {
-    uint32_t a[8], b[8];
-    tmem_ld8_async(taddr + part * 8, a);
-    tmem_ld8_async(taddr + 32 + part * 8, b);
-    wait_ld(a);
-    wait_ld(b);
+  for (int j = 0; j < 8; ++j) split2(make_float2(x[2 * j], x[2 * j + 1]), hi[j], lo[j]);
+  tmem_st8(hi_addr, hi);
+  tmem_st8(lo_addr, lo);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread; 16 k are 8 columns of A.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+constexpr int kDv = 32;  // value columns of a CTA of gdn_state_kernel
+
+// A row's values as operand halves: columns [8 part, 8 part + 8) of the CTA's, in a
+// tile [hi | lo].
+__device__ __forceinline__ void put_split(uint8_t* tile, int row, int part, const float (&x)[8]) {
+  uint4 hi, lo;
+  split8(x, hi, lo);
+  *line16(tile, row, part) = hi;
+  *line16(tile, row, 4 + part) = lo;
+}
+
+// A warp's 8 accumulator columns: the hi product's plus the lo product's.
+__device__ __forceinline__ void get_acc(uint32_t taddr, int part, float (&x)[8]) {
+  uint32_t a[8], b[8];
+  tmem_ld8_async(taddr + part * 8, a);
+  tmem_ld8_async(taddr + 32 + part * 8, b);
+  wait_ld(a);
+  wait_ld(b);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const float2 s = add2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
-                            make_float2(__uint_as_float(b[j]), __uint_as_float(b[j + 1])));
-      x[j] = s.x;
-      x[j + 1] = s.y;
-    }
+  for (int j = 0; j < 8; j += 2) {
+    const float2 s = add2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
+                          make_float2(__uint_as_float(b[j]), __uint_as_float(b[j + 1])));
+    x[j] = s.x;
+    x[j + 1] = s.y;
   }
 }
 
-
-// The same columns as operand halves (see put_split).
-template <int J>
-__device__ __forceinline__ void put_rows(uint8_t* tiles, int row, int part, int lane, const float (&x)[J][4]) {
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t hi, lo;
-      split2(make_float2(x[j][2 * e], x[j][2 * e + 1]), hi, lo);
-      const int rr = row + 8 * e, piece = part * J + j;
-      uint8_t* line = tiles + rr * 128 + 4 * (lane & 3);
-      *reinterpret_cast<uint32_t*>(line + ((piece ^ (rr & 7)) << 4)) = hi;
-      if (J == 2)
-        *reinterpret_cast<uint32_t*>(line + 8192 + ((piece ^ (rr & 7)) << 4)) = lo;
-      else
-        *reinterpret_cast<uint32_t*>(line + (((4 + piece) ^ (rr & 7)) << 4)) = lo;
-    }
-}
-
-// A warp's columns of a token-row accumulator (its part of the slice), 16 rows in
-// the fragment layout: rows lane / 4 and + 8, columns 8 j + 2 (lane % 4) and + 1;
-// 16 columns (J = 2), or 8 of the hi product plus the same 8 of the lo product.
+// The same for a token-row accumulator, 16 rows in the fragment layout: rows
+// lane / 4 and + 8, columns 2 (lane % 4) and + 1.
 __device__ __forceinline__ void ld_frag8(uint32_t taddr, uint32_t (&r)[4]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
 }
-template <int J>
-__device__ __forceinline__ void get_rows(uint32_t taddr, int part, float (&x)[J][4]) {
+__device__ __forceinline__ void get_rows(uint32_t taddr, int part, float2 (&x)[2]) {
   uint32_t a[4], b[4];
-  ld_frag8(taddr + part * 8 * J, a);
-  ld_frag8(taddr + part * 8 * J + (J == 2 ? 8 : 32), b);
+  ld_frag8(taddr + part * 8, a);
+  ld_frag8(taddr + 32 + part * 8, b);
   wait_ld(a);
   wait_ld(b);
 #pragma unroll
-  for (int e = 0; e < 4; e += 2) {
-    const float2 u = make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-    const float2 v = make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1]));
-    const float2 s = J == 2 ? u : add2(u, v);
-    x[0][e] = s.x;
-    x[0][e + 1] = s.y;
-    if (J == 2) {
-      x[J - 1][e] = v.x;
-      x[J - 1][e + 1] = v.y;
-    }
+  for (int e = 0; e < 2; ++e)
+    x[e] = add2(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
+                make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])));
+}
+__device__ __forceinline__ void put_rows(uint8_t* tile, int row, int part, int lane, const float2 (&x)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t hi, lo;
+    split2(x[e], hi, lo);
+    const int rr = row + 8 * e;
+    uint8_t* line = tile + rr * 128 + 4 * (lane & 3);
+    *reinterpret_cast<uint32_t*>(line + ((part ^ (rr & 7)) << 4)) = hi;
+    *reinterpret_cast<uint32_t*>(line + (((4 + part) ^ (rr & 7)) << 4)) = lo;
   }
+}
+
+// The chain warps have written an operand: the warps that issue its products
+// wait for them at a hardware barrier, which wakes them sooner than an mbarrier
+// would and costs the chain one instruction.  kBarSq: S, for Q S.
+enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6 };
+template <bool TMEM>
+__device__ __forceinline__ void chain_arrive(int id) {
+  if (TMEM) wait_st();
+  tc::tc_fence_before();
+  asm volatile("barrier.cta.arrive %0, 544;" ::"r"(id) : "memory");
+}
+// For operands in shared memory the fence between the chain's writes and the
+// tensor core's reads stands here, behind the barrier, in the issuing warp alone:
+// in front of it, in every chain warp, it took about 280 cycles of each stage.
+template <bool TMEM>
+__device__ __forceinline__ void chain_await(int id) {
+  asm volatile("barrier.cta.sync %0, 544;" ::"r"(id) : "memory");
+  if (!TMEM) tc::fence_async_smem();
+  tc::tc_fence_after();
 }
 
 __device__ __forceinline__ int64_t seq_start(const GdnPrefillArgs& a, int n) {
@@ -487,26 +495,12 @@ __device__ __forceinline__ void invert64(uint8_t* t_hi, uint8_t* t_lo, const uin
   inverse_block<2>(t_hi, t_lo, a_hi, a_lo, 0, 32, 32 + 16 * (warp >> 1), 16 * (warp & 1), lane);
 }
 
-// The rows of a chunk from token `tok` on: [K; Q] as two halves of 64 channels,
-// 128 lines each, and behind them the low halves of FP16 keys.
-template <bool F16>
-__device__ __forceinline__ void load_rows(const GdnMaps& maps, uint8_t* kq, int tok, int hk, uint64_t* bar) {
-  tc::mbar_expect_tx(bar, kRowBytes<F16>);
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, bar);
-    tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, bar);
-    if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, bar);
-  }
-}
 // K rows [len, 64) zeroed by `threads` threads: they belong to the next sequence
-// or lie past the last token, and NaN times a zero factor is NaN.
-template <bool F16>
-__device__ __forceinline__ void zero_tail(uint8_t* kq, int len, int t, int threads) {
-  for (int x = t; x < (kC - len) * 16; x += threads) {
-    *line16(kq + (x & 1) * 16384, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
-    if (F16) *line16(kq + 32768 + (x & 1) * 8192, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
-  }
+// or lie past the last token, and NaN times a zero factor is NaN.  The two halves
+// of 64 channels are `half` bytes apart.
+__device__ __forceinline__ void zero_rows(uint8_t* k, int half, int len, int t, int threads) {
+  for (int x = t; x < (kC - len) * 16; x += threads)
+    *line16(k + (x & 1) * half, len + x / 16, (x >> 1) & 7) = make_uint4(0, 0, 0, 0);
 }
 
 template <bool F16>
@@ -561,9 +555,9 @@ __global__ void __launch_bounds__(128, 3)
 
   uint8_t* kq = smem;
   uint8_t* rec = smem + C::kRec;
-  uint8_t* a_hi = smem;
-  uint8_t* a_lo = a_hi + 8192;
-  float* diag = reinterpret_cast<float*>(a_lo + 8192);
+  uint8_t* a_hi = smem;  // over the first half of K, and over the second
+  uint8_t* a_lo = smem + 16384;
+  float* diag = reinterpret_cast<float*>(smem + C::kDiag);
   float* c_hi = reinterpret_cast<float*>(smem + C::kGate);  // c_i = c_hi + c_lo
   float* c_lo = c_hi + kC;
   float* beta_s = c_lo + kC;
@@ -574,7 +568,14 @@ __global__ void __launch_bounds__(128, 3)
     tc::mbar_init(&bars[0], 1);
     tc::mbar_init(&bars[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    load_rows<F16>(maps, kq, (int)t0, h / args.G, &bars[0]);
+    tc::mbar_expect_tx(&bars[0], C::kRowBytes);
+    const int tok = (int)t0, hk = h / args.G;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, &bars[0]);
+      tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, &bars[0]);
+      if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, &bars[0]);
+    }
   }
   if (quad == 0) tc::tmem_alloc(reinterpret_cast<uint32_t*>(&bars[2]), C::kTmCols);
   if (quad == 3) {  // decays and betas: tokens 2 lane and 2 lane + 1
@@ -617,7 +618,8 @@ __global__ void __launch_bounds__(128, 3)
   const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16);
   bool bad = !warp_wait(&bars[0], 0);
   if (len < kC) {
-    zero_tail<F16>(kq, len, t, 128);
+    zero_rows(kq, 16384, len, t, 128);
+    if (F16) zero_rows(kq + 32768, 8192, len, t, 128);
     tc::fence_async_smem();
     __syncthreads();
   }
@@ -735,6 +737,23 @@ __global__ void __launch_bounds__(128, 3)
       *line16(rec + kRecP, i, 2 * jb + 1) = round8(d + 8);
     }
   }
+  if (!krow) {  // Q scaled in place: [K; Q] K^T is done with it
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        uint4* at = line16(kq + a * 16384, 64 + i, p);
+        const uint4 w = *at;
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[2 * e] = r * ei * __uint_as_float(ww[e] << 16);
+          f[2 * e + 1] = r * ei * __uint_as_float(ww[e] & 0xffff0000u);
+        }
+        *at = round8(f);
+      }
+  }
   tc::tc_fence_before();
   bad = __syncthreads_or(bad);
   if (quad == 0) {
@@ -743,40 +762,42 @@ __global__ void __launch_bounds__(128, 3)
   }
   invert64(rec + kRecT, rec + kRecTlo, a_hi, a_lo, diag, beta_s, quad, lane);
   if (krow) {
-    sc.a[i] = r * ei;
+    sc.a[i] = -r * ei;
     sc.s[i] = si;
-    if (i == 63) sc.last = ei;
-  } else {
-    sc.o[i] = r * ei;
-    if (i == 0) sc.done = bad ? 0.f : 1.f;
+    if (i == 63) {
+      sc.last = ei;
+      sc.done = bad ? 0.f : 1.f;
+    }
   }
   tc::fence_async_smem();
   __syncthreads();
   if (t == 0) {
     if (bad) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-    tc::bulk_s2g(args.records + ((int64_t)id * args.HV + h) * kRecStride, rec, kRecBytes);
+    uint8_t* dst = args.records + ((int64_t)id * args.HV + h) * kRecBytes;
+    tc::bulk_s2g(dst, rec, kRecQ);
+    tc::bulk_s2g(dst + kRecQ, kq + 8192, 8192);
+    tc::bulk_s2g(dst + kRecQ + 8192, kq + 24576, 8192);
     tc::bulk_commit();
     tc::bulk_wait_read();
   }
 }
 
-template <int DVS, bool F16>
-__global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
-    gdn_state_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
-  using C = Cfg<DVS, F16>;
-  constexpr int N = DVS / 4;  // value columns per chain thread
-  constexpr int kSlices = kHeadDim / DVS;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
+// What a state CTA works on.
+struct Unit {
+  int h, slice, n;
+  int L, nch, slot;
+  int64_t t0;
+};
+
+// The first steps of a state CTA: its sequence, refusals (false: the whole CTA
+// leaves), barriers and TMEM.  `columns` value columns per CTA.
+__device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* smem, Bars& bars, int columns, Unit& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slice = blockIdx.x % kSlices;
-  const int unit = blockIdx.x / kSlices;
-  const int h = unit % args.HV;
-  int n = unit / args.HV;
-  const bool reporter = tid == 0 && slice == 0 && h == 0;
+  const bool reporter = tid == 0 && s.h == 0 && s.slice == 0;
+  int n = s.n;
   if (args.longest_first) {  // CTAs start in order: sequence n is the n-th longest
     int* len_s = reinterpret_cast<int*>(smem);
-    for (int m = tid; m < args.num_seqs; m += C::kThreads) len_s[m] = seq_len(args, m);
+    for (int m = tid; m < args.num_seqs; m += kStateThreads) len_s[m] = seq_len(args, m);
     __syncthreads();
     if (tid < args.num_seqs) {
       const int mine = len_s[tid];
@@ -795,11 +816,11 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
   if (L > 0 && (slot < 0 || slot >= args.pool_slots)) {  // padding or out of range: zero outputs, no state touched
     stop = true;
     if (slot != -1 && reporter) set_error(args.err_flag, KDA_DEVERR_SLOT);
-    constexpr int kPieces = DVS / 8;
     const int64_t t0 = seq_start(args, n);
-    for (int64_t i = tid; i < (int64_t)L * kPieces; i += C::kThreads)
-      *reinterpret_cast<uint4*>(args.o + ((t0 + i / kPieces) * args.HV + h) * kHeadDim + slice * DVS +
-                                (i % kPieces) * 8) = make_uint4(0, 0, 0, 0);
+    const int pieces = columns / 8;
+    for (int64_t i = tid; i < (int64_t)L * pieces; i += kStateThreads)
+      *reinterpret_cast<uint4*>(args.o + ((t0 + i / pieces) * args.HV + s.h) * kHeadDim + s.slice * columns +
+                                (i % pieces) * 8) = make_uint4(0, 0, 0, 0);
   }
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
     stop = true;
@@ -813,28 +834,29 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     if (lane == 0) bars.chunk0 = id;
   }
   __syncthreads();
-  const int64_t t0 = seq_start(args, n);
-  const int nch = (L + kC - 1) / kC;
-  if (!stop && bars.chunk0 + nch > args.max_chunks) {  // overlapping sequences have more chunks than tokens allow
+  s.t0 = seq_start(args, n);
+  s.L = L;
+  s.slot = slot;
+  s.nch = (L + kC - 1) / kC;
+  s.n = n;
+  if (!stop && bars.chunk0 + s.nch > args.max_chunks) {  // overlapping sequences have more chunks than tokens allow
     stop = true;
     if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
   }
   if (stop) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for the one before too
-    return;
+    return false;
   }
 
   tc::fence_async_smem();  // the lengths lay where rows land
-  if (warp == C::kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
+  if (warp == kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
     bars.timed_out = 0;
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bars.full[i], 1);
-      tc::mbar_init(&bars.free_[i], 2);
-    }
-    for (int i = 0; i < C::kRecs; ++i) {
+    for (int i = 0; i < 3; ++i) {
+      tc::mbar_init(&bars.key[i], 1);
+      tc::mbar_init(&bars.key_free[i], 1);
       tc::mbar_init(&bars.rec[i], 1);
-      tc::mbar_init(&bars.rec_free[i], 1 + kOutWarps);
+      tc::mbar_init(&bars.rec_free[i], 1);
     }
     tc::mbar_init(&bars.tail, 1);
     tc::mbar_init(&bars.x_full, 1);
@@ -842,163 +864,207 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
     tc::mbar_init(&bars.d_full, 1);
     tc::mbar_init(&bars.u_full, 1);
     tc::mbar_init(&bars.o_full, 1);
-    tc::mbar_init(&bars.q_read, kOutWarps);
     tc::mbar_init(&bars.o_read, kOutWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  return true;
+}
+
+// And its last ones.
+__device__ __forceinline__ void end_unit(const GdnPrefillArgs& args, Bars& bars, uint32_t tmem, bool ok) {
+  if (!ok) bars.timed_out = 1;
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (threadIdx.x == 0 && bars.timed_out) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+  if (threadIdx.x >> 5 == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
+}
+
+// The key warp: every chunk's keys, as two halves of 64 channels.
+template <bool F16>
+__device__ __forceinline__ bool load_keys(const GdnPrefillArgs& args, const GdnMaps& maps, uint8_t* smem, Bars& bars,
+                                          const Unit& s, int lane) {
+  using C = Cfg<F16>;
+  bool ok = true;
+  const bool leader = elect_one();
+  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
+  int issued = 0;
+  for (int c = 0; c < s.nch; ++c) {
+    const int sl = c % C::kDepth;
+    if (c >= C::kDepth && !(ok = warp_wait(&bars.key_free[sl], (uint32_t)(c / C::kDepth - 1) & 1u))) break;
+    uint8_t* key = smem + sl * C::kKeyBytes;
+    if (leader) {
+      tc::mbar_expect_tx(&bars.key[sl], C::kKeyBytes);
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        tma_box(key + a * 8192, &maps.k, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
+        if (F16) tma_box(key + 16384 + a * 8192, &maps.k_lo, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
+      }
+    }
+    __syncwarp();
+    issued = c + 1;
+    if (c == s.nch - 1 && s.L % kC != 0) {
+      if (!(ok = warp_wait(&bars.key[sl], (uint32_t)(c / C::kDepth) & 1u))) break;
+      zero_rows(key, 8192, s.L % kC, lane, 32);
+      if (F16) zero_rows(key + 16384, 8192, s.L % kC, lane, 32);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (leader) arrive(&bars.tail);
+    }
+  }
+  // nothing may land after the CTA is gone
+  for (int c = issued > C::kDepth ? issued - C::kDepth : 0; c < issued; ++c)
+    warp_wait(&bars.key[c % C::kDepth], (uint32_t)(c / C::kDepth) & 1u);
+  return ok;
+}
+
+// The record warp.
+template <bool F16>
+__device__ __forceinline__ bool load_records(const GdnPrefillArgs& args, uint8_t* smem, Bars& bars, const Unit& s) {
+  using C = Cfg<F16>;
+  bool ok = true;
+  const bool leader = elect_one();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint8_t* src = args.records + (bars.chunk0 * args.HV + s.h) * kRecBytes;
+  int issued = 0;
+  for (int c = 0; c < s.nch; ++c) {
+    const int sl = c % C::kDepth;
+    if (c >= C::kDepth && !(ok = warp_wait(&bars.rec_free[sl], (uint32_t)(c / C::kDepth - 1) & 1u))) break;
+    if (leader) {
+      tc::mbar_expect_tx(&bars.rec[sl], kRecBytes);
+      tc::bulk_g2s(smem + C::kRec + sl * kRecBytes, src + (int64_t)c * args.HV * kRecBytes, kRecBytes, &bars.rec[sl]);
+    }
+    __syncwarp();
+    issued = c + 1;
+  }
+  for (int c = issued > C::kDepth ? issued - C::kDepth : 0; c < issued; ++c)
+    warp_wait(&bars.rec[c % C::kDepth], (uint32_t)(c / C::kDepth) & 1u);
+  return ok;
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kStateThreads, 1)
+    gdn_state_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+  using C = Cfg<F16>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Unit s;
+  constexpr int kSlices = kHeadDim / kDv;
+  s.slice = blockIdx.x % kSlices;
+  s.h = blockIdx.x / kSlices % args.HV;
+  s.n = blockIdx.x / kSlices / args.HV;
+  if (!begin_unit(args, smem, bars, kDv, s)) return;
+  const int h = s.h, L = s.L, nch = s.nch;
+  const int64_t t0 = s.t0;
   const uint32_t tmem = bars.tmem;
   bool ok = true;
-
   if (warp < kChainWarps) {
     // ---------------------------------------------------------------- chain
     // A warp that runs out of time goes on without waiting, so that the others
     // still meet it.
-    constexpr int J = N / 8;
     const int quad = warp & 3, part = warp >> 2;
-    const int row = 16 * quad + (lane >> 2);   // token rows row and row + 8 of the chunk
-    const int colx = slice * DVS + part * N + 2 * (lane & 3);  // value columns colx + 8 j, + 1 of those
-    const int dk = 32 * quad + lane;           // key channel of the state
-    const int col0 = slice * DVS + part * N;   // value columns col0 + j of the state
+    const int row = 16 * quad + (lane >> 2);  // token rows row and row + 8 of the chunk, columns
+    const int colx = s.slice * kDv + part * 8 + 2 * (lane & 3);  // colx and colx + 1 of those
+    const int dk = 32 * quad + lane;          // key channel of the state,
+    const int col0 = s.slice * kDv + part * 8;  // its columns col0 ..
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    float* root = args.pool + (((size_t)slot * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
-    float S[N];
+    float* root = args.pool + (((size_t)s.slot * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
+    float S[8];
 #pragma unroll
-    for (int j = 0; j < N; ++j) S[j] = root[j * kHeadDim];
+    for (int j = 0; j < 8; ++j) S[j] = root[j * kHeadDim];
     const int64_t cid = bars.chunk0;
-    uint32_t vraw[J][2];
+    uint32_t vraw[2];
     const int64_t vstep = (int64_t)args.HV * kHeadDim;
     const kda_bf16* vsrc = args.v + ((t0 + row) * args.HV + h) * kHeadDim + colx;
     auto load_v = [&](int c) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          vraw[j][e] = c * kC + row + 8 * e < L ? __ldg(reinterpret_cast<const uint32_t*>(vsrc + 8 * e * vstep + 8 * j)) : 0u;
+        vraw[e] = c * kC + row + 8 * e < L ? __ldg(reinterpret_cast<const uint32_t*>(vsrc + 8 * e * vstep)) : 0u;
       vsrc += kC * vstep;
     };
     load_v(0);
-    float last, fa[2], fs[2];  // e^(c_last); -r e^(c_i) and r e^(c_last - c_i) of the two rows
-    auto load_factors = [&](int c) {
-      const int sl = c % C::kRecs;
-      const ChunkScalars& sc =
-          *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecStride + kRecScalars);
-      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u, ok);
-      last = sc.last;
-      fa[0] = -sc.a[row];
-      fa[1] = -sc.a[row + 8];
-      fs[0] = sc.s[row];
-      fs[1] = sc.s[row + 8];
-      ok = ok && sc.done == 1.f;
-    };
     for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kDepth;
       const uint32_t cp = (uint32_t)c & 1u;
-      put_split<DVS>(smem + C::kS, 16384, dk, part, S);
-      chain_arrive(kBarS);
+      put_split(smem + C::kS, dk, part, S);
+      chain_arrive<false>(kBarS);
       asm volatile("barrier.cta.arrive %0, 544;" ::"r"((int)kBarSq) : "memory");
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
 #pragma unroll
-          for (int j = 0; j < N; ++j) dst[j * kHeadDim] = S[j];
-        } else if (reporter) {
+          for (int j = 0; j < 8; ++j) dst[j * kHeadDim] = S[j];
+        } else if (threadIdx.x == 0 && h == 0 && s.slice == 0) {
           set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
         }
       }
-      load_factors(c);
+      const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecBytes + kRecScalars);
+      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u, ok);
+      const float last = sc.last;
+      const float fa[2] = {sc.a[row], sc.a[row + 8]}, fs[2] = {sc.s[row], sc.s[row + 8]};
+      ok = ok && sc.done == 1.f;
       chain_wait(&bars.x_full, cp, ok);
       tc::tc_fence_after();
-      float x[J][4];
-      get_rows<J>(lanes + kTmX, part, x);
+      float2 x[2], y[2];
+      get_rows(lanes + kTmX, part, x);
       // Y = v - r e^c (K S)
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const uint32_t w = vraw[j][e >> 1];
-          float2 v;
-          if constexpr (F16)
-            v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-          else
-            v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-          v = fma2(make_float2(fa[e >> 1], fa[e >> 1]), make_float2(x[j][e], x[j][e + 1]), v);
-          x[j][e] = v.x;
-          x[j][e + 1] = v.y;
-        }
-      put_rows<J>(smem + C::kY, row, part, lane, x);
-      chain_arrive(kBarY);
+      for (int e = 0; e < 2; ++e) {
+        float2 v;
+        if constexpr (F16)
+          v = __half22float2(*reinterpret_cast<const __half2*>(&vraw[e]));
+        else
+          v = make_float2(__uint_as_float(vraw[e] << 16), __uint_as_float(vraw[e] & 0xffff0000u));
+        x[e] = fma2(make_float2(fa[e], fa[e]), x[e], v);
+      }
+      put_rows(smem + C::kY, row, part, lane, x);
+      chain_arrive<false>(kBarY);
       if (c + 1 < nch) load_v(c + 1);
       chain_wait(&bars.d_full, cp, ok);
       tc::tc_fence_after();
-      get_rows<J>(lanes + kTmD, part, x);
-      float y[J][4];
+      get_rows(lanes + kTmX, part, x);
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float2 s = mul2(make_float2(fs[e >> 1], fs[e >> 1]), make_float2(x[j][e], x[j][e + 1]));
-          y[j][e] = s.x;
-          y[j][e + 1] = s.y;
-        }
-      put_rows<J>(smem + C::kY, row, part, lane, y);
-      chain_arrive(kBarDs);
-      put_rows<J>(smem + C::kD, row, part, lane, x);
-      chain_arrive(kBarD);
+      for (int e = 0; e < 2; ++e) y[e] = mul2(make_float2(fs[e], fs[e]), x[e]);
+      put_rows(smem + C::kY, row, part, lane, y);
+      chain_arrive<false>(kBarDs);
+      put_rows(smem + C::kD, row, part, lane, x);
+      chain_arrive<false>(kBarD);
       chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
-      float u[N];
-      get_acc<DVS>(lanes + kTmU, part, u);
+      float u[8];
+      get_acc(lanes + kTmU, part, u);
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const float2 s = fma2(make_float2(last, last), make_float2(S[j], S[j + 1]), make_float2(u[j], u[j + 1]));
-        S[j] = s.x;
-        S[j + 1] = s.y;
+      for (int j = 0; j < 8; j += 2) {
+        const float2 n2 = fma2(make_float2(last, last), make_float2(S[j], S[j + 1]), make_float2(u[j], u[j + 1]));
+        S[j] = n2.x;
+        S[j + 1] = n2.y;
       }
     }
     if (ok)
 #pragma unroll
-      for (int j = 0; j < N; ++j) root[j * kHeadDim] = S[j];
-  } else if (warp < C::kMmaWarp) {
+      for (int j = 0; j < 8; ++j) root[j * kHeadDim] = S[j];
+  } else if (warp < kMmaWarp) {
     // --------------------------------------------------------------- outputs
-    // O = scale rq e^c Q S + P D, 16 token rows a warp.
-    constexpr int J = DVS / 32;
+    // 16 token rows a warp.
     const int quad = warp & 3;
     const int row = 16 * quad + (lane >> 2);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + slice * DVS + 2 * (lane & 3);
+    kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + s.slice * kDv + 2 * (lane & 3);
     const int64_t step = (int64_t)args.HV * kHeadDim;
     for (int c = 0; c < nch; ++c, dst += kC * step) {
-      const int sl = c % C::kRecs;
-      const uint32_t cp = (uint32_t)c & 1u;
-      const ChunkScalars& sc =
-          *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecStride + kRecScalars);
-      if (!(ok = warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u))) break;
-      const float fo[2] = {sc.o[row], sc.o[row + 8]};
-      __syncwarp();
-      if (lane == 0) arrive(&bars.rec_free[sl]);
-      if (!(ok = warp_wait(&bars.xq_full, cp))) break;
+      if (!(ok = warp_wait(&bars.o_full, (uint32_t)c & 1u))) break;
       tc::tc_fence_after();
-      float x[4][J][4];
-#pragma unroll
-      for (int part = 0; part < 4; ++part) get_rows<J>(lanes + kTmQ, part, x[part]);
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(&bars.q_read);
-      if (!(ok = warp_wait(&bars.o_full, cp))) break;
-      tc::tc_fence_after();
-      uint32_t w[4][J][2];
+      uint32_t w[4][2];
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float u[J][4];
-        get_rows<J>(lanes + kTmO, part, u);
+        float2 x[2];
+        get_rows(lanes + kTmO, part, x);
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            w[part][j][e] = pack_out16x2<F16>(fmaf(fo[e], x[part][j][2 * e], u[j][2 * e]),
-                                              fmaf(fo[e], x[part][j][2 * e + 1], u[j][2 * e + 1]));
+        for (int e = 0; e < 2; ++e) w[part][e] = pack_out16x2<F16>(x[e].x, x[e].y);
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -1008,73 +1074,58 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
         if (c * kC + row + 8 * e < L) {
 #pragma unroll
           for (int part = 0; part < 4; ++part)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-              *reinterpret_cast<uint32_t*>(dst + 8 * e * step + 8 * (part * J + j)) = w[part][j][e];
+            *reinterpret_cast<uint32_t*>(dst + 8 * e * step + 8 * part) = w[part][e];
         }
     }
-  } else if (warp == C::kMmaWarp) {
+  } else if (warp == kMmaWarp) {
     // ----------------------------------------------------- the chain's products
     // As the chain warps, it goes on without waiting once out of time.
-    constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
+    constexpr uint32_t kId64 = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
     constexpr uint32_t kIdU = tc::idesc_bf16_f32(128, 64) | tc::kIdescMnA | tc::kIdescMnB;
-    const bool leader = elect_one();
     const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
     const uint64_t y_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kY), 0);
+    const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kRecs, st = c & 1;
-      const uint32_t kq = tc::smem_u32(smem + st * C::kStageBytes);
-      const uint64_t k_op = tc::sw128_desc(kq), kl_op = tc::sw128_desc(kq + 32768);
-      const uint64_t kt_op = tc::sw128_desc_mn(kq, 16384), klt_op = tc::sw128_desc_mn(kq + 32768, 8192);
-      const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecStride));
-      ok = ok && warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u);
+      const int sl = c % C::kDepth;
+      const uint32_t ph = (uint32_t)(c / C::kDepth) & 1u;
+      const uint32_t key = tc::smem_u32(smem + sl * C::kKeyBytes);
+      const uint64_t k_op = tc::sw128_desc(key), kl_op = tc::sw128_desc(key + 16384);
+      const uint64_t kt_op = tc::sw128_desc_mn(key, 8192), klt_op = tc::sw128_desc_mn(key + 16384, 8192);
+      const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecBytes));
+      ok = ok && warp_wait(&bars.key[sl], ph);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
-      chain_await(kBarS);
+      chain_await<false>(kBarS);
       if (leader && ok) {  // X = K S
 #pragma unroll
-        for (int b = 0; b < C::kTiles; ++b)
+        for (int b = 0; b < (F16 ? 2 : 1); ++b)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX, k_op + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
-                         s_op + ((b * 16384 + j * 2048) >> 4), kIdX, b + j > 0);
-        if constexpr (F16) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX, kl_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kIdX,
-                         true);
-        }
+            tc::mma_bf16(tmem + kTmX, (b ? kl_op : k_op) + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4),
+                         kId64, b + j > 0);
         tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
+      ok = ok && warp_wait(&bars.rec[sl], ph);
       // behind D, the chain overwrites what P D of the last chunk reads
       if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);
-      chain_await(kBarY);
+      chain_await<false>(kBarY);
       if (leader && ok) {  // D = T Y
 #pragma unroll
-        for (int b = 0; b < C::kTiles; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmD, t_op + ((j * 32) >> 4), y_op + ((b * 8192 + j * 2048) >> 4), kIdX, b + j > 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          tc::mma_bf16(tmem + kTmD, t_op + ((16384 + j * 32) >> 4), y_op + ((j * 2048) >> 4), kIdX, true);
+            tc::mma_bf16(tmem + kTmX, t_op + (((b ? kRecTlo : 0) + j * 32) >> 4), y_op + ((j * 2048) >> 4), kId64, b + j > 0);
         tc::mma_commit(&bars.d_full);
       }
       __syncwarp();
-      chain_await(kBarDs);
+      chain_await<false>(kBarDs);
       if (leader && ok) {  // dS = K^T D'
 #pragma unroll
-        for (int b = 0; b < C::kTiles; ++b)
+        for (int b = 0; b < (F16 ? 2 : 1); ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmU, kt_op + ((j * 2048) >> 4), y_op + ((b * 8192 + j * 2048) >> 4), kIdU, b + j > 0);
-        if constexpr (F16) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmU, klt_op + ((j * 2048) >> 4), y_op + ((j * 2048) >> 4), kIdU, true);
-        }
-        tc::mma_commit(&bars.free_[st]);
+            tc::mma_bf16(tmem + kTmU, (b ? klt_op : kt_op) + ((j * 2048) >> 4), y_op + ((j * 2048) >> 4), kIdU, b + j > 0);
+        tc::mma_commit(&bars.key_free[sl]);
       }
       __syncwarp();
       // behind dS, the chain overwrites what Q S reads
@@ -1082,93 +1133,314 @@ __global__ void __launch_bounds__(Cfg<DVS, F16>::kThreads, 1)
       if (leader && ok) tc::mma_commit(&bars.u_full);
       __syncwarp();
     }
-  } else if (warp == C::kSideWarp) {
-    // ------------------------- products for the output alone
+  } else if (warp == kSideWarp) {
+    // ----------------------------------------- products for the output alone
     // As the chain warps, it goes on without waiting once out of time.
-    constexpr uint32_t kIdX = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
-    const bool leader = elect_one();
+    constexpr uint32_t kId64 = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
     const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
     const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
+    const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kRecs, st = c & 1;
-      const uint32_t cp = (uint32_t)c & 1u;
-      const uint64_t q_op = tc::sw128_desc(tc::smem_u32(smem + st * C::kStageBytes + 8192));
-      const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecStride + kRecP));
-      ok = ok && warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u);
-      if (c > 0) ok = ok && warp_wait(&bars.q_read, cp ^ 1u);  // the last Q S has been read
-      chain_await(kBarSq);
-      if (leader && ok) {  // Q S
+      const int sl = c % C::kDepth;
+      const uint32_t rec = tc::smem_u32(smem + C::kRec + sl * kRecBytes);
+      const uint64_t q_op = tc::sw128_desc(rec + kRecQ), p_op = tc::sw128_desc(rec + kRecP);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u);
+      if (c > 0) ok = ok && warp_wait(&bars.o_read, (uint32_t)(c - 1) & 1u);
+      chain_await<false>(kBarSq);
+      if (leader && ok) {  // O = Q S
 #pragma unroll
-        for (int b = 0; b < C::kTiles; ++b)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmQ, q_op + (((j >> 2) * 16384 + (j & 3) * 32) >> 4),
-                         s_op + ((b * 16384 + j * 2048) >> 4), kIdX, b + j > 0);
+        for (int j = 0; j < 8; ++j)
+          tc::mma_bf16(tmem + kTmO, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kId64, j > 0);
         tc::mma_commit(&bars.xq_full);
-        tc::mma_commit(&bars.free_[st]);
       }
       __syncwarp();
-      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
-      if (c > 0) ok = ok && warp_wait(&bars.o_read, cp ^ 1u);
-      chain_await(kBarD);  // the chain is also past T and this chunk's scalars
-      if (leader && ok) {  // P D
+      chain_await<false>(kBarD);  // the chain is also past T and this chunk's scalars
+      if (leader && ok) {  // + P D
 #pragma unroll
-        for (int b = 0; b < C::kTiles; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO, p_op + ((j * 32) >> 4), d_op + ((b * 8192 + j * 2048) >> 4), kIdX, b + j > 0);
+        for (int j = 0; j < 4; ++j)
+          tc::mma_bf16(tmem + kTmO, p_op + ((j * 32) >> 4), d_op + ((j * 2048) >> 4), kId64, true);
         tc::mma_commit(&bars.o_full);
         tc::mma_commit(&bars.rec_free[sl]);
       }
       __syncwarp();
     }
-  } else if (warp == C::kRowWarp) {
-    // ------------------------------------------------------------ rows of K, Q
-    const bool leader = elect_one();
-    if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
-    int issued = 0;
-    for (int c = 0; c < nch; ++c) {
-      const int st = c & 1;
-      if (c >= 2 && !(ok = warp_wait(&bars.free_[st], (uint32_t)(c / 2 - 1) & 1u))) break;
-      uint8_t* kq = smem + st * C::kStageBytes;
-      if (leader) load_rows<F16>(maps, kq, (int)t0 + c * kC, h / args.G, &bars.full[st]);
-      __syncwarp();
-      issued = c + 1;
-      if (c == nch - 1 && L % kC != 0) {
-        if (!(ok = warp_wait(&bars.full[st], (uint32_t)(c >> 1) & 1u))) break;
-        zero_tail<F16>(kq, L % kC, lane, 32);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (leader) arrive(&bars.tail);
-      }
-    }
-    // nothing may land after the CTA is gone
-    for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) warp_wait(&bars.full[c & 1], (uint32_t)(c >> 1) & 1u);
+  } else if (warp == kKeyWarp) {
+    ok = load_keys<F16>(args, maps, smem, bars, s, lane);
   } else {
-    // --------------------------------------------------------- chunks' records
-    const bool leader = elect_one();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint8_t* src = args.records + (bars.chunk0 * args.HV + h) * kRecStride;
-    int issued = 0;
+    ok = load_records<F16>(args, smem, bars, s);
+  }
+  end_unit(args, bars, tmem, ok);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kStateThreads, 1)
+    gdn_state_wide_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+  using C = Cfg<F16>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Unit s;
+  s.slice = 0;
+  s.h = blockIdx.x % args.HV;
+  s.n = blockIdx.x / args.HV;
+  if (!begin_unit(args, smem, bars, kHeadDim, s)) return;
+  const int h = s.h, L = s.L, nch = s.nch;
+  const int64_t t0 = s.t0;
+  const uint32_t tmem = bars.tmem;
+  bool ok = true;
+  if (warp < kChainWarps) {
+    // 64 registers for the others leave the chain 88 of the 80 all start with
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    // ---------------------------------------------------------------- chain
+    // A warp that runs out of time goes on without waiting, so that the others
+    // still meet it.
+    const int quad = warp & 3, part = warp >> 2;
+    const int dv = 32 * quad + lane;  // this thread's value column
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const int tok0 = 16 * part;       // its tokens of a chunk; its key channels of the state: 32 part ..
+    float* root = args.pool + (((size_t)s.slot * args.HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
+    float S[32];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(S + 4 * j) = *reinterpret_cast<const float4*>(root + 4 * j);
+    const int64_t cid = bars.chunk0;
+    // v of the 16 tokens.  A lane loads two neighbouring columns of every other
+    // token and trades with its neighbour: 32-bit loads, two tokens a register.
+    const int64_t vstep = (int64_t)args.HV * kHeadDim;
+    const int odd = lane & 1;
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
+    const kda_bf16* vsrc = args.v + ((t0 + tok0 + odd) * args.HV + h) * kHeadDim + (dv & ~1);
+    uint32_t vraw[8];
+    auto load_v = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        vraw[j] = c * kC + tok0 + odd + 2 * j < L ? __ldg(reinterpret_cast<const uint32_t*>(vsrc + 2 * j * vstep)) : 0u;
+      vsrc += kC * vstep;
+    };
+    load_v(0);
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kRecs;
-      if (c >= C::kRecs && !(ok = warp_wait(&bars.rec_free[sl], (uint32_t)(c / C::kRecs - 1) & 1u))) break;
-      if (leader) {
-        tc::mbar_expect_tx(&bars.rec[sl], kRecBytes);
-        tc::bulk_g2s(smem + C::kRec + sl * kRecStride, src + (int64_t)c * args.HV * kRecStride, kRecBytes, &bars.rec[sl]);
+      const int sl = c % C::kDepth;
+      const uint32_t cp = (uint32_t)c & 1u;
+      put_split16(lanes + kTmS + 16 * part, lanes + kTmSlo + 16 * part, S);
+      put_split16(lanes + kTmS + 16 * part + 8, lanes + kTmSlo + 16 * part + 8, S + 16);
+      chain_arrive<true>(kBarS);
+      asm volatile("barrier.cta.arrive %0, 544;" ::"r"((int)kBarSq) : "memory");
+      if (args.intermediate) {
+        if (cid + c < args.inter_chunks) {
+          float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(dst + 4 * j) = *reinterpret_cast<const float4*>(S + 4 * j);
+        } else if (threadIdx.x == 0 && h == 0) {
+          set_error(args.err_flag, KDA_DEVERR_INTERMEDIATE);
+        }
+      }
+      uint32_t v2[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v2[j] = __byte_perm(vraw[j], __shfl_xor_sync(0xffffffffu, vraw[j], 1), pick);
+      const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecBytes + kRecScalars);
+      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u, ok);
+      const float last = sc.last;
+      ok = ok && sc.done == 1.f;
+      chain_wait(&bars.x_full, cp, ok);
+      tc::tc_fence_after();
+      float x[16];
+      {
+        uint32_t r[16];
+        tc::tmem_ld16_async(lanes + kTmX + tok0, r);
+        wait_ld(r);
+        // Y = v - r e^c (K S)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 a = *reinterpret_cast<const float2*>(sc.a + tok0 + 2 * j);
+          float2 v;
+          if constexpr (F16)
+            v = __half22float2(*reinterpret_cast<const __half2*>(&v2[j]));
+          else
+            v = make_float2(__uint_as_float(v2[j] << 16), __uint_as_float(v2[j] & 0xffff0000u));
+          const float2 y = fma2(a, make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), v);
+          x[2 * j] = y.x;
+          x[2 * j + 1] = y.y;
+        }
+      }
+      put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, x);
+      chain_arrive<true>(kBarY);
+      if (c + 1 < nch) load_v(c + 1);
+      chain_wait(&bars.d_full, cp, ok);
+      tc::tc_fence_after();
+      {
+        uint32_t r[16];
+        tc::tmem_ld16_async(lanes + kTmX + tok0, r);
+        wait_ld(r);
+        float y[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[2 * j] = __uint_as_float(r[2 * j]);
+          x[2 * j + 1] = __uint_as_float(r[2 * j + 1]);
+          const float2 s = mul2(*reinterpret_cast<const float2*>(sc.s + tok0 + 2 * j), make_float2(x[2 * j], x[2 * j + 1]));
+          y[2 * j] = s.x;
+          y[2 * j + 1] = s.y;
+        }
+        put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, y);
+      }
+      chain_arrive<true>(kBarDs);
+      put_split16(lanes + kTmD + 8 * part, lanes + kTmDlo + 8 * part, x);
+      chain_arrive<true>(kBarD);
+      chain_wait(&bars.u_full, cp, ok);
+      tc::tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t r[16];
+        tc::tmem_ld16_async(lanes + kTmU + 32 * part + 16 * g, r);
+        wait_ld(r);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 s = fma2(make_float2(last, last), make_float2(S[16 * g + j], S[16 * g + j + 1]),
+                                make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+          S[16 * g + j] = s.x;
+          S[16 * g + j + 1] = s.y;
+        }
+      }
+    }
+    if (ok)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(root + 4 * j) = *reinterpret_cast<const float4*>(S + 4 * j);
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // --------------------------------------------------------------- outputs
+    // 32 value columns a warp, 64 tokens a thread.
+    const int quad = warp & 3, odd = lane & 1;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
+    const int64_t step = (int64_t)args.HV * kHeadDim;
+    kda_bf16* dst = args.o + ((t0 + odd) * args.HV + h) * kHeadDim + ((32 * quad + lane) & ~1);
+    for (int c = 0; c < nch; ++c, dst += kC * step) {
+      if (!(ok = warp_wait(&bars.o_full, (uint32_t)c & 1u))) break;
+      tc::tc_fence_after();
+      uint32_t w[32];  // two tokens of one column each
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t r[16];
+        tc::tmem_ld16_async(lanes + kTmO + 16 * g, r);
+        wait_ld(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[8 * g + j] = pack_out16x2<F16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&bars.o_read);
+      const int left = L - c * kC - odd;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {  // traded for two columns of one token each
+        const uint32_t x = __byte_perm(w[j], __shfl_xor_sync(0xffffffffu, w[j], 1), pick);
+        if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = x;
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ----------------------------------------------------- the chain's products
+    // As the chain warps, it goes on without waiting once out of time.
+    constexpr uint32_t kId64 = tc::idesc_bf16_f32(128, 64);
+    constexpr uint32_t kIdU = tc::idesc_bf16_f32(128, 128) | tc::kIdescMnB;
+    const bool leader = elect_one();
+    for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kDepth;
+      const uint32_t ph = (uint32_t)(c / C::kDepth) & 1u;
+      const uint32_t key = tc::smem_u32(smem + sl * C::kKeyBytes);
+      const uint64_t k_op = tc::sw128_desc(key), kl_op = tc::sw128_desc(key + 16384);
+      const uint64_t kt_op = tc::sw128_desc_mn(key, 8192), klt_op = tc::sw128_desc_mn(key + 16384, 8192);
+      const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecBytes));
+      ok = ok && warp_wait(&bars.key[sl], ph);
+      if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
+      chain_await<true>(kBarS);
+      if (leader && ok) {  // X^T = S^T K^T
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_ts(tmem + kTmX, tmem + (b ? kTmSlo : kTmS) + 8 * j, k_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64,
+                   b + j > 0);
+        if constexpr (F16) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_ts(tmem + kTmX, tmem + kTmS + 8 * j, kl_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64, true);
+        }
+        tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      issued = c + 1;
+      ok = ok && warp_wait(&bars.rec[sl], ph);
+      // behind D, the chain overwrites what P D of the last chunk reads
+      if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);
+      chain_await<true>(kBarY);
+      if (leader && ok) {  // D^T = Y^T T^T: hi hi, lo hi, hi lo
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_ts(tmem + kTmX, tmem + (b == 1 ? kTmYlo : kTmY) + 8 * j, t_op + (((b == 2 ? kRecTlo : 0) + j * 32) >> 4),
+                   kId64, b + j > 0);
+        tc::mma_commit(&bars.d_full);
+      }
+      __syncwarp();
+      chain_await<true>(kBarDs);
+      if (leader && ok) {  // dS^T = D'^T K
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_ts(tmem + kTmU, tmem + (b ? kTmYlo : kTmY) + 8 * j, kt_op + ((j * 2048) >> 4), kIdU, b + j > 0);
+        if constexpr (F16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_ts(tmem + kTmU, tmem + kTmY + 8 * j, klt_op + ((j * 2048) >> 4), kIdU, true);
+        }
+        tc::mma_commit(&bars.key_free[sl]);
+      }
+      __syncwarp();
+      // behind dS, the chain overwrites what Q S reads
+      ok = ok && warp_wait(&bars.xq_full, (uint32_t)c & 1u);
+      if (leader && ok) tc::mma_commit(&bars.u_full);
+      __syncwarp();
     }
-    for (int c = issued > C::kRecs ? issued - C::kRecs : 0; c < issued; ++c)
-      warp_wait(&bars.rec[c % C::kRecs], (uint32_t)(c / C::kRecs) & 1u);
+  } else if (warp == kSideWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ----------------------------------------- products for the output alone
+    // As the chain warps, it goes on without waiting once out of time.
+    constexpr uint32_t kId64 = tc::idesc_bf16_f32(128, 64);
+    const bool leader = elect_one();
+    for (int c = 0; c < nch; ++c) {
+      const int sl = c % C::kDepth;
+      const uint32_t rec = tc::smem_u32(smem + C::kRec + sl * kRecBytes);
+      const uint64_t q_op = tc::sw128_desc(rec + kRecQ), p_op = tc::sw128_desc(rec + kRecP);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u);
+      if (c > 0) ok = ok && warp_wait(&bars.o_read, (uint32_t)(c - 1) & 1u);
+      chain_await<true>(kBarSq);
+      if (leader && ok) {  // O^T = S^T Q^T
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          mma_ts(tmem + kTmO, tmem + kTmS + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64, j > 0);
+        tc::mma_commit(&bars.xq_full);
+      }
+      __syncwarp();
+      chain_await<true>(kBarD);  // the chain is also past T and this chunk's scalars
+      if (leader && ok) {  // + D^T P^T
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_ts(tmem + kTmO, tmem + (b ? kTmDlo : kTmD) + 8 * j, p_op + ((j * 32) >> 4), kId64, true);
+        tc::mma_commit(&bars.o_full);
+        tc::mma_commit(&bars.rec_free[sl]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == kKeyWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    ok = load_keys<F16>(args, maps, smem, bars, s, lane);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    ok = load_records<F16>(args, smem, bars, s);
   }
-  if (!ok) bars.timed_out = 1;
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::tc_fence_after();
-  if (tid == 0 && bars.timed_out) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-  if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
+  end_unit(args, bars, tmem, ok);
 }
 
 // Tensor map of a [T][heads][128] 16-bit tensor, box (64 elements, 1 head, 64
@@ -1249,19 +1521,24 @@ kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t
   return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg<F16>::kSmem, F16, st, a, m);
 }
 
-template <int DVS, bool F16>
-kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
-  using C = Cfg<DVS, F16>;
-  static std::atomic<uint64_t> ready{0};
-  static_assert(C::kSmem <= 232448 && C::kThreads == 768, "shared memory and registers of one CTA");
-  kda_status s = allow_smem(gdn_state_kernel<DVS, F16>, C::kSmem, &ready);
+template <bool F16>
+kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, bool wide, cudaStream_t st) {
+  using C = Cfg<F16>;
+  static std::atomic<uint64_t> ready{0}, wide_ready{0};
+  static_assert(C::kSmem <= 232448 && kStateThreads == 768, "shared memory and registers of one CTA");
+  kda_status s = wide ? allow_smem(gdn_state_wide_kernel<F16>, C::kWideSmem, &wide_ready)
+                      : allow_smem(gdn_state_kernel<F16>, C::kSmem, &ready);
   if (s != KDA_OK) return s;
-  const int64_t grid = (int64_t)a.num_seqs * a.HV * (kHeadDim / DVS);
+  const int64_t grid = (int64_t)a.num_seqs * a.HV * (wide ? 1 : kHeadDim / kDv);
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return launch_after(gdn_state_kernel<DVS, F16>, (unsigned)grid, C::kThreads, C::kSmem, true, st, a, m);
+  return wide ? launch_after(gdn_state_wide_kernel<F16>, (unsigned)grid, kStateThreads, C::kWideSmem, true, st, a, m)
+              : launch_after(gdn_state_kernel<F16>, (unsigned)grid, kStateThreads, C::kSmem, true, st, a, m);
 }
 
 constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred cycles for 8, two thousand for 128
+
+// (sequence, head) pairs per SM from which the wide state kernel is taken.
+constexpr int kWideWaves = 2;
 
 int64_t most_chunks(int num_seqs, int64_t total_tokens) { return total_tokens / kC + num_seqs; }
 
@@ -1277,7 +1554,7 @@ using namespace kda;
 extern "C" size_t kda_gdn_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens) {
   if (num_seqs < 0 || total_tokens < 0 || dims.H <= 0 || dims.HV <= 0) return 0;
   if (total_tokens > INT32_MAX) return SIZE_MAX;  // refused; no capacity check may pass
-  return 3 * split_bytes(dims, total_tokens) + (size_t)most_chunks(num_seqs, total_tokens) * dims.HV * kRecStride;
+  return 3 * split_bytes(dims, total_tokens) + (size_t)most_chunks(num_seqs, total_tokens) * dims.HV * kRecBytes;
 }
 
 extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
@@ -1346,9 +1623,11 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   record_stage(1, st);
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
+  const int64_t heads = (int64_t)num_seqs * dims.HV;
+  const bool wide = heads >= kWideWaves * sms;
   // CTAs that do not all start at once: the longest sequences first
-  args.longest_first = num_seqs > 1 && num_seqs <= kMaxSorted && (int64_t)num_seqs * dims.HV * 4 > sms;
-  s = f16 ? launch_state<32, true>(args, m, st) : launch_state<32, false>(args, m, st);
+  args.longest_first = num_seqs > 1 && num_seqs <= kMaxSorted && heads * (wide ? 1 : 4) > sms;
+  s = f16 ? launch_state<true>(args, m, wide, st) : launch_state<false>(args, m, wide, st);
   record_stage(2, st);
   return s;
 }
