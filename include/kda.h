@@ -342,7 +342,7 @@ typedef struct {
  * intermediate and intermediate_chunks as kda_prefill's: the state at the
  * start of every 64-token chunk.  workspace: kda_gdn_prefill_workspace_size
  * bytes, 16-byte aligned:
- *   (total_tokens / 64 + num_seqs) * HV * 41984      a record per (chunk, head)
+ *   (total_tokens / 64 + num_seqs) * HV * 33792      a record per (chunk, head)
  *   + 3 * align256(total_tokens * H * 256)           FP16 only: q, k as BF16
  * (SIZE_MAX for more than INT32_MAX tokens).  The first call on each device
  * sets the kernels' shared-memory limits; make it before capturing calls into

@@ -16,16 +16,15 @@
 //
 // Two kernels.  Everything of a chunk that does not depend on the state is ready
 // for all chunks at once:
-//   gdn_chunk_kernel, a CTA of 128 threads per (chunk, value head), 3 per SM:
+//   gdn_chunk_kernel, a CTA of 128 threads per (chunk, value head), 4 per SM:
 //     norms, decays, [K; Q] K^T on the tensor cores, A and P, T by blocks, and
-//     one record of 41 KB (T, P, Q scaled by scale rq e^c, the chunk's row
-//     factors) for the second kernel.
+//     one record of 33 KB (T, P, the chunk's row factors) for the second kernel.
 // What is left is a chain of three dependent products a chunk.  Its latency, not
 // bytes or flops, bounds a long sequence, so nothing else is on it.  16 chain
 // warps hold the state in FP32 registers for the whole sequence and turn each
 // product's TMEM accumulator into the next one's operand; one warp issues the
 // products from behind hardware barriers, one Q S and P D, which only the output
-// needs and 4 warps of their own store; two load the chunks' keys and records.
+// needs and 4 warps of their own join; two load the chunks' rows and records.
 // Two forms of that kernel:
 //   gdn_state_kernel, a CTA per (sequence, value head, 32 value columns):
 //       X  = K S           64 x 32 x 128
@@ -46,11 +45,12 @@
 // The first takes a chunk in less time, the second does four times as much in it:
 // it is taken once its CTAs fill the SMs (kda_gdn_prefill has both sides).
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
-// wherever the state depends on them: S, T, Y and D'.  K and Q are BF16 already.
+// wherever the state depends on them, S, T, Y and D'.  K and Q are BF16 already.
 // FP16 keys are split exactly (11 bits into 8 + 8) and FP16 queries rounded to
 // BF16 by a pass over them before the kernels; FP16 operands would need S and D
-// in FP16 halves, whose range is not the state's.  P, the scaled Q and the S that meets it are
-// rounded to BF16 once (2^-9): they only enter the output, itself of 16 bits.
+// in FP16 halves, whose range is not the state's.  So are P and D for the
+// output: Q S and P D cancel where the state repeats what it is written, so that
+// one rounding of P to BF16 showed up as 2 per cent of the outputs' RMS.
 #include <atomic>
 
 #include "kda_host.h"
@@ -87,37 +87,40 @@ struct GdnMaps {
   CUtensorMap q, k, k_lo;
 };
 
-// What the state kernel reads of a chunk beside T, P and Q.
+// What the state kernels read of a chunk beside T and P.
 struct ChunkScalars {
   float a[kC];  // -r_i e^(c_i)
   float s[kC];  // r_j e^(c_last - c_j), 0 past the sequence's end
+  float o[kC];  // scale rq_i e^(c_i)
   float last;   // e^(c_last)
   float done;   // 1: the record is complete
   float pad[2];
 };
-// A chunk's record: T hi, P, T lo (tiles of 64 128-byte swizzled lines), scalars,
-// scaled Q (two halves of 64 channels, 64 lines each).
-constexpr int kRecT = 0, kRecP = 8192, kRecTlo = 16384, kRecScalars = 24576, kRecQ = 25600, kRecBytes = 41984;
-static_assert(kRecScalars + sizeof(ChunkScalars) <= kRecQ, "record");
+// A chunk's record: T hi, T lo, P hi, P lo (tiles of 64 128-byte swizzled lines),
+// scalars.
+constexpr int kRecT = 0, kRecTlo = 8192, kRecP = 16384, kRecPlo = 24576, kRecScalars = 32768, kRecBytes = 33792;
+static_assert(kRecScalars + sizeof(ChunkScalars) <= kRecBytes, "record");
 
 // Shared memory of the chunk kernel: [K; Q] as two halves of 64 channels and
-// 128 lines each, the low halves of FP16 keys, and the record but for Q, which is
-// scaled where it lies.  A's hi and lo halves take the place of K once its
+// 128 lines each, the low halves of FP16 keys, T and the scalars; P goes
+// straight to the record.  A's hi and lo halves take the place of K once its
 // products are done.
 template <bool F16>
 struct ChunkCfg {
   static constexpr int kRowBytes = 32768 + (F16 ? 16384 : 0);
-  static constexpr int kRec = kRowBytes;
-  // A's diagonal blocks in FP32: over the keys' low halves where there are any
-  static constexpr int kDiag = F16 ? 32768 : kRec + kRecQ;
-  static constexpr int kGate = kRec + kRecQ + (F16 ? 0 : 4 * 16 * kLdG * 4);  // float hi[64], lo[64], beta[64], rk[64]
+  static constexpr int kT = kRowBytes;         // T hi, T lo
+  static constexpr int kScalars = kT + 16384;  // 1024 bytes
+  static constexpr int kGate = kScalars + 1024;  // float hi[64], lo[64], beta[64], rk[64]
   static constexpr int kBar = kGate + 4 * kC * 4;
-  static constexpr int kSmem = kBar + 64;
+  // A's diagonal blocks in FP32: over the keys' low halves where there are any
+  static constexpr int kDiag = F16 ? 32768 : kBar + 64;
+  static constexpr int kSmem = kBar + 64 + (F16 ? 0 : 4 * 16 * kLdG * 4);
   static constexpr int kTmCols = F16 ? 128 : 64;
+  static constexpr int kCtas = F16 ? 3 : 4;  // per SM
 };
 
 struct Bars {
-  uint64_t key[3], key_free[3];  // key stages: landed (rows past the end zeroed: tail), consumed
+  uint64_t key[3], key_free[3];  // rows of K and Q: landed (keys past the end zeroed: tail), consumed
   uint64_t tail;
   uint64_t rec[3], rec_free[3];  // records
   uint64_t x_full, xq_full, d_full, u_full;
@@ -134,10 +137,11 @@ constexpr int kMmaWarp = kChainWarps + kOutWarps, kSideWarp = kMmaWarp + 1, kKey
 
 template <bool F16>
 struct Cfg {
-  static constexpr int kKeyBytes = 16384 * (F16 ? 2 : 1);  // K, low halves of FP16 keys
-  static constexpr int kDepth = F16 ? 2 : 3;               // chunks in shared memory
-  static constexpr int kRec = kDepth * kKeyBytes;
-  static constexpr int kBars = kRec + kDepth * kRecBytes;
+  static constexpr int kQ = 16384 * (F16 ? 2 : 1);  // K, low halves of FP16 keys, Q
+  static constexpr int kKeyBytes = kQ + 16384;
+  static constexpr int kKeys = F16 ? 2 : 3, kRecs = 2;     // chunks in shared memory: rows, records
+  static constexpr int kRec = kKeys * kKeyBytes;
+  static constexpr int kBars = kRec + kRecs * kRecBytes;
   // gdn_state_kernel's operands
   static constexpr int kS = (kBars + (int)sizeof(Bars) + 1023) / 1024 * 1024;
   static constexpr int kY = kS + 16384;
@@ -146,10 +150,11 @@ struct Cfg {
 };
 
 // TMEM columns of the wide kernel.  Left operands (two BF16 a column): S, Y and
-// after it D', D; accumulators: X and after it D, dS, O.  The other kernel has
-// accumulators alone, in the same columns.
-constexpr int kTmS = 0, kTmSlo = 64, kTmY = 128, kTmYlo = 160, kTmD = 192, kTmDlo = 224;
-constexpr int kTmX = 256, kTmU = 320, kTmO = 448, kTmCols = 512;
+// after it D'.  Accumulators: X and after it D, dS, Q S, P D; a warp's quarter of
+// D makes room for its D as an operand, 8 columns hi and 8 lo.  The other kernel
+// has accumulators alone, in the same columns.
+constexpr int kTmS = 0, kTmSlo = 64, kTmY = 128, kTmYlo = 160, kTmX = 192, kTmU = 256, kTmQ = 384, kTmO = 448,
+              kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -504,7 +509,7 @@ __device__ __forceinline__ void zero_rows(uint8_t* k, int half, int len, int t, 
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(128, 3)
+__global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     gdn_chunk_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
   using C = ChunkCfg<F16>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -554,7 +559,9 @@ __global__ void __launch_bounds__(128, 3)
   const int left = seq_len(args, n) - c * kC, len = left < kC ? left : kC;
 
   uint8_t* kq = smem;
-  uint8_t* rec = smem + C::kRec;
+  uint8_t* t_hi = smem + C::kT;
+  uint8_t* t_lo = t_hi + 8192;
+  uint8_t* rec = args.records + ((int64_t)id * args.HV + h) * kRecBytes;
   uint8_t* a_hi = smem;  // over the first half of K, and over the second
   uint8_t* a_lo = smem + 16384;
   float* diag = reinterpret_cast<float*>(smem + C::kDiag);
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(128, 3)
   float* c_lo = c_hi + kC;
   float* beta_s = c_lo + kC;
   float* rks = beta_s + kC;
-  ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(rec + kRecScalars);
+  ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(smem + C::kScalars);
   const ScalarGateArgs& ga = args.gate;
   if (t == 0) {
     tc::mbar_init(&bars[0], 1);
@@ -607,10 +614,8 @@ __global__ void __launch_bounds__(128, 3)
     beta_s[2 * lane] = be[0];
     beta_s[2 * lane + 1] = be[1];
   }
-  for (int x = t; x < 8192 / 16; x += 128) {  // blocks of T above the diagonal are not written below
-    reinterpret_cast<uint4*>(rec + kRecT)[x] = make_uint4(0, 0, 0, 0);
-    reinterpret_cast<uint4*>(rec + kRecTlo)[x] = make_uint4(0, 0, 0, 0);
-  }
+  for (int x = t; x < 16384 / 16; x += 128)  // blocks of T above the diagonal are not written below
+    reinterpret_cast<uint4*>(t_hi)[x] = make_uint4(0, 0, 0, 0);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -651,9 +656,9 @@ __global__ void __launch_bounds__(128, 3)
   float2 ss[4];  // four running sums, for latency
 #pragma unroll
   for (int e = 0; e < 4; ++e) ss[e] = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
   for (int a = 0; a < 2; ++a)
-#pragma unroll
+#pragma unroll 4
     for (int p = 0; p < 8; ++p) {
       const uint4 w = *line16(kq + a * 16384, row, p);
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(128, 3)
   const float ui = wide ? r : r * expf(mid);
   const float si = krow && i < len ? r * __expf((c_hi[63] - ci_hi) + (c_lo[63] - ci_lo)) : 0.f;
   const int top = 32 * (quad & 1) + 31;  // last row of this warp
-#pragma unroll
+#pragma unroll 1
   for (int jb = 0; jb < 4; ++jb) {
     float d[16];
     if (16 * jb <= top) {
@@ -733,26 +738,14 @@ __global__ void __launch_bounds__(128, 3)
               make_float4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
       }
     } else {
-      *line16(rec + kRecP, i, 2 * jb) = round8(d);
-      *line16(rec + kRecP, i, 2 * jb + 1) = round8(d + 8);
-    }
-  }
-  if (!krow) {  // Q scaled in place: [K; Q] K^T is done with it
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        uint4* at = line16(kq + a * 16384, 64 + i, p);
-        const uint4 w = *at;
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[2 * e] = r * ei * __uint_as_float(ww[e] << 16);
-          f[2 * e + 1] = r * ei * __uint_as_float(ww[e] & 0xffff0000u);
-        }
-        *at = round8(f);
+      for (int p = 0; p < 2; ++p) {
+        uint4 hi, lo;
+        split8(d + 8 * p, hi, lo);
+        *line16(rec + kRecP, i, 2 * jb + p) = hi;  // global memory
+        *line16(rec + kRecPlo, i, 2 * jb + p) = lo;
       }
+    }
   }
   tc::tc_fence_before();
   bad = __syncthreads_or(bad);
@@ -760,7 +753,7 @@ __global__ void __launch_bounds__(128, 3)
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, C::kTmCols);
   }
-  invert64(rec + kRecT, rec + kRecTlo, a_hi, a_lo, diag, beta_s, quad, lane);
+  invert64(t_hi, t_lo, a_hi, a_lo, diag, beta_s, quad, lane);
   if (krow) {
     sc.a[i] = -r * ei;
     sc.s[i] = si;
@@ -768,15 +761,15 @@ __global__ void __launch_bounds__(128, 3)
       sc.last = ei;
       sc.done = bad ? 0.f : 1.f;
     }
+  } else {
+    sc.o[i] = r * ei;
   }
   tc::fence_async_smem();
   __syncthreads();
   if (t == 0) {
     if (bad) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-    uint8_t* dst = args.records + ((int64_t)id * args.HV + h) * kRecBytes;
-    tc::bulk_s2g(dst, rec, kRecQ);
-    tc::bulk_s2g(dst + kRecQ, kq + 8192, 8192);
-    tc::bulk_s2g(dst + kRecQ + 8192, kq + 24576, 8192);
+    tc::bulk_s2g(rec + kRecT, t_hi, 16384);
+    tc::bulk_s2g(rec + kRecScalars, &sc, 1024);
     tc::bulk_commit();
     tc::bulk_wait_read();
   }
@@ -854,9 +847,9 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
     bars.timed_out = 0;
     for (int i = 0; i < 3; ++i) {
       tc::mbar_init(&bars.key[i], 1);
-      tc::mbar_init(&bars.key_free[i], 1);
+      tc::mbar_init(&bars.key_free[i], 2);
       tc::mbar_init(&bars.rec[i], 1);
-      tc::mbar_init(&bars.rec_free[i], 1);
+      tc::mbar_init(&bars.rec_free[i], 1 + kOutWarps);
     }
     tc::mbar_init(&bars.tail, 1);
     tc::mbar_init(&bars.x_full, 1);
@@ -883,7 +876,7 @@ __device__ __forceinline__ void end_unit(const GdnPrefillArgs& args, Bars& bars,
   if (threadIdx.x >> 5 == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
 }
 
-// The key warp: every chunk's keys, as two halves of 64 channels.
+// The row warp: every chunk's keys and queries, as two halves of 64 channels each.
 template <bool F16>
 __device__ __forceinline__ bool load_keys(const GdnPrefillArgs& args, const GdnMaps& maps, uint8_t* smem, Bars& bars,
                                           const Unit& s, int lane) {
@@ -893,21 +886,22 @@ __device__ __forceinline__ bool load_keys(const GdnPrefillArgs& args, const GdnM
   if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
   int issued = 0;
   for (int c = 0; c < s.nch; ++c) {
-    const int sl = c % C::kDepth;
-    if (c >= C::kDepth && !(ok = warp_wait(&bars.key_free[sl], (uint32_t)(c / C::kDepth - 1) & 1u))) break;
+    const int sl = c % C::kKeys;
+    if (c >= C::kKeys && !(ok = warp_wait(&bars.key_free[sl], (uint32_t)(c / C::kKeys - 1) & 1u))) break;
     uint8_t* key = smem + sl * C::kKeyBytes;
     if (leader) {
       tc::mbar_expect_tx(&bars.key[sl], C::kKeyBytes);
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         tma_box(key + a * 8192, &maps.k, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
+        tma_box(key + C::kQ + a * 8192, &maps.q, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
         if (F16) tma_box(key + 16384 + a * 8192, &maps.k_lo, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
       }
     }
     __syncwarp();
     issued = c + 1;
     if (c == s.nch - 1 && s.L % kC != 0) {
-      if (!(ok = warp_wait(&bars.key[sl], (uint32_t)(c / C::kDepth) & 1u))) break;
+      if (!(ok = warp_wait(&bars.key[sl], (uint32_t)(c / C::kKeys) & 1u))) break;
       zero_rows(key, 8192, s.L % kC, lane, 32);
       if (F16) zero_rows(key + 16384, 8192, s.L % kC, lane, 32);
       tc::fence_async_smem();
@@ -916,8 +910,8 @@ __device__ __forceinline__ bool load_keys(const GdnPrefillArgs& args, const GdnM
     }
   }
   // nothing may land after the CTA is gone
-  for (int c = issued > C::kDepth ? issued - C::kDepth : 0; c < issued; ++c)
-    warp_wait(&bars.key[c % C::kDepth], (uint32_t)(c / C::kDepth) & 1u);
+  for (int c = issued > C::kKeys ? issued - C::kKeys : 0; c < issued; ++c)
+    warp_wait(&bars.key[c % C::kKeys], (uint32_t)(c / C::kKeys) & 1u);
   return ok;
 }
 
@@ -931,8 +925,8 @@ __device__ __forceinline__ bool load_records(const GdnPrefillArgs& args, uint8_t
   const uint8_t* src = args.records + (bars.chunk0 * args.HV + s.h) * kRecBytes;
   int issued = 0;
   for (int c = 0; c < s.nch; ++c) {
-    const int sl = c % C::kDepth;
-    if (c >= C::kDepth && !(ok = warp_wait(&bars.rec_free[sl], (uint32_t)(c / C::kDepth - 1) & 1u))) break;
+    const int sl = c % C::kRecs;
+    if (c >= C::kRecs && !(ok = warp_wait(&bars.rec_free[sl], (uint32_t)(c / C::kRecs - 1) & 1u))) break;
     if (leader) {
       tc::mbar_expect_tx(&bars.rec[sl], kRecBytes);
       tc::bulk_g2s(smem + C::kRec + sl * kRecBytes, src + (int64_t)c * args.HV * kRecBytes, kRecBytes, &bars.rec[sl]);
@@ -940,8 +934,8 @@ __device__ __forceinline__ bool load_records(const GdnPrefillArgs& args, uint8_t
     __syncwarp();
     issued = c + 1;
   }
-  for (int c = issued > C::kDepth ? issued - C::kDepth : 0; c < issued; ++c)
-    warp_wait(&bars.rec[c % C::kDepth], (uint32_t)(c / C::kDepth) & 1u);
+  for (int c = issued > C::kRecs ? issued - C::kRecs : 0; c < issued; ++c)
+    warp_wait(&bars.rec[c % C::kRecs], (uint32_t)(c / C::kRecs) & 1u);
   return ok;
 }
 
@@ -988,7 +982,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     };
     load_v(0);
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kDepth;
+      const int sl = c % C::kRecs;
       const uint32_t cp = (uint32_t)c & 1u;
       put_split(smem + C::kS, dk, part, S);
       chain_arrive<false>(kBarS);
@@ -1003,7 +997,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
       }
       const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecBytes + kRecScalars);
-      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u, ok);
+      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u, ok);
       const float last = sc.last;
       const float fa[2] = {sc.a[row], sc.a[row + 8]}, fs[2] = {sc.s[row], sc.s[row + 8]};
       ok = ok && sc.done == 1.f;
@@ -1049,22 +1043,32 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       for (int j = 0; j < 8; ++j) root[j * kHeadDim] = S[j];
   } else if (warp < kMmaWarp) {
     // --------------------------------------------------------------- outputs
-    // 16 token rows a warp.
+    // O = scale rq e^c Q S + P D, 16 token rows a warp.
     const int quad = warp & 3;
     const int row = 16 * quad + (lane >> 2);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + s.slice * kDv + 2 * (lane & 3);
     const int64_t step = (int64_t)args.HV * kHeadDim;
     for (int c = 0; c < nch; ++c, dst += kC * step) {
+      const int sl = c % C::kRecs;
+      const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecBytes + kRecScalars);
+      if (!(ok = warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u))) break;
+      const float fo[2] = {sc.o[row], sc.o[row + 8]};
+      __syncwarp();
+      if (lane == 0) arrive(&bars.rec_free[sl]);
       if (!(ok = warp_wait(&bars.o_full, (uint32_t)c & 1u))) break;
       tc::tc_fence_after();
       uint32_t w[4][2];
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float2 x[2];
-        get_rows(lanes + kTmO, part, x);
+        float2 x[2], u[2];
+        get_rows(lanes + kTmQ, part, x);
+        get_rows(lanes + kTmO, part, u);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) w[part][e] = pack_out16x2<F16>(x[e].x, x[e].y);
+        for (int e = 0; e < 2; ++e) {
+          const float2 y = fma2(make_float2(fo[e], fo[e]), x[e], u[e]);
+          w[part][e] = pack_out16x2<F16>(y.x, y.y);
+        }
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -1086,13 +1090,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     const uint64_t y_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kY), 0);
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kDepth;
-      const uint32_t ph = (uint32_t)(c / C::kDepth) & 1u;
-      const uint32_t key = tc::smem_u32(smem + sl * C::kKeyBytes);
+      const int ks = c % C::kKeys, sl = c % C::kRecs;
+      const uint32_t key = tc::smem_u32(smem + ks * C::kKeyBytes);
       const uint64_t k_op = tc::sw128_desc(key), kl_op = tc::sw128_desc(key + 16384);
       const uint64_t kt_op = tc::sw128_desc_mn(key, 8192), klt_op = tc::sw128_desc_mn(key + 16384, 8192);
       const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecBytes));
-      ok = ok && warp_wait(&bars.key[sl], ph);
+      ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
       chain_await<false>(kBarS);
       if (leader && ok) {  // X = K S
@@ -1105,7 +1108,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      ok = ok && warp_wait(&bars.rec[sl], ph);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       // behind D, the chain overwrites what P D of the last chunk reads
       if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);
       chain_await<false>(kBarY);
@@ -1125,7 +1128,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             tc::mma_bf16(tmem + kTmU, (b ? klt_op : kt_op) + ((j * 2048) >> 4), y_op + ((j * 2048) >> 4), kIdU, b + j > 0);
-        tc::mma_commit(&bars.key_free[sl]);
+        tc::mma_commit(&bars.key_free[ks]);
       }
       __syncwarp();
       // behind dS, the chain overwrites what Q S reads
@@ -1141,24 +1144,29 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kDepth;
+      const int ks = c % C::kKeys, sl = c % C::kRecs;
       const uint32_t rec = tc::smem_u32(smem + C::kRec + sl * kRecBytes);
-      const uint64_t q_op = tc::sw128_desc(rec + kRecQ), p_op = tc::sw128_desc(rec + kRecP);
-      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u);
+      const uint64_t q_op = tc::sw128_desc(tc::smem_u32(smem + ks * C::kKeyBytes + C::kQ)), p_op = tc::sw128_desc(rec + kRecP);
+      ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       if (c > 0) ok = ok && warp_wait(&bars.o_read, (uint32_t)(c - 1) & 1u);
       chain_await<false>(kBarSq);
-      if (leader && ok) {  // O = Q S
+      if (leader && ok) {  // Q S
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          tc::mma_bf16(tmem + kTmO, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kId64, j > 0);
+          tc::mma_bf16(tmem + kTmQ, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kId64, j > 0);
         tc::mma_commit(&bars.xq_full);
+        tc::mma_commit(&bars.key_free[ks]);
       }
       __syncwarp();
       chain_await<false>(kBarD);  // the chain is also past T and this chunk's scalars
-      if (leader && ok) {  // + P D
+      if (leader && ok) {  // P D
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          tc::mma_bf16(tmem + kTmO, p_op + ((j * 32) >> 4), d_op + ((j * 2048) >> 4), kId64, true);
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc::mma_bf16(tmem + kTmO, p_op + (((b ? kRecPlo - kRecP : 0) + j * 32) >> 4), d_op + ((j * 2048) >> 4), kId64,
+                         b + j > 0);
         tc::mma_commit(&bars.o_full);
         tc::mma_commit(&bars.rec_free[sl]);
       }
@@ -1189,7 +1197,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   const uint32_t tmem = bars.tmem;
   bool ok = true;
   if (warp < kChainWarps) {
-    // 64 registers for the others leave the chain 88 of the 80 all start with
+    // 768 threads start with 80 registers each; 640 at 88 and 128 at 40 are those 61440
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // ---------------------------------------------------------------- chain
     // A warp that runs out of time goes on without waiting, so that the others
@@ -1218,7 +1226,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     };
     load_v(0);
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kDepth;
+      const int sl = c % C::kRecs;
       const uint32_t cp = (uint32_t)c & 1u;
       put_split16(lanes + kTmS + 16 * part, lanes + kTmSlo + 16 * part, S);
       put_split16(lanes + kTmS + 16 * part + 8, lanes + kTmSlo + 16 * part + 8, S + 16);
@@ -1237,7 +1245,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v2[j] = __byte_perm(vraw[j], __shfl_xor_sync(0xffffffffu, vraw[j], 1), pick);
       const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecBytes + kRecScalars);
-      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u, ok);
+      chain_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u, ok);
       const float last = sc.last;
       ok = ok && sc.done == 1.f;
       chain_wait(&bars.x_full, cp, ok);
@@ -1282,7 +1290,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, y);
       }
       chain_arrive<true>(kBarDs);
-      put_split16(lanes + kTmD + 8 * part, lanes + kTmDlo + 8 * part, x);
+      put_split16(lanes + kTmX + tok0, lanes + kTmX + tok0 + 8, x);  // over this warp's quarter of D
       chain_arrive<true>(kBarD);
       chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
@@ -1304,30 +1312,42 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
       for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(root + 4 * j) = *reinterpret_cast<const float4*>(S + 4 * j);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // --------------------------------------------------------------- outputs
-    // 32 value columns a warp, 64 tokens a thread.
+    // O = scale rq e^c Q S + P D, 32 value columns a warp, 64 tokens a thread.
     const int quad = warp & 3, odd = lane & 1;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t pick = odd ? 0x3276u : 0x5410u;
     const int64_t step = (int64_t)args.HV * kHeadDim;
     kda_bf16* dst = args.o + ((t0 + odd) * args.HV + h) * kHeadDim + ((32 * quad + lane) & ~1);
     for (int c = 0; c < nch; ++c, dst += kC * step) {
+      const int sl = c % C::kRecs;
+      const ChunkScalars& sc = *reinterpret_cast<const ChunkScalars*>(smem + C::kRec + sl * kRecBytes + kRecScalars);
+      if (!(ok = warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u))) break;
       if (!(ok = warp_wait(&bars.o_full, (uint32_t)c & 1u))) break;
       tc::tc_fence_after();
       uint32_t w[32];  // two tokens of one column each
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t r[16];
-        tc::tmem_ld16_async(lanes + kTmO + 16 * g, r);
+      for (int g = 0; g < 8; ++g) {
+        uint32_t q[8], r[8];
+        tmem_ld8_async(lanes + kTmQ + 8 * g, q);
+        tmem_ld8_async(lanes + kTmO + 8 * g, r);
+        wait_ld(q);
         wait_ld(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[8 * g + j] = pack_out16x2<F16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = fma2(*reinterpret_cast<const float2*>(sc.o + 8 * g + 2 * j),
+                                make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])),
+                                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+          w[4 * g + j] = pack_out16x2<F16>(y.x, y.y);
+        }
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(&bars.o_read);
+      if (lane == 0) {
+        arrive(&bars.rec_free[sl]);
+        arrive(&bars.o_read);
+      }
       const int left = L - c * kC - odd;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {  // traded for two columns of one token each
@@ -1336,21 +1356,21 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ----------------------------------------------------- the chain's products
     // As the chain warps, it goes on without waiting once out of time.
     constexpr uint32_t kId64 = tc::idesc_bf16_f32(128, 64);
     constexpr uint32_t kIdU = tc::idesc_bf16_f32(128, 128) | tc::kIdescMnB;
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kDepth;
-      const uint32_t ph = (uint32_t)(c / C::kDepth) & 1u;
-      const uint32_t key = tc::smem_u32(smem + sl * C::kKeyBytes);
+      const int ks = c % C::kKeys, sl = c % C::kRecs;
+      const uint32_t key = tc::smem_u32(smem + ks * C::kKeyBytes);
       const uint64_t k_op = tc::sw128_desc(key), kl_op = tc::sw128_desc(key + 16384);
       const uint64_t kt_op = tc::sw128_desc_mn(key, 8192), klt_op = tc::sw128_desc_mn(key + 16384, 8192);
       const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecBytes));
-      ok = ok && warp_wait(&bars.key[sl], ph);
+      ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
+      if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);  // X takes the place of the last D
       chain_await<true>(kBarS);
       if (leader && ok) {  // X^T = S^T K^T
 #pragma unroll
@@ -1367,9 +1387,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         tc::mma_commit(&bars.x_full);
       }
       __syncwarp();
-      ok = ok && warp_wait(&bars.rec[sl], ph);
-      // behind D, the chain overwrites what P D of the last chunk reads
-      if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       chain_await<true>(kBarY);
       if (leader && ok) {  // D^T = Y^T T^T: hi hi, lo hi, hi lo
 #pragma unroll
@@ -1393,7 +1411,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
           for (int j = 0; j < 4; ++j)
             mma_ts(tmem + kTmU, tmem + kTmY + 8 * j, klt_op + ((j * 2048) >> 4), kIdU, true);
         }
-        tc::mma_commit(&bars.key_free[sl]);
+        tc::mma_commit(&bars.key_free[ks]);
       }
       __syncwarp();
       // behind dS, the chain overwrites what Q S reads
@@ -1402,42 +1420,48 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       __syncwarp();
     }
   } else if (warp == kSideWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ----------------------------------------- products for the output alone
     // As the chain warps, it goes on without waiting once out of time.
     constexpr uint32_t kId64 = tc::idesc_bf16_f32(128, 64);
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
-      const int sl = c % C::kDepth;
+      const int ks = c % C::kKeys, sl = c % C::kRecs;
       const uint32_t rec = tc::smem_u32(smem + C::kRec + sl * kRecBytes);
-      const uint64_t q_op = tc::sw128_desc(rec + kRecQ), p_op = tc::sw128_desc(rec + kRecP);
-      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kDepth) & 1u);
+      const uint64_t q_op = tc::sw128_desc(tc::smem_u32(smem + ks * C::kKeyBytes + C::kQ)), p_op = tc::sw128_desc(rec + kRecP);
+      ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
+      ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       if (c > 0) ok = ok && warp_wait(&bars.o_read, (uint32_t)(c - 1) & 1u);
       chain_await<true>(kBarSq);
-      if (leader && ok) {  // O^T = S^T Q^T
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          mma_ts(tmem + kTmO, tmem + kTmS + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64, j > 0);
-        tc::mma_commit(&bars.xq_full);
-      }
-      __syncwarp();
-      chain_await<true>(kBarD);  // the chain is also past T and this chunk's scalars
-      if (leader && ok) {  // + D^T P^T
+      if (leader && ok) {  // S^T Q^T
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_ts(tmem + kTmQ, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64,
+                   b + j > 0);
+        tc::mma_commit(&bars.xq_full);
+        tc::mma_commit(&bars.key_free[ks]);
+      }
+      __syncwarp();
+      chain_await<true>(kBarD);  // the chain is also past T and this chunk's scalars
+      if (leader && ok) {  // D^T P^T
+#pragma unroll
+        for (int b = 0; b < 3; ++b)  // hi hi, lo hi, hi lo
+#pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kTmO, tmem + (b ? kTmDlo : kTmD) + 8 * j, p_op + ((j * 32) >> 4), kId64, true);
+            mma_ts(tmem + kTmO, tmem + kTmX + 16 * j + (b == 1 ? 8 : 0), p_op + (((b == 2 ? kRecPlo - kRecP : 0) + j * 32) >> 4),
+                   kId64, b + j > 0);
         tc::mma_commit(&bars.o_full);
         tc::mma_commit(&bars.rec_free[sl]);
       }
       __syncwarp();
     }
   } else if (warp == kKeyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     ok = load_keys<F16>(args, maps, smem, bars, s, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     ok = load_records<F16>(args, smem, bars, s);
   }
   end_unit(args, bars, tmem, ok);
@@ -1513,7 +1537,7 @@ kda_status launch_after(Kernel kernel, unsigned grid, unsigned threads, int smem
 template <bool F16>
 kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  static_assert(3 * (ChunkCfg<F16>::kSmem + 1024) <= 233472, "three CTAs per SM");
+  static_assert(ChunkCfg<F16>::kCtas * (ChunkCfg<F16>::kSmem + 1024) <= 233472, "CTAs per SM");
   kda_status s = allow_smem(gdn_chunk_kernel<F16>, ChunkCfg<F16>::kSmem, &ready);
   if (s != KDA_OK) return s;
   const int64_t grid = a.max_chunks * a.HV;
@@ -1537,8 +1561,12 @@ kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, bool wide, cu
 
 constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred cycles for 8, two thousand for 128
 
-// (sequence, head) pairs per SM from which the wide state kernel is taken.
-constexpr int kWideWaves = 2;
+// The wide state kernel is taken from 3 / 2 (sequence, head) pairs per SM on.
+// Both sides, 16 heads (whole call, us; the other form in brackets): 8 sequences
+// of 2048 tokens 342 [241], 8 ragged ones with one of 8087 of 16980 tokens 343
+// [524], 16 of 2048 439 [596], 64 of 512 403 [642].  The lengths are on the
+// device; below the border one long sequence costs more than it saves.
+bool take_wide(int64_t heads, int sms) { return 2 * heads >= 3 * (int64_t)sms; }
 
 int64_t most_chunks(int num_seqs, int64_t total_tokens) { return total_tokens / kC + num_seqs; }
 
@@ -1624,7 +1652,7 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
   const int64_t heads = (int64_t)num_seqs * dims.HV;
-  const bool wide = heads >= kWideWaves * sms;
+  const bool wide = take_wide(heads, sms);
   // CTAs that do not all start at once: the longest sequences first
   args.longest_first = num_seqs > 1 && num_seqs <= kMaxSorted && heads * (wide ? 1 : 4) > sms;
   s = f16 ? launch_state<true>(args, m, wide, st) : launch_state<false>(args, m, wide, st);

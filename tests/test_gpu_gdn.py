@@ -226,6 +226,29 @@ def test_prefill_fixed_layout_many_sequences_and_streams():
     assert torch.equal(o, o2) and torch.equal(pool, pool2)
 
 
+@pytest.mark.parametrize("f16", [False, True])
+def test_prefill_many_sequences(f16):
+    """Enough (sequence, head) pairs for the wide state kernel, with ragged,
+    empty and padding sequences, grouped heads and chunk-start states."""
+    rng = np.random.default_rng(0)
+    lengths = [int(x) for x in rng.integers(0, 150, 70)]
+    lengths[3], lengths[5], lengths[7] = 400, 64, 1
+    d = make(14, sum(lengths), 2, 4, 75, f16=f16, given=True, gb_rows=sum(lengths) + 3)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    inter = torch.full((sum(-(-L // 64) for L in lengths), 4, K, K), 9.0, device="cuda")
+    o, pool = prefill(d, lengths, err=err, intermediate=inter)
+    assert int(err) == 0
+    check_prefill(d, lengths, o, pool, intermediate=inter)
+    idx = d["idx"][:70].clone()
+    idx[4] = -1
+    o2, pool2 = prefill(d, lengths, idx=idx)
+    t0 = sum(lengths[:4])
+    keep = [t for t in range(sum(lengths)) if not t0 <= t < t0 + lengths[4]]
+    assert torch.equal(o2[keep], o[keep]) and bool((o2[t0:t0 + lengths[4]] == 0).all())
+    s = int(d["idx"][4])
+    assert torch.equal(pool2[s].cpu(), d["pool"][s])
+
+
 def test_prefill_and_decode_in_a_graph():
     d = make(10, 130, 2, 4, 3)
     x = {n: d[n].cuda() for n in ("q", "k", "v", "a", "b", "idx")}
