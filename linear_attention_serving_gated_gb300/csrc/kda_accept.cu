@@ -8,17 +8,19 @@
 // weights passes u times their whole.
 //
 // The answer is a whole number, so it must not depend on how sums are split.
-// Accept tests are exact: the product of two FP32 numbers fits FP64.  A
-// thread's sum of weights is an FP32 pair (sum, error) whose error part takes
-// what each addition and each difference p - q rounds off (two-sum; 48 bits),
-// and pairs are joined in FP64; FP64 for every element would be bound by its
-// rate, 1/64 of FP32's here.  The whole is the last of the running sums.
+// Accept tests are exact: the product of two FP32 numbers fits FP64.  Sums of
+// weights are FP32 pairs (sum, error) whose error part takes what each addition
+// and each difference p - q rounds off (two-sum; 48 bits), joined in FP64 once
+// per 256 weights: FP64 for every element, at 1/64 of FP32's rate here, would
+// bound the kernel.
 //
 // One cluster per request: every CTA repeats the walk (a few gathered loads,
-// whose latency is the same for one CTA as for all), sums a contiguous part
-// of the row and stores one FP64 sum per warp in the first CTA's shared
-// memory.  The first CTA's first warp finds the warp part that holds the
-// border and goes through that part again, 32 lanes at a time.
+// whose latency is the same for one CTA as for all), its warps sum blocks of 256
+// weights and store one FP64 sum per block in the first CTA's shared memory.  The
+// first CTA scans the block sums, and one warp goes through the block that holds
+// the border.  A row is read once, 32 bytes a lane and block; bound by latency
+// for a few requests and by HBM for many (48 rows of p and q of 131072 FP32: 50
+// MB).
 #include <cooperative_groups.h>
 
 #include "kda_host.h"
@@ -29,7 +31,8 @@ namespace kda {
 namespace {
 
 constexpr int kAccThreads = 256, kAccWarps = kAccThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kBlock = 256;      // weights per block sum, 8 a lane
+constexpr int kMaxBlocks = 1024;  // longer rows take larger blocks
 
 struct AcceptArgs {
   const void* target;
@@ -60,22 +63,78 @@ __device__ __forceinline__ float prob_at(const void* p, int64_t i) {
 // that fell (skip), or p alone.
 struct Row {
   const void* p;
-  const void* q;        // nullptr: no draft row
-  int64_t p0, q0;       // element offsets of the rows
-  const int* skip;      // tokens that fell
+  const void* q;     // nullptr: no draft row
+  int64_t p0, q0;    // element offsets of the rows
+  const int* skip;   // tokens that fell
   int n_skip;
 };
 
-template <int DT>
-__device__ __forceinline__ double weight_at(const Row& r, int j) {
-  const float p = prob_at<DT>(r.p, r.p0 + j);
-  if (r.q) {
-    const float q = prob_at<DT>(r.q, r.q0 + j);
-    return p > q ? (double)p - (double)q : 0.0;
+__device__ __forceinline__ float valid(float x) {  // NaN, negative and infinite entries count as zero
+  x = fmaxf(x, 0.f);
+  return x < __int_as_float(0x7f800000) ? x : 0.f;
+}
+
+// Eight entries of a row: j, j + step, ..; zeros past the end.  VEC: step is 1 and
+// j a multiple of 8 of a row that starts on 16 bytes.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void* base, int64_t row0, int j, int step, int V, float (&x)[8]) {
+  if (VEC && j + 8 <= V) {
+    if constexpr (DT == KDA_DTYPE_F32) {
+      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + row0 + j);
+      const float4 a = __ldg(s), b = __ldg(s + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + row0 + j));
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = in16_to_float<DT == KDA_DTYPE_F16>((uint16_t)(e & 1 ? ww[e / 2] >> 16 : ww[e / 2] & 0xffffu));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = j + e * step;
+      x[e] = 0.f;
+      if (k < V) {
+        if constexpr (DT == KDA_DTYPE_F32)
+          x[e] = __ldg(static_cast<const float*>(base) + row0 + k);
+        else
+          x[e] = in16_to_float<DT == KDA_DTYPE_F16>(__ldg(static_cast<const uint16_t*>(base) + row0 + k));
+      }
+    }
   }
-  for (int s = 0; s < r.n_skip; ++s)
-    if (r.skip[s] == j) return 0.0;
-  return p;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = valid(x[e]);
+}
+
+// Eight weights: w exactly p - q as w + err.
+template <int DT, bool VEC>
+__device__ __forceinline__ void weights8(const Row& row, int j, int step, int V, float (&w)[8], float (&err)[8]) {
+  load8<DT, VEC>(row.p, row.p0, j, step, V, w);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) err[e] = 0.f;
+  if (row.q) {
+    float q[8];
+    load8<DT, VEC>(row.q, row.q0, j, step, V, q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = w[e], d = p - q[e], b = p - d;  // b: q as subtracted
+      err[e] = d > 0.f ? (p - (d + b)) + (b - q[e]) : 0.f;
+      w[e] = fmaxf(d, 0.f);
+    }
+  } else {
+    for (int k = 0; k < row.n_skip; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (row.skip[k] == j + e * step) w[e] = 0.f;
+  }
+}
+
+// (s, c) += (x, y), s the rounded sum and c what it leaves.
+__device__ __forceinline__ void add_pair(float& s, float& c, float x, float y) {
+  const float t = s + x, z = t - s;
+  c += ((s - (t - z)) + (x - z)) + y;
+  s = t;
 }
 
 __device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
@@ -89,35 +148,42 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
 
 // The lowest j in [lo, hi) with weight whose running sum from `before` exceeds
 // `goal`; where rounding leaves none, the last j with weight; -1 where none has
-// any.  One warp: first 32 equal pieces, then the elements of one.
-template <int DT>
+// any.  One warp, lo a multiple of 8.
+template <int DT, bool VEC>
 __device__ int find_in(const Row& row, int lo, int hi, double before, double goal, int lane) {
-  const int piece = (hi - lo + 31) / 32;
-  int a = min(lo + lane * piece, hi), b = min(a + piece, hi);
-  double s = 0.0;
-  for (int j = a; j < b; ++j) s += weight_at<DT>(row, j);
-  const double cum = before + warp_scan(s, lane);
-  const unsigned some = __ballot_sync(0xffffffffu, s > 0.0);
-  const unsigned over = __ballot_sync(0xffffffffu, s > 0.0 && cum > goal);
-  if (!some) return -1;
-  const int L = over ? __ffs(over) - 1 : 31 - __clz(some);
-  double base = __shfl_sync(0xffffffffu, cum - s, L);
-  a = __shfl_sync(0xffffffffu, a, L);
-  b = __shfl_sync(0xffffffffu, b, L);
   int last = -1;
-  for (int j0 = a; j0 < b; j0 += 32) {
-    const double w = j0 + lane < b ? weight_at<DT>(row, j0 + lane) : 0.0;
-    const double c = base + warp_scan(w, lane);
-    const unsigned pos = __ballot_sync(0xffffffffu, w > 0.0);
-    const unsigned o = __ballot_sync(0xffffffffu, w > 0.0 && c > goal);
-    if (o) return j0 + __ffs(o) - 1;
-    if (pos) last = j0 + 31 - __clz(pos);
-    base = __shfl_sync(0xffffffffu, c, 31);
+  for (int j0 = lo; j0 < hi; j0 += kBlock) {
+    const int j = j0 + 8 * lane;
+    float w[8], err[8];
+    weights8<DT, VEC>(row, j, 1, hi, w, err);
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)w[e] + (double)err[e];
+    const double cum = before + warp_scan(sum, lane);
+    const unsigned some = __ballot_sync(0xffffffffu, sum > 0.0);
+    const unsigned over = __ballot_sync(0xffffffffu, sum > 0.0 && cum > goal);
+    if (some) {
+      const int L = over ? __ffs(over) - 1 : 31 - __clz(some);
+      double run = cum - sum;
+      int at = -1;
+      bool found = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        run += (double)w[e] + (double)err[e];
+        if (w[e] > 0.f && !found) {
+          at = j + e;
+          found = run > goal;
+        }
+      }
+      last = __shfl_sync(0xffffffffu, at, L);
+      if (over) return last;
+    }
+    before = __shfl_sync(0xffffffffu, cum, 31);
   }
   return last;
 }
 
-template <int DT, bool TREE>
+template <int DT, bool TREE, bool VEC>
 __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs args) {
   cg::cluster_group cluster = cg::this_cluster();
   auto started = cluster.barrier_arrive();
@@ -125,13 +191,14 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
   const int r = blockIdx.x / parts;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = args.T, V = args.vocab;
-  __shared__ float p_tok[KDA_ACCEPT_MAX_T];
-  __shared__ int tok_s[KDA_ACCEPT_MAX_T], par_s[TREE ? KDA_ACCEPT_MAX_T : 1], skip_s[KDA_ACCEPT_MAX_T];
-  __shared__ float u_s[TREE ? KDA_ACCEPT_MAX_T : 1];
-  __shared__ double sums[kMaxCluster * kAccWarps];
-  __shared__ int first_fall, cur_s, n_skip_s;
+  __shared__ float p_tok[TREE ? KDA_ACCEPT_MAX_T : 1], u_s[TREE ? KDA_ACCEPT_MAX_T : 1];
+  __shared__ int tok_s[TREE ? KDA_ACCEPT_MAX_T : 1], par_s[TREE ? KDA_ACCEPT_MAX_T : 1];
+  __shared__ int skip_s[TREE ? KDA_ACCEPT_MAX_T : 1];
+  __shared__ double sums[kMaxBlocks], warp_sum[kAccWarps], pick_before;
+  __shared__ int first_fall, cur_s, n_skip_s, pick;
 
   const int64_t r0 = (int64_t)r * T;
+  const float u_draw = args.uniforms[r0];
   int n = args.lengths ? args.lengths[r] : T;
   const bool report = rank == 0 && tid == 0;
   if (n < 0 || n > T) {
@@ -141,6 +208,7 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
   if (tid == 0) {
     first_fall = n;
     n_skip_s = 0;
+    pick = -1;
   }
   if constexpr (TREE) {
     bool bad = false;
@@ -157,13 +225,14 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
     __syncthreads();
   }
   // the drafted tokens' probabilities and, for a chain, their tests
-  for (int i = 1 + tid; i < n; i += kAccThreads) {
+  for (int i = 1 + tid; i < T; i += kAccThreads) {
     const int tok = args.tokens[r0 + i];
+    const float u = args.uniforms[r0 + i];
+    if (i >= n) continue;
     const bool in = tok >= 0 && tok < V;
     if (!in && rank == 0) set_error(args.err_flag, KDA_DEVERR_TOKEN);
     const int up = TREE ? par_s[i] : i - 1;
     const float p = in ? prob_at<DT>(args.target, (r0 + up) * args.target_stride + tok) : 0.f;
-    const float u = args.uniforms[r0 + i];
     if constexpr (TREE) {
       p_tok[i] = p;
       tok_s[i] = tok;
@@ -176,12 +245,10 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    int cur = first_fall - 1;
-    if constexpr (TREE) {
+  if constexpr (TREE) {
+    if (tid == 0) {
       // children follow their parents, so one pass over the nodes is the walk
-      cur = 0;
-      int n_skip = 0, depth = 0;
+      int cur = 0, n_skip = 0, depth = 0;
       double left = 1.0;
       if (report && n > 0) args.path[r0] = 0;
       for (int i = 1; i < n; ++i) {
@@ -203,88 +270,116 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
       n_skip_s = n_skip;
       if (report)
         for (int i = n > 0 ? depth + 1 : 0; i < T; ++i) args.path[r0 + i] = -1;
-    } else if (!args.draft && cur + 1 < n) {
-      skip_s[0] = args.tokens[r0 + cur + 1];
-      n_skip_s = 1;
+      cur_s = cur;
     }
-    cur_s = cur;
-    if (report) args.accepted[r] = n > 0 ? cur : -1;
+    __syncthreads();
   }
-  __syncthreads();
-  const int cur = cur_s;
+  const int cur = TREE ? cur_s : first_fall - 1;
+  if (report) args.accepted[r] = n > 0 ? cur : -1;
   if (n == 0) {  // the same for every CTA of the cluster
     cluster.barrier_wait(std::move(started));
     if (report) args.next_token[r] = -1;
     return;
   }
   Row row{args.target, nullptr, (r0 + cur) * args.target_stride, 0, skip_s, n_skip_s};
-  if (!TREE && args.draft && cur + 1 < n) {
-    row.q = args.draft;
-    row.q0 = ((int64_t)r * (T - 1) + cur) * args.draft_stride;
-  }
-  // this warp's part of the row
-  const int per_warp = (V + parts * kAccWarps - 1) / (parts * kAccWarps);
-  const int64_t at = (int64_t)(rank * kAccWarps + warp) * per_warp;
-  const int lo = (int)(at < V ? at : V), hi = (int)(at + per_warp < V ? at + per_warp : V);
-  float s = 0.f, c = 0.f;
-  for (int j = lo + lane; j < hi; j += 32) {
-    const float p = prob_at<DT>(row.p, row.p0 + j);
-    float w = p, e = 0.f;
-    if (row.q) {
-      const float q = prob_at<DT>(row.q, row.q0 + j);
-      w = p - q;
-      const float b = p - w;  // q as subtracted; p - q = w + e exactly
-      e = (p - (w + b)) + (b - q);
-      if (!(p > q)) w = e = 0.f;
+  if (!TREE && cur + 1 < n) {
+    if (args.draft) {
+      row.q = args.draft;
+      row.q0 = ((int64_t)r * (T - 1) + cur) * args.draft_stride;
     } else {
-      for (int k = 0; k < row.n_skip; ++k)
-        if (row.skip[k] == j) w = 0.f;
+      row.skip = args.tokens + r0 + cur + 1;
+      row.n_skip = 1;
     }
-    const float t = s + w, z = t - s;
-    c += (s - (t - z)) + (w - z) + e;
-    s = t;
   }
-  double sum = (double)s + (double)c;
+  // block sums, blocks dealt out to the cluster's warps
+  const int groups = (V + kBlock * kMaxBlocks - 1) / (kBlock * kMaxBlocks), size = groups * kBlock;
+  const int blocks = (V + size - 1) / size;
+  bool waited = false;
+  for (int b = rank * kAccWarps + warp; b < blocks; b += parts * kAccWarps) {
+    float s = 0.f, c = 0.f;
+    for (int g = 0; g < groups; ++g) {
+      const int64_t j0 = (int64_t)b * size + g * kBlock;
+      if (j0 >= V) break;
+      float w[8], err[8];
+      weights8<DT, VEC>(row, (int)j0 + (VEC ? 8 * lane : lane), VEC ? 1 : 32, V, w, err);
 #pragma unroll
-  for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  // every CTA of the cluster has started: its shared memory may be written
-  cluster.barrier_wait(std::move(started));
-  if (lane == 0) *cluster.map_shared_rank(&sums[rank * kAccWarps + warp], 0) = sum;
+      for (int e = 0; e < 8; ++e) add_pair(s, c, w[e], err[e]);
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+      const float s2 = __shfl_xor_sync(0xffffffffu, s, m), c2 = __shfl_xor_sync(0xffffffffu, c, m);
+      add_pair(s, c, s2, c2);
+    }
+    if (!waited) {  // every CTA of the cluster has started: its shared memory may be written
+      cluster.barrier_wait(std::move(started));
+      waited = true;
+    }
+    if (lane == 0) *cluster.map_shared_rank(&sums[b], 0) = (double)s + (double)c;
+  }
+  if (!waited) cluster.barrier_wait(std::move(started));
   cluster.sync();
-  if (rank != 0 || warp != 0) return;
-  const int blocks = parts * kAccWarps;
-  double whole = 0.0;
-  for (int b0 = 0; b0 < blocks; b0 += 32)
-    whole = __shfl_sync(0xffffffffu, whole + warp_scan(b0 + lane < blocks ? sums[b0 + lane] : 0.0, lane), 31);
-  const double u = args.uniforms[r0];
+  if (rank != 0) return;
+  // the first block whose running sum passes the goal, else the last with weight
+  constexpr int kPer = kMaxBlocks / kAccThreads;
+  double x[kPer], mine = 0.0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    x[e] = tid * kPer + e < blocks ? sums[tid * kPer + e] : 0.0;
+    mine += x[e];
+  }
+  const double in_warp = warp_scan(mine, lane);
+  if (lane == 31) warp_sum[warp] = in_warp;
+  __syncthreads();
+  double before = 0.0, whole = 0.0;
+#pragma unroll
+  for (int w = 0; w < kAccWarps; ++w) {
+    if (w == warp) before = whole;
+    whole += warp_sum[w];
+  }
+  before += in_warp - mine;
+  const double u = u_draw;
+  const double goal = u * whole;
+  int last = -1, first = -1;
+  double last_before = 0.0, run = before;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    if (x[e] > 0.0 && first < 0) {
+      last = tid * kPer + e;
+      last_before = run;
+      if (run + x[e] > goal) first = last;
+    }
+    run += x[e];
+  }
+  // one thread wins: the lowest that found its border, or else the highest with weight
+  __shared__ int lowest, highest;
+  if (tid == 0) lowest = kAccThreads, highest = -1;
+  __syncthreads();
+  if (first >= 0) atomicMin(&lowest, tid);
+  if (last >= 0) atomicMax(&highest, tid);
+  __syncthreads();
+  if (tid == (lowest < kAccThreads ? lowest : highest)) {
+    pick = last;
+    pick_before = last_before;
+  }
+  __syncthreads();
+  if (warp != 0) return;
   int answer = -1;
   if (whole > 0.0) {
-    const double goal = u * whole;
-    int part = 0;  // the first part whose running sum passes the goal, else the last with weight
-    double before = 0.0, part_before = 0.0;
-    for (int b0 = 0; b0 < blocks; b0 += 32) {
-      const double x = b0 + lane < blocks ? sums[b0 + lane] : 0.0;
-      const double cum = before + warp_scan(x, lane);
-      const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
-      const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && cum > goal);
-      if (some) {
-        const int pick = over ? __ffs(over) - 1 : 31 - __clz(some);
-        part = b0 + pick;
-        part_before = __shfl_sync(0xffffffffu, cum - x, pick);
-      }
-      if (over) break;
-      before = __shfl_sync(0xffffffffu, cum, 31);
-    }
-    const int64_t p0 = (int64_t)part * per_warp;
-    answer = find_in<DT>(row, (int)p0, (int)(p0 + per_warp < V ? p0 + per_warp : V), part_before, goal, lane);
+    const int64_t a = (int64_t)pick * size;
+    answer = find_in<DT, VEC>(row, (int)a, (int)(a + size < V ? a + size : V), pick_before, goal, lane);
   } else {  // nothing left of the row: all of p
     row.q = nullptr;
     row.n_skip = 0;
     double all = 0.0;
-    for (int j = lane; j < V; j += 32) all += weight_at<DT>(row, j);
+    for (int j0 = 0; j0 < V; j0 += kBlock) {
+      float w[8], err[8];
+      weights8<DT, VEC>(row, j0 + 8 * lane, 1, V, w, err);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) all += (double)w[e];
+    }
 #pragma unroll
     for (int m = 16; m; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
-    answer = find_in<DT>(row, 0, V, 0.0, u * all, lane);
+    answer = find_in<DT, VEC>(row, 0, V, 0.0, u * all, lane);
   }
   if (lane == 0) args.next_token[r] = answer;
 }
@@ -293,9 +388,13 @@ template <int DT>
 kda_status launch_accept(const AcceptArgs& a, int B, bool tree, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
-  // CTAs per request: enough to fill the SMs twice, but at least 128 elements a warp
+  // CTAs per request: enough to fill the SMs twice, but a block at least for each warp
   int parts = 1;
-  while (parts < 8 && (int64_t)B * parts < 2 * sms && (int64_t)parts * kAccWarps * 128 < a.vocab) parts *= 2;
+  while (parts < 8 && (int64_t)B * parts < 2 * sms && (int64_t)parts * kAccWarps * kBlock < a.vocab) parts *= 2;
+  // 16-byte loads where every row starts on 16 bytes
+  const int64_t es = DT == KDA_DTYPE_F32 ? 4 : 2;
+  const bool vec = aligned16(a.target) && a.target_stride * es % 16 == 0 &&
+                   (!a.draft || (aligned16(a.draft) && a.draft_stride * es % 16 == 0));
   if ((int64_t)B * parts > INT32_MAX) return KDA_ERR_SHAPE;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -308,7 +407,9 @@ kda_status launch_accept(const AcceptArgs& a, int B, bool tree, cudaStream_t st)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   record_stage(0, st);
-  cudaLaunchKernelEx(&cfg, tree ? accept_kernel<DT, true> : accept_kernel<DT, false>, a);
+  cudaLaunchKernelEx(&cfg, tree ? (vec ? accept_kernel<DT, true, true> : accept_kernel<DT, true, false>)
+                                : (vec ? accept_kernel<DT, false, true> : accept_kernel<DT, false, false>),
+                     a);
   const kda_status s = launch_status();
   record_stage(1, st);
   record_stage(2, st);

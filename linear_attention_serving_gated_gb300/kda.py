@@ -409,6 +409,40 @@ def kda_set_stage_events(events=None):
 
 
 # -- the gated delta rule with one decay per value head ----------------------
+#
+# These calls take a few microseconds on the GPU at their smallest, so what the
+# host does for one is kept short: one pass of checks per tensor, plain integers
+# for pointers, and the current stream without a Python stream object.
+
+
+def _arg(t, dtype, n, name, shape):
+    """Device pointer of a dense tensor of one element type that holds at least n
+    elements (the rows the kernels touch)."""
+    if t.dtype is not dtype and not (t.dtype is torch.int16 and dtype in _BITS16):
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.numel() < n or not t.is_contiguous():
+        _at_least(t, n, name, shape)
+    if not t.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    return t.data_ptr()
+
+
+_BITS16 = (torch.bfloat16, torch.float16)  # raw int16 bits are accepted for either
+
+
+def _opt(t, dtype, n, name, shape):
+    return None if t is None else _arg(t, dtype, n, name, shape)
+
+
+def _err(err_flag):
+    return None if err_flag is None else _arg(err_flag, torch.int32, 1, "err_flag", "[1]")
+
+
+def _cur(stream):
+    """cudaStream_t of a torch stream, or of the current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 class ScalarGate:
@@ -421,42 +455,27 @@ class ScalarGate:
         self.beta_is_raw, self.use_qk_l2norm, self.scale = beta_is_raw, use_qk_l2norm, scale
 
     def c(self, d):
-        for t, name in ((self.A_log, "A_log"), (self.dt_bias, "dt_bias")):
-            if t is not None:
-                if t.dtype != torch.float32:
-                    raise TypeError("A_log and dt_bias must be float32")
-                _at_least(t, d.HV, name, "[HV]")
-        return kda_scalar_gate(_p(self.A_log), _p(self.dt_bias), int(bool(self.beta_is_raw)),
-                               int(bool(self.use_qk_l2norm)), float(self.scale))
+        return kda_scalar_gate(_opt(self.A_log, torch.float32, d.HV, "A_log", "[HV]"),
+                               _opt(self.dt_bias, torch.float32, d.HV, "dt_bias", "[HV]"),
+                               1 if self.beta_is_raw else 0, 1 if self.use_qk_l2norm else 0, self.scale)
 
 
-def _typed(t, dtype, name):
-    """A device tensor of one element type (None allowed)."""
-    if t is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    return _p(t)
+def _pool_slots(d, state_pool):
+    shape = state_pool.shape
+    if len(shape) != 4 or shape[1] != d.HV or shape[2] != d.V or shape[3] != d.K:
+        raise ValueError(f"state_pool must be [slots, HV, V, K] = [*, {d.HV}, {d.V}, {d.K}] (got {tuple(shape)})")
+    return shape[0]
 
 
-def _scalar_gate_input(d, gate, a):
-    """The gate input: 16-bit with A_log, FP32 log-decays without."""
-    return _in16(d, a, "a") if gate.A_log is not None else _typed(a, torch.float32, "a (log-decays)")
-
-
-def _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, rows, reqs):
-    if state_pool.dim() < 3 or tuple(state_pool.shape[-3:]) != (d.HV, d.V, d.K):
-        raise ValueError(f"state_pool must end in [HV, V, K] = [{d.HV}, {d.V}, {d.K}] "
-                         f"(got {tuple(state_pool.shape)})")
-    _at_least(state_pool, 0, "state_pool", "[slots, HV, V, K]")
-    width = 2 * d.H * d.K + d.HV * d.V
-    if mixed_qkv.dim() != 2 or mixed_qkv.shape[0] < rows or mixed_qkv.shape[1] < width \
-            or mixed_qkv.stride(1) != 1:
-        raise ValueError(f"mixed_qkv must be [>= {rows}, >= {width}] with unit column stride "
-                         f"(got {tuple(mixed_qkv.shape)})")
+def _gate_rows(d, gate, a, rows):
+    """The gate input [>= rows, HV]: 16-bit with A_log, FP32 log-decays without."""
     if a.shape[-1] != d.HV:
-        raise ValueError(f"`a` must have shape [B, HV] = [{rows}, {d.HV}] (got {tuple(a.shape)})")
-    _at_least(a, rows * d.HV, "a", f"[{rows}, HV]")
-    _at_least(b, rows * d.HV, "b", f"[{rows}, HV]")
-    _at_least(state_idx, reqs, "state_idx", f"[{reqs}]")
+        raise ValueError(f"`a` must have shape [rows, HV] = [{rows}, {d.HV}] (got {tuple(a.shape)})")
+    return _arg(a, _t16(d) if gate.A_log is not None else torch.float32, rows * d.HV, "a", "[rows, HV]")
+
+
+def _t16(d):
+    return torch.float16 if d.dtype == KDA_DTYPE_F16 else torch.bfloat16
 
 
 def kda_gdn_prefill_workspace_size(d: kda_dims, num_seqs: int, total_tokens: int) -> int:
@@ -468,74 +487,79 @@ def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, c
     """Varlen prefill (see kda.h).  q,k [T,H,K], v [T,HV,V], a and b
     [gb_rows,HV]; state_pool [slots,HV,V,K] fp32 (in place); o [T,HV,V]
     (written)."""
-    T, gb_rows = q.shape[0], a.shape[0]
-    if a.shape[-1] != d.HV:
-        raise ValueError(f"`a` must have shape [gb_rows, HV] = [*, {d.HV}] (got {tuple(a.shape)})")
-    if state_pool.dim() < 3 or tuple(state_pool.shape[-3:]) != (d.HV, d.V, d.K):
-        raise ValueError(f"state_pool must end in [HV, V, K] = [{d.HV}, {d.V}, {d.K}] "
-                         f"(got {tuple(state_pool.shape)})")
-    _at_least(state_pool, 0, "state_pool", "[slots, HV, V, K]")
-    _at_least(q, T * d.H * d.K, "q", f"[{T}, H, K]")
-    _at_least(k, T * d.H * d.K, "k", f"[{T}, H, K]")
-    _at_least(v, T * d.HV * d.V, "v", f"[{T}, HV, V]")
-    _at_least(a, gb_rows * d.HV, "a", f"[{gb_rows}, HV]")
-    _at_least(b, gb_rows * d.HV, "b", f"[{gb_rows}, HV]")
-    _at_least(o, T * d.HV * d.V, "o", f"[{T}, HV, V]")
-    _at_least(state_idx, num_seqs, "state_idx", f"[{num_seqs}]")
-    _at_least(cu_seqlens, num_seqs + 1, "cu_seqlens", f"[{num_seqs + 1}]")
-    inter_chunks = _intermediate_chunks(d, intermediate)
+    lib, t16 = load(), _t16(d)
+    T, gb_rows, n = q.shape[0], a.shape[0], int(num_seqs)
+    HK, HVV = d.H * d.K, d.HV * d.V
+    slots = _pool_slots(d, state_pool)
+    inter_chunks = _intermediate_chunks(d, intermediate) if intermediate is not None else 0
     if workspace is None:
-        workspace = torch.empty(max(kda_gdn_prefill_workspace_size(d, num_seqs, T), 1), dtype=torch.uint8,
+        workspace = torch.empty(max(int(lib.kda_gdn_prefill_workspace_size(d, n, T)), 1), dtype=torch.uint8,
                                 device=q.device)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = load().kda_gdn_prefill(
-        d, gate.c(d), _in16(d, q, "q"), _in16(d, k, "k"), _in16(d, v, "v"), _scalar_gate_input(d, gate, a),
-        _in16(d, b, "b"), int(gb_rows), _typed(state_pool, torch.float32, "state_pool"), int(state_pool.shape[0]),
-        _typed(state_idx, torch.int32, "state_idx"), _typed(cu_seqlens, torch.int32, "cu_seqlens"), int(num_seqs),
-        int(T), _in16(d, o, "o"), _p(intermediate), inter_chunks, _p(workspace), ws_bytes, _p(err_flag),
-        _stream(stream))
-    _check(st, "kda_gdn_prefill")
+    st = lib.kda_gdn_prefill(
+        d, gate.c(d), _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
+        _arg(v, t16, T * HVV, "v", "[T, HV, V]"), _gate_rows(d, gate, a, gb_rows),
+        _arg(b, t16, gb_rows * d.HV, "b", "[gb_rows, HV]"), gb_rows,
+        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), slots,
+        _arg(state_idx, torch.int32, n, "state_idx", "[num_seqs]"),
+        _opt(cu_seqlens, torch.int32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
+        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), _opt(intermediate, torch.float32, 0, "intermediate", "[chunks, HV, V, K]"),
+        inter_chunks, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_gdn_prefill")
+
+
+def _gdn_rows(d, mixed_qkv, rows):
+    shape, width = mixed_qkv.shape, 2 * d.H * d.K + d.HV * d.V
+    if len(shape) != 2 or shape[0] < rows or shape[1] < width or mixed_qkv.stride(1) != 1:
+        raise ValueError(f"mixed_qkv must be [>= {rows}, >= {width}] with unit column stride (got {tuple(shape)})")
+    if mixed_qkv.dtype is not _t16(d) and mixed_qkv.dtype is not torch.int16:
+        raise TypeError(f"mixed_qkv must be {_t16(d)} (got {mixed_qkv.dtype})")
+    if not mixed_qkv.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    return mixed_qkv.data_ptr()
 
 
 def kda_gdn_decode_packed(d, gate: ScalarGate, mixed_qkv, a, b, state_pool, state_idx, o, err_flag=None,
                           stream=None):
     """One token per request, state in place; a, b [B, HV]."""
-    B = mixed_qkv.shape[0]
-    _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, B, B)
-    _at_least(o, B * d.HV * d.V, "o", f"[{B}, HV, V]")
+    B, t16 = mixed_qkv.shape[0], _t16(d)
     st = load().kda_gdn_decode_packed(
-        d, gate.c(d), _in16(d, mixed_qkv, "mixed_qkv"), int(mixed_qkv.stride(0)), _scalar_gate_input(d, gate, a),
-        _in16(d, b, "b"), int(B), _typed(state_pool, torch.float32, "state_pool"), int(state_pool.shape[0]),
-        _typed(state_idx, torch.int32, "state_idx"), _in16(d, o, "o"), _p(err_flag), _stream(stream))
-    _check(st, "kda_gdn_decode_packed")
+        d, gate.c(d), _gdn_rows(d, mixed_qkv, B), mixed_qkv.stride(0), _gate_rows(d, gate, a, B),
+        _arg(b, t16, B * d.HV, "b", "[B, HV]"), B, _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"),
+        _pool_slots(d, state_pool), _arg(state_idx, torch.int32, B, "state_idx", "[B]"),
+        _arg(o, t16, B * d.HV * d.V, "o", "[B, HV, V]"), _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_gdn_decode_packed")
 
 
-def _gdn_verify(name, d, gate, mixed_qkv, a, b, B, T, parents, state_pool, state_idx, o, snapshots, err_flag,
+def _gdn_verify(name, call, d, gate, mixed_qkv, a, b, B, T, parents, state_pool, state_idx, o, snapshots, err_flag,
                 stream):
-    _gdn_packed_shapes(d, mixed_qkv, a, b, state_pool, state_idx, B * T, B)
-    _at_least(o, B * T * d.HV * d.V, "o", f"[{B}, {T}, HV, V]")
-    _at_least(snapshots, B * T * d.HV * d.V * d.K, "snapshots", f"[{B}, {T}, HV, V, K]")
-    st = getattr(load(), name)(
-        d, gate.c(d), _in16(d, mixed_qkv, "mixed_qkv"), int(mixed_qkv.stride(0)), _scalar_gate_input(d, gate, a),
-        _in16(d, b, "b"), int(B), int(T), *parents, _typed(state_pool, torch.float32, "state_pool"),
-        int(state_pool.shape[0]), _typed(state_idx, torch.int32, "state_idx"), _in16(d, o, "o"),
-        _typed(snapshots, torch.float32, "snapshots"), _p(err_flag), _stream(stream))
-    _check(st, name)
+    B, T = int(B), int(T)
+    rows, t16 = B * T, _t16(d)
+    st = call(
+        d, gate.c(d), _gdn_rows(d, mixed_qkv, rows), mixed_qkv.stride(0), _gate_rows(d, gate, a, rows),
+        _arg(b, t16, rows * d.HV, "b", "[B * T, HV]"), B, T, *parents,
+        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), _pool_slots(d, state_pool),
+        _arg(state_idx, torch.int32, B, "state_idx", "[B]"), _arg(o, t16, rows * d.HV * d.V, "o", "[B, T, HV, V]"),
+        _arg(snapshots, torch.float32, rows * d.HV * d.V * d.K, "snapshots", "[B, T, HV, V, K]"), _err(err_flag),
+        _cur(stream))
+    if st:
+        _check(st, name)
 
 
 def kda_gdn_verify_chain(d, gate: ScalarGate, mixed_qkv, a, b, B, T, state_pool, state_idx, o, snapshots,
                          err_flag=None, stream=None):
     """Chain verify; snapshots as kda_verify_chain's, for kda_commit."""
-    _gdn_verify("kda_gdn_verify_chain", d, gate, mixed_qkv, a, b, B, T, (), state_pool, state_idx, o, snapshots,
-                err_flag, stream)
+    _gdn_verify("kda_gdn_verify_chain", load().kda_gdn_verify_chain, d, gate, mixed_qkv, a, b, B, T, (), state_pool,
+                state_idx, o, snapshots, err_flag, stream)
 
 
 def kda_gdn_verify_tree(d, gate: ScalarGate, mixed_qkv, a, b, B, T, parent_idx, state_pool, state_idx, o,
                         snapshots, err_flag=None, stream=None):
     """Tree verify; parent_idx [B, T] int32."""
-    _at_least(parent_idx, B * T, "parent_idx", f"[{B}, {T}]")
-    _gdn_verify("kda_gdn_verify_tree", d, gate, mixed_qkv, a, b, B, T, (_typed(parent_idx, torch.int32, "parent_idx"),),
-                state_pool, state_idx, o, snapshots, err_flag, stream)
+    _gdn_verify("kda_gdn_verify_tree", load().kda_gdn_verify_tree, d, gate, mixed_qkv, a, b, B, T,
+                (_arg(parent_idx, torch.int32, B * T, "parent_idx", "[B, T]"),), state_pool, state_idx, o, snapshots,
+                err_flag, stream)
 
 
 # -- verification of drafted tokens ------------------------------------------
@@ -543,30 +567,30 @@ def kda_gdn_verify_tree(d, gate: ScalarGate, mixed_qkv, a, b, B, T, parent_idx, 
 _PROBS = {torch.float32: KDA_DTYPE_F32, torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_F16}
 
 
-def _rows_stride(t, name, B, T):
-    """Elements between the rows of probabilities [B, T, vocab]: the rows may be
+def _probs(t, dtype, name, B, T):
+    """Pointer and row stride of probabilities [B, T, vocab]: the rows may be
     padded, but have one stride throughout."""
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != T or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [B, T, vocab] = [{B}, {T}, *] with dense rows (got {tuple(t.shape)})")
-    stride = t.stride(1) if T > 1 else t.stride(0) if B > 1 else t.shape[2]
-    if (B > 1 and t.stride(0) != T * stride) or stride < t.shape[2]:
-        raise ValueError(f"the rows of {name} must lie one stride apart (got strides {tuple(t.stride())})")
-    return int(stride)
+    shape, (s0, s1, s2) = t.shape, t.stride()
+    V = shape[2]
+    stride = s1 if T > 1 else s0 if B > 1 else V
+    if shape[0] != B or shape[1] != T or (V > 1 and s2 != 1):
+        raise ValueError(f"{name} must be [B, T, vocab] = [{B}, {T}, *] with dense rows (got {tuple(shape)})")
+    if (B > 1 and s0 != T * stride) or stride < V:
+        raise ValueError(f"the rows of {name} must lie one stride apart (got strides {(s0, s1, s2)})")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if not t.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    return t.data_ptr(), stride
 
 
-def _accept_args(target, tokens, uniforms, lengths, accepted, next_token):
-    if tokens.dim() != 2:
-        raise ValueError(f"tokens must be [B, T] (got {tuple(tokens.shape)})")
-    B, T = tokens.shape
+def _accept_sizes(target, tokens):
+    if tokens.dim() != 2 or target.dim() != 3:
+        raise ValueError(f"target must be [B, T, vocab] and tokens [B, T] (got {tuple(target.shape)}, "
+                         f"{tuple(tokens.shape)})")
     if target.dtype not in _PROBS:
         raise TypeError(f"target must be float32, bfloat16 or float16 (got {target.dtype})")
-    stride = _rows_stride(target, "target", B, T)
-    _at_least(tokens, B * T, "tokens", f"[{B}, {T}]")
-    _at_least(uniforms, B * T, "uniforms", f"[{B}, {T}]")
-    _at_least(lengths, B, "lengths", f"[{B}]")
-    _at_least(accepted, B, "accepted", f"[{B}]")
-    _at_least(next_token, B, "next_token", f"[{B}]")
-    return B, T, stride
+    return tokens.shape[0], tokens.shape[1], target.shape[2]
 
 
 def kda_accept_chain(target, draft, tokens, uniforms, accepted, next_token, lengths=None, err_flag=None,
@@ -576,36 +600,38 @@ def kda_accept_chain(target, draft, tokens, uniforms, accepted, next_token, leng
     element type, rows possibly padded; tokens [B,T] int32, uniforms [B,T] fp32,
     lengths [B] int32 or None; accepted [B] int32 (for kda_commit) and
     next_token [B] int32 (written)."""
-    B, T, stride = _accept_args(target, tokens, uniforms, lengths, accepted, next_token)
-    draft_stride = 0
-    if T == 1:
-        draft = None  # nothing was drafted
-    if draft is not None:
-        if draft.dtype != target.dtype or draft.shape[-1] != target.shape[-1]:
-            raise ValueError("draft must have target's element type and vocabulary")
-        draft_stride = _rows_stride(draft, "draft", B, T - 1)
+    B, T, V = _accept_sizes(target, tokens)
+    dtype, i32 = target.dtype, torch.int32
+    p, p_stride = _probs(target, dtype, "target", B, T)
+    q, q_stride = None, 0
+    if draft is not None and T > 1:
+        if draft.dim() != 3 or draft.shape[2] != V:
+            raise ValueError("draft must have target's vocabulary")
+        q, q_stride = _probs(draft, dtype, "draft", B, T - 1)
     st = load().kda_accept_chain(
-        _PROBS[target.dtype], _p(target), stride, _p(draft), draft_stride, _typed(tokens, torch.int32, "tokens"),
-        _typed(uniforms, torch.float32, "uniforms"), _typed(lengths, torch.int32, "lengths"), int(B), int(T),
-        int(target.shape[2]), _typed(accepted, torch.int32, "accepted"), _typed(next_token, torch.int32, "next_token"),
-        _p(err_flag), _stream(stream))
-    _check(st, "kda_accept_chain")
+        _PROBS[dtype], p, p_stride, q, q_stride, _arg(tokens, i32, B * T, "tokens", "[B, T]"),
+        _arg(uniforms, torch.float32, B * T, "uniforms", "[B, T]"), _opt(lengths, i32, B, "lengths", "[B]"), B, T, V,
+        _arg(accepted, i32, B, "accepted", "[B]"), _arg(next_token, i32, B, "next_token", "[B]"), _err(err_flag),
+        _cur(stream))
+    if st:
+        _check(st, "kda_accept_chain")
 
 
 def kda_accept_tree(target, tokens, parent_idx, uniforms, accepted, path, next_token, lengths=None, err_flag=None,
                     stream=None):
     """As kda_accept_chain for a tree proposed without probabilities:
     parent_idx [B,T] int32; path [B,T] int32 (written)."""
-    B, T, stride = _accept_args(target, tokens, uniforms, lengths, accepted, next_token)
-    _at_least(parent_idx, B * T, "parent_idx", f"[{B}, {T}]")
-    _at_least(path, B * T, "path", f"[{B}, {T}]")
+    B, T, V = _accept_sizes(target, tokens)
+    dtype, i32 = target.dtype, torch.int32
+    p, p_stride = _probs(target, dtype, "target", B, T)
     st = load().kda_accept_tree(
-        _PROBS[target.dtype], _p(target), stride, _typed(tokens, torch.int32, "tokens"),
-        _typed(parent_idx, torch.int32, "parent_idx"), _typed(uniforms, torch.float32, "uniforms"),
-        _typed(lengths, torch.int32, "lengths"), int(B), int(T), int(target.shape[2]),
-        _typed(accepted, torch.int32, "accepted"), _typed(path, torch.int32, "path"),
-        _typed(next_token, torch.int32, "next_token"), _p(err_flag), _stream(stream))
-    _check(st, "kda_accept_tree")
+        _PROBS[dtype], p, p_stride, _arg(tokens, i32, B * T, "tokens", "[B, T]"),
+        _arg(parent_idx, i32, B * T, "parent_idx", "[B, T]"), _arg(uniforms, torch.float32, B * T, "uniforms", "[B, T]"),
+        _opt(lengths, i32, B, "lengths", "[B]"), B, T, V, _arg(accepted, i32, B, "accepted", "[B]"),
+        _arg(path, i32, B * T, "path", "[B, T]"), _arg(next_token, i32, B, "next_token", "[B]"), _err(err_flag),
+        _cur(stream))
+    if st:
+        _check(st, "kda_accept_tree")
 
 
 # -- pages of a state pool ---------------------------------------------------
@@ -614,68 +640,73 @@ def kda_accept_tree(target, tokens, parent_idx, uniforms, accepted, path, next_t
 def _pages(pool):
     """Pages of a pool tensor [layers, slots, ...] whose slots are dense; the
     layers may lie further apart."""
-    if pool.dim() < 3:
-        raise ValueError(f"pool must be [layers, slots, ...] (got {tuple(pool.shape)})")
-    layers, slots = pool.shape[0], pool.shape[1]
-    if layers > 0 and not pool[0].is_contiguous():
+    shape, size = pool.shape, pool.element_size()
+    if len(shape) < 3:
+        raise ValueError(f"pool must be [layers, slots, ...] (got {tuple(shape)})")
+    if not pool.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    page = 1
+    for n in shape[2:]:
+        page *= n
+    if not pool.is_contiguous() and shape[0] > 0 and not pool[0].is_contiguous():
         raise ValueError("the slots of a layer must be dense")
-    page = pool.element_size() * math.prod(pool.shape[2:])
-    stride = pool.element_size() * (pool.stride(0) if layers > 1 else slots * math.prod(pool.shape[2:]))
-    return kda_pages(_p(pool), page, stride, int(layers), int(slots))
+    stride = pool.stride(0) if shape[0] > 1 else page * shape[1]
+    return kda_pages(pool.data_ptr(), page * size, stride * size, shape[0], shape[1])
 
 
-def _int32_list(t, name):
-    if t is None or t.dim() != 1:
-        raise ValueError(f"{name} must be a list [n]")
-    _at_least(t, 0, name, "[n]")
-    return _typed(t, torch.int32, name)
+def _list(t, name):
+    """Pointer of an int32 list."""
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be a list [n] (got {tuple(t.shape)})")
+    return _arg(t, torch.int32, 0, name, "[n]")
 
 
 def _used(used, slots):
-    if used.dtype not in (torch.uint8, torch.bool):
-        raise TypeError(f"used must be uint8 or bool (got {used.dtype})")
-    _at_least(used, slots, "used", f"[{slots}]")
-    return _p(used)
+    return _arg(used, torch.bool if used.dtype is torch.bool else torch.uint8, slots, "used", "[slots]")
 
 
 def kda_pool_copy(pool, src, dst, err_flag=None, stream=None):
     """pool[:, dst[i]] <- pool[:, src[i]]; pool [layers, slots, ...]."""
-    if src.shape != dst.shape:
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst must have one length")
-    st = load().kda_pool_copy(_pages(pool), _int32_list(src, "src"), _int32_list(dst, "dst"), int(src.shape[0]),
-                              _p(err_flag), _stream(stream))
-    _check(st, "kda_pool_copy")
+    st = load().kda_pool_copy(_pages(pool), _list(src, "src"), _list(dst, "dst"), n, _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_pool_copy")
 
 
 def kda_pool_free(used, table, rows, err_flag=None, stream=None):
     """Frees the pages of table rows `rows` and sets the rows to -1."""
-    slots = int(used.shape[0])
-    st = load().kda_pool_free(_used(used, slots), slots, _int32_list(table, "table"), int(table.shape[0]),
-                              _int32_list(rows, "rows"), int(rows.shape[0]), _p(err_flag), _stream(stream))
-    _check(st, "kda_pool_free")
+    slots = used.shape[0]
+    st = load().kda_pool_free(_used(used, slots), slots, _list(table, "table"), table.shape[0], _list(rows, "rows"),
+                              rows.shape[0], _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_pool_free")
 
 
 def kda_pool_compact(pool, used, table, count, err_flag=None, stream=None):
     """Moves the used pages to slots 0 .. count-1; table, used and count [1]
     int32 follow."""
-    _at_least(count, 1, "count", "[1]")
-    st = load().kda_pool_compact(_pages(pool), _used(used, pool.shape[1]), _int32_list(table, "table"),
-                                 int(table.shape[0]), _typed(count, torch.int32, "count"), _p(err_flag), _stream(stream))
-    _check(st, "kda_pool_compact")
+    pages = _pages(pool)
+    st = load().kda_pool_compact(pages, _used(used, pages.slots), _list(table, "table"), table.shape[0],
+                                 _arg(count, torch.int32, 1, "count", "[1]"), _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_pool_compact")
 
 
 def kda_pool_fork(pool, used, table, parents, rows, children=None, err_flag=None, stream=None):
     """Table row rows[i] gets the lowest free page, a copy of the page of row
     parents[i] (zeros where that is -1); returns children [n] int32, the slots
     given."""
-    if parents.shape != rows.shape:
+    n = rows.shape[0]
+    if parents.shape[0] != n:
         raise ValueError("parents and rows must have one length")
-    n = int(rows.shape[0])
     if children is None:
-        children = torch.empty(n, dtype=torch.int32, device=rows.device)
-    _at_least(children, n, "children", "[n]")
-    st = load().kda_pool_fork(_pages(pool), _used(used, pool.shape[1]), _int32_list(table, "table"),
-                              int(table.shape[0]), _int32_list(parents, "parents"), _int32_list(rows, "rows"), n,
-                              _int32_list(children, "children"), _p(err_flag), _stream(stream))
-    _check(st, "kda_pool_fork")
+        children = torch.empty_like(rows)
+    pages = _pages(pool)
+    st = load().kda_pool_fork(pages, _used(used, pages.slots), _list(table, "table"), table.shape[0],
+                              _list(parents, "parents"), _list(rows, "rows"), n,
+                              _arg(children, torch.int32, n, "children", "[n]"), _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_pool_fork")
     return children
