@@ -10,13 +10,12 @@
 // The answer is a whole number, so it must not depend on how sums are split.
 // Accept tests are exact: the product of two FP32 numbers fits FP64.  Sums of
 // weights are FP32 pairs (sum, error) whose error part takes what each addition
-// and each difference p - q rounds off (two-sum; 48 bits), joined in FP64 once
-// per 256 weights: FP64 for every element, at 1/64 of FP32's rate here, would
-// bound the kernel.
+// and each difference p - q rounds off (two-sum; 48 bits); FP64, at 1/64 of FP32's
+// rate here, is left to the few comparisons with u times the whole.
 //
 // One cluster per request: every CTA repeats the walk (a few gathered loads,
 // whose latency is the same for one CTA as for all), its warps sum blocks of 256
-// weights and store one FP64 sum per block in the first CTA's shared memory.  The
+// weights and store one pair per block in the first CTA's shared memory.  The
 // first CTA scans the block sums, and one warp goes through the block that holds
 // the border.  A row is read once, 32 bytes a lane and block; bound by latency
 // for a few requests and by HBM for many (48 rows of p and q of 131072 FP32: 50
@@ -130,18 +129,24 @@ __device__ __forceinline__ void weights8(const Row& row, int j, int step, int V,
   }
 }
 
-// (s, c) += (x, y), s the rounded sum and c what it leaves.
-__device__ __forceinline__ void add_pair(float& s, float& c, float x, float y) {
-  const float t = s + x, z = t - s;
-  c += ((s - (t - z)) + (x - z)) + y;
-  s = t;
+// A sum as s + c, s rounded and c what that leaves.
+struct Pair {
+  float s, c;
+  __device__ double value() const { return (double)s + (double)c; }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const float t = a.s + b.s, z = t - a.s;
+  return {t, a.c + (((a.s - (t - z)) + (b.s - z)) + b.c)};
 }
-
-__device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
+__device__ __forceinline__ Pair shfl(Pair x, int lane) {
+  return {__shfl_sync(0xffffffffu, x.s, lane), __shfl_sync(0xffffffffu, x.c, lane)};
+}
+template <int WIDTH>
+__device__ __forceinline__ Pair scan(Pair x, int lane) {  // inclusive, over WIDTH lanes
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
+  for (int d = 1; d < WIDTH; d <<= 1) {
+    const Pair y{__shfl_up_sync(0xffffffffu, x.s, d), __shfl_up_sync(0xffffffffu, x.c, d)};
+    if (lane >= d) x = y + x;
   }
   return x;
 }
@@ -150,41 +155,40 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
 // `goal`; where rounding leaves none, the last j with weight; -1 where none has
 // any.  One warp, lo a multiple of 8.
 template <int DT, bool VEC>
-__device__ int find_in(const Row& row, int lo, int hi, double before, double goal, int lane) {
+__device__ int find_in(const Row& row, int lo, int hi, Pair before, double goal, int lane) {
   int last = -1;
   for (int j0 = lo; j0 < hi; j0 += kBlock) {
-    const int j = j0 + 8 * lane;
     float w[8], err[8];
-    weights8<DT, VEC>(row, j, 1, hi, w, err);
-    double sum = 0.0;
+    weights8<DT, VEC>(row, j0 + 8 * lane, 1, hi, w, err);
+    Pair sum{0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += (double)w[e] + (double)err[e];
-    const double cum = before + warp_scan(sum, lane);
-    const unsigned some = __ballot_sync(0xffffffffu, sum > 0.0);
-    const unsigned over = __ballot_sync(0xffffffffu, sum > 0.0 && cum > goal);
+    for (int e = 0; e < 8; ++e) sum = sum + Pair{w[e], err[e]};
+    const Pair cum = before + scan<32>(sum, lane);
+    const unsigned some = __ballot_sync(0xffffffffu, sum.s > 0.f);
+    const unsigned over = __ballot_sync(0xffffffffu, sum.s > 0.f && cum.value() > goal);
     if (some) {
+      // lane L's eight weights, one each for the first lanes
       const int L = over ? __ffs(over) - 1 : 31 - __clz(some);
-      double run = cum - sum;
-      int at = -1;
-      bool found = false;
+      const Pair up = shfl(cum, (L + 31) & 31), base = L > 0 ? up : before;
+      Pair mine{0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        run += (double)w[e] + (double)err[e];
-        if (w[e] > 0.f && !found) {
-          at = j + e;
-          found = run > goal;
-        }
+        const Pair x = shfl(Pair{w[e], err[e]}, L);
+        if (lane == e) mine = x;
       }
-      last = __shfl_sync(0xffffffffu, at, L);
+      const Pair run = base + scan<8>(mine, lane);
+      const unsigned pos = __ballot_sync(0xffffffffu, lane < 8 && mine.s > 0.f);
+      const unsigned hit = __ballot_sync(0xffffffffu, lane < 8 && mine.s > 0.f && run.value() > goal);
+      last = j0 + 8 * L + (hit ? __ffs(hit) - 1 : 31 - __clz(pos));
       if (over) return last;
     }
-    before = __shfl_sync(0xffffffffu, cum, 31);
+    before = shfl(cum, 31);
   }
   return last;
 }
 
 template <int DT, bool TREE, bool VEC>
-__global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs args) {
+__global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs args) {
   cg::cluster_group cluster = cg::this_cluster();
   auto started = cluster.barrier_arrive();
   const int rank = cluster.block_rank(), parts = cluster.num_blocks();
@@ -194,8 +198,8 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
   __shared__ float p_tok[TREE ? KDA_ACCEPT_MAX_T : 1], u_s[TREE ? KDA_ACCEPT_MAX_T : 1];
   __shared__ int tok_s[TREE ? KDA_ACCEPT_MAX_T : 1], par_s[TREE ? KDA_ACCEPT_MAX_T : 1];
   __shared__ int skip_s[TREE ? KDA_ACCEPT_MAX_T : 1];
-  __shared__ double sums[kMaxBlocks], warp_sum[kAccWarps], pick_before;
-  __shared__ int first_fall, cur_s, n_skip_s, pick;
+  __shared__ Pair sums[kMaxBlocks], warp_sum[kAccWarps], pick_before;
+  __shared__ int first_fall, cur_s, n_skip_s, pick, lowest, highest;
 
   const int64_t r0 = (int64_t)r * T;
   const float u_draw = args.uniforms[r0];
@@ -208,7 +212,8 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
   if (tid == 0) {
     first_fall = n;
     n_skip_s = 0;
-    pick = -1;
+    lowest = kAccThreads;
+    highest = -1;
   }
   if constexpr (TREE) {
     bool bad = false;
@@ -294,66 +299,68 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
   // block sums, blocks dealt out to the cluster's warps
   const int groups = (V + kBlock * kMaxBlocks - 1) / (kBlock * kMaxBlocks), size = groups * kBlock;
   const int blocks = (V + size - 1) / size;
+  const int stride = parts * kAccWarps;
+  const int step = VEC ? 1 : 32, at = VEC ? 8 * lane : lane;
   bool waited = false;
-  for (int b = rank * kAccWarps + warp; b < blocks; b += parts * kAccWarps) {
-    float s = 0.f, c = 0.f;
+  for (int b = rank * kAccWarps + warp; b < blocks; b += 2 * stride) {
+    // two blocks at a time, with both blocks' loads in flight
+    Pair sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
     for (int g = 0; g < groups; ++g) {
-      const int64_t j0 = (int64_t)b * size + g * kBlock;
-      if (j0 >= V) break;
-      float w[8], err[8];
-      weights8<DT, VEC>(row, (int)j0 + (VEC ? 8 * lane : lane), VEC ? 1 : 32, V, w, err);
+      float w[2][8], err[2][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) add_pair(s, c, w[e], err[e]);
+      for (int x = 0; x < 2; ++x) {
+        const int64_t j0 = (int64_t)(b + x * stride) * size + g * kBlock + at;  // entries past the end are zeros
+        weights8<DT, VEC>(row, (int)(j0 < V ? j0 : V), step, V, w[x], err[x]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) sum[x] = sum[x] + Pair{w[x][e], err[x][e]};
     }
 #pragma unroll
-    for (int m = 16; m; m >>= 1) {
-      const float s2 = __shfl_xor_sync(0xffffffffu, s, m), c2 = __shfl_xor_sync(0xffffffffu, c, m);
-      add_pair(s, c, s2, c2);
-    }
+    for (int m = 16; m; m >>= 1)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        sum[x] = sum[x] + Pair{__shfl_xor_sync(0xffffffffu, sum[x].s, m), __shfl_xor_sync(0xffffffffu, sum[x].c, m)};
     if (!waited) {  // every CTA of the cluster has started: its shared memory may be written
       cluster.barrier_wait(std::move(started));
       waited = true;
     }
-    if (lane == 0) *cluster.map_shared_rank(&sums[b], 0) = (double)s + (double)c;
+    if (lane < 2 && b + lane * stride < blocks) *cluster.map_shared_rank(&sums[b + lane * stride], 0) = lane ? sum[1] : sum[0];
   }
   if (!waited) cluster.barrier_wait(std::move(started));
   cluster.sync();
   if (rank != 0) return;
   // the first block whose running sum passes the goal, else the last with weight
   constexpr int kPer = kMaxBlocks / kAccThreads;
-  double x[kPer], mine = 0.0;
+  Pair x[kPer], mine{0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    x[e] = tid * kPer + e < blocks ? sums[tid * kPer + e] : 0.0;
-    mine += x[e];
+    x[e] = tid * kPer + e < blocks ? sums[tid * kPer + e] : Pair{0.f, 0.f};
+    mine = mine + x[e];
   }
-  const double in_warp = warp_scan(mine, lane);
+  const Pair in_warp = scan<32>(mine, lane);
   if (lane == 31) warp_sum[warp] = in_warp;
   __syncthreads();
-  double before = 0.0, whole = 0.0;
-#pragma unroll
-  for (int w = 0; w < kAccWarps; ++w) {
-    if (w == warp) before = whole;
-    whole += warp_sum[w];
-  }
-  before += in_warp - mine;
-  const double u = u_draw;
-  const double goal = u * whole;
+  // every warp scans the warps' sums
+  const Pair all_warps = scan<kAccWarps>(lane < kAccWarps ? warp_sum[lane] : Pair{0.f, 0.f}, lane);
+  const double whole = shfl(all_warps, kAccWarps - 1).value(), u = u_draw, goal = u * whole;
+  const Pair up_warp = shfl(all_warps, (warp + 31) & 31), up_lane = shfl(in_warp, (lane + 31) & 31);
+  Pair run{0.f, 0.f}, last_before{0.f, 0.f};
+  if (warp > 0) run = up_warp;
+  if (lane > 0) run = run + up_lane;
   int last = -1, first = -1;
-  double last_before = 0.0, run = before;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    if (x[e] > 0.0 && first < 0) {
+    const Pair next = run + x[e];
+    if (x[e].s > 0.f && first < 0) {
       last = tid * kPer + e;
       last_before = run;
-      if (run + x[e] > goal) first = last;
+      if (next.value() > goal) first = last;
     }
-    run += x[e];
+    run = next;
   }
   // one thread wins: the lowest that found its border, or else the highest with weight
-  __shared__ int lowest, highest;
-  if (tid == 0) lowest = kAccThreads, highest = -1;
-  __syncthreads();
   if (first >= 0) atomicMin(&lowest, tid);
   if (last >= 0) atomicMax(&highest, tid);
   __syncthreads();
@@ -370,16 +377,17 @@ __global__ void __launch_bounds__(kAccThreads) accept_kernel(const AcceptArgs ar
   } else {  // nothing left of the row: all of p
     row.q = nullptr;
     row.n_skip = 0;
-    double all = 0.0;
+    Pair all{0.f, 0.f};
     for (int j0 = 0; j0 < V; j0 += kBlock) {
       float w[8], err[8];
       weights8<DT, VEC>(row, j0 + 8 * lane, 1, V, w, err);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) all += (double)w[e];
+      for (int e = 0; e < 8; ++e) all = all + Pair{w[e], 0.f};
     }
 #pragma unroll
-    for (int m = 16; m; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
-    answer = find_in<DT, VEC>(row, 0, V, 0.0, u * all, lane);
+    for (int m = 16; m; m >>= 1)
+      all = all + Pair{__shfl_xor_sync(0xffffffffu, all.s, m), __shfl_xor_sync(0xffffffffu, all.c, m)};
+    answer = find_in<DT, VEC>(row, 0, V, Pair{0.f, 0.f}, u * all.value(), lane);
   }
   if (lane == 0) args.next_token[r] = answer;
 }
