@@ -404,7 +404,8 @@ kda_status kda_gdn_verify_tree(kda_dims dims, kda_scalar_gate gate, const kda_bf
  */
 #define KDA_DTYPE_F32 2 /* for probs_dtype only */
 #define KDA_DEVERR_TOKEN 64 /* drafted token outside [0, vocab) */
-#define KDA_ACCEPT_MAX_T 1024
+#define KDA_ACCEPT_MAX_T 1024 /* more rows or entries: KDA_ERR_UNSUPPORTED */
+#define KDA_ACCEPT_MAX_VOCAB (1 << 28)
 
 /*
  * Chain: token i stands while all before it do and u[r][i] * q < p, p its

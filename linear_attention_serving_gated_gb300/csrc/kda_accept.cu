@@ -22,6 +22,8 @@
 // MB).
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "kda_host.h"
 
 namespace cg = cooperative_groups;
@@ -32,6 +34,12 @@ namespace {
 constexpr int kAccThreads = 256, kAccWarps = kAccThreads / 32;
 constexpr int kBlock = 256;      // weights per block sum, 8 a lane
 constexpr int kMaxBlocks = 1024;  // longer rows take larger blocks
+constexpr int kRing = 4;          // groups of 256 weights a warp has under way to shared memory
+// 16-byte pieces of a group a lane takes, of p and of q
+template <int DT>
+constexpr int kPieces = DT == KDA_DTYPE_F32 ? 2 : 1;
+template <int DT>
+constexpr int kRingBytes = kRing * 2 * kPieces<DT> * 16 * kAccThreads;
 
 struct AcceptArgs {
   const void* target;
@@ -106,7 +114,15 @@ __device__ __forceinline__ void load8(const void* base, int64_t row0, int j, int
   for (int e = 0; e < 8; ++e) x[e] = valid(x[e]);
 }
 
-// Eight weights: w exactly p - q as w + err.
+// max(p - q, 0), exactly w + err (p and q valid; where p > q the difference's
+// rounding is (p - w) - q).
+__device__ __forceinline__ void difference(float p, float q, float& w, float& err) {
+  const float d = p - q;
+  err = d > 0.f ? (p - d) - q : 0.f;
+  w = fmaxf(d, 0.f);
+}
+
+// Eight weights as w + err.
 template <int DT, bool VEC>
 __device__ __forceinline__ void weights8(const Row& row, int j, int step, int V, float (&w)[8], float (&err)[8]) {
   load8<DT, VEC>(row.p, row.p0, j, step, V, w);
@@ -116,11 +132,7 @@ __device__ __forceinline__ void weights8(const Row& row, int j, int step, int V,
     float q[8];
     load8<DT, VEC>(row.q, row.q0, j, step, V, q);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float p = w[e], d = p - q[e], b = p - d;  // b: q as subtracted
-      err[e] = d > 0.f ? (p - (d + b)) + (b - q[e]) : 0.f;
-      w[e] = fmaxf(d, 0.f);
-    }
+    for (int e = 0; e < 8; ++e) difference(w[e], q[e], w[e], err[e]);
   } else {
     for (int k = 0; k < row.n_skip; ++k)
 #pragma unroll
@@ -141,6 +153,18 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
 __device__ __forceinline__ Pair shfl(Pair x, int lane) {
   return {__shfl_sync(0xffffffffu, x.s, lane), __shfl_sync(0xffffffffu, x.c, lane)};
 }
+// Two sums side by side in packed FP32 arithmetic.
+struct Pair2 {
+  float2 s, c;
+  __device__ void add(float2 x, float2 err) {
+    const float2 neg = make_float2(-1.f, -1.f);
+    const float2 t = add2(s, x), z = fma2(s, neg, t);
+    const float2 a = fma2(fma2(z, neg, t), neg, s), b = fma2(z, neg, x);  // s - (t - z), x - z
+    c = add2(c, add2(add2(a, b), err));
+    s = t;
+  }
+  __device__ Pair joined() const { return Pair{s.x, c.x} + Pair{s.y, c.y}; }
+};
 template <int WIDTH>
 __device__ __forceinline__ Pair scan(Pair x, int lane) {  // inclusive, over WIDTH lanes
 #pragma unroll
@@ -200,6 +224,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   __shared__ int skip_s[TREE ? KDA_ACCEPT_MAX_T : 1];
   __shared__ Pair sums[kMaxBlocks], warp_sum[kAccWarps], pick_before;
   __shared__ int first_fall, cur_s, n_skip_s, pick, lowest, highest;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
 
   const int64_t r0 = (int64_t)r * T;
   const float u_draw = args.uniforms[r0];
@@ -297,36 +322,127 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
     }
   }
   // block sums, blocks dealt out to the cluster's warps
-  const int groups = (V + kBlock * kMaxBlocks - 1) / (kBlock * kMaxBlocks), size = groups * kBlock;
+  // A block sum takes a warp as many instructions as 128 weights do: rows that
+  // are long enough take blocks of 1024.
+  const int least = (V + kBlock * kMaxBlocks - 1) / (kBlock * kMaxBlocks);
+  const int groups = V >= 1024 * parts * kAccWarps && least < 4 ? 4 : least, size = groups * kBlock;
   const int blocks = (V + size - 1) / size;
-  const int stride = parts * kAccWarps;
-  const int step = VEC ? 1 : 32, at = VEC ? 8 * lane : lane;
+  const int stride = parts * kAccWarps, b0 = rank * kAccWarps + warp;
   bool waited = false;
-  for (int b = rank * kAccWarps + warp; b < blocks; b += 2 * stride) {
-    // two blocks at a time, with both blocks' loads in flight
-    Pair sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-    for (int g = 0; g < groups; ++g) {
-      float w[2][8], err[2][8];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int64_t j0 = (int64_t)(b + x * stride) * size + g * kBlock + at;  // entries past the end are zeros
-        weights8<DT, VEC>(row, (int)(j0 < V ? j0 : V), step, V, w[x], err[x]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) sum[x] = sum[x] + Pair{w[x][e], err[x][e]};
-    }
+  auto store = [&](Pair sum, int b) {
 #pragma unroll
     for (int m = 16; m; m >>= 1)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        sum[x] = sum[x] + Pair{__shfl_xor_sync(0xffffffffu, sum[x].s, m), __shfl_xor_sync(0xffffffffu, sum[x].c, m)};
+      sum = sum + Pair{__shfl_xor_sync(0xffffffffu, sum.s, m), __shfl_xor_sync(0xffffffffu, sum.c, m)};
     if (!waited) {  // every CTA of the cluster has started: its shared memory may be written
       cluster.barrier_wait(std::move(started));
       waited = true;
     }
-    if (lane < 2 && b + lane * stride < blocks) *cluster.map_shared_rank(&sums[b + lane * stride], 0) = lane ? sum[1] : sum[0];
+    if (lane == 0) *cluster.map_shared_rank(&sums[b], 0) = sum;
+  };
+  if constexpr (VEC) {
+    // Groups of 256 weights pass through a ring in shared memory, kRing of them
+    // under way.  A lane reads only the pieces it copied, so its own wait is all
+    // the synchronisation there is.
+    constexpr int kP = kPieces<DT>, kEl = 8 / kP;  // entries per 16-byte piece
+    uint4* ring = reinterpret_cast<uint4*>(ring_smem) + warp * (kRing * 2 * kP * 32) + lane;
+    const int mine = b0 < blocks ? (blocks - b0 + stride - 1) / stride * groups : 0;  // groups of this warp
+    const bool has_q = row.q != nullptr;
+    constexpr int kBytes = DT == KDA_DTYPE_F32 ? 4 : 2;
+    const char* p_row = static_cast<const char*>(row.p) + row.p0 * kBytes;
+    const char* q_row = has_q ? static_cast<const char*>(row.q) + row.q0 * kBytes : p_row;
+    int next = 0, next_j = b0 * size + lane * kEl, next_g = 0;  // the group requested next
+    auto request = [&] {
+      if (next < mine) {
+        uint4* dst = ring + (next % kRing) * (2 * kP * 32);
+#pragma unroll
+        for (int x = 0; x < kP; ++x) {
+          const int j = next_j + x * 32 * kEl, left = (V - j) * kBytes;
+          const int bytes = left >= 16 ? 16 : left > 0 ? left : 0;  // zeros past the end
+          const int64_t at = bytes ? (int64_t)j * kBytes : 0;
+          cp_async16_zfill(dst + x * 32, p_row + at, bytes);
+          if (has_q) cp_async16_zfill(dst + (kP + x) * 32, q_row + at, bytes);
+        }
+        ++next;
+        next_j += kBlock;
+        if (++next_g == groups) {
+          next_g = 0;
+          next_j += (stride - 1) * size;
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kRing - 1; ++k) request();
+    auto value = [&](const uint4& w, int e) {
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      if constexpr (DT == KDA_DTYPE_F32) return __uint_as_float(ww[e]);
+      return in16_to_float<DT == KDA_DTYPE_F16>((uint16_t)(e & 1 ? ww[e / 2 % 4] >> 16 : ww[e / 2 % 4] & 0xffffu));
+    };
+    int k = 0;
+    for (int b = b0; b < blocks; b += stride) {
+      // Without a look at infinities: a p of them ends up in the sum, the largest
+      // q is kept, and a block that has met one is summed again, entry by entry.
+      Pair2 sum{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      float q_max = 0.f;
+      for (int g = 0; g < groups; ++g, ++k) {
+        request();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        const uint4* src = ring + (k % kRing) * (2 * kP * 32);
+#pragma unroll
+        for (int x = 0; x < kP; ++x) {
+          const uint4 wp = src[x * 32];
+          if (has_q) {
+            const uint4 wq = src[(kP + x) * 32];
+#pragma unroll
+            for (int e = 0; e < kEl; e += 2) {
+              const float2 neg = make_float2(-1.f, -1.f);
+              const float2 p = make_float2(fmaxf(value(wp, e), 0.f), fmaxf(value(wp, e + 1), 0.f));
+              const float2 q = make_float2(fmaxf(value(wq, e), 0.f), fmaxf(value(wq, e + 1), 0.f));
+              q_max = fmaxf(q_max, fmaxf(q.x, q.y));
+              const float2 d = fma2(q, neg, p), r = fma2(q, neg, fma2(d, neg, p));  // difference()
+              sum.add(make_float2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)),
+                      make_float2(d.x > 0.f ? r.x : 0.f, d.y > 0.f ? r.y : 0.f));
+            }
+          } else {
+            float w[kEl];
+#pragma unroll
+            for (int e = 0; e < kEl; ++e) w[e] = fmaxf(value(wp, e), 0.f);
+            const int j = b * size + g * kBlock + x * 32 * kEl + lane * kEl;
+            for (int s = 0; s < row.n_skip; ++s)
+#pragma unroll
+              for (int e = 0; e < kEl; ++e)
+                if (row.skip[s] == j + e) w[e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kEl; e += 2) sum.add(make_float2(w[e], w[e + 1]), make_float2(0.f, 0.f));
+          }
+        }
+      }
+      Pair total = sum.joined();
+      const float inf = __int_as_float(0x7f800000);
+      if (__any_sync(0xffffffffu, !(total.s < inf) || !(q_max < inf))) {
+        total = Pair{0.f, 0.f};
+        for (int j = b * size + 8 * lane; j < b * size + size; j += kBlock) {
+          float w[8], err[8];
+          weights8<DT, true>(row, j < V ? j : V, 1, V, w, err);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) total = total + Pair{w[e], err[e]};
+        }
+      }
+      store(total, b);
+    }
+    cp_async_wait_all();  // no copy into shared memory outlives the CTA
+  } else {
+    for (int b = b0; b < blocks; b += stride) {
+      Pair sum{0.f, 0.f};
+      for (int g = 0; g < groups; ++g) {
+        const int64_t j0 = (int64_t)b * size + g * kBlock + lane;  // entries past the end are zeros
+        float w[8], err[8];
+        weights8<DT, false>(row, (int)(j0 < V ? j0 : V), 32, V, w, err);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = sum + Pair{w[e], err[e]};
+      }
+      store(sum, b);
+    }
   }
   if (!waited) cluster.barrier_wait(std::move(started));
   cluster.sync();
@@ -392,6 +508,24 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   if (lane == 0) args.next_token[r] = answer;
 }
 
+template <int DT, bool TREE, bool VEC>
+kda_status launch_accept_kernel(const AcceptArgs& a, cudaLaunchConfig_t cfg) {
+  if (VEC) {
+    cfg.dynamicSmemBytes = kRingBytes<DT>;
+    static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
+    if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+      if (cudaFuncSetAttribute(accept_kernel<DT, TREE, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kRingBytes<DT>) != cudaSuccess)
+        return KDA_ERR_CUDA;
+      ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+  }
+  cudaLaunchKernelEx(&cfg, accept_kernel<DT, TREE, VEC>, a);
+  return launch_status();
+}
+
 template <int DT>
 kda_status launch_accept(const AcceptArgs& a, int B, bool tree, cudaStream_t st) {
   const int sms = sm_count();
@@ -415,10 +549,8 @@ kda_status launch_accept(const AcceptArgs& a, int B, bool tree, cudaStream_t st)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   record_stage(0, st);
-  cudaLaunchKernelEx(&cfg, tree ? (vec ? accept_kernel<DT, true, true> : accept_kernel<DT, true, false>)
-                                : (vec ? accept_kernel<DT, false, true> : accept_kernel<DT, false, false>),
-                     a);
-  const kda_status s = launch_status();
+  const kda_status s = tree ? (vec ? launch_accept_kernel<DT, true, true>(a, cfg) : launch_accept_kernel<DT, true, false>(a, cfg))
+                            : (vec ? launch_accept_kernel<DT, false, true>(a, cfg) : launch_accept_kernel<DT, false, false>(a, cfg));
   record_stage(1, st);
   record_stage(2, st);
   return s;
@@ -427,7 +559,7 @@ kda_status launch_accept(const AcceptArgs& a, int B, bool tree, cudaStream_t st)
 kda_status accept_common(int dtype, const AcceptArgs& a, int B, bool tree, void* stream) {
   if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_F16) return KDA_ERR_UNSUPPORTED;
   if (B < 0 || a.T < 1 || a.vocab < 1 || a.target_stride < a.vocab) return KDA_ERR_SHAPE;
-  if (a.T > KDA_ACCEPT_MAX_T) return KDA_ERR_UNSUPPORTED;
+  if (a.T > KDA_ACCEPT_MAX_T || a.vocab > KDA_ACCEPT_MAX_VOCAB) return KDA_ERR_UNSUPPORTED;
   if (a.draft && a.draft_stride < a.vocab) return KDA_ERR_SHAPE;
   if (B == 0) return KDA_OK;
   if (!a.target || !a.tokens || !a.uniforms || !a.accepted || !a.next_token || (tree && (!a.parent || !a.path)))

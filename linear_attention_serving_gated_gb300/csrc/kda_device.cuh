@@ -158,6 +158,13 @@ __device__ __forceinline__ void cp_async16(void* dst_smem, const void* src) {
                "l"(src)
                : "memory");
 }
+// The first `bytes` (0 to 16) of the source, zeros behind them.
+__device__ __forceinline__ void cp_async16_zfill(void* dst_smem, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async4(void* dst_smem, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                    static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),

@@ -66,17 +66,14 @@ def test_accept_host_errors(lib):
     def chain(dt=2, target=D, stride=100, draft=D, dstride=100, tokens=D, B=2, T=3, V=100, out=D):
         return lib.kda_accept_chain(dt, target, stride, draft, dstride, tokens, D, None, B, T, V, out, D, None, None)
 
-    assert chain(dt=3) == chain(T=kda_max_t() + 1) == kda.KDA_ERR_UNSUPPORTED
+    assert chain(dt=3) == chain(T=1025) == kda.KDA_ERR_UNSUPPORTED
+    assert chain(V=(1 << 28) + 1, stride=1 << 30, dstride=1 << 30) == kda.KDA_ERR_UNSUPPORTED
     assert chain(target=None) == chain(tokens=None) == chain(out=None) == kda.KDA_ERR_NULL_ARG
     assert chain(stride=99) == chain(dstride=99) == chain(T=0) == chain(V=0) == chain(B=-1) == kda.KDA_ERR_SHAPE
     assert chain(target=ODD) == chain(draft=ODD) == kda.KDA_ERR_ALIGNMENT
     assert chain(B=0) == kda.KDA_OK
     assert lib.kda_accept_tree(2, D, 100, D, None, D, None, 2, 3, 100, D, D, D, None, None) == kda.KDA_ERR_NULL_ARG
     assert lib.kda_accept_tree(2, D, 100, D, D, D, None, 2, 3, 100, D, None, D, None, None) == kda.KDA_ERR_NULL_ARG
-
-
-def kda_max_t():
-    return 1024
 
 
 def test_pool_host_errors(lib):
