@@ -516,11 +516,28 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);  // rows landed, [K; Q] K^T done, TMEM address
   const int t = threadIdx.x, quad = t >> 5, lane = t & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");  // K and Q were split by the launch before
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
     if (t == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
     return;
   }
+  // what needs nothing of the chunk comes before the walk that finds it
+  uint8_t* kq = smem;
+  uint8_t* t_hi = smem + C::kT;
+  uint8_t* t_lo = t_hi + 8192;
+  if (quad == 0) tc::tmem_alloc(reinterpret_cast<uint32_t*>(&bars[2]), C::kTmCols);
+  if (t == 0) {
+    tc::mbar_init(&bars[0], 1);
+    tc::mbar_init(&bars[1], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int x = t; x < 16384 / 16; x += 128)  // blocks of T above the diagonal are not written below
+    reinterpret_cast<uint4*>(t_hi)[x] = make_uint4(0, 0, 0, 0);
+  auto leave = [&] {  // no chunk here: the grid is an upper bound
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (quad == 0) tc::tmem_dealloc(*reinterpret_cast<const uint32_t*>(&bars[2]), C::kTmCols);
+  };
   // the chunk's sequence: every warp walks over the sequences, 128 at a time
   const int h = blockIdx.x % args.HV, id = blockIdx.x / args.HV;
   int n = -1, c = 0;
@@ -552,29 +569,19 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     }
     base += __shfl_sync(0xffffffffu, run, 31);
   }
-  if (n < 0) return;  // the grid is an upper bound
+  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");  // K and Q were split by the launch before
+  if (n < 0) {
+    leave();
+    return;
+  }
   const int slot = args.state_idx[n];
-  if (slot < 0 || slot >= args.pool_slots) return;
+  if (slot < 0 || slot >= args.pool_slots) {
+    leave();
+    return;
+  }
   const int64_t t0 = seq_start(args, n) + (int64_t)c * kC;
   const int left = seq_len(args, n) - c * kC, len = left < kC ? left : kC;
-
-  uint8_t* kq = smem;
-  uint8_t* t_hi = smem + C::kT;
-  uint8_t* t_lo = t_hi + 8192;
-  uint8_t* rec = args.records + ((int64_t)id * args.HV + h) * kRecBytes;
-  uint8_t* a_hi = smem;  // over the first half of K, and over the second
-  uint8_t* a_lo = smem + 16384;
-  float* diag = reinterpret_cast<float*>(smem + C::kDiag);
-  float* c_hi = reinterpret_cast<float*>(smem + C::kGate);  // c_i = c_hi + c_lo
-  float* c_lo = c_hi + kC;
-  float* beta_s = c_lo + kC;
-  float* rks = beta_s + kC;
-  ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(smem + C::kScalars);
-  const ScalarGateArgs& ga = args.gate;
   if (t == 0) {
-    tc::mbar_init(&bars[0], 1);
-    tc::mbar_init(&bars[1], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tc::mbar_expect_tx(&bars[0], C::kRowBytes);
     const int tok = (int)t0, hk = h / args.G;
 #pragma unroll
@@ -584,43 +591,65 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
       if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, &bars[0]);
     }
   }
-  if (quad == 0) tc::tmem_alloc(reinterpret_cast<uint32_t*>(&bars[2]), C::kTmCols);
-  if (quad == 3) {  // decays and betas: tokens 2 lane and 2 lane + 1
-    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
-    float gl[2], be[2];  // past the end nothing decays and nothing is written
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      gl[e] = be[e] = 0.f;
-      if (2 * lane + e < len) {
-        const int64_t at = (t0 + 2 * lane + e) * args.HV + h;
-        const float b = in16_to_float<F16>(args.beta[at]);
-        gl[e] = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
-        be[e] = ga.beta_is_raw ? sigmoidf_(b) : b;
-      }
+
+  uint8_t* rec = args.records + ((int64_t)id * args.HV + h) * kRecBytes;
+  uint8_t* a_hi = smem;  // over the first half of K, and over the second
+  uint8_t* a_lo = smem + 16384;
+  float* diag = reinterpret_cast<float*>(smem + C::kDiag);
+  float* c_hi = reinterpret_cast<float*>(smem + C::kGate);  // c_i = c_hi + c_lo (first the log-decays)
+  float* c_lo = c_hi + kC;
+  float* beta_s = c_lo + kC;
+  float* rks = beta_s + kC;
+  ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(smem + C::kScalars);
+  const ScalarGateArgs& ga = args.gate;
+  if (t < kC) {  // log-decay and beta of a token; past the end nothing decays and nothing is written
+    float g = 0.f, b = 0.f;
+    if (t < len) {
+      const int64_t at = (t0 + t) * args.HV + h;
+      b = in16_to_float<F16>(args.beta[at]);
+      const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
+      const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
+      g = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
+      b = ga.beta_is_raw ? sigmoidf_(b) : b;
     }
-    // running sums in FP64, kept as two floats: differences of them count
-    double run = (double)gl[0] + (double)gl[1];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, run, d);
-      if (lane >= d) run += up;
-    }
-    const double c0 = run - (double)gl[1];
-    c_hi[2 * lane] = (float)c0;
-    c_lo[2 * lane] = (float)(c0 - (double)(float)c0);
-    c_hi[2 * lane + 1] = (float)run;
-    c_lo[2 * lane + 1] = (float)(run - (double)(float)run);
-    beta_s[2 * lane] = be[0];
-    beta_s[2 * lane + 1] = be[1];
+    c_hi[t] = g;
+    beta_s[t] = b;
   }
-  for (int x = t; x < 16384 / 16; x += 128)  // blocks of T above the diagonal are not written below
-    reinterpret_cast<uint4*>(t_hi)[x] = make_uint4(0, 0, 0, 0);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(&bars[2]);
   const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16);
+  // c_i, the running sums of the log-decays, as pairs hi + lo (two-sum): their
+  // differences count.  Every warp scans all 64, two a lane.
+  float2 c_i, c_mid, c_last;
+  {
+    auto plus = [](float2 a, float2 b) {
+      const float s = a.x + b.x, z = s - a.x;
+      return make_float2(s, a.y + (((a.x - (s - z)) + (b.x - z)) + b.y));
+    };
+    const float2 g = *reinterpret_cast<const float2*>(c_hi + 2 * lane);
+    float2 run = plus(make_float2(g.x, 0.f), make_float2(g.y, 0.f));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
+      if (lane >= d) run = plus(up, run);
+    }
+    const float2 even = plus(run, make_float2(-g.y, 0.f));  // token 2 lane; run: token 2 lane + 1
+    auto from = [](float2 x, int l) {
+      return make_float2(__shfl_sync(0xffffffffu, x.x, l), __shfl_sync(0xffffffffu, x.y, l));
+    };
+    const int i = 32 * (quad & 1) + lane;
+    const float2 a = from(even, i >> 1), b = from(run, i >> 1);
+    c_i = i & 1 ? b : a;
+    c_mid = from(even, kC / 4);
+    c_last = from(run, 31);
+    __syncthreads();  // every warp has read the log-decays
+    if (quad == 0) {
+      *reinterpret_cast<float2*>(c_hi + 2 * lane) = make_float2(even.x, run.x);
+      *reinterpret_cast<float2*>(c_lo + 2 * lane) = make_float2(even.y, run.y);
+    }
+  }
   bool bad = !warp_wait(&bars[0], 0);
   if (len < kC) {
     zero_rows(kq, 16384, len, t, 128);
@@ -679,8 +708,8 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   const float r = (krow ? 1.f : ga.scale) * (ga.use_qk_l2norm ? rsqrtf(sq + kNormEps) : 1.f);
   // r_i r_j e^(c_i - c_j) as a product of row and column factors about the
   // middle of the chunk, where those stay in FP32's range; term by term otherwise
-  const float ci_hi = c_hi[i], ci_lo = c_lo[i];
-  const float mid = (ci_hi - c_hi[kC / 2]) + (ci_lo - c_lo[kC / 2]);
+  const float ci_hi = c_i.x, ci_lo = c_i.y;
+  const float mid = (ci_hi - c_mid.x) + (ci_lo - c_mid.y);
   const bool far = !(fabsf(mid) <= 60.f);
   if (krow) rks[i] = r * expf(-mid);
   bad |= !warp_wait(&bars[1], 0);
@@ -692,7 +721,7 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   tc::tc_fence_after();
   const float ei = __expf(ci_hi + ci_lo);
   const float ui = wide ? r : r * expf(mid);
-  const float si = krow && i < len ? r * __expf((c_hi[63] - ci_hi) + (c_lo[63] - ci_lo)) : 0.f;
+  const float si = krow && i < len ? r * __expf((c_last.x - ci_hi) + (c_last.y - ci_lo)) : 0.f;
   const int top = 32 * (quad & 1) + 31;  // last row of this warp
 #pragma unroll 1
   for (int jb = 0; jb < 4; ++jb) {
