@@ -521,6 +521,10 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     return;
   }
   // what needs nothing of the chunk comes before the walk that finds it
+  const int h = blockIdx.x % args.HV, id = blockIdx.x / args.HV;
+  const ScalarGateArgs& ga = args.gate;
+  const float a_log = ga.A_log ? ga.A_log[h] : 0.f;
+  const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
   uint8_t* kq = smem;
   uint8_t* t_hi = smem + C::kT;
   uint8_t* t_lo = t_hi + 8192;
@@ -539,7 +543,6 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     if (quad == 0) tc::tmem_dealloc(*reinterpret_cast<const uint32_t*>(&bars[2]), C::kTmCols);
   };
   // the chunk's sequence: every warp walks over the sequences, 128 at a time
-  const int h = blockIdx.x % args.HV, id = blockIdx.x / args.HV;
   int n = -1, c = 0;
   for (int n0 = 0, base = 0; n0 < args.num_seqs && n < 0; n0 += 128) {
     int cnt[4], sum = 0;
@@ -574,11 +577,7 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     leave();
     return;
   }
-  const int slot = args.state_idx[n];
-  if (slot < 0 || slot >= args.pool_slots) {
-    leave();
-    return;
-  }
+  // (a sequence without a state slot gets records too, which none reads: to ask would cost each CTA a load's wait)
   const int64_t t0 = seq_start(args, n) + (int64_t)c * kC;
   const int left = seq_len(args, n) - c * kC, len = left < kC ? left : kC;
   if (t == 0) {
@@ -601,15 +600,12 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   float* beta_s = c_lo + kC;
   float* rks = beta_s + kC;
   ChunkScalars& sc = *reinterpret_cast<ChunkScalars*>(smem + C::kScalars);
-  const ScalarGateArgs& ga = args.gate;
   if (t < kC) {  // log-decay and beta of a token; past the end nothing decays and nothing is written
     float g = 0.f, b = 0.f;
     if (t < len) {
       const int64_t at = (t0 + t) * args.HV + h;
       b = in16_to_float<F16>(args.beta[at]);
-      const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-      const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
-      g = scalar_log_decay<F16>(ga, args.a, at, neg_rate, bias);
+      g = scalar_log_decay_of(ga, scalar_gate_in<F16>(ga, args.a, at), -expf(a_log), bias);
       b = ga.beta_is_raw ? sigmoidf_(b) : b;
     }
     c_hi[t] = g;

@@ -106,17 +106,29 @@ __device__ __forceinline__ float fold_beta(const GateArgs& ga, float b_in) {
 // given.  neg_rate = -exp(A_log[h]), bias = dt_bias[h].  Below -128 the decay
 // is zero in FP32 and stays zero in any sum with other log-decays <= 0; the
 // cut keeps such sums finite (-inf - -inf) and lets a NaN through.
+__device__ __forceinline__ float scalar_log_decay_of(const ScalarGateArgs& ga, float a_in, float neg_rate, float bias) {
+  float g = a_in;
+  if (ga.A_log) {
+    const float x = a_in + bias;
+    g = neg_rate * (x > 20.f ? x : log1pf(expf(x)));  // softplus; past 20 it is x to 2^-28
+  }
+  return g < -128.f ? -128.f : g;
+}
+
+// What scalar_log_decay_of takes: 16-bit a, or FP32 log-decays.  Loaded without
+// a branch, so that the loads around it need not wait for its outcome.
+template <bool F16>
+__device__ __forceinline__ float scalar_gate_in(const ScalarGateArgs& ga, const void* a, int64_t at) {
+  const bool raw = ga.A_log != nullptr;
+  const uint16_t* p = static_cast<const uint16_t*>(a) + (raw ? at : 2 * at);
+  const uint16_t lo = p[0], hi = p[raw ? 0 : 1];
+  return raw ? in16_to_float<F16>(lo) : __uint_as_float((uint32_t)hi << 16 | lo);
+}
+
 template <bool F16>
 __device__ __forceinline__ float scalar_log_decay(const ScalarGateArgs& ga, const void* a, int64_t at, float neg_rate,
                                                   float bias) {
-  float g;
-  if (ga.A_log) {
-    const float x = in16_to_float<F16>(static_cast<const uint16_t*>(a)[at]) + bias;
-    g = neg_rate * (x > 20.f ? x : log1pf(expf(x)));  // softplus; past 20 it is x to 2^-28
-  } else {
-    g = static_cast<const float*>(a)[at];
-  }
-  return g < -128.f ? -128.f : g;
+  return scalar_log_decay_of(ga, scalar_gate_in<F16>(ga, a, at), neg_rate, bias);
 }
 
 // Packed FP32 pair arithmetic (sm_100+ f32x2 instructions).
