@@ -445,6 +445,15 @@ def _cur(stream):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _new(n, dtype, device, stream):
+    """Memory for a call's own use, of the allocator's pool for the stream it
+    runs on: what another stream last used may still be in use there."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 class ScalarGate:
     """Fold options of the kda_gdn_* calls (kda_scalar_gate): A_log and dt_bias
     [HV] FP32 device tensors.  Without A_log the gate input is the log-decay
@@ -493,8 +502,7 @@ def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, c
     slots = _pool_slots(d, state_pool)
     inter_chunks = _intermediate_chunks(d, intermediate) if intermediate is not None else 0
     if workspace is None:
-        workspace = torch.empty(max(int(lib.kda_gdn_prefill_workspace_size(d, n, T)), 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new(max(int(lib.kda_gdn_prefill_workspace_size(d, n, T)), 1), torch.uint8, q.device, stream)
     st = lib.kda_gdn_prefill(
         d, gate.c(d), _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
         _arg(v, t16, T * HVV, "v", "[T, HV, V]"), _gate_rows(d, gate, a, gb_rows),
@@ -702,7 +710,7 @@ def kda_pool_fork(pool, used, table, parents, rows, children=None, err_flag=None
     if parents.shape[0] != n:
         raise ValueError("parents and rows must have one length")
     if children is None:
-        children = torch.empty_like(rows)
+        children = _new(n, torch.int32, rows.device, stream)
     pages = _pages(pool)
     st = load().kda_pool_fork(pages, _used(used, pages.slots), _list(table, "table"), table.shape[0],
                               _list(parents, "parents"), _list(rows, "rows"), n,
