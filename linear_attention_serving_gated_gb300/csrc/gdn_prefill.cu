@@ -103,20 +103,24 @@ static_assert(kRecScalars + sizeof(ChunkScalars) <= kRecBytes, "record");
 
 // Shared memory of the chunk kernel: [K; Q] as two halves of 64 channels and
 // 128 lines each, the low halves of FP16 keys, T and the scalars; P goes
-// straight to the record.  A's hi and lo halves take the place of K once its
-// products are done.
+// straight to the record.  A's hi and lo halves take the place of K, and T's
+// that of Q, once their products are done.
 template <bool F16>
 struct ChunkCfg {
   static constexpr int kRowBytes = 32768 + (F16 ? 16384 : 0);
-  static constexpr int kT = kRowBytes;         // T hi, T lo
-  static constexpr int kScalars = kT + 16384;  // 1024 bytes
+  static constexpr int kScalars = kRowBytes;  // 1024 bytes
   static constexpr int kGate = kScalars + 1024;  // float hi[64], lo[64], beta[64], rk[64]
   static constexpr int kBar = kGate + 4 * kC * 4;
   // A's diagonal blocks in FP32: over the keys' low halves where there are any
   static constexpr int kDiag = F16 ? 32768 : kBar + 64;
-  static constexpr int kSmem = kBar + 64 + (F16 ? 0 : 4 * 16 * kLdG * 4);
+  // (the product whose left operand are the 64 lines of K's low halves takes 128:
+  // its last 64 rows are whatever follows them, in bounds, and are not read back)
+  static constexpr int kSmem = F16 ? kRowBytes + 8192 : kBar + 64 + 4 * 16 * kLdG * 4;
+  static_assert(kBar + 64 <= kSmem, "regions");
   static constexpr int kTmCols = F16 ? 128 : 64;
-  static constexpr int kCtas = F16 ? 3 : 4;  // per SM
+  // per SM; five of 96 registers take 500 instead of 507 us for 8 x 4096 tokens,
+  // but 133 instead of 115 for 1 x 4096 (16 heads, whole call)
+  static constexpr int kCtas = 4;
 };
 
 struct Bars {
@@ -526,16 +530,12 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   const float a_log = ga.A_log ? ga.A_log[h] : 0.f;
   const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
   uint8_t* kq = smem;
-  uint8_t* t_hi = smem + C::kT;
-  uint8_t* t_lo = t_hi + 8192;
   if (quad == 0) tc::tmem_alloc(reinterpret_cast<uint32_t*>(&bars[2]), C::kTmCols);
   if (t == 0) {
     tc::mbar_init(&bars[0], 1);
     tc::mbar_init(&bars[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int x = t; x < 16384 / 16; x += 128)  // blocks of T above the diagonal are not written below
-    reinterpret_cast<uint4*>(t_hi)[x] = make_uint4(0, 0, 0, 0);
   auto leave = [&] {  // no chunk here: the grid is an upper bound
     tc::tc_fence_before();
     __syncthreads();
@@ -592,8 +592,10 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   }
 
   uint8_t* rec = args.records + ((int64_t)id * args.HV + h) * kRecBytes;
-  uint8_t* a_hi = smem;  // over the first half of K, and over the second
+  uint8_t* a_hi = smem;  // over the two halves of K
   uint8_t* a_lo = smem + 16384;
+  uint8_t* t_hi = smem + 8192;  // over the two halves of Q
+  uint8_t* t_lo = smem + 24576;
   float* diag = reinterpret_cast<float*>(smem + C::kDiag);
   float* c_hi = reinterpret_cast<float*>(smem + C::kGate);  // c_i = c_hi + c_lo (first the log-decays)
   float* c_lo = c_hi + kC;
@@ -714,6 +716,8 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     if (krow) rks[i] = r;
     __syncthreads();
   }
+  for (int x = t; x < 1024; x += 128)  // blocks of T above the diagonal are not written below
+    reinterpret_cast<uint4*>(x < 512 ? t_hi : t_lo)[x & 511] = make_uint4(0, 0, 0, 0);
   tc::tc_fence_after();
   const float ei = __expf(ci_hi + ci_lo);
   const float ui = wide ? r : r * expf(mid);
@@ -793,7 +797,8 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   __syncthreads();
   if (t == 0) {
     if (bad) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-    tc::bulk_s2g(rec + kRecT, t_hi, 16384);
+    tc::bulk_s2g(rec + kRecT, t_hi, 8192);
+    tc::bulk_s2g(rec + kRecTlo, t_lo, 8192);
     tc::bulk_s2g(rec + kRecScalars, &sc, 1024);
     tc::bulk_commit();
     tc::bulk_wait_read();
