@@ -25,8 +25,8 @@
 // product's TMEM accumulator into the next one's operand; one warp issues the
 // products from behind hardware barriers, one Q S and P D, which only the output
 // needs and 4 warps of their own join; two load the chunks' rows and records.
-// Two forms of that kernel:
-//   gdn_state_kernel, a CTA per (sequence, value head, 32 value columns):
+// Two forms of a CTA of that kernel, gdn_state_kernel:
+//   narrow, a CTA per (sequence, value head, 32 value columns):
 //       X  = K S           64 x 32 x 128
 //       D  = T Y           64 x 32 x 64
 //       dS = K^T D'       128 x 32 x 64, D'_j = e^(c_last - c_j) r_j D_j
@@ -34,7 +34,7 @@
 //     halves beside each other in one 64-wide tile: one product each for both.
 //     M = 64 spreads the token rows over all four warp quadrants of TMEM, 16
 //     lanes each, read in the fragment layout so that all 32 threads work.
-//   gdn_state_wide_kernel, a CTA per (sequence, value head), transposed:
+//   wide, a CTA per (sequence, value head), transposed:
 //       X^T  = S^T K^T     128 x 64 x 128
 //       D^T  = Y^T T^T     128 x 64 x 64
 //       dS^T = D'^T K      128 x 128 x 64
@@ -42,8 +42,9 @@
 //     makes is the next one's left operand, taken from TMEM: a thread's lane of
 //     the accumulator becomes its lane of the operand, and nothing of the chain
 //     passes through shared memory.
-// The first takes a chunk in less time, the second does four times as much in it:
-// it is taken once its CTAs fill the SMs (kda_gdn_prefill has both sides).
+// The first takes a chunk in 1.5 us, the second four times as many columns in
+// 2.8: sequences that the SMs would wait for are narrow, the rest are wide
+// (launch_states, pick_unit).
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
 // wherever the state depends on them, S, T, Y and D'.  K and Q are BF16 already.
 // FP16 keys are split exactly (11 bits into 8 + 8) and FP16 queries rounded to
@@ -80,6 +81,9 @@ struct GdnPrefillArgs {
   uint8_t* records;    // one per (chunk, value head)
   int64_t max_chunks;  // ids the workspace holds
   int longest_first;   // the state kernel takes the sequences by length
+  int most_narrow;     // at most so many sequences in the narrow form beside wide ones,
+  int all_narrow;      // and whether all may take it
+  int sms;
   int32_t* err_flag;
 };
 
@@ -139,6 +143,10 @@ constexpr int kChainWarps = 16, kOutWarps = 4;
 constexpr int kMmaWarp = kChainWarps + kOutWarps, kSideWarp = kMmaWarp + 1, kKeyWarp = kMmaWarp + 2,
               kRecWarp = kMmaWarp + 3, kStateThreads = (kRecWarp + 1) * 32;
 
+// Forms of the state kernel.
+enum { kNarrow, kWide, kMixed };
+constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred cycles for 8, two thousand for 128
+
 template <bool F16>
 struct Cfg {
   static constexpr int kQ = 16384 * (F16 ? 2 : 1);  // K, low halves of FP16 keys, Q
@@ -146,16 +154,16 @@ struct Cfg {
   static constexpr int kKeys = F16 ? 2 : 3, kRecs = 2;     // chunks in shared memory: rows, records
   static constexpr int kRec = kKeys * kKeyBytes;
   static constexpr int kBars = kRec + kRecs * kRecBytes;
-  // gdn_state_kernel's operands
+  // the narrow form's operands
   static constexpr int kS = (kBars + (int)sizeof(Bars) + 1023) / 1024 * 1024;
   static constexpr int kY = kS + 16384;
   static constexpr int kD = kY + 8192;
   static constexpr int kSmem = kD + 8192, kWideSmem = kBars + (int)sizeof(Bars);
 };
 
-// TMEM columns of the wide kernel.  Left operands (two BF16 a column): S, Y and
+// TMEM columns of the wide form.  Left operands (two BF16 a column): S, Y and
 // after it D'.  Accumulators: X and after it D, dS, Q S, P D; a warp's quarter of
-// D makes room for its D as an operand, 8 columns hi and 8 lo.  The other kernel
+// D makes room for its D as an operand, 8 columns hi and 8 lo.  The narrow form
 // has accumulators alone, in the same columns.
 constexpr int kTmS = 0, kTmSlo = 64, kTmY = 128, kTmYlo = 160, kTmX = 192, kTmU = 256, kTmQ = 384, kTmO = 448,
               kTmCols = 512;
@@ -263,7 +271,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
-constexpr int kDv = 32;  // value columns of a CTA of gdn_state_kernel
+constexpr int kDv = 32;  // value columns of a narrow CTA
 
 // A row's values as operand halves: columns [8 part, 8 part + 8) of the CTA's, in a
 // tile [hi | lo].
@@ -808,30 +816,95 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
 // What a state CTA works on.
 struct Unit {
   int h, slice, n;
+  int columns;  // kDv: the narrow form, kHeadDim: the wide one
   int L, nch, slot;
   int64_t t0;
 };
 
-// The first steps of a state CTA: its sequence, refusals (false: the whole CTA
-// leaves), barriers and TMEM.  `columns` value columns per CTA.
-__device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* smem, Bars& bars, int columns, Unit& s) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool reporter = tid == 0 && s.h == 0 && s.slice == 0;
-  int n = s.n;
-  if (args.longest_first) {  // CTAs start in order: sequence n is the n-th longest
-    int* len_s = reinterpret_cast<int*>(smem);
-    for (int m = tid; m < args.num_seqs; m += kStateThreads) len_s[m] = seq_len(args, m);
+// Microseconds / 20 of a state CTA: measured, 16 heads, BF16.
+__device__ __forceinline__ int64_t narrow_time(int64_t chunks) { return 29 * chunks + 120; }
+__device__ __forceinline__ int64_t wide_time(int64_t chunks) { return 62 * chunks + 200; }
+
+// Which unit a state CTA takes; false: none is left.  CTAs start in order, so
+// the longest sequences come first.  In the mixed kernel the k longest ones take
+// the narrow form; every CTA finds the k of the least estimate of the whole: the
+// longest CTA, and, where not all start at once, all CTAs' time over the SMs and
+// the last one behind it.  Wide CTAs beside narrow ones slow these down, by a
+// twelfth in the estimate.  All narrow, all wide and the mix of one k, whole call,
+// 16 heads (us): 8087 and seven shorter of 16980 tokens 284, 524, 292; 8 x 4096
+// 507, 341, -; 4000 twice and 2000 three times 237, -, 275.
+template <int kForm>
+__device__ __forceinline__ bool pick_unit(const GdnPrefillArgs& args, uint8_t* smem, Unit& s) {
+  constexpr int kSlices = kHeadDim / kDv;
+  const int tid = threadIdx.x, seqs = args.num_seqs;
+  int narrow = kForm == kNarrow ? seqs : 0;
+  int* order = reinterpret_cast<int*>(smem);
+  if (kForm == kMixed || args.longest_first) {
+    int* len_s = order + kMaxSorted;
+    int* chunks = len_s + kMaxSorted;
+    unsigned long long* best = reinterpret_cast<unsigned long long*>(chunks + kMaxSorted);
+    if (tid < seqs) len_s[tid] = seq_len(args, tid);
+    if (tid == 0) *best = ~0ull;
     __syncthreads();
-    if (tid < args.num_seqs) {
+    if (tid < seqs) {
       const int mine = len_s[tid];
       int before = 0;
-      for (int m = 0; m < args.num_seqs; ++m) before += len_s[m] > mine || (len_s[m] == mine && m < tid);
-      if (before == n) len_s[args.num_seqs] = tid;
+      for (int m = 0; m < seqs; ++m) before += len_s[m] > mine || (len_s[m] == mine && m < tid);
+      order[before] = tid;
+      chunks[before] = mine > 0 ? (mine + kC - 1) / kC : 0;
     }
     __syncthreads();
-    n = len_s[args.num_seqs];
-    __syncthreads();
+    if (kForm == kMixed) {
+      if (tid <= seqs && (tid <= args.most_narrow || (tid == seqs && args.all_narrow))) {
+        const int64_t k = tid;
+        int64_t in_narrow = 0, all = 0;
+        for (int m = 0; m < seqs; ++m) {
+          in_narrow += m < tid ? chunks[m] : 0;
+          all += chunks[m];
+        }
+        int64_t cost = 0;
+        if (args.HV * (kSlices * k + seqs - k) > args.sms) {
+          const int64_t sum = kSlices * (narrow_time(in_narrow) + narrow_time(0) * (k - 1)) +
+                              wide_time(all - in_narrow) + wide_time(0) * (seqs - k - 1);
+          cost = args.HV * sum / args.sms + (k < seqs ? wide_time(chunks[seqs - 1]) : narrow_time(chunks[seqs - 1]));
+        }
+        if (k > 0) cost = max(cost, narrow_time(chunks[0]));
+        if (k < seqs) cost = max(cost, wide_time(chunks[k]));
+        if (k > 0 && k < seqs) cost += cost / 12;
+        atomicMin(best, (unsigned long long)cost << 8 | (unsigned)tid);
+      }
+      __syncthreads();
+      narrow = (int)(*best & 255);
+    }
   }
+  int b = blockIdx.x;
+  if (b < narrow * kSlices * args.HV) {
+    s.columns = kDv;
+    s.slice = b % kSlices;
+    s.h = b / kSlices % args.HV;
+    s.n = b / kSlices / args.HV;
+  } else {
+    b -= narrow * kSlices * args.HV;
+    s.columns = kHeadDim;
+    s.slice = 0;
+    s.h = b % args.HV;
+    s.n = narrow + b / args.HV;
+  }
+  const bool some = s.n < seqs;
+  if (kForm == kMixed || args.longest_first) {
+    if (some) s.n = order[s.n];
+    __syncthreads();  // the lists lie where rows land
+  }
+  if (!some) asm volatile("griddepcontrol.wait;" ::: "memory");  // as in begin_unit
+  return some;
+}
+
+// The first steps of a state CTA: refusals (false: the whole CTA leaves),
+// barriers and TMEM.
+__device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* smem, Bars& bars, Unit& s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool reporter = tid == 0 && s.h == 0 && s.slice == 0;
+  const int n = s.n;
   const int L = seq_len(args, n);
   const int slot = args.state_idx[n];
   bool stop = L <= 0;
@@ -840,9 +913,9 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
     stop = true;
     if (slot != -1 && reporter) set_error(args.err_flag, KDA_DEVERR_SLOT);
     const int64_t t0 = seq_start(args, n);
-    const int pieces = columns / 8;
+    const int pieces = s.columns / 8;
     for (int64_t i = tid; i < (int64_t)L * pieces; i += kStateThreads)
-      *reinterpret_cast<uint4*>(args.o + ((t0 + i / pieces) * args.HV + s.h) * kHeadDim + s.slice * columns +
+      *reinterpret_cast<uint4*>(args.o + ((t0 + i / pieces) * args.HV + s.h) * kHeadDim + s.slice * kDv +
                                 (i % pieces) * 8) = make_uint4(0, 0, 0, 0);
   }
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
@@ -861,7 +934,6 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
   s.L = L;
   s.slot = slot;
   s.nch = (L + kC - 1) / kC;
-  s.n = n;
   if (!stop && bars.chunk0 + s.nch > args.max_chunks) {  // overlapping sequences have more chunks than tokens allow
     stop = true;
     if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
@@ -871,7 +943,7 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
     return false;
   }
 
-  tc::fence_async_smem();  // the lengths lay where rows land
+  tc::fence_async_smem();  // lists lay where rows land
   if (warp == kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
     bars.timed_out = 0;
@@ -969,19 +1041,12 @@ __device__ __forceinline__ bool load_records(const GdnPrefillArgs& args, uint8_t
   return ok;
 }
 
+// The narrow form: 32 value columns.
 template <bool F16>
-__global__ void __launch_bounds__(kStateThreads, 1)
-    gdn_state_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+__device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const GdnMaps& maps, uint8_t* smem, Bars& bars,
+                                            const Unit& s) {
   using C = Cfg<F16>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Unit s;
-  constexpr int kSlices = kHeadDim / kDv;
-  s.slice = blockIdx.x % kSlices;
-  s.h = blockIdx.x / kSlices % args.HV;
-  s.n = blockIdx.x / kSlices / args.HV;
-  if (!begin_unit(args, smem, bars, kDv, s)) return;
   const int h = s.h, L = s.L, nch = s.nch;
   const int64_t t0 = s.t0;
   const uint32_t tmem = bars.tmem;
@@ -1210,25 +1275,19 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   end_unit(args, bars, tmem, ok);
 }
 
+// The wide form: all value columns, transposed.
 template <bool F16>
-__global__ void __launch_bounds__(kStateThreads, 1)
-    gdn_state_wide_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+__device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnMaps& maps, uint8_t* smem, Bars& bars,
+                                          const Unit& s) {
   using C = Cfg<F16>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Bars& bars = *reinterpret_cast<Bars*>(smem + C::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Unit s;
-  s.slice = 0;
-  s.h = blockIdx.x % args.HV;
-  s.n = blockIdx.x / args.HV;
-  if (!begin_unit(args, smem, bars, kHeadDim, s)) return;
   const int h = s.h, L = s.L, nch = s.nch;
   const int64_t t0 = s.t0;
   const uint32_t tmem = bars.tmem;
   bool ok = true;
   if (warp < kChainWarps) {
-    // 768 threads start with 80 registers each; 640 at 88 and 128 at 40 are those 61440
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    // 768 threads start with 80 registers each; 512 at 96, 128 at 56 and 128 at 40 are those 61440
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // ---------------------------------------------------------------- chain
     // A warp that runs out of time goes on without waiting, so that the others
     // still meet it.
@@ -1342,7 +1401,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
       for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(root + 4 * j) = *reinterpret_cast<const float4*>(S + 4 * j);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // --------------------------------------------------------------- outputs
     // O = scale rq e^c Q S + P D, 32 value columns a warp, 64 tokens a thread.
     const int quad = warp & 3, odd = lane & 1;
@@ -1356,33 +1415,40 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       if (!(ok = warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u))) break;
       if (!(ok = warp_wait(&bars.o_full, (uint32_t)c & 1u))) break;
       tc::tc_fence_after();
-      uint32_t w[32];  // two tokens of one column each
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        uint32_t q[8], r[8];
-        tmem_ld8_async(lanes + kTmQ + 8 * g, q);
-        tmem_ld8_async(lanes + kTmO + 8 * g, r);
-        wait_ld(q);
-        wait_ld(r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 y = fma2(*reinterpret_cast<const float2*>(sc.o + 8 * g + 2 * j),
-                                make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])),
-                                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-          w[4 * g + j] = pack_out16x2<F16>(y.x, y.y);
-        }
-      }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        arrive(&bars.rec_free[sl]);
-        arrive(&bars.o_read);
-      }
       const int left = L - c * kC - odd;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {  // traded for two columns of one token each
-        const uint32_t x = __byte_perm(w[j], __shfl_xor_sync(0xffffffffu, w[j], 1), pick);
-        if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = x;
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[16];  // two tokens of one column each
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int tok = 32 * half + 8 * g;
+          uint32_t q[8], r[8];
+          tmem_ld8_async(lanes + kTmQ + tok, q);
+          tmem_ld8_async(lanes + kTmO + tok, r);
+          wait_ld(q);
+          wait_ld(r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = fma2(*reinterpret_cast<const float2*>(sc.o + tok + 2 * j),
+                                  make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])),
+                                  make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+            w[4 * g + j] = pack_out16x2<F16>(y.x, y.y);
+          }
+        }
+        if (half) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            arrive(&bars.rec_free[sl]);
+            arrive(&bars.o_read);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {  // traded for two columns of one token each
+          const int tok = 32 * half + 2 * j;
+          const uint32_t x = __byte_perm(w[j], __shfl_xor_sync(0xffffffffu, w[j], 1), pick);
+          if (tok < left) *reinterpret_cast<uint32_t*>(dst + tok * step) = x;
+        }
       }
     }
   } else if (warp == kMmaWarp) {
@@ -1497,6 +1563,19 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   end_unit(args, bars, tmem, ok);
 }
 
+template <bool F16, int kForm>
+__global__ void __launch_bounds__(kStateThreads, 1)
+    gdn_state_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + Cfg<F16>::kBars);
+  Unit s;
+  if (!pick_unit<kForm>(args, smem, s) || !begin_unit(args, smem, bars, s)) return;
+  if (kForm == kNarrow || (kForm == kMixed && s.columns == kDv))
+    narrow_unit<F16>(args, maps, smem, bars, s);
+  else
+    wide_unit<F16>(args, maps, smem, bars, s);
+}
+
 // Tensor map of a [T][heads][128] 16-bit tensor, box (64 elements, 1 head, 64
 // tokens) in 128-byte swizzled lines; tokens past the last land as zeros.
 bool encode_half_rows(CUtensorMap* m, const void* base, int64_t heads, int64_t T) {
@@ -1575,28 +1654,42 @@ kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t
   return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg<F16>::kSmem, F16, st, a, m);
 }
 
-template <bool F16>
-kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, bool wide, cudaStream_t st) {
+template <bool F16, int kForm>
+kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, int64_t grid, cudaStream_t st) {
   using C = Cfg<F16>;
-  static std::atomic<uint64_t> ready{0}, wide_ready{0};
-  static_assert(C::kSmem <= 232448 && kStateThreads == 768, "shared memory and registers of one CTA");
-  kda_status s = wide ? allow_smem(gdn_state_wide_kernel<F16>, C::kWideSmem, &wide_ready)
-                      : allow_smem(gdn_state_kernel<F16>, C::kSmem, &ready);
+  constexpr int smem = kForm == kWide ? C::kWideSmem : C::kSmem;
+  static std::atomic<uint64_t> ready{0};
+  static_assert(C::kSmem <= 232448 && C::kWideSmem <= C::kSmem && kStateThreads == 768, "shared memory and registers");
+  kda_status s = allow_smem(gdn_state_kernel<F16, kForm>, smem, &ready);
   if (s != KDA_OK) return s;
-  const int64_t grid = (int64_t)a.num_seqs * a.HV * (wide ? 1 : kHeadDim / kDv);
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return wide ? launch_after(gdn_state_wide_kernel<F16>, (unsigned)grid, kStateThreads, C::kWideSmem, true, st, a, m)
-              : launch_after(gdn_state_kernel<F16>, (unsigned)grid, kStateThreads, C::kSmem, true, st, a, m);
+  return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, smem, true, st, a, m);
 }
 
-constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred cycles for 8, two thousand for 128
-
-// The wide state kernel is taken from 3 / 2 (sequence, head) pairs per SM on.
-// Both sides, 16 heads (whole call, us; the other form in brackets): 8 sequences
-// of 2048 tokens 342 [241], 8 ragged ones with one of 8087 of 16980 tokens 343
-// [524], 16 of 2048 439 [596], 64 of 512 403 [642].  The lengths are on the
-// device; below the border one long sequence costs more than it saves.
-bool take_wide(int64_t heads, int sms) { return 2 * heads >= 3 * (int64_t)sms; }
+// All narrow where that fills the SMs twice at most: the narrow form by itself is
+// compiled without a register spill, for FP16 7% faster than in the mixed kernel
+// (1000, 333, 77 and 2001 tokens, 16 heads, 110 instead of 118 us; 4 x 1024 102
+// instead of 91).  Otherwise what the CTAs settle, since the lengths are on the
+// device.  All wide where there are too many sequences to rank,
+// or so many heads that narrow CTAs could not pay: they take 1.9 times as much of
+// the SMs, and CTAs that find no unit (as many as the launch has beyond those of
+// the choice) cost a microsecond each.
+template <bool F16>
+kda_status launch_states(GdnPrefillArgs a, const GdnMaps& m, cudaStream_t st) {
+  const int64_t heads = (int64_t)a.num_seqs * a.HV, slices = kHeadDim / kDv;
+  a.sms = sm_count();
+  if (a.sms <= 0) return KDA_ERR_CUDA;
+  if (heads * slices <= 2 * a.sms) {
+    a.longest_first = a.num_seqs <= kMaxSorted && heads * slices > a.sms;
+    return launch_state<F16, kNarrow>(a, m, heads * slices, st);
+  }
+  a.all_narrow = 2 * heads < 3 * a.sms;
+  a.most_narrow = (int)(a.sms / (slices * a.HV));
+  a.longest_first = a.num_seqs <= kMaxSorted && heads > a.sms;
+  if (a.num_seqs > kMaxSorted || (!a.all_narrow && a.most_narrow == 0)) return launch_state<F16, kWide>(a, m, heads, st);
+  const int64_t most = a.all_narrow ? a.num_seqs : a.most_narrow;
+  return launch_state<F16, kMixed>(a, m, heads + most * (slices - 1) * a.HV, st);
+}
 
 int64_t most_chunks(int num_seqs, int64_t total_tokens) { return total_tokens / kC + num_seqs; }
 
@@ -1679,13 +1772,7 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   s = f16 ? launch_chunks<true>(args, m, st) : launch_chunks<false>(args, m, st);
   if (s != KDA_OK) return s;
   record_stage(1, st);
-  const int sms = sm_count();
-  if (sms <= 0) return KDA_ERR_CUDA;
-  const int64_t heads = (int64_t)num_seqs * dims.HV;
-  const bool wide = take_wide(heads, sms);
-  // CTAs that do not all start at once: the longest sequences first
-  args.longest_first = num_seqs > 1 && num_seqs <= kMaxSorted && heads * (wide ? 1 : 4) > sms;
-  s = f16 ? launch_state<true>(args, m, wide, st) : launch_state<false>(args, m, wide, st);
+  s = f16 ? launch_states<true>(args, m, st) : launch_states<false>(args, m, st);
   record_stage(2, st);
   return s;
 }

@@ -249,6 +249,23 @@ def test_prefill_many_sequences(f16):
     assert torch.equal(pool2[s].cpu(), d["pool"][s])
 
 
+@pytest.mark.parametrize("lengths,H,HV", [
+    ([1500, 30, 64, 65, 0, 129, 1], 8, 16),   # one sequence by columns, the others whole heads
+    ([300, 1400, 90, 1301, 7, 200], 1, 8),    # two
+    ([130] * 12, 4, 16),                      # none
+    ([100, 33], 4, 64),                       # no sequence fits by columns
+    ([int(x) for x in np.random.default_rng(3).integers(0, 70, 140)], 1, 2),  # too many to rank
+])
+@pytest.mark.parametrize("f16", [False, True])
+def test_prefill_forms_of_the_state_pass(lengths, H, HV, f16):
+    d = make(16, sum(lengths), H, HV, len(lengths) + 1, f16=f16)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    inter = torch.full((sum(-(-L // 64) for L in lengths), HV, K, K), 9.0, device="cuda")
+    o, pool = prefill(d, lengths, err=err, intermediate=inter)
+    assert int(err) == 0
+    check_prefill(d, lengths, o, pool, intermediate=inter)
+
+
 def test_prefill_and_decode_in_a_graph():
     d = make(10, 130, 2, 4, 3)
     x = {n: d[n].cuda() for n in ("q", "k", "v", "a", "b", "idx")}
