@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     if (t < len) {
       const int64_t at = (t0 + t) * args.HV + h;
       b = in16_to_float<F16>(args.beta[at]);
-      g = scalar_log_decay_of(ga, scalar_gate_in<F16>(ga, args.a, at), -expf(a_log), bias);
+      g = scalar_log_decay<F16>(ga, scalar_gate_load(ga, args.a, at), -expf(a_log), bias);
       b = ga.beta_is_raw ? sigmoidf_(b) : b;
     }
     c_hi[t] = g;

@@ -106,29 +106,24 @@ __device__ __forceinline__ float fold_beta(const GateArgs& ga, float b_in) {
 // given.  neg_rate = -exp(A_log[h]), bias = dt_bias[h].  Below -128 the decay
 // is zero in FP32 and stays zero in any sum with other log-decays <= 0; the
 // cut keeps such sums finite (-inf - -inf) and lets a NaN through.
-__device__ __forceinline__ float scalar_log_decay_of(const ScalarGateArgs& ga, float a_in, float neg_rate, float bias) {
-  float g = a_in;
-  if (ga.A_log) {
-    const float x = a_in + bias;
-    g = neg_rate * (x > 20.f ? x : log1pf(expf(x)));  // softplus; past 20 it is x to 2^-28
-  }
-  return g < -128.f ? -128.f : g;
-}
-
-// What scalar_log_decay_of takes: 16-bit a, or FP32 log-decays.  Loaded without
-// a branch, so that the loads around it need not wait for its outcome.
-template <bool F16>
-__device__ __forceinline__ float scalar_gate_in(const ScalarGateArgs& ga, const void* a, int64_t at) {
+// The inputs, 16-bit a or FP32 log-decays, are loaded by scalar_gate_load
+// without a branch, so that other loads need not wait for its outcome.
+__device__ __forceinline__ ushort2 scalar_gate_load(const ScalarGateArgs& ga, const void* a, int64_t at) {
   const bool raw = ga.A_log != nullptr;
   const uint16_t* p = static_cast<const uint16_t*>(a) + (raw ? at : 2 * at);
-  const uint16_t lo = p[0], hi = p[raw ? 0 : 1];
-  return raw ? in16_to_float<F16>(lo) : __uint_as_float((uint32_t)hi << 16 | lo);
+  return make_ushort2(p[0], p[raw ? 0 : 1]);
 }
 
 template <bool F16>
-__device__ __forceinline__ float scalar_log_decay(const ScalarGateArgs& ga, const void* a, int64_t at, float neg_rate,
-                                                  float bias) {
-  return scalar_log_decay_of(ga, scalar_gate_in<F16>(ga, a, at), neg_rate, bias);
+__device__ __forceinline__ float scalar_log_decay(const ScalarGateArgs& ga, ushort2 in, float neg_rate, float bias) {
+  float g;
+  if (ga.A_log) {
+    const float x = in16_to_float<F16>(in.x) + bias;
+    g = neg_rate * (x > 20.f ? x : log1pf(expf(x)));  // softplus; past 20 it is x to 2^-28
+  } else {
+    g = __uint_as_float((uint32_t)in.y << 16 | in.x);
+  }
+  return g < -128.f ? -128.f : g;
 }
 
 // Packed FP32 pair arithmetic (sm_100+ f32x2 instructions).
