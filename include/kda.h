@@ -343,7 +343,7 @@ typedef struct {
  * start of every 64-token chunk.  workspace: kda_gdn_prefill_workspace_size
  * bytes, 16-byte aligned:
  *   (total_tokens / 64 + num_seqs) * HV * 33792      a record per (chunk, head)
- *   + 3 * align256(total_tokens * H * 256)           FP16 only: q, k as BF16
+ *   + 4 * align256(total_tokens * H * 256)           FP16 only: q, k in BF16 halves
  * (SIZE_MAX for more than INT32_MAX tokens).  The first call on each device
  * sets the kernels' shared-memory limits; make it before capturing calls into
  * a CUDA graph.

@@ -46,12 +46,12 @@
 // 2.8: sequences that the SMs would wait for are narrow, the rest are wide
 // (launch_states, pick_unit).
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
-// wherever the state depends on them, S, T, Y and D'.  K and Q are BF16 already.
-// FP16 keys are split exactly (11 bits into 8 + 8) and FP16 queries rounded to
-// BF16 by a pass over them before the kernels; FP16 operands would need S and D
-// in FP16 halves, whose range is not the state's.  So are P and D for the
+// wherever the state depends on them, S, T, Y and D'.  So are P and D for the
 // output: Q S and P D cancel where the state repeats what it is written, so that
-// one rounding of P to BF16 showed up as 2 per cent of the outputs' RMS.
+// one rounding of P to BF16 showed up as 2 per cent of the outputs' RMS.  K and Q
+// are BF16 already.  FP16 K and Q are taken as they are for [K; Q] K^T; beside S
+// and D', whose range is not FP16's, they are split exactly (11 bits into 8 + 8)
+// by a pass over them that runs beside the chunk kernel.
 #include <atomic>
 
 #include "kda_host.h"
@@ -88,7 +88,7 @@ struct GdnPrefillArgs {
 };
 
 struct GdnMaps {
-  CUtensorMap q, k, k_lo;
+  CUtensorMap q, k, q_lo, k_lo;
 };
 
 // What the state kernels read of a chunk beside T and P.
@@ -106,22 +106,16 @@ constexpr int kRecT = 0, kRecTlo = 8192, kRecP = 16384, kRecPlo = 24576, kRecSca
 static_assert(kRecScalars + sizeof(ChunkScalars) <= kRecBytes, "record");
 
 // Shared memory of the chunk kernel: [K; Q] as two halves of 64 channels and
-// 128 lines each, the low halves of FP16 keys, T and the scalars; P goes
-// straight to the record.  A's hi and lo halves take the place of K, and T's
-// that of Q, once their products are done.
-template <bool F16>
+// 128 lines each and the scalars; P goes straight to the record.  A's hi and lo
+// halves take the place of K, and T's that of Q, once their products are done.
 struct ChunkCfg {
-  static constexpr int kRowBytes = 32768 + (F16 ? 16384 : 0);
+  static constexpr int kRowBytes = 32768;
   static constexpr int kScalars = kRowBytes;  // 1024 bytes
   static constexpr int kGate = kScalars + 1024;  // float hi[64], lo[64], beta[64], rk[64]
   static constexpr int kBar = kGate + 4 * kC * 4;
-  // A's diagonal blocks in FP32: over the keys' low halves where there are any
-  static constexpr int kDiag = F16 ? 32768 : kBar + 64;
-  // (the product whose left operand are the 64 lines of K's low halves takes 128:
-  // its last 64 rows are whatever follows them, in bounds, and are not read back)
-  static constexpr int kSmem = F16 ? kRowBytes + 8192 : kBar + 64 + 4 * 16 * kLdG * 4;
-  static_assert(kBar + 64 <= kSmem, "regions");
-  static constexpr int kTmCols = F16 ? 128 : 64;
+  static constexpr int kDiag = kBar + 64;  // A's diagonal blocks in FP32
+  static constexpr int kSmem = kDiag + 4 * 16 * kLdG * 4;
+  static constexpr int kTmCols = 64;
   // per SM; five of 96 registers take 500 instead of 507 us for 8 x 4096 tokens,
   // but 133 instead of 115 for 1 x 4096 (16 heads, whole call)
   static constexpr int kCtas = 4;
@@ -149,8 +143,8 @@ constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred
 
 template <bool F16>
 struct Cfg {
-  static constexpr int kQ = 16384 * (F16 ? 2 : 1);  // K, low halves of FP16 keys, Q
-  static constexpr int kKeyBytes = kQ + 16384;
+  static constexpr int kQ = 16384 * (F16 ? 2 : 1);  // K and Q; each before its low halves if FP16
+  static constexpr int kKeyBytes = 2 * kQ;
   static constexpr int kKeys = F16 ? 2 : 3, kRecs = 2;     // chunks in shared memory: rows, records
   static constexpr int kRec = kKeys * kKeyBytes;
   static constexpr int kBars = kRec + kRecs * kRecBytes;
@@ -213,16 +207,6 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   split2(make_float2(x[2], x[3]), hi.y, lo.y);
   split2(make_float2(x[4], x[5]), hi.z, lo.z);
   split2(make_float2(x[6], x[7]), hi.w, lo.w);
-}
-
-__device__ __forceinline__ uint4 round8(const float* x) {
-  uint32_t h[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * p], x[2 * p + 1]);
-    h[p] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // 16-byte piece `piece` of 128-byte line `row` of a 128-byte-swizzled tile.
@@ -521,9 +505,9 @@ __device__ __forceinline__ void zero_rows(uint8_t* k, int half, int len, int t, 
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
+__global__ void __launch_bounds__(128, ChunkCfg::kCtas)
     gdn_chunk_kernel(const GdnPrefillArgs args, const __grid_constant__ GdnMaps maps) {
-  using C = ChunkCfg<F16>;
+  using C = ChunkCfg;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);  // rows landed, [K; Q] K^T done, TMEM address
   const int t = threadIdx.x, quad = t >> 5, lane = t & 31;
@@ -544,11 +528,16 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     tc::mbar_init(&bars[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // whoever waits for this kernel waits for the one that splits FP16 rows too
+  auto after_split = [] {
+    if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   auto leave = [&] {  // no chunk here: the grid is an upper bound
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     if (quad == 0) tc::tmem_dealloc(*reinterpret_cast<const uint32_t*>(&bars[2]), C::kTmCols);
+    after_split();
   };
   // the chunk's sequence: every warp walks over the sequences, 128 at a time
   int n = -1, c = 0;
@@ -580,7 +569,6 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     }
     base += __shfl_sync(0xffffffffu, run, 31);
   }
-  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");  // K and Q were split by the launch before
   if (n < 0) {
     leave();
     return;
@@ -595,7 +583,6 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     for (int a = 0; a < 2; ++a) {
       tma_box(kq + a * 16384, &maps.k, a * 64, hk, tok, &bars[0]);
       tma_box(kq + a * 16384 + 8192, &maps.q, a * 64, hk, tok, &bars[0]);
-      if (F16) tma_box(kq + 32768 + a * 8192, &maps.k_lo, a * 64, hk, tok, &bars[0]);
     }
   }
 
@@ -659,28 +646,17 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
   bool bad = !warp_wait(&bars[0], 0);
   if (len < kC) {
     zero_rows(kq, 16384, len, t, 128);
-    if (F16) zero_rows(kq + 32768, 8192, len, t, 128);
     tc::fence_async_smem();
     __syncthreads();
   }
   if (quad == 0 && !bad && elect_one()) {  // [K; Q] K^T
-    constexpr uint32_t kIdA = tc::idesc_bf16_f32(128, 64);
-    const uint64_t hi = tc::sw128_desc(tc::smem_u32(kq)), lo = tc::sw128_desc(tc::smem_u32(kq + 32768));
+    constexpr uint32_t kIdA = F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
+    const uint64_t op = tc::sw128_desc(tc::smem_u32(kq));
     tc::tc_fence_after();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint64_t off = ((j >> 2) * 16384 + (j & 3) * 32) >> 4;
-      tc::mma_bf16(tmem, hi + off, hi + off, kIdA, j > 0);
-    }
-    if constexpr (F16) {  // K = hi + lo: K hi K lo^T, Q K lo^T beside, and K lo K hi^T (rows 0..63) apart
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        tc::mma_bf16(tmem, hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4), lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4),
-                     kIdA, true);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        tc::mma_bf16(tmem + 64, lo + (((j >> 2) * 8192 + (j & 3) * 32) >> 4),
-                     hi + (((j >> 2) * 16384 + (j & 3) * 32) >> 4), kIdA, j > 0);
+      tc::mma_bf16(tmem, op + off, op + off, kIdA, j > 0);
     }
     tc::mma_commit(&bars[1]);
   }
@@ -697,15 +673,13 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     for (int p = 0; p < 8; ++p) {
       const uint4 w = *line16(kq + a * 16384, row, p);
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      uint4 w2 = make_uint4(0, 0, 0, 0);
-      if (F16 && krow) w2 = *line16(kq + 32768 + a * 8192, row, p);
-      const uint32_t ww2[4] = {w2.x, w2.y, w2.z, w2.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float f0 = __uint_as_float(ww[e] << 16), f1 = __uint_as_float(ww[e] & 0xffff0000u);
         if (F16) {
-          f0 += __uint_as_float(ww2[e] << 16);
-          f1 += __uint_as_float(ww2[e] & 0xffff0000u);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[e]));
+          f0 = f.x;
+          f1 = f.y;
         }
         ss[e] = fma2(make_float2(f0, f1), make_float2(f0, f1), ss[e]);
       }
@@ -736,12 +710,6 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     float d[16];
     if (16 * jb <= top) {
       tc::tmem_ld16(acc + 16 * jb, d);
-      if (F16 && krow) {
-        float d2[16];
-        tc::tmem_ld16(acc + 64 + 16 * jb, d2);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) d[e] += d2[e];
-      }
       float f[16];
 #pragma unroll
       for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(f + 4 * e) = *reinterpret_cast<const float4*>(rks + 16 * jb + 4 * e);
@@ -811,6 +779,7 @@ __global__ void __launch_bounds__(128, ChunkCfg<F16>::kCtas)
     tc::bulk_commit();
     tc::bulk_wait_read();
   }
+  after_split();
 }
 
 // What a state CTA works on.
@@ -997,7 +966,10 @@ __device__ __forceinline__ bool load_keys(const GdnPrefillArgs& args, const GdnM
       for (int a = 0; a < 2; ++a) {
         tma_box(key + a * 8192, &maps.k, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
         tma_box(key + C::kQ + a * 8192, &maps.q, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
-        if (F16) tma_box(key + 16384 + a * 8192, &maps.k_lo, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
+        if (F16) {
+          tma_box(key + 16384 + a * 8192, &maps.k_lo, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
+          tma_box(key + C::kQ + 16384 + a * 8192, &maps.q_lo, a * 64, s.h / args.G, (int)s.t0 + c * kC, &bars.key[sl]);
+        }
       }
     }
     __syncwarp();
@@ -1248,8 +1220,11 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       chain_await<false>(kBarSq);
       if (leader && ok) {  // Q S
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          tc::mma_bf16(tmem + kTmQ, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4), kId64, j > 0);
+        for (int b = 0; b < (F16 ? 2 : 1); ++b)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            tc::mma_bf16(tmem + kTmQ, q_op + ((b * 16384 + (j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4),
+                         kId64, b + j > 0);
         tc::mma_commit(&bars.xq_full);
         tc::mma_commit(&bars.key_free[ks]);
       }
@@ -1536,6 +1511,11 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
           for (int j = 0; j < 8; ++j)
             mma_ts(tmem + kTmQ, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64,
                    b + j > 0);
+        if constexpr (F16) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_ts(tmem + kTmQ, tmem + kTmS + 8 * j, q_op + ((16384 + (j >> 2) * 8192 + (j & 3) * 32) >> 4), kId64, true);
+        }
         tc::mma_commit(&bars.xq_full);
         tc::mma_commit(&bars.key_free[ks]);
       }
@@ -1590,26 +1570,23 @@ bool encode_half_rows(CUtensorMap* m, const void* base, int64_t heads, int64_t T
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// FP16 q and k as the BF16 operands of the kernel: keys as two halves, whose sum
-// is the key, queries rounded.  One 16-byte piece of each a thread.
+// FP16 q and k as operands of the state kernel: two BF16 halves whose sum they
+// are.  One 16-byte piece of each a thread.
 __global__ void __launch_bounds__(256) split_rows_kernel(const uint4* __restrict__ q, const uint4* __restrict__ k,
-                                                         int64_t n, uint4* q_hi, uint4* k_hi, uint4* k_lo) {
+                                                         int64_t n, uint4* q_hi, uint4* q_lo, uint4* k_hi, uint4* k_lo) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  const uint4 wq = __ldg(q + i), wk = __ldg(k + i);
-  const uint32_t a[4] = {wq.x, wq.y, wq.z, wq.w}, b[4] = {wk.x, wk.y, wk.z, wk.w};
-  float fq[8], fk[8];
+  auto split = [i](const uint4& w, uint4* hi, uint4* lo) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    fq[e] = in16_to_float<true>((uint16_t)(e & 1 ? a[e / 2] >> 16 : a[e / 2] & 0xffffu));
-    fk[e] = in16_to_float<true>((uint16_t)(e & 1 ? b[e / 2] >> 16 : b[e / 2] & 0xffffu));
-  }
-  uint4 hi, lo;
-  split8(fk, hi, lo);
-  q_hi[i] = round8(fq);
-  k_hi[i] = hi;
-  k_lo[i] = lo;
+    for (int e = 0; e < 8; ++e) f[e] = in16_to_float<true>((uint16_t)(e & 1 ? a[e / 2] >> 16 : a[e / 2] & 0xffffu));
+    split8(f, hi[i], lo[i]);
+  };
+  const uint4 wq = __ldg(q + i), wk = __ldg(k + i);
+  split(wq, q_hi, q_lo);
+  split(wk, k_hi, k_lo);
 }
 
 // Sets a kernel's shared-memory limit once per device.
@@ -1646,12 +1623,12 @@ kda_status launch_after(Kernel kernel, unsigned grid, unsigned threads, int smem
 template <bool F16>
 kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  static_assert(ChunkCfg<F16>::kCtas * (ChunkCfg<F16>::kSmem + 1024) <= 233472, "CTAs per SM");
-  kda_status s = allow_smem(gdn_chunk_kernel<F16>, ChunkCfg<F16>::kSmem, &ready);
+  static_assert(ChunkCfg::kCtas * (ChunkCfg::kSmem + 1024) <= 233472, "CTAs per SM");
+  kda_status s = allow_smem(gdn_chunk_kernel<F16>, ChunkCfg::kSmem, &ready);
   if (s != KDA_OK) return s;
   const int64_t grid = a.max_chunks * a.HV;
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg<F16>::kSmem, F16, st, a, m);
+  return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg::kSmem, F16, st, a, m);
 }
 
 template <bool F16, int kForm>
@@ -1693,7 +1670,7 @@ kda_status launch_states(GdnPrefillArgs a, const GdnMaps& m, cudaStream_t st) {
 
 int64_t most_chunks(int num_seqs, int64_t total_tokens) { return total_tokens / kC + num_seqs; }
 
-size_t split_bytes(const kda_dims& d, int64_t total_tokens) {  // one of q, k hi, k lo as BF16
+size_t split_bytes(const kda_dims& d, int64_t total_tokens) {  // a half of q or k as BF16
   return d.dtype == KDA_DTYPE_F16 ? ((size_t)total_tokens * d.H * kHeadDim * 2 + 255) / 256 * 256 : 0;
 }
 
@@ -1705,7 +1682,7 @@ using namespace kda;
 extern "C" size_t kda_gdn_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens) {
   if (num_seqs < 0 || total_tokens < 0 || dims.H <= 0 || dims.HV <= 0) return 0;
   if (total_tokens > INT32_MAX) return SIZE_MAX;  // refused; no capacity check may pass
-  return 3 * split_bytes(dims, total_tokens) + (size_t)most_chunks(num_seqs, total_tokens) * dims.HV * kRecBytes;
+  return 4 * split_bytes(dims, total_tokens) + (size_t)most_chunks(num_seqs, total_tokens) * dims.HV * kRecBytes;
 }
 
 extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
@@ -1753,23 +1730,27 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
   const bool f16 = dims.dtype == KDA_DTYPE_F16;
   const size_t part = split_bytes(dims, total_tokens);
   char* ws = static_cast<char*>(workspace);
-  args.records = reinterpret_cast<uint8_t*>(ws + 3 * part);
+  args.records = reinterpret_cast<uint8_t*>(ws + 4 * part);
   args.max_chunks = most_chunks(num_seqs, total_tokens);
-  GdnMaps m{};
-  if (!encode_half_rows(&m.q, f16 ? static_cast<const void*>(ws) : q, dims.H, total_tokens) ||
-      !encode_half_rows(&m.k, f16 ? static_cast<const void*>(ws + part) : k, dims.H, total_tokens) ||
-      (f16 && !encode_half_rows(&m.k_lo, ws + 2 * part, dims.H, total_tokens)))
+  GdnMaps rows{}, m{};  // of the chunk kernel, which takes q and k as they are, and of the state kernel
+  if (!encode_half_rows(&rows.q, q, dims.H, total_tokens) || !encode_half_rows(&rows.k, k, dims.H, total_tokens))
+    return KDA_ERR_CUDA;
+  m = rows;
+  if (f16 && (!encode_half_rows(&m.q, ws, dims.H, total_tokens) || !encode_half_rows(&m.q_lo, ws + part, dims.H, total_tokens) ||
+              !encode_half_rows(&m.k, ws + 2 * part, dims.H, total_tokens) ||
+              !encode_half_rows(&m.k_lo, ws + 3 * part, dims.H, total_tokens)))
     return KDA_ERR_CUDA;
   record_stage(0, st);
   if (f16) {
     const int64_t n = total_tokens * dims.H * (kHeadDim / 8);
     split_rows_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
         reinterpret_cast<const uint4*>(q), reinterpret_cast<const uint4*>(k), n, reinterpret_cast<uint4*>(ws),
-        reinterpret_cast<uint4*>(ws + part), reinterpret_cast<uint4*>(ws + 2 * part));
+        reinterpret_cast<uint4*>(ws + part), reinterpret_cast<uint4*>(ws + 2 * part),
+        reinterpret_cast<uint4*>(ws + 3 * part));
     s = launch_status();
     if (s != KDA_OK) return s;
   }
-  s = f16 ? launch_chunks<true>(args, m, st) : launch_chunks<false>(args, m, st);
+  s = f16 ? launch_chunks<true>(args, rows, st) : launch_chunks<false>(args, rows, st);
   if (s != KDA_OK) return s;
   record_stage(1, st);
   s = f16 ? launch_states<true>(args, m, st) : launch_states<false>(args, m, st);

@@ -79,6 +79,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// The same with FP16 A/B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return idesc_bf16_f32(M, N) & ~((1u << 7) | (1u << 10));
+}
+
 // Instruction descriptor of kind::tf32: TF32 A/B, FP32 accumulator, both
 // operands K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_tf32_f32(int M, int N) {

@@ -41,7 +41,7 @@ def test_gdn_host_errors(lib):
     assert pre(T=0, gb=0) == kda.KDA_OK  # nothing to do
     f16 = kda.dims(16, dtype=kda.KDA_DTYPE_F16)
     assert kda.kda_gdn_prefill_workspace_size(kda.dims(16), 3, 100) == 4 * 16 * 33792
-    assert kda.kda_gdn_prefill_workspace_size(f16, 3, 100) == 4 * 16 * 33792 + 3 * 100 * 16 * 256
+    assert kda.kda_gdn_prefill_workspace_size(f16, 3, 100) == 4 * 16 * 33792 + 4 * 100 * 16 * 256
     assert kda.kda_gdn_prefill_workspace_size(kda.dims(16), 1, 2 ** 31) == 2 ** 64 - 1
     assert pre(ws=None) == pre(ws_bytes=2 * 16 * 33792 - 1) == kda.KDA_ERR_WORKSPACE
     assert pre(d=f16, ws_bytes=2 * 16 * 33792) == kda.KDA_ERR_WORKSPACE
