@@ -34,6 +34,7 @@
 //     halves beside each other in one 64-wide tile: one product each for both.
 //     M = 64 spreads the token rows over all four warp quadrants of TMEM, 16
 //     lanes each, read in the fragment layout so that all 32 threads work.
+//     thin, thinnest: the same with 16 and 8 value columns, 8 and 4 chain warps.
 //   wide, a CTA per (sequence, value head), transposed:
 //       X^T  = S^T K^T     128 x 64 x 128
 //       D^T  = Y^T T^T     128 x 64 x 64
@@ -42,9 +43,13 @@
 //     makes is the next one's left operand, taken from TMEM: a thread's lane of
 //     the accumulator becomes its lane of the operand, and nothing of the chain
 //     passes through shared memory.
-// The first takes a chunk in 1.5 us, the second four times as many columns in
-// 2.8: sequences that the SMs would wait for are narrow, the rest are wide
-// (launch_states, pick_unit).
+// A chunk takes 1.5 us in the narrow form, 1.2 in the thin one, 1.0 in the
+// thinnest and 2.8 in the wide one, which does four times as many columns as the
+// first: sequences that the SMs would wait for are as thin as they leave room
+// for, the rest are wide (launch_states, pick_unit).
+// Measured (whole call, in a graph): 1 x 4096 tokens, 16 heads, 95.5 us (8 heads
+// 78), of which the chunk kernel 18; 8 x 4096 314; 16980 tokens in 8 sequences
+// with one of 8087 260; 1 x 128, 4 heads 11.
 // Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
 // wherever the state depends on them, S, T, Y and D'.  So are P and D for the
 // output: Q S and P D cancel where the state repeats what it is written, so that
@@ -138,7 +143,7 @@ constexpr int kMmaWarp = kChainWarps + kOutWarps, kSideWarp = kMmaWarp + 1, kKey
               kRecWarp = kMmaWarp + 3, kStateThreads = (kRecWarp + 1) * 32;
 
 // Forms of the state kernel.
-enum { kNarrow, kWide, kMixed };
+enum { kThinnest, kThin, kNarrow, kWide, kMixed };
 constexpr int kMaxSorted = 128;  // sequences a CTA ranks by length: two hundred cycles for 8, two thousand for 128
 
 template <bool F16>
@@ -256,21 +261,37 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
 }
 
 constexpr int kDv = 32;  // value columns of a narrow CTA
+constexpr int kThinDv = 16, kThinnestDv = 8;  // and of the thin ones
 
-// A row's values as operand halves: columns [8 part, 8 part + 8) of the CTA's, in a
-// tile [hi | lo].
+// Operand tiles [hi | lo] of DV + DV value columns: piece `piece` of line `row`.
+template <int DV>
+__device__ __forceinline__ uint8_t* tile16(uint8_t* tile, int row, int piece) {
+  const int turn = DV == 32 ? row & 7 : DV == 16 ? (row >> 1) & 3 : (row >> 2) & 1;
+  return tile + row * 4 * DV + ((piece ^ turn) << 4);
+}
+template <int DV>
+__device__ __forceinline__ uint64_t tile_desc(uint8_t* tile) {
+  if constexpr (DV == 32)
+    return tc::sw128_desc_mn(tc::smem_u32(tile), 0);
+  else
+    return tc::sw_desc_mn<2 * DV>(tc::smem_u32(tile));
+}
+
+// A row's values as operand halves: columns [8 part, 8 part + 8) of the CTA's.
+template <int DV>
 __device__ __forceinline__ void put_split(uint8_t* tile, int row, int part, const float (&x)[8]) {
   uint4 hi, lo;
   split8(x, hi, lo);
-  *line16(tile, row, part) = hi;
-  *line16(tile, row, 4 + part) = lo;
+  *reinterpret_cast<uint4*>(tile16<DV>(tile, row, part)) = hi;
+  *reinterpret_cast<uint4*>(tile16<DV>(tile, row, DV / 8 + part)) = lo;
 }
 
 // A warp's 8 accumulator columns: the hi product's plus the lo product's.
+template <int DV>
 __device__ __forceinline__ void get_acc(uint32_t taddr, int part, float (&x)[8]) {
   uint32_t a[8], b[8];
   tmem_ld8_async(taddr + part * 8, a);
-  tmem_ld8_async(taddr + 32 + part * 8, b);
+  tmem_ld8_async(taddr + DV + part * 8, b);
   wait_ld(a);
   wait_ld(b);
 #pragma unroll
@@ -289,10 +310,11 @@ __device__ __forceinline__ void ld_frag8(uint32_t taddr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
 }
+template <int DV>
 __device__ __forceinline__ void get_rows(uint32_t taddr, int part, float2 (&x)[2]) {
   uint32_t a[4], b[4];
   ld_frag8(taddr + part * 8, a);
-  ld_frag8(taddr + 32 + part * 8, b);
+  ld_frag8(taddr + DV + part * 8, b);
   wait_ld(a);
   wait_ld(b);
 #pragma unroll
@@ -300,15 +322,15 @@ __device__ __forceinline__ void get_rows(uint32_t taddr, int part, float2 (&x)[2
     x[e] = add2(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
                 make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])));
 }
+template <int DV>
 __device__ __forceinline__ void put_rows(uint8_t* tile, int row, int part, int lane, const float2 (&x)[2]) {
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     uint32_t hi, lo;
     split2(x[e], hi, lo);
-    const int rr = row + 8 * e;
-    uint8_t* line = tile + rr * 128 + 4 * (lane & 3);
-    *reinterpret_cast<uint32_t*>(line + ((part ^ (rr & 7)) << 4)) = hi;
-    *reinterpret_cast<uint32_t*>(line + (((4 + part) ^ (rr & 7)) << 4)) = lo;
+    const int at = 4 * (lane & 3);
+    *reinterpret_cast<uint32_t*>(tile16<DV>(tile, row + 8 * e, part) + at) = hi;
+    *reinterpret_cast<uint32_t*>(tile16<DV>(tile, row + 8 * e, DV / 8 + part) + at) = lo;
   }
 }
 
@@ -316,18 +338,22 @@ __device__ __forceinline__ void put_rows(uint8_t* tile, int row, int part, int l
 // wait for them at a hardware barrier, which wakes them sooner than an mbarrier
 // would and costs the chain one instruction.  kBarSq: S, for Q S.
 enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6 };
-template <bool TMEM>
+template <int WARPS>
+__device__ __forceinline__ void barrier_arrive(int id) {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(32 * (WARPS + 1)) : "memory");
+}
+template <bool TMEM, int WARPS>
 __device__ __forceinline__ void chain_arrive(int id) {
   if (TMEM) wait_st();
   tc::tc_fence_before();
-  asm volatile("barrier.cta.arrive %0, 544;" ::"r"(id) : "memory");
+  barrier_arrive<WARPS>(id);
 }
 // For operands in shared memory the fence between the chain's writes and the
 // tensor core's reads stands here, behind the barrier, in the issuing warp alone:
 // in front of it, in every chain warp, it took about 280 cycles of each stage.
-template <bool TMEM>
+template <bool TMEM, int WARPS>
 __device__ __forceinline__ void chain_await(int id) {
-  asm volatile("barrier.cta.sync %0, 544;" ::"r"(id) : "memory");
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(32 * (WARPS + 1)) : "memory");
   if (!TMEM) tc::fence_async_smem();
   tc::tc_fence_after();
 }
@@ -785,7 +811,7 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
 // What a state CTA works on.
 struct Unit {
   int h, slice, n;
-  int columns;  // kDv: the narrow form, kHeadDim: the wide one
+  int columns;  // value columns: kThinnestDv, kThinDv, kDv, or kHeadDim in the wide form
   int L, nch, slot;
   int64_t t0;
 };
@@ -799,14 +825,15 @@ __device__ __forceinline__ int64_t wide_time(int64_t chunks) { return 62 * chunk
 // the narrow form; every CTA finds the k of the least estimate of the whole: the
 // longest CTA, and, where not all start at once, all CTAs' time over the SMs and
 // the last one behind it.  Wide CTAs beside narrow ones slow these down, by a
-// twelfth in the estimate.  All narrow, all wide and the mix of one k, whole call,
-// 16 heads (us): 8087 and seven shorter of 16980 tokens 284, 524, 292; 8 x 4096
-// 507, 341, -; 4000 twice and 2000 three times 237, -, 275.
+// twelfth in the estimate.  All narrow, all wide (both in kernels of their own)
+// and the choice, whole call, 16 heads (us): 8087 and seven shorter of 16980 tokens
+// 256, 407, 260; 8 x 4096 506, 308, 314; 8000 and 20 x 200 239, 389, 249; 64 x 512
+// 569, 354, 367; 8000 and 20 x 1000, L2 cold, 459, 484, 351.
 template <int kForm>
 __device__ __forceinline__ bool pick_unit(const GdnPrefillArgs& args, uint8_t* smem, Unit& s) {
-  constexpr int kSlices = kHeadDim / kDv;
+  constexpr int kCols = kForm == kThinnest ? kThinnestDv : kForm == kThin ? kThinDv : kDv, kSlices = kHeadDim / kCols;
   const int tid = threadIdx.x, seqs = args.num_seqs;
-  int narrow = kForm == kNarrow ? seqs : 0;
+  int narrow = kForm == kWide || kForm == kMixed ? 0 : seqs;
   int* order = reinterpret_cast<int*>(smem);
   if (kForm == kMixed || args.longest_first) {
     int* len_s = order + kMaxSorted;
@@ -848,7 +875,7 @@ __device__ __forceinline__ bool pick_unit(const GdnPrefillArgs& args, uint8_t* s
   }
   int b = blockIdx.x;
   if (b < narrow * kSlices * args.HV) {
-    s.columns = kDv;
+    s.columns = kCols;
     s.slice = b % kSlices;
     s.h = b / kSlices % args.HV;
     s.n = b / kSlices / args.HV;
@@ -884,7 +911,7 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
     const int64_t t0 = seq_start(args, n);
     const int pieces = s.columns / 8;
     for (int64_t i = tid; i < (int64_t)L * pieces; i += kStateThreads)
-      *reinterpret_cast<uint4*>(args.o + ((t0 + i / pieces) * args.HV + s.h) * kHeadDim + s.slice * kDv +
+      *reinterpret_cast<uint4*>(args.o + ((t0 + i / pieces) * args.HV + s.h) * kHeadDim + s.slice * s.columns +
                                 (i % pieces) * 8) = make_uint4(0, 0, 0, 0);
   }
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
@@ -1013,8 +1040,8 @@ __device__ __forceinline__ bool load_records(const GdnPrefillArgs& args, uint8_t
   return ok;
 }
 
-// The narrow form: 32 value columns.
-template <bool F16>
+// The narrow and the thin form: DV value columns.
+template <bool F16, int DV>
 __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const GdnMaps& maps, uint8_t* smem, Bars& bars,
                                             const Unit& s) {
   using C = Cfg<F16>;
@@ -1023,15 +1050,16 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
   const int64_t t0 = s.t0;
   const uint32_t tmem = bars.tmem;
   bool ok = true;
-  if (warp < kChainWarps) {
+  constexpr int kParts = DV / 8, kWarps = 4 * kParts;  // chain warps
+  if (warp < kWarps) {
     // ---------------------------------------------------------------- chain
     // A warp that runs out of time goes on without waiting, so that the others
     // still meet it.
     const int quad = warp & 3, part = warp >> 2;
     const int row = 16 * quad + (lane >> 2);  // token rows row and row + 8 of the chunk, columns
-    const int colx = s.slice * kDv + part * 8 + 2 * (lane & 3);  // colx and colx + 1 of those
+    const int colx = s.slice * DV + part * 8 + 2 * (lane & 3);  // colx and colx + 1 of those
     const int dk = 32 * quad + lane;          // key channel of the state,
-    const int col0 = s.slice * kDv + part * 8;  // its columns col0 ..
+    const int col0 = s.slice * DV + part * 8;  // its columns col0 ..
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     float* root = args.pool + (((size_t)s.slot * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
     float S[8];
@@ -1051,9 +1079,9 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
     for (int c = 0; c < nch; ++c) {
       const int sl = c % C::kRecs;
       const uint32_t cp = (uint32_t)c & 1u;
-      put_split(smem + C::kS, dk, part, S);
-      chain_arrive<false>(kBarS);
-      asm volatile("barrier.cta.arrive %0, 544;" ::"r"((int)kBarSq) : "memory");
+      put_split<DV>(smem + C::kS, dk, part, S);
+      chain_arrive<false, kWarps>(kBarS);
+      barrier_arrive<kWarps>(kBarSq);
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
@@ -1071,7 +1099,7 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       chain_wait(&bars.x_full, cp, ok);
       tc::tc_fence_after();
       float2 x[2], y[2];
-      get_rows(lanes + kTmX, part, x);
+      get_rows<DV>(lanes + kTmX, part, x);
       // Y = v - r e^c (K S)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -1082,22 +1110,22 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
           v = make_float2(__uint_as_float(vraw[e] << 16), __uint_as_float(vraw[e] & 0xffff0000u));
         x[e] = fma2(make_float2(fa[e], fa[e]), x[e], v);
       }
-      put_rows(smem + C::kY, row, part, lane, x);
-      chain_arrive<false>(kBarY);
+      put_rows<DV>(smem + C::kY, row, part, lane, x);
+      chain_arrive<false, kWarps>(kBarY);
       if (c + 1 < nch) load_v(c + 1);
       chain_wait(&bars.d_full, cp, ok);
       tc::tc_fence_after();
-      get_rows(lanes + kTmX, part, x);
+      get_rows<DV>(lanes + kTmX, part, x);
 #pragma unroll
       for (int e = 0; e < 2; ++e) y[e] = mul2(make_float2(fs[e], fs[e]), x[e]);
-      put_rows(smem + C::kY, row, part, lane, y);
-      chain_arrive<false>(kBarDs);
-      put_rows(smem + C::kD, row, part, lane, x);
-      chain_arrive<false>(kBarD);
+      put_rows<DV>(smem + C::kY, row, part, lane, y);
+      chain_arrive<false, kWarps>(kBarDs);
+      put_rows<DV>(smem + C::kD, row, part, lane, x);
+      chain_arrive<false, kWarps>(kBarD);
       chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
       float u[8];
-      get_acc(lanes + kTmU, part, u);
+      get_acc<DV>(lanes + kTmU, part, u);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const float2 n2 = fma2(make_float2(last, last), make_float2(S[j], S[j + 1]), make_float2(u[j], u[j + 1]));
@@ -1108,13 +1136,13 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
     if (ok)
 #pragma unroll
       for (int j = 0; j < 8; ++j) root[j * kHeadDim] = S[j];
-  } else if (warp < kMmaWarp) {
+  } else if (warp >= kChainWarps && warp < kMmaWarp) {
     // --------------------------------------------------------------- outputs
     // O = scale rq e^c Q S + P D, 16 token rows a warp.
     const int quad = warp & 3;
     const int row = 16 * quad + (lane >> 2);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + s.slice * kDv + 2 * (lane & 3);
+    kda_bf16* dst = args.o + ((t0 + row) * args.HV + h) * kHeadDim + s.slice * DV + 2 * (lane & 3);
     const int64_t step = (int64_t)args.HV * kHeadDim;
     for (int c = 0; c < nch; ++c, dst += kC * step) {
       const int sl = c % C::kRecs;
@@ -1125,12 +1153,12 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       if (lane == 0) arrive(&bars.rec_free[sl]);
       if (!(ok = warp_wait(&bars.o_full, (uint32_t)c & 1u))) break;
       tc::tc_fence_after();
-      uint32_t w[4][2];
+      uint32_t w[kParts][2];
 #pragma unroll
-      for (int part = 0; part < 4; ++part) {
+      for (int part = 0; part < kParts; ++part) {
         float2 x[2], u[2];
-        get_rows(lanes + kTmQ, part, x);
-        get_rows(lanes + kTmO, part, u);
+        get_rows<DV>(lanes + kTmQ, part, x);
+        get_rows<DV>(lanes + kTmO, part, u);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float2 y = fma2(make_float2(fo[e], fo[e]), x[e], u[e]);
@@ -1144,17 +1172,17 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       for (int e = 0; e < 2; ++e)
         if (c * kC + row + 8 * e < L) {
 #pragma unroll
-          for (int part = 0; part < 4; ++part)
+          for (int part = 0; part < kParts; ++part)
             *reinterpret_cast<uint32_t*>(dst + 8 * e * step + 8 * part) = w[part][e];
         }
     }
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------- the chain's products
     // As the chain warps, it goes on without waiting once out of time.
-    constexpr uint32_t kId64 = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
-    constexpr uint32_t kIdU = tc::idesc_bf16_f32(128, 64) | tc::kIdescMnA | tc::kIdescMnB;
-    const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
-    const uint64_t y_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kY), 0);
+    constexpr uint32_t kId64 = tc::idesc_bf16_f32(64, 2 * DV) | tc::kIdescMnB;
+    constexpr uint32_t kIdU = tc::idesc_bf16_f32(128, 2 * DV) | tc::kIdescMnA | tc::kIdescMnB;
+    const uint64_t s_op = tile_desc<DV>(smem + C::kS);
+    const uint64_t y_op = tile_desc<DV>(smem + C::kY);
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
       const int ks = c % C::kKeys, sl = c % C::kRecs;
@@ -1164,13 +1192,13 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecBytes));
       ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
-      chain_await<false>(kBarS);
+      chain_await<false, kWarps>(kBarS);
       if (leader && ok) {  // X = K S
 #pragma unroll
         for (int b = 0; b < (F16 ? 2 : 1); ++b)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmX, (b ? kl_op : k_op) + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4),
+            tc::mma_bf16(tmem + kTmX, (b ? kl_op : k_op) + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 64 * DV) >> 4),
                          kId64, b + j > 0);
         tc::mma_commit(&bars.x_full);
       }
@@ -1178,23 +1206,23 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       // behind D, the chain overwrites what P D of the last chunk reads
       if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);
-      chain_await<false>(kBarY);
+      chain_await<false, kWarps>(kBarY);
       if (leader && ok) {  // D = T Y
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmX, t_op + (((b ? kRecTlo : 0) + j * 32) >> 4), y_op + ((j * 2048) >> 4), kId64, b + j > 0);
+            tc::mma_bf16(tmem + kTmX, t_op + (((b ? kRecTlo : 0) + j * 32) >> 4), y_op + ((j * 64 * DV) >> 4), kId64, b + j > 0);
         tc::mma_commit(&bars.d_full);
       }
       __syncwarp();
-      chain_await<false>(kBarDs);
+      chain_await<false, kWarps>(kBarDs);
       if (leader && ok) {  // dS = K^T D'
 #pragma unroll
         for (int b = 0; b < (F16 ? 2 : 1); ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmU, (b ? klt_op : kt_op) + ((j * 2048) >> 4), y_op + ((j * 2048) >> 4), kIdU, b + j > 0);
+            tc::mma_bf16(tmem + kTmU, (b ? klt_op : kt_op) + ((j * 2048) >> 4), y_op + ((j * 64 * DV) >> 4), kIdU, b + j > 0);
         tc::mma_commit(&bars.key_free[ks]);
       }
       __syncwarp();
@@ -1206,9 +1234,9 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
   } else if (warp == kSideWarp) {
     // ----------------------------------------- products for the output alone
     // As the chain warps, it goes on without waiting once out of time.
-    constexpr uint32_t kId64 = tc::idesc_bf16_f32(64, 64) | tc::kIdescMnB;
-    const uint64_t s_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kS), 0);
-    const uint64_t d_op = tc::sw128_desc_mn(tc::smem_u32(smem + C::kD), 0);
+    constexpr uint32_t kId64 = tc::idesc_bf16_f32(64, 2 * DV) | tc::kIdescMnB;
+    const uint64_t s_op = tile_desc<DV>(smem + C::kS);
+    const uint64_t d_op = tile_desc<DV>(smem + C::kD);
     const bool leader = elect_one();
     for (int c = 0; c < nch; ++c) {
       const int ks = c % C::kKeys, sl = c % C::kRecs;
@@ -1217,25 +1245,25 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       if (c > 0) ok = ok && warp_wait(&bars.o_read, (uint32_t)(c - 1) & 1u);
-      chain_await<false>(kBarSq);
+      chain_await<false, kWarps>(kBarSq);
       if (leader && ok) {  // Q S
 #pragma unroll
         for (int b = 0; b < (F16 ? 2 : 1); ++b)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            tc::mma_bf16(tmem + kTmQ, q_op + ((b * 16384 + (j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 2048) >> 4),
+            tc::mma_bf16(tmem + kTmQ, q_op + ((b * 16384 + (j >> 2) * 8192 + (j & 3) * 32) >> 4), s_op + ((j * 64 * DV) >> 4),
                          kId64, b + j > 0);
         tc::mma_commit(&bars.xq_full);
         tc::mma_commit(&bars.key_free[ks]);
       }
       __syncwarp();
-      chain_await<false>(kBarD);  // the chain is also past T and this chunk's scalars
+      chain_await<false, kWarps>(kBarD);  // the chain is also past T and this chunk's scalars
       if (leader && ok) {  // P D
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO, p_op + (((b ? kRecPlo - kRecP : 0) + j * 32) >> 4), d_op + ((j * 2048) >> 4), kId64,
+            tc::mma_bf16(tmem + kTmO, p_op + (((b ? kRecPlo - kRecP : 0) + j * 32) >> 4), d_op + ((j * 64 * DV) >> 4), kId64,
                          b + j > 0);
         tc::mma_commit(&bars.o_full);
         tc::mma_commit(&bars.rec_free[sl]);
@@ -1244,7 +1272,7 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
     }
   } else if (warp == kKeyWarp) {
     ok = load_keys<F16>(args, maps, smem, bars, s, lane);
-  } else {
+  } else if (warp == kRecWarp) {
     ok = load_records<F16>(args, smem, bars, s);
   }
   end_unit(args, bars, tmem, ok);
@@ -1294,8 +1322,8 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       const uint32_t cp = (uint32_t)c & 1u;
       put_split16(lanes + kTmS + 16 * part, lanes + kTmSlo + 16 * part, S);
       put_split16(lanes + kTmS + 16 * part + 8, lanes + kTmSlo + 16 * part + 8, S + 16);
-      chain_arrive<true>(kBarS);
-      asm volatile("barrier.cta.arrive %0, 544;" ::"r"((int)kBarSq) : "memory");
+      chain_arrive<true, kChainWarps>(kBarS);
+      barrier_arrive<kChainWarps>(kBarSq);
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
@@ -1334,7 +1362,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
         }
       }
       put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, x);
-      chain_arrive<true>(kBarY);
+      chain_arrive<true, kChainWarps>(kBarY);
       if (c + 1 < nch) load_v(c + 1);
       chain_wait(&bars.d_full, cp, ok);
       tc::tc_fence_after();
@@ -1353,9 +1381,9 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
         }
         put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, y);
       }
-      chain_arrive<true>(kBarDs);
+      chain_arrive<true, kChainWarps>(kBarDs);
       put_split16(lanes + kTmX + tok0, lanes + kTmX + tok0 + 8, x);  // over this warp's quarter of D
-      chain_arrive<true>(kBarD);
+      chain_arrive<true, kChainWarps>(kBarD);
       chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
 #pragma unroll
@@ -1442,7 +1470,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
       if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);  // X takes the place of the last D
-      chain_await<true>(kBarS);
+      chain_await<true, kChainWarps>(kBarS);
       if (leader && ok) {  // X^T = S^T K^T
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -1459,7 +1487,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       }
       __syncwarp();
       ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
-      chain_await<true>(kBarY);
+      chain_await<true, kChainWarps>(kBarY);
       if (leader && ok) {  // D^T = Y^T T^T: hi hi, lo hi, hi lo
 #pragma unroll
         for (int b = 0; b < 3; ++b)
@@ -1470,7 +1498,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
         tc::mma_commit(&bars.d_full);
       }
       __syncwarp();
-      chain_await<true>(kBarDs);
+      chain_await<true, kChainWarps>(kBarDs);
       if (leader && ok) {  // dS^T = D'^T K
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -1503,7 +1531,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       ok = ok && warp_wait(&bars.rec[sl], (uint32_t)(c / C::kRecs) & 1u);
       if (c > 0) ok = ok && warp_wait(&bars.o_read, (uint32_t)(c - 1) & 1u);
-      chain_await<true>(kBarSq);
+      chain_await<true, kChainWarps>(kBarSq);
       if (leader && ok) {  // S^T Q^T
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -1520,7 +1548,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
         tc::mma_commit(&bars.key_free[ks]);
       }
       __syncwarp();
-      chain_await<true>(kBarD);  // the chain is also past T and this chunk's scalars
+      chain_await<true, kChainWarps>(kBarD);  // the chain is also past T and this chunk's scalars
       if (leader && ok) {  // D^T P^T
 #pragma unroll
         for (int b = 0; b < 3; ++b)  // hi hi, lo hi, hi lo
@@ -1550,8 +1578,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   Bars& bars = *reinterpret_cast<Bars*>(smem + Cfg<F16>::kBars);
   Unit s;
   if (!pick_unit<kForm>(args, smem, s) || !begin_unit(args, smem, bars, s)) return;
-  if (kForm == kNarrow || (kForm == kMixed && s.columns == kDv))
-    narrow_unit<F16>(args, maps, smem, bars, s);
+  if (kForm == kThinnest)
+    narrow_unit<F16, kThinnestDv>(args, maps, smem, bars, s);
+  else if (kForm == kThin)
+    narrow_unit<F16, kThinDv>(args, maps, smem, bars, s);
+  else if (kForm == kNarrow || (kForm == kMixed && s.columns == kDv))
+    narrow_unit<F16, kDv>(args, maps, smem, bars, s);
   else
     wide_unit<F16>(args, maps, smem, bars, s);
 }
@@ -1643,11 +1675,12 @@ kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, int64_t grid,
   return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, smem, true, st, a, m);
 }
 
-// All narrow where that fills the SMs twice at most: the narrow form by itself is
-// compiled without a register spill, for FP16 7% faster than in the mixed kernel
-// (1000, 333, 77 and 2001 tokens, 16 heads, 110 instead of 118 us; 4 x 1024 102
-// instead of 91).  Otherwise what the CTAs settle, since the lengths are on the
-// device.  All wide where there are too many sequences to rank,
+// As thin as lets all CTAs start at once: 1 x 4096 tokens, 16 heads, thin 95.5 us,
+// narrow 115; 8 heads, thinnest 78, thin 84, narrow 104.  All narrow where that
+// fills the SMs twice at most: compiled by itself it spills no register, so that
+// 1000, 333, 77 and 2001 FP16 tokens, 16 heads, take 89 us, in the mixed kernel 101
+// (4 x 1024, the other way: 74, 71).  Otherwise what the CTAs settle, since the
+// lengths are on the device.  All wide where there are too many sequences to rank,
 // or so many heads that narrow CTAs could not pay: they take 1.9 times as much of
 // the SMs, and CTAs that find no unit (as many as the launch has beyond those of
 // the choice) cost a microsecond each.
@@ -1656,6 +1689,9 @@ kda_status launch_states(GdnPrefillArgs a, const GdnMaps& m, cudaStream_t st) {
   const int64_t heads = (int64_t)a.num_seqs * a.HV, slices = kHeadDim / kDv;
   a.sms = sm_count();
   if (a.sms <= 0) return KDA_ERR_CUDA;
+  if (heads * (kHeadDim / kThinnestDv) <= a.sms)
+    return launch_state<F16, kThinnest>(a, m, heads * (kHeadDim / kThinnestDv), st);
+  if (heads * (kHeadDim / kThinDv) <= a.sms) return launch_state<F16, kThin>(a, m, heads * (kHeadDim / kThinDv), st);
   if (heads * slices <= 2 * a.sms) {
     a.longest_first = a.num_seqs <= kMaxSorted && heads * slices > a.sms;
     return launch_state<F16, kNarrow>(a, m, heads * slices, st);

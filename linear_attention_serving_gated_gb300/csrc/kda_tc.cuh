@@ -66,6 +66,19 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem_addr, uint32_t r
   return d;
 }
 
+// The same for an operand of 32 or 16 rows: lines of 64 or 32 bytes, eight of
+// which form an atom, swizzled in 16-byte pieces within 64 or 32 bytes.
+template <int ROWS>
+__device__ __forceinline__ uint64_t sw_desc_mn(uint32_t smem_addr) {
+  static_assert(ROWS == 32 || ROWS == 16, "rows");
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((ROWS * 16) >> 4) << 32;         // SBO
+  d |= static_cast<uint64_t>(1u) << 46;                       // version
+  d |= static_cast<uint64_t>(ROWS == 32 ? 4u : 6u) << 61;     // SWIZZLE_64B, SWIZZLE_32B
+  return d;
+}
+
 // Operand majors of an instruction descriptor: set for an MN-major A or B.
 constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
 

@@ -250,6 +250,9 @@ def test_prefill_many_sequences(f16):
 
 
 @pytest.mark.parametrize("lengths,H,HV", [
+    ([300], 2, 8),                            # 8 value columns a CTA
+    ([300], 4, 16),                           # 16
+    ([190, 70], 8, 16),                       # 32
     ([1500, 30, 64, 65, 0, 129, 1], 8, 16),   # one sequence by columns, the others whole heads
     ([300, 1400, 90, 1301, 7, 200], 1, 8),    # two
     ([130] * 12, 4, 16),                      # none
