@@ -17,9 +17,9 @@
 // lane holding 16 key channels as four float4, so that every 128-bit access
 // of a warp covers four whole 128-byte segments.
 // Measured (in a graph, on three sets of buffers in turn): decode of 48 requests,
-// 32 heads, 32.4 us, 6.3 TB/s or 92% of a copy's rate; one request, 16 heads, 2.4
-// us, a launch's latency; chain verify 16 x 6, 16 heads, 22.2 us, 5.4 TB/s or 79%
-// (six of its seven parts are writes), tree 27.4.
+// 32 heads, 31.9 us, 6.3 TB/s or 93% of a copy's rate; one request, 16 heads, 2.4
+// us, a launch's latency; chain verify 16 x 6, 16 heads, 22 us, 5.4 TB/s or 80%
+// (six of its seven parts are writes), tree 27.1 with random parents.
 #include "kda_host.h"
 
 namespace kda {
@@ -62,6 +62,7 @@ struct Token {
   uint16_t v[GROUPS];
   uint16_t b;
   ushort2 a;
+  int parent;
 };
 
 template <int MODE, int GROUPS, bool F16>
@@ -93,6 +94,7 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
     for (int gi = 0; gi < GROUPS; ++gi) x.v[gi] = __ldg(v + row0 + gi * 4);
     x.b = __ldg(args.b + row * HV + h);
     x.a = scalar_gate_load(args.gate, args.a, row * HV + h);
+    if (MODE == kGdnTree) x.parent = __ldg(args.parent + row);
   };
   Token<GROUPS> next;
   load(0, next);
@@ -104,12 +106,15 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
   const bool ok = slot >= -1 && slot < args.pool_slots;
   if (!ok && reporter) set_error(args.err_flag, KDA_DEVERR_SLOT);
   bool live = ok && slot >= 0;
+  uint32_t keep = 0;  // tree: bit i, a later node reloads node i's snapshot (nodes from 32 on: taken for granted)
   if (MODE == kGdnTree && live) {  // every warp checks the request's parents for itself
     bool bad = false;
     for (int i = lane; i < T; i += 32) {
       const int p = args.parent[t0 + i];
       bad |= p < -1 || p >= i;
+      if (p >= 0 && p < 32 && p != i - 1) keep |= 1u << p;
     }
+    keep = __reduce_or_sync(0xffffffffu, keep);
     if (__any_sync(0xffffffffu, bad)) {
       if (reporter) set_error(args.err_flag, KDA_DEVERR_PARENT);
       live = false;
@@ -132,16 +137,22 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[gi][i] = *reinterpret_cast<const float4*>(src + gi * 4 * K + i * 32);
   };
-  auto store_state = [&](float* dst) {
+  // A chain's snapshots are not read again here (streamed: 4 x 6 tokens 7.0 instead
+  // of 8.4 us); a tree's stay in L1 where a later node starts from them.
+  auto store_state = [&](float* dst, bool again) {
 #pragma unroll
     for (int gi = 0; gi < GROUPS; ++gi)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float4* at = reinterpret_cast<float4*>(dst + gi * 4 * K + i * 32);
         if (MODE == kGdnChain)
-          __stcs(at, S[gi][i]);  // a chain's snapshots are not read again here: 4 x 6 tokens 7.0 instead of 8.4 us
-        else
+          __stcs(at, S[gi][i]);
+        else if (MODE == kGdnDecode)
           *at = S[gi][i];
+        else if (again)
+          st_keep_l1(dst + gi * 4 * K + i * 32, S[gi][i]);
+        else
+          st_skip_l1(dst + gi * 4 * K + i * 32, S[gi][i]);
       }
   };
   load_state(root);
@@ -151,7 +162,7 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
     if (t + 1 < T) load(t + 1, next);
     const int64_t row = t0 + t;
     if (MODE == kGdnTree && t > 0) {
-      const int p = args.parent[row];
+      const int p = x.parent;
       // the parent's snapshot was written by this same thread
       if (p != t - 1)
         load_state(p < 0 ? root : args.snapshots + (((size_t)t0 + p) * HV + h) * head_elems + (size_t)row0 * K + sub * 4);
@@ -194,9 +205,10 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(const GdnStepArgs ar
         args.o[(row * HV + h) * V + row0 + gi * 4] = float_to_out16<F16>(rq * (alpha * red[4 + 2 * gi] + c * red[2]));
     }
     if (MODE == kGdnChain || MODE == kGdnTree)
-      store_state(args.snapshots + ((size_t)row * HV + h) * head_elems + (size_t)row0 * K + sub * 4);
+      store_state(args.snapshots + ((size_t)row * HV + h) * head_elems + (size_t)row0 * K + sub * 4,
+                  t >= 32 || (keep >> t & 1u));
   }
-  if (MODE == kGdnDecode) store_state(root);
+  if (MODE == kGdnDecode) store_state(root, false);
 }
 
 template <int MODE>

@@ -126,6 +126,21 @@ __device__ __forceinline__ float scalar_log_decay(const ScalarGateArgs& ga, usho
   return g < -128.f ? -128.f : g;
 }
 
+// Tree verify's snapshot stores: a snapshot that a later node reloads (its
+// parent is not the node just before it) stays in L1 with evict-last
+// priority, so that the reload, by the same thread, finds it there; the
+// others are not allocated in L1, which keeps room for the kept ones.
+__device__ __forceinline__ void st_keep_l1(float* p, float4 v) {
+  asm volatile("st.global.L1::evict_last.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
+               "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void st_skip_l1(float* p, float4 v) {
+  asm volatile("st.global.L1::no_allocate.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
+               "f"(v.w)
+               : "memory");
+}
+
 // Packed FP32 pair arithmetic (sm_100+ f32x2 instructions).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t d;

@@ -90,20 +90,6 @@ __device__ __forceinline__ float group_sum8(float x) {
   return x;
 }
 
-// Tree verify's snapshot stores: a snapshot that a later node reloads (its
-// parent is not the node just before it) stays in L1 with evict-last
-// priority, so that the reload, by the same thread, finds it there; the
-// others are not allocated in L1, which keeps room for the kept ones.
-__device__ __forceinline__ void st_keep_l1(float* p, float4 v) {
-  asm volatile("st.global.L1::evict_last.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
-               "f"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void st_skip_l1(float* p, float4 v) {
-  asm volatile("st.global.L1::no_allocate.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
-               "f"(v.w)
-               : "memory");
-}
 // The state of decode and ReplaySSM verify (CTAs of two or more row groups)
 // is read once and, for decode, written once: neither needs L1.
 __device__ __forceinline__ float4 ld_skip_l1(const float* p) {
