@@ -10,13 +10,13 @@
 // The answer is a whole number, so it must not depend on how sums are split.
 // Accept tests are exact: the product of two FP32 numbers fits FP64.  Sums of
 // weights are FP32 pairs (sum, error) whose error part takes what each addition
-// and each difference p - q rounds off (two-sum; 48 bits); FP64, at 1/64 of FP32's
-// rate here, is left to the few comparisons with u times the whole.
+// and each difference p - q rounds off (two-sum; 48 bits), and so is u times the
+// whole; FP64, at 1/64 of FP32's rate here, is left to the accept tests.
 //
 // One cluster per request: every CTA repeats the walk (a few gathered loads,
 // whose latency is the same for one CTA as for all), its warps sum blocks of 256
 // weights and store one pair per block in the first CTA's shared memory.  The
-// first CTA scans the block sums, and one warp goes through the block that holds
+// first CTA scans the block sums, and its warps go through the block that holds
 // the border.  A row is read once, 32 bytes a lane and block; bound by latency
 // for a few requests and by HBM for many (48 rows of p and q of 131072 FP32: 50
 // MB).
@@ -144,8 +144,14 @@ __device__ __forceinline__ void weights8(const Row& row, int j, int step, int V,
 // A sum as s + c, s rounded and c what that leaves.
 struct Pair {
   float s, c;
-  __device__ double value() const { return (double)s + (double)c; }
 };
+__device__ __forceinline__ bool operator>(Pair a, Pair b) {  // where it is close, a.s - b.s is exact
+  return (a.s - b.s) + (a.c - b.c) > 0.f;
+}
+__device__ __forceinline__ Pair times(float u, Pair x) {
+  const float h = u * x.s;
+  return {h, fmaf(u, x.s, -h) + u * x.c};
+}
 __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   const float t = a.s + b.s, z = t - a.s;
   return {t, a.c + (((a.s - (t - z)) + (b.s - z)) + b.c)};
@@ -175,38 +181,67 @@ __device__ __forceinline__ Pair scan(Pair x, int lane) {  // inclusive, over WID
   return x;
 }
 
+// Sums of a CTA's warps, and what each found.
+struct Found {
+  Pair sum[kAccWarps];
+  int over[kAccWarps], last[kAccWarps];
+};
+
 // The lowest j in [lo, hi) with weight whose running sum from `before` exceeds
 // `goal`; where rounding leaves none, the last j with weight; -1 where none has
-// any.  One warp, lo a multiple of 8.
+// any.  All warps, 256 weights each at a time; lo a multiple of 8.
 template <int DT, bool VEC>
-__device__ int find_in(const Row& row, int lo, int hi, Pair before, double goal, int lane) {
+__device__ int find_in(const Row& row, int lo, int hi, Pair before, Pair goal, Found& f, int warp, int lane) {
   int last = -1;
-  for (int j0 = lo; j0 < hi; j0 += kBlock) {
+  for (int base = lo; base < hi; base += kAccWarps * kBlock) {
+    const int j0 = base + warp * kBlock;
     float w[8], err[8];
-    weights8<DT, VEC>(row, j0 + 8 * lane, 1, hi, w, err);
+    weights8<DT, VEC>(row, j0 < hi ? j0 + 8 * lane : hi, 1, hi, w, err);
     Pair sum{0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = sum + Pair{w[e], err[e]};
-    const Pair cum = before + scan<32>(sum, lane);
+    const Pair in_warp = scan<32>(sum, lane);
+    if (lane == 31) f.sum[warp] = in_warp;
+    __syncthreads();
+    Pair up_to = before;  // this warp's weights
+#pragma unroll
+    for (int g = 0; g < kAccWarps; ++g) {
+      if (g == warp) up_to = before;
+      before = before + f.sum[g];
+    }
+    const Pair cum = up_to + in_warp;
     const unsigned some = __ballot_sync(0xffffffffu, sum.s > 0.f);
-    const unsigned over = __ballot_sync(0xffffffffu, sum.s > 0.f && cum.value() > goal);
+    const unsigned over = __ballot_sync(0xffffffffu, sum.s > 0.f && cum > goal);
+    int mine_last = -1;
     if (some) {
       // lane L's eight weights, one each for the first lanes
       const int L = over ? __ffs(over) - 1 : 31 - __clz(some);
-      const Pair up = shfl(cum, (L + 31) & 31), base = L > 0 ? up : before;
+      const Pair up = shfl(cum, (L + 31) & 31), start = L > 0 ? up : up_to;
       Pair mine{0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const Pair x = shfl(Pair{w[e], err[e]}, L);
         if (lane == e) mine = x;
       }
-      const Pair run = base + scan<8>(mine, lane);
+      const Pair run = start + scan<8>(mine, lane);
       const unsigned pos = __ballot_sync(0xffffffffu, lane < 8 && mine.s > 0.f);
-      const unsigned hit = __ballot_sync(0xffffffffu, lane < 8 && mine.s > 0.f && run.value() > goal);
-      last = j0 + 8 * L + (hit ? __ffs(hit) - 1 : 31 - __clz(pos));
-      if (over) return last;
+      const unsigned hit = __ballot_sync(0xffffffffu, lane < 8 && mine.s > 0.f && run > goal);
+      mine_last = j0 + 8 * L + (hit ? __ffs(hit) - 1 : 31 - __clz(pos));
     }
-    before = shfl(cum, 31);
+    if (lane == 0) {
+      f.over[warp] = over ? mine_last : -1;
+      f.last[warp] = mine_last;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int g = kAccWarps - 1; g >= 0; --g)
+      if (f.last[g] >= 0) {
+        last = f.last[g];
+        break;
+      }
+#pragma unroll
+    for (int g = 0; g < kAccWarps; ++g)
+      if (f.over[g] >= 0) return f.over[g];
   }
   return last;
 }
@@ -224,6 +259,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   __shared__ int skip_s[TREE ? KDA_ACCEPT_MAX_T : 1];
   __shared__ Pair sums[kMaxBlocks], warp_sum[kAccWarps], pick_before;
   __shared__ int first_fall, cur_s, n_skip_s, pick, lowest, highest;
+  __shared__ Found found;
   extern __shared__ __align__(16) uint8_t ring_smem[];
 
   const int64_t r0 = (int64_t)r * T;
@@ -460,7 +496,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   __syncthreads();
   // every warp scans the warps' sums
   const Pair all_warps = scan<kAccWarps>(lane < kAccWarps ? warp_sum[lane] : Pair{0.f, 0.f}, lane);
-  const double whole = shfl(all_warps, kAccWarps - 1).value(), u = u_draw, goal = u * whole;
+  const Pair whole = shfl(all_warps, kAccWarps - 1), goal = times(u_draw, whole);
   const Pair up_warp = shfl(all_warps, (warp + 31) & 31), up_lane = shfl(in_warp, (lane + 31) & 31);
   Pair run{0.f, 0.f}, last_before{0.f, 0.f};
   if (warp > 0) run = up_warp;
@@ -472,7 +508,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
     if (x[e].s > 0.f && first < 0) {
       last = tid * kPer + e;
       last_before = run;
-      if (next.value() > goal) first = last;
+      if (next > goal) first = last;
     }
     run = next;
   }
@@ -485,16 +521,15 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
     pick_before = last_before;
   }
   __syncthreads();
-  if (warp != 0) return;
-  int answer = -1;
-  if (whole > 0.0) {
+  int answer;
+  if (whole.s > 0.f) {
     const int64_t a = (int64_t)pick * size;
-    answer = find_in<DT, VEC>(row, (int)a, (int)(a + size < V ? a + size : V), pick_before, goal, lane);
+    answer = find_in<DT, VEC>(row, (int)a, (int)(a + size < V ? a + size : V), pick_before, goal, found, warp, lane);
   } else {  // nothing left of the row: all of p
     row.q = nullptr;
     row.n_skip = 0;
     Pair all{0.f, 0.f};
-    for (int j0 = 0; j0 < V; j0 += kBlock) {
+    for (int j0 = warp * kBlock; j0 < V; j0 += kAccWarps * kBlock) {
       float w[8], err[8];
       weights8<DT, VEC>(row, j0 + 8 * lane, 1, V, w, err);
 #pragma unroll
@@ -503,9 +538,14 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
 #pragma unroll
     for (int m = 16; m; m >>= 1)
       all = all + Pair{__shfl_xor_sync(0xffffffffu, all.s, m), __shfl_xor_sync(0xffffffffu, all.c, m)};
-    answer = find_in<DT, VEC>(row, 0, V, Pair{0.f, 0.f}, u * all.value(), lane);
+    if (lane == 0) warp_sum[warp] = all;
+    __syncthreads();
+    all = warp_sum[0];
+#pragma unroll
+    for (int g = 1; g < kAccWarps; ++g) all = all + warp_sum[g];
+    answer = find_in<DT, VEC>(row, 0, V, Pair{0.f, 0.f}, times(u_draw, all), found, warp, lane);
   }
-  if (lane == 0) args.next_token[r] = answer;
+  if (tid == 0) args.next_token[r] = answer;
 }
 
 template <int DT, bool TREE, bool VEC>
