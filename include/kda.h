@@ -401,6 +401,7 @@ kda_status kda_gdn_verify_tree(kda_dims dims, kda_scalar_gate gate, const kda_bf
  *   next_token    [B] int32 out: the token drawn behind it: the lowest j whose
  *                 running sum of weights w_0 + .. + w_j exceeds u[r][0] times
  *                 their whole; -1 where the row has no weight at all
+ * As with kda_gdn_prefill, the first call on each device comes before capture.
  */
 #define KDA_DTYPE_F32 2 /* for probs_dtype only */
 #define KDA_DEVERR_TOKEN 64 /* drafted token outside [0, vocab) */

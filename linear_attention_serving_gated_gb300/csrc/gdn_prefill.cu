@@ -1621,15 +1621,29 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const uint4* __restrict
   split(wk, k_hi, k_lo);
 }
 
-// Sets a kernel's shared-memory limit once per device.
+template <bool F16, int kForm>
+constexpr int kStateSmem = kForm == kWide ? Cfg<F16>::kWideSmem : Cfg<F16>::kSmem;
+
 template <typename Kernel>
-kda_status allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>* ready) {
+bool allow_smem(Kernel kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+template <bool F16, int... kForms>
+bool allow_forms() {
+  return allow_smem(gdn_chunk_kernel<F16>, ChunkCfg::kSmem) &&
+         (allow_smem(gdn_state_kernel<F16, kForms>, kStateSmem<F16, kForms>) && ...);
+}
+// The kernels' shared-memory limits, all of them in the first call on a device:
+// a later one may be under capture.
+kda_status allow_all() {
+  static std::atomic<uint64_t> ready{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
-  if (!(ready->load(std::memory_order_relaxed) >> dev & 1u)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+    if (!allow_forms<false, kThinnest, kThin, kNarrow, kWide, kMixed>() ||
+        !allow_forms<true, kThinnest, kThin, kNarrow, kWide, kMixed>())
       return KDA_ERR_CUDA;
-    ready->fetch_or(1ull << dev, std::memory_order_relaxed);
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   return KDA_OK;
 }
@@ -1654,10 +1668,7 @@ kda_status launch_after(Kernel kernel, unsigned grid, unsigned threads, int smem
 
 template <bool F16>
 kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
-  static std::atomic<uint64_t> ready{0};
   static_assert(ChunkCfg::kCtas * (ChunkCfg::kSmem + 1024) <= 233472, "CTAs per SM");
-  kda_status s = allow_smem(gdn_chunk_kernel<F16>, ChunkCfg::kSmem, &ready);
-  if (s != KDA_OK) return s;
   const int64_t grid = a.max_chunks * a.HV;
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
   return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg::kSmem, F16, st, a, m);
@@ -1666,13 +1677,9 @@ kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t
 template <bool F16, int kForm>
 kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, int64_t grid, cudaStream_t st) {
   using C = Cfg<F16>;
-  constexpr int smem = kForm == kWide ? C::kWideSmem : C::kSmem;
-  static std::atomic<uint64_t> ready{0};
   static_assert(C::kSmem <= 232448 && C::kWideSmem <= C::kSmem && kStateThreads == 768, "shared memory and registers");
-  kda_status s = allow_smem(gdn_state_kernel<F16, kForm>, smem, &ready);
-  if (s != KDA_OK) return s;
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, smem, true, st, a, m);
+  return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, kStateSmem<F16, kForm>, true, st, a, m);
 }
 
 // As thin as lets all CTAs start at once: 1 x 4096 tokens, 16 heads, thin 95.5 us,
@@ -1776,6 +1783,8 @@ extern "C" kda_status kda_gdn_prefill(kda_dims dims, kda_scalar_gate gate, const
               !encode_half_rows(&m.k, ws + 2 * part, dims.H, total_tokens) ||
               !encode_half_rows(&m.k_lo, ws + 3 * part, dims.H, total_tokens)))
     return KDA_ERR_CUDA;
+  s = allow_all();
+  if (s != KDA_OK) return s;
   record_stage(0, st);
   if (f16) {
     const int64_t n = total_tokens * dims.H * (kHeadDim / 8);

@@ -549,20 +549,30 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   if (tid == 0) args.next_token[r] = answer;
 }
 
+template <int DT, bool TREE>
+bool allow_ring() {
+  return cudaFuncSetAttribute(accept_kernel<DT, TREE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kRingBytes<DT>) == cudaSuccess;
+}
+// The kernels' shared-memory limits, all of them in the first call on a device:
+// a later one may be under capture.
+kda_status allow_rings() {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+    if (!allow_ring<KDA_DTYPE_F32, false>() || !allow_ring<KDA_DTYPE_F32, true>() ||
+        !allow_ring<KDA_DTYPE_BF16, false>() || !allow_ring<KDA_DTYPE_BF16, true>() ||
+        !allow_ring<KDA_DTYPE_F16, false>() || !allow_ring<KDA_DTYPE_F16, true>())
+      return KDA_ERR_CUDA;
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  return KDA_OK;
+}
+
 template <int DT, bool TREE, bool VEC>
 kda_status launch_accept_kernel(const AcceptArgs& a, cudaLaunchConfig_t cfg) {
-  if (VEC) {
-    cfg.dynamicSmemBytes = kRingBytes<DT>;
-    static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
-    if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-      if (cudaFuncSetAttribute(accept_kernel<DT, TREE, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kRingBytes<DT>) != cudaSuccess)
-        return KDA_ERR_CUDA;
-      ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
-  }
+  if (VEC) cfg.dynamicSmemBytes = kRingBytes<DT>;
   cudaLaunchKernelEx(&cfg, accept_kernel<DT, TREE, VEC>, a);
   return launch_status();
 }
@@ -570,7 +580,7 @@ kda_status launch_accept_kernel(const AcceptArgs& a, cudaLaunchConfig_t cfg) {
 template <int DT>
 kda_status launch_accept(const AcceptArgs& a, int B, bool tree, cudaStream_t st) {
   const int sms = sm_count();
-  if (sms <= 0) return KDA_ERR_CUDA;
+  if (sms <= 0 || allow_rings() != KDA_OK) return KDA_ERR_CUDA;
   // CTAs per request: enough to fill the SMs twice, but a block at least for each warp
   int parts = 1;
   while (parts < 8 && (int64_t)B * parts < 2 * sms && (int64_t)parts * kAccWarps * kBlock < a.vocab) parts *= 2;
