@@ -337,16 +337,29 @@ __device__ __forceinline__ void put_rows(uint8_t* tile, int row, int part, int l
 // The chain warps have written an operand: the warps that issue its products
 // wait for them at a hardware barrier, which wakes them sooner than an mbarrier
 // would and costs the chain one instruction.  kBarSq: S, for Q S.
-enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6 };
+// A barrier counts arrivals, whoever they come from: one ahead of its phase would
+// count for another warp, and the issuing warp would be left at a later phase for
+// good.  What keeps a chain warp from that is its waits for products; one that has
+// run out of time skips those, and waits at the barriers instead.  kBarPast keeps
+// the two issuing warps within a chunk of each other, so that who has met one at
+// S knows the other to be past D of the chunk before.  By then it is, long since,
+// unless a wait has run out.
+enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6, kBarPast = 7 };
 template <int WARPS>
-__device__ __forceinline__ void barrier_arrive(int id) {
-  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(32 * (WARPS + 1)) : "memory");
+__device__ __forceinline__ void barrier_arrive(int id, bool ok) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p barrier.cta.arrive %0, %1;\n\t"
+      "@!p barrier.cta.sync %0, %1;\n\t}" ::"r"(id),
+      "n"(32 * (WARPS + 1)), "r"(static_cast<uint32_t>(ok))
+      : "memory");
 }
 template <bool TMEM, int WARPS>
-__device__ __forceinline__ void chain_arrive(int id) {
+__device__ __forceinline__ void chain_arrive(int id, bool ok) {
   if (TMEM) wait_st();
   tc::tc_fence_before();
-  barrier_arrive<WARPS>(id);
+  barrier_arrive<WARPS>(id, ok);
 }
 // For operands in shared memory the fence between the chain's writes and the
 // tensor core's reads stands here, behind the barrier, in the issuing warp alone:
@@ -357,6 +370,9 @@ __device__ __forceinline__ void chain_await(int id) {
   if (!TMEM) tc::fence_async_smem();
   tc::tc_fence_after();
 }
+
+__device__ __forceinline__ void past_arrive() { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(static_cast<int>(kBarPast)) : "memory"); }
+__device__ __forceinline__ void past_await() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(static_cast<int>(kBarPast)) : "memory"); }
 
 __device__ __forceinline__ int64_t seq_start(const GdnPrefillArgs& a, int n) {
   return a.cu_seqlens ? (int64_t)a.cu_seqlens[n] : a.total_tokens / a.num_seqs * n;
@@ -1080,8 +1096,8 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       const int sl = c % C::kRecs;
       const uint32_t cp = (uint32_t)c & 1u;
       put_split<DV>(smem + C::kS, dk, part, S);
-      chain_arrive<false, kWarps>(kBarS);
-      barrier_arrive<kWarps>(kBarSq);
+      chain_arrive<false, kWarps>(kBarS, ok);
+      barrier_arrive<kWarps>(kBarSq, ok);
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + col0) * kHeadDim + dk;
@@ -1111,7 +1127,7 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
         x[e] = fma2(make_float2(fa[e], fa[e]), x[e], v);
       }
       put_rows<DV>(smem + C::kY, row, part, lane, x);
-      chain_arrive<false, kWarps>(kBarY);
+      chain_arrive<false, kWarps>(kBarY, ok);
       if (c + 1 < nch) load_v(c + 1);
       chain_wait(&bars.d_full, cp, ok);
       tc::tc_fence_after();
@@ -1119,9 +1135,9 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
 #pragma unroll
       for (int e = 0; e < 2; ++e) y[e] = mul2(make_float2(fs[e], fs[e]), x[e]);
       put_rows<DV>(smem + C::kY, row, part, lane, y);
-      chain_arrive<false, kWarps>(kBarDs);
+      chain_arrive<false, kWarps>(kBarDs, ok);
       put_rows<DV>(smem + C::kD, row, part, lane, x);
-      chain_arrive<false, kWarps>(kBarD);
+      chain_arrive<false, kWarps>(kBarD, ok);
       chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
       float u[8];
@@ -1192,6 +1208,7 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       const uint64_t t_op = tc::sw128_desc(tc::smem_u32(smem + C::kRec + sl * kRecBytes));
       ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
+      if (c > 0) past_await();
       chain_await<false, kWarps>(kBarS);
       if (leader && ok) {  // X = K S
 #pragma unroll
@@ -1231,6 +1248,7 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       if (leader && ok) tc::mma_commit(&bars.u_full);
       __syncwarp();
     }
+    past_await();
   } else if (warp == kSideWarp) {
     // ----------------------------------------- products for the output alone
     // As the chain warps, it goes on without waiting once out of time.
@@ -1258,6 +1276,7 @@ __device__ __forceinline__ void narrow_unit(const GdnPrefillArgs& args, const Gd
       }
       __syncwarp();
       chain_await<false, kWarps>(kBarD);  // the chain is also past T and this chunk's scalars
+      past_arrive();
       if (leader && ok) {  // P D
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -1322,8 +1341,8 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       const uint32_t cp = (uint32_t)c & 1u;
       put_split16(lanes + kTmS + 16 * part, lanes + kTmSlo + 16 * part, S);
       put_split16(lanes + kTmS + 16 * part + 8, lanes + kTmSlo + 16 * part + 8, S + 16);
-      chain_arrive<true, kChainWarps>(kBarS);
-      barrier_arrive<kChainWarps>(kBarSq);
+      chain_arrive<true, kChainWarps>(kBarS, ok);
+      barrier_arrive<kChainWarps>(kBarSq, ok);
       if (args.intermediate) {
         if (cid + c < args.inter_chunks) {
           float* dst = args.intermediate + (((size_t)(cid + c) * args.HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
@@ -1362,7 +1381,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
         }
       }
       put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, x);
-      chain_arrive<true, kChainWarps>(kBarY);
+      chain_arrive<true, kChainWarps>(kBarY, ok);
       if (c + 1 < nch) load_v(c + 1);
       chain_wait(&bars.d_full, cp, ok);
       tc::tc_fence_after();
@@ -1381,9 +1400,9 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
         }
         put_split16(lanes + kTmY + 8 * part, lanes + kTmYlo + 8 * part, y);
       }
-      chain_arrive<true, kChainWarps>(kBarDs);
+      chain_arrive<true, kChainWarps>(kBarDs, ok);
       put_split16(lanes + kTmX + tok0, lanes + kTmX + tok0 + 8, x);  // over this warp's quarter of D
-      chain_arrive<true, kChainWarps>(kBarD);
+      chain_arrive<true, kChainWarps>(kBarD, ok);
       chain_wait(&bars.u_full, cp, ok);
       tc::tc_fence_after();
 #pragma unroll
@@ -1470,6 +1489,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       ok = ok && warp_wait(&bars.key[ks], (uint32_t)(c / C::kKeys) & 1u);
       if (c == nch - 1 && L % kC != 0) ok = ok && warp_wait(&bars.tail, 0);
       if (c > 0) ok = ok && warp_wait(&bars.o_full, (uint32_t)(c - 1) & 1u);  // X takes the place of the last D
+      if (c > 0) past_await();
       chain_await<true, kChainWarps>(kBarS);
       if (leader && ok) {  // X^T = S^T K^T
 #pragma unroll
@@ -1518,6 +1538,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       if (leader && ok) tc::mma_commit(&bars.u_full);
       __syncwarp();
     }
+    past_await();
   } else if (warp == kSideWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ----------------------------------------- products for the output alone
@@ -1549,6 +1570,7 @@ __device__ __forceinline__ void wide_unit(const GdnPrefillArgs& args, const GdnM
       }
       __syncwarp();
       chain_await<true, kChainWarps>(kBarD);  // the chain is also past T and this chunk's scalars
+      past_arrive();
       if (leader && ok) {  // D^T P^T
 #pragma unroll
         for (int b = 0; b < 3; ++b)  // hi hi, lo hi, hi lo
