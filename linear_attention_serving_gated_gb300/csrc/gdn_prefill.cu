@@ -132,6 +132,7 @@ struct Bars {
   uint64_t rec[3], rec_free[3];  // records
   uint64_t x_full, xq_full, d_full, u_full;
   uint64_t o_full, o_read;
+  uint64_t drained[2];  // all products of an issuing warp; used where a wait has run out
   int64_t chunk0;  // id of the sequence's first chunk
   uint32_t tmem;
   int timed_out;
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
   }
   tc::tc_fence_before();
   bad = __syncthreads_or(bad);
-  if (quad == 0) {
+  if (quad == 0 && !bad) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, C::kTmCols);
   }
@@ -820,6 +821,12 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
     tc::bulk_s2g(rec + kRecScalars, &sc, 1024);
     tc::bulk_commit();
     tc::bulk_wait_read();
+  }
+  if (bad && quad == 0) {  // a wait ran out: once more, with its limit, for rows and products under way
+    warp_wait(&bars[0], 0);
+    warp_wait(&bars[1], 0);
+    tc::tc_fence_after();
+    tc::tmem_dealloc(*reinterpret_cast<const uint32_t*>(&bars[2]), C::kTmCols);
   }
   after_split();
 }
@@ -972,6 +979,8 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
     tc::mbar_init(&bars.u_full, 1);
     tc::mbar_init(&bars.o_full, 1);
     tc::mbar_init(&bars.o_read, kOutWarps);
+    tc::mbar_init(&bars.drained[0], 1);
+    tc::mbar_init(&bars.drained[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::tc_fence_before();
@@ -980,14 +989,25 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
   return true;
 }
 
-// And its last ones.
+// And its last ones.  Where a wait has run out, products may still be under way:
+// their issuing warps wait for them, with a limit, before TMEM and shared memory go.
 __device__ __forceinline__ void end_unit(const GdnPrefillArgs& args, Bars& bars, uint32_t tmem, bool ok) {
   if (!ok) bars.timed_out = 1;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (threadIdx.x == 0 && bars.timed_out) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-  if (threadIdx.x >> 5 == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
+  const int warp = threadIdx.x >> 5;
+  if (bars.timed_out) {
+    if (threadIdx.x == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+    if (warp == kMmaWarp || warp == kSideWarp) {
+      uint64_t* bar = &bars.drained[warp == kSideWarp];
+      if (elect_one()) tc::mma_commit(bar);  // the same lane as issued them
+      __syncwarp();
+      warp_wait(bar, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
 }
 
 // The row warp: every chunk's keys and queries, as two halves of 64 channels each.

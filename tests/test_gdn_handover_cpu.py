@@ -166,3 +166,18 @@ def test_every_warp_meets_the_others_whatever_runs_out(unit):
             role = ["chain"] * CHAIN + ["out", "mma", "side"]
             waits = [i for i, s in enumerate(roles[role[who]]) if s[0] == "wait"]
             run(roles, nch, rng, lost=(who, rng.choice(waits), rng.randrange(nch)))
+
+
+def test_nothing_is_under_way_where_a_late_cta_leaves():
+    """Read from the source: where a wait has run out, TMEM is given back only
+    behind a bounded wait for the products and copies of the CTA."""
+    text = open(SRC).read()
+    body = lambda name: text[text.index(name):][:text[text.index(name):].index("\n}\n")]  # noqa: E731
+    end = body("void end_unit(")
+    late = end[end.index("if (bars.timed_out) {"):end.index("tmem_dealloc")]
+    assert late.index("mma_commit(bar)") < late.index("warp_wait(bar, 0)") < late.rindex("__syncthreads()")
+    chunk = body("gdn_chunk_kernel(const GdnPrefillArgs")
+    late = chunk[chunk.index("if (bad && quad == 0) {"):]
+    assert max(late.index("warp_wait(&bars[0], 0)"), late.index("warp_wait(&bars[1], 0)")) < late.index("tmem_dealloc")
+    early = chunk[:chunk.index("if (bad && quad == 0) {")]
+    assert re.search(r"if \(quad == 0 && !bad\) \{\s+tc::tc_fence_after\(\);\s+tc::tmem_dealloc", early)
