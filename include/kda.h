@@ -490,11 +490,12 @@ kda_status kda_pool_fork(kda_pages pages, uint8_t *used, int32_t *table, int tab
  * entry point.  After kda_set_stage_events(ev) with three cudaEvent_t
  * handles passed as void*, each later call records ev[0] on its stream before
  * its first kernel and ev[2] after its last; kda_prefill records ev[1]
- * between its chunk-transform and state-pass kernels, the single-kernel entry
- * points record ev[1] together with ev[2].  Under stream capture they become
- * external event nodes, so every replay of the graph records them.  A NULL
- * entry is not recorded; a NULL array clears the setting, which is
- * process-wide and not meant for concurrent callers.
+ * between its chunk-transform and state-pass kernels, kda_gdn_prefill between
+ * its record and state kernels, kda_pool_compact and kda_pool_fork between
+ * their two, the single-kernel entry points record ev[1] together with ev[2].
+ * Under stream capture they become external event nodes, so every replay of
+ * the graph records them.  A NULL entry is not recorded; a NULL array clears
+ * the setting, which is process-wide and not meant for concurrent callers.
  */
 void kda_set_stage_events(void *const *events);
 

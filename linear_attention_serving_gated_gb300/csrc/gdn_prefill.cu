@@ -1690,7 +1690,7 @@ kda_status allow_all() {
   return KDA_OK;
 }
 
-// A launch that may start while the one before it runs (its kernel waits).
+// A launch that, if dependent, may start while the one before it runs (its kernel waits).
 template <typename Kernel>
 kda_status launch_after(Kernel kernel, unsigned grid, unsigned threads, int smem, bool dependent, cudaStream_t st,
                         const GdnPrefillArgs& a, const GdnMaps& m) {
@@ -1721,7 +1721,8 @@ kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, int64_t grid,
   using C = Cfg<F16>;
   static_assert(C::kSmem <= 232448 && C::kWideSmem <= C::kSmem && kStateThreads == 768, "shared memory and registers");
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, kStateSmem<F16, kForm>, true, st, a, m);
+  return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, kStateSmem<F16, kForm>, !stage_between(), st, a,
+                      m);
 }
 
 // As thin as lets all CTAs start at once: 1 x 4096 tokens, 16 heads, thin 95.5 us,

@@ -70,6 +70,10 @@ inline kda_status launch_status() {
 // stream if one is set.
 void record_stage(int i, cudaStream_t st);
 
+// Whether a stage event is recorded between an entry point's kernels: the
+// second one is then an ordinary launch, not one that may start early.
+bool stage_between();
+
 // The prefill's token-by-token path, for sequences whose log-decays the
 // chunk form's decay windows cannot take: one step per token like decode, the
 // state in registers, o and chunk-start states written per token and chunk,

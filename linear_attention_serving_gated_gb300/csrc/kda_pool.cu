@@ -290,7 +290,8 @@ kda_status check_pages(const kda_pages& p) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// A launch that may start while the one before it runs (the kernel waits).
+// A launch that may start while the one before it runs (the kernel waits), unless
+// a stage event stands between them.
 template <typename... Par, typename... Arg>
 void launch_dependent(void (*kernel)(Par...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, Arg... args) {
   cudaLaunchAttribute attr[1];
@@ -302,7 +303,7 @@ void launch_dependent(void (*kernel)(Par...), unsigned grid, unsigned block, siz
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = stage_between() ? 0 : 1;
   cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -1816,10 +1816,17 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t heads, int64_t T, uin
 }  // namespace
 
 // Recorded as an external event node when the stream is being captured, so
-// the event fires on every replay of the graph.
+// the event fires on every replay of the graph; that flag is an error outside
+// of a capture.
 void record_stage(int i, cudaStream_t st) {
-  if (g_stage_events[i]) cudaEventRecordWithFlags(g_stage_events[i], st, cudaEventRecordExternal);
+  if (!g_stage_events[i]) return;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaStreamIsCapturing(st, &capture);
+  cudaEventRecordWithFlags(g_stage_events[i], st,
+                           capture == cudaStreamCaptureStatusNone ? cudaEventRecordDefault : cudaEventRecordExternal);
 }
+
+bool stage_between() { return g_stage_events[1] != nullptr; }
 
 }  // namespace kda
 
@@ -1964,7 +1971,7 @@ extern "C" kda_status kda_prefill(kda_dims dims, kda_gate gate, const kda_bf16* 
   const bool f16 = dims.dtype == KDA_DTYPE_F16;
   void (*const pass_kernel)(PrefillArgs) = multi ? (f16 ? state_pass_kernel<true, true> : state_pass_kernel<false, true>)
                                                  : (f16 ? state_pass_kernel<true, false> : state_pass_kernel<false, false>);
-  if (g_stage_events[1]) {  // a stage event between the kernels: an ordinary launch
+  if (stage_between()) {
     record_stage(1, st);
     pass_kernel<<<grid, kPassThreads, kPassSmem, st>>>(args);
     s = launch_status();
