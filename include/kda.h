@@ -445,7 +445,9 @@ kda_status kda_accept_tree(int probs_dtype, const void *target, int64_t target_s
  * byte per slot, 0 for a free page (4-byte aligned, slots rounded up to 4
  * bytes).  `table` maps the caller's rows (requests) to slots, -1 for none; it
  * is the state_idx of the other calls.  All of it is on the device: no call
- * reads it from the host.  No two rows share a slot.
+ * reads it from the host.  No two rows share a slot.  Pools of more than
+ * 190000 slots: as with kda_gdn_prefill, the first compact or fork on each
+ * device comes before capture.
  */
 typedef struct {
   void *base;           /* 16-byte aligned */

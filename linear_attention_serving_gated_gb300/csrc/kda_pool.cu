@@ -11,6 +11,8 @@
 // 32-bit word: a binary search over the words, then a bit scan.  A pool of
 // 240 slots is 8 words, so every CTA of a copy builds its own instead of
 // waiting for a plan in memory.
+#include <atomic>
+
 #include "kda_host.h"
 
 namespace kda {
@@ -307,9 +309,22 @@ void launch_dependent(void (*kernel)(Par...), unsigned grid, unsigned block, siz
   cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename Kernel>
-bool allow_smem(Kernel k, size_t bytes) {
-  return bytes <= 48 * 1024 || cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+// The shared-memory limits of the kernels that hold a map of `bytes`.  Without
+// one a kernel gets 48 KiB, its own arrays (under 1 KiB) among them.  Set for the
+// largest map, in the first call on a device that needs more: a later one may be
+// under capture.
+bool allow_map(size_t bytes) {
+  static std::atomic<uint64_t> ready{0};
+  if (bytes + 1024 <= 48 * 1024) return true;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (ready.load(std::memory_order_relaxed) >> dev & 1u) return true;
+  auto allow = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)map_bytes(kMaxSlots)) == cudaSuccess;
+  };
+  if (!allow(compact_copy_kernel) || !allow(compact_update_kernel) || !allow(fork_assign_kernel)) return false;
+  ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return true;
 }
 
 }  // namespace
@@ -362,7 +377,7 @@ extern "C" kda_status kda_pool_compact(kda_pages pages, uint8_t* used, int32_t* 
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
   const size_t smem = map_bytes(pages.slots);
-  if (!allow_smem(compact_copy_kernel, smem) || !allow_smem(compact_update_kernel, smem)) return KDA_ERR_CUDA;
+  if (!allow_map(smem)) return KDA_ERR_CUDA;
   // at most half of the slots move (a move fills a hole)
   const double most = (double)parts * pages.layers * (pages.slots / 2 + 1);
   const unsigned grid = (unsigned)(most < 8.0 * sms ? most : 8.0 * sms);
@@ -390,7 +405,7 @@ extern "C" kda_status kda_pool_fork(kda_pages pages, uint8_t* used, int32_t* tab
   const int64_t parts = (pages.page_bytes + kPartBytes - 1) / kPartBytes;
   if (parts > INT32_MAX || parts * pages.layers > INT32_MAX / n) return KDA_ERR_SHAPE;
   const size_t smem = map_bytes(pages.slots);
-  if (!allow_smem(fork_assign_kernel, smem)) return KDA_ERR_CUDA;
+  if (!allow_map(smem)) return KDA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   record_stage(0, st);
   fork_assign_kernel<<<1, 1024, smem, st>>>(used, pages.slots, table, table_rows, parents, rows, n, children,
