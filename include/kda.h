@@ -479,9 +479,9 @@ kda_status kda_pool_compact(kda_pages pages, uint8_t *used, int32_t *table, int 
 
 /* For i < n, in order: table row rows[i] gets the lowest free page, filled
  * from the page that table row parents[i] held before the call, or with zeros
- * where parents[i] is -1.  rows[i] = -1 is skipped.  A row that holds a page
- * or was listed before, and a parent row without a page, set KDA_DEVERR_PAGE
- * and change nothing.
+ * where parents[i] is -1.  rows[i] = -1 is skipped.  A row that holds anything
+ * but -1 or was listed before, and a parent row without a page, set
+ * KDA_DEVERR_PAGE and change nothing.
  *   children      [n] int32 out: the slot each entry got, -1 for none */
 kda_status kda_pool_fork(kda_pages pages, uint8_t *used, int32_t *table, int table_rows,
                          const int32_t *parents, const int32_t *rows, int n, int32_t *children,

@@ -11,6 +11,8 @@
 // 32-bit word: a binary search over the words, then a bit scan.  A pool of
 // 240 slots is 8 words, so every CTA of a copy builds its own instead of
 // waiting for a plan in memory.
+#include <limits.h>
+
 #include <atomic>
 
 #include "kda_host.h"
@@ -206,8 +208,9 @@ __device__ __forceinline__ bool has_page(const UsedMap& m, const int32_t* table,
 }
 
 // Fork, first kernel: which row gets which page.  Rows without a page are
-// claimed with the marker -2 - i, the lowest i that lists the row winning, so
-// that a row listed twice is served once; claims are then counted in order.
+// claimed with the marker INT_MIN + i, the lowest i that lists the row winning,
+// so that a row listed twice is served once; claims are then counted in order.
+// (A row of another value below -1 holds no slot there is: refused.)
 __global__ void __launch_bounds__(1024) fork_assign_kernel(uint8_t* used, int slots, int32_t* table, int table_rows,
                                                            const int32_t* parents, const int32_t* rows, int n,
                                                            int32_t* children, int32_t* err_flag) {
@@ -223,9 +226,9 @@ __global__ void __launch_bounds__(1024) fork_assign_kernel(uint8_t* used, int sl
       if (row != -1) set_error(err_flag, KDA_DEVERR_PAGE);
       continue;
     }
-    const int mine = -2 - i;
+    const int mine = INT_MIN + i;
     int old = table[row];
-    while (old == -1 || (old < -1 && old < mine)) {
+    while (old == -1 || (old > mine && old < INT_MIN + n)) {
       const int seen = atomicCAS(table + row, old, mine);
       if (seen == old) break;
       old = seen;
@@ -237,13 +240,13 @@ __global__ void __launch_bounds__(1024) fork_assign_kernel(uint8_t* used, int sl
     const int i = i0 + tid;
     const int row = i < n ? rows[i] : -1;
     const bool named = row >= 0 && row < table_rows;
-    const bool mine = named && __ldcg(table + row) == -2 - i;
+    const bool mine = named && __ldcg(table + row) == INT_MIN + i;
     bool win = mine;
     if (mine) {
       const int par = parents[i];
       win = par == -1 || (par >= 0 && par < table_rows && has_page(m, table, par));
     }
-    if (named && !win) set_error(err_flag, KDA_DEVERR_PAGE);  // listed before, holds a page, or no parent
+    if (named && !win) set_error(err_flag, KDA_DEVERR_PAGE);  // listed before, holds a page or none there is, or no parent
     const unsigned b = __ballot_sync(0xffffffffu, win);
     if (lane == 0) warp_sum[warp] = __popc(b);
     __syncthreads();  // and every marker of this round has been read
