@@ -378,8 +378,13 @@ kda_status kda_gdn_verify_tree(kda_dims dims, kda_scalar_gate gate, const kda_bf
 
 /* ---------------------------------------------------------------------------
  * Verification of drafted tokens against the target's probabilities, between a
- * verify call and its commit.  Random numbers are inputs; results are exact
- * whole numbers (accept tests in exact arithmetic, sums in 48 bits or more).
+ * verify call and its commit.  Random numbers are inputs.  A chain's accept
+ * tests are exact (FP64 holds the product of two FP32 numbers); a tree's are
+ * FP64, with Z subtracted in the order of the siblings.  Sums of weights are
+ * pairs of FP32, within 2^-40 of the whole for a vocabulary of up to 2^20,
+ * 2^-34 for the largest, and vocab * 2^-53 where a draft leaves nothing of its
+ * row: a draw nearer than that to a border between two tokens may fall on
+ * either side of it, and on which may depend on B and the rows' alignment.
  *
  * Rows of a request are those of the verify call: row 0 is the token already
  * sampled, rows 1..T-1 the drafted ones.

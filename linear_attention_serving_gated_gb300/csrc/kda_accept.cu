@@ -8,10 +8,11 @@
 // weights passes u times their whole.
 //
 // The answer is a whole number, so it must not depend on how sums are split.
-// Accept tests are exact: the product of two FP32 numbers fits FP64.  Sums of
-// weights are FP32 pairs (sum, error) whose error part takes what each addition
-// and each difference p - q rounds off (two-sum; 48 bits), and so is u times the
-// whole; FP64, at 1/64 of FP32's rate here, is left to the accept tests.
+// A chain's accept tests are exact: the product of two FP32 numbers fits FP64; a
+// tree's are FP64.  Sums of weights are FP32 pairs (sum, error) whose error part
+// takes what each addition and each difference p - q rounds off (two-sum), and so
+// is u times the whole: within 2^-40 of the whole for up to 2^20 entries (see Pair).
+// FP64, at 1/64 of FP32's rate here, is left to the accept tests.
 //
 // One cluster per request: every CTA repeats the walk (a few gathered loads,
 // whose latency is the same for one CTA as for all), its warps sum blocks of 256
@@ -142,10 +143,18 @@ __device__ __forceinline__ void weights8(const Row& row, int j, int step, int V,
   }
 }
 
-// A sum as s + c, s rounded and c what that leaves.
+// A sum as s + c, s rounded and c what that leaves.  The k-th addition in a row
+// loses k 2^-48 of the sum at most, as c may have gathered k roundings of s by then:
+// sums of many terms move c into s every few of them (tidy).  For up to 2^20 entries
+// 16 additions a lane and some 20 of their sums come to 2^-40; a block of 2^28 adds
+// 4 a group, 1024 groups: 2^-34.
 struct Pair {
   float s, c;
 };
+__device__ __forceinline__ Pair tidy(Pair x) {
+  const float t = x.s + x.c;
+  return {t, x.c - (t - x.s)};
+}
 __device__ __forceinline__ bool operator>(Pair a, Pair b) {  // where it is close, a.s - b.s is exact
   return (a.s - b.s) + (a.c - b.c) > 0.f;
 }
@@ -168,6 +177,12 @@ struct Pair2 {
     const float2 t = add2(s, x), z = fma2(s, neg, t);
     const float2 a = fma2(fma2(z, neg, t), neg, s), b = fma2(z, neg, x);  // s - (t - z), x - z
     c = add2(c, add2(add2(a, b), err));
+    s = t;
+  }
+  __device__ void tidy() {
+    const float2 neg = make_float2(-1.f, -1.f);
+    const float2 t = add2(s, c);
+    c = fma2(fma2(s, neg, t), neg, c);
     s = t;
   }
   __device__ Pair joined() const { return Pair{s.x, c.x} + Pair{s.y, c.y}; }
@@ -210,6 +225,7 @@ __device__ int find_in(const Row& row, int lo, int hi, Pair before, Pair goal, F
       if (g == warp) up_to = before;
       before = before + f.sum[g];
     }
+    before = tidy(before);
     const Pair cum = up_to + in_warp;
     const unsigned some = __ballot_sync(0xffffffffu, sum.s > 0.f);
     const unsigned over = __ballot_sync(0xffffffffu, sum.s > 0.f && cum > goal);
@@ -453,6 +469,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
             for (int e = 0; e < kEl; e += 2) sum.add(make_float2(w[e], w[e + 1]), make_float2(0.f, 0.f));
           }
         }
+        sum.tidy();
       }
       Pair total = sum.joined();
       const float inf = __int_as_float(0x7f800000);
@@ -463,6 +480,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
           weights8<DT, true>(row, j < V ? j : V, 1, V, w, err);
 #pragma unroll
           for (int e = 0; e < 8; ++e) total = total + Pair{w[e], err[e]};
+          total = tidy(total);
         }
       }
       store(total, b);
@@ -477,6 +495,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
         weights8<DT, false>(row, (int)(j0 < V ? j0 : V), 32, V, w, err);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = sum + Pair{w[e], err[e]};
+        sum = tidy(sum);
       }
       store(sum, b);
     }
@@ -535,6 +554,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
       weights8<DT, VEC>(row, j0 + 8 * lane, 1, V, w, err);
 #pragma unroll
       for (int e = 0; e < 8; ++e) all = all + Pair{w[e], 0.f};
+      all = tidy(all);
     }
 #pragma unroll
     for (int m = 16; m; m >>= 1)
