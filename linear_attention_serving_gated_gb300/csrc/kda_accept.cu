@@ -162,6 +162,10 @@ __device__ __forceinline__ Pair times(float u, Pair x) {
   const float h = u * x.s;
   return {h, fmaf(u, x.s, -h) + u * x.c};
 }
+// Where the whole is below 2^-60, u times it would lose bits below FP32's smallest
+// number: such rows are drawn from with all weights 2^64 times as large (exact).
+__device__ __forceinline__ float lift_of(Pair whole) { return whole.s < 0x1p-60f ? 0x1p64f : 1.f; }
+__device__ __forceinline__ Pair operator*(float lift, Pair x) { return {lift * x.s, lift * x.c}; }
 __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   const float t = a.s + b.s, z = t - a.s;
   return {t, a.c + (((a.s - (t - z)) + (b.s - z)) + b.c)};
@@ -204,10 +208,10 @@ struct Found {
 };
 
 // The lowest j in [lo, hi) with weight whose running sum from `before` exceeds
-// `goal`; where rounding leaves none, the last j with weight; -1 where none has
+// `goal` (both `lift` times as large); where rounding leaves none, the last j with weight; -1 where none has
 // any.  All warps, 256 weights each at a time; lo a multiple of 8.
 template <int DT, bool VEC>
-__device__ int find_in(const Row& row, int lo, int hi, Pair before, Pair goal, Found& f, int warp, int lane) {
+__device__ int find_in(const Row& row, int lo, int hi, float lift, Pair before, Pair goal, Found& f, int warp, int lane) {
   int last = -1;
   for (int base = lo; base < hi; base += kAccWarps * kBlock) {
     const int j0 = base + warp * kBlock;
@@ -215,7 +219,11 @@ __device__ int find_in(const Row& row, int lo, int hi, Pair before, Pair goal, F
     weights8<DT, VEC>(row, j0 < hi ? j0 + 8 * lane : hi, 1, hi, w, err);
     Pair sum{0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = sum + Pair{w[e], err[e]};
+    for (int e = 0; e < 8; ++e) {
+      w[e] *= lift;
+      err[e] *= lift;
+      sum = sum + Pair{w[e], err[e]};
+    }
     const Pair in_warp = scan<32>(sum, lane);
     if (lane == 31) f.sum[warp] = in_warp;
     __syncthreads();
@@ -516,7 +524,9 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   __syncthreads();
   // every warp scans the warps' sums
   const Pair all_warps = scan<kAccWarps>(lane < kAccWarps ? warp_sum[lane] : Pair{0.f, 0.f}, lane);
-  const Pair whole = shfl(all_warps, kAccWarps - 1), goal = times(u_draw, whole);
+  const Pair whole = shfl(all_warps, kAccWarps - 1);
+  const float lift = lift_of(whole);
+  const Pair goal = times(u_draw, lift * whole);
   const Pair up_warp = shfl(all_warps, (warp + 31) & 31), up_lane = shfl(in_warp, (lane + 31) & 31);
   Pair run{0.f, 0.f}, last_before{0.f, 0.f};
   if (warp > 0) run = up_warp;
@@ -528,7 +538,7 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
     if (x[e].s > 0.f && first < 0) {
       last = tid * kPer + e;
       last_before = run;
-      if (next > goal) first = last;
+      if (lift * next > goal) first = last;
     }
     run = next;
   }
@@ -544,7 +554,8 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
   int answer;
   if (whole.s > 0.f) {
     const int64_t a = (int64_t)pick * size;
-    answer = find_in<DT, VEC>(row, (int)a, (int)(a + size < V ? a + size : V), pick_before, goal, found, warp, lane);
+    answer = find_in<DT, VEC>(row, (int)a, (int)(a + size < V ? a + size : V), lift, lift * pick_before, goal, found, warp,
+                             lane);
   } else {  // nothing left of the row: all of p
     row.q = nullptr;
     row.n_skip = 0;
@@ -564,7 +575,8 @@ __global__ void __launch_bounds__(kAccThreads, 3) accept_kernel(const AcceptArgs
     all = warp_sum[0];
 #pragma unroll
     for (int g = 1; g < kAccWarps; ++g) all = all + warp_sum[g];
-    answer = find_in<DT, VEC>(row, 0, V, Pair{0.f, 0.f}, times(u_draw, all), found, warp, lane);
+    const float up = lift_of(all);
+    answer = find_in<DT, VEC>(row, 0, V, up, Pair{0.f, 0.f}, times(u_draw, up * all), found, warp, lane);
   }
   if (tid == 0) args.next_token[r] = answer;
 }
