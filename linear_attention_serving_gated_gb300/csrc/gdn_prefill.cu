@@ -744,9 +744,9 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
   for (int x = t; x < 1024; x += 128)  // blocks of T above the diagonal are not written below
     reinterpret_cast<uint4*>(x < 512 ? t_hi : t_lo)[x & 511] = make_uint4(0, 0, 0, 0);
   tc::tc_fence_after();
-  const float ei = __expf(ci_hi + ci_lo);
+  const float ei = expf(ci_hi + ci_lo);
   const float ui = wide ? r : r * expf(mid);
-  const float si = krow && i < len ? r * __expf((c_last.x - ci_hi) + (c_last.y - ci_lo)) : 0.f;
+  const float si = krow && i < len ? r * expf((c_last.x - ci_hi) + (c_last.y - ci_lo)) : 0.f;
   const int top = 32 * (quad & 1) + 31;  // last row of this warp
 #pragma unroll 1
   for (int jb = 0; jb < 4; ++jb) {
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
       if (wide) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          f[e] *= __expf((ci_hi - c_hi[16 * jb + e]) + (ci_lo - c_lo[16 * jb + e]));
+          f[e] *= expf((ci_hi - c_hi[16 * jb + e]) + (ci_lo - c_lo[16 * jb + e]));
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {

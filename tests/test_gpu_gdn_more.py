@@ -97,3 +97,20 @@ def test_keys_that_share_a_direction(lengths, f16, slow):
     for n in range(len(lengths)):
         s = int(d["idx"][n])
         assert_s_close(got[s], ref_pool[s])
+
+
+@pytest.mark.parametrize("seqs", [1, 80])  # thinnest, wide
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_decay_alone_is_that_of_decode(seqs, f16, given):
+    """Sequences of one token with beta 0: the state times the decay's factor, the
+    same FP32 product as a decode's, bit for bit."""
+    d = make(23, seqs, 1, 4, seqs, f16=f16, given=given, raw_beta=False)
+    d["b"][:] = 0
+    if given:
+        d["a"] = -torch.linspace(0.0, 80.0, seqs * 4).view(seqs, 4).flip(1).contiguous()
+    _, pool = prefill(d, [1] * seqs)
+    other, o = d["pool"].cuda(), torch.zeros(seqs, 4, K, dtype=d["dt"], device="cuda")
+    kda.kda_gdn_decode_packed(d["dims"], gate_of(d), packed_of(d, seqs).cuda(), d["a"].cuda(), d["b"].cuda(), other,
+                              d["idx"].cuda(), o)
+    assert torch.equal(pool, other)
