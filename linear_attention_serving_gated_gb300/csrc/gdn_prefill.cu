@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);  // rows landed, [K; Q] K^T done, TMEM address
   const int t = threadIdx.x, quad = t >> 5, lane = t & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependency_launch();
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
     if (t == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
     return;
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(128, ChunkCfg::kCtas)
   }
   // whoever waits for this kernel waits for the one that splits FP16 rows too
   auto after_split = [] {
-    if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (F16) grid_dependency_wait();
   };
   auto leave = [&] {  // no chunk here: the grid is an upper bound
     tc::tc_fence_before();
@@ -914,7 +914,7 @@ __device__ __forceinline__ bool pick_unit(const GdnPrefillArgs& args, uint8_t* s
     if (some) s.n = order[s.n];
     __syncthreads();  // the lists lie where rows land
   }
-  if (!some) asm volatile("griddepcontrol.wait;" ::: "memory");  // as in begin_unit
+  if (!some) grid_dependency_wait();  // as in begin_unit
   return some;
 }
 
@@ -958,7 +958,7 @@ __device__ __forceinline__ bool begin_unit(const GdnPrefillArgs& args, uint8_t* 
     if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
   }
   if (stop) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for the one before too
+    grid_dependency_wait();  // whoever waits for this kernel waits for the one before too
     return false;
   }
 
@@ -1017,7 +1017,7 @@ __device__ __forceinline__ bool load_keys(const GdnPrefillArgs& args, const GdnM
   using C = Cfg<F16>;
   bool ok = true;
   const bool leader = elect_one();
-  if constexpr (F16) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (F16) grid_dependency_wait();
   int issued = 0;
   for (int c = 0; c < s.nch; ++c) {
     const int sl = c % C::kKeys;
@@ -1058,7 +1058,7 @@ __device__ __forceinline__ bool load_records(const GdnPrefillArgs& args, uint8_t
   using C = Cfg<F16>;
   bool ok = true;
   const bool leader = elect_one();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_dependency_wait();
   const uint8_t* src = args.records + (bars.chunk0 * args.HV + s.h) * kRecBytes;
   int issued = 0;
   for (int c = 0; c < s.nch; ++c) {
@@ -1648,7 +1648,7 @@ bool encode_half_rows(CUtensorMap* m, const void* base, int64_t heads, int64_t T
 // are.  One 16-byte piece of each a thread.
 __global__ void __launch_bounds__(256) split_rows_kernel(const uint4* __restrict__ q, const uint4* __restrict__ k,
                                                          int64_t n, uint4* q_hi, uint4* q_lo, uint4* k_hi, uint4* k_lo) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependency_launch();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   auto split = [i](const uint4& w, uint4* hi, uint4* lo) {
@@ -1690,30 +1690,12 @@ kda_status allow_all() {
   return KDA_OK;
 }
 
-// A launch that, if dependent, may start while the one before it runs (its kernel waits).
-template <typename Kernel>
-kda_status launch_after(Kernel kernel, unsigned grid, unsigned threads, int smem, bool dependent, cudaStream_t st,
-                        const GdnPrefillArgs& a, const GdnMaps& m) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, kernel, a, m);
-  return launch_status();
-}
-
 template <bool F16>
 kda_status launch_chunks(const GdnPrefillArgs& a, const GdnMaps& m, cudaStream_t st) {
   static_assert(ChunkCfg::kCtas * (ChunkCfg::kSmem + 1024) <= 233472, "CTAs per SM");
   const int64_t grid = a.max_chunks * a.HV;
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return launch_after(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg::kSmem, F16, st, a, m);
+  return launch_dependent(gdn_chunk_kernel<F16>, (unsigned)grid, 128, ChunkCfg::kSmem, F16, st, a, m);
 }
 
 template <bool F16, int kForm>
@@ -1721,8 +1703,8 @@ kda_status launch_state(const GdnPrefillArgs& a, const GdnMaps& m, int64_t grid,
   using C = Cfg<F16>;
   static_assert(C::kSmem <= 232448 && C::kWideSmem <= C::kSmem && kStateThreads == 768, "shared memory and registers");
   if (grid > INT32_MAX) return KDA_ERR_SHAPE;
-  return launch_after(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, kStateSmem<F16, kForm>, !stage_between(), st, a,
-                      m);
+  return launch_dependent(gdn_state_kernel<F16, kForm>, (unsigned)grid, kStateThreads, kStateSmem<F16, kForm>,
+                          !stage_between(), st, a, m);
 }
 
 // As thin as lets all CTAs start at once: 1 x 4096 tokens, 16 heads, thin 95.5 us,

@@ -141,6 +141,12 @@ __device__ __forceinline__ void st_skip_l1(float* p, float4 v) {
                : "memory");
 }
 
+// Programmatic dependent launch: the first lets the next kernel of the stream be
+// scheduled before this one ends; the second waits there for the end of the kernel
+// before and for what it wrote.  Without a dependent launch both are no-ops.
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Packed FP32 pair arithmetic (sm_100+ f32x2 instructions).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t d;

@@ -66,6 +66,25 @@ inline kda_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+// A launch that, if dependent, may start while the one before it runs (its kernel
+// waits: grid_dependency_wait).
+template <typename... Par, typename... Arg>
+kda_status launch_dependent(void (*kernel)(Par...), unsigned grid, unsigned threads, size_t smem, bool dependent,
+                            cudaStream_t st, const Arg&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch_status();
+}
+
 // Profiling aid: records stage event i (see kda_set_stage_events) on the
 // stream if one is set.
 void record_stage(int i, cudaStream_t st);

@@ -25,9 +25,6 @@ constexpr int kThreads = 256;
 constexpr int kVec = 4;  // 16-byte pieces a thread has in flight
 constexpr int kPartBytes = kThreads * kVec * 16;
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Bitmap of the used slots and the number of used slots before each word.
 struct UsedMap {
   uint32_t* bits;
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(uint8_t* used, int 
 // Compaction, first kernel: the moves.  CTAs walk over (move, layer, part).
 __global__ void __launch_bounds__(kThreads) compact_copy_kernel(const kda_pages pg, const uint8_t* used, int parts) {
   extern __shared__ uint32_t map_smem[];
-  pdl_launch();
+  grid_dependency_launch();
   const UsedMap m = build_map(used, pg.slots, map_smem);
   const int count = m.total(), below = m.used_below(count);
   const int64_t per_move = (int64_t)parts * pg.layers, total = (int64_t)(count - below) * per_move;
@@ -187,7 +184,7 @@ __global__ void __launch_bounds__(1024) compact_update_kernel(uint8_t* used, int
   extern __shared__ uint32_t map_smem[];
   const UsedMap m = build_map(used, slots, map_smem);
   const int count = m.total(), below = m.used_below(count);
-  pdl_wait();
+  grid_dependency_wait();
   for (int r = threadIdx.x; r < table_rows; r += blockDim.x) {
     const int s = table[r];
     if (s == -1) continue;
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(1024) fork_assign_kernel(uint8_t* used, int sl
                                                            int32_t* children, int32_t* err_flag) {
   extern __shared__ uint32_t map_smem[];
   __shared__ int warp_sum[32];
-  pdl_launch();
+  grid_dependency_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const UsedMap m = build_map(used, slots, map_smem);
   const int free_pages = slots - m.total();
@@ -279,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) fork_copy_kernel(const kda_pages pg,
   const int i = (int)(blockIdx.x / per_pair);
   const int64_t rest = blockIdx.x % per_pair;
   const int par = parents[i];
-  pdl_wait();
+  grid_dependency_wait();
   const int d = children[i];
   if (d >= 0) copy_part(pg, rest / parts, rest % parts, par >= 0 ? table[par] : -1, d);
 }
@@ -294,23 +291,6 @@ kda_status check_pages(const kda_pages& p) {
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// A launch that may start while the one before it runs (the kernel waits), unless
-// a stage event stands between them.
-template <typename... Par, typename... Arg>
-void launch_dependent(void (*kernel)(Par...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, Arg... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = stage_between() ? 0 : 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // The shared-memory limits of the kernels that hold a map of `bytes`.  Without
 // one a kernel gets 48 KiB, its own arrays (under 1 KiB) among them.  Set for the
@@ -390,8 +370,8 @@ extern "C" kda_status kda_pool_compact(kda_pages pages, uint8_t* used, int32_t* 
   record_stage(1, st);
   s = launch_status();
   if (s != KDA_OK) return s;
-  launch_dependent(compact_update_kernel, 1, 1024, smem, st, used, pages.slots, table, table_rows, count, err_flag);
-  s = launch_status();
+  s = launch_dependent(compact_update_kernel, 1, 1024, smem, !stage_between(), st, used, pages.slots, table, table_rows, count,
+                       err_flag);
   record_stage(2, st);
   return s;
 }
@@ -416,9 +396,8 @@ extern "C" kda_status kda_pool_fork(kda_pages pages, uint8_t* used, int32_t* tab
   record_stage(1, st);
   s = launch_status();
   if (s != KDA_OK) return s;
-  launch_dependent(fork_copy_kernel, (unsigned)(parts * pages.layers * n), kThreads, 0, st, pages,
-                   static_cast<const int32_t*>(table), parents, static_cast<const int32_t*>(children), (int)parts);
-  s = launch_status();
+  s = launch_dependent(fork_copy_kernel, (unsigned)(parts * pages.layers * n), kThreads, 0, !stage_between(), st, pages,
+                       static_cast<const int32_t*>(table), parents, static_cast<const int32_t*>(children), (int)parts);
   record_stage(2, st);
   return s;
 }

@@ -239,12 +239,9 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 
 __device__ __forceinline__ float4& f4(float* p) { return *reinterpret_cast<float4*>(p); }
 
-// Programmatic dependent launch: the chunk transform lets the state pass be
-// scheduled before it ends (its CTAs then take SMs as transform CTAs leave),
-// and the pass waits here for the transform's completion and memory before
-// it reads a record.  Without a dependent launch both are no-ops.
-__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The chunk transform lets the state pass be scheduled before it ends
+// (grid_dependency_launch: its CTAs then take SMs as transform CTAs leave), and
+// the pass waits for the transform before it reads a record.
 
 // ---------------------------------------------------------------------------
 // Per-chunk transform on tcgen05 (all chunks of all sequences in parallel).

@@ -1,7 +1,8 @@
 // kda_tc.cuh -- sm_100-family tensor-core, TMEM, mbarrier and bulk-copy
 // primitives (inline PTX) used by the prefill kernels.
 //
-// Operand layout used everywhere: BF16, K-major, 128-byte swizzle.  A tile
+// Operand layout, but where a function says otherwise (TF32 tiles, operands
+// stored MN-major): BF16 or FP16, K-major, 128-byte swizzle.  A tile
 // of R rows and K columns (K a multiple of 64) is stored as K/64 "atom
 // columns"; atom column a holds columns [64a, 64a+64) of every row, one
 // 128-byte line per row, rows consecutive, so 8 rows form a 1024-byte swizzle
