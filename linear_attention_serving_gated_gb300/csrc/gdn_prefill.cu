@@ -348,13 +348,10 @@ __device__ __forceinline__ void put_rows(uint8_t* tile, int row, int part, int l
 enum { kBarS = 2, kBarY = 3, kBarDs = 4, kBarD = 5, kBarSq = 6, kBarPast = 7 };
 template <int WARPS>
 __device__ __forceinline__ void barrier_arrive(int id, bool ok) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "@p barrier.cta.arrive %0, %1;\n\t"
-      "@!p barrier.cta.sync %0, %1;\n\t}" ::"r"(id),
-      "n"(32 * (WARPS + 1)), "r"(static_cast<uint32_t>(ok))
-      : "memory");
+  if (ok)
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(32 * (WARPS + 1)) : "memory");
+  else
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(32 * (WARPS + 1)) : "memory");
 }
 template <bool TMEM, int WARPS>
 __device__ __forceinline__ void chain_arrive(int id, bool ok) {
