@@ -339,12 +339,16 @@ typedef struct {
  *                 (kda_dims.dtype), without it the FP32 log-decay.  A value
  *                 below -128 counts as -128 (its factor is zero in FP32).
  *   beta          [gb_rows, HV] 16-bit: raw beta (beta_is_raw) or beta.
+ * A NaN or an infinity among a token's inputs reaches the outputs of all 64
+ * tokens of its chunk, and the sequence's state; other sequences it does not.
  * intermediate and intermediate_chunks as kda_prefill's: the state at the
  * start of every 64-token chunk.  workspace: kda_gdn_prefill_workspace_size
  * bytes, 16-byte aligned:
  *   (total_tokens / 64 + num_seqs) * HV * 33792      a record per (chunk, head)
  *   + 4 * align256(total_tokens * H * 256)           FP16 only: q, k in BF16 halves
- * (SIZE_MAX for more than INT32_MAX tokens).  The first call on each device
+ * (SIZE_MAX for more than INT32_MAX tokens): 528 bytes a token and value head,
+ * 2.2 GB for 131072 tokens and 32 heads.  A sequence may be prefilled in parts,
+ * each from the state that the one before left.  The first call on each device
  * sets the kernels' shared-memory limits; make it before capturing calls into
  * a CUDA graph.
  */

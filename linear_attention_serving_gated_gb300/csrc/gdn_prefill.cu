@@ -47,14 +47,21 @@
 // thinnest and 2.8 in the wide one, which does four times as many columns as the
 // first: sequences that the SMs would wait for are as thin as they leave room
 // for, the rest are wide (launch_states, pick_unit).
-// Measured (whole call, in a graph): 1 x 4096 tokens, 16 heads, 95.5 us (8 heads
-// 78), of which the chunk kernel 18; 8 x 4096 314; 16980 tokens in 8 sequences
-// with one of 8087 260; 1 x 128, 4 heads 11.
-// Precision: FP32 operands are split in two BF16 halves (hi + lo, 2^-16 left)
-// wherever the state depends on them, S, T, Y and D'.  So are P and D for the
-// output: Q S and P D cancel where the state repeats what it is written, so that
-// one rounding of P to BF16 showed up as 2 per cent of the outputs' RMS.  K and Q
-// are BF16 already.  FP16 K and Q are taken as they are for [K; Q] K^T; beside S
+// Measured (whole call, in a graph): 1 x 4096 tokens, 16 heads, 96 us (8 heads
+// 79), of which 18 pass before the chain starts; 8 x 4096 313; 16980 tokens in 8
+// sequences with one of 8087 255; 1 x 128, 4 heads 11.  The chunk kernel alone: 23,
+// 132 and 76 us of the first three.
+// Precision: the state is FP32, in registers and in the pool.  As operands, S, T, Y
+// and D' (and A in the inverse) are split in two BF16 halves, hi + lo, which leaves
+// 2^-18; the products of two lo halves, 2^-18 again, are left out in the inverse and
+// in the wide form.  States come out 4.6e-6 of their RMS off (an FP32 loop 1.6e-7),
+// for keys that share nine tenths of a direction with beta near 1 up to 2.1e-5, the
+// largest element 2.4e-4 of the RMS; the framework's bound for FP32 states is 1e-3,
+// and outputs are rounded to 2^-9 or 2^-12.  A third half of T, Y and D' would take
+// the wide form to 544 of TMEM's 512 columns and the FP16 form to 251 of 227 KB of
+// shared memory.  P and D are split for the output: Q S and P D cancel where the
+// state repeats what it is written, so that one rounding of P to BF16 showed up as 2
+// per cent of the outputs' RMS.  K and Q are BF16 already.  FP16 K and Q are taken as they are for [K; Q] K^T; beside S
 // and D', whose range is not FP16's, they are split exactly (11 bits into 8 + 8)
 // by a pass over them that runs beside the chunk kernel.
 #include <atomic>
@@ -431,7 +438,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
 // from l0).  T11 is lower triangular, so the blocks above column block c0 are
 // skipped, and those of T22 right of row block r0.  (A21 T11)^T comes out of the
 // first products in the layout in which the second ones take it.  Every factor
-// is a BF16 pair; lo lo is left out (2^-16).
+// is a BF16 pair; lo lo is left out (2^-18).
 template <int KB>
 __device__ __forceinline__ void inverse_block(uint8_t* t_hi, uint8_t* t_lo, const uint8_t* a_hi, const uint8_t* a_lo,
                                               int k0, int l0, int r0, int c0, int lane) {
