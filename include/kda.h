@@ -496,6 +496,111 @@ kda_status kda_pool_fork(kda_pages pages, uint8_t *used, int32_t *table, int tab
                          const int32_t *parents, const int32_t *rows, int n, int32_t *children,
                          int32_t *err_flag, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with one decay per value head.
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ *
+ * in kda_scalar_gate's terms (beta_is_raw is not read):
+ *   a with A_log       g = -exp(A_log[h]) * softplus(a + dt_bias[h]), a 16-bit
+ *   a without A_log    g = a, FP32
+ *   a NULL             g = -exp(A_log[h]) for every token; dt_bias is not read
+ * A log-decay below -128 counts as -128 (its factor is zero in FP32), one above
+ * 0 as 0.  Token tensors, heads, pool, slots, snapshots, error bits and the rules
+ * of capture are those of the calls above; kda_commit takes these verifies'
+ * snapshots.
+ */
+
+/*
+ * Varlen prefill from an indexed initial-state pool, as kda_gdn_prefill without
+ * beta and chunk-start states.
+ *   a             [gate_rows, HV] or NULL, gate_rows >= total_tokens
+ * A NaN or an infinity among a token's inputs reaches the outputs of all 64
+ * tokens of its chunk, and the sequence's state; other sequences it does not.
+ * A sequence may be prefilled in parts, each from the state that the one before
+ * left.  workspace: kda_lin_prefill_workspace_size bytes, 256-byte aligned.  The
+ * first call on each device comes before capture.
+ */
+size_t kda_lin_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens);
+kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *q,
+                           const kda_bf16 *k, const kda_bf16 *v, const void *a, int64_t gate_rows,
+                           float *state_pool, int pool_slots, const int32_t *state_idx,
+                           const int32_t *cu_seqlens, int num_seqs, int64_t total_tokens,
+                           kda_bf16 *o, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                           void *stream);
+
+/*
+ * Packed single-token decode, chain verify and tree verify: as the kda_gdn_*
+ * calls without beta, a [rows, HV] or NULL.
+ */
+kda_status kda_lin_decode_packed(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *mixed_qkv,
+                                 int64_t row_stride, const void *a, int B, float *state_pool,
+                                 int pool_slots, const int32_t *state_idx, kda_bf16 *o,
+                                 int32_t *err_flag, void *stream);
+kda_status kda_lin_verify_chain(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *mixed_qkv,
+                                int64_t row_stride, const void *a, int B, int T,
+                                const float *state_pool, int pool_slots, const int32_t *state_idx,
+                                kda_bf16 *o, float *snapshots, int32_t *err_flag, void *stream);
+kda_status kda_lin_verify_tree(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *mixed_qkv,
+                               int64_t row_stride, const void *a, int B, int T,
+                               const int32_t *parent_idx, const float *state_pool, int pool_slots,
+                               const int32_t *state_idx, kda_bf16 *o, float *snapshots,
+                               int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens, with the entropy of their distributions
+ * and their top alternatives: of rows of logits x, with z = sum_j exp(x_j),
+ *   logprobs[r]  = x[tokens[r]] - log z
+ *   entropy[r]   = - sum_j p_j log p_j,  p_j = exp(x_j) / z     (nats)
+ * Sums are FP32 (32 terms one after the other, then rescaled partial sums).
+ *   logits        `vocab` elements a row, rows logits_stride elements apart, of
+ *                 type KDA_DTYPE_F32, KDA_DTYPE_BF16 or KDA_DTYPE_F16.  -inf (a
+ *                 masked token) and NaN have no probability, +inf counts as the
+ *                 largest FP32 number.
+ *   tokens        [rows] int32; -1 marks a row that nothing is asked of: its
+ *                 outputs are 0, its alternatives -1.  Others outside [0, vocab)
+ *                 set KDA_DEVERR_TOKEN and count as -1.
+ *   logprobs      [rows] FP32 out; -inf for a token without probability
+ *   entropy       [rows] FP32 out, or NULL; 0 where no token has a probability
+ *   top           alternatives a row, 0 to KDA_LOGPROBS_MAX_TOP
+ *   top_tokens    [rows, top] int32 out: the tokens of the largest logits, the
+ *                 largest first, the lowest token first among equals; -1 where
+ *                 fewer tokens have a probability
+ *   top_logprobs  [rows, top] FP32 out: their log probabilities, -inf with -1
+ */
+#define KDA_LOGPROBS_MAX_TOP 32 /* more: KDA_ERR_UNSUPPORTED, as more than KDA_ACCEPT_MAX_VOCAB tokens */
+kda_status kda_token_logprobs(int logits_dtype, const void *logits, int64_t logits_stride,
+                              const int32_t *tokens, int rows, int vocab, float *logprobs,
+                              float *entropy, int top, int32_t *top_tokens, float *top_logprobs,
+                              int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages kept in 8 or 4 bits: states of ended requests or of common beginnings,
+ * in a quarter or less of their memory.  A group of FP32 values (128 in 8 bits,
+ * 32 in 4, consecutive in the page) shares one FP32 scale:
+ *   scale = max |x| / top,  code = x / scale rounded to nearest (ties to even) in
+ *   [-top, top],            value = code * scale;   top = 127 in 8 bits, 7 in 4.
+ * A value comes back within half a scale, 1/254 (1/14) of its group's largest.
+ * Both are exact: codes follow from the FP32 scale without a rounding in between.
+ * A group with an infinity or a NaN comes back as NaN throughout.
+ * Pages are FP32: page_bytes a multiple of 512 (else KDA_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  void *codes;   /* [slots, layers, page_bytes / 4 values] of 8 or 4 bits, 16-byte aligned; of two
+                    4-bit codes in a byte the first is the low one */
+  float *scales; /* [slots, layers, groups of a page], 16-byte aligned */
+  int bits;      /* 8 or 4 (else KDA_ERR_UNSUPPORTED) */
+  int slots;     /* pages that the archive holds */
+} kda_archive;
+
+/* archive page dst[i] <- pool page src[i] (load: pool page dst[i] <- archive page
+ * src[i]), i < n; a -1 in either skips the pair.  A pair whose dst is another's
+ * too, or with a page out of range, sets KDA_DEVERR_PAGE and is not copied. */
+kda_status kda_pool_store(kda_pages pages, kda_archive archive, const int32_t *src,
+                          const int32_t *dst, int n, int32_t *err_flag, void *stream);
+kda_status kda_pool_load(kda_pages pages, kda_archive archive, const int32_t *src,
+                         const int32_t *dst, int n, int32_t *err_flag, void *stream);
+
 /*
  * Profiling aid (not part of the pages' contract): per-kernel timing of every
  * entry point.  After kda_set_stage_events(ev) with three cudaEvent_t

@@ -1,0 +1,202 @@
+// kda_archive.cu -- pages of a state pool kept in 8 or 4 bits, and read back.
+//
+// A group of values x (128 in 8 bits, 32 in 4) shares an FP32 scale:
+//   scale = max|x| / top,  code = x / scale rounded to nearest, ties to even,
+// top = 127 or 7; read back, a value is code * scale.  Bound by HBM: 4 bytes read
+// and 1.03 (0.625) written a value, and the other way round.  A warp takes rows of
+// 128 values, four a lane, eight rows with all their loads in flight; the largest
+// magnitude of a row is one warp reduction of bit patterns, that of a group of 32
+// three exchanges.
+#include "kda_host.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256, kRowsPerWarp = 8, kRow = 128;
+constexpr int kPartRows = kThreads / 32 * kRowsPerWarp;  // rows of a CTA: 32 KB of a page
+
+struct ArchiveArgs {
+  kda_pages pages;
+  uint8_t* codes;
+  float* scales;
+  int slots;
+  const int32_t *src, *dst;
+  int n;
+  int64_t rows;  // of 128 values, of a page in one layer
+  int parts;     // CTAs of such a page
+  int32_t* err_flag;
+};
+
+// What a CTA works on; false: nothing.  A pair whose destination another pair
+// has too is refused, like one that is out of range.
+struct Work {
+  int src, dst;
+  int64_t layer, row0;  // this warp's first row
+};
+__device__ __forceinline__ bool find_work(const ArchiveArgs& a, int src_slots, int dst_slots, Work& w) {
+  const int64_t per_pair = (int64_t)a.parts * a.pages.layers;
+  const int i = (int)(blockIdx.x / per_pair);
+  const int64_t rest = blockIdx.x % per_pair;
+  w.src = a.src[i];
+  w.dst = a.dst[i];
+  if (w.src == -1 || w.dst == -1) return false;
+  bool bad = w.src < 0 || w.dst < 0 || w.src >= src_slots || w.dst >= dst_slots;
+  for (int j = threadIdx.x; j < a.n && !bad; j += kThreads) bad |= j != i && a.src[j] != -1 && a.dst[j] == w.dst;
+  if (__syncthreads_or(bad)) {
+    if (rest == 0 && threadIdx.x == 0) set_error(a.err_flag, KDA_DEVERR_PAGE);
+    return false;
+  }
+  w.layer = rest / a.parts;
+  w.row0 = rest % a.parts * kPartRows + (int64_t)(threadIdx.x >> 5) * kRowsPerWarp;
+  return true;
+}
+
+// Codes of four values.  x times 1 / scale may fall on the wrong side of a half;
+// the remainder x - c scale is exact (a whole number of the operands' last places,
+// below the scale), and settles it.
+__device__ __forceinline__ int code_of(float x, float scale, float inv, float top) {
+  float c = rintf(x * inv);
+  const float r = fmaf(-c, scale, x), twice = 2.f * fabsf(r);
+  const bool odd = (__float2int_rn(c) & 1) != 0;
+  if (twice > scale || (twice == scale && odd)) c += copysignf(1.f, r);
+  return __float2int_rn(fminf(fmaxf(c, -top), top));
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveArgs a) {
+  constexpr float kTop = BITS == 8 ? 127.f : 7.f;
+  Work w;
+  if (!find_work(a, a.pages.slots, a.slots, w)) return;
+  const int lane = threadIdx.x & 31;
+  const float4* page = reinterpret_cast<const float4*>(static_cast<const char*>(a.pages.base) + w.layer * a.pages.layer_stride +
+                                                       (int64_t)w.src * a.pages.page_bytes);
+  const int64_t to = ((int64_t)w.dst * a.pages.layers + w.layer) * a.rows;  // the archive's row of row 0
+  float4 x[kRowsPerWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i)
+    x[i] = w.row0 + i < a.rows ? __ldcs(page + (w.row0 + i) * (kRow / 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float mine = 0.f;  // the scale that this lane stores
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    const uint32_t b0 = __float_as_uint(x[i].x) & 0x7fffffffu, b1 = __float_as_uint(x[i].y) & 0x7fffffffu,
+                   b2 = __float_as_uint(x[i].z) & 0x7fffffffu, b3 = __float_as_uint(x[i].w) & 0x7fffffffu;
+    uint32_t m = max(max(b0, b1), max(b2, b3));
+    if (BITS == 8) {
+      m = __reduce_max_sync(0xffffffffu, m);
+    } else {
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    }
+    // a group that holds an infinity or a NaN reads back as NaN
+    const bool finite = m < 0x7f800000u;
+    const float scale = finite ? __fdiv_rn(__uint_as_float(m), kTop) : __uint_as_float(0x7fffffffu);
+    int c[4] = {0, 0, 0, 0};
+    const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    if (finite && scale >= 1e-37f) {
+      const float inv = __frcp_rn(scale);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = code_of(v[e], scale, inv, kTop);
+    } else if (finite && scale > 0.f) {  // 1 / scale may be out of range; such quotients have few places and are exact enough to round
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = __double2int_rn(fmin(fmax((double)v[e] / (double)scale, -(double)kTop), (double)kTop));
+    }
+    const int64_t row = to + w.row0 + i;
+    if (w.row0 + i < a.rows) {
+      if (BITS == 8)
+        reinterpret_cast<uint32_t*>(a.codes)[row * (kRow / 4) + lane] =
+            (c[0] & 0xffu) | (c[1] & 0xffu) << 8 | (c[2] & 0xffu) << 16 | (uint32_t)(c[3] & 0xff) << 24;
+      else
+        reinterpret_cast<uint16_t*>(a.codes)[row * (kRow / 4) + lane] =
+            (uint16_t)((c[0] & 15) | (c[1] & 15) << 4 | (c[2] & 15) << 8 | (c[3] & 15) << 12);
+    }
+    if (BITS == 8) {
+      if (lane == i) mine = scale;
+    } else {
+      const float s = __shfl_sync(0xffffffffu, scale, 8 * (lane & 3));
+      if (lane >> 2 == i) mine = s;
+    }
+  }
+  if (BITS == 8) {
+    if (lane < kRowsPerWarp && w.row0 + lane < a.rows) a.scales[to + w.row0 + lane] = mine;
+  } else {
+    if (w.row0 + (lane >> 2) < a.rows) a.scales[(to + w.row0) * 4 + lane] = mine;
+  }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) archive_load_kernel(const ArchiveArgs a) {
+  Work w;
+  if (!find_work(a, a.slots, a.pages.slots, w)) return;
+  const int lane = threadIdx.x & 31;
+  float4* page = reinterpret_cast<float4*>(static_cast<char*>(a.pages.base) + w.layer * a.pages.layer_stride +
+                                           (int64_t)w.dst * a.pages.page_bytes);
+  const int64_t from = ((int64_t)w.src * a.pages.layers + w.layer) * a.rows;
+  uint32_t c[kRowsPerWarp];
+  float s[kRowsPerWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    const int64_t row = from + w.row0 + i;
+    c[i] = 0;
+    s[i] = 0.f;
+    if (w.row0 + i < a.rows) {
+      if (BITS == 8) {
+        c[i] = __ldcs(reinterpret_cast<const uint32_t*>(a.codes) + row * (kRow / 4) + lane);
+        s[i] = __ldcs(a.scales + row);
+      } else {
+        c[i] = __ldcs(reinterpret_cast<const uint16_t*>(a.codes) + row * (kRow / 4) + lane);
+        s[i] = __ldcs(a.scales + row * 4 + (lane >> 3));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (w.row0 + i >= a.rows) continue;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int code = BITS == 8 ? (int)(c[i] << (24 - 8 * e)) >> 24 : (int)(c[i] << (28 - 4 * e)) >> 28;
+      v[e] = (float)code * s[i];
+    }
+    page[(w.row0 + i) * (kRow / 4) + lane] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+kda_status run_archive(const kda_pages& pg, const kda_archive& ar, const int32_t* src, const int32_t* dst, int n,
+                       int32_t* err_flag, void* stream, bool store) {
+  if (ar.bits != 8 && ar.bits != 4) return KDA_ERR_UNSUPPORTED;
+  if (!pg.base || !ar.codes || !ar.scales) return KDA_ERR_NULL_ARG;
+  if (pg.slots < 1 || pg.layers < 1 || pg.page_bytes < 1 || pg.layer_stride < 0 || ar.slots < 1 || n < 0) return KDA_ERR_SHAPE;
+  if (!aligned16(pg.base) || pg.layer_stride % 16 != 0 || !aligned16(ar.codes) || !aligned16(ar.scales)) return KDA_ERR_ALIGNMENT;
+  if (pg.page_bytes % (kRow * 4) != 0) return KDA_ERR_UNSUPPORTED;
+  if (pg.page_bytes > INT64_MAX / pg.slots || (pg.layers > 1 && pg.layer_stride < pg.page_bytes * pg.slots)) return KDA_ERR_SHAPE;
+  if (n == 0) return KDA_OK;
+  if (!src || !dst) return KDA_ERR_NULL_ARG;
+  ArchiveArgs a{pg, static_cast<uint8_t*>(ar.codes), ar.scales, ar.slots, src, dst, n, pg.page_bytes / (kRow * 4), 0, err_flag};
+  const int64_t parts = (a.rows + kPartRows - 1) / kPartRows;
+  if (parts > INT32_MAX || parts * pg.layers > INT32_MAX / n) return KDA_ERR_SHAPE;
+  a.parts = (int)parts;
+  const unsigned grid = (unsigned)(parts * pg.layers * n);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  record_stage(0, st);
+  if (store)
+    (ar.bits == 8 ? archive_store_kernel<8> : archive_store_kernel<4>)<<<grid, kThreads, 0, st>>>(a);
+  else
+    (ar.bits == 8 ? archive_load_kernel<8> : archive_load_kernel<4>)<<<grid, kThreads, 0, st>>>(a);
+  const kda_status s = launch_status();
+  record_stage(1, st);
+  record_stage(2, st);
+  return s;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_pool_store(kda_pages pages, kda_archive archive, const int32_t* src, const int32_t* dst, int n,
+                                     int32_t* err_flag, void* stream) {
+  return kda::run_archive(pages, archive, src, dst, n, err_flag, stream, true);
+}
+
+extern "C" kda_status kda_pool_load(kda_pages pages, kda_archive archive, const int32_t* src, const int32_t* dst, int n,
+                                    int32_t* err_flag, void* stream) {
+  return kda::run_archive(pages, archive, src, dst, n, err_flag, stream, false);
+}

@@ -69,12 +69,18 @@ class kda_pages(ctypes.Structure):
                 ("layers", ctypes.c_int), ("slots", ctypes.c_int)]
 
 
+class kda_archive(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("bits", ctypes.c_int), ("slots", ctypes.c_int)]
+
+
 EXPORTS = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill", "kda_decode_packed",
            "kda_verify_chain", "kda_verify_tree", "kda_commit", "kda_set_stage_events",
            "kda_prefill_noalloc", "kda_replay_ring_bytes", "kda_verify_chain_replay",
            "kda_commit_replay", "kda_gdn_prefill_workspace_size", "kda_gdn_prefill", "kda_gdn_decode_packed", "kda_gdn_verify_chain",
            "kda_gdn_verify_tree", "kda_accept_chain", "kda_accept_tree", "kda_pool_copy", "kda_pool_free",
-           "kda_pool_compact", "kda_pool_fork")
+           "kda_pool_compact", "kda_pool_fork", "kda_lin_prefill_workspace_size", "kda_lin_prefill",
+           "kda_lin_decode_packed", "kda_lin_verify_chain", "kda_lin_verify_tree", "kda_token_logprobs",
+           "kda_pool_store", "kda_pool_load")
 
 PREFILL_STATIC_SCRATCH_BYTES = 128 << 20  # KDA_PREFILL_STATIC_SCRATCH_BYTES in include/kda.h
 
@@ -143,6 +149,23 @@ def load(path: str = LIB_PATH):
         lib.kda_pool_compact.argtypes = [kda_pages, vp, vp, i32, vp, vp, vp]
         lib.kda_pool_fork.restype = i32
         lib.kda_pool_fork.argtypes = [kda_pages, vp, vp, i32, vp, vp, i32, vp, vp, vp]
+        lib.kda_lin_prefill_workspace_size.restype = sz
+        lib.kda_lin_prefill_workspace_size.argtypes = [kda_dims, i32, i64]
+        lib.kda_lin_prefill.restype = i32
+        lib.kda_lin_prefill.argtypes = [kda_dims, kda_scalar_gate, vp, vp, vp, vp, i64, vp, i32, vp, vp, i32, i64, vp,
+                                        vp, sz, vp, vp]
+        lib.kda_lin_decode_packed.restype = i32
+        lib.kda_lin_decode_packed.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, i32, vp, i32, vp, vp, vp, vp]
+        lib.kda_lin_verify_chain.restype = i32
+        lib.kda_lin_verify_chain.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+        lib.kda_lin_verify_tree.restype = i32
+        lib.kda_lin_verify_tree.argtypes = [kda_dims, kda_scalar_gate, vp, i64, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp,
+                                            vp]
+        lib.kda_token_logprobs.restype = i32
+        lib.kda_token_logprobs.argtypes = [i32, vp, i64, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp]
+        for call in (lib.kda_pool_store, lib.kda_pool_load):
+            call.restype = i32
+            call.argtypes = [kda_pages, kda_archive, vp, vp, i32, vp, vp]
         lib.kda_set_stage_events.restype = None
         lib.kda_set_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
         _lib = lib
@@ -718,3 +741,161 @@ def kda_pool_fork(pool, used, table, parents, rows, children=None, err_flag=None
     if st:
         _check(st, "kda_pool_fork")
     return children
+
+
+# -- linear attention with one decay per value head ---------------------------
+
+
+def _lin_gate_rows(d, gate, a, rows):
+    """The gate input [>= rows, HV], or None where the heads' decay is fixed."""
+    return None if a is None else _gate_rows(d, gate, a, rows)
+
+
+def kda_lin_prefill_workspace_size(d: kda_dims, num_seqs: int, total_tokens: int) -> int:
+    return int(load().kda_lin_prefill_workspace_size(d, int(num_seqs), int(total_tokens)))
+
+
+def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_seqlens, num_seqs, o, workspace=None,
+                    err_flag=None, stream=None):
+    """Varlen prefill (see kda.h).  q,k [T,H,K], v [T,HV,V], a [gate_rows,HV] or
+    None (a head's decay is -exp(A_log) for every token); state_pool
+    [slots,HV,V,K] fp32 (in place); o [T,HV,V] (written)."""
+    lib, t16 = load(), _t16(d)
+    T, n = q.shape[0], int(num_seqs)
+    gate_rows = T if a is None else a.shape[0]
+    HK, HVV = d.H * d.K, d.HV * d.V
+    slots = _pool_slots(d, state_pool)
+    if workspace is None:
+        workspace = _new(max(int(lib.kda_lin_prefill_workspace_size(d, n, T)), 1), torch.uint8, q.device, stream)
+    st = lib.kda_lin_prefill(
+        d, gate.c(d), _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
+        _arg(v, t16, T * HVV, "v", "[T, HV, V]"), _lin_gate_rows(d, gate, a, gate_rows), gate_rows,
+        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), slots,
+        _arg(state_idx, torch.int32, n, "state_idx", "[num_seqs]"),
+        _opt(cu_seqlens, torch.int32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
+        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_lin_prefill")
+
+
+def kda_lin_decode_packed(d, gate: ScalarGate, mixed_qkv, a, state_pool, state_idx, o, err_flag=None, stream=None):
+    """One token per request, state in place; a [B, HV] or None."""
+    B = mixed_qkv.shape[0]
+    st = load().kda_lin_decode_packed(
+        d, gate.c(d), _gdn_rows(d, mixed_qkv, B), mixed_qkv.stride(0), _lin_gate_rows(d, gate, a, B), B,
+        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), _pool_slots(d, state_pool),
+        _arg(state_idx, torch.int32, B, "state_idx", "[B]"), _arg(o, _t16(d), B * d.HV * d.V, "o", "[B, HV, V]"),
+        _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_lin_decode_packed")
+
+
+def _lin_verify(name, call, d, gate, mixed_qkv, a, B, T, parents, state_pool, state_idx, o, snapshots, err_flag, stream):
+    B, T = int(B), int(T)
+    rows = B * T
+    st = call(
+        d, gate.c(d), _gdn_rows(d, mixed_qkv, rows), mixed_qkv.stride(0), _lin_gate_rows(d, gate, a, rows), B, T, *parents,
+        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), _pool_slots(d, state_pool),
+        _arg(state_idx, torch.int32, B, "state_idx", "[B]"), _arg(o, _t16(d), rows * d.HV * d.V, "o", "[B, T, HV, V]"),
+        _arg(snapshots, torch.float32, rows * d.HV * d.V * d.K, "snapshots", "[B, T, HV, V, K]"), _err(err_flag),
+        _cur(stream))
+    if st:
+        _check(st, name)
+
+
+def kda_lin_verify_chain(d, gate: ScalarGate, mixed_qkv, a, B, T, state_pool, state_idx, o, snapshots, err_flag=None,
+                         stream=None):
+    """Chain verify; snapshots as kda_verify_chain's, for kda_commit."""
+    _lin_verify("kda_lin_verify_chain", load().kda_lin_verify_chain, d, gate, mixed_qkv, a, B, T, (), state_pool, state_idx,
+                o, snapshots, err_flag, stream)
+
+
+def kda_lin_verify_tree(d, gate: ScalarGate, mixed_qkv, a, B, T, parent_idx, state_pool, state_idx, o, snapshots,
+                        err_flag=None, stream=None):
+    """Tree verify; parent_idx [B, T] int32."""
+    _lin_verify("kda_lin_verify_tree", load().kda_lin_verify_tree, d, gate, mixed_qkv, a, B, T,
+                (_arg(parent_idx, torch.int32, B * T, "parent_idx", "[B, T]"),), state_pool, state_idx, o, snapshots,
+                err_flag, stream)
+
+
+# -- log probabilities of given tokens -----------------------------------------
+
+
+def kda_token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, top_logprobs=None, err_flag=None,
+                       stream=None):
+    """Log probabilities of tokens [rows] int32 under logits [rows, vocab] (float32,
+    bfloat16 or float16, rows possibly padded), see kda.h.  Written: logprobs
+    [rows] fp32; entropy [rows] fp32, top_tokens [rows, top] int32 and
+    top_logprobs [rows, top] fp32 where given."""
+    if logits.dim() != 2 or tokens.dim() != 1 or tokens.shape[0] != logits.shape[0]:
+        raise ValueError(f"logits must be [rows, vocab] and tokens [rows] (got {tuple(logits.shape)}, {tuple(tokens.shape)})")
+    if logits.dtype not in _PROBS:
+        raise TypeError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
+    rows, V = logits.shape
+    stride = logits.stride(0) if rows > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or stride < V:
+        raise ValueError(f"the rows of logits must be dense (got strides {logits.stride()})")
+    if not logits.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    top = 0
+    if top_tokens is not None or top_logprobs is not None:
+        if top_tokens is None or top_logprobs is None or top_tokens.dim() != 2 or top_tokens.shape != top_logprobs.shape or \
+                top_tokens.shape[0] != rows:
+            raise ValueError("top_tokens and top_logprobs must both be [rows, top]")
+        top = top_tokens.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    st = load().kda_token_logprobs(
+        _PROBS[logits.dtype], logits.data_ptr(), stride, _arg(tokens, i32, rows, "tokens", "[rows]"), rows, V,
+        _arg(logprobs, f32, rows, "logprobs", "[rows]"), _opt(entropy, f32, rows, "entropy", "[rows]"), top,
+        _opt(top_tokens, i32, rows * top, "top_tokens", "[rows, top]"),
+        _opt(top_logprobs, f32, rows * top, "top_logprobs", "[rows, top]"), _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_token_logprobs")
+
+
+# -- pages kept in 8 or 4 bits ---------------------------------------------------
+
+
+def _archive(pool, codes, scales):
+    """Pages of a pool, and the archive that keeps them: codes int8
+    [slots, layers, .., K] (8 bits) or uint8 [slots, layers, .., K / 2] (4 bits,
+    two codes a byte), scales fp32 with a scale for every 128 or 32 values."""
+    if pool.dtype is not torch.float32:
+        raise TypeError(f"pool must be float32 (got {pool.dtype})")
+    if codes.dtype is not torch.int8 and codes.dtype is not torch.uint8:
+        raise TypeError(f"codes must be int8 (8 bits) or uint8 (4 bits) (got {codes.dtype})")
+    pages = _pages(pool)
+    bits, group = (8, 128) if codes.dtype is torch.int8 else (4, 32)
+    values = pages.layers * (pages.page_bytes // 4)
+    slots = codes.shape[0] if codes.dim() > 0 else 0
+    n = values * bits // 8
+    if slots and codes.numel() != slots * n or slots != (scales.shape[0] if scales.dim() > 0 else 0) or \
+            scales.numel() * group != slots * values:
+        raise ValueError(f"codes and scales must hold {n} bytes and {values // group} scales a page "
+                         f"(got {tuple(codes.shape)}, {tuple(scales.shape)})")
+    return pages, kda_archive(_arg(codes, codes.dtype, 0, "codes", "[slots, layers, ..]"),
+                              _arg(scales, torch.float32, 0, "scales", "[slots, layers, ..]"), bits, slots)
+
+
+def kda_pool_store(pool, codes, scales, src, dst, err_flag=None, stream=None):
+    """Archive page dst[i] <- pool[:, src[i]]; pool [layers, slots, ...] fp32, codes
+    and scales as in _archive."""
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError("src and dst must have one length")
+    pages, archive = _archive(pool, codes, scales)
+    st = load().kda_pool_store(pages, archive, _list(src, "src"), _list(dst, "dst"), n, _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_pool_store")
+
+
+def kda_pool_load(codes, scales, pool, src, dst, err_flag=None, stream=None):
+    """pool[:, dst[i]] <- archive page src[i]."""
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError("src and dst must have one length")
+    pages, archive = _archive(pool, codes, scales)
+    st = load().kda_pool_load(pages, archive, _list(src, "src"), _list(dst, "dst"), n, _err(err_flag), _cur(stream))
+    if st:
+        _check(st, "kda_pool_load")

@@ -147,3 +147,66 @@ def pool_fork(pool, used, table, parents, rows):
         used[d], table[r] = 1, d
         pool[:, d] = pool[:, before[p]] if p >= 0 else 0
     return missed
+
+
+def lin_decay(rows, a=None, A_log=None, dt_bias=None):
+    """Log-decay of every token and value head of linear attention [rows,HV]."""
+    if a is None:
+        g = np.repeat(-np.exp(np.asarray(A_log, np.float64))[None], rows, 0)
+    else:
+        g = np.asarray(a, np.float64)[:rows]
+        if A_log is not None:
+            g = -np.exp(np.asarray(A_log, np.float64)) * np.logaddexp(0, g + (0 if dt_bias is None else np.asarray(dt_bias, np.float64)))
+    return np.clip(g, -128, 0)  # a NaN stays one
+
+
+def lin_unit(x, l2norm):
+    x = np.asarray(x, np.float64)
+    return x / np.sqrt((x * x).sum(-1, keepdims=True) + 1e-6) if l2norm else x
+
+
+def lin_sequence(S, q, k, v, g, scale, l2norm=True, parents=None):
+    """Linear attention over tokens in order (or a tree): S [HV,V,K], q,k [T,H,K],
+    v [T,HV,V], log-decays g [T,HV].  Outputs [T,HV,V], states [T,HV,V,K]."""
+    S, v = np.asarray(S, np.float64), np.asarray(v, np.float64)
+    G = S.shape[0] // q.shape[1]
+    q, k = (np.repeat(lin_unit(x, l2norm), G, 1) for x in (q, k))
+    states, outs = [], []
+    for t in range(len(q)):
+        p = t - 1 if parents is None else parents[t]
+        S_t = np.exp(g[t])[:, None, None] * (S if p < 0 else states[p]) + v[t][:, :, None] * k[t][:, None, :]
+        states.append(S_t)
+        outs.append(scale * np.einsum("hvk,hk->hv", S_t, q[t]))
+    return np.array(outs), np.array(states)
+
+
+def logprobs(x, token, top):
+    """(log probability, entropy, top tokens, their log probabilities) of one row
+    of logits."""
+    x = np.asarray(x, np.float64)
+    x = np.where(np.isnan(x), -np.inf, np.minimum(x, float(np.finfo(np.float32).max)))
+    tokens, lps = np.full(top, -1), np.full(top, -np.inf)
+    if x.max() == -np.inf:
+        return -np.inf, 0.0, tokens, lps
+    p = np.exp(x - x.max())
+    lp = x - x.max() - np.log(p.sum())
+    p /= p.sum()
+    order = np.argsort(-x, kind="stable")[:top]
+    order = order[x[order] > -np.inf]
+    tokens[:len(order)], lps[:len(order)] = order, lp[order]
+    return lp[token], -float((p[p > 0] * lp[p > 0]).sum()), tokens, lps
+
+
+def archived(x, bits):
+    """(codes, scales, values read back) of FP32 values x [n, 128]."""
+    top, group = (127, 128) if bits == 8 else (7, 32)
+    y = np.asarray(x, np.float32).astype(np.float64).reshape(-1, group)
+    bad = ~np.isfinite(y).all(1)
+    y[bad] = 0
+    scale = (np.abs(y).max(1) / top).astype(np.float32)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        c = np.where(scale[:, None] > 0, np.rint(y / scale.astype(np.float64)[:, None]), 0)
+    c = np.clip(c, -top, top)
+    scale[bad] = np.nan
+    value = c.astype(np.float32) * scale[:, None]
+    return c.reshape(x.shape).astype(np.int8), scale.reshape(len(x), -1), value.reshape(x.shape)

@@ -1,0 +1,93 @@
+"""Inputs, the FP64 oracle's answers and error bounds for linear attention with
+one decay per value head.
+
+Bounds, element by element, from sums of magnitudes.  With u the half step of
+the 16-bit type (BF16 2^-8, FP16 2^-11 relative to the value):
+  - an output is rounded once: u |o|, and FP16 numbers below 2^-14 lie 2^-24 apart,
+    so that their rounding is off by up to 2^-25 whatever u |o| is;
+  - inside a chunk the weights q.k e^(..) of the values are rounded once to 16
+    bits: u (1 + u) scale sum_j |q.k_j| e^(c_i - c_j) |v_j|.  FP16 weights are kept
+    relative to the largest of their row, with steps of 2^-25 of it at the bottom:
+    2^-25 max_j |weight| sum_j |v_j|;
+  - everything else is FP32 or a pair of 16-bit halves: exponentials 2^-17 for the
+    smallest factors, norms 2^-22, halves 2^-17, sums of 64 and 128 terms 2^-16.4
+    of the magnitudes' sum, all told below 2^-14 of scale |q|.(|S| built from
+    magnitudes).  FP16 halves end at 2^-25 absolute: as if every |k| were larger by
+    2^-11, of which 2^-14 is that; as a right or left factor the state is kept
+    relative to its row's largest, 2^-22 of which remains: 2^-22 |q|_1 max_k |S_vk|.
+  - states: 2^-14 of the sum of magnitudes."""
+import numpy as np
+import torch
+
+from linear_attention_serving_gated_gb300 import kda
+from oracle import serving_oracle as so
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+REST = 2.0 ** -14
+
+
+def dims(c):
+    return kda.dims(c["H"], HV=c["HV"], dtype=kda.KDA_DTYPE_F16 if c["dtype"] == "f16" else kda.KDA_DTYPE_BF16)
+
+
+def gate_inputs(gen, gate, rows, HV, dt):
+    """(A_log, dt_bias, a), on the CPU."""
+    if gate == "fixed":
+        return -torch.rand(HV, generator=gen) * 5, None, None
+    if gate == "none":  # a state that keeps everything
+        return None, None, torch.zeros(rows, HV)
+    if gate in ("given", "strong", "out"):
+        a = -torch.rand(rows, HV, generator=gen) ** 3 * 2
+        if gate != "given":  # some tokens forget everything, and some log-decays are no such thing
+            kind = torch.randint(0, 12, (rows, HV), generator=gen)
+            a = torch.where(kind == 0, -60.0, torch.where(kind == 1, -1e9, torch.where(kind == 2, -128.0, a)))
+            if gate == "out":
+                a = torch.where(kind == 3, 5.0, torch.where(kind == 4, -torch.inf, a))
+        return None, None, a
+    A_log = torch.log(torch.rand(HV, generator=gen) * 15 + 1)
+    return A_log, torch.randn(HV, generator=gen) - 4 if gate == "raw" else None, torch.randn(rows, HV, generator=gen).to(dt)
+
+
+def scalar_gate(A_log, dt_bias, norm, scale=128 ** -0.5):
+    up = lambda x: None if x is None else x.cuda()  # noqa: E731
+    return kda.ScalarGate(A_log=up(A_log), dt_bias=up(dt_bias), use_qk_l2norm=norm, scale=scale)
+
+
+def host(x):
+    return None if x is None else x.double().numpy()
+
+
+def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
+    """Error bounds of (outputs [T,HV,V], last state) of one sequence."""
+    G = v.shape[1] // q.shape[1]
+    q, k = (np.repeat(so.lin_unit(x, norm), G, 1) for x in (q, k))
+    v = np.abs(np.asarray(v, np.float64))
+    T = len(q)
+    c = np.cumsum(g, 0)
+    S = np.abs(np.asarray(S0, np.float64))
+    more = 2.0 ** -11 if dtype == "f16" else 0.0
+    o = np.zeros(v.shape)
+    for t in range(T):
+        S = np.exp(g[t])[:, None, None] * S + v[t][:, :, None] * (np.abs(k[t]) + more)[:, None, :]
+        aq = np.abs(q[t])
+        o[t] = REST * scale * np.einsum("hvk,hk->hv", S, aq)
+        if dtype == "f16":
+            o[t] += 2.0 ** -22 * scale * aq.sum(-1)[:, None] * S.max(-1)
+    if not exact_weights:
+        u = U[dtype]
+        for h in range(v.shape[1]):
+            with np.errstate(over="ignore"):
+                w = scale * np.abs(q[:, h] @ k[:, h].T) * np.tril(np.exp(np.minimum(c[:, None, h] - c[None, :, h], 0)))
+            o[:, h] += u * (1 + u) * (w @ v[:, h])
+            if dtype == "f16":
+                o[:, h] += 2.0 ** -25 * w.max(1)[:, None] * np.cumsum(v[:, h], 0)
+    return o, REST * S
+
+
+def check(what, got, ref, bound, dtype=None):
+    got = got.detach().double().cpu().numpy()
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    bound = bound + (U[dtype] * np.abs(ref) if dtype else 0) + (2.0 ** -25 if dtype == "f16" else 1e-30)
+    worst = np.max(np.abs(got - ref) / bound) if ref.size else 0.0
+    assert worst <= 1, f"{what}: {worst:.3f} of its bound"
