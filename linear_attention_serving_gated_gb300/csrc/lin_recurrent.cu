@@ -1,5 +1,5 @@
 // lin_recurrent.cu -- linear attention with one decay per value head, token by
-// token: packed decode, chain and tree verify, and prefill.
+// token: packed decode, chain and tree verify.
 //
 // Per value head, with S kept transposed in the pool ([V][K], K contiguous),
 // raw keys and queries k, q and their inverse norms r_k, r_q:
@@ -21,7 +21,7 @@
 namespace kda {
 namespace {
 
-enum LinMode { kLinDecode = 0, kLinChain = 1, kLinTree = 2, kLinSequence = 3 };
+enum LinMode { kLinDecode = 0, kLinChain = 1, kLinTree = 2 };
 
 struct LinStepArgs {
   LinGateArgs gate;
@@ -30,9 +30,6 @@ struct LinStepArgs {
   int64_t q_stride, k_stride, v_stride;  // elements between token rows
   int T;
   const int32_t* parent;
-  const int32_t* cu_seqlens;
-  int num_seqs;
-  int64_t total_tokens;
   float* pool;
   int pool_slots;
   const int32_t* state_idx;
@@ -73,18 +70,8 @@ __global__ void __launch_bounds__(128) lin_recurrent_kernel(const LinStepArgs ar
   const int row0 = rb * (16 * GROUPS) + warp * (4 * GROUPS) + (lane >> 3);
   const bool reporter = tid == 0 && rb == 0 && h == 0;
 
-  int64_t t0 = (int64_t)r * args.T;
-  int T = MODE == kLinDecode ? 1 : args.T;
-  if (MODE == kLinSequence) {
-    t0 = args.cu_seqlens ? (int64_t)args.cu_seqlens[r] : args.total_tokens / args.num_seqs * r;
-    const int64_t t1 = args.cu_seqlens ? (int64_t)args.cu_seqlens[r + 1] : t0 + args.total_tokens / args.num_seqs;
-    if (t0 < 0 || t1 < t0 || t1 > args.total_tokens || (r == 0 && t0 != 0) || (r == args.num_seqs - 1 && t1 != args.total_tokens)) {
-      if (reporter) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
-      return;
-    }
-    T = (int)(t1 - t0);
-    if (T == 0) return;
-  }
+  const int64_t t0 = (int64_t)r * args.T;
+  const int T = MODE == kLinDecode ? 1 : args.T;
 
   auto load = [&](int t, Token<GROUPS>& x) {
     const int64_t row = t0 + t;
@@ -208,7 +195,7 @@ __global__ void __launch_bounds__(128) lin_recurrent_kernel(const LinStepArgs ar
       store_state(args.snapshots + ((size_t)row * HV + h) * head_elems + (size_t)row0 * K + sub * 4,
                   t >= 32 || (keep >> t & 1u));
   }
-  if (MODE == kLinDecode || MODE == kLinSequence) store_state(root, false);
+  if (MODE == kLinDecode) store_state(root, false);
 }
 
 template <int MODE>
@@ -311,49 +298,4 @@ extern "C" kda_status kda_lin_verify_tree(kda_dims dims, kda_scalar_gate gate, c
                                           float* snapshots, int32_t* err_flag, void* stream) {
   return lin_verify(dims, gate, mixed_qkv, row_stride, a, B, T, parent_idx, state_pool, pool_slots, state_idx, o,
                     snapshots, err_flag, stream, true);
-}
-
-extern "C" size_t kda_lin_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens) {
-  (void)dims;
-  (void)num_seqs;
-  return total_tokens > INT32_MAX ? SIZE_MAX : 0;
-}
-
-extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
-                                      const kda_bf16* v, const void* a, int64_t gate_rows, float* state_pool,
-                                      int pool_slots, const int32_t* state_idx, const int32_t* cu_seqlens, int num_seqs,
-                                      int64_t total_tokens, kda_bf16* o, void* workspace, size_t workspace_bytes,
-                                      int32_t* err_flag, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
-  kda_status s = check_dims(dims);
-  if (s != KDA_OK) return s;
-  if (!state_pool || !state_idx) return KDA_ERR_NULL_ARG;
-  if (num_seqs < 0 || pool_slots < 0 || total_tokens < 0 || total_tokens > INT32_MAX || (a && gate_rows < total_tokens))
-    return KDA_ERR_SHAPE;
-  if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_SHAPE;
-  if (!cu_seqlens && total_tokens % num_seqs != 0) return KDA_ERR_SHAPE;
-  if (total_tokens == 0) return KDA_OK;
-  if (!q || !k || !v || !o) return KDA_ERR_NULL_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state_pool)) return KDA_ERR_ALIGNMENT;
-  LinStepArgs args{};
-  s = check_lin_gate(gate, a, &args.gate);
-  if (s != KDA_OK) return s;
-  args.H = dims.H;
-  args.HV = dims.HV;
-  args.G = dims.HV / dims.H;
-  args.q = q;
-  args.k = k;
-  args.v = v;
-  args.q_stride = args.k_stride = (int64_t)dims.H * dims.K;
-  args.v_stride = (int64_t)dims.HV * dims.V;
-  args.cu_seqlens = cu_seqlens;
-  args.num_seqs = num_seqs;
-  args.total_tokens = total_tokens;
-  args.pool = state_pool;
-  args.pool_slots = pool_slots;
-  args.state_idx = state_idx;
-  args.o = o;
-  args.err_flag = err_flag;
-  return launch_lin<kLinSequence>(args, num_seqs, dims.dtype, static_cast<cudaStream_t>(stream));
 }

@@ -12,10 +12,12 @@ the 16-bit type (BF16 2^-8, FP16 2^-11 relative to the value):
   - everything else is FP32 or a pair of 16-bit halves: exponentials 2^-17 for the
     smallest factors, norms 2^-22, halves 2^-17, sums of 64 and 128 terms 2^-16.4
     of the magnitudes' sum, all told below 2^-14 of scale |q|.(|S| built from
-    magnitudes).  FP16 halves end at 2^-25 absolute: as if every |k| were larger by
-    2^-11, of which 2^-14 is that; as a right or left factor the state is kept
-    relative to its row's largest, 2^-22 of which remains: 2^-22 |q|_1 max_k |S_vk|.
-  - states: 2^-14 of the sum of magnitudes."""
+    magnitudes).  As a factor of FP16's the state is kept relative to its row's
+    largest, 2^-22 of which remains: 2^-22 |q|_1 max_k |S_vk|.
+  - states: 2^-14 of the sum of magnitudes.  FP16 parts of a decayed key end 2^-24
+    apart: off by up to 2^-25 whatever the decay inside the chunk of 64 tokens has left
+    of it (unit keys are taken times 2^15: 2^-40).  That adds 2^-25 sum |v_j| a chunk,
+    which then decays with the state, and |q|_1 of it to an output."""
 import numpy as np
 import torch
 
@@ -66,12 +68,18 @@ def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
     T = len(q)
     c = np.cumsum(g, 0)
     S = np.abs(np.asarray(S0, np.float64))
-    more = 2.0 ** -11 if dtype == "f16" else 0.0
+    step = 0.0 if dtype != "f16" or exact_weights else 2.0 ** -40 if norm else 2.0 ** -25
+    E, E0 = np.zeros(v.shape[1:]), np.zeros(v.shape[1:])  # of a state's rows; at the chunk's start
     o = np.zeros(v.shape)
     for t in range(T):
-        S = np.exp(g[t])[:, None, None] * S + v[t][:, :, None] * (np.abs(k[t]) + more)[:, None, :]
+        S = np.exp(g[t])[:, None, None] * S + v[t][:, :, None] * np.abs(k[t])[:, None, :]
         aq = np.abs(q[t])
-        o[t] = REST * scale * np.einsum("hvk,hk->hv", S, aq)
+        if t % 64 == 0:
+            E0, c0 = E, c[t - 1] if t else 0 * c[0]
+            mine = 0 * E
+        mine = mine + step * v[t]
+        E = np.exp(c[t] - c0)[:, None] * E0 + mine
+        o[t] = scale * (REST * np.einsum("hvk,hk->hv", S, aq) + E0 * aq.sum(-1)[:, None])
         if dtype == "f16":
             o[t] += 2.0 ** -22 * scale * aq.sum(-1)[:, None] * S.max(-1)
     if not exact_weights:
@@ -82,7 +90,7 @@ def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
             o[:, h] += u * (1 + u) * (w @ v[:, h])
             if dtype == "f16":
                 o[:, h] += 2.0 ** -25 * w.max(1)[:, None] * np.cumsum(v[:, h], 0)
-    return o, REST * S
+    return o, REST * S + E[:, :, None]
 
 
 def check(what, got, ref, bound, dtype=None):
