@@ -18,10 +18,10 @@
 //   O2^T = V^T P^T   128 x 64 x 64, V as it landed, P in two halves
 //   dS^T = V^T K'    128 x 128 x 64, K'_j = e^(c_last - c_j) rk_j k_j in three parts
 //                    (FP16: two)
-// 8 warps keep the state and turn it into the operand S^T; 4 prepare the chunk's
-// factors and K'; 4 turn Q K^T into P and write the outputs; one loads rows, two
-// issue the products, those of the state apart from those within the chunk, so
-// that neither waits for the other's operands.
+// 8 warps keep the state and turn it into the operand S^T; 8 take norms and make K';
+// 8 turn Q K^T into P and, a chunk behind, write the outputs; one makes the decays'
+// factors, one loads rows, two issue the products, those of the state apart from
+// those within the chunk, so that neither waits for the other's operands.
 //
 // A long sequence is cut into segments: a first launch computes what each segment
 // adds to a state of zero (no queries, no outputs), and the CTAs of the second sum
@@ -29,7 +29,7 @@
 // in both.
 //
 // Precision: BF16 halves hi + lo leave 2^-18, three parts 2^-26, FP16 halves 2^-23
-// (their range is kept by a power of two for each row of P and of S^T), so that the
+// (a power of two for each row of P and of S^T keeps them in range), so that the
 // state is as exact as FP32 sums leave it and an output is off by its own rounding.
 #include <atomic>
 
@@ -63,36 +63,41 @@ struct LinMaps {
   CUtensorMap q, k, v;
 };
 
-// Factors of a chunk.
+// Factors of a chunk.  b is the first token of i's block of 16; where a block decays
+// by more than e^60 its rows of P get their factors term by term (far).
 struct Scalars {
-  float out[kC];      // scale rq_i e^(c_i)
-  float row[kC];      // scale rq_i e^(c_i - c_b), b the first token of i's block of 16
-  float col[3][kC];   // rk_j e^(c_b - c_j) for b = 16, 32, 48 and j < b
-  float q[kC], k[kC]; // scale rq_i, rk_j
-  float c_hi[kC], c_lo[kC];
-  float last;         // e^(c_last)
+  float c_hi[kC], c_lo[kC];  // c_i
+  float out[kC];             // scale rq_i e^(c_i)
+  float row[kC];             // scale rq_i e^(c_i - c_b); far: scale rq_i
+  float col[4][kC];          // rk_j e^(c_b - c_j) for b = 0, 16, 32, 48 and j < b + 16
+  float k[kC];               // rk_j
+  float big[kC], kk[kC];     // FP16: |q_i| e^(c_b - c_i), far |q_i|; |k_j|^2
+  float last;                // e^(c_last)
   float pad[3];
 };
+constexpr float kFar = 60.f;
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];  // rows landed, consumed
-  uint64_t sc_full[kScalarBufs];           // factors (and V's rows past the end zeroed)
+  uint64_t gate_full[kScalarBufs];         // factors of the decays
+  uint64_t sc_full[kScalarBufs];           // all factors (and V's rows past the end zeroed)
+  uint64_t sc_free[kScalarBufs];           // read
   uint64_t wk_full;                        // K'
-  uint64_t ds_full[2], ds_read[2];         // dS
-  uint64_t s_full, qs_full;                // operand S^T, O1
-  uint64_t qk_full, p_full, o_full;        // Q K^T, P, O2
-  uint64_t o_read;                         // O1 and O2 are in registers
+  uint64_t ds_full, ds_read;               // dS
+  uint64_t s_full, qs_full[2];             // operand S^T, O1
+  uint64_t qk_full[2], p_full, o_full[2];  // Q K^T, P, O2
+  uint64_t o_read[2];                      // O1 and O2 are in registers
   uint64_t drained[2];                     // all products of an issuing warp; used where a wait has run out
   uint32_t tmem;
   int timed_out;
-  float p_scale[kC];        // FP16: the powers of two of P's rows
+  float p_scale[2][kC];     // FP16: the powers of two of P's rows
   float s_max[2][2][128];   //       largest magnitudes of half a row of S^T
-  float s_scale[2][128];    //       powers of two of its rows
+  float s_scale[3][128];    //       powers of two of its rows
 };
 
 // Warps.
-constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 12, kRowWarp = 16, kStateMma = 17, kChunkMma = 18, kSpare = 19,
-              kThreads = 640;
+constexpr int kStateWarps = 8, kPrepWarp = 8, kPrepWarps = 8, kOutWarp = 16, kOutWarps = 8, kRowWarp = 24, kStateMma = 25,
+              kChunkMma = 26, kGateWarp = 27, kThreads = 896;
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
 // the parts of K', P's halves, factors, barriers.
@@ -102,9 +107,9 @@ constexpr int kBars = kScalars + kScalarBufs * (int)sizeof(Scalars);
 constexpr int kSmem = kBars + (int)sizeof(Bars);
 static_assert(kSmem <= 232448 - 1024 && kBars % 16 == 0, "shared memory");
 
-// TMEM columns: dS twice, the operand S^T (two 16-bit numbers a column), O1, and
-// Q K^T, whose place O2 takes.
-constexpr int kTmU = 0, kTmS = 256, kTmSlo = 320, kTmQ = 384, kTmO = 448, kTmCols = 512;
+// TMEM columns: dS, the operand S^T (two 16-bit numbers a column), and for chunks in
+// turn O1 and Q K^T, whose place O2 takes.
+constexpr int kTmU = 0, kTmS = 128, kTmSlo = 192, kTmQ = 256, kTmO = 384, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -154,6 +159,15 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// The power of two that takes numbers of up to m (finite, not negative) near FP16's
+// largest, below 2^15, where the steps at the other end matter least; and back.
+__device__ __forceinline__ float to_2p15(float m, float& back) {
+  uint32_t x = __float_as_uint(m) >> 23;  // m < 2^(x - 126)
+  x = x < 15 ? 15 : x > 253 ? 253 : x;
+  back = __uint_as_float((x - 14) << 23);
+  return __uint_as_float((268 - x) << 23);
+}
+
 // 16-byte piece `piece` of 128-byte line `row` of a 128-byte-swizzled tile.
 __device__ __forceinline__ uint4* line16(uint8_t* tile, int row, int piece) {
   return reinterpret_cast<uint4*>(tile + row * 128 + ((piece ^ (row & 7)) << 4));
@@ -184,6 +198,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// What is done with x comes after what was done before: without it the compiler makes
+// all of a row's operands first, and has no registers for them.
+__device__ __forceinline__ void hold16(float* x) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(x[i]));
+}
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread; 16 k are 8 columns of A.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
@@ -253,9 +274,6 @@ __device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
   const float s = a.x + b.x, z = s - a.x;
   return make_float2(s, a.y + (((a.x - (s - z)) + (b.x - z)) + b.y));
 }
-__device__ __forceinline__ float2 pair_from(float2 x, int l) {
-  return make_float2(__shfl_sync(0xffffffffu, x.x, l), __shfl_sync(0xffffffffu, x.y, l));
-}
 __device__ __forceinline__ float exp_diff(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
 
 // LOCAL: what segments add to a state of zero, or to the pool's.  Otherwise the outputs, and the
@@ -270,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (LOCAL) grid_dependency_launch();
   const int HV = args.HV, h = blockIdx.x % HV, id = blockIdx.x / HV;
   const Segment seg = find_segment(args, id, lane);
-  if (!LOCAL && blockIdx.x == 0 && warp == kSpare)  // bounds of no sequence, which has no CTA of its own
+  if (!LOCAL && blockIdx.x == 0 && warp == kGateWarp)  // bounds of no sequence, which has no CTA of its own
     for (int m = lane; m < args.num_seqs; m += 32)
       if (seq_len(args, m) < 0) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
   // whoever waits for the second launch waits for the first one too
@@ -308,19 +326,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars.full[i], 1);
       tc::mbar_init(&bars.empty[i], LOCAL ? 1 : 2);
     }
-    for (int i = 0; i < kScalarBufs; ++i) tc::mbar_init(&bars.sc_full[i], 4);
-    tc::mbar_init(&bars.wk_full, 4);
+    for (int i = 0; i < kScalarBufs; ++i) {
+      tc::mbar_init(&bars.gate_full[i], 1);
+      tc::mbar_init(&bars.sc_full[i], kPrepWarps);
+      tc::mbar_init(&bars.sc_free[i], LOCAL ? kStateWarps : kOutWarps);
+    }
+    tc::mbar_init(&bars.wk_full, kPrepWarps);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bars.ds_full[i], 1);
-      tc::mbar_init(&bars.ds_read[i], kStateWarps);
+      tc::mbar_init(&bars.qs_full[i], 1);
+      tc::mbar_init(&bars.qk_full[i], 1);
+      tc::mbar_init(&bars.o_full[i], 1);
+      tc::mbar_init(&bars.o_read[i], kOutWarps);
       tc::mbar_init(&bars.drained[i], 1);
     }
+    tc::mbar_init(&bars.ds_full, 1);
+    tc::mbar_init(&bars.ds_read, kStateWarps);
     tc::mbar_init(&bars.s_full, kStateWarps);
-    tc::mbar_init(&bars.qs_full, 1);
-    tc::mbar_init(&bars.qk_full, 1);
-    tc::mbar_init(&bars.p_full, 4);
-    tc::mbar_init(&bars.o_full, 1);
-    tc::mbar_init(&bars.o_read, 4);
+    tc::mbar_init(&bars.p_full, kOutWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::tc_fence_before();
@@ -332,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float k_up = F16 && ga.use_qk_l2norm ? 32768.f : 1.f;
   bool ok = true;
 
-  // 640 threads start with 96 registers each; 256 at 128 and 384 at 72 are 60416 of those 61440
+  // 896 threads start with 72 registers each; 256 at 112 and 640 at 56 are those 64512
   if (warp < kStateWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     // ------------------------------------------------------------------- state
     const int quad = warp & 3, half = warp >> 2;
     const int dv = 32 * quad + lane;  // this thread's value column; its key channels 64 half ..
@@ -354,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4 x = copied ? __ldcg(copy + j * 256) : *reinterpret_cast<const float4*>(root + 4 * j);
         S[4 * j] = x.x, S[4 * j + 1] = x.y, S[4 * j + 2] = x.z, S[4 * j + 3] = x.w;
         if (LOCAL) const_cast<float4*>(copy)[j * 256] = x;
+        if (j % 4 == 3) asm volatile("" ::: "memory");
       }
     } else {
 #pragma unroll
@@ -370,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           S[4 * j + 1] = fmaf(up, x.y, S[4 * j + 1]);
           S[4 * j + 2] = fmaf(up, x.z, S[4 * j + 2]);
           S[4 * j + 3] = fmaf(up, x.w, S[4 * j + 3]);
+          if (j % 4 == 3) asm volatile("" ::: "memory");  // so many loads in flight as there are registers for
         }
         up *= __ldcg(args.local_decay + (int64_t)(id - seg.s + m) * HV + h);
       }
@@ -379,6 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp that runs out of time goes on without waiting, so that the others still
     // meet it at their barrier.
     for (int c = 0; c < nch; ++c) {
+      const int sb = c % kScalarBufs;
+      ok = ok && warp_wait(&bars.gate_full[sb], c / kScalarBufs);
+      const float last = scalars[sb].last;
       if (!LOCAL) {
         float down = 1.f, row_scale = 1.f;
         if constexpr (F16) {  // the row relative to its largest, by a power of two
@@ -388,18 +415,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           bars.s_max[c & 1][half][dv] = m;
           asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
           m = fmaxf(m, bars.s_max[c & 1][half ^ 1][dv]);
-          uint32_t e = __float_as_uint(m) >> 23;
-          e = e < 1 ? 127 : e > 253 ? 253 : e;
-          down = __uint_as_float((254u - e) << 23);
-          row_scale = __uint_as_float(e << 23);
+          down = to_2p15(m, row_scale);
         }
-        if (c > 0) ok = ok && warp_wait(&bars.qs_full, c - 1);  // the operand has been read
-        // (and the scales of chunk c - 2, before whose outputs were read Q S of c - 1 did not start)
-        if (F16 && half == 0) bars.s_scale[c & 1][dv] = row_scale;
+        if (c > 0) ok = ok && warp_wait(&bars.qs_full[(c - 1) & 1], (c - 1) >> 1);  // the operand has been read
+        // (and the scales of chunk c - 3, before whose outputs were read Q S of c - 1 did not start)
+        if (F16 && half == 0) bars.s_scale[c % 3][dv] = row_scale;
         tc::tc_fence_after();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t hi[8], lo[8];
+          hold16(S + 16 * g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float2 x = make_float2(S[16 * g + 2 * j], S[16 * g + 2 * j + 1]), rest;
@@ -416,14 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && ok) arrive(&bars.s_full);
         if (c == nch - 1 && !last_segment) break;  // its state is of no use
       }
-      ok = ok && warp_wait(&bars.sc_full[c % kScalarBufs], c / kScalarBufs);
-      const float last = scalars[c % kScalarBufs].last;
-      ok = ok && warp_wait(&bars.ds_full[c & 1], c >> 1);
+      ok = ok && warp_wait(&bars.ds_full, c);
       tc::tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16];
-        tc::tmem_ld16_async(lanes + kTmU + 128 * (c & 1) + 64 * half + 16 * g, r);
+        tc::tmem_ld16_async(lanes + kTmU + 64 * half + 16 * g, r);
         wait_ld(r);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -436,7 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0 && ok) arrive(&bars.ds_read[c & 1]);
+      if (lane == 0 && ok) {
+        arrive(&bars.ds_read);
+        if (LOCAL) arrive(&bars.sc_free[sb]);
+      }
       decay *= last;
     }
     if (LOCAL) {
@@ -450,235 +476,274 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(root + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp < kOutWarp) {
-      // ------------------------------------------------- a chunk's factors and K'
-      const int w = warp - kPrepWarp, row = 16 * w + (lane & 15), half = lane >> 4;
-      const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-      const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
-      ushort2 raw[2];
-      auto load_gate = [&](int c) {  // tokens 2 lane and 2 lane + 1
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          raw[e] = make_ushort2(0, 0);
-          if (c * kC + 2 * lane + e < L) raw[e] = lin_gate_load(ga, (t0 + c * kC + 2 * lane + e) * HV + h);
-        }
-      };
-      load_gate(0);
+      // ------------------------------------------------------------ norms and K'
+      // a row's quarter a thread: 32 channels, four 16-byte pieces
+      const int row = 8 * (warp - kPrepWarp) + (lane & 7), x4 = lane >> 3, half = (x4 >> 1) * 8192, p0 = 4 * (x4 & 1);
+      const bool squares = ga.use_qk_l2norm || F16;
+      int st = 0, sb = 0;
+      uint32_t st_phase = 0, sb_phase = 0;
       for (int c = 0; c < nch; ++c) {
-        const int st = c % kStages, left = L - c * kC;
-        Scalars& sc = scalars[c % kScalarBufs];
-        float2 even, run;  // c of tokens 2 lane, 2 lane + 1
-        {
-          const float g0 = 2 * lane < left ? lin_log_decay<F16>(ga, raw[0], neg_rate, bias) : 0.f;
-          const float g1 = 2 * lane + 1 < left ? lin_log_decay<F16>(ga, raw[1], neg_rate, bias) : 0.f;
-          run = pair_add(make_float2(g0, 0.f), make_float2(g1, 0.f));
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
-            if (lane >= d) run = pair_add(up, run);
-          }
-          even = pair_add(run, make_float2(-g1, 0.f));
-        }
-        if (c + 1 < nch) load_gate(c + 1);
-        const float2 c_last = pair_from(run, 31);
-        const float2 a = pair_from(even, row >> 1), b = pair_from(run, row >> 1);
-        const float2 c_i = row & 1 ? b : a;
-        const float2 c_b = pair_from(even, 8 * w);
-        if (!(ok = warp_wait(&bars.full[st], c / kStages))) break;
-        uint8_t* rows = smem + st * kStageBytes;
-        uint4 kw[8];
-        float2 sk = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          kw[p] = *line16(rows + kTile + half * 8192, row, p);
-          const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = widen2<F16>(x[e]);
-            sk = fma2(f, f, sk);
-          }
-        }
+        const int left = L - c * kC;
+        Scalars& sc = scalars[sb];
+        if (!(ok = warp_wait(&bars.gate_full[sb], sb_phase))) break;
+        auto c_of = [&](int i) { return make_float2(sc.c_hi[i], sc.c_lo[i]); };
+        const float2 c_i = c_of(row);
+        const float e_w = exp_diff(c_of(kC - 1), c_i);
+        float e_row = 0.f, e_col = 0.f;
+        bool far = false;
         if (!LOCAL) {
+          const float2 c_b = c_of(row & ~15), end = c_of(row | 15);
+          far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
+          e_row = x4 == 0 ? expf(c_i.x + c_i.y) : far ? 1.f : exp_diff(c_i, c_b);  // for out, for row
+          e_col = exp_diff(c_of(16 * x4), c_i);
+        }
+        if (!(ok = warp_wait(&bars.full[st], st_phase))) break;
+        uint8_t* rows = smem + st * kStageBytes;
+        uint4 kw[4];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint4 qw = *line16(rows + half * 8192, row, p);
-            const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
+        for (int p = 0; p < 4; ++p) kw[p] = *line16(rows + kTile + half, row, p0 + p);
+        float nk = 0.f, nq = 0.f;
+        if (squares) {
+          float2 sk = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = widen2<F16>(x[e]);
-              sq = fma2(f, f, sq);
+              sk = fma2(f, f, sk);
             }
           }
-        }
-        float nk = sk.x + sk.y, nq = sq.x + sq.y;
-        nk += __shfl_xor_sync(0xffffffffu, nk, 16);
-        nq += __shfl_xor_sync(0xffffffffu, nq, 16);
-        const float rk = ga.use_qk_l2norm ? rsqrtf(nk + kNormEps) : 1.f;
-        const float rq = ga.scale * (ga.use_qk_l2norm ? rsqrtf(nq + kNormEps) : 1.f);
-        if (half == 0) {
-          sc.out[row] = rq * expf(c_i.x + c_i.y);
-          sc.row[row] = rq * exp_diff(c_i, c_b);
-          sc.q[row] = rq;
-          sc.k[row] = rk;
-          sc.c_hi[row] = c_i.x;
-          sc.c_lo[row] = c_i.y;
-          if (row == 0) sc.last = expf(c_last.x + c_last.y);
-        }
-        if (!LOCAL)
-          for (int x = 1; x < 4; ++x) {  // every lane takes part in the exchange
-            const float2 ref = pair_from(even, 8 * x);
-            if (x > w && (x & 1) == half) sc.col[x - 1][row] = rk * exp_diff(ref, c_i);
-          }
-        if (left < kC && row >= left) {  // the next sequence's values: NaN times zero is NaN
+          nk = sk.x + sk.y;
+          if (!LOCAL) {
 #pragma unroll
-          for (int p = 0; p < 8; ++p) *line16(rows + 2 * kTile + half * 8192, row, p) = make_uint4(0, 0, 0, 0);
+            for (int p = 0; p < 4; ++p) {
+              const uint4 qw = *line16(rows + half, row, p0 + p);
+              const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = widen2<F16>(x[e]);
+                sq = fma2(f, f, sq);
+              }
+            }
+            nq = sq.x + sq.y;
+            nq += __shfl_xor_sync(0xffffffffu, nq, 8);
+            nq += __shfl_xor_sync(0xffffffffu, nq, 16);
+          }
+          nk += __shfl_xor_sync(0xffffffffu, nk, 8);
+          nk += __shfl_xor_sync(0xffffffffu, nk, 16);
+        }
+        const float rk = ga.use_qk_l2norm ? rsqrtf(nk + kNormEps) : 1.f;
+        if (!LOCAL) {
+          const float rq = ga.scale * (ga.use_qk_l2norm ? rsqrtf(nq + kNormEps) : 1.f);
+          if (x4 < 2) (x4 == 0 ? sc.out : sc.row)[row] = rq * e_row;
+          if (x4 == 2) sc.k[row] = rk;
+          if (F16 && x4 == 1) sc.big[row] = __fdividef(sqrtf(nq), e_row);
+          if (F16 && x4 == 2) sc.kk[row] = nk;
+          sc.col[x4][row] = rk * e_col;
+        }
+        if (row >= left) {  // the next sequence's values: NaN times zero is NaN
+#pragma unroll
+          for (int p = 0; p < 4; ++p) *line16(rows + 2 * kTile + half, row, p0 + p) = make_uint4(0, 0, 0, 0);
           tc::fence_async_smem();
         }
         __syncwarp();
-        if (lane == 0) arrive(&bars.sc_full[c % kScalarBufs]);
-        const float wk = row < left ? k_up * rk * exp_diff(c_last, c_i) : 0.f;
-        if (c > 0 && !(ok = warp_wait(&bars.ds_full[(c - 1) & 1], (c - 1) >> 1))) break;  // K' has been read
+        if (lane == 0) arrive(&bars.sc_full[sb]);
+        const float wk = row < left ? k_up * rk * e_w : 0.f;
+        if (c > 0 && !(ok = warp_wait(&bars.ds_full, c - 1))) break;  // K' has been read
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
+        for (int p = 0; p < 4; ++p) {
           const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
           uint32_t part[3][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float2 f = mul2(widen2<F16>(x[e]), make_float2(wk, wk)), rest;
-            if (row >= left) f = make_float2(0.f, 0.f);
+            float2 f = mul2(widen2<F16>(row < left ? x[e] : 0u), make_float2(wk, wk)), rest;
             part[0][e] = round2<F16>(f, rest);
             part[1][e] = round2<F16>(rest, f);
             if (!F16) part[2][e] = round2<F16>(f, rest);
           }
 #pragma unroll
           for (int i = 0; i < (F16 ? 2 : 3); ++i)
-            *line16(smem + kWk + i * kTile + half * 8192, row, p) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
+            *line16(smem + kWk + i * kTile + half, row, p0 + p) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) arrive(&bars.wk_full);
+        if (++st == kStages) st = 0, st_phase ^= 1;
+        if (++sb == kScalarBufs) sb = 0, sb_phase ^= 1;
       }
     } else if (warp < kRowWarp) {
       // ---------------------------------------------------------- P, and the outputs
       if (!LOCAL) {
-        const int w = warp - kOutWarp, r0 = 16 * w + (lane >> 2);  // rows r0 and r0 + 8
+        const int w = warp & 3, part = (warp - kOutWarp) >> 2;
+        const int r0 = 16 * w + (lane >> 2);  // P: rows r0 and r0 + 8
         const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+        uint8_t* at[2];  // where columns 2 (lane % 4) and + 1 of a row's first piece are, but for the swizzle
+#pragma unroll
+        for (int e = 0; e < 2; ++e) at[e] = smem + kP + (r0 + 8 * e) * 128 + 4 * (lane & 3);
+        const int turn = r0 & 7;
+        if (part)
+          for (int j = 2 * w + 2; j < 8; ++j)  // right of the diagonal blocks all is zero, and stays so
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4)) = 0;
+              *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4) + 8192) = 0;
+            }
+        auto put = [&](int j, int e, float2 x) {
+          float2 rest;
+          const uint32_t hi = round2<F16>(x, rest), lo = round2<F16>(rest, x);
+          uint8_t* to = at[e] + ((j ^ turn) << 4);
+          *reinterpret_cast<uint32_t*>(to) = hi;
+          *reinterpret_cast<uint32_t*>(to + 8192) = lo;
+        };
+        // outputs: 32 value columns a warp, 32 tokens a thread
         const int odd = lane & 1;
         const uint32_t pick = odd ? 0x3276u : 0x5410u;
         const int64_t step = (int64_t)HV * kHeadDim;
-        kda_bf16* dst = args.o + ((t0 + odd) * HV + h) * kHeadDim + ((32 * w + lane) & ~1);
-        for (int c = 0; c < nch; ++c, dst += kC * step) {
-          const Scalars& sc = scalars[c % kScalarBufs];
-          if (!(ok = warp_wait(&bars.sc_full[c % kScalarBufs], c / kScalarBufs))) break;
-          const float fr[2] = {sc.row[r0], sc.row[r0 + 8]}, fq[2] = {sc.q[r0], sc.q[r0 + 8]};
-          const float ch[2] = {sc.c_hi[r0], sc.c_hi[r0 + 8]}, cl[2] = {sc.c_lo[r0], sc.c_lo[r0 + 8]};
-          if (!(ok = warp_wait(&bars.qk_full, c))) break;
-          tc::tc_fence_after();
-          float2 p[8][2];
-          uint32_t r[4][4];
-          float big[2] = {0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (j % 4 == 0) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) ld_frag8(lanes + kTmO + 8 * (j + i), r[i]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) wait_ld(r[i]);
-            }
-            const int col = 8 * j + 2 * (lane & 3);
-            float f[2][2];  // the factors of rows r0, r0 + 8 and columns col, col + 1
-            if (j < 2 * w) {
-              const float2 x = *reinterpret_cast<const float2*>(&sc.col[w - 1][col]);
-              f[0][0] = fr[0] * x.x, f[0][1] = fr[0] * x.y, f[1][0] = fr[1] * x.x, f[1][1] = fr[1] * x.y;
-            } else if (j < 2 * w + 2) {
-              const float2 k2 = *reinterpret_cast<const float2*>(&sc.k[col]), h2 = *reinterpret_cast<const float2*>(&sc.c_hi[col]),
-                           l2 = *reinterpret_cast<const float2*>(&sc.c_lo[col]);
+        kda_bf16* dst = args.o + ((t0 + 32 * part + odd) * HV + h) * kHeadDim + ((32 * w + lane) & ~1);
+        for (int c = 0; c <= nch; ++c) {
+          if (c < nch) {
+            const Scalars& sc = scalars[c % kScalarBufs];
+            if (!(ok = warp_wait(&bars.sc_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.qk_full[c & 1], c >> 1))) break;
+            if (c > 0 && !(ok = warp_wait(&bars.o_full[(c - 1) & 1], (c - 1) >> 1))) break;  // the last P has been read
+            tc::tc_fence_after();
+            float2 down[2];  // FP16: powers of two of the rows
+            if constexpr (F16) {  // |q.k| is at most |q| |k|
+              float k2 = 1.f;
+              if (!ga.use_qk_l2norm) {
+                k2 = fmaxf(sc.kk[lane], sc.kk[lane + 32]);
+                k2 = sqrtf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(k2))));
+              }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                f[e][0] = fq[e] * k2.x * __expf(fminf((ch[e] - h2.x) + (cl[e] - l2.x), 0.f));
-                f[e][1] = fq[e] * k2.y * __expf(fminf((ch[e] - h2.y) + (cl[e] - l2.y), 0.f));
+                float back;
+                down[e].x = down[e].y = to_2p15(sc.big[r0 + 8 * e] * k2, back);
+                if (part && (lane & 3) == 0) bars.p_scale[c & 1][r0 + 8 * e] = back;
               }
-            } else {
-              f[0][0] = f[0][1] = f[1][0] = f[1][1] = 0.f;
             }
+            const uint32_t qk = lanes + kTmO + 64 * (c & 1);
+            const bool far = !((sc.c_hi[16 * w] - sc.c_hi[16 * w + 15]) + (sc.c_lo[16 * w] - sc.c_lo[16 * w + 15]) <= kFar);
+            // the two warps of these rows take every other block, from the diagonal
+            for (int b = w - part; b >= 0; b -= 2) {
+              uint32_t r[2][4];
+              ld_frag8(qk + 16 * b, r[0]);
+              ld_frag8(qk + 16 * b + 8, r[1]);
+              wait_ld(r[0]);
+              wait_ld(r[1]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = r0 + 8 * e;
-              p[j][e].x = col <= i ? f[e][0] * __uint_as_float(r[j % 4][2 * e]) : 0.f;
-              p[j][e].y = col + 1 <= i ? f[e][1] * __uint_as_float(r[j % 4][2 * e + 1]) : 0.f;
-              if (F16) big[e] = fmaxf(big[e], fmaxf(fabsf(p[j][e].x), fabsf(p[j][e].y)));
+              for (int i = 0; i < 2; ++i) {
+                const int col = 16 * b + 8 * i + 2 * (lane & 3);
+                float2 x[2];
+                if (!far) {
+                  const float2 f = *reinterpret_cast<const float2*>(&sc.col[w][col]);
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    x[e] = mul2(f, make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])));
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const float2 c_i = make_float2(sc.c_hi[r0 + 8 * e], sc.c_lo[r0 + 8 * e]);
+                    x[e].x = sc.k[col] * exp_diff(c_i, make_float2(sc.c_hi[col], sc.c_lo[col])) * __uint_as_float(r[i][2 * e]);
+                    x[e].y = sc.k[col + 1] * exp_diff(c_i, make_float2(sc.c_hi[col + 1], sc.c_lo[col + 1])) *
+                             __uint_as_float(r[i][2 * e + 1]);
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  if (F16) x[e] = mul2(x[e], down[e]);
+                  if (b == w) {
+                    const int row = r0 + 8 * e;
+                    x[e].x = col <= row ? x[e].x : 0.f;
+                    x[e].y = col < row ? x[e].y : 0.f;
+                  }
+                  put(2 * b + i, e, x[e]);
+                }
+              }
             }
+            tc::fence_async_smem();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&bars.p_full);
           }
-          float down[2] = {1.f, 1.f};
-          if constexpr (F16) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              big[e] = fmaxf(big[e], __shfl_xor_sync(0xffffffffu, big[e], 1));
-              big[e] = fmaxf(big[e], __shfl_xor_sync(0xffffffffu, big[e], 2));
-              uint32_t x = __float_as_uint(big[e]) >> 23;
-              x = x < 1 ? 127 : x > 253 ? 253 : x;
-              down[e] = __uint_as_float((254u - x) << 23);
-              if ((lane & 3) == 0) bars.p_scale[r0 + 8 * e] = __uint_as_float(x << 23);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = r0 + 8 * e;
-              float2 x = p[j][e], rest;
-              if (F16) x = mul2(x, make_float2(down[e], down[e]));
-              const uint32_t hi = round2<F16>(x, rest), lo = round2<F16>(rest, x);
-              const int at = i * 128 + ((j ^ (i & 7)) << 4) + 4 * (lane & 3);
-              *reinterpret_cast<uint32_t*>(smem + kP + at) = hi;
-              *reinterpret_cast<uint32_t*>(smem + kP + 8192 + at) = lo;
-            }
-          tc::fence_async_smem();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive(&bars.p_full);
-          // outputs: 32 value columns a warp, 64 tokens a thread
-          if (!(ok = warp_wait(&bars.qs_full, c) && warp_wait(&bars.o_full, c))) break;
-          tc::tc_fence_after();
-          const float up = F16 ? bars.s_scale[c & 1][32 * w + lane] : 1.f;
-          const int left = L - c * kC - odd;
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
+          if (c > 0) {
+            const int d = c - 1, ob = d & 1;
+            const Scalars& sc = scalars[d % kScalarBufs];
+            if (!(ok = warp_wait(&bars.qs_full[ob], d >> 1) && warp_wait(&bars.o_full[ob], d >> 1))) break;
+            tc::tc_fence_after();
+            const float up = F16 ? bars.s_scale[d % 3][32 * w + lane] : 1.f;
+            const int left = L - d * kC - 32 * part - odd;
             uint32_t y2[16];  // two tokens of one column each
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const int tok = 32 * part + 8 * g;
               uint32_t q[8], r[8];
-              tmem_ld8_async(lanes + kTmQ + tok, q);
-              tmem_ld8_async(lanes + kTmO + tok, r);
+              tmem_ld8_async(lanes + kTmQ + 64 * ob + tok, q);
+              tmem_ld8_async(lanes + kTmO + 64 * ob + tok, r);
               wait_ld(q);
               wait_ld(r);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                float2 f = *reinterpret_cast<const float2*>(sc.out + tok + 2 * j);
-                float2 y = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                float2 f = *reinterpret_cast<const float2*>(sc.out + tok + 2 * j), rest;
+                float2 y = mul2(*reinterpret_cast<const float2*>(sc.row + tok + 2 * j),
+                                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                 if (F16) {
                   f = mul2(f, make_float2(up, up));
-                  y = mul2(y, *reinterpret_cast<const float2*>(bars.p_scale + tok + 2 * j));
+                  y = mul2(y, *reinterpret_cast<const float2*>(bars.p_scale[ob] + tok + 2 * j));
                 }
-                y = fma2(f, make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])), y);
-                y2[4 * g + j] = pack_out16x2<F16>(y.x, y.y);
+                y2[4 * g + j] = round2<F16>(fma2(f, make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])), y), rest);
               }
             }
-            if (part) {
-              tc::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) arrive(&bars.o_read);
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              arrive(&bars.o_read[ob]);
+              arrive(&bars.sc_free[d % kScalarBufs]);
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {  // traded for two columns of one token each
-              const int tok = 32 * part + 2 * j;
               const uint32_t x = __byte_perm(y2[j], __shfl_xor_sync(0xffffffffu, y2[j], 1), pick);
-              if (tok < left) *reinterpret_cast<uint32_t*>(dst + tok * step) = x;
+              if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = x;
             }
+            dst += kC * step;
           }
         }
+      }
+    } else if (warp == kGateWarp) {
+      // --------------------------------------------------------- the decays' factors
+      const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
+      const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
+      ushort2 raw[2][2];  // of the next two chunks, tokens 2 lane and 2 lane + 1
+      auto load_gate = [&](int c, ushort2 (&x)[2]) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[e] = make_ushort2(0, 0);
+          if (c * kC + 2 * lane + e < L) x[e] = lin_gate_load(ga, (t0 + c * kC + 2 * lane + e) * HV + h);
+        }
+      };
+      load_gate(0, raw[0]);
+      load_gate(1, raw[1]);
+      for (int c = 0; c < nch; ++c) {
+        const int left = L - c * kC, sb = c % kScalarBufs;
+        Scalars& sc = scalars[sb];
+        const float g0 = 2 * lane < left ? lin_log_decay<F16>(ga, raw[0][0], neg_rate, bias) : 0.f;
+        const float g1 = 2 * lane + 1 < left ? lin_log_decay<F16>(ga, raw[0][1], neg_rate, bias) : 0.f;
+        raw[0][0] = raw[1][0], raw[0][1] = raw[1][1];
+        load_gate(c + 2, raw[1]);
+        float2 run = pair_add(make_float2(g0, 0.f), make_float2(g1, 0.f));  // c of token 2 lane + 1
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
+          if (lane >= d) run = pair_add(up, run);
+        }
+        const float2 even = pair_add(run, make_float2(-g1, 0.f));  // of token 2 lane
+        if (c >= kScalarBufs && !(ok = warp_wait(&bars.sc_free[sb], c / kScalarBufs - 1))) break;
+        *reinterpret_cast<float2*>(sc.c_hi + 2 * lane) = make_float2(even.x, run.x);
+        *reinterpret_cast<float2*>(sc.c_lo + 2 * lane) = make_float2(even.y, run.y);
+        if (lane == 31) sc.last = expf(run.x + run.y);
+        __syncwarp();
+        if (lane == 0) arrive(&bars.gate_full[sb]);
       }
     } else if (warp == kRowWarp) {
       // -------------------------------------------------------------------- rows
@@ -714,31 +779,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t rows = tc::smem_u32(smem + st * kStageBytes);
         const uint64_t q_op = tc::sw128_desc(rows), v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
         if (!(ok = warp_wait(&bars.full[st], c / kStages) && warp_wait(&bars.wk_full, c))) break;
-        if (c > 1 && !(ok = warp_wait(&bars.ds_read[c & 1], (c >> 1) - 1))) break;
+        if (c > 0 && !(ok = warp_wait(&bars.ds_read, c - 1))) break;
         tc::tc_fence_after();
         if (leader) {  // dS^T = V^T K'
 #pragma unroll
           for (int b = 0; b < (F16 ? 2 : 3); ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc::mma_bf16(tmem + kTmU + 128 * (c & 1), v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU,
+              tc::mma_bf16(tmem + kTmU, v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU,
                            b + j > 0);
-          tc::mma_commit(&bars.ds_full[c & 1]);
+          tc::mma_commit(&bars.ds_full);
           if (LOCAL) tc::mma_commit(&bars.empty[st]);
         }
         __syncwarp();
         if (!LOCAL) {
           if (!(ok = warp_wait(&bars.s_full, c))) break;
-          if (c > 0 && !(ok = warp_wait(&bars.o_read, c - 1))) break;
+          if (c > 1 && !(ok = warp_wait(&bars.o_read[c & 1], (c >> 1) - 1))) break;
           tc::tc_fence_after();
           if (leader) {  // O1^T = S^T Q^T
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                mma_ts(tmem + kTmQ, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
+                mma_ts(tmem + kTmQ + 64 * (c & 1), tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
                        b + j > 0);
-            tc::mma_commit(&bars.qs_full);
+            tc::mma_commit(&bars.qs_full[c & 1]);
             tc::mma_commit(&bars.empty[st]);
           }
           __syncwarp();
@@ -751,23 +816,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdO = (F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64)) | tc::kIdescMnA;
         const bool leader = elect_one();
         const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + kP));
-        for (int c = 0; c < nch; ++c) {
+        auto scores = [&](int c) {  // Q K^T of chunk c, once the outputs of c - 2 are read
           const int st = c % kStages;
           const uint32_t rows = tc::smem_u32(smem + st * kStageBytes);
           const uint64_t q_op = tc::sw128_desc(rows), k_op = tc::sw128_desc(rows + kTile);
-          const uint64_t v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
-          if (!(ok = warp_wait(&bars.full[st], c / kStages))) break;
-          if (c > 0 && !(ok = warp_wait(&bars.o_read, c - 1))) break;  // Q K^T takes the place of the last O2
+          if (!warp_wait(&bars.full[st], c / kStages)) return false;
+          if (c > 1 && !warp_wait(&bars.o_read[c & 1], (c >> 1) - 1)) return false;
           tc::tc_fence_after();
-          if (leader) {  // Q K^T
+          if (leader) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint64_t off = ((j >> 2) * 8192 + (j & 3) * 32) >> 4;
-              tc::mma_bf16(tmem + kTmO, q_op + off, k_op + off, kIdP, j > 0);
+              tc::mma_bf16(tmem + kTmO + 64 * (c & 1), q_op + off, k_op + off, kIdP, j > 0);
             }
-            tc::mma_commit(&bars.qk_full);
+            tc::mma_commit(&bars.qk_full[c & 1]);
           }
           __syncwarp();
+          return true;
+        };
+        ok = scores(0);
+        for (int c = 0; c < nch && ok; ++c) {
+          const int st = c % kStages;
+          const uint64_t v_op = tc::sw128_desc_mn(tc::smem_u32(smem + st * kStageBytes) + 2 * kTile, 8192);
+          if (c + 1 < nch && !(ok = scores(c + 1))) break;
           if (!(ok = warp_wait(&bars.p_full, c))) break;
           tc::tc_fence_after();
           if (leader) {  // O2^T = V^T P^T
@@ -775,8 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < 2; ++b)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                tc::mma_bf16(tmem + kTmO, v_op + ((j * 2048) >> 4), p_op + ((b * 8192 + j * 32) >> 4), kIdO, b + j > 0);
-            tc::mma_commit(&bars.o_full);
+                tc::mma_bf16(tmem + kTmO + 64 * (c & 1), v_op + ((j * 2048) >> 4), p_op + ((b * 8192 + j * 32) >> 4), kIdO,
+                             b + j > 0);
+            tc::mma_commit(&bars.o_full[c & 1]);
             tc::mma_commit(&bars.empty[st]);
           }
           __syncwarp();

@@ -6,14 +6,15 @@ the 16-bit type (BF16 2^-8, FP16 2^-11 relative to the value):
   - an output is rounded once: u |o|, and FP16 numbers below 2^-14 lie 2^-24 apart,
     so that their rounding is off by up to 2^-25 whatever u |o| is;
   - inside a chunk the weights q.k e^(..) of the values are rounded once to 16
-    bits: u (1 + u) scale sum_j |q.k_j| e^(c_i - c_j) |v_j|.  FP16 weights are kept
-    relative to the largest of their row, with steps of 2^-25 of it at the bottom:
-    2^-25 max_j |weight| sum_j |v_j|;
+    bits: u (1 + u) scale sum_j |q.k_j| e^(c_i - c_j) |v_j|.  (A second 16 bits may
+    keep what that drops.)  FP16 weights are kept times a power of two that takes
+    |q_i| max_j |k_j| above 2^14, with steps of 2^-24 at the bottom, 2^-38 of that:
+    2^-39 scale |q_i| max_j |k_j| sum_j |v_j|;
   - everything else is FP32 or a pair of 16-bit halves: exponentials 2^-17 for the
     smallest factors, norms 2^-22, halves 2^-17, sums of 64 and 128 terms 2^-16.4
     of the magnitudes' sum, all told below 2^-14 of scale |q|.(|S| built from
-    magnitudes).  As a factor of FP16's the state is kept relative to its row's
-    largest, 2^-22 of which remains: 2^-22 |q|_1 max_k |S_vk|.
+    magnitudes).  As a factor of FP16's a row of the state is kept likewise: 2^-39 of
+    its largest, 2^-39 |q|_1 max_k |S_vk|.
   - states: 2^-14 of the sum of magnitudes.  FP16 parts of a decayed key end 2^-24
     apart: off by up to 2^-25 whatever the decay inside the chunk of 64 tokens has left
     of it (unit keys are taken times 2^15: 2^-40).  That adds 2^-25 sum |v_j| a chunk,
@@ -81,7 +82,7 @@ def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
         E = np.exp(c[t] - c0)[:, None] * E0 + mine
         o[t] = scale * (REST * np.einsum("hvk,hk->hv", S, aq) + E0 * aq.sum(-1)[:, None])
         if dtype == "f16":
-            o[t] += 2.0 ** -22 * scale * aq.sum(-1)[:, None] * S.max(-1)
+            o[t] += 2.0 ** -39 * scale * aq.sum(-1)[:, None] * S.max(-1)
     if not exact_weights:
         u = U[dtype]
         for h in range(v.shape[1]):
@@ -89,7 +90,8 @@ def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
                 w = scale * np.abs(q[:, h] @ k[:, h].T) * np.tril(np.exp(np.minimum(c[:, None, h] - c[None, :, h], 0)))
             o[:, h] += u * (1 + u) * (w @ v[:, h])
             if dtype == "f16":
-                o[:, h] += 2.0 ** -25 * w.max(1)[:, None] * np.cumsum(v[:, h], 0)
+                norm_of = lambda x: np.sqrt((x * x).sum(-1))  # noqa: E731
+                o[:, h] += 2.0 ** -39 * scale * (norm_of(q[:, h]) * norm_of(k[:, h]).max())[:, None] * np.cumsum(v[:, h], 0)
     return o, REST * S + E[:, :, None]
 
 
