@@ -18,10 +18,13 @@
 //   O2^T = V^T P^T   128 x 64 x 64, V as it landed, P in two halves
 //   dS^T = V^T K'    128 x 128 x 64, K'_j = e^(c_last - c_j) rk_j k_j in three parts
 //                    (FP16: two)
-// 8 warps keep the state and turn it into the operand S^T; 8 take norms and make K';
-// 8 turn Q K^T into P and, a chunk behind, write the outputs; one makes the decays'
-// factors, one loads rows, two issue the products, those of the state apart from
-// those within the chunk, so that neither waits for the other's operands.
+// 16 warps do all the arithmetic, together and a step of it at a time, since what they
+// execute then is in the SM's instruction caches: per chunk the state's update and its
+// operand, P, the outputs of the chunk before, and norms and K' of the chunk behind.
+// (Warps of a task each ran at 6 to 8 cycles an instruction, waiting for it: 5000
+// cycles a chunk.)  The products run meanwhile: each has a step or more of other work
+// before it is needed.  One warp loads rows, one issues products, two make the factors
+// of the decays.
 //
 // A long sequence is cut into segments: a first launch computes what each segment
 // adds to a state of zero (no queries, no outputs), and the CTAs of the second sum
@@ -54,7 +57,7 @@ struct LinPrefillArgs {
   int64_t total_tokens;
   kda_bf16* o;
   int64_t seg_tokens;   // tokens of a segment, a multiple of 64
-  float4* local_state;  // [segment, value head][16][256 threads]: what a segment adds
+  float4* local_state;  // [segment, value head][8][512 threads]: what a segment adds
   float* local_decay;   // [segment, value head]: e^(its log-decays' sum)
   int32_t* err_flag;
 };
@@ -63,13 +66,15 @@ struct LinMaps {
   CUtensorMap q, k, v;
 };
 
-// Factors of a chunk.  b is the first token of i's block of 16; where a block decays
-// by more than e^60 its rows of P get their factors term by term (far).
+// Factors of a chunk: of the decays first, then (all but w) times those of the norms.
+// b is the first token of i's block of 16; where a block decays by more than e^60 the
+// block's rows of P get their factors term by term (far).
 struct Scalars {
   float c_hi[kC], c_lo[kC];  // c_i
   float out[kC];             // scale rq_i e^(c_i)
   float row[kC];             // scale rq_i e^(c_i - c_b); far: scale rq_i
   float col[4][kC];          // rk_j e^(c_b - c_j) for b = 0, 16, 32, 48 and j < b + 16
+  float w[kC];               // e^(c_last - c_j), 0 past the segment's end
   float k[kC];               // rk_j
   float big[kC], kk[kC];     // FP16: |q_i| e^(c_b - c_i), far |q_i|; |k_j|^2
   float last;                // e^(c_last)
@@ -77,27 +82,21 @@ struct Scalars {
 };
 constexpr float kFar = 60.f;
 
+// Warps.
+constexpr int kWorkers = 16, kRowWarp = 16, kMmaWarp = 17, kGateWarp = 18, kThreads = 640;
+
 struct Bars {
-  uint64_t full[kStages], empty[kStages];  // rows landed, consumed
-  uint64_t gate_full[kScalarBufs];         // factors of the decays
-  uint64_t sc_full[kScalarBufs];           // all factors (and V's rows past the end zeroed)
-  uint64_t sc_free[kScalarBufs];           // read
-  uint64_t wk_full;                        // K'
-  uint64_t ds_full, ds_read;               // dS
-  uint64_t s_full, qs_full[2];             // operand S^T, O1
-  uint64_t qk_full[2], p_full, o_full[2];  // Q K^T, P, O2
-  uint64_t o_read[2];                      // O1 and O2 are in registers
-  uint64_t drained[2];                     // all products of an issuing warp; used where a wait has run out
+  uint64_t full[kStages], empty[kStages];                       // rows landed, consumed
+  uint64_t gate_full[kScalarBufs], sc_free[kScalarBufs];        // factors of the decays; all factors read
+  uint64_t wk_full, s_full, p_full;                             // operands: K' (and what else a chunk needs), S^T, P
+  uint64_t qk_full, ds_full, qs_full, o_full;                   // products: Q K^T, dS, O1, O2
+  uint64_t drained;                                             // all products
   uint32_t tmem;
   int timed_out;
-  float p_scale[2][kC];     // FP16: the powers of two of P's rows
-  float s_max[2][2][128];   //       largest magnitudes of half a row of S^T
-  float s_scale[3][128];    //       powers of two of its rows
+  float p_scale[2][kC];       // FP16: the powers of two of P's rows
+  float s_scale[3][128];      //       and of S^T's
+  uint8_t s_big[2][4][128];   //       exponents of the largest of a quarter of a row
 };
-
-// Warps.
-constexpr int kStateWarps = 8, kPrepWarp = 8, kPrepWarps = 8, kOutWarp = 16, kOutWarps = 8, kRowWarp = 24, kStateMma = 25,
-              kChunkMma = 26, kGateWarp = 27, kThreads = 896;
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
 // the parts of K', P's halves, factors, barriers.
@@ -159,10 +158,9 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// The power of two that takes numbers of up to m (finite, not negative) near FP16's
-// largest, below 2^15, where the steps at the other end matter least; and back.
-__device__ __forceinline__ float to_2p15(float m, float& back) {
-  uint32_t x = __float_as_uint(m) >> 23;  // m < 2^(x - 126)
+// The power of two that takes numbers of up to m near FP16's largest, below 2^15,
+// where the steps at the other end matter least; and back.
+__device__ __forceinline__ float to_2p15(uint32_t x, float& back) {  // x: m's exponent field; m < 2^(x - 126)
   x = x < 15 ? 15 : x > 253 ? 253 : x;
   back = __uint_as_float((x - 14) << 23);
   return __uint_as_float((268 - x) << 23);
@@ -198,13 +196,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// What is done with x comes after what was done before: without it the compiler makes
-// all of a row's operands first, and has no registers for them.
-__device__ __forceinline__ void hold16(float* x) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(x[i]));
-}
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread; 16 k are 8 columns of A.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
@@ -274,6 +265,9 @@ __device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
   const float s = a.x + b.x, z = s - a.x;
   return make_float2(s, a.y + (((a.x - (s - z)) + (b.x - z)) + b.y));
 }
+__device__ __forceinline__ float2 pair_from(float2 x, int l) {
+  return make_float2(__shfl_sync(0xffffffffu, x.x, l), __shfl_sync(0xffffffffu, x.y, l));
+}
 __device__ __forceinline__ float exp_diff(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
 
 // LOCAL: what segments add to a state of zero, or to the pool's.  Otherwise the outputs, and the
@@ -319,30 +313,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     leave();
     return;
   }
-  if (warp == kStateMma) tc::tmem_alloc(&bars.tmem, kTmCols);
+  if (warp == kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
     bars.timed_out = 0;
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(&bars.full[i], 1);
-      tc::mbar_init(&bars.empty[i], LOCAL ? 1 : 2);
+      tc::mbar_init(&bars.empty[i], 1);
     }
     for (int i = 0; i < kScalarBufs; ++i) {
       tc::mbar_init(&bars.gate_full[i], 1);
-      tc::mbar_init(&bars.sc_full[i], kPrepWarps);
-      tc::mbar_init(&bars.sc_free[i], LOCAL ? kStateWarps : kOutWarps);
+      tc::mbar_init(&bars.sc_free[i], kWorkers);
     }
-    tc::mbar_init(&bars.wk_full, kPrepWarps);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bars.qs_full[i], 1);
-      tc::mbar_init(&bars.qk_full[i], 1);
-      tc::mbar_init(&bars.o_full[i], 1);
-      tc::mbar_init(&bars.o_read[i], kOutWarps);
-      tc::mbar_init(&bars.drained[i], 1);
-    }
+    tc::mbar_init(&bars.wk_full, kWorkers);
+    tc::mbar_init(&bars.s_full, kWorkers);
+    tc::mbar_init(&bars.p_full, kWorkers);
+    tc::mbar_init(&bars.qk_full, 1);
     tc::mbar_init(&bars.ds_full, 1);
-    tc::mbar_init(&bars.ds_read, kStateWarps);
-    tc::mbar_init(&bars.s_full, kStateWarps);
-    tc::mbar_init(&bars.p_full, kOutWarps);
+    tc::mbar_init(&bars.qs_full, 1);
+    tc::mbar_init(&bars.o_full, 1);
+    tc::mbar_init(&bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::tc_fence_before();
@@ -354,15 +343,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float k_up = F16 && ga.use_qk_l2norm ? 32768.f : 1.f;
   bool ok = true;
 
-  // 896 threads start with 72 registers each; 256 at 112 and 640 at 56 are those 64512
-  if (warp < kStateWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-    // ------------------------------------------------------------------- state
-    const int quad = warp & 3, half = warp >> 2;
-    const int dv = 32 * quad + lane;  // this thread's value column; its key channels 64 half ..
+  if (warp < kWorkers) {
+    // A warp that runs out of time goes on without waiting and without arriving, so
+    // that the others meet it at their barrier and run out too.
+    const int quad = warp & 3, part = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    float* root = args.pool + (((size_t)slot * HV + h) * kHeadDim + dv) * kHeadDim + 64 * half;
-    float S[64];
+    auto done = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0 && ok) arrive(bar);
+    };
+
+    // ------------------------------------------------------------- norms and K'
+    // 4 rows a warp; of its row a thread has a 16-byte piece of either half of the channels
+    const int row = 4 * warp + (lane >> 3), x8 = lane & 7;
+    const bool squares = ga.use_qk_l2norm || F16;
+    int pst = 0, psb = 0;
+    uint32_t pst_phase = 0, psb_phase = 0;
+    auto prepare = [&](int c) {
+      const int left = L - c * kC;
+      Scalars& sc = scalars[psb];
+      ok = ok && warp_wait(&bars.gate_full[psb], psb_phase);
+      ok = ok && warp_wait(&bars.full[pst], pst_phase);
+      uint8_t* rows = smem + pst * kStageBytes;
+      uint4 kw[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) kw[p] = *line16(rows + kTile + p * 8192, row, x8);
+      float nk = 0.f, nq = 0.f;
+      if (squares) {
+        float2 sk = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = widen2<F16>(x[e]);
+            sk = fma2(f, f, sk);
+          }
+        }
+        nk = sk.x + sk.y;
+        if (!LOCAL) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint4 qw = *line16(rows + p * 8192, row, x8);
+            const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = widen2<F16>(x[e]);
+              sq = fma2(f, f, sq);
+            }
+          }
+          nq = sq.x + sq.y;
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+          nk += __shfl_xor_sync(0xffffffffu, nk, d);
+          if (!LOCAL) nq += __shfl_xor_sync(0xffffffffu, nq, d);
+        }
+      }
+      const float rk = ga.use_qk_l2norm ? rsqrtf(nk + kNormEps) : 1.f;
+      if (!LOCAL) {
+        const float rq = ga.scale * (ga.use_qk_l2norm ? rsqrtf(nq + kNormEps) : 1.f);
+        if (F16 && x8 == 7) {
+          sc.big[row] *= sqrtf(nq);
+          sc.kk[row] = nk;
+        }
+        if (x8 < 4)
+          sc.col[x8][row] *= rk;
+        else if (x8 < 6)
+          (x8 == 4 ? sc.out : sc.row)[row] *= rq;
+        else if (x8 == 6)
+          sc.k[row] = rk;
+      }
+      const float wk = row < left ? k_up * rk * sc.w[row] : 0.f;
+      if (row >= left) {  // the next sequence's values and keys: NaN times zero is NaN
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          *line16(rows + 2 * kTile + p * 8192, row, x8) = make_uint4(0, 0, 0, 0);
+          kw[p] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (c > 0) ok = ok && warp_wait(&bars.ds_full, c - 1);  // K' has been read
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
+        uint32_t piece[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 f = mul2(widen2<F16>(x[e]), make_float2(wk, wk)), rest;
+          piece[0][e] = round2<F16>(f, rest);
+          piece[1][e] = round2<F16>(rest, f);
+          if (!F16) piece[2][e] = round2<F16>(f, rest);
+        }
+#pragma unroll
+        for (int i = 0; i < (F16 ? 2 : 3); ++i)
+          *line16(smem + kWk + i * kTile + p * 8192, row, x8) = make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+      }
+      tc::fence_async_smem();
+      done(&bars.wk_full);
+      if (++pst == kStages) pst = 0, pst_phase ^= 1;
+      if (++psb == kScalarBufs) psb = 0, psb_phase ^= 1;
+    };
+
+    // --------------------------------------------------------------------- state
+    const int dv = 32 * quad + lane;  // this thread's value column; its key channels 32 part ..
+    float* root = args.pool + (((size_t)slot * HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
+    float S[32];
     auto record = [&](int64_t segment) { return args.local_state + (segment * HV + h) * 4096 + tid; };
     const int segments = seq_segments(args, seg.n);
     if (!LOCAL) grid_dependency_wait();
@@ -372,515 +457,397 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool copied = !LOCAL && segments > 1;
       const float4* copy = record(id + segments - 1);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float4 x = copied ? __ldcg(copy + j * 256) : *reinterpret_cast<const float4*>(root + 4 * j);
+      for (int j = 0; j < 8; ++j) {
+        const float4 x = copied ? __ldcg(copy + j * 512) : *reinterpret_cast<const float4*>(root + 4 * j);
         S[4 * j] = x.x, S[4 * j + 1] = x.y, S[4 * j + 2] = x.z, S[4 * j + 3] = x.w;
-        if (LOCAL) const_cast<float4*>(copy)[j * 256] = x;
-        if (j % 4 == 3) asm volatile("" ::: "memory");
+        if (LOCAL) const_cast<float4*>(copy)[j * 512] = x;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) S[j] = 0.f;
+      for (int j = 0; j < 32; ++j) S[j] = 0.f;
     }
     if (!LOCAL && seg.s > 0) {
       float up = 1.f;  // decay from the end of a segment before to the start of this one
       for (int m = seg.s - 1; m >= 0 && up > 0.f; --m) {
         const float4* src = record(id - seg.s + m);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 x = __ldcg(src + j * 256);
+        for (int j = 0; j < 8; ++j) {
+          const float4 x = __ldcg(src + j * 512);
           S[4 * j] = fmaf(up, x.x, S[4 * j]);
           S[4 * j + 1] = fmaf(up, x.y, S[4 * j + 1]);
           S[4 * j + 2] = fmaf(up, x.z, S[4 * j + 2]);
           S[4 * j + 3] = fmaf(up, x.w, S[4 * j + 3]);
-          if (j % 4 == 3) asm volatile("" ::: "memory");  // so many loads in flight as there are registers for
         }
         up *= __ldcg(args.local_decay + (int64_t)(id - seg.s + m) * HV + h);
       }
     }
     float decay = 1.f;
     const float k_down = 1.f / k_up;
-    // A warp that runs out of time goes on without waiting, so that the others still
-    // meet it at their barrier.
-    for (int c = 0; c < nch; ++c) {
-      const int sb = c % kScalarBufs;
-      ok = ok && warp_wait(&bars.gate_full[sb], c / kScalarBufs);
-      const float last = scalars[sb].last;
-      if (!LOCAL) {
-        float down = 1.f, row_scale = 1.f;
-        if constexpr (F16) {  // the row relative to its largest, by a power of two
-          float m = 0.f;
-#pragma unroll
-          for (int j = 0; j < 64; ++j) m = fmaxf(m, fabsf(S[j]));
-          bars.s_max[c & 1][half][dv] = m;
-          asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
-          m = fmaxf(m, bars.s_max[c & 1][half ^ 1][dv]);
-          down = to_2p15(m, row_scale);
-        }
-        if (c > 0) ok = ok && warp_wait(&bars.qs_full[(c - 1) & 1], (c - 1) >> 1);  // the operand has been read
-        // (and the scales of chunk c - 3, before whose outputs were read Q S of c - 1 did not start)
-        if (F16 && half == 0) bars.s_scale[c % 3][dv] = row_scale;
-        tc::tc_fence_after();
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t hi[8], lo[8];
-          hold16(S + 16 * g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float2 x = make_float2(S[16 * g + 2 * j], S[16 * g + 2 * j + 1]), rest;
-            if (F16) x = mul2(x, make_float2(down, down));
-            hi[j] = round2<F16>(x, rest);
-            lo[j] = round2<F16>(rest, x);
-          }
-          tmem_st8(lanes + kTmS + 32 * half + 8 * g, hi);
-          tmem_st8(lanes + kTmSlo + 32 * half + 8 * g, lo);
-        }
-        wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && ok) arrive(&bars.s_full);
-        if (c == nch - 1 && !last_segment) break;  // its state is of no use
-      }
+    auto update = [&](int c, float last) {  // S of the next chunk
       ok = ok && warp_wait(&bars.ds_full, c);
       tc::tc_fence_after();
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < 2; ++g) {
         uint32_t r[16];
-        tc::tmem_ld16_async(lanes + kTmU + 64 * half + 16 * g, r);
+        tc::tmem_ld16_async(lanes + kTmU + 32 * part + 16 * g, r);
         wait_ld(r);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           float2 u = make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
           if (F16) u = mul2(u, make_float2(k_down, k_down));
-          const float2 s = fma2(make_float2(last, last), make_float2(S[16 * g + j], S[16 * g + j + 1]), u);
-          S[16 * g + j] = s.x;
-          S[16 * g + j + 1] = s.y;
+          const float2 x = fma2(make_float2(last, last), make_float2(S[16 * g + j], S[16 * g + j + 1]), u);
+          S[16 * g + j] = x.x;
+          S[16 * g + j + 1] = x.y;
+        }
+      }
+      decay *= last;
+    };
+    auto operand = [&](int c) {
+      float down = 1.f;
+      if constexpr (F16) {  // the row times a power of two by its largest
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(S[j]));
+        bars.s_big[c & 1][part][dv] = (uint8_t)(__float_as_uint(m) >> 23);
+        asm volatile("barrier.cta.sync 1, 512;" ::: "memory");
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = max(x, (uint32_t)bars.s_big[c & 1][i][dv]);
+        float back;
+        down = to_2p15(x, back);
+        if (part == 0) bars.s_scale[c % 3][dv] = back;
+      }
+      if (c > 0) ok = ok && warp_wait(&bars.qs_full, c - 1);  // the last operand has been read
+      tc::tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float2 x = make_float2(S[16 * g + 2 * j], S[16 * g + 2 * j + 1]), rest;
+          if (F16) x = mul2(x, make_float2(down, down));
+          hi[j] = round2<F16>(x, rest);
+          lo[j] = round2<F16>(rest, x);
+        }
+        tmem_st8(lanes + kTmS + 16 * part + 8 * g, hi);
+        tmem_st8(lanes + kTmSlo + 16 * part + 8 * g, lo);
+      }
+      wait_st();
+    };
+
+    // ------------------------------------------------------------------------- P
+    // rows r0 and r0 + 8 of a 16 x 16 block, block `part` of the rows' four
+    const int r0 = 16 * quad + (lane >> 2), turn = r0 & 7;
+    uint8_t* at[2];  // where columns 2 (lane % 4) and + 1 of a row's first piece are, but for the swizzle
+#pragma unroll
+    for (int e = 0; e < 2; ++e) at[e] = smem + kP + (r0 + 8 * e) * 128 + 4 * (lane & 3);
+    auto put = [&](int j, int e, uint32_t hi, uint32_t lo) {
+      uint8_t* to = at[e] + ((j ^ turn) << 4);
+      *reinterpret_cast<uint32_t*>(to) = hi;
+      *reinterpret_cast<uint32_t*>(to + 8192) = lo;
+    };
+    if (!LOCAL && part > quad)  // right of the diagonal all is zero, and stays so
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0, 0);
+    auto weights = [&](int c, const Scalars& sc) {
+      ok = ok && warp_wait(&bars.qk_full, c);
+      if (c > 0) ok = ok && warp_wait(&bars.o_full, c - 1);  // the last P has been read
+      tc::tc_fence_after();
+      float2 down[2];  // FP16: powers of two of the rows
+      if constexpr (F16) {  // |q.k| is at most |q| |k|
+        float k2 = 1.f;
+        if (!ga.use_qk_l2norm) {
+          k2 = fmaxf(sc.kk[lane], sc.kk[lane + 32]);
+          k2 = sqrtf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(k2))));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float back;
+          down[e].x = down[e].y = to_2p15(__float_as_uint(sc.big[r0 + 8 * e] * k2) >> 23, back);
+          if (part == 0 && (lane & 3) == 0) bars.p_scale[c & 1][r0 + 8 * e] = back;
+        }
+      }
+      if (part <= quad) {
+        const uint32_t qk = lanes + kTmO + 64 * (c & 1) + 16 * part;
+        uint32_t r[2][4];
+        ld_frag8(qk, r[0]);
+        ld_frag8(qk + 8, r[1]);
+        const int b = 16 * quad;
+        const bool far = !((sc.c_hi[b] - sc.c_hi[b + 15]) + (sc.c_lo[b] - sc.c_lo[b + 15]) <= kFar);
+        wait_ld(r[0]);
+        wait_ld(r[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = 16 * part + 8 * i + 2 * (lane & 3);
+          float2 x[2];
+          if (!far) {
+            const float2 f = *reinterpret_cast<const float2*>(&sc.col[quad][col]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              x[e] = mul2(f, make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 c_i = make_float2(sc.c_hi[r0 + 8 * e], sc.c_lo[r0 + 8 * e]);
+              x[e].x = sc.k[col] * exp_diff(c_i, make_float2(sc.c_hi[col], sc.c_lo[col])) * __uint_as_float(r[i][2 * e]);
+              x[e].y = sc.k[col + 1] * exp_diff(c_i, make_float2(sc.c_hi[col + 1], sc.c_lo[col + 1])) *
+                       __uint_as_float(r[i][2 * e + 1]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (F16) x[e] = mul2(x[e], down[e]);
+            if (part == quad) {
+              const int i_row = r0 + 8 * e;
+              x[e].x = col <= i_row ? x[e].x : 0.f;
+              x[e].y = col < i_row ? x[e].y : 0.f;
+            }
+            float2 rest;
+            const uint32_t hi = round2<F16>(x[e], rest), lo = round2<F16>(rest, x[e]);
+            put(2 * part + i, e, hi, lo);
+          }
+        }
+      }
+      tc::fence_async_smem();
+      tc::tc_fence_before();
+      done(&bars.p_full);
+    };
+
+    // ------------------------------------------------------------------- outputs
+    // 32 value columns a warp, 16 tokens a thread
+    const int odd = lane & 1;
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
+    const int64_t step = (int64_t)HV * kHeadDim;
+    kda_bf16* dst = args.o + ((t0 + 16 * part + odd) * HV + h) * kHeadDim + ((32 * quad + lane) & ~1);
+    // (their products have been waited for, by the next chunk's operand and weights)
+    auto outputs = [&](int c, const Scalars& sc, uint64_t* free) {
+      const int tok = 16 * part, left = L - c * kC - tok - odd;
+      tc::tc_fence_after();
+      const float up = F16 ? bars.s_scale[c % 3][dv] : 1.f;
+      uint32_t y2[8];  // two tokens of one column each
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t q[8], r[8];
+        tmem_ld8_async(lanes + kTmQ + 64 * (c & 1) + tok + 8 * g, q);
+        tmem_ld8_async(lanes + kTmO + 64 * (c & 1) + tok + 8 * g, r);
+        wait_ld(q);
+        wait_ld(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t2 = tok + 8 * g + 2 * j;
+          float2 f = *reinterpret_cast<const float2*>(sc.out + t2), rest;
+          float2 y = mul2(*reinterpret_cast<const float2*>(sc.row + t2),
+                          make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+          if (F16) {
+            f = mul2(f, make_float2(up, up));
+            y = mul2(y, *reinterpret_cast<const float2*>(bars.p_scale[c & 1] + t2));
+          }
+          y2[4 * g + j] = round2<F16>(fma2(f, make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])), y), rest);
         }
       }
       tc::tc_fence_before();
+      done(free);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // traded for two columns of one token each
+        const uint32_t x = __byte_perm(y2[j], __shfl_xor_sync(0xffffffffu, y2[j], 1), pick);
+        if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = x;
+      }
+      dst += kC * step;
+    };
+
+    prepare(0);
+    float last = 1.f;
+    int sb = 0;  // the chunk's factors
+    for (int c = 0; c < nch; ++c) {
+      const Scalars& sc = scalars[sb];
+      if (c > 0) update(c - 1, last);
+      last = sc.last;  // its factors were there for prepare(c)
+      if (!LOCAL) operand(c);
+      tc::tc_fence_before();
+      done(&bars.s_full);
+      const int before = sb == 0 ? kScalarBufs - 1 : sb - 1;
+      if (LOCAL) {
+        done(&bars.sc_free[sb]);
+      } else {
+        weights(c, sc);
+        if (c > 0) outputs(c - 1, scalars[before], &bars.sc_free[before]);
+      }
+      if (c + 1 < nch) prepare(c + 1);
+      if (++sb == kScalarBufs) sb = 0;
+    }
+    if (!LOCAL) {
+      const int b = sb == 0 ? kScalarBufs - 1 : sb - 1;
+      ok = ok && warp_wait(&bars.qs_full, nch - 1);
+      ok = ok && warp_wait(&bars.o_full, nch - 1);
+      outputs(nch - 1, scalars[b], &bars.sc_free[b]);
+    }
+    if (LOCAL || last_segment) {
+      update(nch - 1, last);
+      if (LOCAL) {
+        float4* to = record(id);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) to[j * 512] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+        if (tid == 0) args.local_decay[(int64_t)id * HV + h] = decay;
+      } else if (ok) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(root + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+      }
+    }
+  } else if (warp == kRowWarp) {
+    // ------------------------------------------------------------------------ rows
+    const bool leader = elect_one();
+    int issued = 0;
+    for (int c = 0; c < nch; ++c) {
+      const int st = c % kStages;
+      if (c >= kStages && !(ok = warp_wait(&bars.empty[st], c / kStages - 1))) break;
+      uint8_t* rows = smem + st * kStageBytes;
+      if (leader) {
+        tc::mbar_expect_tx(&bars.full[st], LOCAL ? 2 * kTile : kStageBytes);
+        const int tok = (int)t0 + c * kC;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          tma_box(rows + kTile + a * 8192, &maps.k, a * 64, h / args.G, tok, &bars.full[st]);
+          if (!LOCAL) tma_box(rows + a * 8192, &maps.q, a * 64, h / args.G, tok, &bars.full[st]);
+          tma_box(rows + 2 * kTile + a * 8192, &maps.v, a * 64, h, tok, &bars.full[st]);
+        }
+      }
       __syncwarp();
-      if (lane == 0 && ok) {
-        arrive(&bars.ds_read);
-        if (LOCAL) arrive(&bars.sc_free[sb]);
-      }
-      decay *= last;
+      issued = c + 1;
     }
-    if (LOCAL) {
-      float4* dst = record(id);
+    // nothing may land after the CTA is gone
+    for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c) warp_wait(&bars.full[c % kStages], c / kStages);
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------------- products
+    constexpr uint32_t kType = F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
+    constexpr uint32_t kIdU = (F16 ? tc::idesc_f16_f32(128, 128) : tc::idesc_bf16_f32(128, 128)) | tc::kIdescMnA | tc::kIdescMnB;
+    constexpr uint32_t kIdP = F16 ? tc::idesc_f16_f32(64, 64) : tc::idesc_bf16_f32(64, 64);
+    const bool leader = elect_one();
+    const uint64_t wk_op = tc::sw128_desc_mn(tc::smem_u32(smem + kWk), 8192), p_op = tc::sw128_desc(tc::smem_u32(smem + kP));
+    for (int c = 0; c < nch; ++c) {
+      const int st = c % kStages;
+      const uint32_t rows = tc::smem_u32(smem + st * kStageBytes), turn = 64 * (c & 1);
+      const uint64_t q_op = tc::sw128_desc(rows), k_op = tc::sw128_desc(rows + kTile);
+      const uint64_t v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
+      // K' is the last of what a chunk needs before its state; the outputs of c - 2,
+      // whose place Q K^T takes, were read before
+      if (!(ok = warp_wait(&bars.full[st], c / kStages) && warp_wait(&bars.wk_full, c))) break;
+      tc::tc_fence_after();
+      if (!LOCAL && leader) {  // Q K^T
 #pragma unroll
-      for (int j = 0; j < 16; ++j) dst[j * 256] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-      if (tid == 0) args.local_decay[(int64_t)id * HV + h] = decay;
-    } else if (ok && last_segment) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        *reinterpret_cast<float4*>(root + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-    }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp < kOutWarp) {
-      // ------------------------------------------------------------ norms and K'
-      // a row's quarter a thread: 32 channels, four 16-byte pieces
-      const int row = 8 * (warp - kPrepWarp) + (lane & 7), x4 = lane >> 3, half = (x4 >> 1) * 8192, p0 = 4 * (x4 & 1);
-      const bool squares = ga.use_qk_l2norm || F16;
-      int st = 0, sb = 0;
-      uint32_t st_phase = 0, sb_phase = 0;
-      for (int c = 0; c < nch; ++c) {
-        const int left = L - c * kC;
-        Scalars& sc = scalars[sb];
-        if (!(ok = warp_wait(&bars.gate_full[sb], sb_phase))) break;
-        auto c_of = [&](int i) { return make_float2(sc.c_hi[i], sc.c_lo[i]); };
-        const float2 c_i = c_of(row);
-        const float e_w = exp_diff(c_of(kC - 1), c_i);
-        float e_row = 0.f, e_col = 0.f;
-        bool far = false;
-        if (!LOCAL) {
-          const float2 c_b = c_of(row & ~15), end = c_of(row | 15);
-          far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
-          e_row = x4 == 0 ? expf(c_i.x + c_i.y) : far ? 1.f : exp_diff(c_i, c_b);  // for out, for row
-          e_col = exp_diff(c_of(16 * x4), c_i);
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t off = ((j >> 2) * 8192 + (j & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + kTmO + turn, q_op + off, k_op + off, kIdP, j > 0);
         }
-        if (!(ok = warp_wait(&bars.full[st], st_phase))) break;
-        uint8_t* rows = smem + st * kStageBytes;
-        uint4 kw[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) kw[p] = *line16(rows + kTile + half, row, p0 + p);
-        float nk = 0.f, nq = 0.f;
-        if (squares) {
-          float2 sk = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = widen2<F16>(x[e]);
-              sk = fma2(f, f, sk);
-            }
-          }
-          nk = sk.x + sk.y;
-          if (!LOCAL) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              const uint4 qw = *line16(rows + half, row, p0 + p);
-              const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = widen2<F16>(x[e]);
-                sq = fma2(f, f, sq);
-              }
-            }
-            nq = sq.x + sq.y;
-            nq += __shfl_xor_sync(0xffffffffu, nq, 8);
-            nq += __shfl_xor_sync(0xffffffffu, nq, 16);
-          }
-          nk += __shfl_xor_sync(0xffffffffu, nk, 8);
-          nk += __shfl_xor_sync(0xffffffffu, nk, 16);
-        }
-        const float rk = ga.use_qk_l2norm ? rsqrtf(nk + kNormEps) : 1.f;
-        if (!LOCAL) {
-          const float rq = ga.scale * (ga.use_qk_l2norm ? rsqrtf(nq + kNormEps) : 1.f);
-          if (x4 < 2) (x4 == 0 ? sc.out : sc.row)[row] = rq * e_row;
-          if (x4 == 2) sc.k[row] = rk;
-          if (F16 && x4 == 1) sc.big[row] = __fdividef(sqrtf(nq), e_row);
-          if (F16 && x4 == 2) sc.kk[row] = nk;
-          sc.col[x4][row] = rk * e_col;
-        }
-        if (row >= left) {  // the next sequence's values: NaN times zero is NaN
-#pragma unroll
-          for (int p = 0; p < 4; ++p) *line16(rows + 2 * kTile + half, row, p0 + p) = make_uint4(0, 0, 0, 0);
-          tc::fence_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) arrive(&bars.sc_full[sb]);
-        const float wk = row < left ? k_up * rk * e_w : 0.f;
-        if (c > 0 && !(ok = warp_wait(&bars.ds_full, c - 1))) break;  // K' has been read
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
-          uint32_t part[3][4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 f = mul2(widen2<F16>(row < left ? x[e] : 0u), make_float2(wk, wk)), rest;
-            part[0][e] = round2<F16>(f, rest);
-            part[1][e] = round2<F16>(rest, f);
-            if (!F16) part[2][e] = round2<F16>(f, rest);
-          }
-#pragma unroll
-          for (int i = 0; i < (F16 ? 2 : 3); ++i)
-            *line16(smem + kWk + i * kTile + half, row, p0 + p) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
-        }
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive(&bars.wk_full);
-        if (++st == kStages) st = 0, st_phase ^= 1;
-        if (++sb == kScalarBufs) sb = 0, sb_phase ^= 1;
+        tc::mma_commit(&bars.qk_full);
       }
-    } else if (warp < kRowWarp) {
-      // ---------------------------------------------------------- P, and the outputs
+      __syncwarp();
+      if (!(ok = warp_wait(&bars.s_full, c))) break;
+      tc::tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int b = 0; b < (F16 ? 2 : 3); ++b)  // dS^T = V^T K'
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc::mma_bf16(tmem + kTmU, v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU, b + j > 0);
+        tc::mma_commit(&bars.ds_full);
+        if (LOCAL) {
+          tc::mma_commit(&bars.empty[st]);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)  // O1^T = S^T Q^T
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mma_ts(tmem + kTmQ + turn, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
+                     b + j > 0);
+          tc::mma_commit(&bars.qs_full);
+        }
+      }
+      __syncwarp();
       if (!LOCAL) {
-        const int w = warp & 3, part = (warp - kOutWarp) >> 2;
-        const int r0 = 16 * w + (lane >> 2);  // P: rows r0 and r0 + 8
-        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-        uint8_t* at[2];  // where columns 2 (lane % 4) and + 1 of a row's first piece are, but for the swizzle
-#pragma unroll
-        for (int e = 0; e < 2; ++e) at[e] = smem + kP + (r0 + 8 * e) * 128 + 4 * (lane & 3);
-        const int turn = r0 & 7;
-        if (part)
-          for (int j = 2 * w + 2; j < 8; ++j)  // right of the diagonal blocks all is zero, and stays so
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4)) = 0;
-              *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4) + 8192) = 0;
-            }
-        auto put = [&](int j, int e, float2 x) {
-          float2 rest;
-          const uint32_t hi = round2<F16>(x, rest), lo = round2<F16>(rest, x);
-          uint8_t* to = at[e] + ((j ^ turn) << 4);
-          *reinterpret_cast<uint32_t*>(to) = hi;
-          *reinterpret_cast<uint32_t*>(to + 8192) = lo;
-        };
-        // outputs: 32 value columns a warp, 32 tokens a thread
-        const int odd = lane & 1;
-        const uint32_t pick = odd ? 0x3276u : 0x5410u;
-        const int64_t step = (int64_t)HV * kHeadDim;
-        kda_bf16* dst = args.o + ((t0 + 32 * part + odd) * HV + h) * kHeadDim + ((32 * w + lane) & ~1);
-        for (int c = 0; c <= nch; ++c) {
-          if (c < nch) {
-            const Scalars& sc = scalars[c % kScalarBufs];
-            if (!(ok = warp_wait(&bars.sc_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.qk_full[c & 1], c >> 1))) break;
-            if (c > 0 && !(ok = warp_wait(&bars.o_full[(c - 1) & 1], (c - 1) >> 1))) break;  // the last P has been read
-            tc::tc_fence_after();
-            float2 down[2];  // FP16: powers of two of the rows
-            if constexpr (F16) {  // |q.k| is at most |q| |k|
-              float k2 = 1.f;
-              if (!ga.use_qk_l2norm) {
-                k2 = fmaxf(sc.kk[lane], sc.kk[lane + 32]);
-                k2 = sqrtf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(k2))));
-              }
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float back;
-                down[e].x = down[e].y = to_2p15(sc.big[r0 + 8 * e] * k2, back);
-                if (part && (lane & 3) == 0) bars.p_scale[c & 1][r0 + 8 * e] = back;
-              }
-            }
-            const uint32_t qk = lanes + kTmO + 64 * (c & 1);
-            const bool far = !((sc.c_hi[16 * w] - sc.c_hi[16 * w + 15]) + (sc.c_lo[16 * w] - sc.c_lo[16 * w + 15]) <= kFar);
-            // the two warps of these rows take every other block, from the diagonal
-            for (int b = w - part; b >= 0; b -= 2) {
-              uint32_t r[2][4];
-              ld_frag8(qk + 16 * b, r[0]);
-              ld_frag8(qk + 16 * b + 8, r[1]);
-              wait_ld(r[0]);
-              wait_ld(r[1]);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int col = 16 * b + 8 * i + 2 * (lane & 3);
-                float2 x[2];
-                if (!far) {
-                  const float2 f = *reinterpret_cast<const float2*>(&sc.col[w][col]);
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    x[e] = mul2(f, make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])));
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const float2 c_i = make_float2(sc.c_hi[r0 + 8 * e], sc.c_lo[r0 + 8 * e]);
-                    x[e].x = sc.k[col] * exp_diff(c_i, make_float2(sc.c_hi[col], sc.c_lo[col])) * __uint_as_float(r[i][2 * e]);
-                    x[e].y = sc.k[col + 1] * exp_diff(c_i, make_float2(sc.c_hi[col + 1], sc.c_lo[col + 1])) *
-                             __uint_as_float(r[i][2 * e + 1]);
-                  }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  if (F16) x[e] = mul2(x[e], down[e]);
-                  if (b == w) {
-                    const int row = r0 + 8 * e;
-                    x[e].x = col <= row ? x[e].x : 0.f;
-                    x[e].y = col < row ? x[e].y : 0.f;
-                  }
-                  put(2 * b + i, e, x[e]);
-                }
-              }
-            }
-            tc::fence_async_smem();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&bars.p_full);
-          }
-          if (c > 0) {
-            const int d = c - 1, ob = d & 1;
-            const Scalars& sc = scalars[d % kScalarBufs];
-            if (!(ok = warp_wait(&bars.qs_full[ob], d >> 1) && warp_wait(&bars.o_full[ob], d >> 1))) break;
-            tc::tc_fence_after();
-            const float up = F16 ? bars.s_scale[d % 3][32 * w + lane] : 1.f;
-            const int left = L - d * kC - 32 * part - odd;
-            uint32_t y2[16];  // two tokens of one column each
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int tok = 32 * part + 8 * g;
-              uint32_t q[8], r[8];
-              tmem_ld8_async(lanes + kTmQ + 64 * ob + tok, q);
-              tmem_ld8_async(lanes + kTmO + 64 * ob + tok, r);
-              wait_ld(q);
-              wait_ld(r);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float2 f = *reinterpret_cast<const float2*>(sc.out + tok + 2 * j), rest;
-                float2 y = mul2(*reinterpret_cast<const float2*>(sc.row + tok + 2 * j),
-                                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                if (F16) {
-                  f = mul2(f, make_float2(up, up));
-                  y = mul2(y, *reinterpret_cast<const float2*>(bars.p_scale[ob] + tok + 2 * j));
-                }
-                y2[4 * g + j] = round2<F16>(fma2(f, make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])), y), rest);
-              }
-            }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              arrive(&bars.o_read[ob]);
-              arrive(&bars.sc_free[d % kScalarBufs]);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {  // traded for two columns of one token each
-              const uint32_t x = __byte_perm(y2[j], __shfl_xor_sync(0xffffffffu, y2[j], 1), pick);
-              if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = x;
-            }
-            dst += kC * step;
-          }
-        }
-      }
-    } else if (warp == kGateWarp) {
-      // --------------------------------------------------------- the decays' factors
-      const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-      const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
-      ushort2 raw[2][2];  // of the next two chunks, tokens 2 lane and 2 lane + 1
-      auto load_gate = [&](int c, ushort2 (&x)[2]) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x[e] = make_ushort2(0, 0);
-          if (c * kC + 2 * lane + e < L) x[e] = lin_gate_load(ga, (t0 + c * kC + 2 * lane + e) * HV + h);
-        }
-      };
-      load_gate(0, raw[0]);
-      load_gate(1, raw[1]);
-      for (int c = 0; c < nch; ++c) {
-        const int left = L - c * kC, sb = c % kScalarBufs;
-        Scalars& sc = scalars[sb];
-        const float g0 = 2 * lane < left ? lin_log_decay<F16>(ga, raw[0][0], neg_rate, bias) : 0.f;
-        const float g1 = 2 * lane + 1 < left ? lin_log_decay<F16>(ga, raw[0][1], neg_rate, bias) : 0.f;
-        raw[0][0] = raw[1][0], raw[0][1] = raw[1][1];
-        load_gate(c + 2, raw[1]);
-        float2 run = pair_add(make_float2(g0, 0.f), make_float2(g1, 0.f));  // c of token 2 lane + 1
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
-          if (lane >= d) run = pair_add(up, run);
-        }
-        const float2 even = pair_add(run, make_float2(-g1, 0.f));  // of token 2 lane
-        if (c >= kScalarBufs && !(ok = warp_wait(&bars.sc_free[sb], c / kScalarBufs - 1))) break;
-        *reinterpret_cast<float2*>(sc.c_hi + 2 * lane) = make_float2(even.x, run.x);
-        *reinterpret_cast<float2*>(sc.c_lo + 2 * lane) = make_float2(even.y, run.y);
-        if (lane == 31) sc.last = expf(run.x + run.y);
-        __syncwarp();
-        if (lane == 0) arrive(&bars.gate_full[sb]);
-      }
-    } else if (warp == kRowWarp) {
-      // -------------------------------------------------------------------- rows
-      const bool leader = elect_one();
-      int issued = 0;
-      for (int c = 0; c < nch; ++c) {
-        const int st = c % kStages;
-        if (c >= kStages && !(ok = warp_wait(&bars.empty[st], c / kStages - 1))) break;
-        uint8_t* rows = smem + st * kStageBytes;
-        if (leader) {
-          tc::mbar_expect_tx(&bars.full[st], LOCAL ? 2 * kTile : kStageBytes);
-          const int tok = (int)t0 + c * kC;
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            tma_box(rows + kTile + a * 8192, &maps.k, a * 64, h / args.G, tok, &bars.full[st]);
-            if (!LOCAL) tma_box(rows + a * 8192, &maps.q, a * 64, h / args.G, tok, &bars.full[st]);
-            tma_box(rows + 2 * kTile + a * 8192, &maps.v, a * 64, h, tok, &bars.full[st]);
-          }
-        }
-        __syncwarp();
-        issued = c + 1;
-      }
-      // nothing may land after the CTA is gone
-      for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c) warp_wait(&bars.full[c % kStages], c / kStages);
-    } else if (warp == kStateMma) {
-      // ------------------------------------------------- products of the state
-      constexpr uint32_t kType = F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
-      constexpr uint32_t kIdU = (F16 ? tc::idesc_f16_f32(128, 128) : tc::idesc_bf16_f32(128, 128)) | tc::kIdescMnA | tc::kIdescMnB;
-      const bool leader = elect_one();
-      const uint64_t wk_op = tc::sw128_desc_mn(tc::smem_u32(smem + kWk), 8192);
-      for (int c = 0; c < nch; ++c) {
-        const int st = c % kStages;
-        const uint32_t rows = tc::smem_u32(smem + st * kStageBytes);
-        const uint64_t q_op = tc::sw128_desc(rows), v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
-        if (!(ok = warp_wait(&bars.full[st], c / kStages) && warp_wait(&bars.wk_full, c))) break;
-        if (c > 0 && !(ok = warp_wait(&bars.ds_read, c - 1))) break;
+        if (!(ok = warp_wait(&bars.p_full, c))) break;
         tc::tc_fence_after();
-        if (leader) {  // dS^T = V^T K'
+        if (leader) {  // O2^T = V^T P^T
 #pragma unroll
-          for (int b = 0; b < (F16 ? 2 : 3); ++b)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc::mma_bf16(tmem + kTmU, v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU,
+              tc::mma_bf16(tmem + kTmO + turn, v_op + ((j * 2048) >> 4), p_op + ((b * 8192 + j * 32) >> 4), kType | tc::kIdescMnA,
                            b + j > 0);
-          tc::mma_commit(&bars.ds_full);
-          if (LOCAL) tc::mma_commit(&bars.empty[st]);
+          tc::mma_commit(&bars.o_full);
+          tc::mma_commit(&bars.empty[st]);
         }
         __syncwarp();
-        if (!LOCAL) {
-          if (!(ok = warp_wait(&bars.s_full, c))) break;
-          if (c > 1 && !(ok = warp_wait(&bars.o_read[c & 1], (c >> 1) - 1))) break;
-          tc::tc_fence_after();
-          if (leader) {  // O1^T = S^T Q^T
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                mma_ts(tmem + kTmQ + 64 * (c & 1), tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
-                       b + j > 0);
-            tc::mma_commit(&bars.qs_full[c & 1]);
-            tc::mma_commit(&bars.empty[st]);
-          }
-          __syncwarp();
-        }
-      }
-    } else if (warp == kChunkMma) {
-      // -------------------------------------------- products within the chunk
-      if (!LOCAL) {
-        constexpr uint32_t kIdP = F16 ? tc::idesc_f16_f32(64, 64) : tc::idesc_bf16_f32(64, 64);
-        constexpr uint32_t kIdO = (F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64)) | tc::kIdescMnA;
-        const bool leader = elect_one();
-        const uint64_t p_op = tc::sw128_desc(tc::smem_u32(smem + kP));
-        auto scores = [&](int c) {  // Q K^T of chunk c, once the outputs of c - 2 are read
-          const int st = c % kStages;
-          const uint32_t rows = tc::smem_u32(smem + st * kStageBytes);
-          const uint64_t q_op = tc::sw128_desc(rows), k_op = tc::sw128_desc(rows + kTile);
-          if (!warp_wait(&bars.full[st], c / kStages)) return false;
-          if (c > 1 && !warp_wait(&bars.o_read[c & 1], (c >> 1) - 1)) return false;
-          tc::tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint64_t off = ((j >> 2) * 8192 + (j & 3) * 32) >> 4;
-              tc::mma_bf16(tmem + kTmO + 64 * (c & 1), q_op + off, k_op + off, kIdP, j > 0);
-            }
-            tc::mma_commit(&bars.qk_full[c & 1]);
-          }
-          __syncwarp();
-          return true;
-        };
-        ok = scores(0);
-        for (int c = 0; c < nch && ok; ++c) {
-          const int st = c % kStages;
-          const uint64_t v_op = tc::sw128_desc_mn(tc::smem_u32(smem + st * kStageBytes) + 2 * kTile, 8192);
-          if (c + 1 < nch && !(ok = scores(c + 1))) break;
-          if (!(ok = warp_wait(&bars.p_full, c))) break;
-          tc::tc_fence_after();
-          if (leader) {  // O2^T = V^T P^T
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                tc::mma_bf16(tmem + kTmO + 64 * (c & 1), v_op + ((j * 2048) >> 4), p_op + ((b * 8192 + j * 32) >> 4), kIdO,
-                             b + j > 0);
-            tc::mma_commit(&bars.o_full[c & 1]);
-            tc::mma_commit(&bars.empty[st]);
-          }
-          __syncwarp();
-        }
       }
     }
+  } else {
+    // ----------------------------------------------------------- the decays' factors
+    // one of two warps, every other chunk
+    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
+    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
+    ushort2 next[2];  // of tokens 2 lane and 2 lane + 1
+    auto load_gate = [&](int c) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        next[e] = make_ushort2(0, 0);
+        if (c * kC + 2 * lane + e < L) next[e] = lin_gate_load(ga, (t0 + c * kC + 2 * lane + e) * HV + h);
+      }
+    };
+    load_gate(warp - kGateWarp);
+    for (int c = warp - kGateWarp; c < nch; c += 2) {
+      const int left = L - c * kC, sb = c % kScalarBufs;
+      Scalars& sc = scalars[sb];
+      const float g0 = 2 * lane < left ? lin_log_decay<F16>(ga, next[0], neg_rate, bias) : 0.f;
+      const float g1 = 2 * lane + 1 < left ? lin_log_decay<F16>(ga, next[1], neg_rate, bias) : 0.f;
+      load_gate(c + 2);
+      float2 run = pair_add(make_float2(g0, 0.f), make_float2(g1, 0.f));  // c of token 2 lane + 1
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
+        if (lane >= d) run = pair_add(up, run);
+      }
+      const float2 even = pair_add(run, make_float2(-g1, 0.f));  // of token 2 lane
+      if (c >= kScalarBufs && !(ok = warp_wait(&bars.sc_free[sb], c / kScalarBufs - 1))) break;
+      auto put2 = [&](float* to, float a, float b) { *reinterpret_cast<float2*>(to + 2 * lane) = make_float2(a, b); };
+      const float2 c_last = pair_from(run, 31);
+      put2(sc.w, 2 * lane < left ? exp_diff(c_last, even) : 0.f, 2 * lane + 1 < left ? exp_diff(c_last, run) : 0.f);
+      if (lane == 31) sc.last = expf(run.x + run.y);
+      if (!LOCAL) {
+        put2(sc.c_hi, even.x, run.x);
+        put2(sc.c_lo, even.y, run.y);
+        put2(sc.out, expf(even.x + even.y), expf(run.x + run.y));
+        const float2 c_b = pair_from(even, lane & 24), end = pair_from(run, lane | 7);
+        const bool far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
+        const float e0 = far ? 1.f : exp_diff(even, c_b), e1 = far ? 1.f : exp_diff(run, c_b);
+        put2(sc.row, e0, e1);
+        if (F16) put2(sc.big, 1.f / e0, 1.f / e1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 ref = pair_from(even, 8 * x);
+          const bool some = lane < 8 * x + 8;
+          put2(sc.col[x], some ? exp_diff(ref, even) : 0.f, some ? exp_diff(ref, run) : 0.f);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&bars.gate_full[sb]);
+    }
   }
-  // Where a wait has run out, products may still be under way: their issuing warps
-  // wait for them, with a limit, before TMEM and shared memory go.
+  // All products have been waited for but those whose results nobody needs; where a
+  // wait has run out, with a limit, before TMEM and shared memory go.
   if (!ok) bars.timed_out = 1;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (bars.timed_out) {
-    if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
-    if (warp == kStateMma || warp == kChunkMma) {
-      uint64_t* bar = &bars.drained[warp == kChunkMma];
-      if (elect_one()) tc::mma_commit(bar);  // the same lane as issued them
-      __syncwarp();
-      warp_wait(bar, 0);
-    }
-    __syncthreads();
-  } else {
-    // every product has been waited for but the last ones whose results nobody needs
-    if (warp == kStateMma) {
-      if (elect_one()) tc::mma_commit(&bars.drained[0]);
-      __syncwarp();
-      warp_wait(&bars.drained[0], 0);
-    }
-    __syncthreads();
+  if (warp == kMmaWarp) {
+    if (elect_one()) tc::mma_commit(&bars.drained);  // the same lane as issued them
+    __syncwarp();
+    warp_wait(&bars.drained, 0);
   }
-  if (warp == kStateMma) tc::tmem_dealloc(tmem, kTmCols);
+  if (bars.timed_out && tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
 }
 
 // Tensor map of a [T][heads][128] 16-bit tensor, box (64 elements, 1 head, 64
