@@ -66,7 +66,7 @@ struct LinMaps {
   CUtensorMap q, k, v;
 };
 
-// Factors of a chunk: of the decays first, then (all but w) times those of the norms.
+// Factors of a chunk: of the decays first, then times those of the norms.
 // b is the first token of i's block of 16; where a block decays by more than e^60 the
 // block's rows of P get their factors term by term (far).
 struct Scalars {
@@ -74,7 +74,7 @@ struct Scalars {
   float out[kC];             // scale rq_i e^(c_i)
   float row[kC];             // scale rq_i e^(c_i - c_b); far: scale rq_i
   float col[4][kC];          // rk_j e^(c_b - c_j) for b = 0, 16, 32, 48 and j < b + 16
-  float w[kC];               // e^(c_last - c_j), 0 past the segment's end
+  float w[kC];               // rk_j e^(c_last - c_j), 0 past the segment's end
   float k[kC];               // rk_j
   float big[kC], kk[kC];     // FP16: |q_i| e^(c_b - c_i), far |q_i|; |k_j|^2
   float last;                // e^(c_last)
@@ -86,22 +86,26 @@ constexpr float kFar = 60.f;
 constexpr int kWorkers = 16, kRowWarp = 16, kMmaWarp = 17, kGateWarp = 18, kThreads = 640;
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages];                       // rows landed, consumed
-  uint64_t gate_full[kScalarBufs], sc_free[kScalarBufs];        // factors of the decays; all factors read
-  uint64_t wk_full, s_full, p_full;                             // operands: K' (and what else a chunk needs), S^T, P
-  uint64_t qk_full, ds_full, qs_full, o_full;                   // products: Q K^T, dS, O1, O2
-  uint64_t drained;                                             // all products
+  uint64_t in_full[kScalarBufs];     // rows landed, and factors of the decays
+  uint64_t empty[kStages];           // rows consumed
+  uint64_t sc_free[kScalarBufs];     // factors read
+  uint64_t wk_full, s_full, p_full;  // operands: K' (and what else a chunk needs), S^T, P
+  uint64_t qk_full, sq_full;         // products: Q K^T (and the last O2), dS and O1
+  uint64_t o_full;                   // the segment's last O2
+  uint64_t drained;                  // all products
   uint32_t tmem;
   int timed_out;
-  float p_scale[2][kC];       // FP16: the powers of two of P's rows
-  float s_scale[3][128];      //       and of S^T's
-  uint8_t s_big[2][4][128];   //       exponents of the largest of a quarter of a row
+  float p_scale[2][kC];      // FP16: the powers of two of P's rows
+  float s_scale[3][128];     //       and of S^T's
+  uint8_t s_big[2][4][128];  //       exponents of the largest of a quarter of a row
 };
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
 // the parts of K', P's halves, factors, barriers.
 constexpr int kTile = 16384, kStageBytes = 3 * kTile;
 constexpr int kWk = kStages * kStageBytes, kP = kWk + 3 * kTile, kScalars = kP + 16384;
+constexpr int kLocalStage = 2 * kTile, kLocalWk = 3 * kTile;  // LOCAL: K and V alone, and K' twice
+static_assert(kStages * kLocalStage + 2 * kLocalWk <= kScalars, "the first launch's layout");
 constexpr int kBars = kScalars + kScalarBufs * (int)sizeof(Scalars);
 constexpr int kSmem = kBars + (int)sizeof(Bars);
 static_assert(kSmem <= 232448 - 1024 && kBars % 16 == 0, "shared memory");
@@ -178,11 +182,6 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[M]) {
 #pragma unroll
   for (int i = 0; i < M; ++i) asm volatile("" : "+r"(r[i]));
 }
-__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
 // 16 rows and 8 columns in the fragment layout: rows lane / 4 and + 8, columns
 // 2 (lane % 4) and + 1.
 __device__ __forceinline__ void ld_frag8(uint32_t taddr, uint32_t (&r)[4]) {
@@ -196,6 +195,26 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread; 16 k are 8 columns of A.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
@@ -316,20 +335,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
     bars.timed_out = 0;
-    for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(&bars.full[i], 1);
-      tc::mbar_init(&bars.empty[i], 1);
-    }
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&bars.empty[i], 1);
     for (int i = 0; i < kScalarBufs; ++i) {
-      tc::mbar_init(&bars.gate_full[i], 1);
+      tc::mbar_init(&bars.in_full[i], 2);
       tc::mbar_init(&bars.sc_free[i], kWorkers);
     }
     tc::mbar_init(&bars.wk_full, kWorkers);
     tc::mbar_init(&bars.s_full, kWorkers);
     tc::mbar_init(&bars.p_full, kWorkers);
     tc::mbar_init(&bars.qk_full, 1);
-    tc::mbar_init(&bars.ds_full, 1);
-    tc::mbar_init(&bars.qs_full, 1);
+    tc::mbar_init(&bars.sq_full, 1);
     tc::mbar_init(&bars.o_full, 1);
     tc::mbar_init(&bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -353,95 +368,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && ok) arrive(bar);
     };
 
-    // ------------------------------------------------------------- norms and K'
+    auto await = [&](uint64_t* bar, uint32_t phase) {
+      if (ok && !__all_sync(0xffffffffu, tc::mbar_try_wait(bar, phase & 1u))) ok = warp_wait(bar, phase);
+    };
+    constexpr int kStage = LOCAL ? kLocalStage : kStageBytes, kK = LOCAL ? 0 : kTile;
+
+    // --------------------------------------------------------------------- norms
+    // The squares of 16 rows of K (warps 0 to 3) or Q (4 to 7) are the diagonal of the
+    // rows times themselves, by register-to-register products; then the factors.
+    const int r16 = 16 * (warp & 3) + (lane & 15);
+    const bool normed = warp < 8 && !(LOCAL && warp >= 4) && (ga.use_qk_l2norm || F16);
+    auto norms = [&](int c, int st, Scalars& sc) {
+      await(&bars.in_full[c % kScalarBufs], c / kScalarBufs);
+      if (!normed) return;
+      const uint8_t* tile = smem + st * kStage + (warp < 4 ? kK : 0);
+      float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t f[4];
+        ldm4(tc::smem_u32(tile) + (k >> 2) * 8192 + r16 * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (r16 & 7)) << 4), f);
+        mma16<F16>(lo, f, f[0], f[2]);
+        mma16<F16>(hi, f, f[1], f[3]);
+      }
+      // row g of lo is in lane 4 g + g / 2, and so is row g + 8 of hi
+      const int g = lane >> 2, from = 4 * (lane & 7) + ((lane & 7) >> 1);
+      const float d_lo = __shfl_sync(0xffffffffu, g & 1 ? lo[1] : lo[0], from);
+      const float d_hi = __shfl_sync(0xffffffffu, g & 1 ? hi[3] : hi[2], from);
+      const float n = lane & 8 ? d_hi : d_lo, r = ga.use_qk_l2norm ? rsqrtf(n + kNormEps) : 1.f;
+      const bool upper = lane >= 16;
+      if (warp < 4) {
+        if (ga.use_qk_l2norm) {
+          if (!LOCAL) {
+            sc.col[upper ? 1 : 0][r16] *= r;
+            sc.col[upper ? 3 : 2][r16] *= r;
+          }
+          if (upper) sc.w[r16] *= r; else sc.k[r16] = r;
+        } else if (upper) {
+          sc.kk[r16] = r16 < L - c * kC ? n : 0.f;  // of this sequence alone
+        }
+      } else {
+        if (ga.use_qk_l2norm) (upper ? sc.row : sc.out)[r16] *= r;
+        if (F16 && !upper) sc.big[r16] *= sqrtf(n);
+      }
+    };
+
+    // ------------------------------------------------------------------------- K'
     // 4 rows a warp; of its row a thread has a 16-byte piece of either half of the channels
     const int row = 4 * warp + (lane >> 3), x8 = lane & 7;
-    const bool squares = ga.use_qk_l2norm || F16;
-    int pst = 0, psb = 0;
-    uint32_t pst_phase = 0, psb_phase = 0;
-    auto prepare = [&](int c) {
+    auto keys = [&](int c, int st, const Scalars& sc) {
       const int left = L - c * kC;
-      Scalars& sc = scalars[psb];
-      ok = ok && warp_wait(&bars.gate_full[psb], psb_phase);
-      ok = ok && warp_wait(&bars.full[pst], pst_phase);
-      uint8_t* rows = smem + pst * kStageBytes;
+      uint8_t* rows = smem + st * kStage + kK;
+      uint8_t* to = smem + (LOCAL ? kStages * kLocalStage + (c & 1) * kLocalWk : kWk);
+      const float wk = sc.w[row];
       uint4 kw[2];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) kw[p] = *line16(rows + kTile + p * 8192, row, x8);
-      float nk = 0.f, nq = 0.f;
-      if (squares) {
-        float2 sk = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = widen2<F16>(x[e]);
-            sk = fma2(f, f, sk);
-          }
-        }
-        nk = sk.x + sk.y;
-        if (!LOCAL) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint4 qw = *line16(rows + p * 8192, row, x8);
-            const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = widen2<F16>(x[e]);
-              sq = fma2(f, f, sq);
-            }
-          }
-          nq = sq.x + sq.y;
-        }
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) {
-          nk += __shfl_xor_sync(0xffffffffu, nk, d);
-          if (!LOCAL) nq += __shfl_xor_sync(0xffffffffu, nq, d);
-        }
-      }
-      const float rk = ga.use_qk_l2norm ? rsqrtf(nk + kNormEps) : 1.f;
-      if (!LOCAL) {
-        const float rq = ga.scale * (ga.use_qk_l2norm ? rsqrtf(nq + kNormEps) : 1.f);
-        if (F16 && x8 == 7) {
-          sc.big[row] *= sqrtf(nq);
-          sc.kk[row] = nk;
-        }
-        if (x8 < 4)
-          sc.col[x8][row] *= rk;
-        else if (x8 < 6)
-          (x8 == 4 ? sc.out : sc.row)[row] *= rq;
-        else if (x8 == 6)
-          sc.k[row] = rk;
-      }
-      const float wk = row < left ? k_up * rk * sc.w[row] : 0.f;
+      for (int p = 0; p < 2; ++p) kw[p] = *line16(rows + p * 8192, row, x8);
       if (row >= left) {  // the next sequence's values and keys: NaN times zero is NaN
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          *line16(rows + 2 * kTile + p * 8192, row, x8) = make_uint4(0, 0, 0, 0);
+          *line16(rows + kTile + p * 8192, row, x8) = make_uint4(0, 0, 0, 0);
           kw[p] = make_uint4(0, 0, 0, 0);
         }
       }
-      if (c > 0) ok = ok && warp_wait(&bars.ds_full, c - 1);  // K' has been read
+      const float w = row < left ? wk : 0.f;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
         uint32_t piece[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float2 f = mul2(widen2<F16>(x[e]), make_float2(wk, wk)), rest;
+          float2 f = mul2(widen2<F16>(x[e]), make_float2(w, w)), rest;
           piece[0][e] = round2<F16>(f, rest);
           piece[1][e] = round2<F16>(rest, f);
           if (!F16) piece[2][e] = round2<F16>(f, rest);
         }
 #pragma unroll
         for (int i = 0; i < (F16 ? 2 : 3); ++i)
-          *line16(smem + kWk + i * kTile + p * 8192, row, x8) = make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+          *line16(to + i * kTile + p * 8192, row, x8) = make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
       }
-      tc::fence_async_smem();
-      done(&bars.wk_full);
-      if (++pst == kStages) pst = 0, pst_phase ^= 1;
-      if (++psb == kScalarBufs) psb = 0, psb_phase ^= 1;
     };
 
     // --------------------------------------------------------------------- state
@@ -484,12 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float decay = 1.f;
     const float k_down = 1.f / k_up;
     auto update = [&](int c, float last) {  // S of the next chunk
-      ok = ok && warp_wait(&bars.ds_full, c);
       tc::tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t r[16];
-        tc::tmem_ld16_async(lanes + kTmU + 32 * part + 16 * g, r);
+        tc::tmem_ld16_async(lanes + kTmU + (LOCAL ? 128 * (c & 1) : 0) + 32 * part + 16 * g, r);
         wait_ld(r);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -517,8 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         down = to_2p15(x, back);
         if (part == 0) bars.s_scale[c % 3][dv] = back;
       }
-      if (c > 0) ok = ok && warp_wait(&bars.qs_full, c - 1);  // the last operand has been read
-      tc::tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t hi[8], lo[8];
@@ -552,8 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0, 0);
     auto weights = [&](int c, const Scalars& sc) {
-      ok = ok && warp_wait(&bars.qk_full, c);
-      if (c > 0) ok = ok && warp_wait(&bars.o_full, c - 1);  // the last P has been read
+      await(&bars.qk_full, c);  // the last P has been read too
       tc::tc_fence_after();
       float2 down[2];  // FP16: powers of two of the rows
       if constexpr (F16) {  // |q.k| is at most |q| |k|
@@ -610,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      tc::fence_async_smem();
       tc::tc_fence_before();
       done(&bars.p_full);
     };
@@ -621,22 +620,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t pick = odd ? 0x3276u : 0x5410u;
     const int64_t step = (int64_t)HV * kHeadDim;
     kda_bf16* dst = args.o + ((t0 + 16 * part + odd) * HV + h) * kHeadDim + ((32 * quad + lane) & ~1);
-    // (their products have been waited for, by the next chunk's operand and weights)
+    // (their products have been waited for, by the next chunk's keys and weights)
     auto outputs = [&](int c, const Scalars& sc, uint64_t* free) {
       const int tok = 16 * part, left = L - c * kC - tok - odd;
       tc::tc_fence_after();
       const float up = F16 ? bars.s_scale[c % 3][dv] : 1.f;
       uint32_t y2[8];  // two tokens of one column each
+      uint32_t q[16], r[16];
+      tc::tmem_ld16_async(lanes + kTmQ + 64 * (c & 1) + tok, q);
+      tc::tmem_ld16_async(lanes + kTmO + 64 * (c & 1) + tok, r);
+      wait_ld(q);
+      wait_ld(r);
+      {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t q[8], r[8];
-        tmem_ld8_async(lanes + kTmQ + 64 * (c & 1) + tok + 8 * g, q);
-        tmem_ld8_async(lanes + kTmO + 64 * (c & 1) + tok + 8 * g, r);
-        wait_ld(q);
-        wait_ld(r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t2 = tok + 8 * g + 2 * j;
+        for (int j = 0; j < 8; ++j) {
+          const int t2 = tok + 2 * j;
           float2 f = *reinterpret_cast<const float2*>(sc.out + t2), rest;
           float2 y = mul2(*reinterpret_cast<const float2*>(sc.row + t2),
                           make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
@@ -644,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             f = mul2(f, make_float2(up, up));
             y = mul2(y, *reinterpret_cast<const float2*>(bars.p_scale[c & 1] + t2));
           }
-          y2[4 * g + j] = round2<F16>(fma2(f, make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])), y), rest);
+          y2[j] = round2<F16>(fma2(f, make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1])), y), rest);
         }
       }
       tc::tc_fence_before();
@@ -657,32 +655,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       dst += kC * step;
     };
 
-    prepare(0);
+    auto stage = [&](int c) { return c % kStages; };
+    auto factors = [&](int c) -> Scalars& { return scalars[c % kScalarBufs]; };
+    norms(0, stage(0), factors(0));
+    if (nch > 1) norms(1, stage(1), factors(1));
+    asm volatile("barrier.cta.sync 1, 512;" ::: "memory");
+    keys(0, stage(0), factors(0));
+    done(&bars.wk_full);
     float last = 1.f;
-    int sb = 0;  // the chunk's factors
-    for (int c = 0; c < nch; ++c) {
-      const Scalars& sc = scalars[sb];
-      if (c > 0) update(c - 1, last);
-      last = sc.last;  // its factors were there for prepare(c)
-      if (!LOCAL) operand(c);
-      tc::tc_fence_before();
-      done(&bars.s_full);
-      const int before = sb == 0 ? kScalarBufs - 1 : sb - 1;
-      if (LOCAL) {
-        done(&bars.sc_free[sb]);
-      } else {
-        weights(c, sc);
-        if (c > 0) outputs(c - 1, scalars[before], &bars.sc_free[before]);
+    if (LOCAL) {
+      // K' and dS are there twice: a chunk's product runs while the next one's K' is made
+      for (int c = 0; c < nch; ++c) {
+        if (c > 0) {
+          await(&bars.sq_full, c - 1);
+          update(c - 1, last);
+        }
+        last = factors(c).last;
+        if (c + 2 < nch) norms(c + 2, stage(c + 2), factors(c + 2));
+        if (c + 1 < nch) {
+          await(&bars.wk_full, c);  // all warps are past norms(c + 1)
+          keys(c + 1, stage(c + 1), factors(c + 1));
+        }
+        tc::tc_fence_before();
+        if (c + 1 < nch) done(&bars.wk_full);
+        done(&bars.sc_free[c % kScalarBufs]);
       }
-      if (c + 1 < nch) prepare(c + 1);
-      if (++sb == kScalarBufs) sb = 0;
+    } else {
+      for (int c = 0; c < nch; ++c) {
+        if (c > 0) update(c - 1, last);
+        last = factors(c).last;
+        operand(c);
+        tc::tc_fence_before();
+        done(&bars.s_full);
+        weights(c, factors(c));
+        if (c > 0) outputs(c - 1, factors(c - 1), &bars.sc_free[(c - 1) % kScalarBufs]);
+        if (c + 2 < nch) norms(c + 2, stage(c + 2), factors(c + 2));
+        await(&bars.sq_full, c);  // K' and S^T have been read, dS and O1 are there
+        if (c + 1 < nch) {
+          keys(c + 1, stage(c + 1), factors(c + 1));
+          done(&bars.wk_full);
+        }
+      }
+      await(&bars.o_full, 0);
+      outputs(nch - 1, factors(nch - 1), &bars.sc_free[(nch - 1) % kScalarBufs]);
     }
-    if (!LOCAL) {
-      const int b = sb == 0 ? kScalarBufs - 1 : sb - 1;
-      ok = ok && warp_wait(&bars.qs_full, nch - 1);
-      ok = ok && warp_wait(&bars.o_full, nch - 1);
-      outputs(nch - 1, scalars[b], &bars.sc_free[b]);
-    }
+    if (LOCAL) await(&bars.sq_full, nch - 1);
     if (LOCAL || last_segment) {
       update(nch - 1, last);
       if (LOCAL) {
@@ -698,76 +715,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kRowWarp) {
     // ------------------------------------------------------------------------ rows
+    constexpr int kStage = LOCAL ? kLocalStage : kStageBytes;
     const bool leader = elect_one();
     int issued = 0;
     for (int c = 0; c < nch; ++c) {
       const int st = c % kStages;
       if (c >= kStages && !(ok = warp_wait(&bars.empty[st], c / kStages - 1))) break;
-      uint8_t* rows = smem + st * kStageBytes;
+      uint8_t* rows = smem + st * kStage;
       if (leader) {
-        tc::mbar_expect_tx(&bars.full[st], LOCAL ? 2 * kTile : kStageBytes);
+        uint64_t* bar = &bars.in_full[c % kScalarBufs];
+        tc::mbar_expect_tx(bar, kStage);
         const int tok = (int)t0 + c * kC;
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          tma_box(rows + kTile + a * 8192, &maps.k, a * 64, h / args.G, tok, &bars.full[st]);
-          if (!LOCAL) tma_box(rows + a * 8192, &maps.q, a * 64, h / args.G, tok, &bars.full[st]);
-          tma_box(rows + 2 * kTile + a * 8192, &maps.v, a * 64, h, tok, &bars.full[st]);
+          if (!LOCAL) tma_box(rows + a * 8192, &maps.q, a * 64, h / args.G, tok, bar);
+          tma_box(rows + kStage - 2 * kTile + a * 8192, &maps.k, a * 64, h / args.G, tok, bar);
+          tma_box(rows + kStage - kTile + a * 8192, &maps.v, a * 64, h, tok, bar);
         }
       }
       __syncwarp();
       issued = c + 1;
     }
     // nothing may land after the CTA is gone
-    for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c) warp_wait(&bars.full[c % kStages], c / kStages);
+    for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
+      warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs);
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------------- products
     constexpr uint32_t kType = F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
     constexpr uint32_t kIdU = (F16 ? tc::idesc_f16_f32(128, 128) : tc::idesc_bf16_f32(128, 128)) | tc::kIdescMnA | tc::kIdescMnB;
     constexpr uint32_t kIdP = F16 ? tc::idesc_f16_f32(64, 64) : tc::idesc_bf16_f32(64, 64);
     const bool leader = elect_one();
-    const uint64_t wk_op = tc::sw128_desc_mn(tc::smem_u32(smem + kWk), 8192), p_op = tc::sw128_desc(tc::smem_u32(smem + kP));
-    for (int c = 0; c < nch; ++c) {
-      const int st = c % kStages;
-      const uint32_t rows = tc::smem_u32(smem + st * kStageBytes), turn = 64 * (c & 1);
-      const uint64_t q_op = tc::sw128_desc(rows), k_op = tc::sw128_desc(rows + kTile);
-      const uint64_t v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
-      // K' is the last of what a chunk needs before its state; the outputs of c - 2,
-      // whose place Q K^T takes, were read before
-      if (!(ok = warp_wait(&bars.full[st], c / kStages) && warp_wait(&bars.wk_full, c))) break;
-      tc::tc_fence_after();
-      if (!LOCAL && leader) {  // Q K^T
+    if (LOCAL) {
+      for (int c = 0; c < nch; ++c) {
+        const uint64_t v_op = tc::sw128_desc_mn(tc::smem_u32(smem + c % kStages * kLocalStage) + kTile, 8192);
+        const uint64_t wk_op = tc::sw128_desc_mn(tc::smem_u32(smem + kStages * kLocalStage) + (c & 1) * kLocalWk, 8192);
+        // K' of chunk c, behind the state's update by dS of c - 2
+        if (!(ok = warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.wk_full, c))) break;
+        tc::fence_async_smem();
+        tc::tc_fence_after();
+        if (leader) {  // dS^T = V^T K'
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint64_t off = ((j >> 2) * 8192 + (j & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + kTmO + turn, q_op + off, k_op + off, kIdP, j > 0);
+          for (int b = 0; b < (F16 ? 2 : 3); ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc::mma_bf16(tmem + kTmU + 128 * (c & 1), v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU,
+                           b + j > 0);
+          tc::mma_commit(&bars.sq_full);
+          tc::mma_commit(&bars.empty[c % kStages]);
         }
-        tc::mma_commit(&bars.qk_full);
+        __syncwarp();
       }
-      __syncwarp();
-      if (!(ok = warp_wait(&bars.s_full, c))) break;
-      tc::tc_fence_after();
-      if (leader) {
+    } else {
+      const uint64_t wk_op = tc::sw128_desc_mn(tc::smem_u32(smem + kWk), 8192), p_op = tc::sw128_desc(tc::smem_u32(smem + kP));
+      for (int c = 0; c < nch; ++c) {
+        const int st = c % kStages;
+        const uint32_t rows = tc::smem_u32(smem + st * kStageBytes), turn = 64 * (c & 1);
+        const uint64_t q_op = tc::sw128_desc(rows), k_op = tc::sw128_desc(rows + kTile);
+        const uint64_t v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
+        // K' is the last of what a chunk needs before its state; the outputs of c - 2,
+        // whose place Q K^T takes, were read before
+        if (!(ok = warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.wk_full, c))) break;
+        tc::fence_async_smem();
+        tc::tc_fence_after();
+        if (leader) {  // Q K^T
 #pragma unroll
-        for (int b = 0; b < (F16 ? 2 : 3); ++b)  // dS^T = V^T K'
+          for (int j = 0; j < 8; ++j) {
+            const uint64_t off = ((j >> 2) * 8192 + (j & 3) * 32) >> 4;
+            tc::mma_bf16(tmem + kTmO + turn, q_op + off, k_op + off, kIdP, j > 0);
+          }
+          tc::mma_commit(&bars.qk_full);
+        }
+        __syncwarp();
+        if (!(ok = warp_wait(&bars.s_full, c))) break;
+        tc::tc_fence_after();
+        if (leader) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmU, v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU, b + j > 0);
-        tc::mma_commit(&bars.ds_full);
-        if (LOCAL) {
-          tc::mma_commit(&bars.empty[st]);
-        } else {
+          for (int b = 0; b < (F16 ? 2 : 3); ++b)  // dS^T = V^T K'
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc::mma_bf16(tmem + kTmU, v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU, b + j > 0);
 #pragma unroll
           for (int b = 0; b < 2; ++b)  // O1^T = S^T Q^T
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               mma_ts(tmem + kTmQ + turn, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
                      b + j > 0);
-          tc::mma_commit(&bars.qs_full);
+          tc::mma_commit(&bars.sq_full);
         }
-      }
-      __syncwarp();
-      if (!LOCAL) {
+        __syncwarp();
         if (!(ok = warp_wait(&bars.p_full, c))) break;
+        tc::fence_async_smem();
         tc::tc_fence_after();
         if (leader) {  // O2^T = V^T P^T
 #pragma unroll
@@ -776,8 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j)
               tc::mma_bf16(tmem + kTmO + turn, v_op + ((j * 2048) >> 4), p_op + ((b * 8192 + j * 32) >> 4), kType | tc::kIdescMnA,
                            b + j > 0);
-          tc::mma_commit(&bars.o_full);
           tc::mma_commit(&bars.empty[st]);
+          if (c == nch - 1) tc::mma_commit(&bars.o_full);
         }
         __syncwarp();
       }
@@ -812,16 +849,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c >= kScalarBufs && !(ok = warp_wait(&bars.sc_free[sb], c / kScalarBufs - 1))) break;
       auto put2 = [&](float* to, float a, float b) { *reinterpret_cast<float2*>(to + 2 * lane) = make_float2(a, b); };
       const float2 c_last = pair_from(run, 31);
-      put2(sc.w, 2 * lane < left ? exp_diff(c_last, even) : 0.f, 2 * lane + 1 < left ? exp_diff(c_last, run) : 0.f);
+      put2(sc.w, 2 * lane < left ? k_up * exp_diff(c_last, even) : 0.f, 2 * lane + 1 < left ? k_up * exp_diff(c_last, run) : 0.f);
       if (lane == 31) sc.last = expf(run.x + run.y);
       if (!LOCAL) {
         put2(sc.c_hi, even.x, run.x);
         put2(sc.c_lo, even.y, run.y);
-        put2(sc.out, expf(even.x + even.y), expf(run.x + run.y));
+        put2(sc.out, ga.scale * expf(even.x + even.y), ga.scale * expf(run.x + run.y));
+        put2(sc.k, 1.f, 1.f);
         const float2 c_b = pair_from(even, lane & 24), end = pair_from(run, lane | 7);
         const bool far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
         const float e0 = far ? 1.f : exp_diff(even, c_b), e1 = far ? 1.f : exp_diff(run, c_b);
-        put2(sc.row, e0, e1);
+        put2(sc.row, ga.scale * e0, ga.scale * e1);
         if (F16) put2(sc.big, 1.f / e0, 1.f / e1);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -831,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) arrive(&bars.gate_full[sb]);
+      if (lane == 0) arrive(&bars.in_full[sb]);
     }
   }
   // All products have been waited for but those whose results nobody needs; where a
