@@ -56,7 +56,9 @@ struct LinPrefillArgs {
   int num_seqs;
   int64_t total_tokens;
   kda_bf16* o;
-  int64_t seg_tokens;   // tokens of a segment, a multiple of 64
+  // tokens of a segment, multiples of 64: where no sequence is longer than even_most,
+  // and otherwise
+  int seg_even, seg_ragged, even_most;
   float4* local_state;  // [segment, value head][8][512 threads]: what a segment adds
   float* local_decay;   // [segment, value head]: e^(its log-decays' sum)
   int32_t* err_flag;
@@ -78,6 +80,7 @@ struct Scalars {
   float k[kC];               // rk_j
   float big[kC], kk[kC];     // FP16: |q_i| e^(c_b - c_i), far |q_i|; |k_j|^2
   float last;                // e^(c_last)
+  int far[4];                // of the four blocks
   float pad[3];
 };
 constexpr float kFar = 60.f;
@@ -89,8 +92,10 @@ struct Bars {
   uint64_t in_full[kScalarBufs];     // rows landed, and factors of the decays
   uint64_t empty[kStages];           // rows consumed
   uint64_t sc_free[kScalarBufs];     // factors read
-  uint64_t wk_full, s_full, p_full;  // operands: K' (and what else a chunk needs), S^T, P
-  uint64_t qk_full, sq_full;         // products: Q K^T (and the last O2), dS and O1
+  uint64_t wk_full[2];               // operands: K' (and what else a chunk needs), chunks in turn,
+  uint64_t s_full, p_full;           // S^T, P
+  uint64_t sq_full[2];               // products: dS and O1, chunks in turn,
+  uint64_t qk_full;                  // Q K^T (and the last O2)
   uint64_t o_full;                   // the segment's last O2
   uint64_t drained;                  // all products
   uint32_t tmem;
@@ -124,8 +129,25 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity & 1u));
+// A wait of two seconds at most; false: it ran out.
+//
+// A barrier's phase is known by its parity alone, so that a waiter must not fall two
+// phases behind: the next phase but one of each barrier here needs an arrival that
+// comes after every waiter's wait for this one.  Where products run ahead of their
+// waiters (the first launch's), there is a barrier for either parity of the chunk.
+__device__ __noinline__ bool long_wait(uint64_t* bar, uint32_t parity) {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+  do {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  } while (t - t0 < 2000000000ull);
+  return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) {
+  const uint32_t parity = phase & 1u;
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, long_wait(bar, parity));
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -236,45 +258,48 @@ __device__ __forceinline__ int seq_len(const LinPrefillArgs& a, int n) {
                    (n == a.num_seqs - 1 && t1 != a.total_tokens);
   return bad ? -1 : (int)(t1 - t0);
 }
-__device__ __forceinline__ int seq_segments(const LinPrefillArgs& a, int n) {
-  const int len = seq_len(a, n);
-  return len > 0 ? (int)((len + a.seg_tokens - 1) / a.seg_tokens) : 0;
-}
-
-// The sequence n of segment `id`, and which of its segments it is; n = -1: none.
-// Every warp walks over the sequences, 128 at a time.
+// A CTA's segment: sequence n (-1: none), its s-th of `count`; `record` is the place of
+// the sequence's first segment among all.
 struct Segment {
-  int n, s;
+  int n, s, count, record, tokens;
 };
+
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+
+// The id-th segment: whole ones of all sequences first, then what is left of each, so
+// that the longest start first.  Every warp walks over the sequences for itself.
 __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int id, int lane) {
-  Segment r{-1, 0};
-  for (int n0 = 0, base = 0; n0 < args.num_seqs && r.n < 0; n0 += 128) {
-    int cnt[4], sum = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int m = n0 + 4 * lane + e;
-      cnt[e] = m < args.num_seqs ? seq_segments(args, m) : 0;
-      sum += cnt[e];
-    }
-    int run = sum;
+  const int seqs = args.num_seqs;
+  int most = 0;
+  for (int m = lane; m < seqs; m += 32) most = max(most, seq_len(args, m));
+  most = __reduce_max_sync(0xffffffffu, most);
+  const int L = most <= args.even_most ? args.seg_even : args.seg_ragged;
+  int whole = 0;  // whole segments of all sequences
+  for (int m = lane; m < seqs; m += 32) whole += max(seq_len(args, m), 0) / L;
+  whole = warp_sum(whole);
+  const bool rest = id >= whole;
+  const int want = rest ? id - whole : id;
+  Segment r{-1, 0, 0, 0, L};
+  for (int n0 = 0, base = 0, records = 0; n0 < seqs && r.n < 0; n0 += 32) {
+    const int m = n0 + lane, len = m < seqs ? max(seq_len(args, m), 0) : 0;
+    const int mine = rest ? len % L != 0 : len / L, all = (len + L - 1) / L;
+    int run = mine, run_all = all;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, run, d);
-      if (lane >= d) run += up;
+      const int up = __shfl_up_sync(0xffffffffu, run, d), up_all = __shfl_up_sync(0xffffffffu, run_all, d);
+      if (lane >= d) run += up, run_all += up_all;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, base + run > id);
+    const unsigned past = __ballot_sync(0xffffffffu, base + run > want);
     if (past) {
-      int at = base + run - sum, mine = -1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (mine < 0 && id < at + cnt[e]) mine = e;
-        if (mine < 0) at += cnt[e];
-      }
       const int src = __ffs(past) - 1;
-      r.n = n0 + 4 * src + __shfl_sync(0xffffffffu, mine, src);
-      r.s = id - __shfl_sync(0xffffffffu, at, src);
+      r.n = n0 + src;
+      const int before = __shfl_sync(0xffffffffu, base + run - mine, src);
+      r.count = __shfl_sync(0xffffffffu, all, src);
+      r.s = rest ? r.count - 1 : want - before;
+      r.record = records + __shfl_sync(0xffffffffu, run_all - all, src);
     }
     base += __shfl_sync(0xffffffffu, run, 31);
+    records += __shfl_sync(0xffffffffu, run_all, 31);
   }
   return r;
 }
@@ -313,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int len = seq_len(args, seg.n);
-  const int64_t first = (int64_t)seg.s * args.seg_tokens;
-  const bool last_segment = first + args.seg_tokens >= len;
-  const int L = (int)(last_segment ? len - first : args.seg_tokens), nch = (L + kC - 1) / kC;
+  const int first = seg.s * seg.tokens;
+  const bool last_segment = seg.s == seg.count - 1;
+  const int L = last_segment ? len - first : seg.tokens, nch = (L + kC - 1) / kC;
   const int64_t t0 = seq_start(args, seg.n) + first;
   const int slot = args.state_idx[seg.n];
   const bool no_slot = slot < 0 || slot >= args.pool_slots;
@@ -340,11 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars.in_full[i], 2);
       tc::mbar_init(&bars.sc_free[i], kWorkers);
     }
-    tc::mbar_init(&bars.wk_full, kWorkers);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bars.wk_full[i], kWorkers);
+      tc::mbar_init(&bars.sq_full[i], 1);
+    }
     tc::mbar_init(&bars.s_full, kWorkers);
     tc::mbar_init(&bars.p_full, kWorkers);
     tc::mbar_init(&bars.qk_full, 1);
-    tc::mbar_init(&bars.sq_full, 1);
     tc::mbar_init(&bars.o_full, 1);
     tc::mbar_init(&bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -368,9 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && ok) arrive(bar);
     };
 
-    auto await = [&](uint64_t* bar, uint32_t phase) {
-      if (ok && !__all_sync(0xffffffffu, tc::mbar_try_wait(bar, phase & 1u))) ok = warp_wait(bar, phase);
-    };
+    auto await = [&](uint64_t* bar, uint32_t phase) { ok = ok && warp_wait(bar, phase); };
     constexpr int kStage = LOCAL ? kLocalStage : kStageBytes, kK = LOCAL ? 0 : kTile;
 
     // --------------------------------------------------------------------- norms
@@ -453,13 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* root = args.pool + (((size_t)slot * HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
     float S[32];
     auto record = [&](int64_t segment) { return args.local_state + (segment * HV + h) * 4096 + tid; };
-    const int segments = seq_segments(args, seg.n);
+    auto start = [&]() {
     if (!LOCAL) grid_dependency_wait();
     if (seg.s == 0) {
       // The CTA of the last segment writes the sequence's slot, maybe before this one
       // reads it: the first launch leaves a copy where the last segment has no record.
-      const bool copied = !LOCAL && segments > 1;
-      const float4* copy = record(id + segments - 1);
+      const bool copied = !LOCAL && seg.count > 1;
+      const float4* copy = record(seg.record + seg.count - 1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float4 x = copied ? __ldcg(copy + j * 512) : *reinterpret_cast<const float4*>(root + 4 * j);
@@ -471,9 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 32; ++j) S[j] = 0.f;
     }
     if (!LOCAL && seg.s > 0) {
-      float up = 1.f;  // decay from the end of a segment before to the start of this one
+      // `up`: decay from the end of a segment before to the start of this one
+      const float* d = args.local_decay + (int64_t)seg.record * HV + h;
+      float up = 1.f, next = __ldcg(d + (int64_t)(seg.s - 1) * HV);
       for (int m = seg.s - 1; m >= 0 && up > 0.f; --m) {
-        const float4* src = record(id - seg.s + m);
+        const float4* src = record(seg.record + m);
+        const float here = next;
+        if (m > 0) next = __ldcg(d + (int64_t)(m - 1) * HV);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 x = __ldcg(src + j * 512);
@@ -482,9 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           S[4 * j + 2] = fmaf(up, x.z, S[4 * j + 2]);
           S[4 * j + 3] = fmaf(up, x.w, S[4 * j + 3]);
         }
-        up *= __ldcg(args.local_decay + (int64_t)(id - seg.s + m) * HV + h);
+        up *= here;
       }
     }
+    };
     float decay = 1.f;
     const float k_down = 1.f / k_up;
     auto update = [&](int c, float last) {  // S of the next chunk
@@ -574,8 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t r[2][4];
         ld_frag8(qk, r[0]);
         ld_frag8(qk + 8, r[1]);
-        const int b = 16 * quad;
-        const bool far = !((sc.c_hi[b] - sc.c_hi[b + 15]) + (sc.c_lo[b] - sc.c_lo[b + 15]) <= kFar);
+        const bool far = sc.far[quad] != 0;
         wait_ld(r[0]);
         wait_ld(r[1]);
 #pragma unroll
@@ -648,9 +677,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tc_fence_before();
       done(free);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // traded for two columns of one token each
-        const uint32_t x = __byte_perm(y2[j], __shfl_xor_sync(0xffffffffu, y2[j], 1), pick);
-        if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = x;
+      for (int j = 0; j < 8; ++j)  // traded for two columns of one token each
+        y2[j] = __byte_perm(y2[j], __shfl_xor_sync(0xffffffffu, y2[j], 1), pick);
+      if (c < nch - 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = y2[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (2 * j < left) *reinterpret_cast<uint32_t*>(dst + 2 * j * step) = y2[j];
       }
       dst += kC * step;
     };
@@ -661,23 +696,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nch > 1) norms(1, stage(1), factors(1));
     asm volatile("barrier.cta.sync 1, 512;" ::: "memory");
     keys(0, stage(0), factors(0));
-    done(&bars.wk_full);
+    done(&bars.wk_full[0]);
+    start();  // (the first launch may still be running)
     float last = 1.f;
     if (LOCAL) {
       // K' and dS are there twice: a chunk's product runs while the next one's K' is made
       for (int c = 0; c < nch; ++c) {
         if (c > 0) {
-          await(&bars.sq_full, c - 1);
+          await(&bars.sq_full[(c - 1) & 1], (c - 1) >> 1);
           update(c - 1, last);
         }
         last = factors(c).last;
         if (c + 2 < nch) norms(c + 2, stage(c + 2), factors(c + 2));
         if (c + 1 < nch) {
-          await(&bars.wk_full, c);  // all warps are past norms(c + 1)
+          await(&bars.wk_full[c & 1], c >> 1);  // all warps are past norms(c + 1)
           keys(c + 1, stage(c + 1), factors(c + 1));
         }
         tc::tc_fence_before();
-        if (c + 1 < nch) done(&bars.wk_full);
+        if (c + 1 < nch) done(&bars.wk_full[(c + 1) & 1]);
         done(&bars.sc_free[c % kScalarBufs]);
       }
     } else {
@@ -690,23 +726,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         weights(c, factors(c));
         if (c > 0) outputs(c - 1, factors(c - 1), &bars.sc_free[(c - 1) % kScalarBufs]);
         if (c + 2 < nch) norms(c + 2, stage(c + 2), factors(c + 2));
-        await(&bars.sq_full, c);  // K' and S^T have been read, dS and O1 are there
+        await(&bars.sq_full[c & 1], c >> 1);  // K' and S^T have been read, dS and O1 are there
         if (c + 1 < nch) {
           keys(c + 1, stage(c + 1), factors(c + 1));
-          done(&bars.wk_full);
+          done(&bars.wk_full[(c + 1) & 1]);
         }
       }
       await(&bars.o_full, 0);
       outputs(nch - 1, factors(nch - 1), &bars.sc_free[(nch - 1) % kScalarBufs]);
     }
-    if (LOCAL) await(&bars.sq_full, nch - 1);
+    if (LOCAL) await(&bars.sq_full[(nch - 1) & 1], (nch - 1) >> 1);
     if (LOCAL || last_segment) {
       update(nch - 1, last);
       if (LOCAL) {
-        float4* to = record(id);
+        float4* to = record(seg.record + seg.s);
 #pragma unroll
         for (int j = 0; j < 8; ++j) to[j * 512] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-        if (tid == 0) args.local_decay[(int64_t)id * HV + h] = decay;
+        if (tid == 0) args.local_decay[(int64_t)(seg.record + seg.s) * HV + h] = decay;
       } else if (ok) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -750,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t v_op = tc::sw128_desc_mn(tc::smem_u32(smem + c % kStages * kLocalStage) + kTile, 8192);
         const uint64_t wk_op = tc::sw128_desc_mn(tc::smem_u32(smem + kStages * kLocalStage) + (c & 1) * kLocalWk, 8192);
         // K' of chunk c, behind the state's update by dS of c - 2
-        if (!(ok = warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.wk_full, c))) break;
+        if (!(ok = warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.wk_full[c & 1], c >> 1))) break;
         tc::fence_async_smem();
         tc::tc_fence_after();
         if (leader) {  // dS^T = V^T K'
@@ -760,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j)
               tc::mma_bf16(tmem + kTmU + 128 * (c & 1), v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU,
                            b + j > 0);
-          tc::mma_commit(&bars.sq_full);
+          tc::mma_commit(&bars.sq_full[c & 1]);
           tc::mma_commit(&bars.empty[c % kStages]);
         }
         __syncwarp();
@@ -774,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t v_op = tc::sw128_desc_mn(rows + 2 * kTile, 8192);
         // K' is the last of what a chunk needs before its state; the outputs of c - 2,
         // whose place Q K^T takes, were read before
-        if (!(ok = warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.wk_full, c))) break;
+        if (!(ok = warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs) && warp_wait(&bars.wk_full[c & 1], c >> 1))) break;
         tc::fence_async_smem();
         tc::tc_fence_after();
         if (leader) {  // Q K^T
@@ -800,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j)
               mma_ts(tmem + kTmQ + turn, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
                      b + j > 0);
-          tc::mma_commit(&bars.sq_full);
+          tc::mma_commit(&bars.sq_full[c & 1]);
         }
         __syncwarp();
         if (!(ok = warp_wait(&bars.p_full, c))) break;
@@ -858,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put2(sc.k, 1.f, 1.f);
         const float2 c_b = pair_from(even, lane & 24), end = pair_from(run, lane | 7);
         const bool far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
+        if ((lane & 7) == 0) sc.far[lane >> 3] = far;
         const float e0 = far ? 1.f : exp_diff(even, c_b), e1 = far ? 1.f : exp_diff(run, c_b);
         put2(sc.row, ga.scale * e0, ga.scale * e1);
         if (F16) put2(sc.big, 1.f / e0, 1.f / e1);
@@ -919,17 +956,36 @@ kda_status allow_all() {
   return KDA_OK;
 }
 
-// Tokens of a segment: so many that all segments of all heads fill the SMs about
-// once, 256 at least.
+// Tokens of a segment.  Sequences of one length: the number of segments each that
+// takes least, by what a chunk and a CTA's start cost in thousands of cycles (measured:
+// 4.7 and 6 in the second launch, 2.3 and 5 in the first, which the last segments are
+// spared); with lengths that differ much, segments of half an SM's share.
+struct Segments {
+  int even, ragged, even_most;
+  int64_t most;  // segments of all sequences, at most
+};
+Segments cut(const kda_dims& d, int num_seqs, int64_t total_tokens, int64_t sms) {
+  Segments r{};
+  const int64_t len = (total_tokens + num_seqs - 1) / num_seqs, chunks = (len + kC - 1) / kC, heads = (int64_t)num_seqs * d.HV;
+  double best = 1e300;
+  int64_t even = chunks;
+  for (int64_t n = 1; n <= chunks && n <= 64; ++n) {
+    const int64_t each = (chunks + n - 1) / n, got = (chunks + each - 1) / each;
+    const int64_t waves = (heads * got + sms - 1) / sms, waves1 = (heads * (got - 1) + sms - 1) / sms;
+    const double cost = waves * (4.7 * each + 6) + waves1 * (2.3 * each + 5);
+    if (cost < best) best = cost, even = each;
+  }
+  const int64_t share = (total_tokens * d.HV / (2 * sms) + kC - 1) / kC;
+  r.even = (int)(even * kC);
+  r.ragged = (int)((share < 4 ? 4 : share) * kC);
+  const int64_t even_most = len + len / 4;
+  r.even_most = num_seqs == 1 || even_most > INT32_MAX ? INT32_MAX : (int)even_most;
+  const int64_t least = num_seqs > 1 && r.ragged < r.even ? r.ragged : r.even;
+  r.most = total_tokens / least + num_seqs;
+  return r;
+}
+// The workspace size does not depend on the device: so many SMs as this GPU has.
 constexpr int64_t kSms = 152;
-int64_t segment_tokens(const kda_dims& d, int64_t total_tokens) {
-  const int64_t even = (total_tokens * d.HV + kSms - 1) / kSms;
-  const int64_t L = (even + kC - 1) / kC * kC;
-  return L < 256 ? 256 : L;
-}
-int64_t most_segments(const kda_dims& d, int num_seqs, int64_t total_tokens) {
-  return total_tokens / segment_tokens(d, total_tokens) + num_seqs;
-}
 
 }  // namespace
 }  // namespace kda
@@ -941,8 +997,10 @@ using namespace kda;
 extern "C" size_t kda_lin_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens) {
   if (num_seqs < 0 || total_tokens < 0 || dims.H <= 0 || dims.HV <= 0) return 0;
   if (total_tokens > INT32_MAX) return SIZE_MAX;  // refused; no capacity check may pass
-  if (total_tokens <= segment_tokens(dims, total_tokens)) return 0;
-  return (size_t)most_segments(dims, num_seqs, total_tokens) * dims.HV * (65536 + 16);
+  if (num_seqs == 0 || total_tokens == 0) return 0;
+  const Segments c = cut(dims, num_seqs, total_tokens, kSms);
+  if (total_tokens <= c.even && (num_seqs == 1 || total_tokens <= c.ragged)) return 0;
+  return (size_t)c.most * dims.HV * (65536 + 16);
 }
 
 extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
@@ -975,9 +1033,12 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.num_seqs = num_seqs;
   args.total_tokens = total_tokens;
   args.o = o;
-  args.seg_tokens = segment_tokens(dims, total_tokens);
+  const Segments c = cut(dims, num_seqs, total_tokens, kSms);
+  args.seg_even = c.even;
+  args.seg_ragged = c.ragged;
+  args.even_most = c.even_most;
   args.err_flag = err_flag;
-  const int64_t units = most_segments(dims, num_seqs, total_tokens) * dims.HV;
+  const int64_t units = c.most * dims.HV;
   if (units > INT32_MAX) return KDA_ERR_SHAPE;
   args.local_state = static_cast<float4*>(workspace);
   args.local_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need > 0 ? (size_t)units * 65536 : 0));

@@ -1,0 +1,237 @@
+"""The hand-overs of the linear-attention prefill kernel (csrc/lin_prefill.cu) in a
+model of its barriers: workers, row warp, product warp and factor warps as programs
+of waits, arrivals and accesses, run in random orders.  A barrier's phase is known by
+its parity alone, as on the GPU, so that a waiter that falls two phases behind hangs;
+every access is checked for what it may not overlap."""
+import random
+
+import pytest
+
+STAGES, BUFS = 3, 4
+
+
+class Barrier:
+    def __init__(self, count):
+        self.count, self.pending, self.phase = count, count, 0
+
+    def arrive(self):
+        self.pending -= 1
+        assert self.pending >= 0
+        if self.pending == 0:
+            self.pending, self.phase = self.count, self.phase + 1
+
+    def ready(self, phase):  # try_wait.parity: the phase of this parity is over
+        return (self.phase & 1) != (phase & 1)
+
+
+class Cta:
+    """What the programs share: barriers, who holds what, and the order of products."""
+
+    def __init__(self, nch, local, workers=3):
+        self.nch, self.local, self.workers = nch, local, workers
+        self.bar = {("in", i): Barrier(2 if i >= 0 else 1) for i in range(BUFS)}
+        self.bar |= {("empty", i): Barrier(1) for i in range(STAGES)}
+        self.bar |= {("free", i): Barrier(workers) for i in range(BUFS)}
+        self.bar |= {("wk", i): Barrier(workers) for i in range(2)}
+        self.bar |= {("sq", i): Barrier(1) for i in range(2)}
+        self.bar |= {("s", 0): Barrier(workers), ("p", 0): Barrier(workers), ("qk", 0): Barrier(1), ("o", 0): Barrier(1)}
+        self.queue = []  # products and commits in issue order
+        self.holds = {}  # resource -> chunk whose data it holds
+        self.reading = {}  # resource -> products under way that read or write it
+
+    def put(self, what, chunk):
+        """Data of `chunk` goes into a place that no product under way uses."""
+        assert not self.reading.get(what), f"{what} overwritten for chunk {chunk} under a product"
+        self.holds[what] = chunk
+
+    def use(self, what, chunk):
+        assert self.holds.get(what) == chunk, f"{what} holds {self.holds.get(what)}, wanted {chunk}"
+
+    def product(self, reads, writes, chunk):
+        for r in reads:
+            self.use(r, chunk)
+        for x in list(reads) + list(writes):
+            self.reading[x] = self.reading.get(x, 0) + 1
+        self.queue.append(("product", list(reads) + list(writes), list(writes), chunk))
+
+    def commit(self, bar):
+        self.queue.append(("commit", bar))
+
+    def step_queue(self):
+        kind, *x = self.queue.pop(0)
+        if kind == "commit":
+            self.bar[x[0]].arrive()
+        else:
+            for r in x[0]:
+                self.reading[r] -= 1
+            for w in x[1]:
+                self.holds[w] = x[2]
+
+
+def rows(t):
+    for c in range(t.nch):
+        if c >= STAGES:
+            yield ("empty", c % STAGES), c // STAGES - 1
+        for what in ("K", "V", "Q"):
+            t.put((what, c % STAGES), c)
+        yield
+        t.bar["in", c % BUFS].arrive()
+        yield
+
+
+def factors(t, which):
+    for c in range(which, t.nch, 2):
+        if c >= BUFS:
+            yield ("free", c % BUFS), c // BUFS - 1
+        t.holds["factors", c % BUFS] = c
+        yield
+        t.bar["in", c % BUFS].arrive()
+        yield
+
+
+def worker(t, w):
+    """Worker w: its share of every place is a place of its own; a product needs all."""
+    n, W = t.nch, range(t.workers)
+
+    def norms(c):
+        yield ("in", c % BUFS), c // BUFS
+        t.use(("K", c % STAGES), c)
+        t.use(("factors", c % BUFS), c)
+        t.holds["norms", c % BUFS, w] = c
+
+    def keys(c):
+        for x in W:
+            t.use(("norms", c % BUFS, x), c)
+        t.use(("K", c % STAGES), c)
+        t.put(("wk", c & 1 if t.local else 0, w), c)
+
+    def update(c):
+        t.use(("dS", c & 1 if t.local else 0), c)
+
+    def outputs(c):
+        t.use(("O1", c & 1), c)
+        t.use(("O2", c & 1), c)
+        t.use(("factors", c % BUFS), c)
+        yield
+        t.bar["free", c % BUFS].arrive()
+
+    yield from norms(0)
+    if n > 1:
+        yield from norms(1)
+    yield "meet"
+    keys(0)
+    yield
+    t.bar["wk", 0].arrive()
+    for c in range(n):
+        if t.local:
+            if c > 0:
+                yield ("sq", (c - 1) & 1), (c - 1) >> 1
+                update(c - 1)
+                yield
+            t.use(("factors", c % BUFS), c)
+            if c + 2 < n:
+                yield from norms(c + 2)
+            if c + 1 < n:
+                yield ("wk", c & 1), c >> 1
+                keys(c + 1)
+                yield
+                t.bar["wk", (c + 1) & 1].arrive()
+            yield
+            t.bar["free", c % BUFS].arrive()
+            yield
+        else:
+            if c > 0:
+                update(c - 1)
+            t.use(("factors", c % BUFS), c)
+            yield
+            t.put(("S", w), c)
+            yield
+            t.bar["s", 0].arrive()
+            yield ("qk", 0), c
+            t.use(("QK", c & 1), c)
+            for x in W:
+                t.use(("norms", c % BUFS, x), c)
+            yield
+            t.put(("P", w), c)
+            yield
+            t.bar["p", 0].arrive()
+            yield
+            if c > 0:
+                yield from outputs(c - 1)
+            if c + 2 < n:
+                yield from norms(c + 2)
+            yield ("sq", c & 1), c >> 1
+            if c + 1 < n:
+                keys(c + 1)
+                yield
+                t.bar["wk", (c + 1) & 1].arrive()
+            yield
+    if t.local:
+        yield ("sq", (n - 1) & 1), (n - 1) >> 1
+    else:
+        yield ("o", 0), 0
+        yield from outputs(n - 1)
+    update(n - 1)
+
+
+def products(t):
+    W = range(t.workers)
+    for c in range(t.nch):
+        st = c % STAGES
+        yield ("in", c % BUFS), c // BUFS
+        yield ("wk", c & 1), c >> 1
+        wk = c & 1 if t.local else 0
+        if t.local:
+            t.product([("V", st)] + [("wk", wk, x) for x in W], [("dS", wk)], c)
+            t.commit(("sq", c & 1))
+            t.commit(("empty", st))
+            yield
+            continue
+        t.product([("Q", st), ("K", st)], [("QK", c & 1)], c)
+        t.commit(("qk", 0))
+        yield ("s", 0), c
+        t.product([("V", st)] + [("wk", 0, x) for x in W], [("dS", 0)], c)
+        t.product([("Q", st)] + [("S", x) for x in W], [("O1", c & 1)], c)
+        t.commit(("sq", c & 1))
+        yield ("p", 0), c
+        t.product([("V", st)] + [("P", x) for x in W], [("O2", c & 1)], c)
+        t.commit(("empty", st))
+        if c == t.nch - 1:
+            t.commit(("o", 0))
+        yield
+
+
+def run(nch, local, seed):
+    rng = random.Random(seed)
+    t = Cta(nch, local)
+    progs = [rows(t), products(t), factors(t, 0), factors(t, 1)] + [worker(t, w) for w in range(t.workers)]
+    speed = [rng.choice([0.02, 0.3, 1, 1]) for _ in progs] + [rng.choice([0.02, 0.3, 1])]  # the last: the tensor core
+    wait, met = [None] * len(progs), 0
+    alive = set(range(len(progs)))
+    idle = 0
+    while alive or t.queue:
+        able = [i for i in alive if wait[i] is None or (wait[i] != "meet" and t.bar[wait[i][0]].ready(wait[i][1]))]
+        if [wait[i] for i in range(4, len(progs))] == ["meet"] * t.workers:
+            for i in range(4, len(progs)):
+                wait[i] = None
+            continue
+        if t.queue:
+            able.append(len(progs))
+        assert able, f"{nch} chunks, local {local}, seed {seed}: nothing can go on, waits {wait}"
+        i = rng.choices(able, [speed[k] for k in able])[0]
+        if i == len(progs):
+            t.step_queue()
+            continue
+        wait[i] = None
+        try:
+            wait[i] = next(progs[i])
+        except StopIteration:
+            alive.discard(i)
+            wait[i] = None
+
+
+@pytest.mark.parametrize("local", [False, True])
+@pytest.mark.parametrize("nch", [1, 2, 3, 4, 5, 9, 20])
+def test_every_order_ends_and_overwrites_nothing(nch, local):
+    for seed in range(150):
+        run(nch, local, seed)
