@@ -20,7 +20,7 @@
 //                    (FP16: two)
 // 16 warps do all the arithmetic, together and a step of it at a time, since what they
 // execute then is in the SM's instruction caches: per chunk the state's update and its
-// operand, P, the outputs of the chunk before, and norms and K' of the chunk behind.
+// operand, P, the outputs of the chunk before, and K' of the chunk behind.
 // (Warps of a task each ran at 6 to 8 cycles an instruction, waiting for it: 5000
 // cycles a chunk.)  The products run meanwhile: each has a step or more of other work
 // before it is needed.  One warp loads rows, one issues products, two make the factors
@@ -68,8 +68,7 @@ struct LinMaps {
   CUtensorMap q, k, v;
 };
 
-// Factors of a chunk: of the decays first, then times those of the norms.
-// b is the first token of i's block of 16; where a block decays by more than e^60 the
+// Factors of a chunk: of the decays first, then times those of the norms.  b is the first token of i's block of 16; where a block decays by more than e^60 the
 // block's rows of P get their factors term by term (far).
 struct Scalars {
   float c_hi[kC], c_lo[kC];  // c_i
@@ -86,11 +85,13 @@ struct Scalars {
 constexpr float kFar = 60.f;
 
 // Warps.
-constexpr int kWorkers = 16, kRowWarp = 16, kMmaWarp = 17, kGateWarp = 18, kThreads = 640;
+constexpr int kWorkers = 16, kRowWarp = 16, kMmaWarp = 17, kGateWarp = 18, kNormWarp = 20, kNormWarps = 4, kThreads = 768;
 
 struct Bars {
-  uint64_t in_full[kScalarBufs];     // rows landed, and factors of the decays
-  uint64_t empty[kStages];           // rows consumed
+  uint64_t full[kStages];            // rows landed
+  uint64_t empty[kStages];           // and consumed
+  uint64_t gate_full[kScalarBufs];   // factors of the decays
+  uint64_t in_full[kScalarBufs];     // rows and all factors
   uint64_t sc_free[kScalarBufs];     // factors read
   uint64_t wk_full[2];               // operands: K' (and what else a chunk needs), chunks in turn,
   uint64_t s_full, p_full;           // S^T, P
@@ -258,49 +259,61 @@ __device__ __forceinline__ int seq_len(const LinPrefillArgs& a, int n) {
                    (n == a.num_seqs - 1 && t1 != a.total_tokens);
   return bad ? -1 : (int)(t1 - t0);
 }
-// A CTA's segment: sequence n (-1: none), its s-th of `count`; `record` is the place of
-// the sequence's first segment among all.
+// A CTA's segment: the s-th of `count` of sequence n (-1: none), `tokens` long but for
+// the last; `record` is the place of the sequence's first segment among all.
 struct Segment {
   int n, s, count, record, tokens;
+  int len;     // of the sequence
+  int64_t t0;  // its first token
 };
 
-__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
-
 // The id-th segment: whole ones of all sequences first, then what is left of each, so
-// that the longest start first.  Every warp walks over the sequences for itself.
+// that the longest start first.  Every warp finds it for itself, a sequence a lane.
+// (What runs once a CTA is kept short: instructions that no cache holds yet take five
+// or more times as long as others.)
 __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int id, int lane) {
   const int seqs = args.num_seqs;
-  int most = 0;
-  for (int m = lane; m < seqs; m += 32) most = max(most, seq_len(args, m));
-  most = __reduce_max_sync(0xffffffffu, most);
-  const int L = most <= args.even_most ? args.seg_even : args.seg_ragged;
-  int whole = 0;  // whole segments of all sequences
-  for (int m = lane; m < seqs; m += 32) whole += max(seq_len(args, m), 0) / L;
-  whole = warp_sum(whole);
-  const bool rest = id >= whole;
-  const int want = rest ? id - whole : id;
-  Segment r{-1, 0, 0, 0, L};
-  for (int n0 = 0, base = 0, records = 0; n0 < seqs && r.n < 0; n0 += 32) {
-    const int m = n0 + lane, len = m < seqs ? max(seq_len(args, m), 0) : 0;
-    const int mine = rest ? len % L != 0 : len / L, all = (len + L - 1) / L;
-    int run = mine, run_all = all;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, run, d), up_all = __shfl_up_sync(0xffffffffu, run_all, d);
-      if (lane >= d) run += up, run_all += up_all;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, base + run > want);
-    if (past) {
-      const int src = __ffs(past) - 1;
-      r.n = n0 + src;
-      const int before = __shfl_sync(0xffffffffu, base + run - mine, src);
-      r.count = __shfl_sync(0xffffffffu, all, src);
-      r.s = rest ? r.count - 1 : want - before;
-      r.record = records + __shfl_sync(0xffffffffu, run_all - all, src);
-    }
-    base += __shfl_sync(0xffffffffu, run, 31);
-    records += __shfl_sync(0xffffffffu, run_all, 31);
+  Segment r{-1, 0, 0, 0, args.seg_even, 0, 0};
+  int L = args.seg_even;
+  if (seqs == 1) {
+    const int len = seq_len(args, 0), count = len > 0 ? (len + L - 1) / L : 0;
+    if (id < count) r = Segment{0, id, count, 0, L, len, 0};
+    return r;
   }
+  int most = 0;
+#pragma unroll 1
+  for (int m = lane; m < seqs; m += 32) most = max(most, seq_len(args, m));
+  if (__reduce_max_sync(0xffffffffu, most) > args.even_most) L = args.seg_ragged;
+  // the first turn goes through whole segments, the second through what is left
+  int base = 0;
+#pragma unroll 1
+  for (int turn = 0; turn < 2 && r.n < 0; ++turn) {
+    int records = 0;
+#pragma unroll 1
+    for (int n0 = 0; n0 < seqs && r.n < 0; n0 += 32) {
+      const int m = n0 + lane, len = m < seqs ? max(seq_len(args, m), 0) : 0;
+      const int whole = len / L, all = whole + (len != whole * L), mine = turn ? all - whole : whole;
+      int run = mine, run_all = all;
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, run, d), up_all = __shfl_up_sync(0xffffffffu, run_all, d);
+        if (lane >= d) run += up, run_all += up_all;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + run > id);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        r.n = n0 + src;
+        r.len = __shfl_sync(0xffffffffu, len, src);
+        r.count = __shfl_sync(0xffffffffu, all, src);
+        r.s = turn ? r.count - 1 : id - __shfl_sync(0xffffffffu, base + run - mine, src);
+        r.record = records + __shfl_sync(0xffffffffu, run_all - all, src);
+        r.t0 = seq_start(args, r.n);
+      }
+      base += __shfl_sync(0xffffffffu, run, 31);
+      records += __shfl_sync(0xffffffffu, run_all, 31);
+    }
+  }
+  r.tokens = L;
   return r;
 }
 
@@ -337,11 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     leave();
     return;
   }
-  const int len = seq_len(args, seg.n);
   const int first = seg.s * seg.tokens;
   const bool last_segment = seg.s == seg.count - 1;
-  const int L = last_segment ? len - first : seg.tokens, nch = (L + kC - 1) / kC;
-  const int64_t t0 = seq_start(args, seg.n) + first;
+  const int L = last_segment ? seg.len - first : seg.tokens, nch = (L + kC - 1) / kC;
+  const int64_t t0 = seg.t0 + first;
   const int slot = args.state_idx[seg.n];
   const bool no_slot = slot < 0 || slot >= args.pool_slots;
   if (LOCAL && (last_segment || no_slot)) return;  // nothing starts from its state
@@ -360,9 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::tmem_alloc(&bars.tmem, kTmCols);
   if (tid == 0) {
     bars.timed_out = 0;
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(&bars.empty[i], 1);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&bars.full[i], 1);
+      tc::mbar_init(&bars.empty[i], 1);
+    }
     for (int i = 0; i < kScalarBufs; ++i) {
-      tc::mbar_init(&bars.in_full[i], 2);
+      tc::mbar_init(&bars.gate_full[i], 1);
+      tc::mbar_init(&bars.in_full[i], kNormWarps);
       tc::mbar_init(&bars.sc_free[i], kWorkers);
     }
     for (int i = 0; i < 2; ++i) {
@@ -385,7 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float k_up = F16 && ga.use_qk_l2norm ? 32768.f : 1.f;
   bool ok = true;
 
+  // 768 threads start with 80 registers each; 512 at 96 and 256 at 48 are those 61440
   if (warp < kWorkers) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // A warp that runs out of time goes on without waiting and without arriving, so
     // that the others meet it at their barrier and run out too.
     const int quad = warp & 3, part = warp >> 2;
@@ -398,49 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto await = [&](uint64_t* bar, uint32_t phase) { ok = ok && warp_wait(bar, phase); };
     constexpr int kStage = LOCAL ? kLocalStage : kStageBytes, kK = LOCAL ? 0 : kTile;
 
-    // --------------------------------------------------------------------- norms
-    // The squares of 16 rows of K (warps 0 to 3) or Q (4 to 7) are the diagonal of the
-    // rows times themselves, by register-to-register products; then the factors.
-    const int r16 = 16 * (warp & 3) + (lane & 15);
-    const bool normed = warp < 8 && !(LOCAL && warp >= 4) && (ga.use_qk_l2norm || F16);
-    auto norms = [&](int c, int st, Scalars& sc) {
-      await(&bars.in_full[c % kScalarBufs], c / kScalarBufs);
-      if (!normed) return;
-      const uint8_t* tile = smem + st * kStage + (warp < 4 ? kK : 0);
-      float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint32_t f[4];
-        ldm4(tc::smem_u32(tile) + (k >> 2) * 8192 + r16 * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (r16 & 7)) << 4), f);
-        mma16<F16>(lo, f, f[0], f[2]);
-        mma16<F16>(hi, f, f[1], f[3]);
-      }
-      // row g of lo is in lane 4 g + g / 2, and so is row g + 8 of hi
-      const int g = lane >> 2, from = 4 * (lane & 7) + ((lane & 7) >> 1);
-      const float d_lo = __shfl_sync(0xffffffffu, g & 1 ? lo[1] : lo[0], from);
-      const float d_hi = __shfl_sync(0xffffffffu, g & 1 ? hi[3] : hi[2], from);
-      const float n = lane & 8 ? d_hi : d_lo, r = ga.use_qk_l2norm ? rsqrtf(n + kNormEps) : 1.f;
-      const bool upper = lane >= 16;
-      if (warp < 4) {
-        if (ga.use_qk_l2norm) {
-          if (!LOCAL) {
-            sc.col[upper ? 1 : 0][r16] *= r;
-            sc.col[upper ? 3 : 2][r16] *= r;
-          }
-          if (upper) sc.w[r16] *= r; else sc.k[r16] = r;
-        } else if (upper) {
-          sc.kk[r16] = r16 < L - c * kC ? n : 0.f;  // of this sequence alone
-        }
-      } else {
-        if (ga.use_qk_l2norm) (upper ? sc.row : sc.out)[r16] *= r;
-        if (F16 && !upper) sc.big[r16] *= sqrtf(n);
-      }
-    };
-
     // ------------------------------------------------------------------------- K'
     // 4 rows a warp; of its row a thread has a 16-byte piece of either half of the channels
     const int row = 4 * warp + (lane >> 3), x8 = lane & 7;
     auto keys = [&](int c, int st, const Scalars& sc) {
+      await(&bars.in_full[c % kScalarBufs], c / kScalarBufs);
       const int left = L - c * kC;
       uint8_t* rows = smem + st * kStage + kK;
       uint8_t* to = smem + (LOCAL ? kStages * kLocalStage + (c & 1) * kLocalWk : kWk);
@@ -519,14 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float k_down = 1.f / k_up;
     auto update = [&](int c, float last) {  // S of the next chunk
       tc::tc_fence_after();
+      uint32_t r[2][16];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        tc::tmem_ld16_async(lanes + kTmU + (LOCAL ? 128 * (c & 1) : 0) + 32 * part + 16 * g, r[g]);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        uint32_t r[16];
-        tc::tmem_ld16_async(lanes + kTmU + (LOCAL ? 128 * (c & 1) : 0) + 32 * part + 16 * g, r);
-        wait_ld(r);
+        wait_ld(r[g]);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          float2 u = make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          float2 u = make_float2(__uint_as_float(r[g][j]), __uint_as_float(r[g][j + 1]));
           if (F16) u = mul2(u, make_float2(k_down, k_down));
           const float2 x = fma2(make_float2(last, last), make_float2(S[16 * g + j], S[16 * g + j + 1]), u);
           S[16 * g + j] = x.x;
@@ -692,9 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     auto stage = [&](int c) { return c % kStages; };
     auto factors = [&](int c) -> Scalars& { return scalars[c % kScalarBufs]; };
-    norms(0, stage(0), factors(0));
-    if (nch > 1) norms(1, stage(1), factors(1));
-    asm volatile("barrier.cta.sync 1, 512;" ::: "memory");
     keys(0, stage(0), factors(0));
     done(&bars.wk_full[0]);
     start();  // (the first launch may still be running)
@@ -707,11 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           update(c - 1, last);
         }
         last = factors(c).last;
-        if (c + 2 < nch) norms(c + 2, stage(c + 2), factors(c + 2));
-        if (c + 1 < nch) {
-          await(&bars.wk_full[c & 1], c >> 1);  // all warps are past norms(c + 1)
-          keys(c + 1, stage(c + 1), factors(c + 1));
-        }
+        if (c + 1 < nch) keys(c + 1, stage(c + 1), factors(c + 1));
         tc::tc_fence_before();
         if (c + 1 < nch) done(&bars.wk_full[(c + 1) & 1]);
         done(&bars.sc_free[c % kScalarBufs]);
@@ -725,7 +700,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         done(&bars.s_full);
         weights(c, factors(c));
         if (c > 0) outputs(c - 1, factors(c - 1), &bars.sc_free[(c - 1) % kScalarBufs]);
-        if (c + 2 < nch) norms(c + 2, stage(c + 2), factors(c + 2));
         await(&bars.sq_full[c & 1], c >> 1);  // K' and S^T have been read, dS and O1 are there
         if (c + 1 < nch) {
           keys(c + 1, stage(c + 1), factors(c + 1));
@@ -749,7 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float4*>(root + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
       }
     }
-  } else if (warp == kRowWarp) {
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+  if (warp == kRowWarp) {
     // ------------------------------------------------------------------------ rows
     constexpr int kStage = LOCAL ? kLocalStage : kStageBytes;
     const bool leader = elect_one();
@@ -759,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c >= kStages && !(ok = warp_wait(&bars.empty[st], c / kStages - 1))) break;
       uint8_t* rows = smem + st * kStage;
       if (leader) {
-        uint64_t* bar = &bars.in_full[c % kScalarBufs];
+        uint64_t* bar = &bars.full[st];
         tc::mbar_expect_tx(bar, kStage);
         const int tok = (int)t0 + c * kC;
 #pragma unroll
@@ -773,8 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       issued = c + 1;
     }
     // nothing may land after the CTA is gone
-    for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
-      warp_wait(&bars.in_full[c % kScalarBufs], c / kScalarBufs);
+    for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c) warp_wait(&bars.full[c % kStages], c / kStages);
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------------- products
     constexpr uint32_t kType = F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
@@ -855,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else {
+  } else if (warp < kNormWarp) {
     // ----------------------------------------------------------- the decays' factors
     // one of two warps, every other chunk
     const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
@@ -869,19 +844,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     load_gate(warp - kGateWarp);
+#pragma unroll 1
     for (int c = warp - kGateWarp; c < nch; c += 2) {
       const int left = L - c * kC, sb = c % kScalarBufs;
       Scalars& sc = scalars[sb];
-      const float g0 = 2 * lane < left ? lin_log_decay<F16>(ga, next[0], neg_rate, bias) : 0.f;
-      const float g1 = 2 * lane + 1 < left ? lin_log_decay<F16>(ga, next[1], neg_rate, bias) : 0.f;
+      float g[2];
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) g[e] = 2 * lane + e < left ? lin_log_decay<F16>(ga, e ? next[1] : next[0], neg_rate, bias) : 0.f;
       load_gate(c + 2);
-      float2 run = pair_add(make_float2(g0, 0.f), make_float2(g1, 0.f));  // c of token 2 lane + 1
-#pragma unroll
+      float2 run = pair_add(make_float2(g[0], 0.f), make_float2(g[1], 0.f));  // c of token 2 lane + 1
+#pragma unroll 1
       for (int d = 1; d < 32; d <<= 1) {
         const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
         if (lane >= d) run = pair_add(up, run);
       }
-      const float2 even = pair_add(run, make_float2(-g1, 0.f));  // of token 2 lane
+      const float2 even = pair_add(run, make_float2(-g[1], 0.f));  // of token 2 lane
       if (c >= kScalarBufs && !(ok = warp_wait(&bars.sc_free[sb], c / kScalarBufs - 1))) break;
       auto put2 = [&](float* to, float a, float b) { *reinterpret_cast<float2*>(to + 2 * lane) = make_float2(a, b); };
       const float2 c_last = pair_from(run, 31);
@@ -890,15 +867,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!LOCAL) {
         put2(sc.c_hi, even.x, run.x);
         put2(sc.c_lo, even.y, run.y);
-        put2(sc.out, ga.scale * expf(even.x + even.y), ga.scale * expf(run.x + run.y));
         put2(sc.k, 1.f, 1.f);
+        put2(sc.out, ga.scale * expf(even.x + even.y), ga.scale * expf(run.x + run.y));
         const float2 c_b = pair_from(even, lane & 24), end = pair_from(run, lane | 7);
         const bool far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
         if ((lane & 7) == 0) sc.far[lane >> 3] = far;
         const float e0 = far ? 1.f : exp_diff(even, c_b), e1 = far ? 1.f : exp_diff(run, c_b);
         put2(sc.row, ga.scale * e0, ga.scale * e1);
         if (F16) put2(sc.big, 1.f / e0, 1.f / e1);
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 4; ++x) {
           const float2 ref = pair_from(even, 8 * x);
           const bool some = lane < 8 * x + 8;
@@ -906,8 +883,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) arrive(&bars.in_full[sb]);
+      if (lane == 0) arrive(&bars.gate_full[sb]);
     }
+  } else {
+    // ------------------------------------------------------------------------ norms
+    // The squares of 16 rows are the diagonal of the rows times themselves, by
+    // register-to-register products: of K, then of Q.
+    const int r16 = 16 * (warp - kNormWarp) + (lane & 15);
+    const bool l2 = ga.use_qk_l2norm, upper = lane >= 16;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+      Scalars& sc = scalars[c % kScalarBufs];
+      if (!(ok = warp_wait(&bars.full[c % kStages], c / kStages))) break;
+      float n[2];
+      if (l2 || F16) {
+        const uint32_t tile = tc::smem_u32(smem + c % kStages * (LOCAL ? kLocalStage : kStageBytes));
+#pragma unroll 1
+        for (int b = 0; b < (LOCAL ? 1 : 2); ++b) {
+          const uint32_t at = tile + (b == 0 && !LOCAL ? kTile : 0) + r16 * 128;
+          float lo[2][4] = {}, hi[2][4] = {};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t f[4];
+            ldm4(at + (k >> 2) * 8192 + ((((k & 3) * 2 + (lane >> 4)) ^ (r16 & 7)) << 4), f);
+            mma16<F16>(lo[k & 1], f, f[0], f[2]);
+            mma16<F16>(hi[k & 1], f, f[1], f[3]);
+          }
+          // row g of lo is in lane 4 g + g / 2, and so is row g + 8 of hi
+          const int odd = lane >> 2 & 1, from = 4 * (lane & 7) + ((lane & 7) >> 1);
+          const float d_lo = __shfl_sync(0xffffffffu, odd ? lo[0][1] + lo[1][1] : lo[0][0] + lo[1][0], from);
+          const float d_hi = __shfl_sync(0xffffffffu, odd ? hi[0][3] + hi[1][3] : hi[0][2] + hi[1][2], from);
+          (b ? n[1] : n[0]) = lane & 8 ? d_hi : d_lo;
+        }
+      }
+      if (!(ok = warp_wait(&bars.gate_full[c % kScalarBufs], c / kScalarBufs))) break;
+      if (l2) {
+        const float rk = rsqrtf(n[0] + kNormEps);
+        if (upper) sc.w[r16] *= rk;
+        if (!LOCAL) {
+          if (!upper) sc.k[r16] = rk;
+          sc.col[upper ? 1 : 0][r16] *= rk;
+          sc.col[upper ? 3 : 2][r16] *= rk;
+          (upper ? sc.row : sc.out)[r16] *= rsqrtf(n[1] + kNormEps);
+        }
+      }
+      if (F16 && !LOCAL) {
+        if (upper) sc.big[r16] *= sqrtf(n[1]);
+        else sc.kk[r16] = r16 < L - c * kC ? n[0] : 0.f;  // of this sequence alone
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&bars.in_full[c % kScalarBufs]);
+    }
+  }
   }
   // All products have been waited for but those whose results nobody needs; where a
   // wait has run out, with a limit, before TMEM and shared memory go.

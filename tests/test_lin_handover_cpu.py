@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-STAGES, BUFS = 3, 4
+STAGES, BUFS, NORMS = 3, 4, 2
 
 
 class Barrier:
@@ -29,8 +29,9 @@ class Cta:
 
     def __init__(self, nch, local, workers=3):
         self.nch, self.local, self.workers = nch, local, workers
-        self.bar = {("in", i): Barrier(2 if i >= 0 else 1) for i in range(BUFS)}
-        self.bar |= {("empty", i): Barrier(1) for i in range(STAGES)}
+        self.bar = {("in", i): Barrier(NORMS) for i in range(BUFS)}
+        self.bar |= {("gate", i): Barrier(1) for i in range(BUFS)}
+        self.bar |= {(x, i): Barrier(1) for x in ("full", "empty") for i in range(STAGES)}
         self.bar |= {("free", i): Barrier(workers) for i in range(BUFS)}
         self.bar |= {("wk", i): Barrier(workers) for i in range(2)}
         self.bar |= {("sq", i): Barrier(1) for i in range(2)}
@@ -46,6 +47,11 @@ class Cta:
 
     def use(self, what, chunk):
         assert self.holds.get(what) == chunk, f"{what} holds {self.holds.get(what)}, wanted {chunk}"
+
+    def use_factors(self, chunk):
+        self.use(("decays", chunk % BUFS), chunk)
+        for i in range(NORMS):
+            self.use(("factors", chunk % BUFS, i), chunk)
 
     def product(self, reads, writes, chunk):
         for r in reads:
@@ -75,7 +81,7 @@ def rows(t):
         for what in ("K", "V", "Q"):
             t.put((what, c % STAGES), c)
         yield
-        t.bar["in", c % BUFS].arrive()
+        t.bar["full", c % STAGES].arrive()
         yield
 
 
@@ -83,7 +89,22 @@ def factors(t, which):
     for c in range(which, t.nch, 2):
         if c >= BUFS:
             yield ("free", c % BUFS), c // BUFS - 1
-        t.holds["factors", c % BUFS] = c
+        t.holds["decays", c % BUFS] = c
+        yield
+        t.bar["gate", c % BUFS].arrive()
+        yield
+
+
+def norms(t, i):
+    for c in range(t.nch):
+        yield ("full", c % STAGES), c // STAGES
+        for what in ("K",) if t.local else ("K", "Q"):
+            t.use((what, c % STAGES), c)
+            yield
+        t.use((what, c % STAGES), c)
+        yield ("gate", c % BUFS), c // BUFS
+        t.use(("decays", c % BUFS), c)
+        t.holds["factors", c % BUFS, i] = c
         yield
         t.bar["in", c % BUFS].arrive()
         yield
@@ -91,17 +112,11 @@ def factors(t, which):
 
 def worker(t, w):
     """Worker w: its share of every place is a place of its own; a product needs all."""
-    n, W = t.nch, range(t.workers)
-
-    def norms(c):
-        yield ("in", c % BUFS), c // BUFS
-        t.use(("K", c % STAGES), c)
-        t.use(("factors", c % BUFS), c)
-        t.holds["norms", c % BUFS, w] = c
+    n = t.nch
 
     def keys(c):
-        for x in W:
-            t.use(("norms", c % BUFS, x), c)
+        yield ("in", c % BUFS), c // BUFS
+        t.use_factors(c)
         t.use(("K", c % STAGES), c)
         t.put(("wk", c & 1 if t.local else 0, w), c)
 
@@ -111,15 +126,11 @@ def worker(t, w):
     def outputs(c):
         t.use(("O1", c & 1), c)
         t.use(("O2", c & 1), c)
-        t.use(("factors", c % BUFS), c)
+        t.use_factors(c)
         yield
         t.bar["free", c % BUFS].arrive()
 
-    yield from norms(0)
-    if n > 1:
-        yield from norms(1)
-    yield "meet"
-    keys(0)
+    yield from keys(0)
     yield
     t.bar["wk", 0].arrive()
     for c in range(n):
@@ -128,12 +139,9 @@ def worker(t, w):
                 yield ("sq", (c - 1) & 1), (c - 1) >> 1
                 update(c - 1)
                 yield
-            t.use(("factors", c % BUFS), c)
-            if c + 2 < n:
-                yield from norms(c + 2)
+            t.use_factors(c)
             if c + 1 < n:
-                yield ("wk", c & 1), c >> 1
-                keys(c + 1)
+                yield from keys(c + 1)
                 yield
                 t.bar["wk", (c + 1) & 1].arrive()
             yield
@@ -142,15 +150,14 @@ def worker(t, w):
         else:
             if c > 0:
                 update(c - 1)
-            t.use(("factors", c % BUFS), c)
+            t.use_factors(c)
             yield
             t.put(("S", w), c)
             yield
             t.bar["s", 0].arrive()
             yield ("qk", 0), c
             t.use(("QK", c & 1), c)
-            for x in W:
-                t.use(("norms", c % BUFS, x), c)
+            t.use_factors(c)
             yield
             t.put(("P", w), c)
             yield
@@ -158,11 +165,9 @@ def worker(t, w):
             yield
             if c > 0:
                 yield from outputs(c - 1)
-            if c + 2 < n:
-                yield from norms(c + 2)
             yield ("sq", c & 1), c >> 1
             if c + 1 < n:
-                keys(c + 1)
+                yield from keys(c + 1)
                 yield
                 t.bar["wk", (c + 1) & 1].arrive()
             yield
@@ -204,17 +209,12 @@ def products(t):
 def run(nch, local, seed):
     rng = random.Random(seed)
     t = Cta(nch, local)
-    progs = [rows(t), products(t), factors(t, 0), factors(t, 1)] + [worker(t, w) for w in range(t.workers)]
+    progs = [rows(t), products(t), factors(t, 0), factors(t, 1)] + [norms(t, i) for i in range(NORMS)] + [worker(t, w) for w in range(t.workers)]
     speed = [rng.choice([0.02, 0.3, 1, 1]) for _ in progs] + [rng.choice([0.02, 0.3, 1])]  # the last: the tensor core
-    wait, met = [None] * len(progs), 0
+    wait = [None] * len(progs)
     alive = set(range(len(progs)))
-    idle = 0
     while alive or t.queue:
-        able = [i for i in alive if wait[i] is None or (wait[i] != "meet" and t.bar[wait[i][0]].ready(wait[i][1]))]
-        if [wait[i] for i in range(4, len(progs))] == ["meet"] * t.workers:
-            for i in range(4, len(progs)):
-                wait[i] = None
-            continue
+        able = [i for i in alive if wait[i] is None or t.bar[wait[i][0]].ready(wait[i][1])]
         if t.queue:
             able.append(len(progs))
         assert able, f"{nch} chunks, local {local}, seed {seed}: nothing can go on, waits {wait}"
