@@ -14,8 +14,8 @@
 // its state in FP32 registers.  Every product but Q K^T is transposed, so that its
 // rows are the value columns:
 //   Q K^T             64 x 64 x 128
-//   O1^T = S^T Q^T   128 x 64 x 128, S^T a left operand from TMEM, in two halves
-//   O2^T = V^T P^T   128 x 64 x 64, V as it landed, P in two halves
+//   O1^T = S^T Q^T   128 x 64 x 128, S^T a left operand from TMEM
+//   O2^T = V^T P^T   128 x 64 x 64, V as it landed
 //   dS^T = V^T K'    128 x 128 x 64, K'_j = e^(c_last - c_j) rk_j k_j in three parts
 //                    (FP16: two)
 // 16 warps do all the arithmetic, together and a step of it at a time, since what they
@@ -31,9 +31,12 @@
 // up the state that they start from.  The first segment starts from the pool's state
 // in both.
 //
-// Precision: BF16 halves hi + lo leave 2^-18, three parts 2^-26, FP16 halves 2^-23
-// (a power of two for each row of P and of S^T keeps them in range), so that the
-// state is as exact as FP32 sums leave it and an output is off by its own rounding.
+// Precision.  The state is FP32, in registers and in the pool.  K' is split in three
+// BF16 parts, 2^-26 of it left, or two FP16 ones, 2^-23, so that states are as exact as
+// FP32 sums leave them.  S^T and P as operands are rounded once to the outputs' type:
+// an output, which is rounded itself, comes out up to sqrt 2 times as far off as by its
+// own rounding alone (halves of both took a fifth more time).  FP16's range is kept by a
+// power of two for each row of P and of S^T.
 #include <atomic>
 
 #include "kda_host.h"
@@ -94,9 +97,10 @@ struct Bars {
   uint64_t in_full[kScalarBufs];     // rows and all factors
   uint64_t sc_free[kScalarBufs];     // factors read
   uint64_t wk_full[2];               // operands: K' (and what else a chunk needs), chunks in turn,
-  uint64_t s_full, p_full;           // S^T, P
-  uint64_t sq_full[2];               // products: dS and O1, chunks in turn,
-  uint64_t qk_full;                  // Q K^T (and the last O2)
+  uint64_t u_full, s_full[2];        // dS is in registers; S^T, chunks in turn
+  uint64_t p_full;                   // P
+  uint64_t ds_full[2];               // products: dS, chunks in turn,
+  uint64_t qk_full;                  // Q K^T (and the last O1 and O2)
   uint64_t o_full;                   // the segment's last O2
   uint64_t drained;                  // all products
   uint32_t tmem;
@@ -107,18 +111,18 @@ struct Bars {
 };
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
-// the parts of K', P's halves, factors, barriers.
+// the parts of K', P, factors, barriers.
 constexpr int kTile = 16384, kStageBytes = 3 * kTile;
-constexpr int kWk = kStages * kStageBytes, kP = kWk + 3 * kTile, kScalars = kP + 16384;
+constexpr int kWk = kStages * kStageBytes, kP = kWk + 3 * kTile, kScalars = kP + 8192;
 constexpr int kLocalStage = 2 * kTile, kLocalWk = 3 * kTile;  // LOCAL: K and V alone, and K' twice
 static_assert(kStages * kLocalStage + 2 * kLocalWk <= kScalars, "the first launch's layout");
 constexpr int kBars = kScalars + kScalarBufs * (int)sizeof(Scalars);
 constexpr int kSmem = kBars + (int)sizeof(Bars);
 static_assert(kSmem <= 232448 - 1024 && kBars % 16 == 0, "shared memory");
 
-// TMEM columns: dS, the operand S^T (two 16-bit numbers a column), and for chunks in
-// turn O1 and Q K^T, whose place O2 takes.
-constexpr int kTmU = 0, kTmS = 128, kTmSlo = 192, kTmQ = 256, kTmO = 384, kTmCols = 512;
+// TMEM columns: dS (the first launch's second one beside it), and for chunks in turn the
+// operand S^T (two 16-bit numbers a column), O1, and Q K^T, whose place O2 takes.
+constexpr int kTmU = 0, kTmS = 128, kTmQ = 256, kTmO = 384, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -133,10 +137,11 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 // A wait of two seconds at most; false: it ran out.
 //
 // A barrier's phase is known by its parity alone, so that a waiter must not fall two
-// phases behind: the next phase but one of each barrier here needs an arrival that
-// comes after every waiter's wait for this one.  Where products run ahead of their
-// waiters (the first launch's), there is a barrier for either parity of the chunk.
-__device__ __noinline__ bool long_wait(uint64_t* bar, uint32_t parity) {
+// phases behind, and who arrives must not be a phase ahead of the others: each phase of
+// a barrier here needs arrivals that come after every wait for the phase before last
+// and every arrival at the last one.  Where a chunk's alone would not see to that, there
+// is a barrier for either parity of the chunk.
+__device__ __forceinline__ bool long_wait(uint64_t* bar, uint32_t parity) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
   do {
@@ -335,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + kBars);
   Scalars* scalars = reinterpret_cast<Scalars*>(smem + kScalars);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (by an exchange, so that the compiler knows it for the same in all lanes)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (LOCAL) grid_dependency_launch();
   const int HV = args.HV, h = blockIdx.x % HV, id = blockIdx.x / HV;
   const Segment seg = find_segment(args, id, lane);
@@ -383,9 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.wk_full[i], kWorkers);
-      tc::mbar_init(&bars.sq_full[i], 1);
+      tc::mbar_init(&bars.ds_full[i], 1);
     }
-    tc::mbar_init(&bars.s_full, kWorkers);
+    tc::mbar_init(&bars.u_full, kWorkers);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&bars.s_full[i], kWorkers);
     tc::mbar_init(&bars.p_full, kWorkers);
     tc::mbar_init(&bars.qk_full, 1);
     tc::mbar_init(&bars.o_full, 1);
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = bars.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   const LinGateArgs& ga = args.gate;
   // FP16: unit keys are at most 1 and become K' times 2^15, so that small ones keep their places
   const float k_up = F16 && ga.use_qk_l2norm ? 32768.f : 1.f;
@@ -534,16 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        uint32_t hi[8], lo[8];
+        uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float2 x = make_float2(S[16 * g + 2 * j], S[16 * g + 2 * j + 1]), rest;
           if (F16) x = mul2(x, make_float2(down, down));
-          hi[j] = round2<F16>(x, rest);
-          lo[j] = round2<F16>(rest, x);
+          w[j] = round2<F16>(x, rest);
         }
-        tmem_st8(lanes + kTmS + 16 * part + 8 * g, hi);
-        tmem_st8(lanes + kTmSlo + 16 * part + 8 * g, lo);
+        tmem_st8(lanes + kTmS + 64 * (c & 1) + 16 * part + 8 * g, w);
       }
       wait_st();
     };
@@ -554,16 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* at[2];  // where columns 2 (lane % 4) and + 1 of a row's first piece are, but for the swizzle
 #pragma unroll
     for (int e = 0; e < 2; ++e) at[e] = smem + kP + (r0 + 8 * e) * 128 + 4 * (lane & 3);
-    auto put = [&](int j, int e, uint32_t hi, uint32_t lo) {
-      uint8_t* to = at[e] + ((j ^ turn) << 4);
-      *reinterpret_cast<uint32_t*>(to) = hi;
-      *reinterpret_cast<uint32_t*>(to + 8192) = lo;
-    };
+    auto put = [&](int j, int e, uint32_t x) { *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4)) = x; };
     if (!LOCAL && part > quad)  // right of the diagonal all is zero, and stays so
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0, 0);
+        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0);
     auto weights = [&](int c, const Scalars& sc) {
       await(&bars.qk_full, c);  // the last P has been read too
       tc::tc_fence_after();
@@ -616,8 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[e].y = col < i_row ? x[e].y : 0.f;
             }
             float2 rest;
-            const uint32_t hi = round2<F16>(x[e], rest), lo = round2<F16>(rest, x[e]);
-            put(2 * part + i, e, hi, lo);
+            put(2 * part + i, e, round2<F16>(x[e], rest));
           }
         }
       }
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K' and dS are there twice: a chunk's product runs while the next one's K' is made
       for (int c = 0; c < nch; ++c) {
         if (c > 0) {
-          await(&bars.sq_full[(c - 1) & 1], (c - 1) >> 1);
+          await(&bars.ds_full[(c - 1) & 1], (c - 1) >> 1);
           update(c - 1, last);
         }
         last = factors(c).last;
@@ -694,13 +694,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       for (int c = 0; c < nch; ++c) {
         if (c > 0) update(c - 1, last);
+        tc::tc_fence_before();
+        done(&bars.u_full);
         last = factors(c).last;
         operand(c);
         tc::tc_fence_before();
-        done(&bars.s_full);
+        done(&bars.s_full[c & 1]);
         weights(c, factors(c));
         if (c > 0) outputs(c - 1, factors(c - 1), &bars.sc_free[(c - 1) % kScalarBufs]);
-        await(&bars.sq_full[c & 1], c >> 1);  // K' and S^T have been read, dS and O1 are there
+        await(&bars.ds_full[c & 1], c >> 1);  // K' has been read, dS is there
         if (c + 1 < nch) {
           keys(c + 1, stage(c + 1), factors(c + 1));
           done(&bars.wk_full[(c + 1) & 1]);
@@ -709,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       await(&bars.o_full, 0);
       outputs(nch - 1, factors(nch - 1), &bars.sc_free[(nch - 1) % kScalarBufs]);
     }
-    if (LOCAL) await(&bars.sq_full[(nch - 1) & 1], (nch - 1) >> 1);
+    if (LOCAL) await(&bars.ds_full[(nch - 1) & 1], (nch - 1) >> 1);
     if (LOCAL || last_segment) {
       update(nch - 1, last);
       if (LOCAL) {
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j)
               tc::mma_bf16(tmem + kTmU + 128 * (c & 1), v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU,
                            b + j > 0);
-          tc::mma_commit(&bars.sq_full[c & 1]);
+          tc::mma_commit(&bars.ds_full[c & 1]);
           tc::mma_commit(&bars.empty[c % kStages]);
         }
         __syncwarp();
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_commit(&bars.qk_full);
         }
         __syncwarp();
-        if (!(ok = warp_wait(&bars.s_full, c))) break;
+        if (!(ok = warp_wait(&bars.u_full, c))) break;
         tc::tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -805,13 +807,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               tc::mma_bf16(tmem + kTmU, v_op + ((j * 2048) >> 4), wk_op + ((b * kTile + j * 2048) >> 4), kIdU, b + j > 0);
+          tc::mma_commit(&bars.ds_full[c & 1]);
+        }
+        __syncwarp();
+        if (!(ok = warp_wait(&bars.s_full[c & 1], c >> 1))) break;
+        tc::tc_fence_after();
+        if (leader) {  // O1^T = S^T Q^T
 #pragma unroll
-          for (int b = 0; b < 2; ++b)  // O1^T = S^T Q^T
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              mma_ts(tmem + kTmQ + turn, tmem + (b ? kTmSlo : kTmS) + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
-                     b + j > 0);
-          tc::mma_commit(&bars.sq_full[c & 1]);
+          for (int j = 0; j < 8; ++j)
+            mma_ts(tmem + kTmQ + turn, tmem + kTmS + turn + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType, j > 0);
         }
         __syncwarp();
         if (!(ok = warp_wait(&bars.p_full, c))) break;
@@ -819,11 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
         if (leader) {  // O2^T = V^T P^T
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tc::mma_bf16(tmem + kTmO + turn, v_op + ((j * 2048) >> 4), p_op + ((b * 8192 + j * 32) >> 4), kType | tc::kIdescMnA,
-                           b + j > 0);
+          for (int j = 0; j < 4; ++j)
+            tc::mma_bf16(tmem + kTmO + turn, v_op + ((j * 2048) >> 4), p_op + ((j * 32) >> 4), kType | tc::kIdescMnA, j > 0);
           tc::mma_commit(&bars.empty[st]);
           if (c == nch - 1) tc::mma_commit(&bars.o_full);
         }

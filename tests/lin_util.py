@@ -6,10 +6,11 @@ the 16-bit type (BF16 2^-8, FP16 2^-11 relative to the value):
   - an output is rounded once: u |o|, and FP16 numbers below 2^-14 lie 2^-24 apart,
     so that their rounding is off by up to 2^-25 whatever u |o| is;
   - inside a chunk the weights q.k e^(..) of the values are rounded once to 16
-    bits: u (1 + u) scale sum_j |q.k_j| e^(c_i - c_j) |v_j|.  (A second 16 bits may
-    keep what that drops.)  FP16 weights are kept times a power of two that takes
+    bits: u (1 + u) scale sum_j |q.k_j| e^(c_i - c_j) |v_j|.  FP16 weights are kept times a power of two that takes
     |q_i| max_j |k_j| above 2^14, with steps of 2^-24 at the bottom, 2^-38 of that:
     2^-39 scale |q_i| max_j |k_j| sum_j |v_j|;
+  - for its product with q the state before a chunk is rounded once to 16 bits:
+    u (1 + u) scale e^(c_i) sum_k |q_k| |S_vk|;
   - everything else is FP32 or a pair of 16-bit halves: exponentials 2^-17 for the
     smallest factors, norms 2^-22, halves 2^-17, sums of 64 and 128 terms 2^-16.4
     of the magnitudes' sum, all told below 2^-14 of scale |q|.(|S| built from
@@ -61,11 +62,13 @@ def host(x):
     return None if x is None else x.double().numpy()
 
 
-def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
-    """Error bounds of (outputs [T,HV,V], last state) of one sequence."""
+def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False, parts=(0,)):
+    """Error bounds of (outputs [T,HV,V], last state) of one sequence, prefilled in
+    parts that start at the given tokens."""
     G = v.shape[1] // q.shape[1]
     q, k = (np.repeat(so.lin_unit(x, norm), G, 1) for x in (q, k))
-    v = np.abs(np.asarray(v, np.float64))
+    X, signed = np.asarray(S0, np.float64), np.asarray(v, np.float64)  # the state itself
+    v = np.abs(signed)
     T = len(q)
     c = np.cumsum(g, 0)
     S = np.abs(np.asarray(S0, np.float64))
@@ -75,12 +78,16 @@ def bounds(S0, q, k, v, g, scale, norm, dtype, exact_weights=False):
     for t in range(T):
         S = np.exp(g[t])[:, None, None] * S + v[t][:, :, None] * np.abs(k[t])[:, None, :]
         aq = np.abs(q[t])
-        if t % 64 == 0:
+        if (t - max(x for x in parts if x <= t)) % 64 == 0:  # a chunk starts
             E0, c0 = E, c[t - 1] if t else 0 * c[0]
-            mine = 0 * E
+            X0, mine = np.abs(X), 0 * E
+        X = np.exp(g[t])[:, None, None] * X + signed[t][:, :, None] * k[t][:, None, :]
         mine = mine + step * v[t]
         E = np.exp(c[t] - c0)[:, None] * E0 + mine
         o[t] = scale * (REST * np.einsum("hvk,hk->hv", S, aq) + E0 * aq.sum(-1)[:, None])
+        if not exact_weights:
+            u = U[dtype]
+            o[t] += u * (1 + u) * scale * np.exp(c[t] - c0)[:, None] * np.einsum("hvk,hk->hv", X0, aq)
         if dtype == "f16":
             o[t] += 2.0 ** -39 * scale * aq.sum(-1)[:, None] * S.max(-1)
     if not exact_weights:

@@ -34,8 +34,8 @@ class Cta:
         self.bar |= {(x, i): Barrier(1) for x in ("full", "empty") for i in range(STAGES)}
         self.bar |= {("free", i): Barrier(workers) for i in range(BUFS)}
         self.bar |= {("wk", i): Barrier(workers) for i in range(2)}
-        self.bar |= {("sq", i): Barrier(1) for i in range(2)}
-        self.bar |= {("s", 0): Barrier(workers), ("p", 0): Barrier(workers), ("qk", 0): Barrier(1), ("o", 0): Barrier(1)}
+        self.bar |= {("ds", i): Barrier(1) for i in range(2)}
+        self.bar |= {("u", 0): Barrier(workers), ("s", 0): Barrier(workers), ("s", 1): Barrier(workers), ("p", 0): Barrier(workers), ("qk", 0): Barrier(1), ("o", 0): Barrier(1)}
         self.queue = []  # products and commits in issue order
         self.holds = {}  # resource -> chunk whose data it holds
         self.reading = {}  # resource -> products under way that read or write it
@@ -58,6 +58,8 @@ class Cta:
             self.use(r, chunk)
         for x in list(reads) + list(writes):
             self.reading[x] = self.reading.get(x, 0) + 1
+        for x in writes:
+            self.holds[x] = None  # until it is done
         self.queue.append(("product", list(reads) + list(writes), list(writes), chunk))
 
     def commit(self, bar):
@@ -118,6 +120,8 @@ def worker(t, w):
         yield ("in", c % BUFS), c // BUFS
         t.use_factors(c)
         t.use(("K", c % STAGES), c)
+        if w == 0:
+            t.put(("V", c % STAGES), c)  # rows past the end zeroed
         t.put(("wk", c & 1 if t.local else 0, w), c)
 
     def update(c):
@@ -136,7 +140,7 @@ def worker(t, w):
     for c in range(n):
         if t.local:
             if c > 0:
-                yield ("sq", (c - 1) & 1), (c - 1) >> 1
+                yield ("ds", (c - 1) & 1), (c - 1) >> 1
                 update(c - 1)
                 yield
             t.use_factors(c)
@@ -150,11 +154,15 @@ def worker(t, w):
         else:
             if c > 0:
                 update(c - 1)
+                yield
+                update(c - 1)
+            t.bar["u", 0].arrive()
+            yield
             t.use_factors(c)
             yield
-            t.put(("S", w), c)
+            t.put(("S", c & 1, w), c)
             yield
-            t.bar["s", 0].arrive()
+            t.bar["s", c & 1].arrive()
             yield ("qk", 0), c
             t.use(("QK", c & 1), c)
             t.use_factors(c)
@@ -165,14 +173,14 @@ def worker(t, w):
             yield
             if c > 0:
                 yield from outputs(c - 1)
-            yield ("sq", c & 1), c >> 1
+            yield ("ds", c & 1), c >> 1
             if c + 1 < n:
                 yield from keys(c + 1)
                 yield
                 t.bar["wk", (c + 1) & 1].arrive()
             yield
     if t.local:
-        yield ("sq", (n - 1) & 1), (n - 1) >> 1
+        yield ("ds", (n - 1) & 1), (n - 1) >> 1
     else:
         yield ("o", 0), 0
         yield from outputs(n - 1)
@@ -188,16 +196,17 @@ def products(t):
         wk = c & 1 if t.local else 0
         if t.local:
             t.product([("V", st)] + [("wk", wk, x) for x in W], [("dS", wk)], c)
-            t.commit(("sq", c & 1))
+            t.commit(("ds", c & 1))
             t.commit(("empty", st))
             yield
             continue
         t.product([("Q", st), ("K", st)], [("QK", c & 1)], c)
         t.commit(("qk", 0))
-        yield ("s", 0), c
+        yield ("u", 0), c
         t.product([("V", st)] + [("wk", 0, x) for x in W], [("dS", 0)], c)
-        t.product([("Q", st)] + [("S", x) for x in W], [("O1", c & 1)], c)
-        t.commit(("sq", c & 1))
+        t.commit(("ds", c & 1))
+        yield ("s", c & 1), c >> 1
+        t.product([("Q", st)] + [("S", c & 1, x) for x in W], [("O1", c & 1)], c)
         yield ("p", 0), c
         t.product([("V", st)] + [("P", x) for x in W], [("O2", c & 1)], c)
         t.commit(("empty", st))
