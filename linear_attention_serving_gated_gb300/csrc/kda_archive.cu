@@ -27,28 +27,33 @@ struct ArchiveArgs {
   int32_t* err_flag;
 };
 
-// What a CTA works on; false: nothing.  A pair whose destination another pair
-// has too is refused, like one that is out of range.
+// What a CTA works on.  Its loads start as soon as its own pair is known to be in range;
+// whether another pair has the same destination is found out while they are under way.
 struct Work {
-  int src, dst;
+  int pair, src, dst;
   int64_t layer, row0;  // this warp's first row
+  bool in_range;
 };
-__device__ __forceinline__ bool find_work(const ArchiveArgs& a, int src_slots, int dst_slots, Work& w) {
+__device__ __forceinline__ Work find_work(const ArchiveArgs& a, int src_slots, int dst_slots) {
+  Work w;
   const int64_t per_pair = (int64_t)a.parts * a.pages.layers;
-  const int i = (int)(blockIdx.x / per_pair);
+  w.pair = (int)(blockIdx.x / per_pair);
   const int64_t rest = blockIdx.x % per_pair;
-  w.src = a.src[i];
-  w.dst = a.dst[i];
-  if (w.src == -1 || w.dst == -1) return false;
-  bool bad = w.src < 0 || w.dst < 0 || w.src >= src_slots || w.dst >= dst_slots;
-  for (int j = threadIdx.x; j < a.n && !bad; j += kThreads) bad |= j != i && a.src[j] != -1 && a.dst[j] == w.dst;
-  if (__syncthreads_or(bad)) {
-    if (rest == 0 && threadIdx.x == 0) set_error(a.err_flag, KDA_DEVERR_PAGE);
-    return false;
-  }
+  w.src = a.src[w.pair];
+  w.dst = a.dst[w.pair];
+  w.in_range = w.src >= 0 && w.dst >= 0 && w.src < src_slots && w.dst < dst_slots;
   w.layer = rest / a.parts;
   w.row0 = rest % a.parts * kPartRows + (int64_t)(threadIdx.x >> 5) * kRowsPerWarp;
-  return true;
+  return w;
+}
+// Whether the pair is one to copy; the whole CTA, a barrier.
+__device__ __forceinline__ bool accept(const ArchiveArgs& a, const Work& w) {
+  if (w.src == -1 || w.dst == -1) return false;
+  bool bad = !w.in_range;
+  for (int j = threadIdx.x; j < a.n && !bad; j += kThreads) bad |= j != w.pair && a.src[j] != -1 && a.dst[j] == w.dst;
+  if (!__syncthreads_or(bad)) return true;
+  if (blockIdx.x % ((int64_t)a.parts * a.pages.layers) == 0 && threadIdx.x == 0) set_error(a.err_flag, KDA_DEVERR_PAGE);
+  return false;
 }
 
 // Codes of four values.  x times 1 / scale may fall on the wrong side of a half;
@@ -65,8 +70,7 @@ __device__ __forceinline__ int code_of(float x, float scale, float inv, float to
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveArgs a) {
   constexpr float kTop = BITS == 8 ? 127.f : 7.f;
-  Work w;
-  if (!find_work(a, a.pages.slots, a.slots, w)) return;
+  const Work w = find_work(a, a.pages.slots, a.slots);
   const int lane = threadIdx.x & 31;
   const float4* page = reinterpret_cast<const float4*>(static_cast<const char*>(a.pages.base) + w.layer * a.pages.layer_stride +
                                                        (int64_t)w.src * a.pages.page_bytes);
@@ -74,7 +78,8 @@ __global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveAr
   float4 x[kRowsPerWarp];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i)
-    x[i] = w.row0 + i < a.rows ? __ldcs(page + (w.row0 + i) * (kRow / 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[i] = w.in_range && w.row0 + i < a.rows ? __ldcs(page + (w.row0 + i) * (kRow / 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!accept(a, w)) return;
   float mine = 0.f;  // the scale that this lane stores
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
@@ -125,8 +130,7 @@ __global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveAr
 
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) archive_load_kernel(const ArchiveArgs a) {
-  Work w;
-  if (!find_work(a, a.slots, a.pages.slots, w)) return;
+  const Work w = find_work(a, a.slots, a.pages.slots);
   const int lane = threadIdx.x & 31;
   float4* page = reinterpret_cast<float4*>(static_cast<char*>(a.pages.base) + w.layer * a.pages.layer_stride +
                                            (int64_t)w.dst * a.pages.page_bytes);
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) archive_load_kernel(const ArchiveArg
     const int64_t row = from + w.row0 + i;
     c[i] = 0;
     s[i] = 0.f;
-    if (w.row0 + i < a.rows) {
+    if (w.in_range && w.row0 + i < a.rows) {
       if (BITS == 8) {
         c[i] = __ldcs(reinterpret_cast<const uint32_t*>(a.codes) + row * (kRow / 4) + lane);
         s[i] = __ldcs(a.scales + row);
@@ -148,6 +152,7 @@ __global__ void __launch_bounds__(kThreads) archive_load_kernel(const ArchiveArg
       }
     }
   }
+  if (!accept(a, w)) return;
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
     if (w.row0 + i >= a.rows) continue;

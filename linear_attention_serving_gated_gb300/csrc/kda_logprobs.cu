@@ -3,20 +3,21 @@
 //
 // Of a row's logits x, with m the largest and z = sum exp(x - m):
 //   log p_j = x_j - m - log z,   entropy = log z - sum (x - m) exp(x - m) / z.
-// One pass over the row: a thread keeps m, z and the sum of the entropy of what it
-// has read (rescaled where m grows), and the tile's values stay in registers for
-// the search of the alternatives.
+// One pass over the row, in tiles of 12 KiB.  A thread copies its own pieces of a tile
+// to shared memory two tiles ahead and reads them back itself, so that no barrier stands
+// between a load and its use; it keeps m, z and the sum of the entropy of what it has
+// read, rescaled where m grows.
 //
-// Alternatives.  Of 8 warps' threads each takes the largest value of its own; the
-// ceil(top / 8)-th largest of those in every warp bounds from below what at least
-// top values of the tile reach, so that only values at or above the least of the 8
-// bounds (and above every earlier tile's) are candidates: some fifty of the first
-// tile's 8192, fewer of each later one.  They go to a list in shared memory, as
-// keys that no two entries share: the value's bits in an order of their own, then
-// the token's complement, so that among equals the lowest token comes first.  A
-// tile with more candidates than the list has room for (rows of one value) is
-// searched key by key instead.  At the end a key's rank is the number of larger
-// ones.
+// Alternatives.  Of the first tile each thread takes its largest value; the
+// ceil(top / 8)-th largest of those in every warp bounds from below what at least top
+// values of the tile reach, so that only values at or above the least of the 8 bounds
+// are candidates: some fifty of 3072 or 6144.  They go to a list in shared memory, as keys that
+// no two entries share: the value's bits in an order of their own, then the token's
+// complement, so that among equals the lowest token comes first.  Whenever the list
+// has grown to 256 it is cut to its top largest, and the last of them is the new bound,
+// which fewer values of each later tile reach.  A tile with more candidates than the
+// list has room for (rows of one value) is searched key by key instead.  A key's rank
+// is the number of larger ones.
 //
 // A row is split over the CTAs of a cluster where there are few rows; rank 0 joins
 // what the others leave in its shared memory.
@@ -33,10 +34,12 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
-constexpr int kPerThread = 32;  // a tile's values in a thread's registers
-constexpr int kTile = kThreads * kPerThread;
-constexpr int kList = 2048;     // candidates
+constexpr int kPieces = 3;      // 16-byte pieces of a tile a thread has
+constexpr int kAhead = 2;       // tiles under way
+constexpr int kList = 1024;     // candidates
+constexpr int kCut = 256;       // so many are cut to the top ones
 constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct LogprobsArgs {
   const void* logits;
@@ -87,24 +90,10 @@ __device__ __forceinline__ float one(const void* row, int64_t i) {
   return DT == KDA_DTYPE_F16 ? in16_to_float<true>(b) : in16_to_float<false>(b);
 }
 
-// A 16-byte piece widened.
-template <int DT>
-__device__ __forceinline__ void widen(uint4 w, float* x) {
-  if (DT == KDA_DTYPE_F32) {
-    x[0] = __uint_as_float(w.x);
-    x[1] = __uint_as_float(w.y);
-    x[2] = __uint_as_float(w.z);
-    x[3] = __uint_as_float(w.w);
-  } else {
-    const float4 a = in16x4_to_f4<DT == KDA_DTYPE_F16>(make_uint2(w.x, w.y)), b = in16x4_to_f4<DT == KDA_DTYPE_F16>(make_uint2(w.z, w.w));
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-}
-
 struct Lists {
+  uint4 ring[kAhead + 1][kPieces][kThreads];
   unsigned long long list[kList], best[kMaxTop], warp_best[kWarps];
-  int count;
+  int count, before;  // entries; and of earlier tiles
   uint32_t bound[kWarps];
   Stats stats[kWarps];
 };
@@ -126,15 +115,57 @@ __device__ __forceinline__ void rank_list(Lists& s, int n, int top) {
   __syncthreads();
 }
 
+__device__ __forceinline__ float no_infinity(float x) { return x == INFINITY ? FLT_MAX : x; }
+
+// 2^x, results below the smallest normal number as zero.
+__device__ __forceinline__ float exp2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two entries of a word (or the two words' one each) widened.
+template <int DT>
+__device__ __forceinline__ void widen(uint4 w, float2* x) {
+  if (DT == KDA_DTYPE_F32) {
+    x[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    x[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+  } else {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = DT == KDA_DTYPE_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&u[i]))
+                                 : make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  }
+}
+
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArgs args) {
-  constexpr int kSize = DT == KDA_DTYPE_F32 ? 4 : 2, kEach = 16 / kSize, kPieces = kPerThread / kEach;
-  __shared__ Lists s;
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArgs args) {
+  constexpr int kSize = DT == KDA_DTYPE_F32 ? 4 : 2, kEach = 16 / kSize;
+  __shared__ __align__(16) Lists s;
   __shared__ Joined joined;
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / ranks, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int top = TOP ? args.top : 0;
+  const char* row = static_cast<const char*>(args.logits) + (int64_t)r * args.stride * kSize;
+  // single entries before the first and behind the last whole 16 bytes, the others in pieces
+  const int to_piece = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / kSize;
+  const int head = to_piece < args.vocab ? to_piece : args.vocab;
+  const int pieces = (args.vocab - head) / kEach, tail = args.vocab - head - pieces * kEach;
+  const uint4* body = reinterpret_cast<const uint4*>(row + head * kSize);
+  const int tiles = (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
+  auto piece_of = [&](int tile, int j) { return (tile * kPieces + j) * kThreads + tid; };
+  auto fetch = [&](int tile, int slot) {  // (one group for every tile, of nothing behind the last)
+    if (tile < tiles) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        if (piece_of(tile, j) < pieces) cp_async16(&s.ring[slot][j][tid], body + piece_of(tile, j));
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(rank + i * ranks, i);
   const int token = args.tokens[r];
   if (token < 0 || token >= args.vocab) {  // nothing is asked of this row
     if (rank == 0) {
@@ -148,133 +179,158 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
         args.top_logprobs[(int64_t)r * top + tid] = 0.f;
       }
     }
+    cp_async_wait_all();
     return;  // the whole cluster
   }
   cluster_arrive();  // rank 0 has started before the others write to it
-  const char* row = static_cast<const char*>(args.logits) + (int64_t)r * args.stride * kSize;
   const float x_token = one<DT>(row, token);
-  // single entries before the first and behind the last whole 16 bytes, the others in pieces
-  const int to_piece = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / kSize;
-  const int head = to_piece < args.vocab ? to_piece : args.vocab;
-  const int pieces = (args.vocab - head) / kEach, tail = args.vocab - head - pieces * kEach;
-  const uint4* body = reinterpret_cast<const uint4*>(row + head * kSize);
-  const int tiles = (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
 
-  if (tid == 0) s.count = 0;
+  if (tid == 0) s.count = s.before = 0;
+  if (TOP) __syncthreads();
   Stats mine{-INFINITY, 0.f, 0.f};
   uint32_t least = kOrderedLowest;  // what a candidate has to reach
+  int slot = 0;
   for (int tile = rank; tile < tiles || tile == 0; tile += ranks) {
-    float x[kPerThread + 1];
-    int single = -1;  // the token of the single entry
-    x[kPerThread] = -INFINITY;
-    {
-      uint4 w[kPieces] = {};
-      const int p0 = tile * kThreads * kPieces + tid;
+    fetch(tile + kAhead * ranks, slot + kAhead > kAhead ? slot - 1 : kAhead);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    uint4 w[kPieces];
+    // a missing piece holds -inf
+    constexpr uint32_t kNone = DT == KDA_DTYPE_F32 ? 0xff800000u : DT == KDA_DTYPE_F16 ? 0xfc00fc00u : 0xff80ff80u;
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j)
-        if (p0 + j * kThreads < pieces) w[j] = __ldcs(body + p0 + j * kThreads);
-      if (tile == 0 && tid < head + tail) {
-        single = tid < head ? tid : args.vocab - tail + (tid - head);
-        x[kPerThread] = one<DT>(row, single);
-      }
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        widen<DT>(w[j], x + j * kEach);
-        if (p0 + j * kThreads >= pieces)
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) x[j * kEach + e] = -INFINITY;
-      }
+    for (int j = 0; j < kPieces; ++j) {
+      w[j] = make_uint4(kNone, kNone, kNone, kNone);
+      if (piece_of(tile, j) < pieces) w[j] = s.ring[slot][j][tid];
     }
+    slot = slot == kAhead ? 0 : slot + 1;
+    // the single entries in front with the first tile, those behind with rank 0's last
+    // one, so that a CTA's tokens come in order (but within a tile)
+    int single = -1;
+    float x_single = -INFINITY;
+    if (rank == 0) {
+      if (tile == 0 && tid < head) single = tid;
+      if (tile + ranks >= tiles && tid >= 32 && tid < 32 + tail) single = args.vocab - tail + tid - 32;
+      if (single >= 0) x_single = one<DT>(row, single);
+    }
+    float2 x[kEach / 2];
     float big = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) big = fmaxf(big, x[e]);  // NaN is left out
-    if (fmaxf(big, x[kPerThread]) == INFINITY) {  // counts as the largest number
+    for (int j = 0; j < kPieces; ++j) {
+      widen<DT>(w[j], x);
 #pragma unroll
-      for (int e = 0; e <= kPerThread; ++e) x[e] = x[e] == INFINITY ? FLT_MAX : x[e];
-      big = fminf(big, FLT_MAX);
+      for (int e = 0; e < kEach / 2; ++e) big = fmaxf(big, fmaxf(x[e].x, x[e].y));  // NaN is left out
     }
-    const float m = fmaxf(mine.m, fmaxf(big, x[kPerThread]));
+    // +inf counts as the largest number
+    const float m = fmaxf(mine.m, fminf(fmaxf(big, x_single), FLT_MAX));
     if (m > -INFINITY) {
-      const float down = fmaxf(mine.m - m, -1e4f), scale = __expf(down);
-      float z = mine.z * scale, t = (mine.t + mine.z * down) * scale;
+      const float down = fmaxf(mine.m - m, -1e4f), scale = exp2_(down * kLog2e);
+      float2 z = make_float2(mine.z * scale, 0.f), t = make_float2((mine.t + mine.z * down) * scale, 0.f);
+      auto add = [&](float2 v) {
+        // -inf and NaN: no weight; +inf: that of the largest number
+        const float2 d = add2(v, make_float2(-m, -m));
+        const float2 c = make_float2(fminf(fmaxf(d.x, -1e4f), 0.f), fminf(fmaxf(d.y, -1e4f), 0.f));
+        const float2 y = mul2(c, make_float2(kLog2e, kLog2e));
+        const float2 p = make_float2(exp2_(y.x), exp2_(y.y));
+        z = add2(z, p);
+        t = fma2(c, p, t);
+      };
 #pragma unroll
-      for (int e = 0; e <= kPerThread; ++e) {
-        const float d = fmaxf(x[e] - m, -1e4f);  // -inf and NaN: no weight
-        const float p = __expf(d);
-        z += p;
-        t = fmaf(d, p, t);
+      for (int j = 0; j < kPieces; ++j) {
+        widen<DT>(w[j], x);
+#pragma unroll
+        for (int e = 0; e < kEach / 2; ++e) add(x[e]);
       }
-      mine = Stats{m, z, t};
+      if (single >= 0) add(make_float2(x_single, -INFINITY));
+      mine = Stats{m, z.x + z.y, t.x + t.y};
     }
     if constexpr (TOP) {
-      const uint32_t u = ordered(big);
-      uint32_t left = u, bound = 0;
-      for (int i = 0; i < (top + kWarps - 1) / kWarps; ++i) {
-        bound = __reduce_max_sync(0xffffffffu, left);
-        if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
-      }
-      if (lane == 0) s.bound[warp] = bound;
-      __syncthreads();
-      const int before = s.count;
-      bound = s.bound[0];
+      auto token_at = [&](int j, int e) { return head + piece_of(tile, j) * kEach + e; };
+      auto each = [&](auto&& f) {  // every entry of the tile, as a number or -inf or NaN
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) bound = min(bound, s.bound[i]);
-      const bool full = bound >= least;  // then `top` values reach the bound
-      if (full) least = bound;
-      __syncthreads();  // everyone has read the count
-      auto token_at = [&](int e) {
-        return e == kPerThread ? single : head + (tile * kThreads * kPieces + e / kEach * kThreads + tid) * kEach + e % kEach;
-      };
-      if (max(u, ordered(fmaxf(x[kPerThread], -INFINITY))) >= least) {
-        const float bar = unordered(least);
+        for (int j = 0; j < kPieces; ++j) {
+          widen<DT>(w[j], x);
 #pragma unroll
-        for (int e = 0; e <= kPerThread; ++e)
-          if (x[e] >= bar) {
-            const int at = atomicAdd(&s.count, 1);
-            if (at < kList) s.list[at] = key_of(x[e], token_at(e));
+          for (int e = 0; e < kEach / 2; ++e) {
+            f(no_infinity(x[e].x), token_at(j, 2 * e));
+            f(no_infinity(x[e].y), token_at(j, 2 * e + 1));
           }
-      }
-      __syncthreads();
-      const int n = s.count;
-      if (n > kList) {  // too many at once: the tile's largest keys one by one
-        __syncthreads();
-        unsigned long long last = ~0ull;
-        int found = 0;
-        for (; found < top; ++found) {
-          unsigned long long k = 0;
-#pragma unroll
-          for (int e = 0; e <= kPerThread; ++e)
-            if (x[e] >= -FLT_MAX) {
-              const unsigned long long key = key_of(x[e], token_at(e));
-              if (key < last && key > k) k = key;
-            }
-#pragma unroll
-          for (int d = 16; d; d >>= 1) {
-            const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
-            k = o > k ? o : k;
-          }
-          if (lane == 0) s.warp_best[warp] = k;
-          __syncthreads();
-          k = s.warp_best[0];
-          for (int i = 1; i < kWarps; ++i) k = s.warp_best[i] > k ? s.warp_best[i] : k;
-          __syncthreads();
-          if (k == 0) break;
-          if (tid == 0) s.list[before + found] = k;
-          last = k;
         }
-        if (tid == 0) s.count = before + found;
+        if (single >= 0) f(no_infinity(x_single), single);
+      };
+      const uint32_t u = ordered(fminf(big, FLT_MAX));
+      bool full = false;  // `top` values reach the bound
+      if (tile == rank) {
+        uint32_t left = u, bound = 0;
+        for (int i = 0; i < (top + kWarps - 1) / kWarps; ++i) {
+          bound = __reduce_max_sync(0xffffffffu, left);
+          if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
+        }
+        if (lane == 0) s.bound[warp] = bound;
         __syncthreads();
+        bound = s.bound[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) bound = min(bound, s.bound[i]);
+        full = bound >= least;
+        if (full) least = bound;
       }
-      if (s.count > kList - 2 * kMaxTop || n > kList) {  // room for the next tile's
+      bool cut = false;
+      if (max(u, ordered(fmaxf(fminf(x_single, FLT_MAX), -INFINITY))) >= least) {
+        const float bar = unordered(least);
+        each([&](float v, int at) {
+          if (v >= bar) {
+            const int i = atomicAdd(&s.count, 1);
+            if (i < kList) s.list[i] = key_of(v, at);
+            cut |= i >= kCut;
+          }
+        });
+      }
+      if (full) ++least;  // among equals the lower tokens, which are listed, come first
+      if (__syncthreads_or(cut)) {
+        const int n = s.count;
+        if (n > kList) {  // too many at once: the tile's largest keys one by one
+          // what is listed of earlier tiles stays; what this one listed is not the lot, and goes
+          const int before = s.before;
+          __syncthreads();
+          unsigned long long last = ~0ull;
+          int found = 0;
+          for (; found < top; ++found) {
+            unsigned long long k = 0;
+            each([&](float v, int at) {
+              if (v >= -FLT_MAX) {
+                const unsigned long long key = key_of(v, at);
+                if (key < last && key > k) k = key;
+              }
+            });
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+              const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
+              k = o > k ? o : k;
+            }
+            if (lane == 0) s.warp_best[warp] = k;
+            __syncthreads();
+            k = s.warp_best[0];
+            for (int i = 1; i < kWarps; ++i) k = s.warp_best[i] > k ? s.warp_best[i] : k;
+            __syncthreads();
+            if (k == 0) break;
+            if (tid == 0) s.list[before + found] = k;
+            last = k;
+          }
+          if (tid == 0) s.count = before + found;
+          __syncthreads();
+        }
         const int have = s.count;
         rank_list(s, have, top);
         if (tid < kMaxTop) s.list[tid] = s.best[tid];
-        if (tid == 0) s.count = min(have, top);
+        const unsigned long long kth = s.best[top - 1];
+        if (kth) least = max(least, (uint32_t)(kth >> 32) + 1);
+        if (tid == 0) s.count = s.before = min(have, top);
         __syncthreads();
+      } else if (tid == 0) {
+        s.before = s.count;  // every entry of this tile is there; none of the next one yet
       }
-      if (full) ++least;  // among equals the lower tokens, which are listed, come first
+      __syncthreads();
     }
   }
+  cp_async_wait_all();
 
   // the CTA's part of the row, then the row
 #pragma unroll
@@ -338,6 +394,7 @@ template <int DT>
 kda_status launch_logprobs(const LogprobsArgs& a, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return KDA_ERR_CUDA;
+  constexpr int kTile = kThreads * kPieces * (DT == KDA_DTYPE_F32 ? 4 : 8);
   const int64_t tiles = ((int64_t)a.vocab + kTile - 1) / kTile;
   int ranks = 1;
   while (ranks < kMaxCluster && ranks < tiles && (int64_t)a.rows * ranks < 3 * (int64_t)sms) ranks *= 2;

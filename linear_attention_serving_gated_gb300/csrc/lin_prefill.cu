@@ -53,15 +53,15 @@ struct LinPrefillArgs {
   LinGateArgs gate;
   int HV, G;
   float* pool;
-  int pool_slots;
+  int pool_slots, pool32;  // whether the pool is aligned to 32 bytes
   const int32_t* state_idx;
   const int32_t* cu_seqlens;
   int num_seqs;
   int64_t total_tokens;
   kda_bf16* o;
   // tokens of a segment, multiples of 64: where no sequence is longer than even_most,
-  // and otherwise
-  int seg_even, seg_ragged, even_most;
+  // and otherwise; sequences of at most uncut tokens then stay in one piece
+  int seg_even, seg_ragged, even_most, uncut;
   float4* local_state;  // [segment, value head][8][512 threads]: what a segment adds
   float* local_decay;   // [segment, value head]: e^(its log-decays' sum)
   int32_t* err_flag;
@@ -244,6 +244,34 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Eight values: 32 bytes at once, a sector of L2, where they are so aligned, since the
+// lanes of a warp lie 512 bytes apart in a state (1 x 128 tokens, 4 heads: 12.6 us
+// instead of 14.7).
+__device__ __forceinline__ void ld8(const float* p, float* x, bool aligned32) {
+  if (aligned32) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
+  }
+}
+__device__ __forceinline__ void st8(float* p, const float* x, bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  }
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread; 16 k are 8 columns of A.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -272,8 +300,9 @@ struct Segment {
   int64_t t0;  // its first token
 };
 
-// The id-th segment: whole ones of all sequences first, then what is left of each, so
-// that the longest start first.  Every warp finds it for itself, a sequence a lane.
+// The id-th segment: longer sequences that stay in one piece, then the whole segments of
+// the others, then what is left of those and the short ones, so that the longest start
+// first.  Every warp finds it for itself, a sequence a lane.
 // (What runs once a CTA is kept short: instructions that no cache holds yet take five
 // or more times as long as others.)
 __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int id, int lane) {
@@ -285,19 +314,23 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
     if (id < count) r = Segment{0, id, count, 0, L, len, 0};
     return r;
   }
-  int most = 0;
+  int most = 0, uncut = 0;
 #pragma unroll 1
   for (int m = lane; m < seqs; m += 32) most = max(most, seq_len(args, m));
-  if (__reduce_max_sync(0xffffffffu, most) > args.even_most) L = args.seg_ragged;
-  // the first turn goes through whole segments, the second through what is left
+  if (__reduce_max_sync(0xffffffffu, most) > args.even_most) {
+    L = args.seg_ragged;
+    uncut = args.uncut;
+  }
   int base = 0;
 #pragma unroll 1
-  for (int turn = 0; turn < 2 && r.n < 0; ++turn) {
+  for (int turn = uncut ? 0 : 1; turn < 3 && r.n < 0; ++turn) {
     int records = 0;
 #pragma unroll 1
     for (int n0 = 0; n0 < seqs && r.n < 0; n0 += 32) {
       const int m = n0 + lane, len = m < seqs ? max(seq_len(args, m), 0) : 0;
-      const int whole = len / L, all = whole + (len != whole * L), mine = turn ? all - whole : whole;
+      const bool one = len > L && len <= uncut;
+      const int whole = one ? 0 : len / L, all = one ? 1 : whole + (len != whole * L);
+      const int mine = turn == 0 ? one : turn == 1 ? whole : one ? 0 : all - whole;
       int run = mine, run_all = all;
 #pragma unroll 1
       for (int d = 1; d < 32; d <<= 1) {
@@ -310,7 +343,7 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
         r.n = n0 + src;
         r.len = __shfl_sync(0xffffffffu, len, src);
         r.count = __shfl_sync(0xffffffffu, all, src);
-        r.s = turn ? r.count - 1 : id - __shfl_sync(0xffffffffu, base + run - mine, src);
+        r.s = turn != 1 ? r.count - 1 : id - __shfl_sync(0xffffffffu, base + run - mine, src);
         r.record = records + __shfl_sync(0xffffffffu, run_all - all, src);
         r.t0 = seq_start(args, r.n);
       }
@@ -465,18 +498,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* root = args.pool + (((size_t)slot * HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
     float S[32];
     auto record = [&](int64_t segment) { return args.local_state + (segment * HV + h) * 4096 + tid; };
+    // (The first launch leaves the pool as it is: what it does not leave behind can be
+    // read while it runs.)
+    if (seg.s == 0 && (LOCAL || seg.count == 1))
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) ld8(root + j, S + j, args.pool32);
     auto start = [&]() {
     if (!LOCAL) grid_dependency_wait();
     if (seg.s == 0) {
       // The CTA of the last segment writes the sequence's slot, maybe before this one
       // reads it: the first launch leaves a copy where the last segment has no record.
-      const bool copied = !LOCAL && seg.count > 1;
-      const float4* copy = record(seg.record + seg.count - 1);
+      float4* copy = record(seg.record + seg.count - 1);
+      if (LOCAL) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 x = copied ? __ldcg(copy + j * 512) : *reinterpret_cast<const float4*>(root + 4 * j);
-        S[4 * j] = x.x, S[4 * j + 1] = x.y, S[4 * j + 2] = x.z, S[4 * j + 3] = x.w;
-        if (LOCAL) const_cast<float4*>(copy)[j * 512] = x;
+        for (int j = 0; j < 8; ++j) copy[j * 512] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+      } else if (seg.count > 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 x = __ldcg(copy + j * 512);
+          S[4 * j] = x.x, S[4 * j + 1] = x.y, S[4 * j + 2] = x.z, S[4 * j + 3] = x.w;
+        }
       }
     } else {
 #pragma unroll
@@ -721,8 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) args.local_decay[(int64_t)(seg.record + seg.s) * HV + h] = decay;
       } else if (ok) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(root + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+        for (int j = 0; j < 32; j += 8) st8(root + j, S + j, args.pool32);
       }
     }
   } else {
@@ -987,9 +1027,10 @@ kda_status allow_all() {
 // Tokens of a segment.  Sequences of one length: the number of segments each that
 // takes least, by what a chunk and a CTA's start cost in thousands of cycles (measured:
 // 4.7 and 6 in the second launch, 2.3 and 5 in the first, which the last segments are
-// spared); with lengths that differ much, segments of half an SM's share.
+// spared); with lengths that differ much, segments of half an SM's share, for sequences
+// of more than 1.2 shares.
 struct Segments {
-  int even, ragged, even_most;
+  int even, ragged, even_most, uncut;
   int64_t most;  // segments of all sequences, at most
 };
 Segments cut(const kda_dims& d, int num_seqs, int64_t total_tokens, int64_t sms) {
@@ -1006,6 +1047,7 @@ Segments cut(const kda_dims& d, int num_seqs, int64_t total_tokens, int64_t sms)
   const int64_t share = (total_tokens * d.HV / (2 * sms) + kC - 1) / kC;
   r.even = (int)(even * kC);
   r.ragged = (int)((share < 4 ? 4 : share) * kC);
+  r.uncut = (int)(r.ragged * 12ll / 5 < INT32_MAX ? r.ragged * 12ll / 5 : INT32_MAX);
   const int64_t even_most = len + len / 4;
   r.even_most = num_seqs == 1 || even_most > INT32_MAX ? INT32_MAX : (int)even_most;
   const int64_t least = num_seqs > 1 && r.ragged < r.even ? r.ragged : r.even;
@@ -1056,6 +1098,7 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.G = dims.HV / dims.H;
   args.pool = state_pool;
   args.pool_slots = pool_slots;
+  args.pool32 = (reinterpret_cast<uintptr_t>(state_pool) & 31u) == 0;
   args.state_idx = state_idx;
   args.cu_seqlens = cu_seqlens;
   args.num_seqs = num_seqs;
@@ -1065,6 +1108,7 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.seg_even = c.even;
   args.seg_ragged = c.ragged;
   args.even_most = c.even_most;
+  args.uncut = c.uncut;
   args.err_flag = err_flag;
   const int64_t units = c.most * dims.HV;
   if (units > INT32_MAX) return KDA_ERR_SHAPE;

@@ -187,7 +187,7 @@ def test_prefill_captured_and_on_another_stream():
 
 
 def test_prefill_of_aligned_views():
-    """q, k, v and o inside larger tensors, 16 bytes off."""
+    """q, k, v, o and the pool inside larger tensors, 16 bytes off."""
     c = case([150, 33], H=1, HV=2)
     x = draw(c, 65)
     want = run(c, x)
@@ -196,12 +196,15 @@ def test_prefill_of_aligned_views():
         big = torch.full((up[n].numel() + 8,), float("nan"), dtype=up[n].dtype, device="cuda")
         big[8:] = up[n].flatten()
         up[n] = big[8:].view(up[n].shape)
+    states = torch.full((up["pool"].numel() + 4,), 3.0, device="cuda")  # a pool that is aligned to 16 bytes and no more
+    states[4:] = up["pool"].flatten()
+    up["pool"] = states[4:].view(up["pool"].shape)
     big = torch.full((want[0].numel() + 16,), 3.0, dtype=want[0].dtype, device="cuda")
     o = big[8:-8].view(want[0].shape)
     kda.kda_lin_prefill(lu.dims(c), lu.scalar_gate(x["A_log"], x["dt_bias"], True), up["q"], up["k"], up["v"], up["a"], up["pool"],
                         up["idx"], up["cu"], 2, o)
     assert torch.equal(o, want[0]) and torch.equal(up["pool"], want[1])
-    assert (big[:8] == 3).all() and (big[-8:] == 3).all()
+    assert (big[:8] == 3).all() and (big[-8:] == 3).all() and (states[:4] == 3).all()
 
 
 def packed(c, x):
