@@ -56,9 +56,9 @@ __device__ __forceinline__ bool accept(const ArchiveArgs& a, const Work& w) {
   return false;
 }
 
-// Codes of four values.  x times 1 / scale may fall on the wrong side of a half;
-// the remainder x - c scale is exact (a whole number of the operands' last places,
-// below the scale), and settles it.
+// The code of x, settled where x times 1 / scale may have fallen on the wrong side of a
+// half: the remainder x - c scale is exact (a whole number of the operands' last places,
+// below the scale).
 __device__ __forceinline__ int code_of(float x, float scale, float inv, float top) {
   float c = rintf(x * inv);
   const float r = fmaf(-c, scale, x), twice = 2.f * fabsf(r);
@@ -68,7 +68,7 @@ __device__ __forceinline__ int code_of(float x, float scale, float inv, float to
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) archive_store_kernel(const ArchiveArgs a) {
   constexpr float kTop = BITS == 8 ? 127.f : 7.f;
   const Work w = find_work(a, a.pages.slots, a.slots);
   const int lane = threadIdx.x & 31;
@@ -98,9 +98,19 @@ __global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveAr
     int c[4] = {0, 0, 0, 0};
     const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     if (finite && scale >= 1e-37f) {
-      const float inv = __frcp_rn(scale);
+      // x / scale rounded by adding 1.5 * 2^23, whose low bits are then the code; a
+      // remainder that is not below half a scale is one in a million, and settled exactly
+      const float inv = __frcp_rn(scale), half = 0.5f * scale;
+      bool close = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = code_of(v[e], scale, inv, kTop);
+      for (int e = 0; e < 4; ++e) {
+        const float y = fmaf(v[e], inv, 12582912.f);
+        close |= fabsf(fmaf(12582912.f - y, scale, v[e])) >= half;
+        c[e] = __float_as_int(y) - 0x4b400000;
+      }
+      if (close)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = code_of(v[e], scale, inv, kTop);
     } else if (finite && scale > 0.f) {  // 1 / scale may be out of range; such quotients have few places and are exact enough to round
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[e] = __double2int_rn(fmin(fmax((double)v[e] / (double)scale, -(double)kTop), (double)kTop));
@@ -109,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveAr
     if (w.row0 + i < a.rows) {
       if (BITS == 8)
         reinterpret_cast<uint32_t*>(a.codes)[row * (kRow / 4) + lane] =
-            (c[0] & 0xffu) | (c[1] & 0xffu) << 8 | (c[2] & 0xffu) << 16 | (uint32_t)(c[3] & 0xff) << 24;
+            __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
       else
         reinterpret_cast<uint16_t*>(a.codes)[row * (kRow / 4) + lane] =
             (uint16_t)((c[0] & 15) | (c[1] & 15) << 4 | (c[2] & 15) << 8 | (c[3] & 15) << 12);
@@ -129,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) archive_store_kernel(const ArchiveAr
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(kThreads) archive_load_kernel(const ArchiveArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) archive_load_kernel(const ArchiveArgs a) {
   const Work w = find_work(a, a.slots, a.pages.slots);
   const int lane = threadIdx.x & 31;
   float4* page = reinterpret_cast<float4*>(static_cast<char*>(a.pages.base) + w.layer * a.pages.layer_stride +
@@ -159,8 +169,10 @@ __global__ void __launch_bounds__(kThreads) archive_load_kernel(const ArchiveArg
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int code = BITS == 8 ? (int)(c[i] << (24 - 8 * e)) >> 24 : (int)(c[i] << (28 - 4 * e)) >> 28;
-      v[e] = (float)code * s[i];
+      // the code plus 128 (or 8) as the low bits of 2^23 (conversions run at a quarter of this rate)
+      const uint32_t u = BITS == 8 ? __byte_perm(c[i] ^ 0x80808080u, 0x4b000000u, 0x7650 | e)
+                                   : (((c[i] ^ 0x8888u) >> (4 * e)) & 15u) | 0x4b000000u;
+      v[e] = (__uint_as_float(u) - (BITS == 8 ? 8388736.f : 8388616.f)) * s[i];
     }
     page[(w.row0 + i) * (kRow / 4) + lane] = make_float4(v[0], v[1], v[2], v[3]);
   }

@@ -3,19 +3,19 @@
 //
 // Of a row's logits x, with m the largest and z = sum exp(x - m):
 //   log p_j = x_j - m - log z,   entropy = log z - sum (x - m) exp(x - m) / z.
-// One pass over the row, in tiles of 12 KiB.  A thread copies its own pieces of a tile
-// to shared memory two tiles ahead and reads them back itself, so that no barrier stands
+// One pass over the row, in tiles of 16 KiB.  A thread copies its own pieces of a tile
+// to shared memory a tile ahead and reads them back itself, so that no barrier stands
 // between a load and its use; it keeps m, z and the sum of the entropy of what it has
 // read, rescaled where m grows.
 //
 // Alternatives.  Of the first tile each thread takes its largest value; the
 // ceil(top / 8)-th largest of those in every warp bounds from below what at least top
 // values of the tile reach, so that only values at or above the least of the 8 bounds
-// are candidates: some fifty of 3072 or 6144.  They go to a list in shared memory, as keys that
-// no two entries share: the value's bits in an order of their own, then the token's
-// complement, so that among equals the lowest token comes first.  Whenever the list
-// has grown to 256 it is cut to its top largest, and the last of them is the new bound,
-// which fewer values of each later tile reach.  A tile with more candidates than the
+// are candidates: some fifty of 4096 or 8192.  They go to a list in shared memory, as
+// keys that no two entries share: the value's bits in an order of their own, then the
+// token's complement, so that among equals the lowest token comes first.  After the
+// first tile, and whenever the list has grown to 64, it is cut to its top largest, and
+// the last of them is the new bound: of the i-th tile some top / i values reach it.  A tile with more candidates than the
 // list has room for (rows of one value) is searched key by key instead.  A key's rank
 // is the number of larger ones.
 //
@@ -34,10 +34,10 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
-constexpr int kPieces = 3;      // 16-byte pieces of a tile a thread has
+constexpr int kPieces = 4;      // 16-byte pieces of a tile a thread has
 constexpr int kAhead = 2;       // tiles under way
 constexpr int kList = 1024;     // candidates
-constexpr int kCut = 256;       // so many are cut to the top ones
+constexpr int kCut = 64;        // so many are cut to the top ones
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -91,9 +91,9 @@ __device__ __forceinline__ float one(const void* row, int64_t i) {
 }
 
 struct Lists {
-  uint4 ring[kAhead + 1][kPieces][kThreads];
-  unsigned long long list[kList], best[kMaxTop], warp_best[kWarps];
-  int count, before;  // entries; and of earlier tiles
+  uint4 ring[kAhead][kPieces][kThreads];
+  unsigned long long list[kList + kMaxTop], best[kMaxTop], warp_best[kWarps];
+  int count;
   uint32_t bound[kWarps];
   Stats stats[kWarps];
 };
@@ -156,8 +156,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   const uint4* body = reinterpret_cast<const uint4*>(row + head * kSize);
   const int tiles = (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
   auto piece_of = [&](int tile, int j) { return (tile * kPieces + j) * kThreads + tid; };
+  auto whole = [&](int tile) { return (tile + 1) * (kPieces * kThreads) <= pieces; };
   auto fetch = [&](int tile, int slot) {  // (one group for every tile, of nothing behind the last)
-    if (tile < tiles) {
+    if (whole(tile)) {
+      const uint4* from = body + piece_of(tile, 0);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) cp_async16(&s.ring[slot][j][tid], from + j * kThreads);
+    } else if (tile < tiles) {
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
         if (piece_of(tile, j) < pieces) cp_async16(&s.ring[slot][j][tid], body + piece_of(tile, j));
@@ -185,23 +190,25 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   cluster_arrive();  // rank 0 has started before the others write to it
   const float x_token = one<DT>(row, token);
 
-  if (tid == 0) s.count = s.before = 0;
+  if (tid == 0) s.count = 0;
   if (TOP) __syncthreads();
   Stats mine{-INFINITY, 0.f, 0.f};
   uint32_t least = kOrderedLowest;  // what a candidate has to reach
   int slot = 0;
   for (int tile = rank; tile < tiles || tile == 0; tile += ranks) {
-    fetch(tile + kAhead * ranks, slot + kAhead > kAhead ? slot - 1 : kAhead);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     uint4 w[kPieces];
     // a missing piece holds -inf
     constexpr uint32_t kNone = DT == KDA_DTYPE_F32 ? 0xff800000u : DT == KDA_DTYPE_F16 ? 0xfc00fc00u : 0xff80ff80u;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      w[j] = make_uint4(kNone, kNone, kNone, kNone);
-      if (piece_of(tile, j) < pieces) w[j] = s.ring[slot][j][tid];
+    for (int j = 0; j < kPieces; ++j) w[j] = s.ring[slot][j][tid];
+    fetch(tile + kAhead * ranks, slot);
+    slot ^= 1;
+    if (!whole(tile)) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        if (piece_of(tile, j) >= pieces) w[j] = make_uint4(kNone, kNone, kNone, kNone);
     }
-    slot = slot == kAhead ? 0 : slot + 1;
     // the single entries in front with the first tile, those behind with rank 0's last
     // one, so that a CTA's tokens come in order (but within a tile)
     int single = -1;
@@ -225,21 +232,29 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
       const float down = fmaxf(mine.m - m, -1e4f), scale = exp2_(down * kLog2e);
       float2 z = make_float2(mine.z * scale, 0.f), t = make_float2((mine.t + mine.z * down) * scale, 0.f);
       auto add = [&](float2 v) {
-        // -inf and NaN: no weight; +inf: that of the largest number
         const float2 d = add2(v, make_float2(-m, -m));
-        const float2 c = make_float2(fminf(fmaxf(d.x, -1e4f), 0.f), fminf(fmaxf(d.y, -1e4f), 0.f));
+        const float2 c = make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f));  // -inf and NaN: no weight
         const float2 y = mul2(c, make_float2(kLog2e, kLog2e));
         const float2 p = make_float2(exp2_(y.x), exp2_(y.y));
         z = add2(z, p);
         t = fma2(c, p, t);
       };
+      if (big < INFINITY) {
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        widen<DT>(w[j], x);
+        for (int j = 0; j < kPieces; ++j) {
+          widen<DT>(w[j], x);
 #pragma unroll
-        for (int e = 0; e < kEach / 2; ++e) add(x[e]);
+          for (int e = 0; e < kEach / 2; ++e) add(x[e]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          widen<DT>(w[j], x);
+#pragma unroll
+          for (int e = 0; e < kEach / 2; ++e) add(make_float2(no_infinity(x[e].x), no_infinity(x[e].y)));
+        }
       }
-      if (single >= 0) add(make_float2(x_single, -INFINITY));
+      if (single >= 0) add(make_float2(no_infinity(x_single), -INFINITY));
       mine = Stats{m, z.x + z.y, t.x + t.y};
     }
     if constexpr (TOP) {
@@ -272,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         full = bound >= least;
         if (full) least = bound;
       }
-      bool cut = false;
+      bool cut = tile == rank && tile + ranks < tiles;  // a better bound for the tiles to come
       if (max(u, ordered(fmaxf(fminf(x_single, FLT_MAX), -INFINITY))) >= least) {
         const float bar = unordered(least);
         each([&](float v, int at) {
@@ -287,8 +302,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
       if (__syncthreads_or(cut)) {
         const int n = s.count;
         if (n > kList) {  // too many at once: the tile's largest keys one by one
-          // what is listed of earlier tiles stays; what this one listed is not the lot, and goes
-          const int before = s.before;
+          // What is listed of this tile, whose tokens are higher than earlier ones', is not
+          // the lot, and goes.
+          const uint32_t first = tile == 0 ? 0 : head + tile * (kPieces * kThreads * kEach);
+          for (int i = tid; i < kList; i += kThreads)
+            if (~(uint32_t)s.list[i] >= first) s.list[i] = 0;
           __syncthreads();
           unsigned long long last = ~0ull;
           int found = 0;
@@ -311,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
             for (int i = 1; i < kWarps; ++i) k = s.warp_best[i] > k ? s.warp_best[i] : k;
             __syncthreads();
             if (k == 0) break;
-            if (tid == 0) s.list[before + found] = k;
+            if (tid == 0) s.list[kList + found] = k;
             last = k;
           }
-          if (tid == 0) s.count = before + found;
+          if (tid == 0) s.count = kList + found;
           __syncthreads();
         }
         const int have = s.count;
@@ -322,12 +340,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         if (tid < kMaxTop) s.list[tid] = s.best[tid];
         const unsigned long long kth = s.best[top - 1];
         if (kth) least = max(least, (uint32_t)(kth >> 32) + 1);
-        if (tid == 0) s.count = s.before = min(have, top);
+        if (tid == 0) s.count = min(have, top);
         __syncthreads();
-      } else if (tid == 0) {
-        s.before = s.count;  // every entry of this tile is there; none of the next one yet
       }
-      __syncthreads();
     }
   }
   cp_async_wait_all();
