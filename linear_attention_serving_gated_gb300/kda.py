@@ -766,15 +766,16 @@ def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_s
     HK, HVV = d.H * d.K, d.HV * d.V
     slots = _pool_slots(d, state_pool)
     if workspace is None:
-        workspace = _new(max(int(lib.kda_lin_prefill_workspace_size(d, n, T)), 1), torch.uint8, q.device, stream)
+        need = lib.kda_lin_prefill_workspace_size(d, n, T)
+        workspace = _new(need, torch.uint8, q.device, stream) if need else None
     st = lib.kda_lin_prefill(
         d, gate.c(d), _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
         _arg(v, t16, T * HVV, "v", "[T, HV, V]"), _lin_gate_rows(d, gate, a, gate_rows), gate_rows,
         _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), slots,
         _arg(state_idx, torch.int32, n, "state_idx", "[num_seqs]"),
         _opt(cu_seqlens, torch.int32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
-        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _err(err_flag), _cur(stream))
+        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _err(err_flag), _cur(stream))
     if st:
         _check(st, "kda_lin_prefill")
 
