@@ -38,6 +38,7 @@ constexpr int kPieces = 4;      // 16-byte pieces of a tile a thread has
 constexpr int kAhead = 2;       // tiles under way
 constexpr int kList = 1024;     // candidates
 constexpr int kCut = 64;        // so many are cut to the top ones
+constexpr int kBatch = 4;       // tiles between two looks at the list
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -75,12 +76,20 @@ __device__ __forceinline__ unsigned long long key_of(float x, int token) {
 }
 constexpr uint32_t kOrderedLowest = 0x00800000u;  // of -FLT_MAX: what is below is -inf, and no alternative
 
-__device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
-  const float m = fmaxf(a.m, b.m);
+// Of the lanes' parts together, in every lane.
+__device__ __forceinline__ Stats warp_join(Stats a) {
+  float m = a.m;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   if (m == -INFINITY) return Stats{m, 0.f, 0.f};
-  // differences of -inf are of sums of nothing
-  const float da = fmaxf(a.m - m, -1e4f), db = fmaxf(b.m - m, -1e4f), ea = expf(da), eb = expf(db);
-  return Stats{m, a.z * ea + b.z * eb, (a.t + a.z * da) * ea + (b.t + b.z * db) * eb};
+  const float down = fmaxf(a.m - m, -1e4f), e = expf(down);  // (a part of nothing: -inf less m)
+  float z = a.z * e, t = (a.t + a.z * down) * e;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    z += __shfl_xor_sync(0xffffffffu, z, d);
+    t += __shfl_xor_sync(0xffffffffu, t, d);
+  }
+  return Stats{m, z, t};
 }
 
 template <int DT>
@@ -192,9 +201,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
 
   if (tid == 0) s.count = 0;
   if (TOP) __syncthreads();
-  Stats mine{-INFINITY, 0.f, 0.f};
+  float top_x = -INFINITY;  // the largest value so far
+  float2 z = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
   uint32_t least = kOrderedLowest;  // what a candidate has to reach
-  int slot = 0;
+  int slot = 0, batch = rank;  // the first tile since the last look at the list
+  bool cut = false;
   for (int tile = rank; tile < tiles || tile == 0; tile += ranks) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     uint4 w[kPieces];
@@ -227,12 +238,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
       for (int e = 0; e < kEach / 2; ++e) big = fmaxf(big, fmaxf(x[e].x, x[e].y));  // NaN is left out
     }
     // +inf counts as the largest number
-    const float m = fmaxf(mine.m, fminf(fmaxf(big, x_single), FLT_MAX));
+    const float m = fmaxf(top_x, fminf(fmaxf(big, x_single), FLT_MAX));
+    if (m > top_x) {
+      const float down = fmaxf(top_x - m, -1e4f), scale = exp2_(down * kLog2e);
+      const float2 down2 = make_float2(down, down), scale2 = make_float2(scale, scale);
+      t = mul2(fma2(z, down2, t), scale2);
+      z = mul2(z, scale2);
+      top_x = m;
+    }
     if (m > -INFINITY) {
-      const float down = fmaxf(mine.m - m, -1e4f), scale = exp2_(down * kLog2e);
-      float2 z = make_float2(mine.z * scale, 0.f), t = make_float2((mine.t + mine.z * down) * scale, 0.f);
+      const float2 minus = make_float2(-m, -m);
       auto add = [&](float2 v) {
-        const float2 d = add2(v, make_float2(-m, -m));
+        const float2 d = add2(v, minus);
         const float2 c = make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f));  // -inf and NaN: no weight
         const float2 y = mul2(c, make_float2(kLog2e, kLog2e));
         const float2 p = make_float2(exp2_(y.x), exp2_(y.y));
@@ -255,21 +272,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         }
       }
       if (single >= 0) add(make_float2(no_infinity(x_single), -INFINITY));
-      mine = Stats{m, z.x + z.y, t.x + t.y};
     }
     if constexpr (TOP) {
-      auto token_at = [&](int j, int e) { return head + piece_of(tile, j) * kEach + e; };
-      auto each = [&](auto&& f) {  // every entry of the tile, as a number or -inf or NaN
+      auto each = [&](const uint4 (&w)[kPieces], int tile, auto&& f) {  // entries, as numbers or -inf or NaN
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
           widen<DT>(w[j], x);
 #pragma unroll
           for (int e = 0; e < kEach / 2; ++e) {
-            f(no_infinity(x[e].x), token_at(j, 2 * e));
-            f(no_infinity(x[e].y), token_at(j, 2 * e + 1));
+            const int at = head + piece_of(tile, j) * kEach + 2 * e;
+            f(no_infinity(x[e].x), at);
+            f(no_infinity(x[e].y), at + 1);
           }
         }
-        if (single >= 0) f(no_infinity(x_single), single);
       };
       const uint32_t u = ordered(fminf(big, FLT_MAX));
       bool full = false;  // `top` values reach the bound
@@ -287,24 +302,31 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         full = bound >= least;
         if (full) least = bound;
       }
-      bool cut = tile == rank && tile + ranks < tiles;  // a better bound for the tiles to come
+      cut |= tile == rank && tile + ranks < tiles;  // a better bound for the tiles to come
       if (max(u, ordered(fmaxf(fminf(x_single, FLT_MAX), -INFINITY))) >= least) {
         const float bar = unordered(least);
-        each([&](float v, int at) {
+        auto list = [&](float v, int at) {
           if (v >= bar) {
             const int i = atomicAdd(&s.count, 1);
             if (i < kList) s.list[i] = key_of(v, at);
             cut |= i >= kCut;
           }
-        });
+        };
+        each(w, tile, list);
+        if (single >= 0) list(no_infinity(x_single), single);
       }
       if (full) ++least;  // among equals the lower tokens, which are listed, come first
+      const bool look = tile == rank || (tile - batch) / ranks == kBatch - 1 || tile + ranks >= tiles;
+      if (!look) continue;
+      const int from = batch;
+      batch = tile + ranks;
       if (__syncthreads_or(cut)) {
+        cut = false;
         const int n = s.count;
-        if (n > kList) {  // too many at once: the tile's largest keys one by one
-          // What is listed of this tile, whose tokens are higher than earlier ones', is not
+        if (n > kList) {  // too many at once: the batch's largest keys one by one
+          // What is listed of this batch, whose tokens are higher than earlier ones', is not
           // the lot, and goes.
-          const uint32_t first = tile == 0 ? 0 : head + tile * (kPieces * kThreads * kEach);
+          const uint32_t first = from == 0 ? 0 : head + from * (kPieces * kThreads * kEach);
           for (int i = tid; i < kList; i += kThreads)
             if (~(uint32_t)s.list[i] >= first) s.list[i] = 0;
           __syncthreads();
@@ -312,12 +334,22 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
           int found = 0;
           for (; found < top; ++found) {
             unsigned long long k = 0;
-            each([&](float v, int at) {
+            auto best = [&](float v, int at) {
               if (v >= -FLT_MAX) {
                 const unsigned long long key = key_of(v, at);
                 if (key < last && key > k) k = key;
               }
-            });
+            };
+#pragma unroll 1
+            for (int t = from; t <= tile; t += ranks) {
+              uint4 v[kPieces];
+#pragma unroll
+              for (int j = 0; j < kPieces; ++j)
+                v[j] = piece_of(t, j) < pieces ? __ldg(body + piece_of(t, j)) : make_uint4(kNone, kNone, kNone, kNone);
+              each(v, t, best);
+            }
+            // (a single entry of an earlier tile of the batch: the first tile is one of its own)
+            if (single >= 0) best(no_infinity(x_single), single);
 #pragma unroll
             for (int d = 16; d; d >>= 1) {
               const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
@@ -347,28 +379,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   }
   cp_async_wait_all();
 
-  // the CTA's part of the row, then the row
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const Stats o{__shfl_xor_sync(0xffffffffu, mine.m, d), __shfl_xor_sync(0xffffffffu, mine.z, d),
-                  __shfl_xor_sync(0xffffffffu, mine.t, d)};
-    mine = join(mine, o);
+  // the warp's part of the row, then the CTA's, then the row
+  {
+    const Stats mine = warp_join(Stats{top_x, z.x + z.y, t.x + t.y});
+    if (lane == 0) s.stats[warp] = mine;
   }
-  if (lane == 0) s.stats[warp] = mine;
   __syncthreads();
   if constexpr (TOP) rank_list(s, s.count, top);
   cluster_wait();
   Joined* to = cluster.map_shared_rank(&joined, 0);
   if (TOP && tid < kMaxTop) to->keys[rank][tid] = s.best[tid];
-  if (tid == 0) {
-    Stats all = s.stats[0];
-    for (int i = 1; i < kWarps; ++i) all = join(all, s.stats[i]);
-    to->stats[rank] = all;
+  if (warp == 0) {
+    const Stats all = warp_join(lane < kWarps ? s.stats[lane] : Stats{-INFINITY, 0.f, 0.f});
+    if (lane == 0) to->stats[rank] = all;
   }
   cluster.sync();
   if (rank != 0) return;
-  Stats all = joined.stats[0];
-  for (int i = 1; i < ranks; ++i) all = join(all, joined.stats[i]);
+  const Stats all = warp_join(lane < ranks ? joined.stats[lane] : Stats{-INFINITY, 0.f, 0.f});
   const float log_z = logf(all.z);
   const bool some = all.m > -INFINITY;
   auto log_p = [&](float x) { return some && x >= -FLT_MAX ? (fminf(x, FLT_MAX) - all.m) - log_z : -INFINITY; };
