@@ -13,10 +13,10 @@
 // values of the tile reach, so that only values at or above the least of the 8 bounds
 // are candidates: some fifty of 4096 or 8192.  They go to a list in shared memory, as
 // keys that no two entries share: the value's bits in an order of their own, then the
-// token's complement, so that among equals the lowest token comes first.  After the
-// first tile, and whenever the list has grown to 64, it is cut to its top largest, and
-// the last of them is the new bound: of the i-th tile some top / i values reach it.  A tile with more candidates than the
-// list has room for (rows of one value) is searched key by key instead.  A key's rank
+// token's complement, so that among equals the lowest token comes first.  After 1, 2, 4,
+// 8 .. tiles the list is cut to its top largest, and the last of them is the new bound,
+// which some top values reach until the next time.  Tiles with more candidates than the
+// list has room for (rows of one value) are searched key by key instead.  A key's rank
 // is the number of larger ones.
 //
 // A row is split over the CTAs of a cluster where there are few rows; rank 0 joins
@@ -37,8 +37,6 @@ constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
 constexpr int kPieces = 4;      // 16-byte pieces of a tile a thread has
 constexpr int kAhead = 2;       // tiles under way
 constexpr int kList = 1024;     // candidates
-constexpr int kCut = 64;        // so many are cut to the top ones
-constexpr int kBatch = 4;       // tiles between two looks at the list
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -204,8 +202,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   float top_x = -INFINITY;  // the largest value so far
   float2 z = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
   uint32_t least = kOrderedLowest;  // what a candidate has to reach
-  int slot = 0, batch = rank;  // the first tile since the last look at the list
-  bool cut = false;
+  int slot = 0, batch = rank, seen = 0;  // the first tile since the last look at the list; tiles so far
   for (int tile = rank; tile < tiles || tile == 0; tile += ranks) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     uint4 w[kPieces];
@@ -230,12 +227,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
       if (single >= 0) x_single = one<DT>(row, single);
     }
     float2 x[kEach / 2];
-    float big = -INFINITY;
+    float big = -INFINITY, piece_big[kPieces];
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       widen<DT>(w[j], x);
+      piece_big[j] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < kEach / 2; ++e) big = fmaxf(big, fmaxf(x[e].x, x[e].y));  // NaN is left out
+      for (int e = 0; e < kEach / 2; ++e) piece_big[j] = fmaxf(piece_big[j], fmaxf(x[e].x, x[e].y));  // NaN is left out
+      big = fmaxf(big, piece_big[j]);
     }
     // +inf counts as the largest number
     const float m = fmaxf(top_x, fminf(fmaxf(big, x_single), FLT_MAX));
@@ -274,16 +273,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
       if (single >= 0) add(make_float2(no_infinity(x_single), -INFINITY));
     }
     if constexpr (TOP) {
-      auto each = [&](const uint4 (&w)[kPieces], int tile, auto&& f) {  // entries, as numbers or -inf or NaN
+      auto each = [&](uint4 w, int piece, auto&& f) {  // a piece's entries
+        widen<DT>(w, x);
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-          widen<DT>(w[j], x);
-#pragma unroll
-          for (int e = 0; e < kEach / 2; ++e) {
-            const int at = head + piece_of(tile, j) * kEach + 2 * e;
-            f(no_infinity(x[e].x), at);
-            f(no_infinity(x[e].y), at + 1);
-          }
+        for (int e = 0; e < kEach / 2; ++e) {
+          f(x[e].x, head + piece * kEach + 2 * e);
+          f(x[e].y, head + piece * kEach + 2 * e + 1);
         }
       };
       const uint32_t u = ordered(fminf(big, FLT_MAX));
@@ -302,30 +297,30 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         full = bound >= least;
         if (full) least = bound;
       }
-      cut |= tile == rank && tile + ranks < tiles;  // a better bound for the tiles to come
       if (max(u, ordered(fmaxf(fminf(x_single, FLT_MAX), -INFINITY))) >= least) {
         const float bar = unordered(least);
         auto list = [&](float v, int at) {
           if (v >= bar) {
             const int i = atomicAdd(&s.count, 1);
-            if (i < kList) s.list[i] = key_of(v, at);
-            cut |= i >= kCut;
+            if (i < kList) s.list[i] = key_of(no_infinity(v), at);
           }
         };
-        each(w, tile, list);
-        if (single >= 0) list(no_infinity(x_single), single);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+          if (piece_big[j] >= bar) each(w[j], piece_of(tile, j), list);
+        if (single >= 0) list(x_single, single);
       }
       if (full) ++least;  // among equals the lower tokens, which are listed, come first
-      const bool look = tile == rank || (tile - batch) / ranks == kBatch - 1 || tile + ranks >= tiles;
-      if (!look) continue;
-      const int from = batch;
-      batch = tile + ranks;
-      if (__syncthreads_or(cut)) {
-        cut = false;
+      ++seen;
+      if ((seen & (seen - 1)) == 0 || tile + ranks >= tiles) {
+        const int from = batch;
+        batch = tile + ranks;
+        __syncthreads();
         const int n = s.count;
-        if (n > kList) {  // too many at once: the batch's largest keys one by one
-          // What is listed of this batch, whose tokens are higher than earlier ones', is not
-          // the lot, and goes.
+        __syncthreads();
+        if (n > kList) {  // too many: the largest keys of the tiles since, one by one
+          // What is listed of them, whose tokens are higher than earlier ones', is not the
+          // lot, and goes.
           const uint32_t first = from == 0 ? 0 : head + from * (kPieces * kThreads * kEach);
           for (int i = tid; i < kList; i += kThreads)
             if (~(uint32_t)s.list[i] >= first) s.list[i] = 0;
@@ -336,20 +331,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
             unsigned long long k = 0;
             auto best = [&](float v, int at) {
               if (v >= -FLT_MAX) {
-                const unsigned long long key = key_of(v, at);
+                const unsigned long long key = key_of(no_infinity(v), at);
                 if (key < last && key > k) k = key;
               }
             };
 #pragma unroll 1
-            for (int t = from; t <= tile; t += ranks) {
-              uint4 v[kPieces];
-#pragma unroll
+            for (int t = from; t <= tile; t += ranks)
+#pragma unroll 1
               for (int j = 0; j < kPieces; ++j)
-                v[j] = piece_of(t, j) < pieces ? __ldg(body + piece_of(t, j)) : make_uint4(kNone, kNone, kNone, kNone);
-              each(v, t, best);
-            }
-            // (a single entry of an earlier tile of the batch: the first tile is one of its own)
-            if (single >= 0) best(no_infinity(x_single), single);
+                if (piece_of(t, j) < pieces) each(__ldg(body + piece_of(t, j)), piece_of(t, j), best);
+            // the single entries: of the first tile, or of the last one
+            if (rank == 0 && from == 0 && tid < head) best(one<DT>(row, tid), tid);
+            if (single >= head) best(x_single, single);
 #pragma unroll
             for (int d = 16; d; d >>= 1) {
               const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
