@@ -57,7 +57,7 @@ struct LinPrefillArgs {
   const int32_t* state_idx;
   const int32_t* cu_seqlens;
   int num_seqs;
-  int64_t total_tokens;
+  int64_t total_tokens, each;  // tokens; of a sequence, without cu_seqlens
   kda_bf16* o;
   // tokens of a segment, multiples of 64: where no sequence is longer than even_most,
   // and otherwise; sequences of at most uncut tokens then stay in one piece
@@ -283,7 +283,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
 }
 
 __device__ __forceinline__ int64_t seq_start(const LinPrefillArgs& a, int n) {
-  return a.cu_seqlens ? (int64_t)a.cu_seqlens[n] : a.total_tokens / a.num_seqs * n;
+  return a.cu_seqlens ? (int64_t)a.cu_seqlens[n] : a.each * n;
 }
 // Tokens of sequence n, -1 where its bounds are not those of a sequence.
 __device__ __forceinline__ int seq_len(const LinPrefillArgs& a, int n) {
@@ -317,11 +317,30 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
   int most = 0, uncut = 0;
 #pragma unroll 1
   for (int m = lane; m < seqs; m += 32) most = max(most, seq_len(args, m));
-  if (__reduce_max_sync(0xffffffffu, most) > args.even_most) {
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (most > args.even_most) {
     L = args.seg_ragged;
     uncut = args.uncut;
   }
+  r.tokens = L;
   int base = 0;
+  if (most <= L) {  // every sequence is one segment: the id-th that has tokens
+#pragma unroll 1
+    for (int n0 = 0; n0 < seqs; n0 += 32) {
+      const int len = n0 + lane < seqs ? seq_len(args, n0 + lane) : 0;
+      const unsigned some = __ballot_sync(0xffffffffu, len > 0);
+      if (base + __popc(some) > id) {
+        const int src = __fns(some, 0, id - base + 1);
+        r.n = n0 + src;
+        r.len = __shfl_sync(0xffffffffu, len, src);
+        r.count = 1;
+        r.t0 = seq_start(args, r.n);
+        break;
+      }
+      base += __popc(some);
+    }
+    return r;
+  }
 #pragma unroll 1
   for (int turn = uncut ? 0 : 1; turn < 3 && r.n < 0; ++turn) {
     int records = 0;
@@ -351,7 +370,6 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
       records += __shfl_sync(0xffffffffu, run_all, 31);
     }
   }
-  r.tokens = L;
   return r;
 }
 
@@ -1103,6 +1121,7 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.cu_seqlens = cu_seqlens;
   args.num_seqs = num_seqs;
   args.total_tokens = total_tokens;
+  args.each = total_tokens / num_seqs;
   args.o = o;
   const Segments c = cut(dims, num_seqs, total_tokens, kSms);
   args.seg_even = c.even;

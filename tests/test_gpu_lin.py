@@ -50,7 +50,7 @@ def run(c, x, **kw):
     return o, up["pool"]
 
 
-def compare(c, x, o, pool, parts=(0,)):
+def compare(c, x, o, pool, parts=(0,), others=True):
     g = so.lin_decay(len(x["q"]), lu.host(x["a"]), lu.host(x["A_log"]), lu.host(x["dt_bias"]))
     want = lu.host(x["pool"])
     for n, slot in enumerate(x["idx"].tolist()):
@@ -62,6 +62,8 @@ def compare(c, x, o, pool, parts=(0,)):
         o_b, s_b = lu.bounds(want[slot], q, k, v, g[s], SCALE, c["norm"], c["dtype"], parts=parts)
         lu.check(f"o of sequence {n}", o[s], o_ref, o_b, c["dtype"])
         lu.check(f"state of sequence {n}", pool[slot], states[-1], s_b)
+    if not others:
+        return
     rest = [s for s in range(len(want)) if s not in [i for i, L in zip(x["idx"].tolist(), c["lengths"]) if L]]
     assert torch.equal(pool[rest].cpu(), x["pool"][rest]), "a slot of no sequence"
 
@@ -75,6 +77,29 @@ def test_prefill(i):
     torch.cuda.synchronize()
     assert err.item() == 0
     compare(c, x, o, pool)
+
+
+def test_prefill_of_many_sequences():
+    """More sequences than a warp has lanes, of 0 to 9 tokens, and with two long ones
+    among them; each against itself alone."""
+    gen = torch.Generator().manual_seed(40)
+    lengths = torch.randint(0, 10, (150,), generator=gen).tolist()
+    for more in ((), (700, 1500)):
+        lengths[60:60 + len(more)] = more
+        c = case(lengths, H=2, gate="fixed")
+        x = draw(c, 41)
+        err = torch.zeros(1, dtype=i32, device="cuda")
+        o, pool = run(c, x, err_flag=err)
+        assert err.item() == 0
+        some = [0, 1, 31, 32, 60, 61, 62, 63, 64, 100, 149]
+        for n in some:
+            s = slice(int(x["cu"][n]), int(x["cu"][n + 1]))
+            if s.start == s.stop:
+                continue
+            y = dict(x, cu=torch.tensor([0, lengths[n]], dtype=i32), idx=x["idx"][n:n + 1], **{k: x[k][s] for k in "qkv"})
+            compare(dict(c, lengths=[lengths[n]]), y, o[s], pool, others=False)
+        rest = [k for k in range(len(pool)) if k not in x["idx"].tolist()]
+        assert torch.equal(pool[rest].cpu(), x["pool"][rest])
 
 
 def test_prefill_fixed_layout_equals_cu_seqlens():
