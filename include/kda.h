@@ -552,7 +552,8 @@ kda_status kda_lin_verify_tree(kda_dims dims, kda_scalar_gate gate, const kda_bf
  * and their top alternatives: of rows of logits x, with z = sum_j exp(x_j),
  *   logprobs[r]  = x[tokens[r]] - log z
  *   entropy[r]   = - sum_j p_j log p_j,  p_j = exp(x_j) / z     (nats)
- * Sums are FP32 (32 terms one after the other, then rescaled partial sums).
+ * Sums are FP32, of the largest logit's 1 apart, so that a log probability near 0 is as
+ * exact as any other.
  *   logits        `vocab` elements a row, rows logits_stride elements apart, of
  *                 type KDA_DTYPE_F32, KDA_DTYPE_BF16 or KDA_DTYPE_F16.  -inf (a
  *                 masked token) and NaN have no probability, +inf counts as the

@@ -1,12 +1,20 @@
 // kda_logprobs.cu -- log probabilities of given tokens, with the entropy of their
 // distributions and their top alternatives.
 //
-// Of a row's logits x, with m the largest and z = sum exp(x - m):
-//   log p_j = x_j - m - log z,   entropy = log z - sum (x - m) exp(x - m) / z.
+// Of a row's logits x, with m the largest and z = sum exp(x - m) = 1 + r:
+//   log p_j = x_j - m - log(1 + r),   entropy = log(1 + r) - sum (x - m) exp(x - m) / (1 + r).
 // One pass over the row, in tiles of 16 KiB.  A thread copies its own pieces of a tile
 // to shared memory a tile ahead and reads them back itself, so that no barrier stands
 // between a load and its use; it keeps m, z and the sum of the entropy of what it has
 // read, rescaled where m grows.
+//
+// Precision.  r is kept without the 1 of the largest value, so that the log probability
+// of a token that is all but certain, log(1 + r) with a small r, is as exact as any
+// other.  (With 1 + r in FP32 it is off by 2^-23 at best.)  For that a thread sums the
+// tile with its largest value apart from the others, and where a warp's r is small the
+// entries that its largest value came with are summed once more, without it.  (Counting
+// entries equal to m as they come took a sixth more time.)  What is left is 2^-22 of an
+// exponential and the rounding of x - m in units of ln 2, 2^-24 |x - m|.
 //
 // Alternatives.  Of the first tile each thread takes its largest value; the
 // ceil(top / 8)-th largest of those in every warp bounds from below what at least top
@@ -52,7 +60,7 @@ struct LogprobsArgs {
 };
 
 struct Stats {
-  float m, z, t;  // largest value, sum exp(x - m), sum (x - m) exp(x - m)
+  float m, r, t;  // largest value, sum exp(x - m) - 1, sum (x - m) exp(x - m)
 };
 
 // Rank 0's: what the CTAs of a cluster leave for it.
@@ -81,13 +89,14 @@ __device__ __forceinline__ Stats warp_join(Stats a) {
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   if (m == -INFINITY) return Stats{m, 0.f, 0.f};
   const float down = fmaxf(a.m - m, -1e4f), e = expf(down);  // (a part of nothing: -inf less m)
-  float z = a.z * e, t = (a.t + a.z * down) * e;
+  const bool first = __ffs(__ballot_sync(0xffffffffu, a.m == m)) - 1 == (threadIdx.x & 31);
+  float r = first ? a.r : (1.f + a.r) * e, t = (a.t + (1.f + a.r) * down) * e;
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
-    z += __shfl_xor_sync(0xffffffffu, z, d);
+    r += __shfl_xor_sync(0xffffffffu, r, d);
     t += __shfl_xor_sync(0xffffffffu, t, d);
   }
-  return Stats{m, z, t};
+  return Stats{m, r, t};
 }
 
 template <int DT>
@@ -164,6 +173,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   const int tiles = (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
   auto piece_of = [&](int tile, int j) { return (tile * kPieces + j) * kThreads + tid; };
   auto whole = [&](int tile) { return (tile + 1) * (kPieces * kThreads) <= pieces; };
+  // the single entries in front with the first tile, those behind with rank 0's last one,
+  // so that a CTA's tokens come in order (but within a tile)
+  auto single_of = [&](int tile) {
+    if (rank != 0) return -1;
+    if (tile + ranks >= tiles && tid >= 32 && tid < 32 + tail) return args.vocab - tail + tid - 32;
+    return tile == 0 && tid < head ? tid : -1;
+  };
   auto fetch = [&](int tile, int slot) {  // (one group for every tile, of nothing behind the last)
     if (whole(tile)) {
       const uint4* from = body + piece_of(tile, 0);
@@ -199,8 +215,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
 
   if (tid == 0) s.count = 0;
   if (TOP) __syncthreads();
-  float top_x = -INFINITY;  // the largest value so far
-  float2 z = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+  float top_x = -INFINITY;  // the largest value so far,
+  int top_tile = 0;         // the tile that it came with,
+  float top_z = 0.f;        // that tile's part of z
+  float z = 0.f;            // and the others'
+  float2 t = make_float2(0.f, 0.f);
   uint32_t least = kOrderedLowest;  // what a candidate has to reach
   int slot = 0, batch = rank, seen = 0;  // the first tile since the last look at the list; tiles so far
   for (int tile = rank; tile < tiles || tile == 0; tile += ranks) {
@@ -217,15 +236,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
       for (int j = 0; j < kPieces; ++j)
         if (piece_of(tile, j) >= pieces) w[j] = make_uint4(kNone, kNone, kNone, kNone);
     }
-    // the single entries in front with the first tile, those behind with rank 0's last
-    // one, so that a CTA's tokens come in order (but within a tile)
-    int single = -1;
-    float x_single = -INFINITY;
-    if (rank == 0) {
-      if (tile == 0 && tid < head) single = tid;
-      if (tile + ranks >= tiles && tid >= 32 && tid < 32 + tail) single = args.vocab - tail + tid - 32;
-      if (single >= 0) x_single = one<DT>(row, single);
-    }
+    const int single = single_of(tile);
+    const float x_single = single >= 0 ? one<DT>(row, single) : -INFINITY;
     float2 x[kEach / 2];
     float big = -INFINITY, piece_big[kPieces];
 #pragma unroll
@@ -238,21 +250,24 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     }
     // +inf counts as the largest number
     const float m = fmaxf(top_x, fminf(fmaxf(big, x_single), FLT_MAX));
-    if (m > top_x) {
+    const bool fresh = m > top_x;
+    if (fresh) {
       const float down = fmaxf(top_x - m, -1e4f), scale = exp2_(down * kLog2e);
-      const float2 down2 = make_float2(down, down), scale2 = make_float2(scale, scale);
-      t = mul2(fma2(z, down2, t), scale2);
-      z = mul2(z, scale2);
+      z += top_z;
+      t = make_float2(fmaf(z, down, t.x) * scale, t.y * scale);
+      z *= scale;
       top_x = m;
+      top_tile = tile;
     }
     if (m > -INFINITY) {
       const float2 minus = make_float2(-m, -m);
+      float2 sum = make_float2(0.f, 0.f);
       auto add = [&](float2 v) {
         const float2 d = add2(v, minus);
         const float2 c = make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f));  // -inf and NaN: no weight
         const float2 y = mul2(c, make_float2(kLog2e, kLog2e));
         const float2 p = make_float2(exp2_(y.x), exp2_(y.y));
-        z = add2(z, p);
+        sum = add2(sum, p);
         t = fma2(c, p, t);
       };
       if (big < INFINITY) {
@@ -271,6 +286,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         }
       }
       if (single >= 0) add(make_float2(no_infinity(x_single), -INFINITY));
+      const float part = sum.x + sum.y;
+      if (fresh) top_z = part; else z += part;
     }
     if constexpr (TOP) {
       auto each = [&](uint4 w, int piece, auto&& f) {  // a piece's entries
@@ -374,8 +391,40 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
 
   // the warp's part of the row, then the CTA's, then the row
   {
-    const Stats mine = warp_join(Stats{top_x, z.x + z.y, t.x + t.y});
-    if (lane == 0) s.stats[warp] = mine;
+    float m = top_x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const int most = __ffs(__ballot_sync(0xffffffffu, top_x == m)) - 1;
+    const float down = fmaxf(top_x - m, -1e4f), e = expf(down);
+    float r = lane == most ? z : (z + top_z) * e, all_t = (t.x + t.y + (z + top_z) * down) * e;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      r += __shfl_xor_sync(0xffffffffu, r, d);
+      all_t += __shfl_xor_sync(0xffffffffu, all_t, d);
+    }
+    float mine = __shfl_sync(0xffffffffu, top_z - 1.f, most);
+    if (m == -INFINITY) {
+      mine = r = all_t = 0.f;
+    } else if (r + mine < 0.25f) {  // a lane for each piece, one for the single entry
+      const int tile = __shfl_sync(0xffffffffu, top_tile, most), single = __shfl_sync(0xffffffffu, single_of(top_tile), most);
+      const int piece = piece_of(tile, lane) - lane + most;
+      mine = 0.f;
+      auto add = [&](float v) {
+        const float d = no_infinity(v) - m;
+        if (d != 0.f) mine += expf(fmaxf(d, -1e4f));
+      };
+      if (lane < kPieces && piece < pieces) {
+        float2 x[kEach / 2];
+        widen<DT>(__ldg(body + piece), x);
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) add(x[i].x), add(x[i].y);
+      } else if (lane == kPieces && single >= 0) {
+        add(one<DT>(row, single));
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    }
+    if (lane == 0) s.stats[warp] = Stats{m, r + mine, all_t};
   }
   __syncthreads();
   if constexpr (TOP) rank_list(s, s.count, top);
@@ -389,12 +438,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   cluster.sync();
   if (rank != 0) return;
   const Stats all = warp_join(lane < ranks ? joined.stats[lane] : Stats{-INFINITY, 0.f, 0.f});
-  const float log_z = logf(all.z);
+  const float log_z = log1pf(all.r);
   const bool some = all.m > -INFINITY;
   auto log_p = [&](float x) { return some && x >= -FLT_MAX ? (fminf(x, FLT_MAX) - all.m) - log_z : -INFINITY; };
   if (tid == 0) {
     args.logprobs[r] = log_p(x_token);
-    if (args.entropy) args.entropy[r] = some ? log_z - all.t / all.z : 0.f;
+    if (args.entropy) args.entropy[r] = some ? log_z - all.t / (1.f + all.r) : 0.f;
   }
   if constexpr (TOP) {
     static_assert(kMaxCluster * kMaxTop == kThreads, "a thread per entry");

@@ -169,3 +169,27 @@ def test_captured_and_on_another_stream():
     call(stream=st)
     torch.cuda.current_stream().wait_stream(st)
     compare(x, tokens.tolist(), 5, out)
+
+
+@pytest.mark.parametrize("vocab", [2, 9, 300, 5000])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_all_but_certain_tokens(dtype, vocab):
+    """Log probabilities and entropies near 0 are exact relative to themselves.  Logits
+    are multiples of 1/8 between -16 and 26, so differences of them are exact; in units of
+    2^-24: an exponential 4 and 42 (2^-22 of the approximation; half a unit of an argument
+    of up to 61 in units of ln 2), 24 for the sums of 20 entries a thread with the joins,
+    4 for the logarithm and the quotient: 74, below 2^-17."""
+    gen = torch.Generator().manual_seed(vocab)
+    rows = 12
+    x = -torch.randint(0, 8 * 16, (rows, vocab), generator=gen).float() / 8
+    at = torch.randint(0, vocab, (rows,), generator=gen)
+    x[torch.arange(rows), at] = 4.0 + 2 * torch.arange(rows).clamp(max=14)
+    got = run(x.to(DT[dtype]).cuda(), at, 1)
+    lp = torch.log_softmax(x.double(), -1)
+    r = torch.exp(x.double() - x.double().amax(-1, keepdim=True))
+    r[torch.arange(rows), at] = 0
+    want = -torch.log1p(r.sum(-1))
+    entropy = -(lp * lp.exp()).masked_fill(torch.nn.functional.one_hot(at, vocab).bool(), 0).sum(-1) - want * want.exp()
+    for name, g, w in (("logprobs", got[0], want), ("entropy", got[1], entropy), ("top_logprobs", got[3][:, 0], want)):
+        off = ((g.double().cpu() - w).abs() / w.abs().clamp(min=1e-30)).max().item()
+        assert off <= 2.0 ** -17, f"{name}: {off:.2e}"
