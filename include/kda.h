@@ -518,8 +518,12 @@ kda_status kda_pool_fork(kda_pages pages, uint8_t *used, int32_t *table, int tab
  * A NaN or an infinity among a token's inputs reaches the outputs of all 64
  * tokens of its chunk, and the sequence's state; other sequences it does not.
  * A sequence may be prefilled in parts, each from the state that the one before
- * left.  workspace: kda_lin_prefill_workspace_size bytes, 256-byte aligned.  The
- * first call on each device comes before capture.
+ * left.  Where cu_seqlens decreases, so that sequences overlap and have more tokens
+ * than there are, none runs.
+ *   workspace     kda_lin_prefill_workspace_size bytes, 16-byte aligned; the states of
+ *                 segments that long sequences are cut into, 64 KiB a segment and value
+ *                 head, and 0 (workspace may be NULL) where none can be cut
+ * The first call on each device comes before capture.
  */
 size_t kda_lin_prefill_workspace_size(kda_dims dims, int num_seqs, int64_t total_tokens);
 kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16 *q,

@@ -293,7 +293,8 @@ __device__ __forceinline__ int seq_len(const LinPrefillArgs& a, int n) {
   return bad ? -1 : (int)(t1 - t0);
 }
 // A CTA's segment: the s-th of `count` of sequence n (-1: none), `tokens` long but for
-// the last; `record` is the place of the sequence's first segment among all.
+// the last; `record` is the place of the sequence's first segment among those of
+// sequences in several.
 struct Segment {
   int n, s, count, record, tokens;
   int len;     // of the sequence
@@ -302,9 +303,10 @@ struct Segment {
 
 // The id-th segment: longer sequences that stay in one piece, then the whole segments of
 // the others, then what is left of those and the short ones, so that the longest start
-// first.  Every warp finds it for itself, a sequence a lane.
+// first; LOCAL: the id-th whole segment.  Every warp finds it for itself, a sequence a lane.
 // (What runs once a CTA is kept short: instructions that no cache holds yet take five
 // or more times as long as others.)
+template <bool LOCAL>
 __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int id, int lane) {
   const int seqs = args.num_seqs;
   Segment r{-1, 0, 0, 0, args.seg_even, 0, 0};
@@ -315,9 +317,17 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
     return r;
   }
   int most = 0, uncut = 0;
+  int64_t sum = 0;
 #pragma unroll 1
-  for (int m = lane; m < seqs; m += 32) most = max(most, seq_len(args, m));
+  for (int m = lane; m < seqs; m += 32) {
+    const int len = max(seq_len(args, m), 0);
+    most = max(most, len);
+    sum += len;
+  }
   most = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll 1
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (sum > args.total_tokens) return r;  // they overlap: more segments than there is room for
   if (most > args.even_most) {
     L = args.seg_ragged;
     uncut = args.uncut;
@@ -326,7 +336,7 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
   int base = 0;
   if (most <= L) {  // every sequence is one segment: the id-th that has tokens
 #pragma unroll 1
-    for (int n0 = 0; n0 < seqs; n0 += 32) {
+    for (int n0 = 0; !LOCAL && n0 < seqs; n0 += 32) {
       const int len = n0 + lane < seqs ? seq_len(args, n0 + lane) : 0;
       const unsigned some = __ballot_sync(0xffffffffu, len > 0);
       if (base + __popc(some) > id) {
@@ -342,7 +352,7 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
     return r;
   }
 #pragma unroll 1
-  for (int turn = uncut ? 0 : 1; turn < 3 && r.n < 0; ++turn) {
+  for (int turn = LOCAL || !uncut ? 1 : 0; turn < (LOCAL ? 2 : 3) && r.n < 0; ++turn) {
     int records = 0;
 #pragma unroll 1
     for (int n0 = 0; n0 < seqs && r.n < 0; n0 += 32) {
@@ -350,7 +360,8 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
       const bool one = len > L && len <= uncut;
       const int whole = one ? 0 : len / L, all = one ? 1 : whole + (len != whole * L);
       const int mine = turn == 0 ? one : turn == 1 ? whole : one ? 0 : all - whole;
-      int run = mine, run_all = all;
+      const int kept = all > 1 ? all : 0;
+      int run = mine, run_all = kept;
 #pragma unroll 1
       for (int d = 1; d < 32; d <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, run, d), up_all = __shfl_up_sync(0xffffffffu, run_all, d);
@@ -363,7 +374,7 @@ __device__ __forceinline__ Segment find_segment(const LinPrefillArgs& args, int 
         r.len = __shfl_sync(0xffffffffu, len, src);
         r.count = __shfl_sync(0xffffffffu, all, src);
         r.s = turn != 1 ? r.count - 1 : id - __shfl_sync(0xffffffffu, base + run - mine, src);
-        r.record = records + __shfl_sync(0xffffffffu, run_all - all, src);
+        r.record = records + __shfl_sync(0xffffffffu, run_all - kept, src);
         r.t0 = seq_start(args, r.n);
       }
       base += __shfl_sync(0xffffffffu, run, 31);
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (LOCAL) grid_dependency_launch();
   const int HV = args.HV, h = blockIdx.x % HV, id = blockIdx.x / HV;
-  const Segment seg = find_segment(args, id, lane);
+  const Segment seg = find_segment<LOCAL>(args, id, lane);
   if (!LOCAL && blockIdx.x == 0 && warp == kGateWarp)  // bounds of no sequence, which has no CTA of its own
     for (int m = lane; m < args.num_seqs; m += 32)
       if (seq_len(args, m) < 0) set_error(args.err_flag, KDA_DEVERR_SEQLENS);
@@ -1045,11 +1056,11 @@ kda_status allow_all() {
 // Tokens of a segment.  Sequences of one length: the number of segments each that
 // takes least, by what a chunk and a CTA's start cost in thousands of cycles (measured:
 // 4.7 and 6 in the second launch, 2.3 and 5 in the first, which the last segments are
-// spared); with lengths that differ much, segments of half an SM's share, for sequences
-// of more than 1.2 shares.
+// spared); with lengths that differ much (one of more than 1.25 times the mean), segments
+// of half an SM's share, for sequences of more than 1.2 shares.
 struct Segments {
   int even, ragged, even_most, uncut;
-  int64_t most;  // segments of all sequences, at most
+  int64_t most, whole, records;  // segments, whole segments, segments of sequences in several: at most
 };
 Segments cut(const kda_dims& d, int num_seqs, int64_t total_tokens, int64_t sms) {
   Segments r{};
@@ -1063,13 +1074,23 @@ Segments cut(const kda_dims& d, int num_seqs, int64_t total_tokens, int64_t sms)
     if (cost < best) best = cost, even = each;
   }
   const int64_t share = (total_tokens * d.HV / (2 * sms) + kC - 1) / kC;
-  r.even = (int)(even * kC);
-  r.ragged = (int)((share < 4 ? 4 : share) * kC);
-  r.uncut = (int)(r.ragged * 12ll / 5 < INT32_MAX ? r.ragged * 12ll / 5 : INT32_MAX);
-  const int64_t even_most = len + len / 4;
-  r.even_most = num_seqs == 1 || even_most > INT32_MAX ? INT32_MAX : (int)even_most;
-  const int64_t least = num_seqs > 1 && r.ragged < r.even ? r.ragged : r.even;
-  r.most = total_tokens / least + num_seqs;
+  const int64_t even_most = len + len / 4, ragged = (share < 4 ? 4 : share) * kC;
+  const bool pieces = even < chunks, may_differ = num_seqs > 1 && total_tokens > ragged * 12 / 5;
+  const int64_t L = pieces || num_seqs == 1 ? even * kC : (even_most + kC - 1) / kC * kC;
+  auto tokens = [](int64_t n) { return (int)(n < INT32_MAX ? n : INT32_MAX / kC * kC); };
+  r.even = tokens(L);
+  r.ragged = tokens(ragged);
+  r.uncut = tokens(ragged * 12 / 5);
+  r.even_most = num_seqs == 1 ? INT32_MAX : tokens(even_most);
+  r.most = num_seqs;
+  auto count = [&](int64_t n) {
+    const int64_t whole = total_tokens / n, records = whole < num_seqs ? 2 * whole : whole + num_seqs;
+    r.most = whole + num_seqs > r.most ? whole + num_seqs : r.most;
+    r.whole = whole > r.whole ? whole : r.whole;
+    r.records = records > r.records ? records : r.records;
+  };
+  if (pieces) count(L);
+  if (may_differ) count(ragged);
   return r;
 }
 // The workspace size does not depend on the device: so many SMs as this GPU has.
@@ -1086,9 +1107,7 @@ extern "C" size_t kda_lin_prefill_workspace_size(kda_dims dims, int num_seqs, in
   if (num_seqs < 0 || total_tokens < 0 || dims.H <= 0 || dims.HV <= 0) return 0;
   if (total_tokens > INT32_MAX) return SIZE_MAX;  // refused; no capacity check may pass
   if (num_seqs == 0 || total_tokens == 0) return 0;
-  const Segments c = cut(dims, num_seqs, total_tokens, kSms);
-  if (total_tokens <= c.even && (num_seqs == 1 || total_tokens <= c.ragged)) return 0;
-  return (size_t)c.most * dims.HV * (65536 + 16);
+  return (size_t)cut(dims, num_seqs, total_tokens, kSms).records * dims.HV * (65536 + 16);
 }
 
 extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const kda_bf16* q, const kda_bf16* k,
@@ -1129,10 +1148,10 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.even_most = c.even_most;
   args.uncut = c.uncut;
   args.err_flag = err_flag;
-  const int64_t units = c.most * dims.HV;
+  const int64_t units = c.most * dims.HV, whole = c.whole * dims.HV;
   if (units > INT32_MAX) return KDA_ERR_SHAPE;
   args.local_state = static_cast<float4*>(workspace);
-  args.local_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need > 0 ? (size_t)units * 65536 : 0));
+  args.local_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need > 0 ? (size_t)c.records * dims.HV * 65536 : 0));
   LinMaps m;
   if (!encode_rows(&m.q, q, dims.H, total_tokens) || !encode_rows(&m.k, k, dims.H, total_tokens) ||
       !encode_rows(&m.v, v, dims.HV, total_tokens))
@@ -1143,7 +1162,7 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   record_stage(0, st);
   if (need > 0) {
-    s = launch_dependent(f16 ? lin_prefill_kernel<true, true> : lin_prefill_kernel<false, true>, (unsigned)units, kThreads, kSmem,
+    s = launch_dependent(f16 ? lin_prefill_kernel<true, true> : lin_prefill_kernel<false, true>, (unsigned)whole, kThreads, kSmem,
                          false, st, args, m);
     if (s != KDA_OK) return s;
   }

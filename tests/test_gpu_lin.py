@@ -149,6 +149,62 @@ def test_prefill_bad_bounds(cu):
     assert torch.equal(pool[free].cpu(), x["pool"][free])
 
 
+@pytest.mark.parametrize("n,T", [(7, 2000), (40, 4000), (9, 64)])
+def test_prefill_of_overlapping_sequences(n, T):
+    """Bounds that go back and forth: flagged, nothing runs, and nothing is written past
+    the workspace."""
+    c = case([T], H=1, gate="given")
+    x = draw(c, 63, spare=n)
+    x.update(cu=torch.tensor([T * (i & 1) for i in range(n)] + [T], dtype=i32), idx=torch.arange(n, dtype=i32))
+    size = kda.kda_lin_prefill_workspace_size(lu.dims(c), n, T)
+    ws = torch.full((size + 2 ** 20,), 77, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=i32, device="cuda")
+    o, pool = run(dict(c, lengths=[0] * n), x, err_flag=err, workspace=ws[:max(size, 1)])
+    assert err.item() == kda.KDA_DEVERR_SEQLENS and (o == 7).all() and torch.equal(pool.cpu(), x["pool"]) and (ws == 77).all()
+
+
+SIZES = [(1, 128, 4), (1, 4096, 16), (8, 16980, 2), (64, 16384, 4), (200, 9000, 8), (16, 16, 64), (3, 764, 2), (2, 9000, 1),
+         (5, 4001, 7), (33, 10000, 3)]
+
+
+@pytest.mark.parametrize("n,T,HV", SIZES)
+def test_prefill_workspace_holds_every_cut(n, T, HV):
+    """Lengths of every kind keep within the workspace, and the longest sequence ends where
+    it ends without a cut."""
+    import random
+
+    size = kda.kda_lin_prefill_workspace_size(kda.dims(HV), n, T)
+    rng = random.Random(n * T)
+    d = lu.dims(case([T], H=1, HV=HV))
+    for kind in range(6):
+        w = [rng.random() ** (kind * 2) + (1e-3 if kind < 4 else 0) for _ in range(n)]
+        if kind == 5:
+            w = [1.0] + [0.0] * (n - 1)
+        lengths = [int(T * x / sum(w)) for x in w]
+        lengths[rng.randrange(n)] += T - sum(lengths)
+        ws = torch.full((size + 2 ** 18,), 77, dtype=torch.uint8, device="cuda")
+        c = case(lengths, H=1, HV=HV, gate="fixed")
+        x = draw(c, kind)
+        err = torch.zeros(1, dtype=i32, device="cuda")
+        o, pool = run(c, x, err_flag=err, workspace=ws[:max(size, 1)])
+        assert err.item() == 0 and (ws[size:] == 77).all()
+        at = max(range(n), key=lambda i: lengths[i])  # the longest, alone and uncut, in parts of 64
+        s0 = sum(lengths[:at])
+        idx, L, end = x["idx"][at:at + 1].cuda(), lengths[at], s0 + lengths[at]
+        parts = {}
+        for name, f in (("state", lambda t: t.cuda()), ("magnitude", lambda t: t.abs().cuda())):
+            q, k, v, parts[name] = (f(x[key]) for key in ("q", "k", "v", "pool"))
+            for t in range(s0, end, 64):
+                e = min(t + 64, end)
+                kda.kda_lin_prefill(d, lu.scalar_gate(x["A_log"], None, True), q[t:e], k[t:e], v[t:e], None, parts[name], idx, None, 1,
+                                    torch.empty_like(v[t:e]))
+        # the same terms, in another order: 2^-24 of the magnitudes' sum for each of the at most
+        # 64 additions and 3 products of a chunk's, and for a product and a sum a chunk, twice
+        bound = (2 * 67 + 4 * (L // 64 + 1)) * 2.0 ** -24 * parts["magnitude"][idx.long()]
+        assert ((pool[idx.long()] - parts["state"][idx.long()]).abs() <= bound).all()
+        assert torch.isfinite(o[s0:end]).all() and not (o[s0:end] == 7).all(-1).any()
+
+
 def test_prefill_nan_stays_in_its_sequence():
     c = case([90, 66, 130], H=2)
     x = draw(c, 62)
