@@ -585,7 +585,8 @@ kda_status kda_token_logprobs(int logits_dtype, const void *logits, int64_t logi
  * 32 in 4, consecutive in the page) shares one FP32 scale:
  *   scale = max |x| / top,  code = x / scale rounded to nearest (ties to even) in
  *   [-top, top],            value = code * scale;   top = 127 in 8 bits, 7 in 4.
- * A value comes back within half a scale, 1/254 (1/14) of its group's largest.
+ * A value comes back within half a scale, 1/254 (1/14) of its group's largest (where
+ * the scale is below FP32's smallest normal number, within 2^-143 more).
  * Both are exact: codes follow from the FP32 scale without a rounding in between.
  * A group with an infinity or a NaN comes back as NaN throughout.
  * Pages are FP32: page_bytes a multiple of 512 (else KDA_ERR_UNSUPPORTED).
