@@ -1062,8 +1062,11 @@ kda_status allow_all() {
 // Tokens of a segment.  Sequences of one length: the number of segments each that
 // takes least, by what a chunk and a CTA's start cost in thousands of cycles (measured:
 // 4.7 and 6 in the second launch, 2.3 and 5 in the first, which the last segments are
-// spared); with lengths that differ much (one of more than 1.25 times the mean), segments
-// of half an SM's share, for sequences of more than 1.2 shares.
+// spared).  With lengths that differ much (one of more than 1.25 times the mean), segments
+// of an SM's share of the chunks, at least 4, for sequences of more than 1.6 of them; of
+// half a share, for sequences of more than 1.5 shares, where that is 16 chunks or more;
+// and below 2 for all.  In a model of the SMs with these costs that takes 1 to 7% longer
+// than the best lengths for each of 500 batches, half shares throughout 11 to 20%.
 struct Segments {
   int even, ragged, even_most, uncut;
   int64_t most, whole, records;  // segments, whole segments, segments of sequences in several: at most
@@ -1079,14 +1082,15 @@ Segments cut(const kda_dims& d, int num_seqs, int64_t total_tokens, int64_t sms)
     const double cost = waves * (4.7 * each + 6) + waves1 * (2.3 * each + 5);
     if (cost < best) best = cost, even = each;
   }
-  const int64_t share = (total_tokens * d.HV / (2 * sms) + kC - 1) / kC;
-  const int64_t even_most = len + len / 4, ragged = (share < 4 ? 4 : share) * kC;
-  const bool pieces = even < chunks, may_differ = num_seqs > 1 && total_tokens > ragged * 12 / 5;
+  const int64_t share = (total_tokens * d.HV / sms + kC - 1) / kC, few = share < 16 ? share : (share + 1) / 2;
+  const int64_t even_most = len + len / 4, ragged = (few < 4 ? 4 : few) * kC;
+  const int64_t uncut = share <= 2 ? ragged : share < 16 ? ragged * 8 / 5 : ragged * 3;
+  const bool pieces = even < chunks, may_differ = num_seqs > 1 && total_tokens > uncut;
   const int64_t L = pieces || num_seqs == 1 ? even * kC : (even_most + kC - 1) / kC * kC;
   auto tokens = [](int64_t n) { return (int)(n < INT32_MAX ? n : INT32_MAX / kC * kC); };
   r.even = tokens(L);
   r.ragged = tokens(ragged);
-  r.uncut = tokens(ragged * 12 / 5);
+  r.uncut = tokens(uncut);
   r.even_most = num_seqs == 1 ? INT32_MAX : tokens(even_most);
   r.most = num_seqs;
   auto count = [&](int64_t n) {
