@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   const float x_token = one<DT>(row, token);
 
   if (tid == 0) s.count = 0;
+  if (TOP && tid < kMaxTop) s.best[tid] = 0;  // a CTA of the single entries' share has no tile
   if (TOP) __syncthreads();
   float top_x = -INFINITY;  // the largest value so far,
   int top_tile = 0;         // the tile that it came with,
@@ -431,8 +432,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     }
     if (lane == 0) s.stats[warp] = Stats{m, r + mine, all_t};
   }
-  __syncthreads();
-  if constexpr (TOP) rank_list(s, s.count, top);
+  __syncthreads();  // (`best` holds the last tile's look at the list)
   cluster_wait();
   Joined* to = cluster.map_shared_rank(&joined, 0);
   if (TOP && tid < kMaxTop) to->keys[rank][tid] = s.best[tid];
