@@ -465,7 +465,7 @@ def _cur(stream):
     """cudaStream_t of a torch stream, or of the current one."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _new(n, dtype, device, stream):
@@ -746,9 +746,37 @@ def kda_pool_fork(pool, used, table, parents, rows, children=None, err_flag=None
 # -- linear attention with one decay per value head ---------------------------
 
 
-def _lin_gate_rows(d, gate, a, rows):
-    """The gate input [>= rows, HV], or None where the heads' decay is fixed."""
-    return None if a is None else _gate_rows(d, gate, a, rows)
+_F32, _I32, _I16 = torch.float32, torch.int32, torch.int16
+
+
+def _lin_gate(gate, a, rows, HV, t16):
+    """(kda_scalar_gate, gate input [>= rows, HV] or None where the heads' decay is fixed)."""
+    A_log, bias = gate.A_log, gate.dt_bias
+    g = kda_scalar_gate(None if A_log is None else _arg(A_log, _F32, HV, "A_log", "[HV]"),
+                        None if bias is None else _arg(bias, _F32, HV, "dt_bias", "[HV]"), 0, 1 if gate.use_qk_l2norm else 0,
+                        gate.scale)
+    if a is None:
+        return g, None
+    if a.shape[-1] != HV:
+        raise ValueError(f"`a` must have shape [rows, HV] = [{rows}, {HV}] (got {tuple(a.shape)})")
+    return g, _arg(a, _F32 if A_log is None else t16, rows * HV, "a", "[rows, HV]")
+
+
+def _lin_packed(d, gate, mixed_qkv, a, rows, B, state_pool, state_idx, o):
+    """What the packed calls have in common, checked: the arguments up to the gate
+    input, the pool and what goes with it, and a token's values."""
+    H, HV, K, V, t16 = d.H, d.HV, d.K, d.V, _t16(d)
+    shape, strides, dtype = mixed_qkv.shape, mixed_qkv.stride(), mixed_qkv.dtype
+    if len(shape) != 2 or shape[0] < rows or shape[1] < 2 * H * K + HV * V or strides[1] != 1 or not mixed_qkv.is_cuda or \
+            (dtype is not t16 and dtype is not _I16):
+        _gdn_rows(d, mixed_qkv, rows)  # says what is wrong
+    g, gate_rows = _lin_gate(gate, a, rows, HV, t16)
+    slots = state_pool.shape
+    if len(slots) != 4 or slots[1] != HV or slots[2] != V or slots[3] != K:
+        _pool_slots(d, state_pool)
+    return (d, g, mixed_qkv.data_ptr(), strides[0], gate_rows), \
+        (_arg(state_pool, _F32, 0, "state_pool", "[slots, HV, V, K]"), slots[0], _arg(state_idx, _I32, B, "state_idx", "[B]"),
+         _arg(o, t16, rows * HV * V, "o", "[rows, HV, V]")), HV * V * K
 
 
 def kda_lin_prefill_workspace_size(d: kda_dims, num_seqs: int, total_tokens: int) -> int:
@@ -760,22 +788,26 @@ def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_s
     """Varlen prefill (see kda.h).  q,k [T,H,K], v [T,HV,V], a [gate_rows,HV] or
     None (a head's decay is -exp(A_log) for every token); state_pool
     [slots,HV,V,K] fp32 (in place); o [T,HV,V] (written)."""
-    lib, t16 = load(), _t16(d)
+    lib, t16, HV, V = load(), _t16(d), d.HV, d.V
     T, n = q.shape[0], int(num_seqs)
     gate_rows = T if a is None else a.shape[0]
-    HK, HVV = d.H * d.K, d.HV * d.V
+    HK, HVV = d.H * d.K, HV * V
     slots = _pool_slots(d, state_pool)
+    g, rows = _lin_gate(gate, a, gate_rows, HV, t16)
+    size = 0
     if workspace is None:
         need = lib.kda_lin_prefill_workspace_size(d, n, T)
-        workspace = _new(need, torch.uint8, q.device, stream) if need else None
+        if need:
+            workspace, size = _new(need, torch.uint8, q.device, stream), need
+    else:
+        size = workspace.numel() * workspace.element_size()
     st = lib.kda_lin_prefill(
-        d, gate.c(d), _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
-        _arg(v, t16, T * HVV, "v", "[T, HV, V]"), _lin_gate_rows(d, gate, a, gate_rows), gate_rows,
-        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), slots,
-        _arg(state_idx, torch.int32, n, "state_idx", "[num_seqs]"),
-        _opt(cu_seqlens, torch.int32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
-        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _err(err_flag), _cur(stream))
+        d, g, _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
+        _arg(v, t16, T * HVV, "v", "[T, HV, V]"), rows, gate_rows,
+        _arg(state_pool, _F32, 0, "state_pool", "[slots, HV, V, K]"), slots, _arg(state_idx, _I32, n, "state_idx", "[num_seqs]"),
+        None if cu_seqlens is None else _arg(cu_seqlens, _I32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
+        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), None if workspace is None else workspace.data_ptr(), size, _err(err_flag),
+        _cur(stream))
     if st:
         _check(st, "kda_lin_prefill")
 
@@ -783,24 +815,17 @@ def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_s
 def kda_lin_decode_packed(d, gate: ScalarGate, mixed_qkv, a, state_pool, state_idx, o, err_flag=None, stream=None):
     """One token per request, state in place; a [B, HV] or None."""
     B = mixed_qkv.shape[0]
-    st = load().kda_lin_decode_packed(
-        d, gate.c(d), _gdn_rows(d, mixed_qkv, B), mixed_qkv.stride(0), _lin_gate_rows(d, gate, a, B), B,
-        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), _pool_slots(d, state_pool),
-        _arg(state_idx, torch.int32, B, "state_idx", "[B]"), _arg(o, _t16(d), B * d.HV * d.V, "o", "[B, HV, V]"),
-        _err(err_flag), _cur(stream))
+    head, pool, _ = _lin_packed(d, gate, mixed_qkv, a, B, B, state_pool, state_idx, o)
+    st = load().kda_lin_decode_packed(*head, B, *pool, _err(err_flag), _cur(stream))
     if st:
         _check(st, "kda_lin_decode_packed")
 
 
 def _lin_verify(name, call, d, gate, mixed_qkv, a, B, T, parents, state_pool, state_idx, o, snapshots, err_flag, stream):
-    B, T = int(B), int(T)
     rows = B * T
-    st = call(
-        d, gate.c(d), _gdn_rows(d, mixed_qkv, rows), mixed_qkv.stride(0), _lin_gate_rows(d, gate, a, rows), B, T, *parents,
-        _arg(state_pool, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), _pool_slots(d, state_pool),
-        _arg(state_idx, torch.int32, B, "state_idx", "[B]"), _arg(o, _t16(d), rows * d.HV * d.V, "o", "[B, T, HV, V]"),
-        _arg(snapshots, torch.float32, rows * d.HV * d.V * d.K, "snapshots", "[B, T, HV, V, K]"), _err(err_flag),
-        _cur(stream))
+    head, pool, values = _lin_packed(d, gate, mixed_qkv, a, rows, B, state_pool, state_idx, o)
+    st = call(*head, B, T, *parents, *pool, _arg(snapshots, _F32, rows * values, "snapshots", "[B, T, HV, V, K]"),
+              _err(err_flag), _cur(stream))
     if st:
         _check(st, name)
 
@@ -808,16 +833,17 @@ def _lin_verify(name, call, d, gate, mixed_qkv, a, B, T, parents, state_pool, st
 def kda_lin_verify_chain(d, gate: ScalarGate, mixed_qkv, a, B, T, state_pool, state_idx, o, snapshots, err_flag=None,
                          stream=None):
     """Chain verify; snapshots as kda_verify_chain's, for kda_commit."""
-    _lin_verify("kda_lin_verify_chain", load().kda_lin_verify_chain, d, gate, mixed_qkv, a, B, T, (), state_pool, state_idx,
-                o, snapshots, err_flag, stream)
+    _lin_verify("kda_lin_verify_chain", load().kda_lin_verify_chain, d, gate, mixed_qkv, a, int(B), int(T), (), state_pool,
+                state_idx, o, snapshots, err_flag, stream)
 
 
 def kda_lin_verify_tree(d, gate: ScalarGate, mixed_qkv, a, B, T, parent_idx, state_pool, state_idx, o, snapshots,
                         err_flag=None, stream=None):
     """Tree verify; parent_idx [B, T] int32."""
+    B, T = int(B), int(T)
     _lin_verify("kda_lin_verify_tree", load().kda_lin_verify_tree, d, gate, mixed_qkv, a, B, T,
-                (_arg(parent_idx, torch.int32, B * T, "parent_idx", "[B, T]"),), state_pool, state_idx, o, snapshots,
-                err_flag, stream)
+                (_arg(parent_idx, _I32, B * T, "parent_idx", "[B, T]"),), state_pool, state_idx, o, snapshots, err_flag,
+                stream)
 
 
 # -- log probabilities of given tokens -----------------------------------------
@@ -829,28 +855,32 @@ def kda_token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, 
     bfloat16 or float16, rows possibly padded), see kda.h.  Written: logprobs
     [rows] fp32; entropy [rows] fp32, top_tokens [rows, top] int32 and
     top_logprobs [rows, top] fp32 where given."""
-    if logits.dim() != 2 or tokens.dim() != 1 or tokens.shape[0] != logits.shape[0]:
-        raise ValueError(f"logits must be [rows, vocab] and tokens [rows] (got {tuple(logits.shape)}, {tuple(tokens.shape)})")
-    if logits.dtype not in _PROBS:
+    shape, dtype = logits.shape, _PROBS.get(logits.dtype)
+    if len(shape) != 2 or tokens.dim() != 1 or tokens.shape[0] != shape[0]:
+        raise ValueError(f"logits must be [rows, vocab] and tokens [rows] (got {tuple(shape)}, {tuple(tokens.shape)})")
+    if dtype is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
-    rows, V = logits.shape
-    stride = logits.stride(0) if rows > 1 else V
-    if (V > 1 and logits.stride(1) != 1) or stride < V:
+    rows, V = shape
+    stride, unit = logits.stride()
+    if rows <= 1:
+        stride = V
+    if (V > 1 and unit != 1) or stride < V:
         raise ValueError(f"the rows of logits must be dense (got strides {logits.stride()})")
     if not logits.is_cuda:
         raise ValueError("libkda takes device tensors")
-    top = 0
+    top, best, best_lp = 0, None, None
     if top_tokens is not None or top_logprobs is not None:
         if top_tokens is None or top_logprobs is None or top_tokens.dim() != 2 or top_tokens.shape != top_logprobs.shape or \
                 top_tokens.shape[0] != rows:
             raise ValueError("top_tokens and top_logprobs must both be [rows, top]")
         top = top_tokens.shape[1]
-    f32, i32 = torch.float32, torch.int32
+        best = _arg(top_tokens, _I32, rows * top, "top_tokens", "[rows, top]")
+        best_lp = _arg(top_logprobs, _F32, rows * top, "top_logprobs", "[rows, top]")
     st = load().kda_token_logprobs(
-        _PROBS[logits.dtype], logits.data_ptr(), stride, _arg(tokens, i32, rows, "tokens", "[rows]"), rows, V,
-        _arg(logprobs, f32, rows, "logprobs", "[rows]"), _opt(entropy, f32, rows, "entropy", "[rows]"), top,
-        _opt(top_tokens, i32, rows * top, "top_tokens", "[rows, top]"),
-        _opt(top_logprobs, f32, rows * top, "top_logprobs", "[rows, top]"), _err(err_flag), _cur(stream))
+        dtype, logits.data_ptr(), stride, _arg(tokens, _I32, rows, "tokens", "[rows]"), rows, V,
+        _arg(logprobs, _F32, rows, "logprobs", "[rows]"),
+        None if entropy is None else _arg(entropy, _F32, rows, "entropy", "[rows]"), top, best, best_lp, _err(err_flag),
+        _cur(stream))
     if st:
         _check(st, "kda_token_logprobs")
 
@@ -858,45 +888,40 @@ def kda_token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, 
 # -- pages kept in 8 or 4 bits ---------------------------------------------------
 
 
-def _archive(pool, codes, scales):
-    """Pages of a pool, and the archive that keeps them: codes int8
+def _archive(name, call, pool, codes, scales, src, dst, err_flag, stream):
+    """A call on pages of a pool and the archive that keeps them: codes int8
     [slots, layers, .., K] (8 bits) or uint8 [slots, layers, .., K / 2] (4 bits,
     two codes a byte), scales fp32 with a scale for every 128 or 32 values."""
-    if pool.dtype is not torch.float32:
+    kind, pairs, kept, held = codes.dtype, src.shape, codes.shape, scales.shape
+    if pool.dtype is not _F32:
         raise TypeError(f"pool must be float32 (got {pool.dtype})")
-    if codes.dtype is not torch.int8 and codes.dtype is not torch.uint8:
-        raise TypeError(f"codes must be int8 (8 bits) or uint8 (4 bits) (got {codes.dtype})")
+    if kind is not torch.int8 and kind is not torch.uint8:
+        raise TypeError(f"codes must be int8 (8 bits) or uint8 (4 bits) (got {kind})")
+    if len(pairs) != 1 or dst.shape != pairs:
+        raise ValueError(f"src and dst must be lists of one length (got {tuple(pairs)}, {tuple(dst.shape)})")
     pages = _pages(pool)
-    bits, group = (8, 128) if codes.dtype is torch.int8 else (4, 32)
-    values = pages.layers * (pages.page_bytes // 4)
-    slots = codes.shape[0] if codes.dim() > 0 else 0
+    bits, group = (8, 128) if kind is torch.int8 else (4, 32)
+    slots = kept[0] if len(kept) else 0
+    all_slots = pool.shape[1]
+    values = pool.numel() // all_slots if all_slots else 0  # of a page, in all layers
     n = values * bits // 8
-    if slots and codes.numel() != slots * n or slots != (scales.shape[0] if scales.dim() > 0 else 0) or \
-            scales.numel() * group != slots * values:
+    if slots != (held[0] if len(held) else 0) or (all_slots and (codes.numel() != slots * n or scales.numel() * group != slots * values)):
         raise ValueError(f"codes and scales must hold {n} bytes and {values // group} scales a page "
-                         f"(got {tuple(codes.shape)}, {tuple(scales.shape)})")
-    return pages, kda_archive(_arg(codes, codes.dtype, 0, "codes", "[slots, layers, ..]"),
-                              _arg(scales, torch.float32, 0, "scales", "[slots, layers, ..]"), bits, slots)
+                         f"(got {tuple(kept)}, {tuple(held)})")
+    n = pairs[0]
+    st = call(pages, kda_archive(_arg(codes, kind, 0, "codes", "[slots, layers, ..]"),
+                                 _arg(scales, _F32, 0, "scales", "[slots, layers, ..]"), bits, slots),
+              _arg(src, _I32, n, "src", "[n]"), _arg(dst, _I32, n, "dst", "[n]"), n, _err(err_flag), _cur(stream))
+    if st:
+        _check(st, name)
 
 
 def kda_pool_store(pool, codes, scales, src, dst, err_flag=None, stream=None):
     """Archive page dst[i] <- pool[:, src[i]]; pool [layers, slots, ...] fp32, codes
     and scales as in _archive."""
-    n = src.shape[0]
-    if dst.shape[0] != n:
-        raise ValueError("src and dst must have one length")
-    pages, archive = _archive(pool, codes, scales)
-    st = load().kda_pool_store(pages, archive, _list(src, "src"), _list(dst, "dst"), n, _err(err_flag), _cur(stream))
-    if st:
-        _check(st, "kda_pool_store")
+    _archive("kda_pool_store", load().kda_pool_store, pool, codes, scales, src, dst, err_flag, stream)
 
 
 def kda_pool_load(codes, scales, pool, src, dst, err_flag=None, stream=None):
     """pool[:, dst[i]] <- archive page src[i]."""
-    n = src.shape[0]
-    if dst.shape[0] != n:
-        raise ValueError("src and dst must have one length")
-    pages, archive = _archive(pool, codes, scales)
-    st = load().kda_pool_load(pages, archive, _list(src, "src"), _list(dst, "dst"), n, _err(err_flag), _cur(stream))
-    if st:
-        _check(st, "kda_pool_load")
+    _archive("kda_pool_load", load().kda_pool_load, pool, codes, scales, src, dst, err_flag, stream)
