@@ -73,7 +73,7 @@ struct LinPrefillArgs {
 };
 
 struct LinMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, pool;
 };
 
 // Factors of a chunk: of the decays first, then times those of the norms.  b is the first
@@ -109,6 +109,7 @@ struct Bars {
   uint64_t qk_full;                  // Q K^T (and the last O1 and O2)
   uint64_t o_full;                   // the segment's last O2
   uint64_t drained;                  // all products
+  uint64_t state_full, state_read;   // the pool's state landed, and is in registers
   uint32_t tmem;
   int timed_out;
   float p_scale[2][kC];      // FP16: the powers of two of P's rows
@@ -117,11 +118,16 @@ struct Bars {
 };
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
-// the parts of K', P, factors, barriers.
+// the parts of K', P and 8 KB, factors, barriers.  The pool's state lands, in four boxes of
+// 32 key channels, where chunk 2's rows (LOCAL: chunk 1's K') and P will be.  (Read with
+// plain loads, 32 bytes a lane and lanes 512 apart, it held up the SM's memory instructions
+// for 3500 cycles.)
 constexpr int kTile = 16384, kStageBytes = 3 * kTile;
-constexpr int kWk = kStages * kStageBytes, kP = kWk + 3 * kTile, kScalars = kP + 8192;
+constexpr int kWk = kStages * kStageBytes, kP = kWk + 3 * kTile, kScalars = kP + kTile;
 constexpr int kLocalStage = 2 * kTile, kLocalWk = 3 * kTile;  // LOCAL: K and V alone, and K' twice
 static_assert(kStages * kLocalStage + 2 * kLocalWk <= kScalars, "the first launch's layout");
+constexpr int kState = 2 * kStageBytes, kLocalState = kWk;
+static_assert(kStages * kLocalStage + kLocalWk == kLocalState, "the second K' of the first launch");
 constexpr int kBars = kScalars + kScalarBufs * (int)sizeof(Scalars);
 constexpr int kSmem = kBars + (int)sizeof(Bars);
 static_assert(kSmem <= 232448 - 1024 && kBars % 16 == 0, "shared memory");
@@ -251,22 +257,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
 }
 
 // Eight values: 32 bytes at once, a sector of L2, where they are so aligned, since the
-// lanes of a warp lie 512 bytes apart in a state (1 x 128 tokens, 4 heads: 12.6 us
-// instead of 14.7).
-__device__ __forceinline__ void ld8(const float* p, float* x, bool aligned32) {
-  if (aligned32) {
-    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + i);
-      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-    }
-  }
-}
+// lanes of a warp lie 512 bytes apart in a state.
 __device__ __forceinline__ void st8(float* p, const float* x, bool aligned32) {
   if (aligned32) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
@@ -428,16 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool last_segment = seg.s == seg.count - 1;
   const int L = last_segment ? seg.len - first : seg.tokens, nch = (L + kC - 1) / kC;
   const int64_t t0 = seg.t0 + first;
+  if (LOCAL && last_segment) return;  // nothing starts from its state
   const int slot = args.state_idx[seg.n];
-  const bool no_slot = slot < 0 || slot >= args.pool_slots;
-  if (LOCAL && (last_segment || no_slot)) return;  // nothing starts from its state
-  if (no_slot) {  // padding or out of range: zero outputs, no state touched
-    if (slot != -1 && tid == 0 && h == 0 && seg.s == 0) set_error(args.err_flag, KDA_DEVERR_SLOT);
-    for (int64_t i = tid; i < (int64_t)L * 16; i += kThreads)
-      *reinterpret_cast<uint4*>(args.o + ((t0 + i / 16) * HV + h) * kHeadDim + (i % 16) * 8) = make_uint4(0, 0, 0, 0);
-    leave();
-    return;
-  }
   if (tc::smem_u32(smem) & 1023u) {  // swizzled tiles start on 1024 bytes
     if (tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
     leave();
@@ -465,12 +448,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&bars.qk_full, 1);
     tc::mbar_init(&bars.o_full, 1);
     tc::mbar_init(&bars.drained, 1);
+    tc::mbar_init(&bars.state_full, 1);
+    tc::mbar_init(&bars.state_read, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
+  if (slot < 0 || slot >= args.pool_slots) {  // padding or out of range: zero outputs, no state touched
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
+    if (!LOCAL) {
+      if (slot != -1 && tid == 0 && h == 0 && seg.s == 0) set_error(args.err_flag, KDA_DEVERR_SLOT);
+      for (int64_t i = tid; i < (int64_t)L * 16; i += kThreads)
+        *reinterpret_cast<uint4*>(args.o + ((t0 + i / 16) * HV + h) * kHeadDim + (i % 16) * 8) = make_uint4(0, 0, 0, 0);
+    }
+    leave();
+    return;
+  }
+  const bool from_pool = seg.s == 0 && (LOCAL || seg.count == 1);
   const LinGateArgs& ga = args.gate;
   // FP16: unit keys are at most 1 and become K' times 2^15, so that small ones keep their places
   const float k_up = F16 && ga.use_qk_l2norm ? 32768.f : 1.f;
@@ -533,13 +529,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* root = args.pool + (((size_t)slot * HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
     float S[32];
     auto record = [&](int64_t segment) { return args.local_state + (segment * HV + h) * 4096 + tid; };
-    // (The first launch leaves the pool as it is: what it does not leave behind can be
-    // read while it runs.)
-    if (seg.s == 0 && (LOCAL || seg.count == 1))
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) ld8(root + j, S + j, args.pool32);
     auto start = [&]() {
-    if (!LOCAL) grid_dependency_wait();
+    // (The first launch leaves the pool as it is: what it does not leave behind can be
+    // read while it runs, and a sequence in one piece needs nothing of it.)
+    if (!LOCAL && seg.count > 1) grid_dependency_wait();
+    if (from_pool) {
+      await(&bars.state_full, 0);
+      uint8_t* box = smem + (part == 3 ? kP : (LOCAL ? kLocalState : kState) + part * kTile);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(line16(box, dv, j));
+        S[4 * j] = x.x, S[4 * j + 1] = x.y, S[4 * j + 2] = x.z, S[4 * j + 3] = x.w;
+      }
+      asm volatile("barrier.cta.sync 1, 512;" ::: "memory");  // its place is others' now
+      if (!LOCAL && tid == 0 && ok) arrive(&bars.state_read);
+    }
     if (seg.s == 0) {
       // The CTA of the last segment writes the sequence's slot, maybe before this one
       // reads it: the first launch leaves a copy where the last segment has no record.
@@ -636,11 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int e = 0; e < 2; ++e) at[e] = smem + kP + (r0 + 8 * e) * 128 + 4 * (lane & 3);
     auto put = [&](int j, int e, uint32_t x) { *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4)) = x; };
-    if (!LOCAL && part > quad)  // right of the diagonal all is zero, and stays so
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0);
     auto weights = [&](int c, const Scalars& sc) {
       await(&bars.qk_full, c);  // the last P has been read too
       tc::tc_fence_after();
@@ -753,6 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     keys(0, stage(0), factors(0));
     done(&bars.wk_full[0]);
     start();  // (the first launch may still be running)
+    if (!LOCAL && part > quad)  // right of the diagonal all is zero, and stays so
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0);
     float last = 1.f;
     if (LOCAL) {
       // K' and dS are there twice: a chunk's product runs while the next one's K' is made
@@ -810,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < nch; ++c) {
       const int st = c % kStages;
       if (c >= kStages && !(ok = warp_wait(&bars.empty[st], c / kStages - 1))) break;
+      if (!LOCAL && c == 2 && from_pool && !(ok = warp_wait(&bars.state_read, 0))) break;
       uint8_t* rows = smem + st * kStage;
       if (leader) {
         uint64_t* bar = &bars.full[st];
@@ -821,12 +826,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_box(rows + kStage - 2 * kTile + a * 8192, &maps.k, a * 64, h / args.G, tok, bar);
           tma_box(rows + kStage - kTile + a * 8192, &maps.v, a * 64, h, tok, bar);
         }
+        if (c == 0 && from_pool) {
+          tc::mbar_expect_tx(&bars.state_full, 4 * kTile);
+          uint8_t* to = smem + (LOCAL ? kLocalState : kState);
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            tma_box(a == 3 ? smem + kP : to + a * kTile, &maps.pool, a * 32, 0, (slot * HV + h) * kHeadDim, &bars.state_full);
+        }
       }
       __syncwarp();
       issued = c + 1;
     }
     // nothing may land after the CTA is gone
     for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c) warp_wait(&bars.full[c % kStages], c / kStages);
+    if (from_pool) warp_wait(&bars.state_full, 0);
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------------- products
     constexpr uint32_t kType = F16 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
@@ -909,8 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kNormWarp) {
     // ----------------------------------------------------------- the decays' factors
     // one of two warps, every other chunk
-    const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
-    const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
+    const float log_rate = ga.A_log ? ga.A_log[h] : 0.f, bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
     ushort2 next[2];  // of tokens 2 lane and 2 lane + 1
     auto load_gate = [&](int c) {
 #pragma unroll
@@ -920,6 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     load_gate(warp - kGateWarp);
+    const float neg_rate = ga.A_log ? -expf(log_rate) : 0.f;
 #pragma unroll 1
     for (int c = warp - kGateWarp; c < nch; c += 2) {
       const int left = L - c * kC, sb = c % kScalarBufs;
@@ -1024,6 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     warp_wait(&bars.drained, 0);
   }
   if (bars.timed_out && tid == 0) set_error(args.err_flag, KDA_DEVERR_TIMEOUT);
+  leave();
   __syncthreads();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmCols);
 }
@@ -1038,6 +1052,19 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t heads, int64_t T) {
   const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kC};
   const cuuint32_t estride[3] = {1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dim, stride, box, estride,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same of a pool of FP32 states, box (32 key channels, 1, 128 value columns).
+bool encode_pool(CUtensorMap* m, const void* base, int64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)kHeadDim, 1u, (cuuint64_t)rows};
+  const cuuint64_t stride[2] = {(cuuint64_t)kHeadDim * 4, (cuuint64_t)kHeadDim * 4};
+  const cuuint32_t box[3] = {32u, 1u, (cuuint32_t)kHeadDim};
+  const cuuint32_t estride[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dim, stride, box, estride,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1164,7 +1191,8 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   args.local_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need > 0 ? (size_t)c.records * dims.HV * 65536 : 0));
   LinMaps m;
   if (!encode_rows(&m.q, q, dims.H, total_tokens) || !encode_rows(&m.k, k, dims.H, total_tokens) ||
-      !encode_rows(&m.v, v, dims.HV, total_tokens))
+      !encode_rows(&m.v, v, dims.HV, total_tokens) ||
+      !encode_pool(&m.pool, state_pool, (pool_slots > 0 ? (int64_t)pool_slots : 1) * dims.HV * kHeadDim))
     return KDA_ERR_CUDA;
   s = allow_all();
   if (s != KDA_OK) return s;

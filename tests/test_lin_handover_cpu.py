@@ -27,8 +27,8 @@ class Barrier:
 class Cta:
     """What the programs share: barriers, who holds what, and the order of products."""
 
-    def __init__(self, nch, local, workers=3):
-        self.nch, self.local, self.workers = nch, local, workers
+    def __init__(self, nch, local, workers=3, pool=False):
+        self.nch, self.local, self.workers, self.pool = nch, local, workers, pool
         self.bar = {("in", i): Barrier(NORMS) for i in range(BUFS)}
         self.bar |= {("gate", i): Barrier(1) for i in range(BUFS)}
         self.bar |= {(x, i): Barrier(1) for x in ("full", "empty") for i in range(STAGES)}
@@ -36,6 +36,10 @@ class Cta:
         self.bar |= {("wk", i): Barrier(workers) for i in range(2)}
         self.bar |= {("ds", i): Barrier(1) for i in range(2)}
         self.bar |= {("u", 0): Barrier(workers), ("s", 0): Barrier(workers), ("s", 1): Barrier(workers), ("p", 0): Barrier(workers), ("qk", 0): Barrier(1), ("o", 0): Barrier(1)}
+        self.bar |= {("state", 0): Barrier(1), ("read", 0): Barrier(1), ("met", 0): Barrier(workers)}
+        # the pool's state lands where these will be
+        self.state = [("wk", 1, x) for x in range(workers)] if local else [(x, 2) for x in ("K", "V", "Q")] + [
+            ("P", x) for x in range(workers)]
         self.queue = []  # products and commits in issue order
         self.holds = {}  # resource -> chunk whose data it holds
         self.reading = {}  # resource -> products under way that read or write it
@@ -80,10 +84,17 @@ def rows(t):
     for c in range(t.nch):
         if c >= STAGES:
             yield ("empty", c % STAGES), c // STAGES - 1
+        if c == 2 and t.pool and not t.local:
+            yield ("read", 0), 0
         for what in ("K", "V", "Q"):
             t.put((what, c % STAGES), c)
         yield
         t.bar["full", c % STAGES].arrive()
+        if c == 0 and t.pool:
+            for place in t.state:
+                t.put(place, "state")
+            yield
+            t.bar["state", 0].arrive()
         yield
 
 
@@ -137,6 +148,15 @@ def worker(t, w):
     yield from keys(0)
     yield
     t.bar["wk", 0].arrive()
+    if t.pool:
+        yield ("state", 0), 0
+        for place in t.state:
+            t.use(place, "state")
+            yield
+        t.bar["met", 0].arrive()
+        yield ("met", 0), 0
+        if w == 0:
+            t.bar["read", 0].arrive()
     for c in range(n):
         if t.local:
             if c > 0:
@@ -217,7 +237,7 @@ def products(t):
 
 def run(nch, local, seed):
     rng = random.Random(seed)
-    t = Cta(nch, local)
+    t = Cta(nch, local, pool=bool(seed & 1))
     progs = [rows(t), products(t), factors(t, 0), factors(t, 1)] + [norms(t, i) for i in range(NORMS)] + [worker(t, w) for w in range(t.workers)]
     speed = [rng.choice([0.02, 0.3, 1, 1]) for _ in progs] + [rng.choice([0.02, 0.3, 1])]  # the last: the tensor core
     wait = [None] * len(progs)
