@@ -57,8 +57,7 @@ constexpr int kStages = 3, kScalarBufs = 4;
 struct LinPrefillArgs {
   LinGateArgs gate;
   int HV, G;
-  float* pool;
-  int pool_slots, pool32;  // whether the pool is aligned to 32 bytes
+  int pool_slots;
   const int32_t* state_idx;
   const int32_t* cu_seqlens;
   int num_seqs;
@@ -119,9 +118,9 @@ struct Bars {
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
 // the parts of K', P and 8 KB, factors, barriers.  The pool's state lands, in four boxes of
-// 32 key channels, where chunk 2's rows (LOCAL: chunk 1's K') and P will be.  (Read with
-// plain loads, 32 bytes a lane and lanes 512 apart, it held up the SM's memory instructions
-// for 3500 cycles.)
+// 32 key channels, where chunk 2's rows (LOCAL: chunk 1's K') and P will be, and leaves the
+// same way.  (Plain accesses, 32 bytes a lane and lanes 512 apart, held up the SM's memory
+// instructions for 3500 cycles.)
 constexpr int kTile = 16384, kStageBytes = 3 * kTile;
 constexpr int kWk = kStages * kStageBytes, kP = kWk + 3 * kTile, kScalars = kP + kTile;
 constexpr int kLocalStage = 2 * kTile, kLocalWk = 3 * kTile;  // LOCAL: K and V alone, and K' twice
@@ -142,6 +141,12 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c
       "[%5];" ::"r"(tc::smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* map, int c0, int c1, int c2, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(src))
+               : "memory");
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
@@ -254,19 +259,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Eight values: 32 bytes at once, a sector of L2, where they are so aligned, since the
-// lanes of a warp lie 512 bytes apart in a state.
-__device__ __forceinline__ void st8(float* p, const float* x, bool aligned32) {
-  if (aligned32) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
-                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  }
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread; 16 k are 8 columns of A.
@@ -526,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // --------------------------------------------------------------------- state
     const int dv = 32 * quad + lane;  // this thread's value column; its key channels 32 part ..
-    float* root = args.pool + (((size_t)slot * HV + h) * kHeadDim + dv) * kHeadDim + 32 * part;
+    uint8_t* box = smem + (part == 3 ? kP : (LOCAL ? kLocalState : kState) + part * kTile);  // of the pool's state
     float S[32];
     auto record = [&](int64_t segment) { return args.local_state + (segment * HV + h) * 4096 + tid; };
     auto start = [&]() {
@@ -535,7 +527,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!LOCAL && seg.count > 1) grid_dependency_wait();
     if (from_pool) {
       await(&bars.state_full, 0);
-      uint8_t* box = smem + (part == 3 ? kP : (LOCAL ? kLocalState : kState) + part * kTile);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float4 x = *reinterpret_cast<const float4*>(line16(box, dv, j));
@@ -799,9 +790,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) to[j * 512] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
         if (tid == 0) args.local_decay[(int64_t)(seg.record + seg.s) * HV + h] = decay;
-      } else if (ok) {
+      } else {  // back to the pool as it came; all products are done
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) st8(root + j, S + j, args.pool32);
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(line16(box, dv, j)) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+        if (!ok) bars.timed_out = 1;
+        tc::fence_async_smem();
+        asm volatile("barrier.cta.sync 1, 512;" ::: "memory");
+        if (tid == 0 && !*static_cast<volatile int*>(&bars.timed_out)) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            tma_store_box(&maps.pool, a * 32, 0, (slot * HV + h) * kHeadDim, smem + (a == 3 ? kP : kState + a * kTile));
+          tc::bulk_commit();
+          tc::bulk_wait_read();  // shared memory stays until then
+        }
       }
     }
   } else {
@@ -1170,9 +1172,7 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
   if (s != KDA_OK) return s;
   args.HV = dims.HV;
   args.G = dims.HV / dims.H;
-  args.pool = state_pool;
   args.pool_slots = pool_slots;
-  args.pool32 = (reinterpret_cast<uintptr_t>(state_pool) & 31u) == 0;
   args.state_idx = state_idx;
   args.cu_seqlens = cu_seqlens;
   args.num_seqs = num_seqs;
