@@ -6,8 +6,8 @@
 // and 1.03 (0.625) written a value, and the other way round.  A warp takes rows of
 // 128 values, four a lane, eight rows with all their loads in flight; the largest
 // magnitude of a row is one warp reduction of bit patterns, that of a group of 32
-// three exchanges.  70 pages of 4 MiB stored and read back in 8 bits: 122 us, 6.05 TB/s,
-// 89% of a copy's rate; codes by conversions 139 us, and loads behind the check of the
+// three exchanges.  70 pages of 4 MiB stored and read back in 8 bits: 123 us, 6.0 TB/s,
+// 88% of a copy's rate; codes by conversions 139 us, and loads behind the check of the
 // pairs 148.
 #include "kda_host.h"
 

@@ -28,8 +28,8 @@
 //
 // Bound by the workers' instructions: 4400 cycles a chunk, of which the products take
 // 1500 and shared memory 2500, and 2200 in the first launch.  1 x 4096 tokens at 16
-// heads 43 us (68 MB: 1.6 TB/s), 8 x 4096 151 us (3.7 TB/s), 16 980 tokens in eight
-// sequences 132 us; 1 x 128 at 4 heads 12.5 us, most of it a CTA's start and the state.
+// heads 43 us (69 MB: 1.6 TB/s), 8 x 4096 149 us (3.7 TB/s), 16 980 tokens in eight
+// sequences 122 us; 1 x 128 at 4 heads 11 us, a third of it a CTA's start.
 //
 // A long sequence is cut into segments: a first launch computes what each segment
 // adds to a state of zero (no queries, no outputs), and the CTAs of the second sum

@@ -16,8 +16,8 @@
 // lane holding 16 key channels as four float4, so that every 128-bit access
 // of a warp covers four whole 128-byte segments.
 //
-// Decode of 48 requests at 32 value heads 31.5 us (6.4 TB/s), of one at 16 heads 2.1 us, a
-// launch's time; chain verify of 16 x 6 at 16 heads 20.5 us (85% of a copy's rate, six
+// Decode of 48 requests at 32 value heads 31.9 us (6.3 TB/s), of one at 16 heads 2.3 us, a
+// launch's time; chain verify of 16 x 6 at 16 heads 20.8 us (84% of a copy's rate, six
 // of seven parts of it writes); tree verify of 4 x 10 at 8 heads 9.3 us, ten steps of
 // 0.8 us one after the other in each of 256 CTAs.
 #include "kda_host.h"

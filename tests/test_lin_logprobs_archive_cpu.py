@@ -39,6 +39,10 @@ def test_lin_host_errors(lib):
     assert pre(g=sgate(None), a=ODD) == pre(a=ctypes.c_void_p(0x10001)) == kda.KDA_ERR_ALIGNMENT
     assert pre(T=0, rows=0) == kda.KDA_OK  # nothing to do
     assert kda.kda_lin_prefill_workspace_size(kda.dims(16), 1, 2 ** 31) == 2 ** 64 - 1
+    need = kda.kda_lin_prefill_workspace_size(kda.dims(16), 1, 4096)
+    assert need > 0 == kda.kda_lin_prefill_workspace_size(kda.dims(16), 1, 64)
+    assert pre(T=4096, rows=4096, ws=None) == pre(T=4096, rows=4096, ws_bytes=need - 1) == kda.KDA_ERR_WORKSPACE
+    assert pre(T=4096, rows=4096, ws=ODD) == kda.KDA_ERR_ALIGNMENT
 
     def dec(d=kda.dims(16), g=sgate(), stride=row, a=D, pool=D, qkv=D, B=2):
         return lib.kda_lin_decode_packed(d, g, qkv, stride, a, B, pool, 240, D, D, None, None)
