@@ -160,6 +160,22 @@ __device__ __forceinline__ void widen(uint4 w, float2* x) {
   }
 }
 
+// The largest of a piece's entries, NaN left out; -inf where there is none.
+template <int DT>
+__device__ __forceinline__ float piece_max(uint4 w) {
+  float2 m;
+  if constexpr (DT == KDA_DTYPE_F32) {
+    m = make_float2(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else if constexpr (DT == KDA_DTYPE_F16) {
+    auto h = [](uint32_t u) { return *reinterpret_cast<const __half2*>(&u); };
+    m = __half22float2(__hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w))));
+  } else {
+    auto b = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+    m = __bfloat1622float2(__hmax2(__hmax2(b(w.x), b(w.y)), __hmax2(b(w.z), b(w.w))));
+  }
+  return fmaxf(-INFINITY, fmaxf(m.x, m.y));
+}
+
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArgs args) {
   constexpr int kSize = DT == KDA_DTYPE_F32 ? 4 : 2, kEach = 16 / kSize;
@@ -248,10 +264,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     float big = -INFINITY, piece_big[kPieces];
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      widen<DT>(w[j], x);
-      piece_big[j] = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < kEach / 2; ++e) piece_big[j] = fmaxf(piece_big[j], fmaxf(x[e].x, x[e].y));  // NaN is left out
+      piece_big[j] = piece_max<DT>(w[j]);
       big = fmaxf(big, piece_big[j]);
     }
     // +inf counts as the largest number
