@@ -19,13 +19,13 @@
 // Alternatives.  Of the first tile each thread takes its largest value; the
 // ceil(top / 8)-th largest of those in every warp bounds from below what at least top
 // values of the tile reach, so that only values at or above the least of the 8 bounds
-// are candidates: some fifty of 4096 or 8192.  They go to a list in shared memory, as
-// keys that no two entries share: the value's bits in an order of their own, then the
-// token's complement, so that among equals the lowest token comes first.  After 1, 2, 4,
-// 8 .. tiles the list is cut to its top largest, and the last of them is the new bound,
-// which some top values reach until the next time.  Tiles with more candidates than the
-// list has room for (rows of one value) are searched key by key instead.  A key's rank
-// is the number of larger ones.
+// are candidates: some fifty of 4096 or 8192.  The pieces that hold some go to a list in
+// shared memory as they are.  After 1, 2, 4, 8 .. tiles the CTA takes the candidates out of
+// them, as keys that no two entries share (the value's bits in an order of their own, then
+// the token's complement, so that among equals the lowest token comes first), ranks these,
+// a key's rank being the number of larger ones, and keeps the top largest: the last of them
+// is the new bound.  Tiles with more than the lists have room for (rows of one value) are
+// searched key by key instead.
 //
 // A row is split over the CTAs of a cluster where there are few rows; rank 0 joins
 // what the others leave in its shared memory.
@@ -49,7 +49,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
 constexpr int kPieces = 4;      // 16-byte pieces of a tile a thread has
 constexpr int kAhead = 2;       // tiles under way
-constexpr int kList = 1024;     // candidates
+constexpr int kList = 512;      // candidates, and pieces that hold some
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -113,8 +113,10 @@ __device__ __forceinline__ float one(const void* row, int64_t i) {
 
 struct Lists {
   uint4 ring[kAhead][kPieces][kThreads];
-  unsigned long long list[kList + kMaxTop], best[kMaxTop], warp_best[kWarps];
-  int count;
+  unsigned long long list[2][kList + kMaxTop], warp_best[kWarps];  // two lists, in turn
+  uint4 piece[kList];
+  int piece_at[kList];
+  int count[2], piece_count;
   uint32_t bound[kWarps];
   Stats stats[kWarps];
 };
@@ -122,18 +124,15 @@ struct Lists {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The list's `top` largest keys, in falling order, to `best`, zeros behind them; the
-// whole CTA, ends with a barrier.
-__device__ __forceinline__ void rank_list(Lists& s, int n, int top) {
-  if (threadIdx.x < kMaxTop) s.best[threadIdx.x] = 0;
-  __syncthreads();
+// The `top` largest of a list's n keys, in falling order; 0 is none.
+__device__ __forceinline__ void rank_keys(const unsigned long long* list, int n, int top, unsigned long long* to) {
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const unsigned long long mine = s.list[i];
+    const unsigned long long mine = list[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += s.list[j] > mine;
-    if (rank < top) s.best[rank] = mine;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += list[j] > mine;
+    if (rank < top && mine) to[rank] = mine;
   }
-  __syncthreads();
 }
 
 __device__ __forceinline__ float no_infinity(float x) { return x == INFINITY ? FLT_MAX : x; }
@@ -234,8 +233,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   cluster_arrive();  // rank 0 has started before the others write to it
   const float x_token = one<DT>(row, token);
 
-  if (tid == 0) s.count = 0;
-  if (TOP && tid < kMaxTop) s.best[tid] = 0;  // a CTA of the single entries' share has no tile
+  if (tid == 0) s.count[0] = s.piece_count = 0;
   if (TOP) __syncthreads();
   float top_x = -INFINITY;  // the largest value so far,
   int top_tile = 0;         // the tile that it came with,
@@ -244,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   float2 t = make_float2(0.f, 0.f);
   uint32_t least = kOrderedLowest;  // what a candidate has to reach
   int slot = 0, batch = rank, seen = 0;  // the first tile since the last look at the list; tiles so far
+  int cur = 0;                           // the list in use
   for (int tile = rank; tile < tiles || tile == 0; tile += ranks) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     uint4 w[kPieces];
@@ -318,7 +317,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         }
       };
       const uint32_t u = ordered(fminf(big, FLT_MAX));
-      bool full = false;  // `top` values reach the bound
       if (tile == rank) {
         uint32_t left = u, bound = 0;
         for (int i = 0; i < (top + kWarps - 1) / kWarps; ++i) {
@@ -330,36 +328,49 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         bound = s.bound[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) bound = min(bound, s.bound[i]);
-        full = bound >= least;
-        if (full) least = bound;
+        least = max(least, bound);
       }
-      if (max(u, ordered(fmaxf(fminf(x_single, FLT_MAX), -INFINITY))) >= least) {
-        const float bar = unordered(least);
-        auto list = [&](float v, int at) {
-          if (v >= bar) {
-            const int i = atomicAdd(&s.count, 1);
-            if (i < kList) s.list[i] = key_of(no_infinity(v), at);
-          }
-        };
+      const float bar = unordered(least);
+      auto list = [&](float v, int at) {
+        if (v >= bar) {
+          const int i = atomicAdd(&s.count[cur], 1);
+          if (i < kList) s.list[cur][i] = key_of(no_infinity(v), at);
+        }
+      };
+      if (u >= least) {
+        int at = 0;
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j)
-          if (piece_big[j] >= bar) each(w[j], piece_of(tile, j), list);
-        if (single >= 0) list(x_single, single);
+        for (int j = 0; j < kPieces; ++j) at += piece_big[j] >= bar;
+        at = atomicAdd(&s.piece_count, at);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          if (piece_big[j] >= bar && at < kList) {
+            s.piece[at] = w[j];
+            s.piece_at[at++] = piece_of(tile, j);
+          }
+        }
       }
-      if (full) ++least;  // among equals the lower tokens, which are listed, come first
+      if (single >= 0) list(x_single, single);
       ++seen;
       if ((seen & (seen - 1)) == 0 || tile + ranks >= tiles) {
         const int from = batch;
         batch = tile + ranks;
+        unsigned long long *keys = s.list[cur], *next = s.list[cur ^ 1];
         __syncthreads();
-        const int n = s.count;
-        __syncthreads();
+        int n = s.piece_count;
+        if (n <= kList) {
+          for (int i = tid; i < n; i += kThreads) each(s.piece[i], s.piece_at[i], list);
+          __syncthreads();
+          n = s.count[cur];
+        }
         if (n > kList) {  // too many: the largest keys of the tiles since, one by one
           // What is listed of them, whose tokens are higher than earlier ones', is not the
           // lot, and goes.
           const uint32_t first = from == 0 ? 0 : head + from * (kPieces * kThreads * kEach);
+          const int have = s.count[cur];
           for (int i = tid; i < kList; i += kThreads)
-            if (~(uint32_t)s.list[i] >= first) s.list[i] = 0;
+            if (i >= have || ~(uint32_t)keys[i] >= first) keys[i] = 0;
+          if (tid < kMaxTop) next[tid] = 0;
           __syncthreads();
           unsigned long long last = ~0ull;
           int found = 0;
@@ -390,19 +401,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
             for (int i = 1; i < kWarps; ++i) k = s.warp_best[i] > k ? s.warp_best[i] : k;
             __syncthreads();
             if (k == 0) break;
-            if (tid == 0) s.list[kList + found] = k;
+            if (tid == 0) keys[kList + found] = k;
             last = k;
           }
-          if (tid == 0) s.count = kList + found;
           __syncthreads();
+          rank_keys(keys, kList + found, top, next);
+          __syncthreads();
+          n = __syncthreads_count(tid < top && next[tid] != 0);
+        } else {
+          rank_keys(keys, n, top, next);
         }
-        const int have = s.count;
-        rank_list(s, have, top);
-        if (tid < kMaxTop) s.list[tid] = s.best[tid];
-        const unsigned long long kth = s.best[top - 1];
-        if (kth) least = max(least, (uint32_t)(kth >> 32) + 1);
-        if (tid == 0) s.count = min(have, top);
+        cur ^= 1;
+        if (tid == 0) s.count[cur] = min(n, top), s.piece_count = 0;
         __syncthreads();
+        if (n >= top) least = max(least, (uint32_t)(next[top - 1] >> 32) + 1);
       }
     }
   }
@@ -445,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     }
     if (lane == 0) s.stats[warp] = Stats{m, r + mine, all_t};
   }
-  __syncthreads();  // (`best` holds the last tile's look at the list)
+  __syncthreads();
   cluster_wait();
   Joined* to = cluster.map_shared_rank(&joined, 0);
-  if (TOP && tid < kMaxTop) to->keys[rank][tid] = s.best[tid];
+  // (the last tile's look at the list; a CTA of the single entries' share has no tile)
+  if (TOP && tid < kMaxTop) to->keys[rank][tid] = tid < s.count[cur] ? s.list[cur][tid] : 0;
   if (warp == 0) {
     const Stats all = warp_join(lane < kWarps ? s.stats[lane] : Stats{-INFINITY, 0.f, 0.f});
     if (lane == 0) to->stats[rank] = all;
