@@ -111,6 +111,13 @@ __device__ __forceinline__ float one(const void* row, int64_t i) {
   return DT == KDA_DTYPE_F16 ? in16_to_float<true>(b) : in16_to_float<false>(b);
 }
 
+template <int DT>
+__device__ __forceinline__ float shared_one(const void* from, int i) {
+  if (DT == KDA_DTYPE_F32) return static_cast<const float*>(from)[i];
+  const uint16_t b = static_cast<const uint16_t*>(from)[i];
+  return DT == KDA_DTYPE_F16 ? in16_to_float<true>(b) : in16_to_float<false>(b);
+}
+
 struct Lists {
   uint4 ring[kAhead][kPieces][kThreads];
   unsigned long long list[2][kList + kMaxTop], warp_best[kWarps];  // two lists, in turn
@@ -359,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         __syncthreads();
         int n = s.piece_count;
         if (n <= kList) {
-          for (int i = tid; i < n; i += kThreads) each(s.piece[i], s.piece_at[i], list);
+          for (int i = tid; i < n * kEach; i += kThreads)  // an entry a thread
+            list(shared_one<DT>(s.piece, i), head + s.piece_at[i / kEach] * kEach + i % kEach);
           __syncthreads();
           n = s.count[cur];
         }
