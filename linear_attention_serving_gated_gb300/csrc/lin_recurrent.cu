@@ -78,23 +78,29 @@ __global__ void __launch_bounds__(128) lin_recurrent_kernel(const LinStepArgs ar
   const int64_t t0 = (int64_t)r * args.T;
   const int T = MODE == kLinDecode ? 1 : args.T;
 
-  auto load = [&](int t, Token<GROUPS>& x) {
-    const int64_t row = t0 + t;
-    const kda_bf16* q = args.q + row * args.q_stride + (h / args.G) * K + sub * 4;
-    const kda_bf16* k = args.k + row * args.k_stride + (h / args.G) * K + sub * 4;
-    const kda_bf16* v = args.v + row * args.v_stride + h * V;
+  // tokens come one after the other: pointers that go on a row a step
+  const kda_bf16* kp = args.k + t0 * args.k_stride + (h / args.G) * K + sub * 4;
+  const kda_bf16* qp = args.q + t0 * args.q_stride + (h / args.G) * K + sub * 4;
+  const kda_bf16* vp = args.v + t0 * args.v_stride + h * V + row0;
+  const int32_t* pp = args.parent + t0;
+  int64_t gate_at = t0 * HV + h;
+  auto load = [&](Token<GROUPS>& x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x.k[i] = __ldg(reinterpret_cast<const uint2*>(k + i * 32));
-      x.q[i] = __ldg(reinterpret_cast<const uint2*>(q + i * 32));
+      x.k[i] = __ldg(reinterpret_cast<const uint2*>(kp + i * 32));
+      x.q[i] = __ldg(reinterpret_cast<const uint2*>(qp + i * 32));
     }
 #pragma unroll
-    for (int gi = 0; gi < GROUPS; ++gi) x.v[gi] = __ldg(v + row0 + gi * 4);
-    x.a = lin_gate_load(args.gate, row * HV + h);
-    if (MODE == kLinTree) x.parent = __ldg(args.parent + row);
+    for (int gi = 0; gi < GROUPS; ++gi) x.v[gi] = __ldg(vp + gi * 4);
+    x.a = lin_gate_load(args.gate, gate_at);
+    if (MODE == kLinTree) x.parent = __ldg(pp++);
+    if (MODE != kLinDecode) {
+      kp += args.k_stride, qp += args.q_stride, vp += args.v_stride;
+      gate_at += HV;
+    }
   };
   Token<GROUPS> next;
-  load(0, next);
+  load(next);
   const LinGateArgs& ga = args.gate;
   const float neg_rate = ga.A_log ? -expf(ga.A_log[h]) : 0.f;
   const float bias = ga.dt_bias ? ga.dt_bias[h] : 0.f;
@@ -153,16 +159,19 @@ __global__ void __launch_bounds__(128) lin_recurrent_kernel(const LinStepArgs ar
       }
   };
   load_state(root);
+  kda_bf16* o = args.o + (t0 * HV + h) * V + row0;
+  float* snapshot = args.snapshots + ((size_t)t0 * HV + h) * head_elems + (size_t)row0 * K + sub * 4;
 
+  constexpr int kUnroll = GROUPS == 1 && MODE != kLinDecode ? 2 : 1;
+#pragma unroll kUnroll
   for (int t = 0; t < T; ++t) {
     const Token<GROUPS> x = next;
-    if (t + 1 < T) load(t + 1, next);
-    const int64_t row = t0 + t;
+    if (t + 1 < T) load(next);
     if (MODE == kLinTree && t > 0) {
       const int p = x.parent;
       // the parent's snapshot was written by this same thread
       if (p != t - 1)
-        load_state(p < 0 ? root : args.snapshots + (((size_t)t0 + p) * HV + h) * head_elems + (size_t)row0 * K + sub * 4);
+        load_state(p < 0 ? root : snapshot - (int64_t)(t - p) * (HV * (int64_t)head_elems));
     }
     float4 q[4], k[4];
 #pragma unroll
@@ -194,11 +203,12 @@ __global__ void __launch_bounds__(128) lin_recurrent_kernel(const LinStepArgs ar
         S[gi][i] = make_float4(lo.x, lo.y, hi.x, hi.y);
       }
       if (sub == 0)
-        args.o[(row * HV + h) * V + row0 + gi * 4] = float_to_out16<F16>(rq * (alpha * red[3 + gi] + c * red[2]));
+        (MODE == kLinDecode ? args.o + (t0 * HV + h) * V + row0 : o)[gi * 4] = float_to_out16<F16>(rq * (alpha * red[3 + gi] + c * red[2]));
     }
     if (MODE == kLinChain || MODE == kLinTree)
-      store_state(args.snapshots + ((size_t)row * HV + h) * head_elems + (size_t)row0 * K + sub * 4,
-                  t >= 32 || (keep >> t & 1u));
+      store_state(snapshot, t >= 32 || (keep >> t & 1u));
+    o += HV * V;
+    snapshot += HV * head_elems;
   }
   if (MODE == kLinDecode) store_state(root, false);
 }
