@@ -193,3 +193,25 @@ def test_all_but_certain_tokens(dtype, vocab):
     for name, g, w in (("logprobs", got[0], want), ("entropy", got[1], entropy), ("top_logprobs", got[3][:, 0], want)):
         off = ((g.double().cpu() - w).abs() / w.abs().clamp(min=1e-30)).max().item()
         assert off <= 2.0 ** -17, f"{name}: {off:.2e}"
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_candidates_late_in_long_rows(dtype):
+    """Rows of many tiles, a CTA a row (504 rows), whose candidates come late, in crowds, in
+    equal values or between entries without a probability."""
+    vocab, top = 70000, 32  # (rows that start alike are summed alike)
+    i = torch.arange(vocab)
+    gen = torch.Generator().manual_seed(9)
+    x = torch.zeros(6, vocab)
+    x[0] = i / vocab * 50  # rising: all of it
+    x[1] = torch.where(i < 40000, torch.randn(vocab, generator=gen), 5.0)  # equal ones behind 40000 others
+    x[2] = torch.randn(vocab, generator=gen) + (i // 8192).float()  # each tile above the one before
+    x[3] = torch.where(torch.rand(vocab, generator=gen) < 0.6, -torch.inf, torch.randn(vocab, generator=gen) * 4)
+    x[4] = torch.where(i % 4096 < 600, 30.0 + (i // 30000).float(), 0.0)  # crowds of equal ones
+    x[5] = torch.where(i > vocab - 20, 1.0, -torch.inf)  # fewer than asked for, at the end
+    x = x.to(DT[dtype])
+    tokens = [vocab - 1, 3, 65000, 7, 60000, vocab - 2]
+    got = run(x.cuda().repeat(84, 1), tokens * 84, top)
+    for g in got:
+        assert torch.equal(g.view(84, 6, *g.shape[1:]), g[:6].expand(84, 6, *g.shape[1:]))
+    compare(x, tokens, top, [g[:6] for g in got])
