@@ -1,4 +1,6 @@
-"""Builds libkda.so in-tree from csrc/*.cu for sm_103a with nvcc.
+"""Builds libkda.so in-tree from csrc/*.cu for sm_103a with nvcc, and the binding's
+checks of arguments, _host_args.so, from csrc/host_args.cpp with g++ and PyTorch's
+headers.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library next to this file.  Rebuilds only when a source is newer than the
@@ -10,11 +12,13 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
+HOST = os.path.join(HERE, "_host_args.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -29,15 +33,26 @@ def _nvcc() -> str:
 def _sources():
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
-    deps.append(os.path.join(os.path.dirname(HERE), "include", "kda.h"))
+    deps += [os.path.join(os.path.dirname(HERE), "include", "kda.h"), os.path.join(CSRC, "host_args.cpp")]
     return srcs, deps
 
 
+def _host_command(out):
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"], "-I", include,
+            "-I", os.path.join(include, "torch", "csrc", "api", "include"), os.path.join(CSRC, "host_args.cpp"), "-o", out,
+            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(HOST):
         return True
     _, deps = _sources()
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
@@ -55,15 +70,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 print(" ".join(cmd))
             procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        host = os.path.join(tmp, "_host_args.so")
+        cmd = _host_command(host)
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         failed = []
         for cmd, p in procs:
             out, _ = p.communicate()
             if p.returncode != 0:
                 failed.append((cmd, out.decode(errors="replace")))
         if failed:
-            raise RuntimeError("nvcc failed:\n" + "\n".join(" ".join(c) + "\n" + o for c, o in failed))
+            raise RuntimeError("compilation failed:\n" + "\n".join(" ".join(c) + "\n" + o for c, o in failed))
         tmp_lib = os.path.join(tmp, "libkda.so")
         subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp_lib, *objs])
+        shutil.move(host, HOST)
         os.replace(tmp_lib, LIB) if os.path.dirname(tmp_lib) == os.path.dirname(LIB) else shutil.move(tmp_lib, LIB)
     return LIB
 

@@ -89,10 +89,14 @@ _lib = None
 
 def load(path: str = LIB_PATH):
     """Load libkda.so (built by build.py).  Raises if it is missing."""
-    global _lib
+    global _lib, _arg
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError(f"libkda.so not built ({path}); run linear_attention_serving_gated_gb300.build.build()")
+        from . import _host_args  # built beside it
+
+        _host_args.otherwise(_checked_arg)
+        _arg = _host_args.arg
         lib = ctypes.CDLL(path)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
         lib.kda_status_string.restype = ctypes.c_char_p
@@ -438,9 +442,10 @@ def kda_set_stage_events(events=None):
 # for pointers, and the current stream without a Python stream object.
 
 
-def _arg(t, dtype, n, name, shape):
+def _checked_arg(t, dtype, n, name, shape):
     """Device pointer of a dense tensor of one element type that holds at least n
-    elements (the rows the kernels touch)."""
+    elements (the rows the kernels touch), or what is wrong with it.  load() puts
+    native code in front of it, as _arg."""
     if t.dtype is not dtype and not (t.dtype is torch.int16 and dtype in _BITS16):
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.numel() < n or not t.is_contiguous():
@@ -450,6 +455,7 @@ def _arg(t, dtype, n, name, shape):
     return t.data_ptr()
 
 
+_arg = _checked_arg
 _BITS16 = (torch.bfloat16, torch.float16)  # raw int16 bits are accepted for either
 
 
