@@ -1,9 +1,13 @@
-// host_args.cpp -- the binding's check of one tensor argument, in native code.
+// host_args.cpp -- the binding's checks of a tensor argument, in native code.
 //
 // arg(t, dtype, n, name, shape) -> device pointer of a dense CUDA tensor of one element
 // type that holds at least n elements (int16 holds the bits of either 16-bit type).
 // Anything else goes to the function given to otherwise(), which says what is wrong.  From
 // Python the five questions take 0.35 us a tensor, and a call has six to ten; here 0.1.
+//
+// rows(t, dtype, n, width) -> (device pointer, row stride) of at least n rows of at least
+// `width` elements that lie together; states(t, HV, V, K) -> (device pointer, slots) of a
+// dense FP32 pool [slots, HV, V, K].  Both give None where t is no such thing.
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -12,18 +16,24 @@ namespace {
 
 PyObject* other = nullptr;
 
+bool number(PyObject* n, long long* out) {
+  *out = PyLong_AsLongLong(n);
+  if (*out != -1 || !PyErr_Occurred()) return true;
+  PyErr_Clear();
+  return false;
+}
+
+bool of_type(const at::Tensor& x, PyObject* dtype) {
+  const at::ScalarType want = reinterpret_cast<THPDtype*>(dtype)->scalar_type, have = x.scalar_type();
+  return have == want || (have == at::kShort && (want == at::kHalf || want == at::kBFloat16));
+}
+
 bool pointer_of(PyObject* t, PyObject* dtype, PyObject* n, void** out) {
-  if (!THPVariable_Check(t) || !THPDtype_Check(dtype)) return false;
-  const long long least = PyLong_AsLongLong(n);
-  if (least == -1 && PyErr_Occurred()) {
-    PyErr_Clear();
-    return false;
-  }
+  long long least;
+  if (!THPVariable_Check(t) || !THPDtype_Check(dtype) || !number(n, &least)) return false;
   try {
     const at::Tensor& x = THPVariable_Unpack(t);
-    const at::ScalarType want = reinterpret_cast<THPDtype*>(dtype)->scalar_type, have = x.scalar_type();
-    const bool bits = have == at::kShort && (want == at::kHalf || want == at::kBFloat16);
-    if ((have != want && !bits) || !x.is_cuda() || !x.is_contiguous() || x.numel() < least) return false;
+    if (!of_type(x, dtype) || !x.is_cuda() || !x.is_contiguous() || x.numel() < least) return false;
     *out = x.data_ptr();
     return true;
   } catch (...) {  // a tensor without memory of its own
@@ -38,6 +48,42 @@ PyObject* arg(PyObject*, PyObject* const* args, Py_ssize_t count) {
   return PyObject_Vectorcall(other, args, (size_t)count, nullptr);
 }
 
+PyObject* pair(void* p, long long n) {
+  PyObject* pointer = PyLong_FromVoidPtr(p);
+  PyObject* value = PyLong_FromLongLong(n);
+  PyObject* both = pointer && value ? PyTuple_Pack(2, pointer, value) : nullptr;
+  Py_XDECREF(pointer);
+  Py_XDECREF(value);
+  return both;
+}
+
+PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  long long n, width;
+  if (count == 4 && THPVariable_Check(args[0]) && THPDtype_Check(args[1]) && number(args[2], &n) && number(args[3], &width)) {
+    try {
+      const at::Tensor& x = THPVariable_Unpack(args[0]);
+      if (of_type(x, args[1]) && x.is_cuda() && x.dim() == 2 && x.size(0) >= n && x.size(1) >= width && x.stride(1) == 1)
+        return pair(x.data_ptr(), x.stride(0));
+    } catch (...) {
+    }
+  }
+  Py_RETURN_NONE;
+}
+
+PyObject* states(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  long long want[3];
+  if (count == 4 && THPVariable_Check(args[0]) && number(args[1], want) && number(args[2], want + 1) && number(args[3], want + 2)) {
+    try {
+      const at::Tensor& x = THPVariable_Unpack(args[0]);
+      if (x.scalar_type() == at::kFloat && x.is_cuda() && x.dim() == 4 && x.size(1) == want[0] && x.size(2) == want[1] &&
+          x.size(3) == want[2] && x.is_contiguous())
+        return pair(x.data_ptr(), x.size(0));
+    } catch (...) {
+    }
+  }
+  Py_RETURN_NONE;
+}
+
 PyObject* otherwise(PyObject*, PyObject* f) {
   Py_INCREF(f);
   Py_XSETREF(other, f);
@@ -46,6 +92,8 @@ PyObject* otherwise(PyObject*, PyObject* f) {
 
 PyMethodDef methods[] = {
     {"arg", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(arg)), METH_FASTCALL, nullptr},
+    {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rows)), METH_FASTCALL, nullptr},
+    {"states", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(states)), METH_FASTCALL, nullptr},
     {"otherwise", otherwise, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

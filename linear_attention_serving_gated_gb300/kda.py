@@ -89,14 +89,14 @@ _lib = None
 
 def load(path: str = LIB_PATH):
     """Load libkda.so (built by build.py).  Raises if it is missing."""
-    global _lib, _arg
+    global _lib, _arg, _rows, _states
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError(f"libkda.so not built ({path}); run linear_attention_serving_gated_gb300.build.build()")
         from . import _host_args  # built beside it
 
         _host_args.otherwise(_checked_arg)
-        _arg = _host_args.arg
+        _arg, _rows, _states = _host_args.arg, _host_args.rows, _host_args.states
         lib = ctypes.CDLL(path)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
         lib.kda_status_string.restype = ctypes.c_char_p
@@ -455,6 +455,19 @@ def _checked_arg(t, dtype, n, name, shape):
     return t.data_ptr()
 
 
+def _rows(t, dtype, n, width):
+    """(device pointer, row stride) of at least n rows of `width` elements; None: not such
+    a tensor (or load() has not put native code here yet)."""
+
+
+def _states(t, HV, V, K):
+    """(device pointer, slots) of a dense FP32 pool [slots, HV, V, K]; None as in _rows."""
+
+
+def _pool(d, t, HV, V, K):
+    return _states(t, HV, V, K) or (_arg(t, torch.float32, 0, "state_pool", "[slots, HV, V, K]"), _pool_slots(d, t))
+
+
 _arg = _checked_arg
 _BITS16 = (torch.bfloat16, torch.float16)  # raw int16 bits are accepted for either
 
@@ -752,7 +765,7 @@ def kda_pool_fork(pool, used, table, parents, rows, children=None, err_flag=None
 # -- linear attention with one decay per value head ---------------------------
 
 
-_F32, _I32, _I16 = torch.float32, torch.int32, torch.int16
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _lin_gate(gate, a, rows, HV, t16):
@@ -771,17 +784,12 @@ def _lin_gate(gate, a, rows, HV, t16):
 def _lin_packed(d, gate, mixed_qkv, a, rows, B, state_pool, state_idx, o):
     """What the packed calls have in common, checked: the arguments up to the gate
     input, the pool and what goes with it, and a token's values."""
+    load()
     H, HV, K, V, t16 = d.H, d.HV, d.K, d.V, _t16(d)
-    shape, strides, dtype = mixed_qkv.shape, mixed_qkv.stride(), mixed_qkv.dtype
-    if len(shape) != 2 or shape[0] < rows or shape[1] < 2 * H * K + HV * V or strides[1] != 1 or not mixed_qkv.is_cuda or \
-            (dtype is not t16 and dtype is not _I16):
-        _gdn_rows(d, mixed_qkv, rows)  # says what is wrong
+    qkv = _rows(mixed_qkv, t16, rows, 2 * H * K + HV * V) or (_gdn_rows(d, mixed_qkv, rows), mixed_qkv.stride(0))
     g, gate_rows = _lin_gate(gate, a, rows, HV, t16)
-    slots = state_pool.shape
-    if len(slots) != 4 or slots[1] != HV or slots[2] != V or slots[3] != K:
-        _pool_slots(d, state_pool)
-    return (d, g, mixed_qkv.data_ptr(), strides[0], gate_rows), \
-        (_arg(state_pool, _F32, 0, "state_pool", "[slots, HV, V, K]"), slots[0], _arg(state_idx, _I32, B, "state_idx", "[B]"),
+    return (d, g, *qkv, gate_rows), \
+        (*_pool(d, state_pool, HV, V, K), _arg(state_idx, _I32, B, "state_idx", "[B]"),
          _arg(o, t16, rows * HV * V, "o", "[rows, HV, V]")), HV * V * K
 
 
@@ -798,7 +806,7 @@ def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_s
     T, n = q.shape[0], int(num_seqs)
     gate_rows = T if a is None else a.shape[0]
     HK, HVV = d.H * d.K, HV * V
-    slots = _pool_slots(d, state_pool)
+    pool = _pool(d, state_pool, HV, V, d.K)
     g, rows = _lin_gate(gate, a, gate_rows, HV, t16)
     size = 0
     if workspace is None:
@@ -810,7 +818,7 @@ def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_s
     st = lib.kda_lin_prefill(
         d, g, _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
         _arg(v, t16, T * HVV, "v", "[T, HV, V]"), rows, gate_rows,
-        _arg(state_pool, _F32, 0, "state_pool", "[slots, HV, V, K]"), slots, _arg(state_idx, _I32, n, "state_idx", "[num_seqs]"),
+        *pool, _arg(state_idx, _I32, n, "state_idx", "[num_seqs]"),
         None if cu_seqlens is None else _arg(cu_seqlens, _I32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
         _arg(o, t16, T * HVV, "o", "[T, HV, V]"), None if workspace is None else workspace.data_ptr(), size, _err(err_flag),
         _cur(stream))
@@ -866,14 +874,20 @@ def kda_token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, 
         raise ValueError(f"logits must be [rows, vocab] and tokens [rows] (got {tuple(shape)}, {tuple(tokens.shape)})")
     if dtype is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
-    rows, V = shape
-    stride, unit = logits.stride()
+    lib, (rows, V) = load(), shape
+    at = _rows(logits, logits.dtype, rows, V)
+    if at is None:  # (rows of one token may be apart)
+        unit = logits.stride(1)
+        if not logits.is_cuda:
+            raise ValueError("libkda takes device tensors")
+        if V > 1 and unit != 1:
+            raise ValueError(f"the rows of logits must be dense (got strides {logits.stride()})")
+        at = logits.data_ptr(), logits.stride(0)
+    x, stride = at
     if rows <= 1:
         stride = V
-    if (V > 1 and unit != 1) or stride < V:
+    if stride < V:
         raise ValueError(f"the rows of logits must be dense (got strides {logits.stride()})")
-    if not logits.is_cuda:
-        raise ValueError("libkda takes device tensors")
     top, best, best_lp = 0, None, None
     if top_tokens is not None or top_logprobs is not None:
         if top_tokens is None or top_logprobs is None or top_tokens.dim() != 2 or top_tokens.shape != top_logprobs.shape or \
@@ -882,8 +896,8 @@ def kda_token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, 
         top = top_tokens.shape[1]
         best = _arg(top_tokens, _I32, rows * top, "top_tokens", "[rows, top]")
         best_lp = _arg(top_logprobs, _F32, rows * top, "top_logprobs", "[rows, top]")
-    st = load().kda_token_logprobs(
-        dtype, logits.data_ptr(), stride, _arg(tokens, _I32, rows, "tokens", "[rows]"), rows, V,
+    st = lib.kda_token_logprobs(
+        dtype, x, stride, _arg(tokens, _I32, rows, "tokens", "[rows]"), rows, V,
         _arg(logprobs, _F32, rows, "logprobs", "[rows]"),
         None if entropy is None else _arg(entropy, _F32, rows, "entropy", "[rows]"), top, best, best_lp, _err(err_flag),
         _cur(stream))
