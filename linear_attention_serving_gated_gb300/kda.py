@@ -93,8 +93,10 @@ def load(path: str = LIB_PATH):
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError(f"libkda.so not built ({path}); run linear_attention_serving_gated_gb300.build.build()")
-        from . import _host_args  # built beside it
-
+        try:
+            from . import _host_args  # built beside it
+        except ImportError as e:
+            raise RuntimeError("_host_args.so not built; run linear_attention_serving_gated_gb300.build.build()") from e
         _host_args.otherwise(_checked_arg)
         _arg, _rows, _states = _host_args.arg, _host_args.rows, _host_args.states
         lib = ctypes.CDLL(path)
