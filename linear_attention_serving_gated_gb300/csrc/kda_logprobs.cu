@@ -24,8 +24,9 @@
 // them, as keys that no two entries share (the value's bits in an order of their own, then
 // the token's complement, so that among equals the lowest token comes first), ranks these,
 // a key's rank being the number of larger ones, and keeps the top largest: the last of them
-// is the new bound.  Tiles with more than the lists have room for (rows of one value) are
-// searched key by key instead.
+// is the new bound.  Tiles with more than the lists have room for (rising values, or one
+// value) are read again, twice: for a bound from each thread's largest key, and for the
+// keys that reach it.
 //
 // A row is split over the CTAs of a cluster where there are few rows; rank 0 joins
 // what the others leave in its shared memory.
@@ -371,49 +372,77 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
           __syncthreads();
           n = s.count[cur];
         }
-        if (n > kList) {  // too many: the largest keys of the tiles since, one by one
-          // What is listed of them, whose tokens are higher than earlier ones', is not the
-          // lot, and goes.
+        if (n > kList) {  // too many: the tiles since are read again
+          // What is listed of them, whose tokens are higher than earlier ones', is not the lot.
           const uint32_t first = from == 0 ? 0 : head + from * (kPieces * kThreads * kEach);
-          const int have = s.count[cur];
-          for (int i = tid; i < kList; i += kThreads)
-            if (i >= have || ~(uint32_t)keys[i] >= first) keys[i] = 0;
-          if (tid < kMaxTop) next[tid] = 0;
-          __syncthreads();
-          unsigned long long last = ~0ull;
-          int found = 0;
-          for (; found < top; ++found) {
-            unsigned long long k = 0;
-            auto best = [&](float v, int at) {
-              if (v >= -FLT_MAX) {
-                const unsigned long long key = key_of(no_infinity(v), at);
-                if (key < last && key > k) k = key;
-              }
+          const int have = min(s.count[cur], kList);
+          auto again = [&](auto&& f) {  // their keys
+            auto entry = [&](float v, int at) {
+              if (v >= -FLT_MAX) f(key_of(no_infinity(v), at));
             };
 #pragma unroll 1
             for (int t = from; t <= tile; t += ranks)
 #pragma unroll 1
               for (int j = 0; j < kPieces; ++j)
-                if (piece_of(t, j) < pieces) each(__ldg(body + piece_of(t, j)), piece_of(t, j), best);
+                if (piece_of(t, j) < pieces) each(__ldg(body + piece_of(t, j)), piece_of(t, j), entry);
             // the single entries: of the first tile, or of the last one
-            if (rank == 0 && from == 0 && tid < head) best(one<DT>(row, tid), tid);
-            if (single >= head) best(x_single, single);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) {
-              const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
-              k = o > k ? o : k;
-            }
-            if (lane == 0) s.warp_best[warp] = k;
-            __syncthreads();
-            k = s.warp_best[0];
-            for (int i = 1; i < kWarps; ++i) k = s.warp_best[i] > k ? s.warp_best[i] : k;
-            __syncthreads();
-            if (k == 0) break;
-            if (tid == 0) keys[kList + found] = k;
-            last = k;
-          }
+            if (rank == 0 && from == 0 && tid < head) entry(one<DT>(row, tid), tid);
+            if (single >= head) entry(x_single, single);
+          };
+          // The top-th largest of the threads' largest keys bounds them.
+          unsigned long long *largest = reinterpret_cast<unsigned long long*>(s.piece), *some = largest + kThreads;
+          constexpr int kSome = (int)(sizeof(s.piece) / 8) - kThreads;
+          unsigned long long mine = 0;
+          again([&](unsigned long long key) { mine = key > mine ? key : mine; });
+          largest[tid] = mine;
+          if (tid < kMaxTop) next[tid] = 0;
+          if (tid == 0) s.piece_count = 0, s.warp_best[0] = 0;
           __syncthreads();
-          rank_keys(keys, kList + found, top, next);
+          int larger = 0;
+          for (int i = 0; i < kThreads; ++i) larger += largest[i] > mine;
+          if (mine && larger == top - 1) s.warp_best[0] = mine;
+          __syncthreads();
+          const unsigned long long bound = s.warp_best[0];
+          auto take = [&](unsigned long long key) {
+            const int i = atomicAdd(&s.piece_count, 1);
+            if (i < kSome) some[i] = key;
+          };
+          again([&](unsigned long long key) {
+            if (key >= bound) take(key);
+          });
+          for (int i = tid; i < have; i += kThreads)
+            if (~(uint32_t)keys[i] < first) take(keys[i]);
+          __syncthreads();
+          n = s.piece_count;
+          if (n <= kSome) {
+            rank_keys(some, n, top, next);
+          } else {  // (a few threads have them all) the largest key, and again
+            for (int i = tid; i < kList; i += kThreads)
+              if (i >= have || ~(uint32_t)keys[i] >= first) keys[i] = 0;
+            unsigned long long last = ~0ull;
+            int found = 0;
+            for (; found < top; ++found) {
+              unsigned long long k = 0;
+              again([&](unsigned long long key) {
+                if (key < last && key > k) k = key;
+              });
+#pragma unroll
+              for (int d = 16; d; d >>= 1) {
+                const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
+                k = o > k ? o : k;
+              }
+              __syncthreads();
+              if (lane == 0) s.warp_best[warp] = k;
+              __syncthreads();
+              k = s.warp_best[0];
+              for (int i = 1; i < kWarps; ++i) k = s.warp_best[i] > k ? s.warp_best[i] : k;
+              if (k == 0) break;
+              if (tid == 0) keys[kList + found] = k;
+              last = k;
+            }
+            __syncthreads();
+            rank_keys(keys, kList + found, top, next);
+          }
           __syncthreads();
           n = __syncthreads_count(tid < top && next[tid] != 0);
         } else {

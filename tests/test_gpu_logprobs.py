@@ -202,16 +202,18 @@ def test_candidates_late_in_long_rows(dtype):
     vocab, top = 70000, 32  # (rows that start alike are summed alike)
     i = torch.arange(vocab)
     gen = torch.Generator().manual_seed(9)
-    x = torch.zeros(6, vocab)
+    x = torch.zeros(8, vocab)
     x[0] = i / vocab * 50  # rising: all of it
     x[1] = torch.where(i < 40000, torch.randn(vocab, generator=gen), 5.0)  # equal ones behind 40000 others
     x[2] = torch.randn(vocab, generator=gen) + (i // 8192).float()  # each tile above the one before
     x[3] = torch.where(torch.rand(vocab, generator=gen) < 0.6, -torch.inf, torch.randn(vocab, generator=gen) * 4)
     x[4] = torch.where(i % 4096 < 600, 30.0 + (i // 30000).float(), 0.0)  # crowds of equal ones
     x[5] = torch.where(i > vocab - 20, 1.0, -torch.inf)  # fewer than asked for, at the end
+    for r, n in ((6, 4), (7, 8)):  # crowds that 31 threads of 256 read
+        x[r] = torch.where(i // n % 256 < 31, 10 + i / vocab, torch.rand(vocab, generator=gen))
     x = x.to(DT[dtype])
-    tokens = [vocab - 1, 3, 65000, 7, 60000, vocab - 2]
-    got = run(x.cuda().repeat(84, 1), tokens * 84, top)
+    tokens = [vocab - 1, 3, 65000, 7, 60000, vocab - 2, 9, 11]
+    got = run(x.cuda().repeat(63, 1), tokens * 63, top)
     for g in got:
-        assert torch.equal(g.view(84, 6, *g.shape[1:]), g[:6].expand(84, 6, *g.shape[1:]))
-    compare(x, tokens, top, [g[:6] for g in got])
+        assert torch.equal(g.view(63, 8, *g.shape[1:]), g[:8].expand(63, 8, *g.shape[1:]))
+    compare(x, tokens, top, [g[:8] for g in got])
