@@ -14,8 +14,8 @@
 // its state in FP32 registers.  Every product but Q K^T is transposed, so that its
 // rows are the value columns:
 //   Q K^T             64 x 64 x 128
-//   O1^T = S^T Q^T   128 x 64 x 128, S^T a left operand from TMEM
-//   O2^T = V^T P^T   128 x 64 x 64, V as it landed
+//   O1^T = S^T Q^T   128 x 64 x 128, S^T a left operand from TMEM, in two halves
+//   O2^T = V^T P^T   128 x 64 x 64, V as it landed, P in two halves
 //   dS^T = V^T K'    128 x 128 x 64, K'_j = e^(c_last - c_j) rk_j k_j in three parts
 //                    (FP16: two)
 // 16 warps do all the arithmetic, together and a step of it at a time, since what they
@@ -26,10 +26,10 @@
 // before it is needed.  One warp loads rows, one issues products, two make the factors
 // of the decays, four those of the norms.
 //
-// Bound by the workers' instructions: 4400 cycles a chunk, of which the products take
-// 1500 and shared memory 2500, and 2200 in the first launch.  1 x 4096 tokens at 16
-// heads 43 us (69 MB: 1.6 TB/s), 8 x 4096 149 us (3.7 TB/s), 16 980 tokens in eight
-// sequences 122 us; 1 x 128 at 4 heads 11 us, a third of it a CTA's start.
+// Bound by the workers' instructions: 4800 cycles a chunk, in the shadow of which are the
+// products, and 2200 in the first launch.  1 x 4096 tokens at 16 heads 44 us (69 MB:
+// 1.6 TB/s), 8 x 4096 162 us (3.4 TB/s), 16 980 tokens in eight sequences 126 us;
+// 1 x 128 at 4 heads 11 us, a third of it a CTA's start.
 //
 // A long sequence is cut into segments: a first launch computes what each segment
 // adds to a state of zero (no queries, no outputs), and the CTAs of the second sum
@@ -38,10 +38,11 @@
 //
 // Precision.  The state is FP32, in registers and in the pool.  K' is split in three
 // BF16 parts, 2^-26 of it left, or two FP16 ones, 2^-23, so that states are as exact as
-// FP32 sums leave them.  S^T and P as operands are rounded once to the outputs' type:
-// an output, which is rounded itself, comes out up to sqrt 2 times as far off as by its
-// own rounding alone (halves of both took a fifth more time).  FP16's range is kept by a
-// power of two for each row of P and of S^T.
+// FP32 sums leave them.  S^T and P as operands are halves hi + lo of the outputs' type,
+// 2^-18 (FP16: 2^-22) of them left, so that an output is as exact as its own rounding.
+// (Rounded once, they made outputs up to sqrt 2 times as far off, for 4 to 9% less time:
+// the second halves' instructions, not their products.)  FP16's range is kept by a power
+// of two for each row of P and of S^T.
 #include <atomic>
 
 #include "kda_host.h"
@@ -92,7 +93,9 @@ struct Scalars {
 };
 constexpr float kFar = 60.f;
 
-// Warps.
+// Warps.  Who waits for whom is run in a model, with the places that are written and read:
+// tests/test_lin_handover_cpu.py and tests/test_lin_handover_halves_cpu.py (the second
+// launch).  A change of the hand-overs here goes there too.
 constexpr int kWorkers = 16, kRowWarp = 16, kMmaWarp = 17, kGateWarp = 18, kNormWarp = 20, kNormWarps = 4, kThreads = 768;
 
 struct Bars {
@@ -102,11 +105,10 @@ struct Bars {
   uint64_t in_full[kScalarBufs];     // rows and all factors
   uint64_t sc_free[kScalarBufs];     // factors read
   uint64_t wk_full[2];               // operands: K' (and what else a chunk needs), chunks in turn,
-  uint64_t u_full, s_full[2];        // dS is in registers; S^T, chunks in turn
-  uint64_t p_full;                   // P
+  uint64_t u_full, p_full;           // dS is in registers; S^T and P
   uint64_t ds_full[2];               // products: dS, chunks in turn,
-  uint64_t qk_full;                  // Q K^T (and the last O1 and O2)
-  uint64_t o_full;                   // the segment's last O2
+  uint64_t qk_full;                  // Q K^T
+  uint64_t o_full;                   // O1 and O2
   uint64_t drained;                  // all products
   uint64_t state_full, state_read;   // the pool's state landed, and is in registers
   uint32_t tmem;
@@ -117,7 +119,7 @@ struct Bars {
 };
 
 // Shared memory: stages of Q, K and V (two halves of 64 channels and 64 lines each),
-// the parts of K', P and 8 KB, factors, barriers.  The pool's state lands, in four boxes of
+// the parts of K', P's halves, factors, barriers.  The pool's state lands, in four boxes of
 // 32 key channels, where chunk 2's rows (LOCAL: chunk 1's K') and P will be, and leaves the
 // same way.  (Plain accesses, 32 bytes a lane and lanes 512 apart, held up the SM's memory
 // instructions for 3500 cycles.)
@@ -131,8 +133,8 @@ constexpr int kBars = kScalars + kScalarBufs * (int)sizeof(Scalars);
 constexpr int kSmem = kBars + (int)sizeof(Bars);
 static_assert(kSmem <= 232448 - 1024 && kBars % 16 == 0, "shared memory");
 
-// TMEM columns: dS (the first launch's second one beside it), and for chunks in turn the
-// operand S^T (two 16-bit numbers a column), O1, and Q K^T, whose place O2 takes.
+// TMEM columns: dS (the first launch's second one beside it), the halves of the operand S^T
+// (two 16-bit numbers a column), and for chunks in turn O1, and Q K^T, whose place O2 takes.
 constexpr int kTmU = 0, kTmS = 128, kTmQ = 256, kTmO = 384, kTmCols = 512;
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
@@ -435,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars.ds_full[i], 1);
     }
     tc::mbar_init(&bars.u_full, kWorkers);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&bars.s_full[i], kWorkers);
     tc::mbar_init(&bars.p_full, kWorkers);
     tc::mbar_init(&bars.qk_full, 1);
     tc::mbar_init(&bars.o_full, 1);
@@ -595,9 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       decay *= last;
     };
-    auto operand = [&](int c) {
+    // S^T as an operand; FP16: a row times a power of two by its largest
+    auto power = [&](int c) {
       float down = 1.f;
-      if constexpr (F16) {  // the row times a power of two by its largest
+      if constexpr (F16) {
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(S[j]));
@@ -610,6 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         down = to_2p15(x, back);
         if (part == 0) bars.s_scale[c % 3][dv] = back;
       }
+      return down;
+    };
+    auto operand = [&](int half, float down) {  // (and wait_st)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t w[8];
@@ -618,10 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 x = make_float2(S[16 * g + 2 * j], S[16 * g + 2 * j + 1]), rest;
           if (F16) x = mul2(x, make_float2(down, down));
           w[j] = round2<F16>(x, rest);
+          if (half) w[j] = round2<F16>(rest, x);
         }
-        tmem_st8(lanes + kTmS + 64 * (c & 1) + 16 * part + 8 * g, w);
+        tmem_st8(lanes + kTmS + 64 * half + 16 * part + 8 * g, w);
       }
-      wait_st();
     };
 
     // ------------------------------------------------------------------------- P
@@ -630,9 +635,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* at[2];  // where columns 2 (lane % 4) and + 1 of a row's first piece are, but for the swizzle
 #pragma unroll
     for (int e = 0; e < 2; ++e) at[e] = smem + kP + (r0 + 8 * e) * 128 + 4 * (lane & 3);
-    auto put = [&](int j, int e, uint32_t x) { *reinterpret_cast<uint32_t*>(at[e] + ((j ^ turn) << 4)) = x; };
-    auto weights = [&](int c, const Scalars& sc) {
-      await(&bars.qk_full, c);  // the last P has been read too
+    auto put = [&](int j, int e, uint32_t hi, uint32_t lo) {
+      uint8_t* to = at[e] + ((j ^ turn) << 4);
+      *reinterpret_cast<uint32_t*>(to) = hi;
+      *reinterpret_cast<uint32_t*>(to + kTile / 2) = lo;
+    };
+    auto weights = [&](int c, const Scalars& sc, float s_down) {
+      await(&bars.qk_full, c);
       tc::tc_fence_after();
       float2 down[2];  // FP16: powers of two of the rows
       if constexpr (F16) {  // |q.k| is at most |q| |k|
@@ -648,12 +657,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (part == 0 && (lane & 3) == 0) bars.p_scale[c & 1][r0 + 8 * e] = back;
         }
       }
+      if (part > quad) operand(1, s_down);
       if (part <= quad) {
         const uint32_t qk = lanes + kTmO + 64 * (c & 1) + 16 * part;
         uint32_t r[2][4];
         ld_frag8(qk, r[0]);
         ld_frag8(qk + 8, r[1]);
         const bool far = sc.far[quad] != 0;
+        operand(1, s_down);  // (while these come)
         wait_ld(r[0]);
         wait_ld(r[1]);
 #pragma unroll
@@ -683,10 +694,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[e].y = col < i_row ? x[e].y : 0.f;
             }
             float2 rest;
-            put(2 * part + i, e, round2<F16>(x[e], rest));
+            const uint32_t hi = round2<F16>(x[e], rest), lo = round2<F16>(rest, x[e]);
+            put(2 * part + i, e, hi, lo);
           }
         }
       }
+      wait_st();
       tc::tc_fence_before();
       done(&bars.p_full);
     };
@@ -697,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t pick = odd ? 0x3276u : 0x5410u;
     const int64_t step = (int64_t)HV * kHeadDim;
     kda_bf16* dst = args.o + ((t0 + 16 * part + odd) * HV + h) * kHeadDim + ((32 * quad + lane) & ~1);
-    // (their products have been waited for, by the next chunk's keys and weights)
+    // (their products have been waited for, before the next chunk's operand)
     auto outputs = [&](int c, const Scalars& sc, uint64_t* free) {
       const int tok = 16 * part, left = L - c * kC - tok - odd;
       tc::tc_fence_after();
@@ -747,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0);
+        for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0, 0);
     float last = 1.f;
     if (LOCAL) {
       // K' and dS are there twice: a chunk's product runs while the next one's K' is made
@@ -768,10 +781,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_before();
         done(&bars.u_full);
         last = factors(c).last;
-        operand(c);
-        tc::tc_fence_before();
-        done(&bars.s_full[c & 1]);
-        weights(c, factors(c));
+        const float down = power(c);
+        if (c > 0) {  // the last operand and the last P have been read
+          await(&bars.o_full, c - 1);
+          tc::tc_fence_after();
+        }
+        operand(0, down);
+        weights(c, factors(c), down);
         if (c > 0) outputs(c - 1, factors(c - 1), &bars.sc_free[(c - 1) % kScalarBufs]);
         await(&bars.ds_full[c & 1], c >> 1);  // K' has been read, dS is there
         if (c + 1 < nch) {
@@ -779,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           done(&bars.wk_full[(c + 1) & 1]);
         }
       }
-      await(&bars.o_full, 0);
+      await(&bars.o_full, nch - 1);
       outputs(nch - 1, factors(nch - 1), &bars.sc_free[(nch - 1) % kScalarBufs]);
     }
     if (LOCAL) await(&bars.ds_full[(nch - 1) & 1], (nch - 1) >> 1);
@@ -900,23 +916,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_commit(&bars.ds_full[c & 1]);
         }
         __syncwarp();
-        if (!(ok = warp_wait(&bars.s_full[c & 1], c >> 1))) break;
-        tc::tc_fence_after();
-        if (leader) {  // O1^T = S^T Q^T
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            mma_ts(tmem + kTmQ + turn, tmem + kTmS + turn + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType, j > 0);
-        }
-        __syncwarp();
         if (!(ok = warp_wait(&bars.p_full, c))) break;
         tc::fence_async_smem();
         tc::tc_fence_after();
-        if (leader) {  // O2^T = V^T P^T
+        if (leader) {  // O1^T = S^T Q^T, O2^T = V^T P^T
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc::mma_bf16(tmem + kTmO + turn, v_op + ((j * 2048) >> 4), p_op + ((j * 32) >> 4), kType | tc::kIdescMnA, j > 0);
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mma_ts(tmem + kTmQ + turn, tmem + kTmS + 64 * b + 8 * j, q_op + (((j >> 2) * 8192 + (j & 3) * 32) >> 4), kType,
+                     b + j > 0);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc::mma_bf16(tmem + kTmO + turn, v_op + ((j * 2048) >> 4), p_op + ((b * (kTile / 2) + j * 32) >> 4),
+                           kType | tc::kIdescMnA, b + j > 0);
           tc::mma_commit(&bars.empty[st]);
-          if (c == nch - 1) tc::mma_commit(&bars.o_full);
+          tc::mma_commit(&bars.o_full);
         }
         __syncwarp();
       }
