@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
           n = s.count[cur];
         }
         if (n > kList) {  // too many: the tiles since are read again
+          __syncthreads();  // all have read how many pieces there are, which is counted anew below
           // What is listed of them, whose tokens are higher than earlier ones', is not the lot.
           const uint32_t first = from == 0 ? 0 : head + from * (kPieces * kThreads * kEach);
           const int have = min(s.count[cur], kList);
