@@ -37,12 +37,13 @@
 // in both.  (Whole, the 64 chunks of 1 x 4096 would take some 150 us on 16 SMs.)
 //
 // Precision.  The state is FP32, in registers and in the pool.  K' is split in three
-// BF16 parts, 2^-26 of it left, or two FP16 ones, 2^-23, so that states are as exact as
-// FP32 sums leave them.  S^T and P as operands are halves hi + lo of the outputs' type,
-// 2^-18 (FP16: 2^-22) of them left, so that an output is as exact as its own rounding.
-// (Rounded once, they made outputs up to sqrt 2 times as far off, for 4 to 9% less time:
-// the second halves' instructions, not their products.)  FP16's range is kept by a power
-// of two for each row of P and of S^T.
+// BF16 parts, 2^-26 of it left, or two FP16 ones, 2^-23 of it or 2^-39 of the chunk's
+// largest, so that states are as exact as FP32 sums leave them.  S^T and P as operands
+// are halves hi + lo of the outputs' type, 2^-17 (FP16: 2^-23) of them left, so that an
+// output is as exact as its own rounding.  (Rounded once, they made outputs up to sqrt 2
+// times as far off, for 4 to 9% less time: the second halves' instructions, not their
+// products.)  FP16's range is kept by a power of two for each row of P and of S^T, and for
+// a chunk's K'.
 #include <atomic>
 
 #include "kda_host.h"
@@ -87,8 +88,9 @@ struct Scalars {
   float w[kC];               // rk_j e^(c_last - c_j), 0 past the segment's end
   float k[kC];               // rk_j
   float big[kC], kk[kC];     // FP16: |q_i| e^(c_b - c_i), far |q_i|; |k_j|^2
-  float last;                // e^(c_last)
+  float k_big[4];            // FP16, keys as they are: the largest w_j |k_j| of 16 tokens each
   int far[4];                // of the four blocks
+  float last;                // e^(c_last)
   float pad[3];
 };
 constexpr float kFar = 60.f;
@@ -386,8 +388,9 @@ __device__ __forceinline__ float2 pair_from(float2 x, int l) {
 __device__ __forceinline__ float exp_diff(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
 
 // LOCAL: what segments add to a state of zero, or to the pool's.  Otherwise the outputs, and the
-// final states.
-template <bool F16, bool LOCAL>
+// final states.  SIZED: FP16 keys as they are, K' times a power of two by the chunk's largest.
+// (Unit keys' power is the same for all; asked for in each chunk it took 4% more.)
+template <bool F16, bool LOCAL, bool SIZED>
 __global__ void __launch_bounds__(kThreads, 1)
     lin_prefill_kernel(const LinPrefillArgs args, const __grid_constant__ LinMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -461,8 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const bool from_pool = seg.s == 0 && (LOCAL || seg.count == 1);
   const LinGateArgs& ga = args.gate;
-  // FP16: unit keys are at most 1 and become K' times 2^15, so that small ones keep their places
-  const float k_up = F16 && ga.use_qk_l2norm ? 32768.f : 1.f;
+  // FP16: unit keys are at most 1 and become K' times 2^15, so that small ones keep their places;
+  // keys as they are times a power of two by the chunk's largest (K' made of them alone ended at
+  // 2^-24: states 4e-5 of their RMS off for keys of size 1e-3)
+  constexpr float k_up = F16 && !SIZED ? 32768.f : 1.f;
   bool ok = true;
 
   // 768 threads start with 80 registers each; 512 at 96 and 256 at 48 are those 61440
@@ -483,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------------- K'
     // 4 rows a warp; of its row a thread has a 16-byte piece of either half of the channels
     const int row = 4 * warp + (lane >> 3), x8 = lane & 7;
+    auto key_power = [&](const Scalars& sc, float& back) {
+      const float4 m = *reinterpret_cast<const float4*>(sc.k_big);  // (in order as whole numbers, NaN the largest)
+      return to_2p15(max(max(__float_as_uint(m.x), __float_as_uint(m.y)), max(__float_as_uint(m.z), __float_as_uint(m.w))) >> 23, back);
+    };
     auto keys = [&](int c, int st, const Scalars& sc) {
       await(&bars.in_full[c % kScalarBufs], c / kScalarBufs);
       const int left = L - c * kC;
@@ -499,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           kw[p] = make_uint4(0, 0, 0, 0);
         }
       }
-      const float w = row < left ? wk : 0.f;
+      float w = row < left ? wk : 0.f, back;
+      if (SIZED) w *= key_power(sc, back);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const uint32_t x[4] = {kw[p].x, kw[p].y, kw[p].z, kw[p].w};
@@ -574,9 +584,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     };
-    float decay = 1.f;
-    const float k_down = 1.f / k_up;
-    auto update = [&](int c, float last) {  // S of the next chunk
+    float decay = 1.f, last = 1.f, k_down = 1.f / k_up;  // of the chunk whose dS is under way
+    auto take = [&](const Scalars& sc) {
+      last = sc.last;
+      if (SIZED) key_power(sc, k_down);
+    };
+    auto update = [&](int c) {  // S of the next chunk
       tc::tc_fence_after();
       uint32_t r[2][16];
 #pragma unroll
@@ -761,15 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) put(2 * part + i, e, 0, 0);
-    float last = 1.f;
     if (LOCAL) {
       // K' and dS are there twice: a chunk's product runs while the next one's K' is made
       for (int c = 0; c < nch; ++c) {
         if (c > 0) {
           await(&bars.ds_full[(c - 1) & 1], (c - 1) >> 1);
-          update(c - 1, last);
+          update(c - 1);
         }
-        last = factors(c).last;
+        take(factors(c));
         if (c + 1 < nch) keys(c + 1, stage(c + 1), factors(c + 1));
         tc::tc_fence_before();
         if (c + 1 < nch) done(&bars.wk_full[(c + 1) & 1]);
@@ -777,10 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       for (int c = 0; c < nch; ++c) {
-        if (c > 0) update(c - 1, last);
+        if (c > 0) update(c - 1);
         tc::tc_fence_before();
         done(&bars.u_full);
-        last = factors(c).last;
+        take(factors(c));
         const float down = power(c);
         if (c > 0) {  // the last operand and the last P have been read
           await(&bars.o_full, c - 1);
@@ -800,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (LOCAL) await(&bars.ds_full[(nch - 1) & 1], (nch - 1) >> 1);
     if (LOCAL || last_segment) {
-      update(nch - 1, last);
+      update(nch - 1);
       if (LOCAL) {
         float4* to = record(seg.record + seg.s);
 #pragma unroll
@@ -1035,6 +1047,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           (upper ? sc.row : sc.out)[r16] *= rsqrtf(n[1] + kNormEps);
         }
       }
+      if (SIZED) {
+        const float m = r16 < L - c * kC ? sc.w[r16] * sqrtf(n[0]) : 0.f;  // of this sequence alone
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) sc.k_big[warp - kNormWarp] = __uint_as_float(most);
+      }
       if (F16 && !LOCAL) {
         if (upper) sc.big[r16] *= sqrtf(n[1]);
         else sc.kk[r16] = r16 < L - c * kC ? n[0] : 0.f;  // of this sequence alone
@@ -1088,6 +1105,13 @@ bool encode_pool(CUtensorMap* m, const void* base, int64_t rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+using Kernel = void (*)(LinPrefillArgs, LinMaps);
+Kernel pick(bool f16, bool sized, bool local) {
+  if (!f16) return local ? lin_prefill_kernel<false, true, false> : lin_prefill_kernel<false, false, false>;
+  if (!sized) return local ? lin_prefill_kernel<true, true, false> : lin_prefill_kernel<true, false, false>;
+  return local ? lin_prefill_kernel<true, true, true> : lin_prefill_kernel<true, false, true>;
+}
+
 // The kernels' shared-memory limits, all of them in the first call on a device: a
 // later one may be under capture.
 kda_status allow_all() {
@@ -1098,9 +1122,9 @@ kda_status allow_all() {
   auto allow = [](auto kernel) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess;
   };
-  if (!allow(lin_prefill_kernel<false, false>) || !allow(lin_prefill_kernel<false, true>) ||
-      !allow(lin_prefill_kernel<true, false>) || !allow(lin_prefill_kernel<true, true>))
-    return KDA_ERR_CUDA;
+  for (bool local : {false, true})
+    for (const Kernel kernel : {pick(false, false, local), pick(true, false, local), pick(true, true, local)})
+      if (!allow(kernel)) return KDA_ERR_CUDA;
   ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   return KDA_OK;
 }
@@ -1213,19 +1237,17 @@ extern "C" kda_status kda_lin_prefill(kda_dims dims, kda_scalar_gate gate, const
     return KDA_ERR_CUDA;
   s = allow_all();
   if (s != KDA_OK) return s;
-  const bool f16 = dims.dtype == KDA_DTYPE_F16;
+  const bool f16 = dims.dtype == KDA_DTYPE_F16, sized = f16 && !gate.use_qk_l2norm;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   record_stage(0, st);
   // (without cu_seqlens the lengths are known here)
   const bool local = need > 0 && (cu_seqlens || args.each > c.even);
   if (local) {
-    s = launch_dependent(f16 ? lin_prefill_kernel<true, true> : lin_prefill_kernel<false, true>, (unsigned)whole, kThreads, kSmem,
-                         false, st, args, m);
+    s = launch_dependent(pick(f16, sized, true), (unsigned)whole, kThreads, kSmem, false, st, args, m);
     if (s != KDA_OK) return s;
   }
   record_stage(1, st);
-  s = launch_dependent(f16 ? lin_prefill_kernel<true, false> : lin_prefill_kernel<false, false>, (unsigned)units, kThreads, kSmem,
-                       local && !stage_between(), st, args, m);
+  s = launch_dependent(pick(f16, sized, false), (unsigned)units, kThreads, kSmem, local && !stage_between(), st, args, m);
   record_stage(2, st);
   return s;
 }
