@@ -69,7 +69,7 @@ struct LinPrefillArgs {
   // and otherwise; sequences of at most uncut tokens then stay in one piece
   int seg_even, seg_ragged, even_most, uncut;
   float4* local_state;  // [segment, value head][8][512 threads]: what a segment adds
-  float* local_decay;   // [segment, value head]: e^(its log-decays' sum)
+  float* local_decay;   // [segment, value head]: e^(its log-decays' sum), negative where that state is not finite
   int32_t* err_flag;
 };
 
@@ -175,6 +175,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) {
   const uint32_t parity = phase & 1u;
   if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, long_wait(bar, parity));
+}
+// Whether it is so for any thread of the 16 worker warps, which all come here.
+__device__ __forceinline__ bool any_worker(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 512, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -565,22 +578,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 32; ++j) S[j] = 0.f;
     }
     if (!LOCAL && seg.s > 0) {
-      // `up`: decay from the end of a segment before to the start of this one
+      // `up`: decay from the end of a segment before to the start of this one.  Where it is
+      // zero, segments that are not finite still count (NaN), as they do in one piece.
       const float* d = args.local_decay + (int64_t)seg.record * HV + h;
-      float up = 1.f, next = __ldcg(d + (int64_t)(seg.s - 1) * HV);
-      for (int m = seg.s - 1; m >= 0 && up > 0.f; --m) {
-        const float4* src = record(seg.record + m);
-        const float here = next;
-        if (m > 0) next = __ldcg(d + (int64_t)(m - 1) * HV);
+      float up = 1.f;
+      for (int m0 = seg.s - 1; m0 >= 0; m0 -= 32) {
+        const float here = m0 >= lane ? __ldcg(d + (int64_t)(m0 - lane) * HV) : 0.f;
+        const unsigned bad = __ballot_sync(0xffffffffu, __float_as_int(here) < 0);
+        for (int i = 0; i < 32 && i <= m0; ++i) {
+          if (up == 0.f) {
+            if (bad >> i == 0) break;
+            i += __ffs(bad >> i) - 1;
+          }
+          const float4* src = record(seg.record + m0 - i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 x = __ldcg(src + j * 512);
-          S[4 * j] = fmaf(up, x.x, S[4 * j]);
-          S[4 * j + 1] = fmaf(up, x.y, S[4 * j + 1]);
-          S[4 * j + 2] = fmaf(up, x.z, S[4 * j + 2]);
-          S[4 * j + 3] = fmaf(up, x.w, S[4 * j + 3]);
+          for (int j = 0; j < 8; ++j) {
+            const float4 x = __ldcg(src + j * 512);
+            S[4 * j] = fmaf(up, x.x, S[4 * j]);
+            S[4 * j + 1] = fmaf(up, x.y, S[4 * j + 1]);
+            S[4 * j + 2] = fmaf(up, x.z, S[4 * j + 2]);
+            S[4 * j + 3] = fmaf(up, x.w, S[4 * j + 3]);
+          }
+          up *= fabsf(__shfl_sync(0xffffffffu, here, i));
         }
-        up *= here;
       }
     }
     };
@@ -817,6 +837,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4* to = record(seg.record + seg.s);
 #pragma unroll
         for (int j = 0; j < 8; ++j) to[j * 512] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+        float zero = 0.f;  // NaN where one is not finite
+#pragma unroll
+        for (int j = 0; j < 32; ++j) zero = fmaf(S[j], 0.f, zero);
+        if (any_worker(zero != 0.f)) decay = -decay;
         if (tid == 0) args.local_decay[(int64_t)(seg.record + seg.s) * HV + h] = decay;
       } else {  // back to the pool as it came; all products are done
 #pragma unroll
