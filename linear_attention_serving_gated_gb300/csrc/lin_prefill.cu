@@ -77,14 +77,16 @@ struct LinMaps {
   CUtensorMap q, k, v, pool;
 };
 
-// Factors of a chunk: of the decays first, then times those of the norms.  b is the first
-// token of i's block of 16; where a block decays by more than e^60 the block's rows of P
-// get their factors term by term (far).
+// Factors of a chunk: of the decays first, then times those of the norms.  c_b is halfway
+// between c of the first and of the last token of i's block of 16, so that both factors of a
+// weight stay within e^30 (from the first token they reach e^60, and tokens of size 1e6, not
+// normalised, FP32's largest); where a block decays by more than e^60 the block's rows of P get
+// their factors term by term (far).
 struct Scalars {
   float c_hi[kC], c_lo[kC];  // c_i
   float out[kC];             // scale rq_i e^(c_i)
   float row[kC];             // scale rq_i e^(c_i - c_b); far: scale rq_i
-  float col[4][kC];          // rk_j e^(c_b - c_j) for b = 0, 16, 32, 48 and j < b + 16
+  float col[4][kC];          // rk_j e^(c_b - c_j) for the four blocks and j up to their ends
   float w[kC];               // rk_j e^(c_last - c_j), 0 past the segment's end
   float k[kC];               // rk_j
   float big[kC], kk[kC];     // FP16: |q_i| e^(c_b - c_i), far |q_i|; |k_j|^2
@@ -1013,15 +1015,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         put2(sc.c_lo, even.y, run.y);
         put2(sc.k, 1.f, 1.f);
         put2(sc.out, ga.scale * expf(even.x + even.y), ga.scale * expf(run.x + run.y));
-        const float2 c_b = pair_from(even, lane & 24), end = pair_from(run, lane | 7);
-        const bool far = !((c_b.x - end.x) + (c_b.y - end.y) <= kFar);
+        const float2 start = pair_from(even, lane & 24), end = pair_from(run, lane | 7);
+        const bool far = !((start.x - end.x) + (start.y - end.y) <= kFar);
+        const float2 c_b = make_float2(0.5f * (start.x + end.x), 0.f);
         if ((lane & 7) == 0) sc.far[lane >> 3] = far;
         const float e0 = far ? 1.f : exp_diff(even, c_b), e1 = far ? 1.f : exp_diff(run, c_b);
         put2(sc.row, ga.scale * e0, ga.scale * e1);
         if (F16) put2(sc.big, 1.f / e0, 1.f / e1);
 #pragma unroll 1
         for (int x = 0; x < 4; ++x) {
-          const float2 ref = pair_from(even, 8 * x);
+          const float2 ref = make_float2(__shfl_sync(0xffffffffu, c_b.x, 8 * x), 0.f);
           const bool some = lane < 8 * x + 8;
           put2(sc.col[x], some ? exp_diff(ref, even) : 0.f, some ? exp_diff(ref, run) : 0.f);
         }
