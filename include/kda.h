@@ -584,7 +584,8 @@ kda_status kda_token_logprobs(int logits_dtype, const void *logits, int64_t logi
  * in a quarter or less of their memory.  A group of FP32 values (128 in 8 bits,
  * 32 in 4, consecutive in the page) shares one FP32 scale:
  *   scale = max |x| / top,  code = x / scale rounded to nearest (ties to even) in
- *   [-top, top],            value = code * scale;   top = 127 in 8 bits, 7 in 4.
+ *   [-top, top],            value = code * scale;   top = 127 in 8 bits, 7 in 4
+ * (a scale whose value of code top would be past FP32's largest number: the one below).
  * A value comes back within half a scale, 1/254 (1/14) of its group's largest (where
  * the scale is below FP32's smallest normal number, within 2^-143 more).
  * Both are exact: codes follow from the FP32 scale without a rounding in between.

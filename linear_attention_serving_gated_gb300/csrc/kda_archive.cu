@@ -96,7 +96,9 @@ __global__ void __launch_bounds__(kThreads, 4) archive_store_kernel(const Archiv
     }
     // a group that holds an infinity or a NaN reads back as NaN
     const bool finite = m < 0x7f800000u;
-    const float scale = finite ? __fdiv_rn(__uint_as_float(m), kTop) : __uint_as_float(0x7fffffffu);
+    float scale = finite ? __fdiv_rn(__uint_as_float(m), kTop) : __uint_as_float(0x7fffffffu);
+    // 127 times the scale of the largest FP32 number is past it; the one below is not
+    if (BITS == 8 && scale > 0x1.020406p121f) scale = 0x1.020406p121f;
     int c[4] = {0, 0, 0, 0};
     const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     if (finite && scale >= 1e-37f) {
