@@ -294,6 +294,14 @@ def _intermediate_chunks(d, intermediate):
     return int(intermediate.shape[0])
 
 
+def _space(workspace):
+    """(device pointer, bytes) of a workspace: dense, so that it holds its bytes at its pointer."""
+    _at_least(workspace, 0, "workspace", "[bytes]")
+    if not workspace.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _prefill_shapes(d, q, k, v, g, beta, state_pool, state_idx, cu_seqlens, num_seqs, o):
     """Every element the prefill kernels touch for T = q.shape[0] tokens and
     gb_rows = g.shape[0] gate rows must exist (the library sees pointers)."""
@@ -327,8 +335,8 @@ def kda_prefill(d, gate: Gate, q, k, v, g, beta, state_pool, state_idx, cu_seqle
     st = load().kda_prefill(
         d, gate.c(), _in16(d, q, "q"), _in16(d, k, "k"), _in16(d, v, "v"), _in16(d, g, "g"), _in16(d, beta, "beta"),
         int(gb_rows), _p(state_pool), int(state_pool.shape[0]), _p(state_idx), _p(cu_seqlens),
-        int(num_seqs), int(T), _in16(d, o, "o"), _p(intermediate), inter_chunks, _p(workspace),
-        int(workspace.numel() * workspace.element_size()), _p(err_flag), _stream(stream))
+        int(num_seqs), int(T), _in16(d, o, "o"), _p(intermediate), inter_chunks, *_space(workspace),
+        _p(err_flag), _stream(stream))
     _check(st, "kda_prefill")
 
 
@@ -555,7 +563,7 @@ def kda_gdn_prefill(d, gate: ScalarGate, q, k, v, a, b, state_pool, state_idx, c
         _arg(state_idx, torch.int32, n, "state_idx", "[num_seqs]"),
         _opt(cu_seqlens, torch.int32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
         _arg(o, t16, T * HVV, "o", "[T, HV, V]"), _opt(intermediate, torch.float32, 0, "intermediate", "[chunks, HV, V, K]"),
-        inter_chunks, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _err(err_flag), _cur(stream))
+        inter_chunks, *_space(workspace), _err(err_flag), _cur(stream))
     if st:
         _check(st, "kda_gdn_prefill")
 
@@ -810,20 +818,20 @@ def kda_lin_prefill(d, gate: ScalarGate, q, k, v, a, state_pool, state_idx, cu_s
     HK, HVV = d.H * d.K, HV * V
     pool = _pool(d, state_pool, HV, V, d.K)
     g, rows = _lin_gate(gate, a, gate_rows, HV, t16)
-    size = 0
+    space = None, 0
     if workspace is None:
         need = lib.kda_lin_prefill_workspace_size(d, n, T)
         if need:
-            workspace, size = _new(need, torch.uint8, q.device, stream), need
+            workspace = _new(need, torch.uint8, q.device, stream)
+            space = workspace.data_ptr(), need
     else:
-        size = workspace.numel() * workspace.element_size()
+        space = _space(workspace)
     st = lib.kda_lin_prefill(
         d, g, _arg(q, t16, T * HK, "q", "[T, H, K]"), _arg(k, t16, T * HK, "k", "[T, H, K]"),
         _arg(v, t16, T * HVV, "v", "[T, HV, V]"), rows, gate_rows,
         *pool, _arg(state_idx, _I32, n, "state_idx", "[num_seqs]"),
         None if cu_seqlens is None else _arg(cu_seqlens, _I32, n + 1, "cu_seqlens", "[num_seqs + 1]"), n, T,
-        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), None if workspace is None else workspace.data_ptr(), size, _err(err_flag),
-        _cur(stream))
+        _arg(o, t16, T * HVV, "o", "[T, HV, V]"), *space, _err(err_flag), _cur(stream))
     if st:
         _check(st, "kda_lin_prefill")
 
