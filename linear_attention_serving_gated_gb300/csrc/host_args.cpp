@@ -1,7 +1,7 @@
 // host_args.cpp -- the binding's checks of a tensor argument, in native code.
 //
-// arg(t, dtype, n, name, shape) -> device pointer of a dense CUDA tensor of one element
-// type that holds at least n elements (int16 holds the bits of either 16-bit type).
+// arg(t, dtype, n, name, shape) -> device pointer of a dense tensor of the current CUDA
+// device and of one element type that holds at least n elements (int16 holds the bits of either 16-bit type).
 // Anything else goes to the function given to otherwise(), which says what is wrong.  From
 // Python the five questions take 0.35 us a tensor, and a call has six to ten; here 0.1.
 //
@@ -9,6 +9,7 @@
 // `width` elements that lie together; states(t, HV, V, K) -> (device pointer, slots) of a
 // dense FP32 pool [slots, HV, V, K].  Both give None where t is no such thing.
 #include <Python.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -28,12 +29,20 @@ bool of_type(const at::Tensor& x, PyObject* dtype) {
   return have == want || (have == at::kShort && (want == at::kHalf || want == at::kBFloat16));
 }
 
+// Whether a tensor is in the memory of the device that the call runs on, the current one.
+bool here(const at::Tensor& x) {
+  if (!x.is_cuda()) return false;
+  static const c10::impl::DeviceGuardImplInterface* devices = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA);
+  static const bool several = devices->deviceCount() > 1;
+  return !several || x.get_device() == devices->getDevice().index();
+}
+
 bool pointer_of(PyObject* t, PyObject* dtype, PyObject* n, void** out) {
   long long least;
   if (!THPVariable_Check(t) || !THPDtype_Check(dtype) || !number(n, &least)) return false;
   try {
     const at::Tensor& x = THPVariable_Unpack(t);
-    if (!of_type(x, dtype) || !x.is_cuda() || !x.is_contiguous() || x.numel() < least) return false;
+    if (!of_type(x, dtype) || !here(x) || !x.is_contiguous() || x.numel() < least) return false;
     *out = x.data_ptr();
     return true;
   } catch (...) {  // a tensor without memory of its own
@@ -62,7 +71,7 @@ PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t count) {
   if (count == 4 && THPVariable_Check(args[0]) && THPDtype_Check(args[1]) && number(args[2], &n) && number(args[3], &width)) {
     try {
       const at::Tensor& x = THPVariable_Unpack(args[0]);
-      if (of_type(x, args[1]) && x.is_cuda() && x.dim() == 2 && x.size(0) >= n && x.size(1) >= width && x.stride(1) == 1)
+      if (of_type(x, args[1]) && here(x) && x.dim() == 2 && x.size(0) >= n && x.size(1) >= width && x.stride(1) == 1)
         return pair(x.data_ptr(), x.stride(0));
     } catch (...) {
     }
@@ -75,7 +84,7 @@ PyObject* states(PyObject*, PyObject* const* args, Py_ssize_t count) {
   if (count == 4 && THPVariable_Check(args[0]) && number(args[1], want) && number(args[2], want + 1) && number(args[3], want + 2)) {
     try {
       const at::Tensor& x = THPVariable_Unpack(args[0]);
-      if (x.scalar_type() == at::kFloat && x.is_cuda() && x.dim() == 4 && x.size(1) == want[0] && x.size(2) == want[1] &&
+      if (x.scalar_type() == at::kFloat && here(x) && x.dim() == 4 && x.size(1) == want[0] && x.size(2) == want[1] &&
           x.size(3) == want[2] && x.is_contiguous())
         return pair(x.data_ptr(), x.size(0));
     } catch (...) {

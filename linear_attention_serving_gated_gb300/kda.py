@@ -297,9 +297,7 @@ def _intermediate_chunks(d, intermediate):
 def _space(workspace):
     """(device pointer, bytes) of a workspace: dense, so that it holds its bytes at its pointer."""
     _at_least(workspace, 0, "workspace", "[bytes]")
-    if not workspace.is_cuda:
-        raise ValueError("libkda takes device tensors")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return _here(workspace), workspace.numel() * workspace.element_size()
 
 
 def _prefill_shapes(d, q, k, v, g, beta, state_pool, state_idx, cu_seqlens, num_seqs, o):
@@ -452,6 +450,15 @@ def kda_set_stage_events(events=None):
 # for pointers, and the current stream without a Python stream object.
 
 
+def _here(t):
+    """Device pointer of a tensor of the current device, on which the call runs."""
+    if not t.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"libkda takes tensors of the current device, cuda:{torch._C._cuda_getDevice()} (got cuda:{t.get_device()})")
+    return t.data_ptr()
+
+
 def _checked_arg(t, dtype, n, name, shape):
     """Device pointer of a dense tensor of one element type that holds at least n
     elements (the rows the kernels touch), or what is wrong with it.  load() puts
@@ -460,9 +467,7 @@ def _checked_arg(t, dtype, n, name, shape):
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.numel() < n or not t.is_contiguous():
         _at_least(t, n, name, shape)
-    if not t.is_cuda:
-        raise ValueError("libkda takes device tensors")
-    return t.data_ptr()
+    return _here(t)
 
 
 def _rows(t, dtype, n, width):
@@ -574,9 +579,7 @@ def _gdn_rows(d, mixed_qkv, rows):
         raise ValueError(f"mixed_qkv must be [>= {rows}, >= {width}] with unit column stride (got {tuple(shape)})")
     if mixed_qkv.dtype is not _t16(d) and mixed_qkv.dtype is not torch.int16:
         raise TypeError(f"mixed_qkv must be {_t16(d)} (got {mixed_qkv.dtype})")
-    if not mixed_qkv.is_cuda:
-        raise ValueError("libkda takes device tensors")
-    return mixed_qkv.data_ptr()
+    return _here(mixed_qkv)
 
 
 def kda_gdn_decode_packed(d, gate: ScalarGate, mixed_qkv, a, b, state_pool, state_idx, o, err_flag=None,
@@ -639,9 +642,7 @@ def _probs(t, dtype, name, B, T):
         raise ValueError(f"the rows of {name} must lie one stride apart (got strides {(s0, s1, s2)})")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if not t.is_cuda:
-        raise ValueError("libkda takes device tensors")
-    return t.data_ptr(), stride
+    return _here(t), stride
 
 
 def _accept_sizes(target, tokens):
@@ -703,15 +704,13 @@ def _pages(pool):
     shape, size = pool.shape, pool.element_size()
     if len(shape) < 3:
         raise ValueError(f"pool must be [layers, slots, ...] (got {tuple(shape)})")
-    if not pool.is_cuda:
-        raise ValueError("libkda takes device tensors")
-    page = 1
+    base, page = _here(pool), 1
     for n in shape[2:]:
         page *= n
     if not pool.is_contiguous() and shape[0] > 0 and not pool[0].is_contiguous():
         raise ValueError("the slots of a layer must be dense")
     stride = pool.stride(0) if shape[0] > 1 else page * shape[1]
-    return kda_pages(pool.data_ptr(), page * size, stride * size, shape[0], shape[1])
+    return kda_pages(base, page * size, stride * size, shape[0], shape[1])
 
 
 def _list(t, name):
@@ -888,11 +887,9 @@ def kda_token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, 
     at = _rows(logits, logits.dtype, rows, V)
     if at is None:  # (rows of one token may be apart)
         unit = logits.stride(1)
-        if not logits.is_cuda:
-            raise ValueError("libkda takes device tensors")
         if V > 1 and unit != 1:
             raise ValueError(f"the rows of logits must be dense (got strides {logits.stride()})")
-        at = logits.data_ptr(), logits.stride(0)
+        at = _here(logits), logits.stride(0)
     x, stride = at
     if rows <= 1:
         stride = V
