@@ -1,10 +1,11 @@
 """Builds libkda.so in-tree from csrc/*.cu for sm_103a with nvcc, and the binding's
-checks of arguments, _host_args.so, from csrc/host_args.cpp with g++ and PyTorch's
-headers.
+checks of arguments, _host_args.so (with Python's tag in its name), from
+csrc/host_args.cpp with g++ and PyTorch's headers.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library next to this file.  Rebuilds only when a source is newer than the
-library.
+library, or when the binding's checks were built for another PyTorch or Python:
+they read tensors by PyTorch's own layout.
 """
 from __future__ import annotations
 
@@ -18,7 +19,8 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
-HOST = os.path.join(HERE, "_host_args.so")
+HOST = os.path.join(HERE, "_host_args" + sysconfig.get_config_var("EXT_SUFFIX"))
+HOST_FOR = os.path.join(HERE, "_host_args.built_for")  # made_for() of its build
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -48,8 +50,24 @@ def _host_command(out):
             "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
+def made_for() -> str:
+    """What the binding's checks are built against."""
+    import torch
+
+    return f"PyTorch {torch.__version__}, C++ ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, {os.path.basename(HOST)}"
+
+
+def built_for() -> str | None:
+    """made_for() of the build that is there, if one is."""
+    try:
+        with open(HOST_FOR) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(HOST):
+    if not os.path.exists(LIB) or not os.path.exists(HOST) or built_for() != made_for():
         return True
     _, deps = _sources()
     t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
@@ -82,7 +100,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError("compilation failed:\n" + "\n".join(" ".join(c) + "\n" + o for c, o in failed))
         tmp_lib = os.path.join(tmp, "libkda.so")
         subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp_lib, *objs])
+        for old in (HOST_FOR, os.path.join(HERE, "_host_args.so")):  # (any Python would import one without a tag)
+            if os.path.exists(old):
+                os.remove(old)
         shutil.move(host, HOST)
+        with open(HOST_FOR, "w") as f:
+            f.write(made_for())
         os.replace(tmp_lib, LIB) if os.path.dirname(tmp_lib) == os.path.dirname(LIB) else shutil.move(tmp_lib, LIB)
     return LIB
 

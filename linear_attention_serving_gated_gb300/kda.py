@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from . import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
 
@@ -93,7 +95,13 @@ def load(path: str = LIB_PATH):
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError(f"libkda.so not built ({path}); run linear_attention_serving_gated_gb300.build.build()")
+        built, here = build.built_for(), build.made_for()
+        if built is not None and built != here:  # it would read tensors by another layout
+            raise RuntimeError(f"_host_args.so is built for {built}; this is {here}: run "
+                               "linear_attention_serving_gated_gb300.build.build()")
         try:
+            if built is None:
+                raise ImportError("what it is built for is not known")
             from . import _host_args  # built beside it
         except ImportError as e:
             raise RuntimeError("_host_args.so not built; run linear_attention_serving_gated_gb300.build.build()") from e
