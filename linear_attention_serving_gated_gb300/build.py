@@ -74,6 +74,18 @@ def stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def install(src: str, dst: str) -> None:
+    """src as dst, by a copy beside dst and a rename: a process that has the old file
+    mapped keeps it whole."""
+    tmp = f"{dst}.{os.getpid()}"
+    try:
+        shutil.copy(src, tmp)
+        os.replace(tmp, dst)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return LIB
@@ -103,10 +115,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for old in (HOST_FOR, os.path.join(HERE, "_host_args.so")):  # (any Python would import one without a tag)
             if os.path.exists(old):
                 os.remove(old)
-        shutil.move(host, HOST)
+        install(host, HOST)
         with open(HOST_FOR, "w") as f:
             f.write(made_for())
-        os.replace(tmp_lib, LIB) if os.path.dirname(tmp_lib) == os.path.dirname(LIB) else shutil.move(tmp_lib, LIB)
+        install(tmp_lib, LIB)
     return LIB
 
 

@@ -53,3 +53,20 @@ def test_load_refuses_what_another_pytorch_built(built, monkeypatch):
     os.remove(build.HOST_FOR)
     with pytest.raises(RuntimeError, match="_host_args.so not built"):
         kda.load()
+
+
+def test_installed_beside_and_renamed(tmp_path):
+    """A library that a process has open stays what it is there."""
+    old, new = tmp_path / "lib.so", tmp_path / "build" / "lib.so"
+    new.parent.mkdir()
+    old.write_text("old")
+    new.write_text("new")
+    with open(old) as mapped:
+        build.install(str(new), str(old))
+        assert mapped.read() == "old" and os.fstat(mapped.fileno()).st_ino != os.stat(old).st_ino
+    assert old.read_text() == "new" and sorted(p.name for p in tmp_path.iterdir()) == ["build", "lib.so"]
+
+
+def test_build_moves_no_file_onto_a_library():
+    with open(build.__file__) as f:
+        assert "shutil.move" not in f.read()  # (between file systems it copies into the file that is there)
