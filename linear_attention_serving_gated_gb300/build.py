@@ -44,10 +44,10 @@ def _host_command(out):
 
     root = os.path.dirname(torch.__file__)
     include, lib = os.path.join(root, "include"), os.path.join(root, "lib")
-    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"], "-I", include,
-            "-I", os.path.join(include, "torch", "csrc", "api", "include"), os.path.join(CSRC, "host_args.cpp"), "-o", out,
-            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    headers = (sysconfig.get_paths()["include"], include, os.path.join(include, "torch", "csrc", "api", "include"))
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-Wextra",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(x for h in headers for x in ("-isystem", h)),
+            os.path.join(CSRC, "host_args.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def made_for() -> str:

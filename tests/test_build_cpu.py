@@ -1,5 +1,6 @@
 """What build() takes for up to date."""
 import os
+import subprocess
 import sysconfig
 import time
 
@@ -70,3 +71,10 @@ def test_installed_beside_and_renamed(tmp_path):
 def test_build_moves_no_file_onto_a_library():
     with open(build.__file__) as f:
         assert "shutil.move" not in f.read()  # (between file systems it copies into the file that is there)
+
+
+def test_the_bindings_checks_compile_without_warnings(tmp_path):
+    command = build._host_command(str(tmp_path / "x.so"))
+    assert "-Wall" in command and "-w" not in command
+    said = subprocess.run(command, capture_output=True, text=True)
+    assert said.returncode == 0 and said.stdout == said.stderr == ""
