@@ -1074,14 +1074,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           (upper ? sc.row : sc.out)[r16] *= rsqrtf(n[1] + kNormEps);
         }
       }
+      // |k_j|^2 of this sequence's keys, one that is not finite for FP16's largest: the others keep
+      // their places
+      const float k2 = r16 >= L - c * kC ? 0.f : n[0] < 5.5e11f ? n[0] : 5.5e11f;
       if (SIZED) {
-        const float m = r16 < L - c * kC ? sc.w[r16] * sqrtf(n[0]) : 0.f;  // of this sequence alone
+        const float m = sc.w[r16] * sqrtf(k2);
         const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         if (lane == 0) sc.k_big[warp - kNormWarp] = __uint_as_float(most);
       }
       if (F16 && !LOCAL) {
         if (upper) sc.big[r16] *= sqrtf(n[1]);
-        else sc.kk[r16] = r16 < L - c * kC ? n[0] : 0.f;  // of this sequence alone
+        else sc.kk[r16] = k2;
       }
       __syncwarp();
       if (lane == 0) arrive(&bars.in_full[c % kScalarBufs]);
