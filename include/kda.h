@@ -520,6 +520,10 @@ kda_status kda_pool_fork(kda_pages pages, uint8_t *used, int32_t *table, int tab
  * A sequence may be prefilled in parts, each from the state that the one before
  * left.  Where cu_seqlens decreases, so that sequences overlap and have more tokens
  * than there are, none runs.
+ * States are sums in FP32, outputs as exact as their own rounding.  The sums' order
+ * follows the segments that long sequences are cut into, and these the tokens and
+ * lengths of the whole call: the same sequence in another batch may differ in the
+ * last places.  The same call gives the same bits.
  *   workspace     kda_lin_prefill_workspace_size bytes, 16-byte aligned; the states of
  *                 segments that long sequences are cut into, 64 KiB a segment and value
  *                 head, and 0 (workspace may be NULL) where none can be cut
