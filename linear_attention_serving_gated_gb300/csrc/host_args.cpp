@@ -7,7 +7,8 @@
 //
 // rows(t, dtype, n, width) -> (device pointer, row stride) of at least n rows of at least
 // `width` elements that lie together; states(t, HV, V, K) -> (device pointer, slots) of a
-// dense FP32 pool [slots, HV, V, K].  Both give None where t is no such thing.
+// dense FP32 pool [slots, HV, V, K]; place(t) -> device pointer of a tensor of the current
+// device, dense or not.  They give None where t is no such thing.
 #include <Python.h>
 #include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/Dtype.h>
@@ -32,9 +33,11 @@ bool of_type(const at::Tensor& x, PyObject* dtype) {
 // Whether a tensor is in the memory of the device that the call runs on, the current one.
 bool here(const at::Tensor& x) {
   if (!x.is_cuda()) return false;
-  static const c10::impl::DeviceGuardImplInterface* devices = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA);
-  static const bool several = devices->deviceCount() > 1;
-  return !several || x.get_device() == devices->getDevice().index();
+  static const c10::impl::DeviceGuardImplInterface* const several = [] {  // null: there is one
+    const auto* devices = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA);
+    return devices->deviceCount() > 1 ? devices : nullptr;
+  }();
+  return !several || x.get_device() == several->getDevice().index();
 }
 
 bool pointer_of(PyObject* t, PyObject* dtype, PyObject* n, void** out) {
@@ -55,6 +58,17 @@ PyObject* arg(PyObject*, PyObject* const* args, Py_ssize_t count) {
   if (count == 5 && pointer_of(args[0], args[1], args[2], &p)) return PyLong_FromVoidPtr(p);
   if (!other) return PyErr_Format(PyExc_RuntimeError, "otherwise() has not been called");
   return PyObject_Vectorcall(other, args, (size_t)count, nullptr);
+}
+
+PyObject* place(PyObject*, PyObject* t) {
+  if (THPVariable_Check(t)) {
+    try {
+      const at::Tensor& x = THPVariable_Unpack(t);
+      if (here(x)) return PyLong_FromVoidPtr(x.data_ptr());
+    } catch (...) {
+    }
+  }
+  Py_RETURN_NONE;
 }
 
 PyObject* pair(void* p, long long n) {
@@ -103,6 +117,7 @@ PyMethodDef methods[] = {
     {"arg", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(arg)), METH_FASTCALL, nullptr},
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rows)), METH_FASTCALL, nullptr},
     {"states", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(states)), METH_FASTCALL, nullptr},
+    {"place", place, METH_O, nullptr},
     {"otherwise", otherwise, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

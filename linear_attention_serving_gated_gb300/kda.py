@@ -91,7 +91,7 @@ _lib = None
 
 def load(path: str = LIB_PATH):
     """Load libkda.so (built by build.py).  Raises if it is missing."""
-    global _lib, _arg, _rows, _states
+    global _lib, _arg, _rows, _states, _place
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError(f"libkda.so not built ({path}); run linear_attention_serving_gated_gb300.build.build()")
@@ -106,7 +106,7 @@ def load(path: str = LIB_PATH):
         except ImportError as e:
             raise RuntimeError("_host_args.so not built; run linear_attention_serving_gated_gb300.build.build()") from e
         _host_args.otherwise(_checked_arg)
-        _arg, _rows, _states = _host_args.arg, _host_args.rows, _host_args.states
+        _arg, _rows, _states, _place = _host_args.arg, _host_args.rows, _host_args.states, _host_args.place
         lib = ctypes.CDLL(path)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
         lib.kda_status_string.restype = ctypes.c_char_p
@@ -460,6 +460,9 @@ def kda_set_stage_events(events=None):
 
 def _here(t):
     """Device pointer of a tensor of the current device, on which the call runs."""
+    at = _place(t)
+    if at is not None:
+        return at
     if not t.is_cuda:
         raise ValueError("libkda takes device tensors")
     if t.get_device() != torch._C._cuda_getDevice():
@@ -485,6 +488,10 @@ def _rows(t, dtype, n, width):
 
 def _states(t, HV, V, K):
     """(device pointer, slots) of a dense FP32 pool [slots, HV, V, K]; None as in _rows."""
+
+
+def _place(t):
+    """Device pointer of a tensor of the current device; None as in _rows."""
 
 
 def _pool(d, t, HV, V, K):

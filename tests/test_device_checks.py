@@ -36,6 +36,18 @@ def test_tensors_of_another_device(monkeypatch):
             call(1)
 
 
+def test_native_place():
+    kda.load()
+    assert all(kda._place(t) is None for t in (torch.zeros(3), On(0, 3), torch.empty(3, device="meta"), None, 7))
+
+
+@pytest.mark.gpu
+def test_native_place_on_the_device():
+    kda.load()
+    x = torch.zeros(6, 8, device="cuda")
+    assert kda._place(x) == x.data_ptr() and kda._place(x.t()[2:]) == x.t()[2:].data_ptr() == kda._here(x.t()[2:])
+
+
 def test_logits_of_another_device(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     kda.load()
